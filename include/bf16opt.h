@@ -83,7 +83,7 @@ extern "C" {
  * changes.  bf16opt_abi_version() returns the value the library was built
  * with; code compiled against a header with another value must not use it.
  * No CUDA call; never fails. */
-#define BF16OPT_ABI_VERSION 2
+#define BF16OPT_ABI_VERSION 3
 int bf16opt_abi_version(void);
 
 /* ---- modes and flags --------------------------------------------------- */
@@ -418,6 +418,193 @@ int bf16opt_step_path(const bf16opt_t *h, int *path);
  * device's count into *count (0 = every pass completed) and clears it.
  * Errors: INVALID_ARG (count NULL), UNSUPPORTED (no device), CUDA. */
 int bf16opt_pipeline_timeouts(uint32_t *count);
+
+/* ---- training operators ------------------------------------------------------
+ * The memory-bound operators of a training step whose bf16 gradients the
+ * accumulate passes take: a distillation loss at the head, the norms, gate and
+ * residual scale around a block, and a router's balance loss, each with its
+ * gradient.  No counterpart in the paper.
+ *
+ * They need no handle.  A call enqueues its kernels on `stream`, on the
+ * current device, and neither allocates nor synchronises, so it can be captured
+ * in a CUDA graph.  Every pointer is device memory unless stated otherwise, aligned to its
+ * element; rows may start anywhere (a row stride counts elements and is at
+ * least the row's length).  16-byte aligned rows run fastest.  An output may
+ * not overlap an input or another output except where stated.  Descriptors are
+ * read during the call.  Results are deterministic: the same inputs give the
+ * same bits, whatever runs beside them.  Errors are reported as by the calls
+ * without a handle: INVALID_ARG, ALIGNMENT, UNSUPPORTED (no CUDA device) or
+ * CUDA, with the message in bf16opt_last_error(NULL); nothing is enqueued after
+ * INVALID_ARG or ALIGNMENT.  A call over 0 rows does nothing (weight gradients
+ * and losses of no rows are written as 0). */
+#define BF16OPT_TYPE_BF16 0
+#define BF16OPT_TYPE_F32 1
+#define BF16OPT_INDEX_I32 0
+#define BF16OPT_INDEX_I64 1
+
+/* Distillation from a teacher's top logits.  z: the student's logits of a row;
+ * (id_i, t_i), i < k: the teacher's kept entries; T: temperature.
+ *   p_i = softmax over the row's entries of t / T, or, with teacher_lse,
+ *         exp(t_i / T - teacher_lse[row]) (the teacher's own probabilities, whose
+ *         sum P may be below 1); q = softmax(z / T); s = softmax(z);
+ *   loss = w [ kl_weight T^2 (sum_i p_i (log p_i - log q[id_i]))
+ *              + ce_weight (-log s[label]) ],           w = row_weight[row] or 1
+ *   dz_j = w dloss [ kl_weight T (P q_j - sum_{i: id_i = j} p_i)
+ *              + ce_weight (s_j - [j = label]) ].
+ * An entry whose id is outside [0, vocab) or whose t is -inf does not exist; a
+ * row without entries has no first term; a label outside [0, vocab) gives no
+ * second term.  Entries may repeat an id.  A row whose w is 0 is not read: its
+ * loss, log-sum-exps and gradient are 0.  Logits of -inf are masked
+ * vocabulary: q = s = 0 there (a teacher's entry or label on one makes the loss
+ * +inf; in a row with no other logit q = s = 0 everywhere).  NaN and +inf in
+ * a row give NaN in that row alone. */
+#define BF16OPT_DISTILL_MAX_K 1024
+
+typedef struct {
+    uint64_t rows;               /* tokens */
+    uint32_t vocab;              /* 1 .. 2^30 */
+    uint32_t k;                  /* teacher's entries per row, 0 .. BF16OPT_DISTILL_MAX_K */
+    int32_t logits_type;         /* BF16OPT_TYPE_* of logits and dlogits */
+    int32_t teacher_type;        /* BF16OPT_TYPE_* of teacher_logits */
+    int32_t ids_type;            /* BF16OPT_INDEX_* of teacher_ids */
+    int32_t labels_type;         /* BF16OPT_INDEX_* of labels */
+    const void *logits;          /* [rows, vocab] */
+    uint64_t logits_stride;
+    const void *teacher_ids;     /* [rows, k] */
+    uint64_t ids_stride;
+    const void *teacher_logits;  /* [rows, k] */
+    uint64_t teacher_stride;
+    const float *teacher_lse;    /* NULL, or [rows]: log-sum-exp of the teacher's whole row at T */
+    const void *labels;          /* NULL, or [rows] */
+    const float *row_weight;     /* NULL, or [rows] */
+    float temperature;           /* finite, > 0 */
+    float kl_weight, ce_weight;  /* finite, >= 0; without labels there is no second term */
+} bf16opt_distill_t;
+
+/* loss: [rows] FP32.  lse: NULL, or [rows, 2] FP32: the log-sum-exp of z / T
+ * and of z (the second repeats the first where ce_weight is 0 or labels is
+ * NULL, and both are at T = 1 where kl_weight is 0), for bf16opt_distill_backward. */
+int bf16opt_distill_forward(const bf16opt_distill_t *d, float *loss, float *lse, void *stream);
+
+/* dlogits [rows, vocab], rounded once from FP32; it may be d->logits itself
+ * with the same stride (the logits are then overwritten).  lse: as the forward
+ * call with the same descriptor left it.  dloss: NULL (1), or [rows] FP32: the
+ * gradient of the row's loss. */
+int bf16opt_distill_backward(const bf16opt_distill_t *d, const float *lse, const float *dloss, void *dlogits,
+                             uint64_t dlogits_stride, void *stream);
+
+/* Loss and gradient (for a gradient of dloss, or 1, of each row's loss) in one
+ * pass: every logit is read once.  lse may be NULL. */
+int bf16opt_distill_loss_grad(const bf16opt_distill_t *d, const float *dloss, float *loss, float *lse, void *dlogits,
+                              uint64_t dlogits_stride, void *stream);
+
+/* A block's output joined to the residual stream, with the norm behind the
+ * block and the one before the next:
+ *   u = N_post(y);  r = residual_scale x + branch_scale act(gate) u;  h = N_pre(r)
+ * N is, for a row v of `hidden` elements,
+ *   BF16OPT_NORM_NONE   v,
+ *   BF16OPT_NORM_RMS    v / sqrt(mean(v^2) + eps) * weight + bias,
+ *   BF16OPT_NORM_LAYER  (v - mean) / sqrt(var + eps) * weight + bias,
+ * (a NULL weight is 1, a NULL bias 0); act is the identity or the sigmoid.  The gate
+ * (NULL: 1) has gate_rows rows: rows / gate_rows consecutive rows share one, so
+ * it is one learned vector (1), one for each sequence, or one for each token.
+ * Statistics, products and sums are FP32; r and h are each rounded once (h is
+ * computed from the unrounded r).  stats [rows, 4] FP32 keeps mean and
+ * 1/sqrt(.. + eps) of r and of y (mean 0 for RMS, both 0 for NONE).
+ *   backward: dr, dh (gradients of r by other readers and of h; either may be
+ *   NULL: 0), r, y, stats as the forward call left them:
+ *     g = dr + N_pre'(dh);  dx = residual_scale g;  du = branch_scale act(gate) g;
+ *     dgate = branch_scale act'(gate) sum over the rows that share it of g u;
+ *     dy = N_post'(du); the norms' weights' and biases' gradients over all rows.
+ *   Row sums are FP32 in a fixed order.  NaN stays in its row, but for the
+ *   weights' and shared gates' gradients. */
+#define BF16OPT_NORM_NONE 0
+#define BF16OPT_NORM_RMS 1
+#define BF16OPT_NORM_LAYER 2
+#define BF16OPT_GATE_IDENTITY 0
+#define BF16OPT_GATE_SIGMOID 1
+#define BF16OPT_NORM_MAX_HIDDEN 16384
+
+typedef struct {
+    uint64_t rows;
+    uint32_t hidden;             /* 1 .. BF16OPT_NORM_MAX_HIDDEN */
+    int32_t branch_type;         /* BF16OPT_TYPE_* of y, h, gate and their gradients */
+    int32_t stream_type;         /* BF16OPT_TYPE_* of x, r and their gradients; F32 if branch_type is F32 */
+    int32_t weight_type;         /* BF16OPT_TYPE_* of the norms' weights and biases and of their gradients */
+    int32_t pre, post;           /* BF16OPT_NORM_* of N_pre and N_post */
+    int32_t gate_act;            /* BF16OPT_GATE_* */
+    uint32_t reserved;           /* must be 0 */
+    uint64_t gate_rows;          /* 0 without a gate; divides rows */
+    const void *gate;            /* NULL, or [gate_rows, hidden] */
+    const void *pre_weight, *pre_bias, *post_weight, *post_bias;   /* each NULL or [hidden] */
+    float residual_scale, branch_scale;   /* finite */
+    float eps;                   /* finite, > 0 */
+} bf16opt_norm_gate_t;
+
+/* All rows are contiguous ([rows, hidden]).  h: NULL if pre is NONE.  stats may
+ * be NULL (no backward).  r may be x (the stream updated in place), h may be y. */
+int bf16opt_norm_gate_forward(const bf16opt_norm_gate_t *d, const void *x, const void *y, void *r, void *h,
+                              float *stats, void *stream);
+
+/* Bytes of scratch that the backward call of this descriptor needs (device
+ * memory, 16-byte aligned, used on `stream` during the call only).  No CUDA
+ * kernel; errors: INVALID_ARG, UNSUPPORTED. */
+int bf16opt_norm_gate_workspace(const bf16opt_norm_gate_t *d, uint64_t *bytes);
+
+/* The outputs of weights that d does not have are NULL; any other may be NULL
+ * too, and is then not computed, except dx and dy. dx may be dr, dy may be dh. */
+int bf16opt_norm_gate_backward(const bf16opt_norm_gate_t *d, const void *dr, const void *dh, const void *r,
+                               const void *y, const float *stats, void *dx, void *dy, void *dgate, void *dpre_weight,
+                               void *dpre_bias, void *dpost_weight, void *dpost_bias, void *workspace,
+                               uint64_t workspace_bytes, void *stream);
+
+/* A router's choice and its balance.  z: a token's logits over the experts,
+ * p = softmax(z).  Chosen: the k largest logits, ties to the lowest expert,
+ * in descending order; weights: their p, divided by their sum if renormalise.
+ * The tokens form `groups` runs of tokens / groups (1: one batch; one for each
+ * sequence: each sequence balanced for itself).  Over the n live tokens of a
+ * group (mask NULL or nonzero), with counts_e tokens sent to expert e:
+ *   f_e = counts_e experts / (k n),  P_e = mean p_e,
+ *   loss = 1/groups sum over groups [ balance_weight sum_e f_e P_e
+ *                                     + z_weight mean (log sum exp z)^2 ],
+ * a group without live tokens adding 0.  Backward, with f constant, dloss the
+ * gradient of the loss and dweights that of the weights:
+ *   dz_j = dloss / (groups n) [ balance_weight p_j (f_j - sum_e f_e p_e)
+ *          + 2 z_weight lse p_j ] + the gradient of the weights.
+ * A masked token has ids -1, weights and gradient 0.  An expert whose logit
+ * is -inf is never chosen (missing choices: id -1, weight 0, not counted); a token whose logits
+ * all are is as if masked.  A NaN is chosen after every number but before -inf;
+ * it makes the token's weights, the loss and the group's gradient NaN. */
+#define BF16OPT_BALANCE_MAX_EXPERTS 1024
+#define BF16OPT_BALANCE_MAX_K 32
+
+typedef struct {
+    uint64_t tokens;
+    uint32_t experts;            /* 1 .. BF16OPT_BALANCE_MAX_EXPERTS */
+    uint32_t k;                  /* 1 .. min(experts, BF16OPT_BALANCE_MAX_K) */
+    uint64_t groups;             /* >= 1, divides tokens */
+    int32_t logits_type;         /* BF16OPT_TYPE_* of logits and dlogits */
+    int32_t renormalise;         /* 0 or 1 */
+    const void *logits;          /* [tokens, experts] */
+    uint64_t logits_stride;
+    const uint8_t *mask;         /* NULL, or [tokens]: 0 = masked */
+    float balance_weight, z_weight;   /* finite, >= 0 */
+} bf16opt_balance_t;
+
+/* ids [tokens, k] int32, weights [tokens, k] FP32, counts [groups, experts]
+ * int32, loss [1] FP32, saved [tokens + groups] FP32 (each token's log-sum-exp,
+ * then each group's n, for the backward call).  workspace: as for
+ * bf16opt_norm_gate_workspace. */
+int bf16opt_balance_workspace(const bf16opt_balance_t *d, uint64_t *bytes);
+int bf16opt_balance_forward(const bf16opt_balance_t *d, int32_t *ids, float *weights, int32_t *counts, float *loss,
+                            float *saved, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* ids, counts, saved: as the forward call with the same descriptor left them.
+ * dweights: NULL (0) or [tokens, k] FP32.  dloss: NULL (1) or [1] FP32.
+ * dlogits [tokens, experts] with its stride; it may be d->logits itself. */
+int bf16opt_balance_backward(const bf16opt_balance_t *d, const int32_t *ids, const int32_t *counts, const float *saved,
+                             const float *dweights, const float *dloss, void *dlogits, uint64_t dlogits_stride,
+                             void *stream);
 
 /* ---- checked build -------------------------------------------------------
  * No counterpart in the paper: a debugging aid standing in for a memory

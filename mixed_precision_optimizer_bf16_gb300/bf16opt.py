@@ -31,6 +31,19 @@ BF16OPT_PATH_NONE = 0
 BF16OPT_PATH_VECTOR = 1
 BF16OPT_PATH_PIPELINE = 2
 BF16OPT_PATH_HOST = 3
+BF16OPT_TYPE_BF16 = 0
+BF16OPT_TYPE_F32 = 1
+BF16OPT_INDEX_I32 = 0
+BF16OPT_INDEX_I64 = 1
+BF16OPT_DISTILL_MAX_K = 1024
+BF16OPT_NORM_NONE = 0
+BF16OPT_NORM_RMS = 1
+BF16OPT_NORM_LAYER = 2
+BF16OPT_GATE_IDENTITY = 0
+BF16OPT_GATE_SIGMOID = 1
+BF16OPT_NORM_MAX_HIDDEN = 16384
+BF16OPT_BALANCE_MAX_EXPERTS = 1024
+BF16OPT_BALANCE_MAX_K = 32
 
 c_u64, c_u32, c_i32, c_f32, c_vp = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
 
@@ -65,15 +78,39 @@ class bf16opt_norm_result_t(ctypes.Structure):
     _fields_ = [("sumsq", ctypes.c_double), ("norm", ctypes.c_double), ("clip_coef", ctypes.c_double)]
 
 
+class bf16opt_distill_t(ctypes.Structure):
+    _fields_ = [("rows", c_u64), ("vocab", c_u32), ("k", c_u32), ("logits_type", c_i32), ("teacher_type", c_i32),
+                ("ids_type", c_i32), ("labels_type", c_i32), ("logits", c_vp), ("logits_stride", c_u64),
+                ("teacher_ids", c_vp), ("ids_stride", c_u64), ("teacher_logits", c_vp), ("teacher_stride", c_u64),
+                ("teacher_lse", c_vp), ("labels", c_vp), ("row_weight", c_vp), ("temperature", c_f32),
+                ("kl_weight", c_f32), ("ce_weight", c_f32)]
+
+
+class bf16opt_norm_gate_t(ctypes.Structure):
+    _fields_ = [("rows", c_u64), ("hidden", c_u32), ("branch_type", c_i32), ("stream_type", c_i32),
+                ("weight_type", c_i32), ("pre", c_i32), ("post", c_i32), ("gate_act", c_i32), ("reserved", c_u32),
+                ("gate_rows", c_u64), ("gate", c_vp), ("pre_weight", c_vp), ("pre_bias", c_vp), ("post_weight", c_vp),
+                ("post_bias", c_vp), ("residual_scale", c_f32), ("branch_scale", c_f32), ("eps", c_f32)]
+
+
+class bf16opt_balance_t(ctypes.Structure):
+    _fields_ = [("tokens", c_u64), ("experts", c_u32), ("k", c_u32), ("groups", c_u64), ("logits_type", c_i32),
+                ("renormalise", c_i32), ("logits", c_vp), ("logits_stride", c_u64), ("mask", c_vp),
+                ("balance_weight", c_f32), ("z_weight", c_f32)]
+
+
 # Functions the header declares (the tests check the library exports them all).
 EXPORTS = ("bf16opt_create", "bf16opt_create_offload", "bf16opt_accumulate", "bf16opt_grad_norm", "bf16opt_step", "bf16opt_destroy",
            "bf16opt_get_step", "bf16opt_set_step", "bf16opt_error_string", "bf16opt_last_error",
            "bf16opt_grad_norm_static", "bf16opt_lr_factor", "bf16opt_set_lr_schedule",
            "bf16opt_grad_norm_local", "bf16opt_set_global_sumsq", "bf16opt_set_rank_sumsqs",
            "bf16opt_sum_rank_sumsqs", "bf16opt_set_skip_nonfinite", "bf16opt_debug_faults",
-           "bf16opt_pipeline_timeouts", "bf16opt_step_path", "bf16opt_abi_version")
+           "bf16opt_pipeline_timeouts", "bf16opt_step_path", "bf16opt_abi_version",
+           "bf16opt_distill_forward", "bf16opt_distill_backward", "bf16opt_distill_loss_grad",
+           "bf16opt_norm_gate_forward", "bf16opt_norm_gate_workspace", "bf16opt_norm_gate_backward",
+           "bf16opt_balance_workspace", "bf16opt_balance_forward", "bf16opt_balance_backward")
 
-ABI_VERSION = 2   # BF16OPT_ABI_VERSION of the header these declarations mirror
+ABI_VERSION = 3   # BF16OPT_ABI_VERSION of the header these declarations mirror
 
 _lib = None
 
@@ -143,6 +180,18 @@ def load(path=None):
     L.bf16opt_set_lr_schedule.argtypes = [hp, ctypes.POINTER(bf16opt_lr_schedule_t)]
     L.bf16opt_grad_norm_static.restype = ctypes.c_int
     L.bf16opt_grad_norm_static.argtypes = [c_vp, c_u64, c_f32, c_f32, c_vp, c_vp]
+    dd, dn, db = (ctypes.POINTER(t) for t in (bf16opt_distill_t, bf16opt_norm_gate_t, bf16opt_balance_t))
+    L.bf16opt_distill_forward.argtypes = [dd, c_vp, c_vp, c_vp]
+    L.bf16opt_distill_backward.argtypes = [dd, c_vp, c_vp, c_vp, c_u64, c_vp]
+    L.bf16opt_distill_loss_grad.argtypes = [dd, c_vp, c_vp, c_vp, c_vp, c_u64, c_vp]
+    L.bf16opt_norm_gate_forward.argtypes = [dn, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]
+    L.bf16opt_norm_gate_workspace.argtypes = [dn, ctypes.POINTER(c_u64)]
+    L.bf16opt_norm_gate_backward.argtypes = [dn] + [c_vp] * 13 + [c_u64, c_vp]
+    L.bf16opt_balance_workspace.argtypes = [db, ctypes.POINTER(c_u64)]
+    L.bf16opt_balance_forward.argtypes = [db] + [c_vp] * 6 + [c_u64, c_vp]
+    L.bf16opt_balance_backward.argtypes = [db] + [c_vp] * 6 + [c_u64, c_vp]
+    for name in EXPORTS[-9:]:
+        getattr(L, name).restype = ctypes.c_int
     if path == lib_path():
         _lib = L
     return L
@@ -275,6 +324,52 @@ def bf16opt_step_path(h):
     path = ctypes.c_int(0)
     rc = load().bf16opt_step_path(h, ctypes.byref(path))
     return rc, path.value
+
+
+# Training operators: descriptors as structs, device addresses as ints (None: NULL).
+
+def bf16opt_distill_forward(d, loss, lse=None, stream=0):
+    return load().bf16opt_distill_forward(d, loss, lse, stream)
+
+
+def bf16opt_distill_backward(d, lse, dloss, dlogits, dlogits_stride, stream=0):
+    return load().bf16opt_distill_backward(d, lse, dloss, dlogits, dlogits_stride, stream)
+
+
+def bf16opt_distill_loss_grad(d, dloss, loss, lse, dlogits, dlogits_stride, stream=0):
+    return load().bf16opt_distill_loss_grad(d, dloss, loss, lse, dlogits, dlogits_stride, stream)
+
+
+def bf16opt_norm_gate_forward(d, x, y, r, h=None, stats=None, stream=0):
+    return load().bf16opt_norm_gate_forward(d, x, y, r, h, stats, stream)
+
+
+def bf16opt_norm_gate_workspace(d):
+    """(status, bytes)."""
+    n = c_u64(0)
+    rc = load().bf16opt_norm_gate_workspace(d, n)
+    return rc, n.value
+
+
+def bf16opt_norm_gate_backward(d, dr, dh, r, y, stats, dx, dy, dgate, dpre_weight, dpre_bias, dpost_weight, dpost_bias,
+                               workspace, workspace_bytes, stream=0):
+    return load().bf16opt_norm_gate_backward(d, dr, dh, r, y, stats, dx, dy, dgate, dpre_weight, dpre_bias, dpost_weight,
+                                             dpost_bias, workspace, workspace_bytes, stream)
+
+
+def bf16opt_balance_workspace(d):
+    """(status, bytes)."""
+    n = c_u64(0)
+    rc = load().bf16opt_balance_workspace(d, n)
+    return rc, n.value
+
+
+def bf16opt_balance_forward(d, ids, weights, counts, loss, saved, workspace=None, workspace_bytes=0, stream=0):
+    return load().bf16opt_balance_forward(d, ids, weights, counts, loss, saved, workspace, workspace_bytes, stream)
+
+
+def bf16opt_balance_backward(d, ids, counts, saved, dweights, dloss, dlogits, dlogits_stride, stream=0):
+    return load().bf16opt_balance_backward(d, ids, counts, saved, dweights, dloss, dlogits, dlogits_stride, stream)
 
 
 def bf16opt_last_error(h=None):

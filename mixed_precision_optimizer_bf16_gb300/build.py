@@ -5,9 +5,9 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB_PATH = os.path.join(HERE, "libbf16opt.so")
-SOURCES = [os.path.join(HERE, "csrc", "bf16opt.cu")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("bf16opt.cu", "distill.cu", "norm_gate.cu", "balance.cu")]
 DEPS = SOURCES + [os.path.join(HERE, "csrc", "kernels.cuh"), os.path.join(HERE, "csrc", "host_adam.h"),
-                  os.path.join(ROOT, "include", "bf16opt.h")]
+                  os.path.join(HERE, "csrc", "ops_common.cuh"), os.path.join(ROOT, "include", "bf16opt.h")]
 
 # -ffp-contract=off: host code rounds every product on its own (the offloaded
 # step's host update repeats the device kernel's operations exactly)
@@ -16,7 +16,7 @@ PROBE_SOURCES = [os.path.join(HERE, "csrc", "hbm_probe.cu")]
 PROBE_DEPS = PROBE_SOURCES + [os.path.join(ROOT, "include", "hbm_probe.h")]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-Xcompiler", "-ffp-contract=off", "-shared"]
+              "-Xcompiler", "-fPIC", "-Xcompiler", "-ffp-contract=off", "-shared", "--threads", "4"]
 
 
 def nvcc():

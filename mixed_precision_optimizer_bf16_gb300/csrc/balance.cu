@@ -1,0 +1,620 @@
+// balance.cu -- a router's choice of experts, their counts, the balance loss and
+// the z-loss, forward and backward (bf16opt_balance_* of include/bf16opt.h).
+//
+// A warp takes a token: each lane holds a run of PER experts in registers, so
+// the softmax, the k largest logits and the mean probabilities come from one
+// read of the logits.  A CTA walks a contiguous run of tokens and keeps the
+// sums of the group it is in; a group that lies within one CTA is finished
+// there, the others leave partial sums that a second kernel joins in the CTAs'
+// order.  (f_e, the share of tokens of an expert, is known only after the last
+// token, so the gradient is a second pass.)
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "ops_common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace bf16ops {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+
+struct Args {
+    uint64_t tokens, groups, per_group;
+    uint32_t experts, k;
+    int renormalise;
+    const void *logits;
+    uint64_t stride;
+    bool vec;                       // every lane's run is one aligned run of the row
+    const uint8_t *mask;
+    float balance_weight, z_weight;
+    int32_t *ids;
+    float *weights;
+    int32_t *counts;
+    float *loss, *lse, *live;       // live: tokens of each group that count
+    // scratch: losses [groups]; then per CTA two slots of experts sums, experts counts, squares, live
+    float *group_loss, *slots;
+    uint32_t teams;
+};
+
+__host__ __device__ inline size_t slot_floats(uint32_t experts) { return 2 * (size_t)experts + 2; }
+
+__host__ __device__ inline uint64_t team_row(uint64_t rows, uint32_t teams, uint32_t p) {
+    return rows / teams * p + rows % teams * p / teams;
+}
+__device__ __forceinline__ uint32_t team_of(uint64_t rows, uint32_t teams, uint64_t row) {
+    uint32_t p = (uint32_t)(row / (rows / teams + 1));
+    while (team_row(rows, teams, p + 1) <= row) ++p;
+    return p;
+}
+
+// Logits as unsigned keys in their order: -inf (an expert that is off) 0, NaN 1,
+// then the numbers; both zeros are one key.
+__device__ __forceinline__ uint32_t key_of(float z) {
+    const uint32_t b = __float_as_uint(z + 0.f);
+    const uint32_t k = b & 0x80000000u ? ~b : b | 0x80000000u;
+    return z != z ? 1u : z == -INFINITY ? 0u : k;
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+    if (k == 1u) return NAN;
+    if (k == 0u) return -INFINITY;
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// A lane's run of the row: experts [lane * PER, lane * PER + PER), -inf beyond.
+template <class T, int PER>
+__device__ __forceinline__ void load_run(const T *row, uint32_t experts, uint32_t lane, bool vec, float (&z)[PER]) {
+    const uint32_t e0 = lane * PER;
+    constexpr int BYTES = PER * (int)sizeof(T);
+    if (vec && BYTES >= 4) {
+        if (e0 < experts) {
+            if constexpr (BYTES >= 16) {
+                constexpr int N = Vec<T>::N;
+#pragma unroll
+                for (int v = 0; v < PER / N; ++v) {
+                    float f[N];
+                    Vec<T>::unpack(__ldcs(reinterpret_cast<const uint4 *>(row + e0) + v), f);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) z[v * N + i] = f[i];
+                }
+            } else if constexpr (BYTES >= 4) {
+                uint32_t w[BYTES / 4];
+                if constexpr (BYTES == 8) {
+                    const uint2 q = __ldcs(reinterpret_cast<const uint2 *>(row + e0));
+                    w[0] = q.x, w[1] = q.y;
+                } else {
+                    w[0] = __ldcs(reinterpret_cast<const uint32_t *>(row + e0));
+                }
+#pragma unroll
+                for (int i = 0; i < BYTES / 4; ++i) {
+                    if constexpr (sizeof(T) == 2) z[2 * i] = bf16_lo(w[i]), z[2 * i + 1] = bf16_hi(w[i]);
+                    else z[i] = __uint_as_float(w[i]);
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) z[i] = -INFINITY;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) z[i] = e0 + i < experts ? to_f32(row[e0 + i]) : -INFINITY;
+}
+template <class T, int PER>
+__device__ __forceinline__ void store_run(T *row, uint32_t experts, uint32_t lane, bool vec, const float (&g)[PER]) {
+    const uint32_t e0 = lane * PER;
+    constexpr int BYTES = PER * (int)sizeof(T);
+    if (vec && BYTES >= 16) {
+        if constexpr (BYTES >= 16) {
+            constexpr int N = Vec<T>::N;
+            if (e0 < experts) {
+#pragma unroll
+                for (int v = 0; v < PER / N; ++v) {
+                    float f[N];
+#pragma unroll
+                    for (int i = 0; i < N; ++i) f[i] = g[v * N + i];
+                    reinterpret_cast<uint4 *>(row + e0)[v] = Vec<T>::pack(f);
+                }
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (e0 + i < experts) from_f32(row[e0 + i], g[i]);
+}
+
+// sum over the CTA, the same bits in every thread
+__device__ __forceinline__ float cta_sum(float v, float *buf) {
+    v = warp_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.f;
+    for (int i = 0; i < kWarps; ++i) s += buf[i];
+    return s;
+}
+
+template <class T, int PER>
+__global__ void __launch_bounds__(kThreads) k_balance_forward(const Args a) {
+    extern __shared__ float sm[];
+    float *sm_p = sm;                                             // [warps][experts]
+    int *sm_count = reinterpret_cast<int *>(sm + kWarps * a.experts);   // [experts]
+    __shared__ float sm_sq[kWarps], sm_buf[kWarps];
+    __shared__ int sm_live[kWarps];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = blockIdx.x;
+    pdl_enter();
+    const uint64_t t0 = team_row(a.tokens, a.teams, team), t1 = team_row(a.tokens, a.teams, team + 1);
+    float whole = 0.f;   // one CTA: the loss of all groups
+    for (uint64_t g = t0 / a.per_group; g * a.per_group < t1; ++g) {
+        const uint64_t first = g * a.per_group, last = first + a.per_group;
+        const uint64_t b = first > t0 ? first : t0, e = last < t1 ? last : t1;
+        for (uint32_t i = threadIdx.x; i < a.experts; i += kThreads) sm_count[i] = 0;
+        __syncthreads();
+        float sum[PER] = {};
+        float squares = 0.f;
+        int live = 0;
+        for (uint64_t t = b + warp; t < e; t += kWarps) {
+            float z[PER];
+            const bool off = a.mask && a.mask[t] == 0;
+            float lse = -INFINITY, inv = 0.f, mx = 0.f;
+            uint32_t key[PER], best = 0, at = 0;
+            if (!off) {
+                load_run<T, PER>(reinterpret_cast<const T *>(a.logits) + t * a.stride, a.experts, lane, a.vec, z);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    key[i] = key_of(z[i]);
+                    if (key[i] > best) best = key[i], at = i;
+                }
+                const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+                mx = value_of(top);
+                if (top != 0u) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        z[i] = key[i] == 0u ? 0.f : ex2((z[i] - mx) * kLog2e);
+                        s += z[i];
+                    }
+                    s = warp_sum(s);
+                    inv = 1.f / s;
+                    lse = mx + logf(s);
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) sum[i] = fmaf(z[i], inv, sum[i]);
+                    squares = fmaf(lse, lse, squares);
+                    ++live;
+                }
+            }
+            if (lane == 0) a.lse[t] = lse;
+            // the k largest, one by one; lane c keeps choice c
+            int32_t my_id = -1;
+            float my_p = 0.f, total = 0.f;
+            if (lse != -INFINITY) {
+                for (uint32_t c = 0; c < a.k; ++c) {
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+                    if (top == 0u) break;
+                    const uint32_t from = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+                    const int32_t id = (int32_t)__shfl_sync(0xffffffffu, lane * PER + at, from);
+                    const float p = ex2((value_of(top) - mx) * kLog2e) * inv;
+                    total += p;
+                    if (lane == c) my_id = id, my_p = p;
+                    if (lane == from) {
+                        best = 0;
+                        uint32_t next = 0;
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            if (i == (int)at) key[i] = 0u;
+                            if (key[i] > best) best = key[i], next = i;
+                        }
+                        at = next;
+                    }
+                }
+                if (my_id >= 0) atomicAdd(&sm_count[my_id], 1);   // whole numbers: the order does not matter
+            }
+            if (lane < a.k) {
+                a.ids[t * a.k + lane] = my_id;
+                a.weights[t * a.k + lane] = my_id < 0 ? 0.f : a.renormalise ? my_p / total : my_p;
+            }
+        }
+        // the warps' sums, joined in their order
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (lane * PER + i < a.experts) sm_p[warp * a.experts + lane * PER + i] = sum[i];
+        if (lane == 0) sm_sq[warp] = squares, sm_live[warp] = live;
+        __syncthreads();
+        float sq = 0.f;
+        int n = 0;
+        for (int i = 0; i < kWarps; ++i) sq += sm_sq[i], n += sm_live[i];
+        if (b == first && e == last) {   // the whole group
+            float fp = 0.f;
+            for (uint32_t i = threadIdx.x; i < a.experts; i += kThreads) {
+                float p = 0.f;
+                for (int w = 0; w < kWarps; ++w) p += sm_p[w * a.experts + i];
+                a.counts[g * a.experts + i] = sm_count[i];
+                fp = fmaf((float)sm_count[i], p, fp);
+            }
+            fp = cta_sum(fp, sm_buf);
+            const float nf = (float)n;
+            const float l = n == 0 ? 0.f
+                                   : a.balance_weight * (fp / nf) * ((float)a.experts / ((float)a.k * nf)) + a.z_weight * (sq / nf);
+            whole += l;
+            if (threadIdx.x == 0) {
+                a.live[g] = nf;
+                if (a.teams > 1) a.group_loss[g] = l;
+            }
+        } else {
+            float *slot = a.slots + (2 * (size_t)team + (b == first && first > t0 ? 1 : 0)) * slot_floats(a.experts);
+            for (uint32_t i = threadIdx.x; i < a.experts; i += kThreads) {
+                float p = 0.f;
+                for (int w = 0; w < kWarps; ++w) p += sm_p[w * a.experts + i];
+                slot[i] = p;
+                slot[a.experts + i] = __int_as_float(sm_count[i]);
+            }
+            if (threadIdx.x == 0) slot[2 * a.experts] = sq, slot[2 * a.experts + 1] = __int_as_float(n);
+        }
+        __syncthreads();
+    }
+    if (a.teams == 1 && threadIdx.x == 0) *a.loss = whole / (float)a.groups;
+}
+
+// One cluster per group: joins the partial sums of a group that several CTAs
+// worked on.  A CTA takes a share of the experts; the loss's terms meet in rank 0.
+__global__ void __launch_bounds__(kThreads) k_balance_join(const Args a) {
+    __shared__ float sm_p[kWarps][32];
+    __shared__ int sm_c[kWarps][32];
+    __shared__ float sm_buf[kWarps], sm_rank[8];
+    cg::cluster_group cluster = cg::this_cluster();
+    const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_enter();
+    if (ranks > 1) cluster.sync();
+    const size_t sf = slot_floats(a.experts);
+    for (uint64_t g = blockIdx.x / ranks; g < a.groups; g += gridDim.x / ranks) {
+        const uint64_t first = g * a.per_group, last = first + a.per_group - 1;
+        const uint32_t p0 = team_of(a.tokens, a.teams, first), p1 = team_of(a.tokens, a.teams, last);
+        if (p0 == p1) continue;
+        const uint32_t parts = p1 - p0 + 1;
+        const uint32_t second = first > team_row(a.tokens, a.teams, p0) ? 1 : 0;
+        auto slot = [&](uint32_t i) { return a.slots + (2 * (size_t)(p0 + i) + (i == 0 ? second : 0)) * sf; };
+        float sq = 0.f;
+        int n = 0;
+        for (uint32_t i = threadIdx.x; i < parts; i += kThreads) {
+            const float *s = slot(i);
+            sq += s[2 * a.experts];
+            n += __float_as_int(s[2 * a.experts + 1]);
+        }
+        sq = cta_sum(sq, sm_buf);
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        __shared__ int sm_n[kWarps];
+        if (lane == 0) sm_n[warp] = n;
+        __syncthreads();
+        n = 0;
+        for (int i = 0; i < kWarps; ++i) n += sm_n[i];
+        // experts by 32, the parts by runs over the warps
+        float fp = 0.f;
+        for (uint32_t c = rank * 32; c < a.experts; c += ranks * 32) {
+            const uint32_t e = c + lane;
+            float p = 0.f;
+            int cnt = 0;
+            const uint32_t i0 = parts * warp / kWarps, i1 = parts * (warp + 1) / kWarps;
+            if (e < a.experts)
+#pragma unroll 4
+                for (uint32_t i = i0; i < i1; ++i) {
+                    const float *s = slot(i);
+                    p += s[e];
+                    cnt += __float_as_int(s[a.experts + e]);
+                }
+            sm_p[warp][lane] = p, sm_c[warp][lane] = cnt;
+            __syncthreads();
+            if (warp == 0 && e < a.experts) {
+                for (int w = 1; w < kWarps; ++w) p += sm_p[w][lane], cnt += sm_c[w][lane];
+                a.counts[g * a.experts + e] = cnt;
+                fp = fmaf((float)cnt, p, fp);
+            }
+            __syncthreads();
+        }
+        fp = cta_sum(fp, sm_buf);
+        if (ranks > 1) {
+            if (threadIdx.x == 0) *cluster.map_shared_rank(&sm_rank[rank], 0) = fp;
+            cluster.sync();
+            fp = 0.f;
+            if (rank == 0)
+                for (uint32_t i = 0; i < ranks; ++i) fp += sm_rank[i];
+            cluster.sync();
+        }
+        if (rank == 0 && threadIdx.x == 0) {
+            const float nf = (float)n;
+            const float l = n == 0 ? 0.f
+                                   : a.balance_weight * (fp / nf) * ((float)a.experts / ((float)a.k * nf)) + a.z_weight * (sq / nf);
+            a.live[g] = nf;
+            if (a.groups == 1) *a.loss = l;
+            else a.group_loss[g] = l;
+        }
+        __syncthreads();
+    }
+}
+
+// The groups' losses, summed in order by one CTA.
+__global__ void __launch_bounds__(kThreads) k_balance_sum(const float *group_loss, uint64_t groups, float *loss) {
+    __shared__ float buf[kWarps];
+    pdl_enter();
+    float s = 0.f;
+    for (uint64_t i = threadIdx.x; i < groups; i += kThreads) s += group_loss[i];
+    s = cta_sum(s, buf);
+    if (threadIdx.x == 0) *loss = s / (float)groups;
+}
+
+struct BackArgs {
+    const int32_t *ids, *counts;
+    const float *lse, *live, *dweights, *dloss;
+    void *dlogits;
+    uint64_t stride;
+    bool vec;
+};
+
+template <class T, int PER>
+__global__ void __launch_bounds__(kThreads) k_balance_backward(const Args a, const BackArgs q) {
+    const uint32_t lane = threadIdx.x & 31;
+    pdl_enter();
+    const uint64_t warps = (uint64_t)gridDim.x * kWarps, me = (uint64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const float dloss = q.dloss ? *q.dloss : 1.f;
+    uint64_t group = ~0ull;
+    float f[PER], scale = 0.f, share = 0.f;
+    for (uint64_t t = me; t < a.tokens; t += warps) {
+        const T *row = reinterpret_cast<const T *>(a.logits) + t * a.stride;
+        T *out = reinterpret_cast<T *>(q.dlogits) + t * q.stride;
+        const float lse = q.lse[t];
+        float z[PER];
+        if (lse == -INFINITY) {   // masked
+#pragma unroll
+            for (int i = 0; i < PER; ++i) z[i] = 0.f;
+            store_run<T, PER>(out, a.experts, lane, q.vec, z);
+            continue;
+        }
+        const uint64_t g = t / a.per_group;
+        if (g != group) {
+            group = g;
+            const float n = q.live[g];
+            scale = dloss / ((float)a.groups * n);
+            share = (float)a.experts / ((float)a.k * n);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const uint32_t e = lane * PER + i;
+                f[i] = e < a.experts ? share * (float)q.counts[g * a.experts + e] : 0.f;
+            }
+        }
+        load_run<T, PER>(row, a.experts, lane, a.vec, z);
+        // the choices: lane c has choice c
+        const bool mine = lane < a.k;
+        const int32_t id = mine ? q.ids[t * a.k + lane] : -1;
+        const bool there = id >= 0 && id < (int32_t)a.experts;
+        const float up = there && q.dweights ? q.dweights[t * a.k + lane] : 0.f;
+        const float p = there ? ex2((to_f32(row[id]) - lse) * kLog2e) : 0.f;
+        float extra, dot;
+        if (a.renormalise) {
+            const float w = p / warp_sum(p);
+            dot = warp_sum(there ? w * up : 0.f);
+            extra = w * (up - dot);
+            dot = 0.f;
+        } else {
+            extra = p * up;
+            dot = warp_sum(extra);
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            z[i] = ex2((z[i] - lse) * kLog2e);
+            s = fmaf(f[i], z[i], s);
+        }
+        s = warp_sum(s);
+        const float ab = a.balance_weight * scale;
+        const float rest = 2.f * a.z_weight * scale * lse - ab * s - dot;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) z[i] *= fmaf(ab, f[i], rest);
+        __syncwarp();
+        store_run<T, PER>(out, a.experts, lane, q.vec, z);
+        __syncwarp();   // the row is stored: the choices' elements go over it
+        if (there && q.dweights) {
+            const float fe = share * (float)q.counts[g * a.experts + id];
+            from_f32(out[id], fmaf(p, fmaf(ab, fe, rest), extra));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------- host
+
+int bad(const char *m) { return fail(BF16OPT_ERR_INVALID_ARG, std::string("balance: ") + m); }
+
+int check(const bf16opt_balance_t *d) {
+    if (!d) return bad("the descriptor is NULL");
+    if (!type_ok(d->logits_type)) return bad("unknown element type");
+    if (d->experts < 1 || d->experts > BF16OPT_BALANCE_MAX_EXPERTS) return bad("experts must lie in [1, BF16OPT_BALANCE_MAX_EXPERTS]");
+    if (d->k < 1 || d->k > d->experts || d->k > BF16OPT_BALANCE_MAX_K) return bad("k must lie in [1, min(experts, BF16OPT_BALANCE_MAX_K)]");
+    if (d->groups < 1 || d->tokens % d->groups != 0 || (d->tokens && d->groups > d->tokens)) return bad("groups must divide tokens");
+    if (d->tokens >= (1ull << 40) || d->groups >= (1ull << 40)) return bad("too many tokens");
+    if (d->tokens / d->groups >= (1ull << 31)) return bad("a group has 2^31 tokens or more");
+    if (d->logits_stride < d->experts) return bad("a row stride is below experts");
+    if (d->renormalise != 0 && d->renormalise != 1) return bad("renormalise must be 0 or 1");
+    if (!(std::isfinite(d->balance_weight) && d->balance_weight >= 0.f) || !(std::isfinite(d->z_weight) && d->z_weight >= 0.f))
+        return bad("balance_weight and z_weight must be finite and >= 0");
+    uint64_t n = 0;
+    if (!span_bytes(d->tokens, d->logits_stride, d->experts, type_bytes(d->logits_type), n)) return bad("the sizes overflow");
+    return BF16OPT_OK;
+}
+
+// CTAs of the forward pass: two per SM, each with at least 64 tokens.
+uint32_t teams_of(const bf16opt_balance_t *d, int sms) {
+    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>((uint64_t)sms * 2, d->tokens / 64));
+}
+uint64_t workspace_floats(const bf16opt_balance_t *d, uint32_t teams) {
+    return teams == 1 ? 0 : (d->groups + 3) / 4 * 4 + 2 * (uint64_t)teams * slot_floats(d->experts);
+}
+
+int per_of(uint32_t experts) {
+    int p = 1;
+    while (p * 32 < (int)experts) p *= 2;
+    return p;
+}
+
+Args args_of(const bf16opt_balance_t *d) {
+    Args a = {};
+    a.tokens = d->tokens, a.groups = d->groups, a.per_group = d->tokens / d->groups;
+    a.experts = d->experts, a.k = d->k, a.renormalise = d->renormalise;
+    a.logits = d->logits, a.stride = d->logits_stride;
+    a.mask = d->mask, a.balance_weight = d->balance_weight, a.z_weight = d->z_weight;
+    return a;
+}
+
+// Whether a lane's run of `per` elements is one aligned run in every row.
+bool runs(const void *p, uint64_t stride, uint32_t experts, int per, uint64_t elem) {
+    const uint64_t run = std::min<uint64_t>(16, per * elem);
+    return experts % per == 0 && !misaligned(p, run) && stride * elem % run == 0;
+}
+
+template <class F>
+int by_per(int per, F &&f) {
+    switch (per) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 8: return f(std::integral_constant<int, 8>());
+    case 16: return f(std::integral_constant<int, 16>());
+    default: return f(std::integral_constant<int, 32>());
+    }
+}
+
+int done(cudaError_t e) { return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "balance kernel launch"); }
+
+int workspace(const bf16opt_balance_t *d, uint64_t *bytes) {
+    bf16opt_fail_unbound(BF16OPT_OK, "");
+    const int rc = check(d);
+    if (rc != BF16OPT_OK) return rc;
+    if (!bytes) return bad("bytes is NULL");
+    const int sms = sm_count();
+    if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "balance: no CUDA device");
+    *bytes = workspace_floats(d, teams_of(d, sms)) * 4;
+    return BF16OPT_OK;
+}
+
+struct Part {
+    const void *p;
+    uint64_t n;
+};
+bool apart(std::initializer_list<Part> outs, std::initializer_list<Part> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (const Part &x : ins)
+            if (overlap(o->p, o->n, x.p, x.n)) return false;
+        for (auto e = outs.begin(); e != o; ++e)
+            if (overlap(o->p, o->n, e->p, e->n)) return false;
+    }
+    return true;
+}
+
+int forward(const bf16opt_balance_t *d, int32_t *ids, float *weights, int32_t *counts, float *loss, float *saved, void *ws,
+            uint64_t ws_bytes, void *stream) {
+    bf16opt_fail_unbound(BF16OPT_OK, "");
+    const int rc = check(d);
+    if (rc != BF16OPT_OK) return rc;
+    if (!counts || !loss || !saved || (d->tokens && (!d->logits || !ids || !weights))) return bad("a pointer is NULL");
+    const uint64_t elem = type_bytes(d->logits_type);
+    if (misaligned(d->logits, elem) || misaligned(ids, 4) || misaligned(weights, 4) || misaligned(counts, 4) ||
+        misaligned(loss, 4) || misaligned(saved, 4) || misaligned(ws, 16))
+        return fail(BF16OPT_ERR_ALIGNMENT, "balance: a pointer is not aligned to its element (workspace: 16 bytes)");
+    const int sms = sm_count();
+    if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "balance: no CUDA device");
+    const cudaStream_t st = (cudaStream_t)stream;
+    const uint64_t cb = d->groups * d->experts * 4, tk = d->tokens * d->k * 4;
+    if (d->tokens == 0) {
+        cudaError_t e = cudaMemsetAsync(counts, 0, cb, st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(loss, 0, 4, st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(saved, 0, d->groups * 4, st);
+        return done(e);
+    }
+    const uint32_t teams = teams_of(d, sms);
+    const uint64_t need = workspace_floats(d, teams) * 4;
+    if (need && (!ws || ws_bytes < need)) return bad("the workspace is too small");
+    uint64_t zb = 0;
+    span_bytes(d->tokens, d->logits_stride, d->experts, elem, zb);
+    if (!apart({{ids, tk}, {weights, tk}, {counts, cb}, {loss, 4}, {saved, (d->tokens + d->groups) * 4}, {ws, need}},
+               {{d->logits, zb}, {d->mask, d->tokens}}))
+        return bad("an output overlaps an input or another output");
+    Args a = args_of(d);
+    a.ids = ids, a.weights = weights, a.counts = counts, a.loss = loss, a.lse = saved, a.live = saved + d->tokens;
+    a.group_loss = (float *)ws, a.slots = (float *)ws + (d->groups + 3) / 4 * 4, a.teams = teams;
+    const int per = per_of(d->experts);
+    a.vec = runs(d->logits, d->logits_stride, d->experts, per, elem);
+    const size_t smem = (kWarps + 1) * (size_t)d->experts * 4;
+    int r = by_per(per, [&](auto p) {
+        constexpr int PER = decltype(p)::value;
+        Launch l{teams, (unsigned)kThreads, smem, st, 0, true};
+        return done(d->logits_type == BF16OPT_TYPE_BF16 ? launch(l, k_balance_forward<__nv_bfloat16, PER>, a)
+                                                        : launch(l, k_balance_forward<float, PER>, a));
+    });
+    if (r != BF16OPT_OK || teams == 1) return r;
+    const unsigned cluster = d->groups == 1 && (uint64_t)teams * d->experts >= 8192 ? 8 : 1;
+    Launch l{(unsigned)std::min<uint64_t>(d->groups, 1024) * cluster, (unsigned)kThreads, 0, st, cluster, true};
+    r = done(launch(l, k_balance_join, a));
+    if (r != BF16OPT_OK || d->groups == 1) return r;
+    Launch l2{1, (unsigned)kThreads, 0, st, 0, true};
+    return done(launch(l2, k_balance_sum, (const float *)a.group_loss, a.groups, loss));
+}
+
+int backward(const bf16opt_balance_t *d, const int32_t *ids, const int32_t *counts, const float *saved, const float *dweights,
+             const float *dloss, void *dlogits, uint64_t dlogits_stride, void *stream) {
+    bf16opt_fail_unbound(BF16OPT_OK, "");
+    const int rc = check(d);
+    if (rc != BF16OPT_OK) return rc;
+    if (dlogits_stride < d->experts) return bad("a row stride is below experts");
+    if (d->tokens == 0) return BF16OPT_OK;
+    if (!d->logits || !ids || !counts || !saved || !dlogits) return bad("a pointer is NULL");
+    const uint64_t elem = type_bytes(d->logits_type);
+    if (misaligned(d->logits, elem) || misaligned(dlogits, elem) || misaligned(ids, 4) || misaligned(counts, 4) ||
+        misaligned(saved, 4) || misaligned(dweights, 4) || misaligned(dloss, 4))
+        return fail(BF16OPT_ERR_ALIGNMENT, "balance: a pointer is not aligned to its element");
+    uint64_t zb = 0, gb = 0;
+    span_bytes(d->tokens, d->logits_stride, d->experts, elem, zb);
+    if (!span_bytes(d->tokens, dlogits_stride, d->experts, elem, gb)) return bad("the sizes overflow");
+    const uint64_t tk = d->tokens * d->k * 4;
+    const bool in_place = dlogits == d->logits && dlogits_stride == d->logits_stride;
+    if (!apart({{dlogits, gb}}, {{in_place ? nullptr : d->logits, zb}, {ids, tk}, {counts, d->groups * d->experts * 4},
+                                 {saved, (d->tokens + d->groups) * 4}, {dweights, tk}, {dloss, 4}}))
+        return bad("an output overlaps an input");
+    const int sms = sm_count();
+    if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "balance: no CUDA device");
+    Args a = args_of(d);
+    BackArgs q;
+    q.ids = ids, q.counts = counts, q.lse = saved, q.live = saved + d->tokens, q.dweights = dweights, q.dloss = dloss;
+    q.dlogits = dlogits, q.stride = dlogits_stride;
+    const int per = per_of(d->experts);
+    a.vec = runs(d->logits, d->logits_stride, d->experts, per, elem);
+    q.vec = runs(dlogits, dlogits_stride, d->experts, per, elem);
+    const unsigned grid = (unsigned)std::min<uint64_t>((d->tokens + kWarps - 1) / kWarps, (uint64_t)sms * 8);
+    return by_per(per, [&](auto p) {
+        constexpr int PER = decltype(p)::value;
+        Launch l{grid, (unsigned)kThreads, 0, (cudaStream_t)stream, 0, true};
+        return done(d->logits_type == BF16OPT_TYPE_BF16 ? launch(l, k_balance_backward<__nv_bfloat16, PER>, a, q)
+                                                        : launch(l, k_balance_backward<float, PER>, a, q));
+    });
+}
+
+}  // namespace
+}  // namespace bf16ops
+
+extern "C" int bf16opt_balance_workspace(const bf16opt_balance_t *d, uint64_t *bytes) {
+    return bf16ops::guarded([&] { return bf16ops::workspace(d, bytes); });
+}
+
+extern "C" int bf16opt_balance_forward(const bf16opt_balance_t *d, int32_t *ids, float *weights, int32_t *counts, float *loss,
+                                       float *saved, void *workspace, uint64_t workspace_bytes, void *stream) {
+    return bf16ops::guarded(
+        [&] { return bf16ops::forward(d, ids, weights, counts, loss, saved, workspace, workspace_bytes, stream); });
+}
+
+extern "C" int bf16opt_balance_backward(const bf16opt_balance_t *d, const int32_t *ids, const int32_t *counts,
+                                        const float *saved, const float *dweights, const float *dloss, void *dlogits,
+                                        uint64_t dlogits_stride, void *stream) {
+    return bf16ops::guarded(
+        [&] { return bf16ops::backward(d, ids, counts, saved, dweights, dloss, dlogits, dlogits_stride, stream); });
+}

@@ -23,6 +23,7 @@
 #include "../../include/bf16opt.h"
 #include "host_adam.h"
 #include "kernels.cuh"
+#include "ops_common.cuh"
 
 using namespace bf16k;
 
@@ -605,6 +606,15 @@ cudaMemoryType memory_kind(const void *p, int *device) {
 }
 
 }  // namespace
+
+// Errors of the training operators' calls (ops_common.cuh), which have no handle.
+int bf16opt_fail_unbound(int code, const char *msg) {
+    try {
+        return fail(nullptr, code, msg);
+    } catch (const std::exception &) {
+        return code;   // no memory for the message
+    }
+}
 
 extern "C" {
 

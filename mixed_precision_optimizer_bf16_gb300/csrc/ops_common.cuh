@@ -1,0 +1,185 @@
+// ops_common.cuh -- what the training operators' translation units share: typed
+// loads and stores, block reductions, and the host side's error reporting and
+// launches.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <exception>
+#include <string>
+#include <utility>
+
+#include "../../include/bf16opt.h"
+
+// Records a handle-less call's message for bf16opt_last_error(NULL) and returns
+// `code` (bf16opt.cu; not exported).
+__attribute__((visibility("hidden"))) int bf16opt_fail_unbound(int code, const char *msg);
+
+namespace bf16ops {
+
+// ------------------------------------------------------------------ device side
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// 2^x by the special-function unit, subnormal results flushed to 0.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// One 16-byte vector of the element type T: 8 bf16 or 4 FP32.
+template <class T>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ __forceinline__ static void unpack(const uint4 &v, float (&f)[8]) {
+        f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
+        f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
+    }
+    __device__ __forceinline__ static uint4 pack(const float (&f)[8]) {
+        return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    }
+};
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    __device__ __forceinline__ static void unpack(const uint4 &v, float (&f)[4]) {
+        f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+    }
+    __device__ __forceinline__ static uint4 pack(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ void from_f32(__nv_bfloat16 &d, float x) { d = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void from_f32(float &d, float x) { d = x; }
+
+// One element of a buffer whose type is known at run time (BF16OPT_TYPE_*).
+__device__ __forceinline__ float load_typed(const void *p, int type, uint64_t i) {
+    return type == BF16OPT_TYPE_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i])
+                                     : reinterpret_cast<const float *>(p)[i];
+}
+__device__ __forceinline__ void store_typed(void *p, int type, uint64_t i, float x) {
+    if (type == BF16OPT_TYPE_BF16) reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
+    else reinterpret_cast<float *>(p)[i] = x;
+}
+__device__ __forceinline__ int64_t load_index(const void *p, int type, uint64_t i) {
+    return type == BF16OPT_INDEX_I32 ? (int64_t)reinterpret_cast<const int32_t *>(p)[i]
+                                     : reinterpret_cast<const int64_t *>(p)[i];
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Programmatic dependent launch: wait for the prerequisite grids before the
+// first memory access, and let the successor be scheduled.
+__device__ __forceinline__ void pdl_enter() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// -------------------------------------------------------------------- host side
+
+inline int fail(int code, const std::string &msg) { return bf16opt_fail_unbound(code, msg.c_str()); }
+inline int fail_cuda(cudaError_t e, const char *what) {
+    return fail(BF16OPT_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+inline bool type_ok(int t) { return t == BF16OPT_TYPE_BF16 || t == BF16OPT_TYPE_F32; }
+inline bool index_ok(int t) { return t == BF16OPT_INDEX_I32 || t == BF16OPT_INDEX_I64; }
+inline uint64_t type_bytes(int t) { return t == BF16OPT_TYPE_BF16 ? 2 : 4; }
+inline uint64_t index_bytes(int t) { return t == BF16OPT_INDEX_I32 ? 4 : 8; }
+inline bool misaligned(const void *p, uint64_t bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
+
+// Rows of `len` elements, `stride` apart: the bytes they span (0 for no rows).
+// false if that does not fit 63 bits.
+inline bool span_bytes(uint64_t rows, uint64_t stride, uint64_t len, uint64_t elem, uint64_t &out) {
+    const unsigned __int128 n = rows == 0 ? 0 : ((unsigned __int128)(rows - 1) * stride + len) * elem;
+    out = (uint64_t)n;
+    return n < ((unsigned __int128)1 << 63);
+}
+inline bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+// Multiprocessors of the current device; 0 without one.  Asked once per device.
+inline int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (dev >= 0 && dev < 64)
+        if (const int n = known[dev].load(std::memory_order_relaxed)) return n;
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// An exception (an allocation of a message's string) does not cross the C ABI.
+template <class F>
+int guarded(F &&f) {
+    try {
+        return f();
+    } catch (const std::exception &) {
+        return bf16opt_fail_unbound(BF16OPT_ERR_OOM, "host allocation failed");
+    }
+}
+
+struct Launch {
+    unsigned grid, block;
+    size_t smem = 0;
+    cudaStream_t stream = nullptr;
+    unsigned cluster = 0;    // CTAs per cluster; 0: no cluster
+    bool dependent = false;  // programmatic dependent launch (the kernel calls pdl_enter)
+};
+
+template <class... KArgs, class... Args>
+cudaError_t launch(const Launch &l, void (*kernel)(KArgs...), Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(l.grid);
+    cfg.blockDim = dim3(l.block);
+    cfg.dynamicSmemBytes = l.smem;
+    cfg.stream = l.stream;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (l.cluster) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = l.cluster;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (l.dependent) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+}  // namespace bf16ops
