@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(kThreads) k_balance_sum(const float *group_los
     for (uint64_t i = threadIdx.x; i < groups; i += kThreads) s += group_loss[i];
     s = cta_sum(s, buf);
     if (threadIdx.x == 0) *loss = s / (float)groups;
+    pdl_leave();
 }
 
 struct BackArgs {

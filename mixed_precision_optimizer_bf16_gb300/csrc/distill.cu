@@ -25,10 +25,17 @@ namespace cg = cooperative_groups;
 namespace bf16ops {
 namespace {
 
-constexpr int kThreads = 256;
+#ifndef BF16K_DISTILL_THREADS
+#define BF16K_DISTILL_THREADS 256
+#endif
+#ifndef BF16K_DISTILL_U
+#define BF16K_DISTILL_U 4
+#endif
+constexpr int kThreads = BF16K_DISTILL_THREADS;
 constexpr int kWarps = kThreads / 32;
-constexpr int kU = 4;                 // vectors in flight per thread
+constexpr int kU = BF16K_DISTILL_U;                 // vectors in flight per thread
 constexpr int kMaxCluster = 8;
+constexpr int kEntries = (BF16OPT_DISTILL_MAX_K + kThreads) / kThreads;   // of one thread, the label's included
 constexpr int kResident = 3;          // CTAs per SM that the registers allow
 
 struct Args {
@@ -55,7 +62,7 @@ struct Args {
 };
 
 // Running softmax of a stream of numbers: their maximum, and the sums of
-// exp((z - max) / T) and (TWO) exp(z - max).
+// exp((z - max) / T) and of exp(z - max).
 struct Stat {
     float m, st, s1;
 };
@@ -66,12 +73,17 @@ struct Teach {
 
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.f : m; }
 
+// Each product and sum rounded by itself, so that join(a, b) and join(b, a) are the same bits.
+__device__ __forceinline__ float weighted(float a, float ea, float b, float eb) {
+    return __fadd_rn(__fmul_rn(a, ea), __fmul_rn(b, eb));
+}
+template <int POWER>
 __device__ __forceinline__ Stat join(const Stat &a, const Stat &b, float c_t) {
     Stat r;
     r.m = fmaxf(a.m, b.m);
     const float m = safe_max(r.m);
-    r.st = a.st * ex2((a.m - m) * c_t) + b.st * ex2((b.m - m) * c_t);
-    r.s1 = a.s1 * ex2((a.m - m) * kLog2e) + b.s1 * ex2((b.m - m) * kLog2e);
+    r.st = weighted(a.st, ex2((a.m - m) * c_t), b.st, ex2((b.m - m) * c_t));
+    r.s1 = POWER ? weighted(a.s1, ex2((a.m - m) * kLog2e), b.s1, ex2((b.m - m) * kLog2e)) : 0.f;
     return r;
 }
 __device__ __forceinline__ Teach join(const Teach &a, const Teach &b) {
@@ -79,9 +91,78 @@ __device__ __forceinline__ Teach join(const Teach &a, const Teach &b) {
     r.m = fmaxf(a.m, b.m);
     const float m = safe_max(r.m);
     const float ea = ex2((a.m - m) * kLog2e), eb = ex2((b.m - m) * kLog2e);
-    r.s = a.s * ea + b.s * eb;
-    r.d = (ea > 0.f ? a.d * ea : 0.f) + (eb > 0.f ? b.d * eb : 0.f);   // a d of +inf (masked z) may meet a weight of 0
+    r.s = weighted(a.s, ea, b.s, eb);
+    // a d of +inf (masked z) may meet a weight of 0
+    r.d = weighted(ea > 0.f ? a.d : 0.f, ea, eb > 0.f ? b.d : 0.f, eb);
     return r;
+}
+// Joined over the warp: first the maximum, then the sums scaled to it, so that
+// a step is a shuffle and one operation; every lane gets the same bits.
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+template <int POWER>
+__device__ __forceinline__ Stat warp_join(const Stat &a, float c_t) {
+    Stat r;
+    r.m = warp_max(a.m);
+    const float d = a.m - safe_max(r.m);
+    r.st = warp_sum(a.st * ex2(d * c_t));
+    r.s1 = POWER ? warp_sum(a.s1 * ex2(d * kLog2e)) : 0.f;
+    return r;
+}
+__device__ __forceinline__ Teach warp_join(const Teach &a) {
+    Teach r;
+    r.m = warp_max(a.m);
+    const float e = ex2((a.m - safe_max(r.m)) * kLog2e);
+    r.s = warp_sum(a.s * e);
+    r.d = warp_sum(e > 0.f ? a.d * e : 0.f);
+    return r;
+}
+
+// exp(d) from e = exp(d / T): T = POWER (2 or 4) by squaring.
+template <int POWER>
+__device__ __forceinline__ float2 powered(float2 e) {
+    const float2 q = mul2(e, e);
+    return POWER == 4 ? mul2(q, q) : q;
+}
+
+// A vector's elements as pairs.
+template <class T>
+__device__ __forceinline__ void pairs(const uint4 &v, float2 (&f)[Vec<T>::N / 2]) {
+    if constexpr (sizeof(T) == 2) {
+        f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x)), f[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+        f[2] = make_float2(bf16_lo(v.z), bf16_hi(v.z)), f[3] = make_float2(bf16_lo(v.w), bf16_hi(v.w));
+    } else {
+        f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y)), f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmax2(reinterpret_cast<const __nv_bfloat162 &>(a), reinterpret_cast<const __nv_bfloat162 &>(b));
+    return reinterpret_cast<const uint32_t &>(r);
+}
+// Largest element of U vectors (NaN passed over).
+template <class T, int U>
+__device__ __forceinline__ float largest(const uint4 (&q)[U]) {
+    if constexpr (sizeof(T) == 2) {
+        uint32_t m = max_bf16x2(max_bf16x2(q[0].x, q[0].y), max_bf16x2(q[0].z, q[0].w));
+#pragma unroll
+        for (int u = 1; u < U; ++u) m = max_bf16x2(m, max_bf16x2(max_bf16x2(q[u].x, q[u].y), max_bf16x2(q[u].z, q[u].w)));
+        return fmaxf(bf16_lo(m), bf16_hi(m));
+    } else {
+        float m = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(q[u].x), __uint_as_float(q[u].y))), fmaxf(__uint_as_float(q[u].z), __uint_as_float(q[u].w)));
+        return m;
+    }
+}
+// A vector of -inf.
+template <class T>
+__device__ __forceinline__ uint4 nothing() {
+    const uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+    return make_uint4(w, w, w, w);
 }
 
 // A row's slice of one CTA: `head` elements before the first 16-byte boundary
@@ -91,7 +172,7 @@ struct Slice {
     uint32_t tail0, lo, hi;           // first trailing element; this CTA's elements are [lo, hi)
 };
 template <class T>
-__device__ __forceinline__ Slice slice_of(const T *row, uint32_t vocab, uint32_t rank, uint32_t ranks) {
+__device__ __forceinline__ Slice slice_of(const T *row, uint32_t vocab, uint32_t rank, uint32_t ranks, uint32_t log2_ranks) {
     constexpr uint32_t N = Vec<T>::N;
     Slice s;
     const uint32_t off = (uint32_t)((uintptr_t)row & 15u) / (uint32_t)sizeof(T);
@@ -99,8 +180,8 @@ __device__ __forceinline__ Slice slice_of(const T *row, uint32_t vocab, uint32_t
     if (s.head > vocab) s.head = vocab;
     s.nv = (vocab - s.head) / N;
     s.tail0 = s.head + s.nv * N;
-    s.v0 = (uint32_t)((uint64_t)s.nv * rank / ranks);
-    s.v1 = (uint32_t)((uint64_t)s.nv * (rank + 1) / ranks);
+    s.v0 = (uint32_t)(((uint64_t)s.nv * rank) >> log2_ranks);
+    s.v1 = (uint32_t)(((uint64_t)s.nv * (rank + 1)) >> log2_ranks);
     s.lo = rank == 0 ? 0u : s.head + s.v0 * N;
     s.hi = rank + 1 == ranks ? vocab : s.head + s.v1 * N;
     return s;
@@ -120,44 +201,125 @@ __device__ __forceinline__ void store_vec(T *out, const float (&g)[Vec<T>::N], b
     }
 }
 
+// Slots of the table of ids: a power of two, at least twice the entries.
+__host__ __device__ constexpr uint32_t table_size(uint32_t k) {
+    uint32_t n = 4;
+    while (n < 2 * (k + 1)) n *= 2;
+    return n;
+}
+
 // FORWARD: the row's sums are computed here (else read from lse_in).  GRAD: the
-// gradient is written.  TWO: the sum and the gradient at temperature 1 are
-// needed next to those at T.  KEEP: the slice stays in shared memory between
-// the two (else it is read again).
-template <class T, bool FORWARD, bool GRAD, bool TWO, bool KEEP>
+// gradient is written.  POWER: 0, only the softmax at T is needed; 1, the one at
+// temperature 1 too; 2 or 4, the same with T = POWER, where exp(d) is a power
+// of exp(d / T) -- the special-function unit is what such a row is short of.
+//
+// RING: the slice's vectors pass through shared memory.  Every vector has a
+// slot that only one thread touches, so no barrier guards it: the thread copies
+// a vector in asynchronously, waits for its own copies, reads it for the sums
+// and again for the gradient, and right after the last read copies the
+// same vector of the cluster's next row in.  The next row is thus on its way while
+// this one is finished.  Without RING (a slice larger than the shared memory)
+// the gradient reads the logits a second time.
+template <class T, bool FORWARD, bool GRAD, int POWER, bool RING>
 __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, uint32_t slice_vecs) {
-    constexpr int N = Vec<T>::N;
+    constexpr int N = Vec<T>::N, P = N / 2;
+    constexpr bool kExact = sizeof(T) == 4;   // FP32 logits: z - base is formed before it is scaled
     extern __shared__ __align__(16) unsigned char smem_raw[];
     // slice | ids, x (then what the entry takes off the gradient), z of the entries
-    uint4 *keep = reinterpret_cast<uint4 *>(smem_raw);
-    int32_t *sm_id = reinterpret_cast<int32_t *>(smem_raw + (KEEP ? (size_t)slice_vecs * 16 : 0));
+    uint4 *ring = reinterpret_cast<uint4 *>(smem_raw);
+    int32_t *sm_id = reinterpret_cast<int32_t *>(smem_raw + (RING ? (size_t)slice_vecs * 16 : 0));
     float *sm_x = reinterpret_cast<float *>(sm_id + (a.k + 1));
     float *sm_z = sm_x + (a.k + 1);
-    __shared__ Stat sm_stat[kWarps];
-    __shared__ Teach sm_teach[kWarps];
-    __shared__ Stat sm_cluster[2][kMaxCluster];
+    int32_t *sm_table = reinterpret_cast<int32_t *>(sm_z + (a.k + 1));   // GRAD: [table_size(k)], ids of the slice's entries
+    __shared__ Stat sm_stat[2][kMaxCluster * kWarps];
+    __shared__ Teach sm_teach[2][kWarps];
+    __shared__ uint32_t sm_twice[2];      // the last turn of that parity in which an id came twice
+    __shared__ int32_t sm_label[2];
+    __shared__ float sm_label_z[2];
 
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    const uint32_t log2_ranks = 31 - __clz(ranks);   // a power of two
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t n_entries = a.k + 1;   // the label is the last one
+    const uint32_t n_entries = a.k + 1;   // the label is the last one, thread kThreads - 1's
     const float c_t = a.inv_t * kLog2e;
+    const uint64_t step = gridDim.x / ranks;
+    const uint32_t table = table_size(a.k);
+    if (GRAD) {
+        for (uint32_t i = tid; i < table; i += kThreads) sm_table[i] = -1;
+        if (tid < 2) sm_twice[tid] = 0;
+        __syncthreads();
+    }
     pdl_enter();
     if (FORWARD && ranks > 1) cluster.sync();   // every CTA's shared memory exists
 
-    uint32_t turn = 0;
-    for (uint64_t row = blockIdx.x / ranks; row < a.rows; row += gridDim.x / ranks) {
-        const T *z = reinterpret_cast<const T *>(a.logits) + row * a.logits_stride;
+    auto row_of = [&](uint64_t row) { return reinterpret_cast<const T *>(a.logits) + row * a.logits_stride; };
+    auto weight_of = [&](uint64_t row) { return row >= a.rows ? 0.f : a.row_weight ? a.row_weight[row] : 1.f; };
+    // entry `tid` of a row, fetched one row ahead (the others when they are needed)
+    int64_t ahead_id = -1;
+    float ahead_t = 0.f;
+    auto fetch_entry = [&](uint64_t row, float w) {
+        ahead_id = -1;
+        if (w != 0.f && tid < a.k) {
+            ahead_id = load_index(a.ids, a.ids_type, row * a.ids_stride + tid);
+            ahead_t = load_typed(a.teacher, a.teacher_type, row * a.teacher_stride + tid);
+        } else if (w != 0.f && tid == kThreads - 1 && a.ce_weight != 0.f && a.k < kThreads) {
+            ahead_id = load_index(a.labels, a.labels_type, row);
+        }
+    };
+
+    uint64_t row = blockIdx.x / ranks;
+    float w = weight_of(row);
+    fetch_entry(row, w);
+    if (RING && w != 0.f) {
+        const Slice s = slice_of(row_of(row), a.vocab, rank, ranks, log2_ranks);
+        const uint4 *zv = reinterpret_cast<const uint4 *>(row_of(row) + s.head) + s.v0;
+        for (uint32_t j = tid; j < s.v1 - s.v0; j += kThreads) copy_async16(ring + j, zv + j);
+    }
+    copy_commit();
+
+    uint32_t turn = 1;
+    for (; row < a.rows; row += step) {
+        const T *z = row_of(row);
         T *out = GRAD ? reinterpret_cast<T *>(a.dlogits) + row * a.dlogits_stride : nullptr;
-        const Slice s = slice_of(z, a.vocab, rank, ranks);
+        const Slice s = slice_of(z, a.vocab, rank, ranks, log2_ranks);
         const bool whole = GRAD && (((uintptr_t)out ^ (uintptr_t)z) & 15u) == 0;
-        const uint4 *zv = reinterpret_cast<const uint4 *>(z + s.head);
-        const float w = a.row_weight ? a.row_weight[row] : 1.f;
+        const uint4 *zv = reinterpret_cast<const uint4 *>(z + s.head) + s.v0;
+        T *ov = GRAD ? out + s.head + (size_t)s.v0 * N : nullptr;
+        const uint32_t nv = s.v1 - s.v0;
+        // the cluster's next row: what the ring is refilled from
+        const uint64_t next = row + step;
+        const float w_next = weight_of(next);
+        const uint4 *zv_next = nullptr;
+        uint32_t nv_next = 0;
+        if (RING && w_next != 0.f) {
+            const Slice sn = slice_of(row_of(next), a.vocab, rank, ranks, log2_ranks);
+            zv_next = reinterpret_cast<const uint4 *>(row_of(next) + sn.head) + sn.v0;
+            nv_next = sn.v1 - sn.v0;
+        }
+        auto refill = [&](uint32_t first) {
+            if (RING) {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const uint32_t j = first + u * kThreads;
+                    if (j < nv_next) copy_async16(ring + j, zv_next + j);
+                }
+            }
+        };
+        // vectors that the next row has and this one has not
+        auto refill_rest = [&]() {
+            if (RING) {
+                uint32_t j = tid;
+                if (nv > tid) j += (nv - tid + kThreads * kU - 1) / (kThreads * kU) * (kThreads * kU);
+                for (; j < nv_next; j += kThreads) copy_async16(ring + j, zv_next + j);
+                copy_commit();
+            }
+        };
 
         if (w == 0.f) {   // not read: zeros
             if (GRAD) {
                 float zero[N] = {};
-                for (uint32_t v = s.v0 + tid; v < s.v1; v += kThreads) store_vec<T>(out + s.head + (size_t)v * N, zero, whole);
+                for (uint32_t j = tid; j < nv; j += kThreads) store_vec<T>(ov + (size_t)j * N, zero, whole);
                 if (rank == 0 && tid < s.head) from_f32(out[tid], 0.f);
                 if (rank + 1 == ranks && tid < a.vocab - s.tail0) from_f32(out[s.tail0 + tid], 0.f);
             }
@@ -165,120 +327,164 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
                 a.loss[row] = 0.f;
                 if (a.lse_out) a.lse_out[2 * row] = a.lse_out[2 * row + 1] = 0.f;
             }
+            for (uint32_t j = tid; j < nv_next; j += kThreads) copy_async16(ring + j, zv_next + j);
+            copy_commit();
+            w = w_next;
+            fetch_entry(next, w);
             continue;
         }
 
-        // ---- the teacher's entries and the label
-        Teach te = {-INFINITY, 0.f, 0.f};
-        for (uint32_t e = tid; e < a.k; e += kThreads) {
-            const int64_t id64 = load_index(a.ids, a.ids_type, row * a.ids_stride + e);
-            const float x = load_typed(a.teacher, a.teacher_type, row * a.teacher_stride + e) * a.inv_t;
-            const bool there = id64 >= 0 && id64 < (int64_t)a.vocab && x != -INFINITY;
-            const int32_t id = there ? (int32_t)id64 : -1;
-            const float zi = there ? to_f32(z[id]) : 0.f;
-            sm_id[e] = id, sm_x[e] = x, sm_z[e] = zi;
-            if (there) {
-                const Teach one = {x, 1.f, x - zi * a.inv_t};
-                te = join(te, one);
-            }
-        }
-        if (tid == 0) {
-            int64_t id64 = -1;
-            if (a.ce_weight != 0.f) id64 = load_index(a.labels, a.labels_type, row);
-            const bool there = id64 >= 0 && id64 < (int64_t)a.vocab;
-            sm_id[a.k] = there ? (int32_t)id64 : -1;
-            sm_z[a.k] = there ? to_f32(z[id64]) : 0.f;
-        }
+        // ---- the teacher's entries and the label: z[id] is asked for here, used after the sums
+        const bool mine = ahead_id >= 0 && ahead_id < (int64_t)a.vocab;
+        const float ahead_z = mine ? to_f32(z[ahead_id]) : 0.f;
+        const float lse_teacher_in = a.teacher_lse ? a.teacher_lse[row] : 0.f;
+        const float up = GRAD ? w * (a.dloss ? a.dloss[row] : 1.f) : 0.f;
 
         // ---- the slice's running maximum and sums
+        if (RING) copy_wait<0>();
         Stat st = {-INFINITY, 0.f, 0.f};
         if (FORWARD) {
-            for (uint32_t v = s.v0 + tid; v < s.v1; v += kThreads * kU) {
+            float2 sum_t = both(0.f), sum_1 = both(0.f);
+            for (uint32_t j0 = tid; j0 < nv; j0 += kThreads * kU) {
                 uint4 q[kU];
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
-                    const uint32_t j = v + u * kThreads;
-                    if (j < s.v1) q[u] = KEEP || !GRAD ? __ldcs(zv + j) : __ldcg(zv + j);
+                    const uint32_t j = j0 + u * kThreads;
+                    q[u] = j >= nv ? nothing<T>() : RING ? ring[j] : GRAD ? __ldcg(zv + j) : __ldcs(zv + j);
                 }
+                const float mx = largest<T, kU>(q);
+                if (mx > st.m) {
+                    const float m = safe_max(st.m);
+                    sum_t = mul2(sum_t, both(ex2((m - mx) * c_t)));
+                    if (POWER) sum_1 = mul2(sum_1, both(ex2((m - mx) * kLog2e)));
+                    st.m = mx;
+                }
+                const float m = safe_max(st.m);
+                const float2 neg = both(kExact ? -m : -(m * c_t)), neg1 = both(kExact ? -m : -(m * kLog2e));
+                const float2 ct2 = both(c_t), c12 = both(kLog2e);
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
-                    const uint32_t j = v + u * kThreads;
-                    if (j >= s.v1) break;
-                    if (KEEP) keep[j - s.v0] = q[u];
-                    float f[N];
-                    Vec<T>::unpack(q[u], f);
-                    float mx = f[0];
+                    float2 f[P];
+                    pairs<T>(q[u], f);
 #pragma unroll
-                    for (int i = 1; i < N; ++i) mx = fmaxf(mx, f[i]);
-                    if (mx > st.m) {
-                        st.st *= ex2((st.m - mx) * c_t);
-                        if (TWO) st.s1 *= ex2((st.m - mx) * kLog2e);
-                        st.m = mx;
-                    }
-                    const float m = safe_max(st.m);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        st.st += ex2((f[i] - m) * c_t);
-                        if (TWO) st.s1 += ex2((f[i] - m) * kLog2e);
+                    for (int i = 0; i < P; ++i) {
+                        const float2 d = kExact ? mul2(add2(f[i], neg), ct2) : fma2(f[i], ct2, neg);
+                        const float2 e = make_float2(ex2(d.x), ex2(d.y));
+                        sum_t = add2(sum_t, e);
+                        if (POWER == 1) {
+                            const float2 d1 = kExact ? mul2(add2(f[i], neg1), c12) : fma2(f[i], c12, neg1);
+                            sum_1 = add2(sum_1, make_float2(ex2(d1.x), ex2(d1.y)));
+                        } else if (POWER > 1) {
+                            sum_1 = add2(sum_1, powered<POWER>(e));
+                        }
                     }
                 }
+                if (!GRAD) refill(j0);
             }
+            if (!GRAD) refill_rest();
+            st.st = sum_t.x + sum_t.y;
+            st.s1 = sum_1.x + sum_1.y;
             uint32_t at = 0xffffffffu;
             if (rank == 0 && tid < s.head) at = tid;
             else if (rank + 1 == ranks && tid >= 32 && tid - 32 < a.vocab - s.tail0) at = s.tail0 + tid - 32;
             if (at != 0xffffffffu) {
                 const float f = to_f32(z[at]);
                 const float one = f == -INFINITY ? 0.f : f == f ? 1.f : f;   // a NaN stays one
-                st = join(st, Stat{f == f ? f : -INFINITY, one, one}, c_t);
+                st = join<POWER>(st, Stat{f == f ? f : -INFINITY, one, one}, c_t);
             }
         }
 
-        // ---- joined over the CTA and the cluster, in a fixed order
+        // ---- the entries' softmax
+        Teach te = {-INFINITY, 0.f, 0.f};
+        uint32_t slots[kEntries];   // where this thread's entries stand in the table
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            if (FORWARD) {
-                Stat b;
-                b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-                b.st = __shfl_xor_sync(0xffffffffu, st.st, o);
-                b.s1 = TWO ? __shfl_xor_sync(0xffffffffu, st.s1, o) : 0.f;
-                st = join(st, b, c_t);
+        for (int i = 0; i < kEntries; ++i) slots[i] = 0xffffffffu;
+        // An id of the slice goes into an open table; one that is there already has come twice.
+        auto enter = [&](int32_t id) -> uint32_t {
+            if (!GRAD || id < (int32_t)s.lo || id >= (int32_t)s.hi) return 0xffffffffu;
+            uint32_t at = (uint32_t)id * 2654435761u & (table - 1);
+            for (uint32_t n = 0; n < table; ++n) {
+                const int32_t was = atomicCAS(&sm_table[at], -1, id);
+                if (was == -1) return at;
+                if (was == id) break;
+                at = (at + 1) & (table - 1);
             }
-            Teach t;
-            t.m = __shfl_xor_sync(0xffffffffu, te.m, o);
-            t.s = __shfl_xor_sync(0xffffffffu, te.s, o);
-            t.d = __shfl_xor_sync(0xffffffffu, te.d, o);
-            te = join(te, t);
-        }
-        if (lane == 0) {
-            sm_stat[warp] = st;
-            sm_teach[warp] = te;
-        }
-        __syncthreads();
-        te = sm_teach[0];
+            sm_twice[turn & 1] = turn;
+            return 0xffffffffu;
+        };
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) te = join(te, sm_teach[i]);
+        for (int i = 0; i < kEntries; ++i) {
+            const uint32_t e = tid + i * kThreads;
+            if (e >= a.k) break;
+            const int64_t id64 = i == 0 ? ahead_id : load_index(a.ids, a.ids_type, row * a.ids_stride + e);
+            const float x = (i == 0 ? ahead_t : load_typed(a.teacher, a.teacher_type, row * a.teacher_stride + e)) * a.inv_t;
+            const bool there = id64 >= 0 && id64 < (int64_t)a.vocab && x != -INFINITY;
+            const int32_t id = there ? (int32_t)id64 : -1;
+            const float zi = i == 0 ? ahead_z : there ? to_f32(z[id]) : 0.f;
+            sm_id[e] = id, sm_x[e] = x, sm_z[e] = zi;
+            if (there) {
+                const Teach one = {x, 1.f, x - zi * a.inv_t};
+                te = i == 0 ? one : join(te, one);
+            }
+            slots[i] = enter(id);
+        }
+        if (tid == kThreads - 1) {   // the label, entry a.k
+            int64_t id64 = -1;
+            float zi = ahead_z;
+            if (a.ce_weight != 0.f) {
+                id64 = ahead_id;
+                if (a.k >= kThreads) {   // this thread had an entry to fetch
+                    id64 = load_index(a.labels, a.labels_type, row);
+                    zi = id64 >= 0 && id64 < (int64_t)a.vocab ? to_f32(z[id64]) : 0.f;
+                }
+            }
+            const int32_t id = id64 >= 0 && id64 < (int64_t)a.vocab ? (int32_t)id64 : -1;
+            sm_id[a.k] = sm_label[turn & 1] = id;
+            sm_z[a.k] = sm_label_z[turn & 1] = zi;
+            slots[kEntries - 1] = enter(id);
+        }
+        w = w_next;
+        fetch_entry(next, w_next);
+
+        // ---- joined over the warp, and the warps of the cluster (CTA) in one step
+        const uint32_t teach_warps = min((uint32_t)kWarps, (a.k + 31) / 32);
+        if (warp < teach_warps) {
+            te = warp_join(te);
+            if (lane == 0) sm_teach[turn & 1][warp] = te;
+        }
+        if (FORWARD) {
+            st = warp_join<POWER>(st, c_t);
+            if (lane < ranks) {
+                Stat *to = &sm_stat[turn & 1][rank * kWarps + warp];
+                *(ranks > 1 ? cluster.map_shared_rank(to, lane) : to) = st;
+            }
+        }
+        if (FORWARD && ranks > 1) cluster.sync();
+        else __syncthreads();
+        if (!GRAD && (rank != 0 || warp != 0)) {   // the loss is one warp's
+            ++turn;
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i)
+            if (slots[i] != 0xffffffffu) sm_table[slots[i]] = -1;   // everybody's are in: for the next row
+        te = lane < teach_warps ? sm_teach[turn & 1][lane] : Teach{-INFINITY, 0.f, 0.f};
+        te = warp_join(te);
         float lse_t, lse_1;
         bool empty;   // no logit but -inf in the row
         // q = exp2((z - base_t) c_t + rest_t): the base near the row's top, so that z - base is exact there
         float base_t, rest_t, base_1, rest_1;
         if (FORWARD) {
-            st = sm_stat[0];
-#pragma unroll
-            for (int i = 1; i < kWarps; ++i) st = join(st, sm_stat[i], c_t);
-            if (ranks > 1) {
-                if (tid < ranks) *cluster.map_shared_rank(&sm_cluster[turn & 1][rank], tid) = st;
-                cluster.sync();
-                st = sm_cluster[turn & 1][0];
-                for (uint32_t i = 1; i < ranks; ++i) st = join(st, sm_cluster[turn & 1][i], c_t);
-                ++turn;
-            }
+            st = lane < ranks * kWarps ? sm_stat[turn & 1][lane] : Stat{-INFINITY, 0.f, 0.f};
+            if (lane + 32 < ranks * kWarps) st = join<POWER>(st, sm_stat[turn & 1][lane + 32], c_t);
+            st = warp_join<POWER>(st, c_t);
             const float m = safe_max(st.m);
             empty = st.m == -INFINITY && st.st == 0.f;
             lse_t = empty ? -INFINITY : m * a.inv_t + logf(st.st);
-            lse_1 = empty ? -INFINITY : (TWO ? m + logf(st.s1) : lse_t);
+            lse_1 = empty ? -INFINITY : (POWER ? m + logf(st.s1) : lse_t);
             base_t = base_1 = m;
             rest_t = empty ? 0.f : -log2f(st.st);
-            rest_1 = TWO && !empty ? -log2f(st.s1) : 0.f;
+            rest_1 = POWER && !empty ? -log2f(st.s1) : 0.f;
         } else {
             lse_t = a.lse_in[2 * row];
             lse_1 = a.lse_in[2 * row + 1];
@@ -291,73 +497,99 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
 
         // ---- the row's loss
         const bool some = te.s != 0.f;   // the teacher has entries here (NaN counts)
-        const float lse_teacher = a.teacher_lse ? a.teacher_lse[row] : te.m + logf(te.s);
+        const float lse_teacher = a.teacher_lse ? lse_teacher_in : te.m + logf(te.s);
         const float mass = !some ? 0.f : a.teacher_lse ? te.s * ex2((te.m - lse_teacher) * kLog2e) : te.s == te.s ? 1.f : te.s;
-        const bool has_label = sm_id[a.k] >= 0;
+        const bool has_label = sm_label[turn & 1] >= 0;
         if (FORWARD && rank == 0 && tid == 0) {
+            const float wr = a.row_weight ? a.row_weight[row] : 1.f;
             float kl = 0.f, ce = 0.f;
             if (some && a.kl_weight != 0.f && mass != 0.f)
                 kl = empty ? INFINITY : a.kl_weight * a.temperature * a.temperature * mass * (te.d / te.s + (lse_t - lse_teacher));
-            if (has_label) ce = empty ? INFINITY : a.ce_weight * (lse_1 - sm_z[a.k]);
-            a.loss[row] = w * (kl + ce);
+            if (has_label) ce = empty ? INFINITY : a.ce_weight * (lse_1 - sm_label_z[turn & 1]);
+            a.loss[row] = wr * (kl + ce);
             if (a.lse_out) a.lse_out[2 * row] = lse_t, a.lse_out[2 * row + 1] = lse_1;
         }
         if (!GRAD) {
-            __syncthreads();
+            ++turn;
             continue;
         }
 
         // ---- the gradient of the slice
-        const float up = w * (a.dloss ? a.dloss[row] : 1.f);
         const float hard = has_label ? up * a.ce_weight : 0.f;
         const float soft = up * a.kl_weight * a.temperature;
         float a_t = soft * mass, a_1 = hard;
-        if (!TWO) a_t += hard, a_1 = 0.f;   // both terms have the same softmax
-        auto grad = [&](float f) {
-            float g = a_t * ex2(fmaf(f - base_t, c_t, rest_t));
-            if (TWO) g = fmaf(a_1, ex2(fmaf(f - base_1, kLog2e, rest_1)), g);
+        if (!POWER) a_t += hard, a_1 = 0.f;   // both terms have the same softmax
+        // T = POWER: exp2((z - base_1) log2e + rest_1) = e^POWER exp2(shift), e the value at T; e <= 1 and the
+        // factor stays with a_1 (where a factor overflows, the top's own e is as small as the factor is large)
+        const float shift = POWER > 1 ? ((base_t - base_1) * kLog2e + (rest_1 - (float)POWER * rest_t)) : 0.f;
+        const float a_p = POWER > 1 ? a_1 * ex2(shift) : 0.f;
+        const float off_t = fmaf(-base_t, c_t, rest_t), off_1 = fmaf(-base_1, kLog2e, rest_1);
+        auto grad2 = [&](float2 f) {
+            const float2 d = kExact ? fma2(add2(f, both(-base_t)), both(c_t), both(rest_t)) : fma2(f, both(c_t), both(off_t));
+            const float2 e = make_float2(ex2(d.x), ex2(d.y));
+            float2 g = mul2(both(a_t), e);
+            if (POWER == 1) {
+                const float2 d1 = kExact ? fma2(add2(f, both(-base_1)), both(kLog2e), both(rest_1)) : fma2(f, both(kLog2e), both(off_1));
+                g = fma2(both(a_1), make_float2(ex2(d1.x), ex2(d1.y)), g);
+            } else if (POWER > 1) {
+                g = fma2(both(a_p), powered<POWER>(e), g);
+            }
             return g;
         };
-        for (uint32_t v = s.v0 + tid; v < s.v1; v += kThreads * kU) {
+        auto grad = [&](float f) { return grad2(make_float2(f, f)).x; };
+        for (uint32_t j0 = tid; j0 < nv; j0 += kThreads * kU) {
             uint4 q[kU];
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
-                const uint32_t j = v + u * kThreads;
-                if (j < s.v1) q[u] = KEEP ? keep[j - s.v0] : __ldcs(zv + j);
+                const uint32_t j = j0 + u * kThreads;
+                if (j < nv) q[u] = RING ? ring[j] : __ldcs(zv + j);
             }
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
-                const uint32_t j = v + u * kThreads;
-                if (j >= s.v1) break;
-                float f[N];
-                Vec<T>::unpack(q[u], f);
+                const uint32_t j = j0 + u * kThreads;
+                if (j >= nv) break;
+                float2 f[P];
+                pairs<T>(q[u], f);
+                float g[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) f[i] = grad(f[i]);
-                store_vec<T>(out + s.head + (size_t)j * N, f, whole);
+                for (int i = 0; i < P; ++i) {
+                    const float2 r = grad2(f[i]);
+                    g[2 * i] = r.x, g[2 * i + 1] = r.y;
+                }
+                store_vec<T>(ov + (size_t)j * N, g, whole);
             }
+            refill(j0);
         }
+        refill_rest();
         if (rank == 0 && tid < s.head) from_f32(out[tid], grad(to_f32(z[tid])));
         if (rank + 1 == ranks && tid < a.vocab - s.tail0)
             from_f32(out[s.tail0 + tid], grad(to_f32(z[s.tail0 + tid])));
 
         // ---- the entries of the slice
+        const bool twice = sm_twice[turn & 1] == turn;
+        ++turn;
         for (uint32_t e = tid; e < a.k; e += kThreads) sm_x[e] = soft * ex2((sm_x[e] - lse_teacher) * kLog2e);
-        if (tid == 0) sm_x[a.k] = hard;
+        if (tid == kThreads - 1) sm_x[a.k] = hard;
         __syncthreads();   // the slice's gradient is stored, the entries' parts are there
-        for (uint32_t e = tid; e < n_entries; e += kThreads) {
+        auto put = [&](uint32_t e) {
             const int32_t id = sm_id[e];
-            if (id < (int32_t)s.lo || id >= (int32_t)s.hi) continue;
-            bool first = true;
-            float take = 0.f;
-            for (uint32_t o = 0; o < n_entries; ++o)
-                if (sm_id[o] == id) {
-                    if (o < e) first = false;
-                    take += sm_x[o];
-                }
-            if (first) from_f32(out[id], grad(sm_z[e]) - take);
-        }
-        __syncthreads();   // the next row overwrites the entries
+            if (id < (int32_t)s.lo || id >= (int32_t)s.hi) return;
+            float take = sm_x[e];
+            if (twice) {   // the first of its id collects the others' parts, in their order
+                take = 0.f;
+                for (uint32_t o = 0; o < n_entries; ++o)
+                    if (sm_id[o] == id) {
+                        if (o < e) return;
+                        take += sm_x[o];
+                    }
+            }
+            from_f32(out[id], grad(sm_z[e]) - take);
+        };
+        for (uint32_t e = tid; e < a.k; e += kThreads) put(e);
+        if (tid == kThreads - 1) put(a.k);
+        if (twice) __syncthreads();   // the next row overwrites entries that others read
     }
+    pdl_leave();
 }
 
 // ---------------------------------------------------------------------- host
@@ -414,24 +646,30 @@ int check(const bf16opt_distill_t *d, const void *loss, bool need_loss, const vo
 // cluster can be made large enough for that, else one.
 constexpr size_t kSliceMany = 64 * 1024, kSliceOne = 200 * 1024;
 
-template <class T, bool FORWARD, bool GRAD, bool TWO, bool KEEP>
+template <class T, bool FORWARD, bool GRAD, int POWER, bool RING>
 int launch_k(const Args &a, unsigned cluster, uint32_t slice_vecs, int sms, cudaStream_t stream) {
-    auto k = k_distill<T, FORWARD, GRAD, TWO, KEEP>;
-    const size_t smem = (KEEP ? (size_t)slice_vecs * 16 : 0) + (size_t)(a.k + 1) * 12;
-    if (smem > 48 * 1024) {
+    auto k = k_distill<T, FORWARD, GRAD, POWER, RING>;
+    const size_t smem = (RING ? (size_t)slice_vecs * 16 : 0) + (size_t)(a.k + 1) * 12 + (GRAD ? table_size(a.k) * 4 : 0);
+    if (smem > 32 * 1024) {   // with the static arrays, more than a kernel may have unasked
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return fail_cuda(e, "distill kernel attribute");
     }
-    // enough clusters for the CTAs that an SM can hold; each walks its rows
-    const uint64_t per_sm = std::min<uint64_t>(kResident, (227 * 1024) / (smem + 2048));
-    const uint64_t clusters = std::min<uint64_t>(a.rows, std::max<uint64_t>(1, (uint64_t)sms * per_sm / cluster));
-    Launch l{(unsigned)(clusters * cluster), (unsigned)kThreads, smem, stream, cluster, true};
+    // As many clusters as fit at once (a cluster of eight cannot use every SM: those of a
+    // processing cluster are not a multiple of it), each walking its rows; more would run as a
+    // second wave: 57 clusters where 51 fit took 639 us on 2048 rows of 250880 bf16.
+    Launch l{cluster, (unsigned)kThreads, smem, stream, cluster, true};
+    int fit = 0;
+    const cudaError_t eo = clusters_that_fit(l, k, fit);
+    if (eo != cudaSuccess || fit < 1) return fail_cuda(eo != cudaSuccess ? eo : cudaErrorLaunchOutOfResources, "distill occupancy");
+    // in equal shares: with 512 rows, 47 clusters of at most 11 rows instead of 51
+    const uint64_t turns = (a.rows + fit - 1) / fit;
+    l.grid = (unsigned)((a.rows + turns - 1) / turns) * cluster;
     const cudaError_t e = launch(l, k, a, slice_vecs);
     return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "distill kernel launch");
 }
 
 template <class T, bool FORWARD, bool GRAD>
-int launch_t(const Args &a, bool two, cudaStream_t stream) {
+int launch_t(const Args &a, int power, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "distill: no CUDA device");
     // CTAs per row: enough that a slice leaves room for three CTAs per SM, and,
@@ -442,14 +680,17 @@ int launch_t(const Args &a, bool two, cudaStream_t stream) {
                                      (a.rows * cluster * 2 <= (uint64_t)sms && vecs / cluster > 4 * kThreads)))
         cluster *= 2;
     const uint32_t slice_vecs = (uint32_t)(vecs / cluster + 1);
-    const bool keep = FORWARD && GRAD && (size_t)slice_vecs * 16 <= kSliceOne;
-    if constexpr (FORWARD && GRAD) {
-        if (keep)
-            return two ? launch_k<T, FORWARD, GRAD, true, true>(a, cluster, slice_vecs, sms, stream)
-                       : launch_k<T, FORWARD, GRAD, false, true>(a, cluster, slice_vecs, sms, stream);
+    auto go = [&](auto p) {
+        constexpr int POWER = decltype(p)::value;
+        return (size_t)slice_vecs * 16 <= kSliceOne ? launch_k<T, FORWARD, GRAD, POWER, true>(a, cluster, slice_vecs, sms, stream)
+                                                    : launch_k<T, FORWARD, GRAD, POWER, false>(a, cluster, slice_vecs, sms, stream);
+    };
+    switch (power) {
+    case 0: return go(std::integral_constant<int, 0>());
+    case 2: return go(std::integral_constant<int, 2>());
+    case 4: return go(std::integral_constant<int, 4>());
+    default: return go(std::integral_constant<int, 1>());
     }
-    return two ? launch_k<T, FORWARD, GRAD, true, false>(a, cluster, slice_vecs, sms, stream)
-               : launch_k<T, FORWARD, GRAD, false, false>(a, cluster, slice_vecs, sms, stream);
 }
 
 template <bool FORWARD, bool GRAD>
@@ -470,9 +711,10 @@ int run(const bf16opt_distill_t *d, const float *lse_in, const float *dloss, flo
     a.inv_t = 1.f / a.temperature;
     a.dloss = dloss, a.lse_in = lse_in, a.loss = loss, a.lse_out = lse_out;
     a.dlogits = dlogits, a.dlogits_stride = dlogits_stride;
-    const bool two = a.ce_weight != 0.f && a.temperature != 1.f;
-    return d->logits_type == BF16OPT_TYPE_BF16 ? launch_t<__nv_bfloat16, FORWARD, GRAD>(a, two, (cudaStream_t)stream)
-                                               : launch_t<float, FORWARD, GRAD>(a, two, (cudaStream_t)stream);
+    int power = a.ce_weight == 0.f || a.temperature == 1.f ? 0 : 1;
+    if (power && (a.temperature == 2.f || a.temperature == 4.f)) power = (int)a.temperature;
+    return d->logits_type == BF16OPT_TYPE_BF16 ? launch_t<__nv_bfloat16, FORWARD, GRAD>(a, power, (cudaStream_t)stream)
+                                               : launch_t<float, FORWARD, GRAD>(a, power, (cudaStream_t)stream);
 }
 
 }  // namespace

@@ -5,10 +5,12 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <exception>
+#include <mutex>
 #include <string>
 #include <utility>
 
@@ -34,6 +36,38 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two FP32 numbers in one register pair: one instruction for both.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t &>(r)) : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t &>(r)) : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(r))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+    return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// 16 bytes from global to shared memory without registers in between; the
+// thread's copies up to a commit are one group.
+__device__ __forceinline__ void copy_async16(void *smem, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most N of this thread's newest groups are in flight.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -88,12 +122,14 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Programmatic dependent launch: wait for the prerequisite grids before the
-// first memory access, and let the successor be scheduled.
-__device__ __forceinline__ void pdl_enter() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
+// Programmatic dependent launch: pdl_enter waits for the prerequisite grids
+// before the first memory access; pdl_leave, at a CTA's end, lets the successor's CTAs be
+// scheduled once every CTA has come that far.  (Allowed at the start,
+// they take the slots that come free first: a successor of one or two CTAs per SM
+// then sits on part of the SMs.  The router's two passes over 262144 x 256 took
+// 741 us back to back that way, 533 us one at a time.)
+__device__ __forceinline__ void pdl_enter() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_leave() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // -------------------------------------------------------------------- host side
 
@@ -156,6 +192,47 @@ struct Launch {
     unsigned cluster = 0;    // CTAs per cluster; 0: no cluster
     bool dependent = false;  // programmatic dependent launch (the kernel calls pdl_enter)
 };
+
+// Clusters of this launch that the device holds at once.  The question costs
+// tens of microseconds, so the answers are kept, by kernel, device and shape.
+template <class... KArgs>
+cudaError_t clusters_that_fit(const Launch &l, void (*kernel)(KArgs...), int &n) {
+    struct Known {
+        const void *kernel;
+        int device;
+        unsigned cluster, block;
+        size_t smem;
+        int n;
+    };
+    static std::mutex mu;
+    static Known known[64];
+    static unsigned used = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const void *key = reinterpret_cast<const void *>(kernel);
+    std::lock_guard<std::mutex> lock(mu);
+    for (unsigned i = 0; i < std::min(used, 64u); ++i) {
+        const Known &k = known[i];
+        if (k.kernel == key && k.device == dev && k.cluster == l.cluster && k.block == l.block && k.smem == l.smem) {
+            n = k.n;
+            return cudaSuccess;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(l.cluster);
+    cfg.blockDim = dim3(l.block);
+    cfg.dynamicSmemBytes = l.smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = l.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e == cudaSuccess) known[used++ % 64] = Known{key, dev, l.cluster, l.block, l.smem, n};
+    return e;
+}
 
 template <class... KArgs, class... Args>
 cudaError_t launch(const Launch &l, void (*kernel)(KArgs...), Args &&...args) {
