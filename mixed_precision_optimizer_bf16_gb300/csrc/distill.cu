@@ -26,7 +26,7 @@ namespace bf16ops {
 namespace {
 
 #ifndef BF16K_DISTILL_THREADS
-#define BF16K_DISTILL_THREADS 256
+#define BF16K_DISTILL_THREADS 384
 #endif
 #ifndef BF16K_DISTILL_U
 #define BF16K_DISTILL_U 4
@@ -36,7 +36,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kU = BF16K_DISTILL_U;                 // vectors in flight per thread
 constexpr int kMaxCluster = 8;
 constexpr int kEntries = (BF16OPT_DISTILL_MAX_K + kThreads) / kThreads;   // of one thread, the label's included
-constexpr int kResident = 3;          // CTAs per SM that the registers allow
+constexpr int kResident = 768 / kThreads;   // CTAs per SM that the registers allow
 
 struct Args {
     uint64_t rows;
@@ -213,25 +213,26 @@ __host__ __device__ constexpr uint32_t table_size(uint32_t k) {
 // temperature 1 too; 2 or 4, the same with T = POWER, where exp(d) is a power
 // of exp(d / T) -- the special-function unit is what such a row is short of.
 //
-// RING: the slice's vectors pass through shared memory.  Every vector has a
-// slot that only one thread touches, so no barrier guards it: the thread copies
-// a vector in asynchronously, waits for its own copies, reads it for the sums
-// and again for the gradient, and right after the last read copies the
-// same vector of the cluster's next row in.  The next row is thus on its way while
-// this one is finished.  Without RING (a slice larger than the shared memory)
-// the gradient reads the logits a second time.
-template <class T, bool FORWARD, bool GRAD, int POWER, bool RING>
-__global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, uint32_t slice_vecs) {
+// A slice passes through a ring of shared memory, `depth` groups of kU vectors
+// of every thread.  A slot is touched by one thread alone, so no barrier guards
+// it: the thread copies its vectors in asynchronously, waits for its own copies
+// and, after the last use, copies in what comes `depth` groups later -- of this row
+// or of the cluster's next ones.  With both passes (FORWARD and GRAD) the slice's last
+// `depth` groups stay in the ring for the gradient, which starts with them; the ones
+// before are read a second time, from L2, where the row still is.
+template <class T, bool FORWARD, bool GRAD, int POWER>
+__global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, uint32_t depth) {
     constexpr int N = Vec<T>::N, P = N / 2;
+    constexpr uint32_t kGroup = kThreads * kU;
     constexpr bool kExact = sizeof(T) == 4;   // FP32 logits: z - base is formed before it is scaled
     extern __shared__ __align__(16) unsigned char smem_raw[];
     // slice | ids, x (then what the entry takes off the gradient), z of the entries
     uint4 *ring = reinterpret_cast<uint4 *>(smem_raw);
-    int32_t *sm_id = reinterpret_cast<int32_t *>(smem_raw + (RING ? (size_t)slice_vecs * 16 : 0));
+    int32_t *sm_id = reinterpret_cast<int32_t *>(smem_raw + (size_t)depth * kGroup * 16);
     float *sm_x = reinterpret_cast<float *>(sm_id + (a.k + 1));
     float *sm_z = sm_x + (a.k + 1);
     int32_t *sm_table = reinterpret_cast<int32_t *>(sm_z + (a.k + 1));   // GRAD: [table_size(k)], ids of the slice's entries
-    __shared__ Stat sm_stat[2][kMaxCluster * kWarps];
+    __shared__ Stat sm_stat[2][kMaxCluster * kWarps];   // [turn][rank][warp]
     __shared__ Teach sm_teach[2][kWarps];
     __shared__ uint32_t sm_twice[2];      // the last turn of that parity in which an id came twice
     __shared__ int32_t sm_label[2];
@@ -268,15 +269,85 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
         }
     };
 
+    // a row's numbers, asked for one row ahead
+    struct Scalars {
+        float up, teacher_lse, lse_t, lse_1;
+    };
+    auto scalars_of = [&](uint64_t row) {
+        Scalars v = {1.f, 0.f, 0.f, 0.f};
+        if (row < a.rows) {
+            if (GRAD && a.dloss) v.up = a.dloss[row];
+            if (a.teacher_lse) v.teacher_lse = a.teacher_lse[row];
+            if (!FORWARD) v.lse_t = a.lse_in[2 * row], v.lse_1 = a.lse_in[2 * row + 1];
+        }
+        return v;
+    };
+
     uint64_t row = blockIdx.x / ranks;
-    float w = weight_of(row);
+    float w = weight_of(row), w_next = weight_of(row + step);
+    Scalars now = scalars_of(row);
     fetch_entry(row, w);
-    if (RING && w != 0.f) {
-        const Slice s = slice_of(row_of(row), a.vocab, rank, ranks, log2_ranks);
-        const uint4 *zv = reinterpret_cast<const uint4 *>(row_of(row) + s.head) + s.v0;
-        for (uint32_t j = tid; j < s.v1 - s.v0; j += kThreads) copy_async16(ring + j, zv + j);
-    }
-    copy_commit();
+    // What is copied into the ring next: group `i` of `n` of a row's slice.
+    struct Cursor {
+        uint64_t row;
+        const uint4 *zv;
+        uint32_t nv, n, i;
+        bool again;        // the groups that did not stay, for the gradient
+        float w, w_next;
+    } cur = {};
+    auto open_row = [&]() {   // the first row from cur.row on that is read at all
+        while (cur.row < a.rows && cur.w == 0.f) cur.row += step, cur.w = cur.w_next, cur.w_next = weight_of(cur.row + step);
+        if (cur.row < a.rows) {
+            const Slice s = slice_of(row_of(cur.row), a.vocab, rank, ranks, log2_ranks);
+            cur.zv = reinterpret_cast<const uint4 *>(row_of(cur.row) + s.head) + s.v0 + tid;
+            cur.nv = s.v1 - s.v0;
+            cur.n = max(1u, (cur.nv + kGroup - 1) / kGroup);
+            cur.i = 0;
+            cur.again = false;
+        }
+    };
+    uint32_t issued = 0, issued_slot = 0;
+    auto issue = [&]() {
+        if (cur.row < a.rows) {
+            uint4 *to = ring + issued_slot * kGroup + tid;
+            const uint4 *from = cur.zv + cur.i * kGroup;
+            if ((cur.i + 1) * kGroup <= cur.nv) {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) copy_async16(to + u * kThreads, from + u * kThreads);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    if (cur.i * kGroup + u * kThreads + tid < cur.nv) copy_async16(to + u * kThreads, from + u * kThreads);
+            }
+            ++cur.i;
+            const bool over = cur.i == (cur.again ? cur.n - depth : cur.n);
+            if (over && FORWARD && GRAD && !cur.again && cur.n > depth) {
+                cur.again = true;
+                cur.i = 0;
+            } else if (over) {
+                cur.row += step, cur.w = cur.w_next, cur.w_next = weight_of(cur.row + step);
+                open_row();
+            }
+        }
+        copy_commit();
+        ++issued;
+        issued_slot = issued_slot + 1 == depth ? 0 : issued_slot + 1;
+    };
+    cur.row = row, cur.w = w, cur.w_next = w_next;
+    open_row();
+    for (uint32_t i = 0; i < depth; ++i) issue();
+    uint32_t seen = 0, slot = 0;   // groups of the ring that have been waited for, and the slot of the next
+    // the next group of the ring, once it is there: `full` without looking at the slice's end
+    auto take = [&](uint4 (&q)[kU], uint32_t i, uint32_t nv) {
+        copy_wait_for(issued - 1 - seen);
+        const uint4 *from = ring + slot * kGroup + tid;
+        const bool full = (i + 1) * kGroup <= nv;
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            q[u] = full || i * kGroup + u * kThreads + tid < nv ? from[u * kThreads] : nothing<T>();
+        ++seen;
+        slot = slot + 1 == depth ? 0 : slot + 1;
+    };
 
     uint32_t turn = 1;
     for (; row < a.rows; row += step) {
@@ -287,34 +358,10 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
         const uint4 *zv = reinterpret_cast<const uint4 *>(z + s.head) + s.v0;
         T *ov = GRAD ? out + s.head + (size_t)s.v0 * N : nullptr;
         const uint32_t nv = s.v1 - s.v0;
-        // the cluster's next row: what the ring is refilled from
+        const uint32_t n = max(1u, (nv + kGroup - 1) / kGroup), stay = n > depth ? n - depth : 0u;   // groups from `stay` on stay
         const uint64_t next = row + step;
-        const float w_next = weight_of(next);
-        const uint4 *zv_next = nullptr;
-        uint32_t nv_next = 0;
-        if (RING && w_next != 0.f) {
-            const Slice sn = slice_of(row_of(next), a.vocab, rank, ranks, log2_ranks);
-            zv_next = reinterpret_cast<const uint4 *>(row_of(next) + sn.head) + sn.v0;
-            nv_next = sn.v1 - sn.v0;
-        }
-        auto refill = [&](uint32_t first) {
-            if (RING) {
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const uint32_t j = first + u * kThreads;
-                    if (j < nv_next) copy_async16(ring + j, zv_next + j);
-                }
-            }
-        };
-        // vectors that the next row has and this one has not
-        auto refill_rest = [&]() {
-            if (RING) {
-                uint32_t j = tid;
-                if (nv > tid) j += (nv - tid + kThreads * kU - 1) / (kThreads * kU) * (kThreads * kU);
-                for (; j < nv_next; j += kThreads) copy_async16(ring + j, zv_next + j);
-                copy_commit();
-            }
-        };
+        const float w_after = weight_of(next + step);
+        const Scalars then = scalars_of(next);
 
         if (w == 0.f) {   // not read: zeros
             if (GRAD) {
@@ -327,9 +374,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
                 a.loss[row] = 0.f;
                 if (a.lse_out) a.lse_out[2 * row] = a.lse_out[2 * row + 1] = 0.f;
             }
-            for (uint32_t j = tid; j < nv_next; j += kThreads) copy_async16(ring + j, zv_next + j);
-            copy_commit();
-            w = w_next;
+            w = w_next, w_next = w_after, now = then;
             fetch_entry(next, w);
             continue;
         }
@@ -337,21 +382,15 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
         // ---- the teacher's entries and the label: z[id] is asked for here, used after the sums
         const bool mine = ahead_id >= 0 && ahead_id < (int64_t)a.vocab;
         const float ahead_z = mine ? to_f32(z[ahead_id]) : 0.f;
-        const float lse_teacher_in = a.teacher_lse ? a.teacher_lse[row] : 0.f;
-        const float up = GRAD ? w * (a.dloss ? a.dloss[row] : 1.f) : 0.f;
+        const float up = w * now.up, wr = w;
 
         // ---- the slice's running maximum and sums
-        if (RING) copy_wait<0>();
         Stat st = {-INFINITY, 0.f, 0.f};
         if (FORWARD) {
             float2 sum_t = both(0.f), sum_1 = both(0.f);
-            for (uint32_t j0 = tid; j0 < nv; j0 += kThreads * kU) {
+            for (uint32_t i = 0; i < n; ++i) {
                 uint4 q[kU];
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const uint32_t j = j0 + u * kThreads;
-                    q[u] = j >= nv ? nothing<T>() : RING ? ring[j] : GRAD ? __ldcg(zv + j) : __ldcs(zv + j);
-                }
+                take(q, i, nv);
                 const float mx = largest<T, kU>(q);
                 if (mx > st.m) {
                     const float m = safe_max(st.m);
@@ -379,9 +418,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
                         }
                     }
                 }
-                if (!GRAD) refill(j0);
+                if (!GRAD || i < stay) issue();
             }
-            if (!GRAD) refill_rest();
             st.st = sum_t.x + sum_t.y;
             st.s1 = sum_1.x + sum_1.y;
             uint32_t at = 0xffffffffu;
@@ -443,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
             sm_z[a.k] = sm_label_z[turn & 1] = zi;
             slots[kEntries - 1] = enter(id);
         }
-        w = w_next;
         fetch_entry(next, w_next);
+        w = w_next, w_next = w_after;
 
         // ---- joined over the warp, and the warps of the cluster (CTA) in one step
         const uint32_t teach_warps = min((uint32_t)kWarps, (a.k + 31) / 32);
@@ -462,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
         if (FORWARD && ranks > 1) cluster.sync();
         else __syncthreads();
         if (!GRAD && (rank != 0 || warp != 0)) {   // the loss is one warp's
+            now = then;
             ++turn;
             continue;
         }
@@ -476,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
         float base_t, rest_t, base_1, rest_1;
         if (FORWARD) {
             st = lane < ranks * kWarps ? sm_stat[turn & 1][lane] : Stat{-INFINITY, 0.f, 0.f};
-            if (lane + 32 < ranks * kWarps) st = join<POWER>(st, sm_stat[turn & 1][lane + 32], c_t);
+            for (uint32_t i = lane + 32; i < ranks * kWarps; i += 32) st = join<POWER>(st, sm_stat[turn & 1][i], c_t);
             st = warp_join<POWER>(st, c_t);
             const float m = safe_max(st.m);
             empty = st.m == -INFINITY && st.st == 0.f;
@@ -486,8 +525,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
             rest_t = empty ? 0.f : -log2f(st.st);
             rest_1 = POWER && !empty ? -log2f(st.s1) : 0.f;
         } else {
-            lse_t = a.lse_in[2 * row];
-            lse_1 = a.lse_in[2 * row + 1];
+            lse_t = now.lse_t;
+            lse_1 = now.lse_1;
             empty = lse_t == -INFINITY;
             base_t = empty ? 0.f : lse_t * a.temperature;
             rest_t = empty ? 0.f : fmaf(lse_t, a.temperature, -base_t) * -c_t;
@@ -497,11 +536,11 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
 
         // ---- the row's loss
         const bool some = te.s != 0.f;   // the teacher has entries here (NaN counts)
-        const float lse_teacher = a.teacher_lse ? lse_teacher_in : te.m + logf(te.s);
+        const float lse_teacher = a.teacher_lse ? now.teacher_lse : te.m + logf(te.s);
         const float mass = !some ? 0.f : a.teacher_lse ? te.s * ex2((te.m - lse_teacher) * kLog2e) : te.s == te.s ? 1.f : te.s;
         const bool has_label = sm_label[turn & 1] >= 0;
+        now = then;
         if (FORWARD && rank == 0 && tid == 0) {
-            const float wr = a.row_weight ? a.row_weight[row] : 1.f;
             float kl = 0.f, ce = 0.f;
             if (some && a.kl_weight != 0.f && mass != 0.f)
                 kl = empty ? INFINITY : a.kl_weight * a.temperature * a.temperature * mass * (te.d / te.s + (lse_t - lse_teacher));
@@ -537,30 +576,41 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
             return g;
         };
         auto grad = [&](float f) { return grad2(make_float2(f, f)).x; };
-        for (uint32_t j0 = tid; j0 < nv; j0 += kThreads * kU) {
-            uint4 q[kU];
+        auto grad_group = [&](const uint4 (&q)[kU], uint32_t i) {
+            const bool full = (i + 1) * kGroup <= nv;
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
-                const uint32_t j = j0 + u * kThreads;
-                if (j < nv) q[u] = RING ? ring[j] : __ldcs(zv + j);
-            }
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const uint32_t j = j0 + u * kThreads;
-                if (j >= nv) break;
+                const uint32_t j = i * kGroup + u * kThreads + tid;
+                if (!full && j >= nv) break;
                 float2 f[P];
                 pairs<T>(q[u], f);
                 float g[N];
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const float2 r = grad2(f[i]);
-                    g[2 * i] = r.x, g[2 * i + 1] = r.y;
+                for (int k = 0; k < P; ++k) {
+                    const float2 r = grad2(f[k]);
+                    g[2 * k] = r.x, g[2 * k + 1] = r.y;
                 }
                 store_vec<T>(ov + (size_t)j * N, g, whole);
             }
-            refill(j0);
+        };
+        if (FORWARD) {   // the groups that stayed: the last ones seen
+            uint32_t at = n - stay > slot ? slot + depth - (n - stay) : slot - (n - stay);
+            for (uint32_t i = stay; i < n; ++i) {
+                const uint4 *from = ring + at * kGroup + tid;
+                uint4 q[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) q[u] = from[u * kThreads];
+                at = at + 1 == depth ? 0 : at + 1;
+                grad_group(q, i);
+                issue();
+            }
         }
-        refill_rest();
+        for (uint32_t i = 0; i < (FORWARD ? stay : n); ++i) {
+            uint4 q[kU];
+            take(q, i, nv);
+            grad_group(q, i);
+            issue();
+        }
         if (rank == 0 && tid < s.head) from_f32(out[tid], grad(to_f32(z[tid])));
         if (rank + 1 == ranks && tid < a.vocab - s.tail0)
             from_f32(out[s.tail0 + tid], grad(to_f32(z[s.tail0 + tid])));
@@ -642,14 +692,20 @@ int check(const bf16opt_distill_t *d, const void *loss, bool need_loss, const vo
     return BF16OPT_OK;
 }
 
-// Shared memory that a slice may take: three CTAs of an SM's 227 KB where the
-// cluster can be made large enough for that, else one.
-constexpr size_t kSliceMany = 64 * 1024, kSliceOne = 200 * 1024;
+// Shared memory of the ring: two CTAs per SM.
+#ifndef BF16K_DISTILL_RING
+#define BF16K_DISTILL_RING 100
+#endif
+#ifndef BF16K_DISTILL_OVER
+#define BF16K_DISTILL_OVER 3
+#endif
+constexpr size_t kRingBytes = BF16K_DISTILL_RING * 1024;
 
-template <class T, bool FORWARD, bool GRAD, int POWER, bool RING>
-int launch_k(const Args &a, unsigned cluster, uint32_t slice_vecs, int sms, cudaStream_t stream) {
-    auto k = k_distill<T, FORWARD, GRAD, POWER, RING>;
-    const size_t smem = (RING ? (size_t)slice_vecs * 16 : 0) + (size_t)(a.k + 1) * 12 + (GRAD ? table_size(a.k) * 4 : 0);
+template <class T, bool FORWARD, bool GRAD, int POWER>
+int launch_k(const Args &a, unsigned cluster, cudaStream_t stream) {
+    auto k = k_distill<T, FORWARD, GRAD, POWER>;
+    const uint32_t depth = (uint32_t)(kRingBytes / (kThreads * kU * 16));
+    const size_t smem = (size_t)depth * kThreads * kU * 16 + (size_t)(a.k + 1) * 12 + (GRAD ? table_size(a.k) * 4 : 0);
     if (smem > 32 * 1024) {   // with the static arrays, more than a kernel may have unasked
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return fail_cuda(e, "distill kernel attribute");
@@ -664,7 +720,7 @@ int launch_k(const Args &a, unsigned cluster, uint32_t slice_vecs, int sms, cuda
     // in equal shares: with 512 rows, 47 clusters of at most 11 rows instead of 51
     const uint64_t turns = (a.rows + fit - 1) / fit;
     l.grid = (unsigned)((a.rows + turns - 1) / turns) * cluster;
-    const cudaError_t e = launch(l, k, a, slice_vecs);
+    const cudaError_t e = launch(l, k, a, depth);
     return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "distill kernel launch");
 }
 
@@ -672,18 +728,16 @@ template <class T, bool FORWARD, bool GRAD>
 int launch_t(const Args &a, int power, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "distill: no CUDA device");
-    // CTAs per row: enough that a slice leaves room for three CTAs per SM, and,
-    // with few rows, enough that the SMs are used.
+    // CTAs per row: so many that the rows in flight, but for what the rings hold of
+    // them, take less than half of L2; and, with few rows, so many that the SMs are used.
     const uint64_t vecs = a.vocab / Vec<T>::N + 1;
     unsigned cluster = 1;
-    while (cluster < kMaxCluster && ((vecs * 16 + cluster - 1) / cluster > kSliceMany ||
-                                     (a.rows * cluster * 2 <= (uint64_t)sms && vecs / cluster > 4 * kThreads)))
+    while (cluster < kMaxCluster && ((GRAD && FORWARD && vecs * 16 / cluster > kRingBytes * BF16K_DISTILL_OVER) ||
+                                     (a.rows * cluster <= (uint64_t)sms && vecs / cluster > 4 * kThreads)))
         cluster *= 2;
-    const uint32_t slice_vecs = (uint32_t)(vecs / cluster + 1);
     auto go = [&](auto p) {
         constexpr int POWER = decltype(p)::value;
-        return (size_t)slice_vecs * 16 <= kSliceOne ? launch_k<T, FORWARD, GRAD, POWER, true>(a, cluster, slice_vecs, sms, stream)
-                                                    : launch_k<T, FORWARD, GRAD, POWER, false>(a, cluster, slice_vecs, sms, stream);
+        return launch_k<T, FORWARD, GRAD, POWER>(a, cluster, stream);
     };
     switch (power) {
     case 0: return go(std::integral_constant<int, 0>());

@@ -70,6 +70,25 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// The same for a number that is the same in all threads; above 7 it waits for more than it need.
+__device__ __forceinline__ void copy_wait_for(uint32_t n) {
+    switch (n) {
+    case 0: copy_wait<0>(); break;
+    case 1: copy_wait<1>(); break;
+    case 2: copy_wait<2>(); break;
+    case 3: copy_wait<3>(); break;
+    case 4: copy_wait<4>(); break;
+    case 5: copy_wait<5>(); break;
+    case 6: copy_wait<6>(); break;
+    default: copy_wait<7>(); break;
+    }
+}
+
+// Asks for a run of global memory in L2: 16-byte aligned, a multiple of 16 bytes.
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // One 16-byte vector of the element type T: 8 bf16 or 4 FP32.
