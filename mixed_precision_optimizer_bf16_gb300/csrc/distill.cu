@@ -25,18 +25,32 @@ namespace cg = cooperative_groups;
 namespace bf16ops {
 namespace {
 
-#ifndef BF16K_DISTILL_THREADS
-#define BF16K_DISTILL_THREADS 384
-#endif
 #ifndef BF16K_DISTILL_U
 #define BF16K_DISTILL_U 4
 #endif
-constexpr int kThreads = BF16K_DISTILL_THREADS;
-constexpr int kWarps = kThreads / 32;
-constexpr int kU = BF16K_DISTILL_U;                 // vectors in flight per thread
+#ifndef BF16K_DISTILL_SMALL
+#define BF16K_DISTILL_SMALL 192
+#endif
+#ifndef BF16K_DISTILL_LARGE
+#define BF16K_DISTILL_LARGE 256
+#endif
+constexpr int kU = BF16K_DISTILL_U;   // vectors of a thread in a group
 constexpr int kMaxCluster = 8;
-constexpr int kEntries = (BF16OPT_DISTILL_MAX_K + kThreads) / kThreads;   // of one thread, the label's included
-constexpr int kResident = 768 / kThreads;   // CTAs per SM that the registers allow
+constexpr int kSmall = BF16K_DISTILL_SMALL, kLarge = BF16K_DISTILL_LARGE;   // threads of a CTA
+#ifndef BF16K_DISTILL_LIMIT
+#define BF16K_DISTILL_LIMIT 5000
+#endif
+#ifndef BF16K_DISTILL_RES_SMALL
+#define BF16K_DISTILL_RES_SMALL 4
+#endif
+#ifndef BF16K_DISTILL_RES_LARGE
+#define BF16K_DISTILL_RES_LARGE 2
+#endif
+// CTAs of an SM, and groups in the ring of each, by their threads.
+__host__ __device__ constexpr int resident(int threads) { return threads == kLarge ? BF16K_DISTILL_RES_LARGE : BF16K_DISTILL_RES_SMALL; }
+__host__ __device__ constexpr int ring_depth(int threads) { return 200 * 1024 / resident(threads) / (threads * kU * 16); }
+// Entries of one thread, the label's included.
+__host__ __device__ constexpr int entries(int threads) { return (BF16OPT_DISTILL_MAX_K + threads) / threads; }
 
 struct Args {
     uint64_t rows;
@@ -98,11 +112,6 @@ __device__ __forceinline__ Teach join(const Teach &a, const Teach &b) {
 }
 // Joined over the warp: first the maximum, then the sums scaled to it, so that
 // a step is a shuffle and one operation; every lane gets the same bits.
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
 template <int POWER>
 __device__ __forceinline__ Stat warp_join(const Stat &a, float c_t) {
     Stat r;
@@ -220,10 +229,11 @@ __host__ __device__ constexpr uint32_t table_size(uint32_t k) {
 // or of the cluster's next ones.  With both passes (FORWARD and GRAD) the slice's last
 // `depth` groups stay in the ring for the gradient, which starts with them; the ones
 // before are read a second time, from L2, where the row still is.
-template <class T, bool FORWARD, bool GRAD, int POWER>
-__global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, uint32_t depth) {
+template <int kThreads, class T, bool FORWARD, bool GRAD, int POWER>
+__global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const Args a) {
     constexpr int N = Vec<T>::N, P = N / 2;
-    constexpr uint32_t kGroup = kThreads * kU;
+    constexpr uint32_t kGroup = kThreads * kU, depth = ring_depth(kThreads);
+    constexpr int kWarps = kThreads / 32, kEntries = entries(kThreads);
     constexpr bool kExact = sizeof(T) == 4;   // FP32 logits: z - base is formed before it is scaled
     extern __shared__ __align__(16) unsigned char smem_raw[];
     // slice | ids, x (then what the entry takes off the gradient), z of the entries
@@ -256,19 +266,24 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
 
     auto row_of = [&](uint64_t row) { return reinterpret_cast<const T *>(a.logits) + row * a.logits_stride; };
     auto weight_of = [&](uint64_t row) { return row >= a.rows ? 0.f : a.row_weight ? a.row_weight[row] : 1.f; };
-    // entry `tid` of a row, fetched one row ahead (the others when they are needed)
-    int64_t ahead_id = -1;
-    float ahead_t = 0.f;
-    auto fetch_entry = [&](uint64_t row, float w) {
-        ahead_id = -1;
-        if (w != 0.f && tid < a.k) {
-            ahead_id = load_index(a.ids, a.ids_type, row * a.ids_stride + tid);
-            ahead_t = load_typed(a.teacher, a.teacher_type, row * a.teacher_stride + tid);
-        } else if (w != 0.f && tid == kThreads - 1 && a.ce_weight != 0.f && a.k < kThreads) {
-            ahead_id = load_index(a.labels, a.labels_type, row);
-        }
+    // Entry `tid` of a row (of thread kThreads - 1 the label, where it has no entry; further
+    // entries when they are needed): its id and logit are asked for two rows ahead, the student's
+    // logit at the id one row ahead.
+    struct Entry {
+        int64_t id;
+        float t;
     };
-
+    auto fetch_entry = [&](uint64_t row, float w) {
+        Entry e = {-1, 0.f};
+        if (w != 0.f && tid < a.k) {
+            e.id = load_index(a.ids, a.ids_type, row * a.ids_stride + tid);
+            e.t = load_typed(a.teacher, a.teacher_type, row * a.teacher_stride + tid);
+        } else if (w != 0.f && tid == kThreads - 1 && a.ce_weight != 0.f && a.k < kThreads) {
+            e.id = load_index(a.labels, a.labels_type, row);
+        }
+        return e;
+    };
+    auto fetch_z = [&](uint64_t row, const Entry &e) { return e.id >= 0 && e.id < (int64_t)a.vocab ? to_f32(row_of(row)[e.id]) : 0.f; };
     // a row's numbers, asked for one row ahead
     struct Scalars {
         float up, teacher_lse, lse_t, lse_1;
@@ -286,7 +301,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
     uint64_t row = blockIdx.x / ranks;
     float w = weight_of(row), w_next = weight_of(row + step);
     Scalars now = scalars_of(row);
-    fetch_entry(row, w);
+    Entry entry = fetch_entry(row, w), entry_next = fetch_entry(row + step, w_next);
+    float entry_z = fetch_z(row, entry);
     // What is copied into the ring next: group `i` of `n` of a row's slice.
     struct Cursor {
         uint64_t row;
@@ -307,17 +323,20 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
         }
     };
     uint32_t issued = 0, issued_slot = 0;
+    // what is read again comes in at normal priority, all else to be dropped first
+    const uint64_t once = l2_policy_first(), twice_read = l2_policy_normal();
     auto issue = [&]() {
         if (cur.row < a.rows) {
             uint4 *to = ring + issued_slot * kGroup + tid;
             const uint4 *from = cur.zv + cur.i * kGroup;
+            const uint64_t policy = FORWARD && GRAD && !cur.again && cur.n > depth && cur.i < cur.n - depth ? twice_read : once;
             if ((cur.i + 1) * kGroup <= cur.nv) {
 #pragma unroll
-                for (int u = 0; u < kU; ++u) copy_async16(to + u * kThreads, from + u * kThreads);
+                for (int u = 0; u < kU; ++u) copy_async16(to + u * kThreads, from + u * kThreads, policy);
             } else {
 #pragma unroll
                 for (int u = 0; u < kU; ++u)
-                    if (cur.i * kGroup + u * kThreads + tid < cur.nv) copy_async16(to + u * kThreads, from + u * kThreads);
+                    if (cur.i * kGroup + u * kThreads + tid < cur.nv) copy_async16(to + u * kThreads, from + u * kThreads, policy);
             }
             ++cur.i;
             const bool over = cur.i == (cur.again ? cur.n - depth : cur.n);
@@ -375,13 +394,13 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
                 if (a.lse_out) a.lse_out[2 * row] = a.lse_out[2 * row + 1] = 0.f;
             }
             w = w_next, w_next = w_after, now = then;
-            fetch_entry(next, w);
+            entry = entry_next, entry_next = fetch_entry(next + step, w_next);
+            entry_z = fetch_z(next, entry);
             continue;
         }
 
-        // ---- the teacher's entries and the label: z[id] is asked for here, used after the sums
-        const bool mine = ahead_id >= 0 && ahead_id < (int64_t)a.vocab;
-        const float ahead_z = mine ? to_f32(z[ahead_id]) : 0.f;
+        const Entry entry_after = fetch_entry(next + step, w_after);
+        const float z_next = fetch_z(next, entry_next);
         const float up = w * now.up, wr = w;
 
         // ---- the slice's running maximum and sums
@@ -454,11 +473,11 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
         for (int i = 0; i < kEntries; ++i) {
             const uint32_t e = tid + i * kThreads;
             if (e >= a.k) break;
-            const int64_t id64 = i == 0 ? ahead_id : load_index(a.ids, a.ids_type, row * a.ids_stride + e);
-            const float x = (i == 0 ? ahead_t : load_typed(a.teacher, a.teacher_type, row * a.teacher_stride + e)) * a.inv_t;
+            const int64_t id64 = i == 0 ? entry.id : load_index(a.ids, a.ids_type, row * a.ids_stride + e);
+            const float x = (i == 0 ? entry.t : load_typed(a.teacher, a.teacher_type, row * a.teacher_stride + e)) * a.inv_t;
             const bool there = id64 >= 0 && id64 < (int64_t)a.vocab && x != -INFINITY;
             const int32_t id = there ? (int32_t)id64 : -1;
-            const float zi = i == 0 ? ahead_z : there ? to_f32(z[id]) : 0.f;
+            const float zi = i == 0 ? entry_z : there ? to_f32(z[id]) : 0.f;
             sm_id[e] = id, sm_x[e] = x, sm_z[e] = zi;
             if (there) {
                 const Teach one = {x, 1.f, x - zi * a.inv_t};
@@ -468,9 +487,9 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
         }
         if (tid == kThreads - 1) {   // the label, entry a.k
             int64_t id64 = -1;
-            float zi = ahead_z;
+            float zi = entry_z;
             if (a.ce_weight != 0.f) {
-                id64 = ahead_id;
+                id64 = entry.id;
                 if (a.k >= kThreads) {   // this thread had an entry to fetch
                     id64 = load_index(a.labels, a.labels_type, row);
                     zi = id64 >= 0 && id64 < (int64_t)a.vocab ? to_f32(z[id64]) : 0.f;
@@ -481,17 +500,19 @@ __global__ void __launch_bounds__(kThreads, kResident) k_distill(const Args a, u
             sm_z[a.k] = sm_label_z[turn & 1] = zi;
             slots[kEntries - 1] = enter(id);
         }
-        fetch_entry(next, w_next);
+        entry = entry_next, entry_next = entry_after, entry_z = z_next;
         w = w_next, w_next = w_after;
 
         // ---- joined over the warp, and the warps of the cluster (CTA) in one step
         const uint32_t teach_warps = min((uint32_t)kWarps, (a.k + 31) / 32);
-        if (warp < teach_warps) {
+        if (warp < teach_warps) {   // (both, so that their shuffles run side by side)
             te = warp_join(te);
+            if (FORWARD) st = warp_join<POWER>(st, c_t);
             if (lane == 0) sm_teach[turn & 1][warp] = te;
+        } else if (FORWARD) {
+            st = warp_join<POWER>(st, c_t);
         }
         if (FORWARD) {
-            st = warp_join<POWER>(st, c_t);
             if (lane < ranks) {
                 Stat *to = &sm_stat[turn & 1][rank * kWarps + warp];
                 *(ranks > 1 ? cluster.map_shared_rank(to, lane) : to) = st;
@@ -692,20 +713,10 @@ int check(const bf16opt_distill_t *d, const void *loss, bool need_loss, const vo
     return BF16OPT_OK;
 }
 
-// Shared memory of the ring: two CTAs per SM.
-#ifndef BF16K_DISTILL_RING
-#define BF16K_DISTILL_RING 100
-#endif
-#ifndef BF16K_DISTILL_OVER
-#define BF16K_DISTILL_OVER 3
-#endif
-constexpr size_t kRingBytes = BF16K_DISTILL_RING * 1024;
-
-template <class T, bool FORWARD, bool GRAD, int POWER>
+template <int kThreads, class T, bool FORWARD, bool GRAD, int POWER>
 int launch_k(const Args &a, unsigned cluster, cudaStream_t stream) {
-    auto k = k_distill<T, FORWARD, GRAD, POWER>;
-    const uint32_t depth = (uint32_t)(kRingBytes / (kThreads * kU * 16));
-    const size_t smem = (size_t)depth * kThreads * kU * 16 + (size_t)(a.k + 1) * 12 + (GRAD ? table_size(a.k) * 4 : 0);
+    auto k = k_distill<kThreads, T, FORWARD, GRAD, POWER>;
+    const size_t smem = (size_t)ring_depth(kThreads) * kThreads * kU * 16 + (size_t)(a.k + 1) * 12 + (GRAD ? table_size(a.k) * 4 : 0);
     if (smem > 32 * 1024) {   // with the static arrays, more than a kernel may have unasked
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return fail_cuda(e, "distill kernel attribute");
@@ -720,7 +731,7 @@ int launch_k(const Args &a, unsigned cluster, cudaStream_t stream) {
     // in equal shares: with 512 rows, 47 clusters of at most 11 rows instead of 51
     const uint64_t turns = (a.rows + fit - 1) / fit;
     l.grid = (unsigned)((a.rows + turns - 1) / turns) * cluster;
-    const cudaError_t e = launch(l, k, a, depth);
+    const cudaError_t e = launch(l, k, a);
     return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "distill kernel launch");
 }
 
@@ -730,14 +741,19 @@ int launch_t(const Args &a, int power, cudaStream_t stream) {
     if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "distill: no CUDA device");
     // CTAs per row: so many that the rows in flight, but for what the rings hold of
     // them, take less than half of L2; and, with few rows, so many that the SMs are used.
+    constexpr bool kBoth = FORWARD && GRAD;
     const uint64_t vecs = a.vocab / Vec<T>::N + 1;
+    const bool large = kBoth && vecs > BF16K_DISTILL_LIMIT;
+    const uint64_t ring = large ? (uint64_t)ring_depth(kLarge) * kU * kLarge : (uint64_t)ring_depth(kSmall) * kU * kSmall;
     unsigned cluster = 1;
-    while (cluster < kMaxCluster && ((GRAD && FORWARD && vecs * 16 / cluster > kRingBytes * BF16K_DISTILL_OVER) ||
-                                     (a.rows * cluster <= (uint64_t)sms && vecs / cluster > 4 * kThreads)))
+    while (cluster < kMaxCluster && ((kBoth && vecs / cluster > ring * 3) ||
+                                     (a.rows * cluster <= (uint64_t)sms && vecs / cluster > 4 * kSmall)))
         cluster *= 2;
     auto go = [&](auto p) {
         constexpr int POWER = decltype(p)::value;
-        return launch_k<T, FORWARD, GRAD, POWER>(a, cluster, stream);
+        if constexpr (kBoth)
+            if (large) return launch_k<kLarge, T, FORWARD, GRAD, POWER>(a, cluster, stream);
+        return launch_k<kSmall, T, FORWARD, GRAD, POWER>(a, cluster, stream);
     };
     switch (power) {
     case 0: return go(std::integral_constant<int, 0>());

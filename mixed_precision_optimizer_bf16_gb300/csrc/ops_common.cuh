@@ -31,6 +31,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Largest of the warp's values (NaN passed over), in every lane.
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // 2^x by the special-function unit, subnormal results flushed to 0.
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -60,8 +67,21 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // 16 bytes from global to shared memory without registers in between; the
 // thread's copies up to a commit are one group.
-__device__ __forceinline__ void copy_async16(void *smem, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(src) : "memory");
+__device__ __forceinline__ void copy_async16(void *smem, const void *src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(src),
+                 "l"(policy)
+                 : "memory");
+}
+// L2 policies for data that is read once, and for data that is read again soon.
+__device__ __forceinline__ uint64_t l2_policy_first() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t l2_policy_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Until at most N of this thread's newest groups are in flight.
@@ -82,11 +102,6 @@ __device__ __forceinline__ void copy_wait_for(uint32_t n) {
     case 6: copy_wait<6>(); break;
     default: copy_wait<7>(); break;
     }
-}
-
-// Asks for a run of global memory in L2: 16-byte aligned, a multiple of 16 bytes.
-__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;
