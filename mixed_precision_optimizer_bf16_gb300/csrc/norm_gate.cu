@@ -16,6 +16,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ops_common.cuh"
 
@@ -234,7 +235,7 @@ k_norm_forward(const Args a, const TS *x, const TB *y, TS *r, TB *h, float *stat
 // ----------------------------------------------------------------------- backward
 
 constexpr int kColumns = 4096;   // columns of one CTA: 512 threads of 8
-constexpr int kSums = 8;
+constexpr int kSums = 8;      // per row
 
 struct BackArgs {
     const void *dr, *dh, *r, *y;
@@ -244,7 +245,8 @@ struct BackArgs {
     // [2 teams][hidden] of the gates' that straddle teams
     float *part, *gate_part;
     uint32_t teams;
-    bool need_weights, shared_gate;   // shared_gate: rows share gate rows and dgate is wanted
+    uint32_t want;         // bits: the weights' gradients asked for, in the order of part
+    bool shared_gate;      // rows share gate rows and dgate is wanted
 };
 
 // Rows [first(p), first(p + 1)) are team p's.
@@ -287,11 +289,65 @@ __device__ __forceinline__ float warp_sum8(const float (&s)[8], uint32_t lane) {
 }
 __device__ __forceinline__ uint32_t lane_value(uint32_t lane) { return (lane & 1) * 4 + (lane & 2) + ((lane & 4) >> 2); }
 
-template <class TB, class TS, bool VEC>
-__global__ void __launch_bounds__(512, 1) k_norm_backward(const Args a, const BackArgs q) {
-    // [2][CTAs of the cluster][8 sums]
-    __shared__ float sm_sums[2][16][kSums];        // [turn][warp]
-    __shared__ float sm_cluster[2][4][kSums];      // [turn][rank]
+// Eight columns of a row as four pairs.
+struct Cols {
+    float2 v[4];
+};
+template <class T>
+__device__ __forceinline__ Cols unpack8(const uint4 *p, uint32_t stride) {
+    Cols c;
+    const uint4 a = p[0];
+    if constexpr (sizeof(T) == 2) {
+        c.v[0] = make_float2(bf16_lo(a.x), bf16_hi(a.x)), c.v[1] = make_float2(bf16_lo(a.y), bf16_hi(a.y));
+        c.v[2] = make_float2(bf16_lo(a.z), bf16_hi(a.z)), c.v[3] = make_float2(bf16_lo(a.w), bf16_hi(a.w));
+    } else {
+        const uint4 b = p[stride];
+        c.v[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y)), c.v[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+        c.v[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y)), c.v[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+    }
+    return c;
+}
+__device__ __forceinline__ Cols all8(float x) {
+    Cols c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.v[i] = both(x);
+    return c;
+}
+__device__ __forceinline__ Cols cols_of(const float (&f)[8]) {
+    Cols c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+    return c;
+}
+template <bool VEC, class T>
+__device__ __forceinline__ void store_cols(T *row, uint32_t n, uint32_t threads, uint32_t t, const Cols &c) {
+    const float f[8] = {c.v[0].x, c.v[0].y, c.v[1].x, c.v[1].y, c.v[2].x, c.v[2].y, c.v[3].x, c.v[3].y};
+    store8<VEC>(row, n, 0, threads, t, f);
+}
+__device__ __forceinline__ float2 sigmoid2(float2 x) { return make_float2(sigmoid(x.x), sigmoid(x.y)); }
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+constexpr int kBackThreads = kColumns / 8;
+
+// 16-byte units of one row that a thread keeps in the ring: y, dh, [gate] of the
+// branch's type, r, dr of the stream's.
+template <class TB, class TS, bool GATE>
+__host__ __device__ constexpr int ring_units() {
+    return (GATE ? 3 : 2) * (int)sizeof(TB) / 2 + 2 * (int)sizeof(TS) / 2;
+}
+
+// A team (a CTA, or a cluster that shares the columns) walks down its rows in two
+// overlapped steps: the sums of row k + 1 are taken and published while those of
+// row k are still on their way, then row k's outputs are written.  The rows
+// come through a ring in shared memory whose slots belong to one thread each, filled
+// by asynchronous copies `depth` rows ahead.  VEC: rows of whole 16-byte vectors;
+// else elements are loaded one by one, twice, and there is no ring.
+template <class TB, class TS, bool VEC, bool GATE>
+__global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a, const BackArgs q, uint32_t depth) {
+    constexpr int UNITS = ring_units<TB, TS, GATE>(), UB = sizeof(TB) / 2, US = sizeof(TS) / 2;
+    extern __shared__ __align__(16) unsigned char ring_raw[];
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const uint32_t threads = blockDim.x, t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = threads / 32;
@@ -299,149 +355,252 @@ __global__ void __launch_bounds__(512, 1) k_norm_backward(const Args a, const Ba
     // this CTA's columns: [c0, c0 + n)
     const uint32_t c0 = rank * threads * 8;
     const uint32_t n = c0 < a.hidden ? min(a.hidden - c0, threads * 8) : 0u;
+    const bool mine = VEC && column<true>(0, threads, t, 0) < n;
     const float inv_h = 1.f / (float)a.hidden;
-    const bool pre = a.pre.kind != BF16OPT_NORM_NONE, post = a.post.kind != BF16OPT_NORM_NONE;
+    const bool pre = a.pre.kind != BF16OPT_NORM_NONE && q.dh, post = a.post.kind != BF16OPT_NORM_NONE;
     const bool pre_layer = a.pre.kind == BF16OPT_NORM_LAYER, post_layer = a.post.kind == BF16OPT_NORM_LAYER;
     pdl_enter();
     if (ranks > 1) cluster.sync();
 
-    const uint32_t wb = a.weight_type == BF16OPT_TYPE_BF16 ? 2 : 4;
-    auto at = [&](const void *w) { return w ? (const void *)((const char *)w + (size_t)c0 * wb) : nullptr; };
-    const void *w1p = at(a.pre.weight), *w2p = at(a.post.weight), *b2p = at(a.post.bias);
-
-    float dw1[8] = {}, db1[8] = {}, dw2[8] = {}, db2[8] = {}, dg[8] = {};
     const uint64_t row0 = team_row(a.rows, q.teams, team), row1 = team_row(a.rows, q.teams, team + 1);
-    uint64_t group = a.gate ? row0 / a.rows_per_gate : 0;
+    uint4 *ring = reinterpret_cast<uint4 *>(ring_raw) + t;   // [slot][unit][thread]
+    const uint32_t slot_units = threads * UNITS;
+    // Sums of a row, [rank, warp][kSums], three rows deep: a CTA may still read one row's
+    // after it has arrived for the next, when another sets out with the one after that.
+    float *sm_sums = reinterpret_cast<float *>(ring_raw + (VEC ? (size_t)depth * slot_units * 16 : 0));
+    auto sums_of = [&](uint32_t turn) { return sm_sums + turn % 3 * (ranks * warps * kSums); };
+    // Which gate row a row has, and how many rows it has it for still: one division at the
+    // start. One for the copies, one for the rows as they are worked on.
+    struct GateRow {
+        uint64_t row, left;
+    };
+    auto gate_at = [&](uint64_t row) {
+        GateRow g = {0, 0};
+        if (GATE) g.row = row / a.rows_per_gate, g.left = (g.row + 1) * a.rows_per_gate - row;
+        return g;
+    };
+    auto gate_next = [&](GateRow &g) {
+        if (GATE && --g.left == 0) ++g.row, g.left = a.rows_per_gate;
+    };
+    GateRow copy_gate = gate_at(row0), gate = copy_gate;
+    const uint64_t once = l2_policy_first();
+    uint64_t copy_row = row0;
+    uint32_t copy_slot = 0;
+    // Copies the next row into its slot; missing inputs stay the zeros they are made below.
+    auto fill = [&]() {
+        if (VEC && mine && copy_row < row1) {
+            uint4 *to = ring + copy_slot * slot_units;
+            const uint64_t o = copy_row * a.hidden + c0 + t * 8;
+            auto put = [&](int at, const auto *base, uint64_t off) {
+#pragma unroll
+                for (int i = 0; i < (int)sizeof(*base) / 2; ++i)
+                    copy_async16(to + (at + i) * threads, reinterpret_cast<const uint4 *>(base + off) + i, once);
+            };
+            put(0, reinterpret_cast<const TB *>(q.y), o);
+            if (pre) {
+                put(UB, reinterpret_cast<const TB *>(q.dh), o);
+                put(2 * UB, reinterpret_cast<const TS *>(q.r), o);
+            }
+            if (q.dr) put(2 * UB + US, reinterpret_cast<const TS *>(q.dr), o);
+            if (GATE) put(2 * UB + 2 * US, reinterpret_cast<const TB *>(a.gate), copy_gate.row * a.hidden + c0 + t * 8);
+        }
+        copy_commit();
+        ++copy_row;
+        gate_next(copy_gate);
+        copy_slot = copy_slot + 1 == depth ? 0 : copy_slot + 1;
+    };
+    if (VEC) {
+        for (uint32_t s = 0; s < depth; ++s)   // what no copy fills
+            for (int i = 0; i < UNITS; ++i)
+                if (!mine || (!pre && i >= UB && i < 2 * UB + US) || (!q.dr && i >= 2 * UB + US && i < 2 * UB + 2 * US))
+                    ring[s * slot_units + i * threads] = make_uint4(0, 0, 0, 0);
+        for (uint32_t s = 0; s < depth; ++s) fill();
+    }
+    struct Row {
+        Cols y, dh, r, dr, gate;
+    };
+    auto load_row = [&](uint64_t row, uint32_t slot, const GateRow &g) {
+        Row w;
+        if constexpr (VEC) {
+            const uint4 *p = ring + slot * slot_units;
+            w.y = unpack8<TB>(p, threads), w.dh = unpack8<TB>(p + UB * threads, threads);
+            w.r = unpack8<TS>(p + 2 * UB * threads, threads), w.dr = unpack8<TS>(p + (2 * UB + US) * threads, threads);
+            if constexpr (GATE) w.gate = unpack8<TB>(p + (2 * UB + 2 * US) * threads, threads);
+        } else {
+            const uint64_t o = row * a.hidden + c0;
+            float f[8];
+            load8<false>(reinterpret_cast<const TB *>(q.y) + o, n, 0, threads, t, f), w.y = cols_of(f);
+            w.dh = w.r = w.dr = all8(0.f);
+            if (pre) load8<false>(reinterpret_cast<const TB *>(q.dh) + o, n, 0, threads, t, f), w.dh = cols_of(f);
+            if (pre) load8<false>(reinterpret_cast<const TS *>(q.r) + o, n, 0, threads, t, f), w.r = cols_of(f);
+            if (q.dr) load8<false>(reinterpret_cast<const TS *>(q.dr) + o, n, 0, threads, t, f), w.dr = cols_of(f);
+            if constexpr (GATE) {
+                load8<false>(reinterpret_cast<const TB *>(a.gate) + g.row * a.hidden + c0, n, 0, threads, t, f);
+                w.gate = cols_of(f);
+            }
+        }
+        return w;
+    };
+    // Statistics of a row: mean and 1/deviation of r and of y; of a norm that is not there 0 and 1.
+    auto stats_of = [&](uint64_t row) {
+        float4 s = make_float4(0.f, 1.f, 0.f, 1.f);
+        if (row < row1) {
+            if (pre) s.x = q.stats[4 * row], s.y = q.stats[4 * row + 1];
+            if (post) s.z = q.stats[4 * row + 2], s.w = q.stats[4 * row + 3];
+        }
+        return s;
+    };
+
+    // weights: 0 beyond the row, so that what is there counts for nothing
+    const uint32_t wb = a.weight_type == BF16OPT_TYPE_BF16 ? 2 : 4;
+    auto weights = [&](const void *w, float none) {
+        float f[8];
+        load8_weight<VEC>(w ? (const char *)w + (size_t)c0 * wb : nullptr, a.weight_type, n, 0, threads, t, none, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (column<VEC>(0, threads, t, i) >= n) f[i] = 0.f;
+        return cols_of(f);
+    };
+    const Cols w1 = weights(a.pre.weight, 1.f), w2 = weights(a.post.weight, 1.f);
+    Cols b2;
+    if (GATE) b2 = weights(a.post.bias, 0.f);
+
+    Cols dw1 = all8(0.f), db1 = dw1, dw2 = dw1, db2 = dw1, dg = dw1;
+    const float2 bs = both(a.branch_scale), rs = both(a.residual_scale);
+
+    // the eight sums of a row, published to every CTA of the team
+    auto publish = [&](uint64_t row, uint32_t slot, const GateRow &g, const float4 &st, uint32_t turn) {
+        const Row w = load_row(row, slot, g);
+        const float2 x1 = both(st.y), x0 = both(-st.x), y1 = both(st.w), y0 = both(-st.z);
+        float2 s2[kSums];
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) s2[k] = both(0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 xhat = mul2(add2(w.r.v[i], x0), x1), yhat = mul2(add2(w.y.v[i], y0), y1);
+            const float2 av = mul2(w1.v[i], w.dh.v[i]);
+            const float2 base = fma2(x1, av, w.dr.v[i]);
+            float2 c = mul2(bs, w2.v[i]);
+            if (GATE) c = mul2(c, a.gate_act == BF16OPT_GATE_SIGMOID ? sigmoid2(w.gate.v[i]) : w.gate.v[i]);
+            const float2 cy = mul2(c, yhat);
+            s2[0] = add2(s2[0], av);
+            s2[1] = fma2(av, xhat, s2[1]);
+            s2[2] = fma2(c, base, s2[2]);
+            s2[3] = add2(s2[3], c);
+            s2[4] = fma2(c, xhat, s2[4]);
+            s2[5] = fma2(cy, base, s2[5]);
+            s2[6] = add2(s2[6], cy);
+            s2[7] = fma2(cy, xhat, s2[7]);
+        }
+        float s[kSums];
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) s[k] = s2[k].x + s2[k].y;
+        const float sum = warp_sum8(s, lane);   // lane l < 8: value lane_value(l)
+        float *to = sums_of(turn) + (rank * warps + warp) * kSums + lane_value(lane & 7);
+        if (ranks > 1) {
+            if ((lane >> 3) < ranks) *cluster.map_shared_rank(to, lane >> 3) = sum;   // eight lanes to each rank
+        } else if (lane < 8) {
+            *to = sum;
+        }
+    };
+
+    float4 st = stats_of(row0), st1 = stats_of(row0 + 1);
+    uint32_t slot = 0, slot1 = depth == 1 ? 0 : 1;
+    if (row0 < row1) {
+        if (VEC) copy_wait_for(depth - 1);
+        publish(row0, 0, gate, st, 0);
+    }
+    if (ranks > 1) cluster_arrive();
     uint32_t turn = 0;
     for (uint64_t row = row0; row < row1; ++row, ++turn) {
-        const uint64_t o = row * a.hidden + c0;
-        float r8[8], y8[8], dr8[8], dh8[8], g8[8], w1[8], w2[8];
-        const float mu1 = pre ? q.stats[4 * row] : 0.f, rs1 = pre ? q.stats[4 * row + 1] : 0.f;
-        const float mu2 = post ? q.stats[4 * row + 2] : 0.f, rs2 = post ? q.stats[4 * row + 3] : 1.f;
-        load8<VEC>(reinterpret_cast<const TB *>(q.y) + o, n, 0, threads, t, y8);
-        if (q.dr) load8<VEC>(reinterpret_cast<const TS *>(q.dr) + o, n, 0, threads, t, dr8);
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dr8[i] = 0.f;
-        if (pre && q.dh) {
-            load8<VEC>(reinterpret_cast<const TS *>(q.r) + o, n, 0, threads, t, r8);
-            load8<VEC>(reinterpret_cast<const TB *>(q.dh) + o, n, 0, threads, t, dh8);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r8[i] = mu1, dh8[i] = 0.f;
+        const float4 st2 = stats_of(row + 2);
+        if (ranks > 1) cluster_wait();
+        else __syncthreads();
+        // the next row's sums set out before this row's are used
+        if (row + 1 < row1) {
+            if (VEC) copy_wait_for(depth - 2);
+            GateRow g = gate;
+            gate_next(g);
+            publish(row + 1, slot1, g, st1, turn + 1);
         }
-        if (a.gate) load8<VEC>(reinterpret_cast<const TB *>(a.gate) + row / a.rows_per_gate * a.hidden + c0, n, 0, threads, t, g8);
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g8[i] = 1.f;
-        load8_weight<VEC>(w1p, a.weight_type, n, 0, threads, t, 1.f, w1);
-        load8_weight<VEC>(w2p, a.weight_type, n, 0, threads, t, 1.f, w2);
+        if (ranks > 1) cluster_arrive();
 
-        float s[kSums] = {};
+        float sum = 0.f;
+        for (uint32_t i = lane >> 3; i < ranks * warps; i += 4) sum += sums_of(turn)[i * kSums + (lane & 7)];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        float s[kSums];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool in = column<VEC>(0, threads, t, i) < n;
-            const float xhat = in ? (r8[i] - mu1) * rs1 : 0.f, yhat = in ? (y8[i] - mu2) * rs2 : 0.f;
-            const float av = w1[i] * dh8[i];
-            const float base = fmaf(rs1, av, dr8[i]);
-            float act = g8[i];
-            if (a.gate_act == BF16OPT_GATE_SIGMOID && a.gate) act = sigmoid(act);
-            const float c = in ? a.branch_scale * w2[i] * act : 0.f;
-            s[0] += av;
-            s[1] = fmaf(av, xhat, s[1]);
-            s[2] = fmaf(c, base, s[2]);
-            s[3] += c;
-            s[4] = fmaf(c, xhat, s[4]);
-            const float cy = c * yhat;
-            s[5] = fmaf(cy, base, s[5]);
-            s[6] += cy;
-            s[7] = fmaf(cy, xhat, s[7]);
-        }
-        const float mine = warp_sum8(s, lane);
-        if (lane < 8) sm_sums[turn & 1][warp][lane_value(lane)] = mine;
-        __syncthreads();
-        if (ranks > 1) {
-            if (t < ranks * kSums) {
-                float v = 0.f;
-                for (uint32_t i = 0; i < warps; ++i) v += sm_sums[turn & 1][i][t & 7];
-                *cluster.map_shared_rank(&sm_cluster[turn & 1][rank][t & 7], t >> 3) = v;
-            }
-            cluster.sync();
-        }
-#pragma unroll
-        for (int k = 0; k < kSums; ++k) s[k] = 0.f;
-        if (ranks > 1) {
-            for (uint32_t i = 0; i < ranks; ++i)
-#pragma unroll
-                for (int k = 0; k < kSums; ++k) s[k] += sm_cluster[turn & 1][i][k];
-        } else {
-            for (uint32_t i = 0; i < warps; ++i)
-#pragma unroll
-                for (int k = 0; k < kSums; ++k) s[k] += sm_sums[turn & 1][i][k];
-        }
-        // g = base - rs1 (m1 + xhat m2);  e = c g;  dy = rs2 (e - n1 - yhat n2)
-        const float m1 = pre_layer ? s[0] * inv_h * rs1 : 0.f, m2 = s[1] * inv_h * rs1;
+        for (int k = 0; k < kSums; ++k) s[k] = __shfl_sync(0xffffffffu, sum, k);
+        // g = base - (m1 + xhat m2);  e = c g;  dy = rs2 (e - n1 - yhat n2)
+        const float m1 = pre_layer ? s[0] * inv_h * st.y : 0.f, m2 = s[1] * inv_h * st.y;
         const float n1 = post_layer ? (s[2] - m1 * s[3] - m2 * s[4]) * inv_h : 0.f;
         const float n2 = post ? (s[5] - m1 * s[6] - m2 * s[7]) * inv_h : 0.f;
 
-        if (a.gate && q.shared_gate && row / a.rows_per_gate != group) {   // the gate's rows end: its sum is whole if they began here
-            const bool began = group * a.rows_per_gate >= row0;
-            if (began) store8<VEC>(reinterpret_cast<TB *>(q.dgate) + group * a.hidden + c0, n, 0, threads, t, dg);
-            else store8<VEC>(q.gate_part + (size_t)(2 * team) * a.hidden + c0, n, 0, threads, t, dg);
+        const Row w = load_row(row, slot, gate);
+        const float2 x1 = both(st.y), x0 = both(-st.x), y1 = both(st.w), y0 = both(-st.z);
+        const float2 nm1 = both(-m1), nm2 = both(-m2), nn1 = both(-n1), nn2 = both(-n2);
+        Cols dx, dy, dgr;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dg[i] = 0.f;
-            group = row / a.rows_per_gate;
-        }
-        float b2[8];
-        load8_weight<VEC>(b2p, a.weight_type, n, 0, threads, t, 0.f, b2);
-        float dx8[8], dy8[8], dgr[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool in = column<VEC>(0, threads, t, i) < n;
-            const float xhat = in ? (r8[i] - mu1) * rs1 : 0.f, yhat = in ? (y8[i] - mu2) * rs2 : 0.f;
-            const float base = fmaf(rs1, w1[i] * dh8[i], dr8[i]);
-            const float g = base - fmaf(xhat, m2, m1);
-            dx8[i] = a.residual_scale * g;
-            const float du = a.branch_scale * g;
-            float act = g8[i], slope = 1.f;
-            if (a.gate_act == BF16OPT_GATE_SIGMOID && a.gate) {
-                act = sigmoid(act);
-                slope = act * (1.f - act);
+        for (int i = 0; i < 4; ++i) {
+            const float2 xhat = mul2(add2(w.r.v[i], x0), x1), yhat = mul2(add2(w.y.v[i], y0), y1);
+            const float2 base = fma2(x1, mul2(w1.v[i], w.dh.v[i]), w.dr.v[i]);
+            const float2 g = add2(fma2(xhat, nm2, base), nm1);
+            dx.v[i] = mul2(rs, g);
+            float2 dn = mul2(bs, g);
+            if (GATE) {
+                float2 act = w.gate.v[i];
+                const float2 du = mul2(dn, fma2(yhat, w2.v[i], b2.v[i]));
+                if (a.gate_act == BF16OPT_GATE_SIGMOID) {
+                    act = sigmoid2(act);
+                    dgr.v[i] = mul2(du, mul2(act, make_float2(1.f - act.x, 1.f - act.y)));
+                } else {
+                    dgr.v[i] = du;
+                }
+                dn = mul2(act, dn);
             }
-            dgr[i] = slope * du * fmaf(yhat, w2[i], b2[i]);
-            const float dn = act * du;
-            dw2[i] = fmaf(dn, yhat, dw2[i]);
-            db2[i] += dn;
-            dw1[i] = fmaf(dh8[i], xhat, dw1[i]);
-            db1[i] += dh8[i];
-            dy8[i] = post ? rs2 * (fmaf(w2[i], dn, -n1) - yhat * n2) : dn;
+            dw2.v[i] = fma2(dn, yhat, dw2.v[i]);
+            db2.v[i] = add2(db2.v[i], dn);
+            dw1.v[i] = fma2(w.dh.v[i], xhat, dw1.v[i]);
+            db1.v[i] = add2(db1.v[i], w.dh.v[i]);
+            dy.v[i] = mul2(y1, add2(fma2(w2.v[i], dn, mul2(yhat, nn2)), nn1));
         }
-        store8<VEC>(reinterpret_cast<TS *>(q.dx) + o, n, 0, threads, t, dx8);
-        store8<VEC>(reinterpret_cast<TB *>(q.dy) + o, n, 0, threads, t, dy8);
-        if (a.gate && q.dgate) {
+        const uint64_t o = row * a.hidden + c0;
+        store_cols<VEC>(reinterpret_cast<TS *>(q.dx) + o, n, threads, t, dx);
+        store_cols<VEC>(reinterpret_cast<TB *>(q.dy) + o, n, threads, t, dy);
+        if (GATE && q.dgate) {
             if (q.shared_gate) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dg[i] += dgr[i];
+                for (int i = 0; i < 4; ++i) dg.v[i] = add2(dg.v[i], dgr.v[i]);
+                if (gate.left == 1 || row + 1 == row1) {   // its rows end, here or for this team
+                    const uint64_t first = gate.row * a.rows_per_gate;
+                    // the sum is whole if they all are this team's; else a part: the team's first gate's, or its last's
+                    if (first >= row0 && gate.left == 1) store_cols<VEC>(reinterpret_cast<TB *>(q.dgate) + gate.row * a.hidden + c0, n, threads, t, dg);
+                    else store_cols<VEC>(q.gate_part + (size_t)(2 * team + (first > row0)) * a.hidden + c0, n, threads, t, dg);
+                    dg = all8(0.f);
+                }
             } else {
-                store8<VEC>(reinterpret_cast<TB *>(q.dgate) + o, n, 0, threads, t, dgr);
+                store_cols<VEC>(reinterpret_cast<TB *>(q.dgate) + o, n, threads, t, dgr);
             }
         }
+        if (VEC) {
+            fill();
+            slot = slot1;
+            slot1 = slot1 + 1 == depth ? 0 : slot1 + 1;
+        }
+        st = st1, st1 = st2;
+        gate_next(gate);
     }
-    if (q.shared_gate && row0 < row1) {
-        const bool began = group * a.rows_per_gate >= row0, ends = (group + 1) * a.rows_per_gate <= row1;
-        if (began && ends) store8<VEC>(reinterpret_cast<TB *>(q.dgate) + group * a.hidden + c0, n, 0, threads, t, dg);
-        else store8<VEC>(q.gate_part + (size_t)(2 * team + (began && group != row0 / a.rows_per_gate)) * a.hidden + c0, n, 0, threads, t, dg);
-    }
-    if (q.need_weights) {
-        float *p = q.part + (size_t)team * 4 * a.hidden + c0;
-        store8<VEC>(p, n, 0, threads, t, dw1);
-        store8<VEC>(p + a.hidden, n, 0, threads, t, db1);
-        store8<VEC>(p + 2 * (size_t)a.hidden, n, 0, threads, t, dw2);
-        store8<VEC>(p + 3 * (size_t)a.hidden, n, 0, threads, t, db2);
-    }
+    if (ranks > 1) cluster_wait();   // for the last arrival: nobody leaves while others may write here
+    float *p = q.part + (size_t)team * 4 * a.hidden + c0;
+    if (q.want & 1) store_cols<VEC>(p, n, threads, t, dw1);
+    if (q.want & 2) store_cols<VEC>(p + a.hidden, n, threads, t, db1);
+    if (q.want & 4) store_cols<VEC>(p + 2 * (size_t)a.hidden, n, threads, t, dw2);
+    if (q.want & 8) store_cols<VEC>(p + 3 * (size_t)a.hidden, n, threads, t, db2);
+    pdl_leave();
 }
 
-// The partial sums joined, in the teams' order: 32 columns by 8 runs of teams.
+// The partial sums joined, in the teams' order: 32 columns by kRuns runs of teams.
 // blockIdx.y < 4: that weight's gradient; else gate row blockIdx.y - 4, if its
 // rows straddle teams.
 struct JoinArgs {
@@ -452,8 +611,9 @@ struct JoinArgs {
     uint64_t rows, gate_rows, rows_per_gate;
     uint32_t teams, hidden;
 };
-__global__ void __launch_bounds__(256) k_norm_join(const JoinArgs j) {
-    __shared__ float sm[8][32];
+constexpr int kRuns = 16;
+__global__ void __launch_bounds__(32 * kRuns) k_norm_join(const JoinArgs j) {
+    __shared__ float sm[kRuns][32];
     pdl_enter();
     const uint32_t lane = threadIdx.x & 31, run = threadIdx.x >> 5;
     const uint32_t c = blockIdx.x * 32 + lane;
@@ -476,13 +636,14 @@ __global__ void __launch_bounds__(256) k_norm_join(const JoinArgs j) {
         }
         if (!out) continue;
         float s = 0.f;
-        const uint32_t i0 = (uint32_t)((uint64_t)count * run / 8), i1 = (uint32_t)((uint64_t)count * (run + 1) / 8);
+        const uint32_t i0 = count * run / kRuns, i1 = count * (run + 1) / kRuns;
         if (c < j.hidden)
+#pragma unroll 8
             for (uint32_t i = i0; i < i1; ++i) s += p[i * stride + (i ? 0 : skip) + c];
         sm[run][lane] = s;
         __syncthreads();
         if (run == 0 && c < j.hidden) {
-            for (int i = 1; i < 8; ++i) s += sm[i][lane];
+            for (int i = 1; i < kRuns; ++i) s += sm[i][lane];
             store_typed(out, b < 4 ? j.weight_type : j.gate_type, at, s);
         }
         __syncthreads();
@@ -570,26 +731,61 @@ int forward_v(const Args &a, const void *x, const void *y, void *r, void *h, flo
 // The backward pass's shape, from the sizes and the device alone.
 struct Shape {
     unsigned cluster, threads;
+    uint32_t depth;          // rows in the ring
+    size_t smem;
     uint32_t teams;
     uint64_t part_floats, gate_floats;
 };
-Shape shape_of(const bf16opt_norm_gate_t *d, int sms) {
-    Shape s;
+
+template <class F>
+int by_types(const bf16opt_norm_gate_t *d, F &&f) {
+    using B = __nv_bfloat16;
+    if (d->branch_type == BF16OPT_TYPE_F32) return f((float *)nullptr, (float *)nullptr);
+    if (d->stream_type == BF16OPT_TYPE_F32) return f((B *)nullptr, (float *)nullptr);
+    return f((B *)nullptr, (B *)nullptr);
+}
+
+constexpr size_t kSmemBytes = 226 * 1024;   // of a multiprocessor; each CTA takes 1 KB besides its own
+
+template <class TB, class TS, bool VEC, bool GATE>
+int shape_v(const bf16opt_norm_gate_t *d, int sms, Shape &s) {
     s.cluster = (d->hidden + kColumns - 1) / kColumns;
     if (s.cluster == 3) s.cluster = 4;
     const uint32_t cols = (d->hidden + s.cluster - 1) / s.cluster;
     s.threads = ((cols + 7) / 8 + 31) / 32 * 32;
-    const uint64_t teams = std::max<uint64_t>(1, (uint64_t)sms * std::max(1u, 512 / s.threads) / s.cluster);
+    const unsigned per_sm = std::max(1u, std::min(512u / s.threads, 16u));   // 128 registers a thread
+    const size_t row = (size_t)s.threads * ring_units<TB, TS, GATE>() * 16, sums = 3 * s.cluster * s.threads / 32 * kSums * sizeof(float);
+    s.depth = VEC ? (uint32_t)std::max<size_t>(2, std::min<size_t>(8, (kSmemBytes / per_sm - sums - 1024) / row)) : 2;
+    s.smem = (VEC ? s.depth * row : 0) + sums;
+    uint64_t teams = (uint64_t)sms * per_sm;
+    if (s.cluster > 1) {
+        auto k = k_norm_backward<TB, TS, VEC, GATE>;
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
+        int fit = 0;
+        if (e == cudaSuccess) e = clusters_that_fit(Launch{s.cluster, s.threads, s.smem, nullptr, s.cluster, true}, k, fit);
+        if (e != cudaSuccess || fit < 1) return fail_cuda(e != cudaSuccess ? e : cudaErrorLaunchOutOfResources, "norm_gate occupancy");
+        teams = fit;
+    }
     s.teams = (uint32_t)std::min<uint64_t>(teams, std::max<uint64_t>(1, d->rows));
     s.part_floats = (uint64_t)s.teams * 4 * d->hidden;
     s.gate_floats = d->gate_rows && d->gate_rows != d->rows ? (uint64_t)s.teams * 2 * d->hidden : 0;
-    return s;
+    return BF16OPT_OK;
+}
+template <class TB, class TS>
+int shape_t(const bf16opt_norm_gate_t *d, bool vec, int sms, Shape &s) {
+    if (vec) return d->gate ? shape_v<TB, TS, true, true>(d, sms, s) : shape_v<TB, TS, true, false>(d, sms, s);
+    return d->gate ? shape_v<TB, TS, false, true>(d, sms, s) : shape_v<TB, TS, false, false>(d, sms, s);
 }
 
-template <class TB, class TS, bool VEC>
+template <class TB, class TS, bool VEC, bool GATE>
 int backward_v(const Args &a, const BackArgs &q, const Shape &s, cudaStream_t st) {
-    Launch l{s.teams * s.cluster, s.threads, 0, st, s.cluster, true};
-    const cudaError_t e = launch(l, k_norm_backward<TB, TS, VEC>, a, q);
+    auto k = k_norm_backward<TB, TS, VEC, GATE>;
+    if (s.smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
+        if (e != cudaSuccess) return fail_cuda(e, "norm_gate kernel attribute");
+    }
+    Launch l{s.teams * s.cluster, s.threads, s.smem, st, s.cluster, true};
+    const cudaError_t e = launch(l, k, a, q, s.depth);
     return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "norm_gate kernel launch");
 }
 
@@ -613,12 +809,11 @@ int forward(const bf16opt_norm_gate_t *d, const void *x, const void *y, void *r,
     const Args a = args_of(d);
     const cudaStream_t st = (cudaStream_t)stream;
     const bool vec = vectors(d, {x, y, r, h});
-    using B = __nv_bfloat16;
-    if (d->branch_type == BF16OPT_TYPE_F32)
-        return vec ? forward_v<float, float, true>(a, x, y, r, h, stats, st) : forward_v<float, float, false>(a, x, y, r, h, stats, st);
-    if (d->stream_type == BF16OPT_TYPE_F32)
-        return vec ? forward_v<B, float, true>(a, x, y, r, h, stats, st) : forward_v<B, float, false>(a, x, y, r, h, stats, st);
-    return vec ? forward_v<B, B, true>(a, x, y, r, h, stats, st) : forward_v<B, B, false>(a, x, y, r, h, stats, st);
+    return by_types(d, [&](auto bp, auto tp) {
+        using TB = std::remove_pointer_t<decltype(bp)>;
+        using TS = std::remove_pointer_t<decltype(tp)>;
+        return vec ? forward_v<TB, TS, true>(a, x, y, r, h, stats, st) : forward_v<TB, TS, false>(a, x, y, r, h, stats, st);
+    });
 }
 
 int workspace(const bf16opt_norm_gate_t *d, uint64_t *bytes) {
@@ -628,8 +823,15 @@ int workspace(const bf16opt_norm_gate_t *d, uint64_t *bytes) {
     if (!bytes) return fail(BF16OPT_ERR_INVALID_ARG, "norm_gate: bytes is NULL");
     const int sms = sm_count();
     if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "norm_gate: no CUDA device");
-    const Shape s = shape_of(d, sms);
-    *bytes = (s.part_floats + s.gate_floats) * 4;
+    // the larger of what aligned and other rows take: the pointers are not known yet
+    Shape s[2];
+    for (int vec = 0; vec < 2; ++vec) {
+        const int r = by_types(d, [&](auto b, auto t) {
+            return shape_t<std::remove_pointer_t<decltype(b)>, std::remove_pointer_t<decltype(t)>>(d, vec, sms, s[vec]);
+        });
+        if (r != BF16OPT_OK) return r;
+    }
+    *bytes = std::max(s[0].part_floats + s[0].gate_floats, s[1].part_floats + s[1].gate_floats) * 4;
     return BF16OPT_OK;
 }
 
@@ -648,9 +850,10 @@ int backward(const bf16opt_norm_gate_t *d, const void *dr, const void *dh, const
     if (d->rows && (!y || !dx || !dy || (dh && !r) || ((pre || post) && !stats))) return bad("r, y, stats, dx or dy is NULL");
     const uint64_t tb = type_bytes(d->branch_type), ts = type_bytes(d->stream_type), tw = type_bytes(d->weight_type);
     void *const outs[4] = {dpre_weight, dpre_bias, dpost_weight, dpost_bias};
-    bool need = false;
-    for (void *w : outs) {
-        need = need || w;
+    uint32_t want = 0;
+    for (int i = 0; i < 4; ++i) {
+        void *const w = outs[i];
+        want |= w ? 1u << i : 0u;
         if (misaligned(w, tw)) return fail(BF16OPT_ERR_ALIGNMENT, "norm_gate: a pointer is not aligned to its element");
     }
     if (misaligned(dr, ts) || misaligned(r, ts) || misaligned(dx, ts) || misaligned(dh, tb) || misaligned(y, tb) ||
@@ -666,7 +869,12 @@ int backward(const bf16opt_norm_gate_t *d, const void *dr, const void *dh, const
         if (dgate && e == cudaSuccess) e = cudaMemsetAsync(dgate, 0, d->gate_rows * d->hidden * tb, st);
         return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "norm_gate clearing the weights' gradients");
     }
-    const Shape s = shape_of(d, sms);
+    const bool vec = vectors(d, {dr, dh, r, y, dx, dy, dgate});
+    Shape s;
+    rc = by_types(d, [&](auto b, auto t) {
+        return shape_t<std::remove_pointer_t<decltype(b)>, std::remove_pointer_t<decltype(t)>>(d, vec, sms, s);
+    });
+    if (rc != BF16OPT_OK) return rc;
     const uint64_t ws_need = (s.part_floats + s.gate_floats) * 4;
     if (!ws || ws_bytes < ws_need) return bad("the workspace is too small");
     const uint64_t n = d->rows * d->hidden, hw = d->hidden * tw, gb = d->gate_rows * d->hidden * tb;
@@ -679,17 +887,15 @@ int backward(const bf16opt_norm_gate_t *d, const void *dr, const void *dh, const
     BackArgs q;
     q.dr = dr, q.dh = dh, q.r = r, q.y = y, q.stats = stats, q.dx = dx, q.dy = dy, q.dgate = dgate;
     q.part = (float *)ws, q.gate_part = (float *)ws + s.part_floats;
-    q.teams = s.teams, q.need_weights = need;
+    q.teams = s.teams, q.want = want;
     q.shared_gate = dgate && d->gate_rows != d->rows;
-    const bool vec = vectors(d, {dr, dh, r, y, dx, dy, dgate});
-    using B = __nv_bfloat16;
-    if (d->branch_type == BF16OPT_TYPE_F32)
-        rc = vec ? backward_v<float, float, true>(a, q, s, st) : backward_v<float, float, false>(a, q, s, st);
-    else if (d->stream_type == BF16OPT_TYPE_F32)
-        rc = vec ? backward_v<B, float, true>(a, q, s, st) : backward_v<B, float, false>(a, q, s, st);
-    else
-        rc = vec ? backward_v<B, B, true>(a, q, s, st) : backward_v<B, B, false>(a, q, s, st);
-    if (rc != BF16OPT_OK || (!need && !q.shared_gate)) return rc;
+    rc = by_types(d, [&](auto bp, auto tp) {
+        using TB = std::remove_pointer_t<decltype(bp)>;
+        using TS = std::remove_pointer_t<decltype(tp)>;
+        if (vec) return d->gate ? backward_v<TB, TS, true, true>(a, q, s, st) : backward_v<TB, TS, true, false>(a, q, s, st);
+        return d->gate ? backward_v<TB, TS, false, true>(a, q, s, st) : backward_v<TB, TS, false, false>(a, q, s, st);
+    });
+    if (rc != BF16OPT_OK || (!want && !q.shared_gate)) return rc;
     JoinArgs j;
     j.part = q.part, j.gate_part = q.gate_part;
     for (int i = 0; i < 4; ++i) j.out[i] = outs[i];
@@ -699,7 +905,7 @@ int backward(const bf16opt_norm_gate_t *d, const void *dr, const void *dh, const
     j.teams = s.teams, j.hidden = a.hidden;
     dim3 grid((a.hidden + 31) / 32, (unsigned)std::min<uint64_t>(4 + (j.dgate ? a.gate_rows : 0), 4096));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid, cfg.blockDim = dim3(256), cfg.stream = st;
+    cfg.gridDim = grid, cfg.blockDim = dim3(32 * kRuns), cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
