@@ -147,9 +147,10 @@ __device__ __forceinline__ void pairs(const uint4 &v, float2 (&f)[Vec<T>::N / 2]
         f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y)), f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
     }
 }
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hmax2(reinterpret_cast<const __nv_bfloat162 &>(a), reinterpret_cast<const __nv_bfloat162 &>(b));
-    return reinterpret_cast<const uint32_t &>(r);
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {   // NaN passed over
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 // Largest element of U vectors (NaN passed over).
 template <class T, int U>
@@ -200,13 +201,11 @@ __device__ __forceinline__ Slice slice_of(const T *row, uint32_t vocab, uint32_t
 // aligned as the input row's, else element by element.
 template <class T>
 __device__ __forceinline__ void store_vec(T *out, const float (&g)[Vec<T>::N], bool whole) {
-    const uint4 v = Vec<T>::pack(g);
     if (whole) {
-        __stcs(reinterpret_cast<uint4 *>(out), v);
+        __stcs(reinterpret_cast<uint4 *>(out), Vec<T>::pack(g));
     } else {
-        const T *e = reinterpret_cast<const T *>(&v);
 #pragma unroll
-        for (int i = 0; i < Vec<T>::N; ++i) out[i] = e[i];
+        for (int i = 0; i < Vec<T>::N; ++i) from_f32(out[i], g[i]);
     }
 }
 
@@ -323,20 +322,17 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
         }
     };
     uint32_t issued = 0, issued_slot = 0;
-    // what is read again comes in at normal priority, all else to be dropped first
-    const uint64_t once = l2_policy_first(), twice_read = l2_policy_normal();
     auto issue = [&]() {
         if (cur.row < a.rows) {
             uint4 *to = ring + issued_slot * kGroup + tid;
             const uint4 *from = cur.zv + cur.i * kGroup;
-            const uint64_t policy = FORWARD && GRAD && !cur.again && cur.n > depth && cur.i < cur.n - depth ? twice_read : once;
             if ((cur.i + 1) * kGroup <= cur.nv) {
 #pragma unroll
-                for (int u = 0; u < kU; ++u) copy_async16(to + u * kThreads, from + u * kThreads, policy);
+                for (int u = 0; u < kU; ++u) copy_async16(to + u * kThreads, from + u * kThreads);
             } else {
 #pragma unroll
                 for (int u = 0; u < kU; ++u)
-                    if (cur.i * kGroup + u * kThreads + tid < cur.nv) copy_async16(to + u * kThreads, from + u * kThreads, policy);
+                    if (cur.i * kGroup + u * kThreads + tid < cur.nv) copy_async16(to + u * kThreads, from + u * kThreads);
             }
             ++cur.i;
             const bool over = cur.i == (cur.again ? cur.n - depth : cur.n);

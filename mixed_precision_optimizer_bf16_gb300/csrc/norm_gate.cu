@@ -128,7 +128,11 @@ __device__ __forceinline__ void load8_weight(const void *w, int type, uint32_t n
     }
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + ex2(-x * kLog2e)); }
+__device__ __forceinline__ float sigmoid(float x) {
+    float y;   // the reciprocal to one unit in the last place
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + ex2(-x * kLog2e)));
+    return y;
+}
 
 // ------------------------------------------------------------------------ forward
 
@@ -234,8 +238,12 @@ k_norm_forward(const Args a, const TS *x, const TB *y, TS *r, TB *h, float *stat
 
 // ----------------------------------------------------------------------- backward
 
-constexpr int kColumns = 4096;   // columns of one CTA: 512 threads of 8
-constexpr int kSums = 8;      // per row
+// Columns of one CTA at most, so that two of 224 threads with 16 columns fit an
+// SM's registers (146 a thread).  With 8 columns a thread, what a row costs a warp
+// apart from its columns (the two reductions, addresses, copies) was as much as the
+// columns: 608 instructions a row of 8, 282 us on 4096 x 14336.
+constexpr int kColumns = 3584;
+constexpr int kSums = 8;         // per row
 
 struct BackArgs {
     const void *dr, *dh, *r, *y;
@@ -319,19 +327,46 @@ __device__ __forceinline__ Cols cols_of(const float (&f)[8]) {
     for (int i = 0; i < 4; ++i) c.v[i] = make_float2(f[2 * i], f[2 * i + 1]);
     return c;
 }
+// Eight columns from `c` on of a row of n: VEC: whole vectors, all of them there or none;
+// else one by one, 0 beyond the row.
+template <class T>
+__device__ __forceinline__ Cols load_cols(const T *row, uint32_t c, uint32_t n) {
+    float f[8];
+    if (c + 8 <= n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = to_f32(row[c + i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = c + i < n ? to_f32(row[c + i]) : 0.f;
+    }
+    return cols_of(f);
+}
 template <bool VEC, class T>
-__device__ __forceinline__ void store_cols(T *row, uint32_t n, uint32_t threads, uint32_t t, const Cols &c) {
-    const float f[8] = {c.v[0].x, c.v[0].y, c.v[1].x, c.v[1].y, c.v[2].x, c.v[2].y, c.v[3].x, c.v[3].y};
-    store8<VEC>(row, n, 0, threads, t, f);
+__device__ __forceinline__ void store_cols(T *row, uint32_t c, uint32_t n, const Cols &x) {
+    const float f[8] = {x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y, x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y};
+    if (VEC) {
+        if (c >= n) return;
+        if constexpr (sizeof(T) == 2) {
+            __stcs(reinterpret_cast<uint4 *>(row + c), Vec<T>::pack(f));
+        } else {
+            __stcs(reinterpret_cast<float4 *>(row + c), make_float4(f[0], f[1], f[2], f[3]));
+            __stcs(reinterpret_cast<float4 *>(row + c) + 1, make_float4(f[4], f[5], f[6], f[7]));
+        }
+    } else if (c + 8 <= n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) from_f32(row[c + i], f[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < n) from_f32(row[c + i], f[i]);
+    }
 }
 __device__ __forceinline__ float2 sigmoid2(float2 x) { return make_float2(sigmoid(x.x), sigmoid(x.y)); }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-constexpr int kBackThreads = kColumns / 8;
-
-// 16-byte units of one row that a thread keeps in the ring: y, dh, [gate] of the
+// 16-byte units of eight columns of a row that a thread keeps in the ring: y, dh, [gate] of the
 // branch's type, r, dr of the stream's.
 template <class TB, class TS, bool GATE>
 __host__ __device__ constexpr int ring_units() {
@@ -342,20 +377,21 @@ __host__ __device__ constexpr int ring_units() {
 // overlapped steps: the sums of row k + 1 are taken and published while those of
 // row k are still on their way, then row k's outputs are written.  The rows
 // come through a ring in shared memory whose slots belong to one thread each, filled
-// by asynchronous copies `depth` rows ahead.  VEC: rows of whole 16-byte vectors;
-// else elements are loaded one by one, twice, and there is no ring.
-template <class TB, class TS, bool VEC, bool GATE>
-__global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a, const BackArgs q, uint32_t depth) {
+// by asynchronous copies `depth` rows ahead.  A thread has V runs of eight columns,
+// `threads` runs apart.  VEC: rows of whole 16-byte vectors; else elements are
+// loaded one by one, twice, and there is no ring.
+template <class TB, class TS, bool VEC, bool GATE, int V>
+__global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Args a, const BackArgs q, uint32_t depth) {
     constexpr int UNITS = ring_units<TB, TS, GATE>(), UB = sizeof(TB) / 2, US = sizeof(TS) / 2;
     extern __shared__ __align__(16) unsigned char ring_raw[];
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const uint32_t threads = blockDim.x, t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = threads / 32;
     const uint32_t team = blockIdx.x / ranks;
-    // this CTA's columns: [c0, c0 + n)
-    const uint32_t c0 = rank * threads * 8;
-    const uint32_t n = c0 < a.hidden ? min(a.hidden - c0, threads * 8) : 0u;
-    const bool mine = VEC && column<true>(0, threads, t, 0) < n;
+    // this CTA's columns: [c0, c0 + n); this thread's runs begin at col(0), col(1) ...
+    const uint32_t c0 = rank * threads * 8 * V;
+    const uint32_t n = c0 < a.hidden ? min(a.hidden - c0, threads * 8 * V) : 0u;
+    auto col = [&](int v) { return (v * threads + t) * 8; };
     const float inv_h = 1.f / (float)a.hidden;
     const bool pre = a.pre.kind != BF16OPT_NORM_NONE && q.dh, post = a.post.kind != BF16OPT_NORM_NONE;
     const bool pre_layer = a.pre.kind == BF16OPT_NORM_LAYER, post_layer = a.post.kind == BF16OPT_NORM_LAYER;
@@ -363,46 +399,50 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a,
     if (ranks > 1) cluster.sync();
 
     const uint64_t row0 = team_row(a.rows, q.teams, team), row1 = team_row(a.rows, q.teams, team + 1);
-    uint4 *ring = reinterpret_cast<uint4 *>(ring_raw) + t;   // [slot][unit][thread]
-    const uint32_t slot_units = threads * UNITS;
+    uint4 *ring = reinterpret_cast<uint4 *>(ring_raw) + t;   // [slot][run][unit][thread]
+    const uint32_t slot_units = threads * UNITS * V;
     // Sums of a row, [rank, warp][kSums], three rows deep: a CTA may still read one row's
     // after it has arrived for the next, when another sets out with the one after that.
     float *sm_sums = reinterpret_cast<float *>(ring_raw + (VEC ? (size_t)depth * slot_units * 16 : 0));
-    auto sums_of = [&](uint32_t turn) { return sm_sums + turn % 3 * (ranks * warps * kSums); };
+    const uint32_t entries = ranks * warps;
+    uint32_t sums_at = 0;   // of the row that is worked on
+    auto sums_next = [&](uint32_t at) { return at == 2 * entries * kSums ? 0u : at + entries * kSums; };
+
     // Which gate row a row has, and how many rows it has it for still: one division at the
     // start. One for the copies, one for the rows as they are worked on.
     struct GateRow {
         uint64_t row, left;
     };
-    auto gate_at = [&](uint64_t row) {
-        GateRow g = {0, 0};
-        if (GATE) g.row = row / a.rows_per_gate, g.left = (g.row + 1) * a.rows_per_gate - row;
-        return g;
-    };
+    GateRow copy_gate = {0, 0};
+    if (GATE) copy_gate.row = row0 / a.rows_per_gate, copy_gate.left = (copy_gate.row + 1) * a.rows_per_gate - row0;
+    GateRow gate = copy_gate;
     auto gate_next = [&](GateRow &g) {
         if (GATE && --g.left == 0) ++g.row, g.left = a.rows_per_gate;
     };
-    GateRow copy_gate = gate_at(row0), gate = copy_gate;
-    const uint64_t once = l2_policy_first();
+
     uint64_t copy_row = row0;
     uint32_t copy_slot = 0;
     // Copies the next row into its slot; missing inputs stay the zeros they are made below.
     auto fill = [&]() {
-        if (VEC && mine && copy_row < row1) {
-            uint4 *to = ring + copy_slot * slot_units;
-            const uint64_t o = copy_row * a.hidden + c0 + t * 8;
-            auto put = [&](int at, const auto *base, uint64_t off) {
+        if (VEC && copy_row < row1) {
+            const uint64_t o = copy_row * a.hidden + c0;
 #pragma unroll
-                for (int i = 0; i < (int)sizeof(*base) / 2; ++i)
-                    copy_async16(to + (at + i) * threads, reinterpret_cast<const uint4 *>(base + off) + i, once);
-            };
-            put(0, reinterpret_cast<const TB *>(q.y), o);
-            if (pre) {
-                put(UB, reinterpret_cast<const TB *>(q.dh), o);
-                put(2 * UB, reinterpret_cast<const TS *>(q.r), o);
+            for (int v = 0; v < V; ++v) {
+                if (col(v) >= n) break;
+                uint4 *to = ring + copy_slot * slot_units + v * UNITS * threads;
+                auto put = [&](int at, const auto *base, uint64_t off) {
+#pragma unroll
+                    for (int i = 0; i < (int)sizeof(*base) / 2; ++i)
+                        copy_async16(to + (at + i) * threads, reinterpret_cast<const uint4 *>(base + off + col(v)) + i);
+                };
+                put(0, reinterpret_cast<const TB *>(q.y), o);
+                if (pre) {
+                    put(UB, reinterpret_cast<const TB *>(q.dh), o);
+                    put(2 * UB, reinterpret_cast<const TS *>(q.r), o);
+                }
+                if (q.dr) put(2 * UB + US, reinterpret_cast<const TS *>(q.dr), o);
+                if (GATE) put(2 * UB + 2 * US, reinterpret_cast<const TB *>(a.gate), copy_gate.row * a.hidden + c0);
             }
-            if (q.dr) put(2 * UB + US, reinterpret_cast<const TS *>(q.dr), o);
-            if (GATE) put(2 * UB + 2 * US, reinterpret_cast<const TB *>(a.gate), copy_gate.row * a.hidden + c0 + t * 8);
         }
         copy_commit();
         ++copy_row;
@@ -411,33 +451,31 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a,
     };
     if (VEC) {
         for (uint32_t s = 0; s < depth; ++s)   // what no copy fills
-            for (int i = 0; i < UNITS; ++i)
-                if (!mine || (!pre && i >= UB && i < 2 * UB + US) || (!q.dr && i >= 2 * UB + US && i < 2 * UB + 2 * US))
-                    ring[s * slot_units + i * threads] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                for (int i = 0; i < UNITS; ++i)
+                    if (col(v) >= n || (!pre && i >= UB && i < 2 * UB + US) || (!q.dr && i >= 2 * UB + US && i < 2 * UB + 2 * US))
+                        ring[s * slot_units + (v * UNITS + i) * threads] = make_uint4(0, 0, 0, 0);
         for (uint32_t s = 0; s < depth; ++s) fill();
     }
-    struct Row {
+    struct Run {
         Cols y, dh, r, dr, gate;
     };
-    auto load_row = [&](uint64_t row, uint32_t slot, const GateRow &g) {
-        Row w;
+    auto load_run = [&](uint64_t row, uint32_t slot, const GateRow &g, int v) {
+        Run w;
         if constexpr (VEC) {
-            const uint4 *p = ring + slot * slot_units;
+            const uint4 *p = ring + slot * slot_units + v * UNITS * threads;
             w.y = unpack8<TB>(p, threads), w.dh = unpack8<TB>(p + UB * threads, threads);
             w.r = unpack8<TS>(p + 2 * UB * threads, threads), w.dr = unpack8<TS>(p + (2 * UB + US) * threads, threads);
             if constexpr (GATE) w.gate = unpack8<TB>(p + (2 * UB + 2 * US) * threads, threads);
         } else {
             const uint64_t o = row * a.hidden + c0;
-            float f[8];
-            load8<false>(reinterpret_cast<const TB *>(q.y) + o, n, 0, threads, t, f), w.y = cols_of(f);
-            w.dh = w.r = w.dr = all8(0.f);
-            if (pre) load8<false>(reinterpret_cast<const TB *>(q.dh) + o, n, 0, threads, t, f), w.dh = cols_of(f);
-            if (pre) load8<false>(reinterpret_cast<const TS *>(q.r) + o, n, 0, threads, t, f), w.r = cols_of(f);
-            if (q.dr) load8<false>(reinterpret_cast<const TS *>(q.dr) + o, n, 0, threads, t, f), w.dr = cols_of(f);
-            if constexpr (GATE) {
-                load8<false>(reinterpret_cast<const TB *>(a.gate) + g.row * a.hidden + c0, n, 0, threads, t, f);
-                w.gate = cols_of(f);
-            }
+            const Cols zero = all8(0.f);
+            w.y = load_cols(reinterpret_cast<const TB *>(q.y) + o, col(v), n);
+            w.dh = pre ? load_cols(reinterpret_cast<const TB *>(q.dh) + o, col(v), n) : zero;
+            w.r = pre ? load_cols(reinterpret_cast<const TS *>(q.r) + o, col(v), n) : zero;
+            w.dr = q.dr ? load_cols(reinterpret_cast<const TS *>(q.dr) + o, col(v), n) : zero;
+            if constexpr (GATE) w.gate = load_cols(reinterpret_cast<const TB *>(a.gate) + g.row * a.hidden + c0, col(v), n);
         }
         return w;
     };
@@ -451,152 +489,180 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a,
         return s;
     };
 
-    // weights: 0 beyond the row, so that what is there counts for nothing
-    const uint32_t wb = a.weight_type == BF16OPT_TYPE_BF16 ? 2 : 4;
-    auto weights = [&](const void *w, float none) {
+    // weights: 0 beyond the row, so that what is there counts for nothing; the post-norm's
+    // with the branch's scale in it
+    auto weights = [&](const void *w, float none, float scale, int v) {
         float f[8];
-        load8_weight<VEC>(w ? (const char *)w + (size_t)c0 * wb : nullptr, a.weight_type, n, 0, threads, t, none, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (column<VEC>(0, threads, t, i) >= n) f[i] = 0.f;
+            f[i] = col(v) + i < n ? scale * (w ? load_typed(w, a.weight_type, c0 + col(v) + i) : none) : 0.f;
         return cols_of(f);
     };
-    const Cols w1 = weights(a.pre.weight, 1.f), w2 = weights(a.post.weight, 1.f);
-    Cols b2;
-    if (GATE) b2 = weights(a.post.bias, 0.f);
+    Cols w1[V], w2[V], b2[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        w1[v] = weights(a.pre.weight, 1.f, 1.f, v);
+        w2[v] = weights(a.post.weight, 1.f, a.branch_scale, v);
+        if (GATE) b2[v] = weights(a.post.bias, 0.f, a.branch_scale, v);
+    }
 
-    Cols dw1 = all8(0.f), db1 = dw1, dw2 = dw1, db2 = dw1, dg = dw1;
-    const float2 bs = both(a.branch_scale), rs = both(a.residual_scale);
+    // sums down the rows; of the post-norm's gradients without the branch's scale, which comes at the end
+    Cols dw1[V], db1[V], dw2[V], db2[V], dg[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) dw1[v] = db1[v] = dw2[v] = db2[v] = dg[v] = all8(0.f);
+    const float2 rs = both(a.residual_scale);
 
     // the eight sums of a row, published to every CTA of the team
-    auto publish = [&](uint64_t row, uint32_t slot, const GateRow &g, const float4 &st, uint32_t turn) {
-        const Row w = load_row(row, slot, g);
+    auto publish = [&](uint64_t row, uint32_t slot, const GateRow &gr, const float4 &st, uint32_t at) {
         const float2 x1 = both(st.y), x0 = both(-st.x), y1 = both(st.w), y0 = both(-st.z);
         float2 s2[kSums];
 #pragma unroll
         for (int k = 0; k < kSums; ++k) s2[k] = both(0.f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 xhat = mul2(add2(w.r.v[i], x0), x1), yhat = mul2(add2(w.y.v[i], y0), y1);
-            const float2 av = mul2(w1.v[i], w.dh.v[i]);
-            const float2 base = fma2(x1, av, w.dr.v[i]);
-            float2 c = mul2(bs, w2.v[i]);
-            if (GATE) c = mul2(c, a.gate_act == BF16OPT_GATE_SIGMOID ? sigmoid2(w.gate.v[i]) : w.gate.v[i]);
-            const float2 cy = mul2(c, yhat);
-            s2[0] = add2(s2[0], av);
-            s2[1] = fma2(av, xhat, s2[1]);
-            s2[2] = fma2(c, base, s2[2]);
-            s2[3] = add2(s2[3], c);
-            s2[4] = fma2(c, xhat, s2[4]);
-            s2[5] = fma2(cy, base, s2[5]);
-            s2[6] = add2(s2[6], cy);
-            s2[7] = fma2(cy, xhat, s2[7]);
+        for (int v = 0; v < V; ++v) {
+            const Run w = load_run(row, slot, gr, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 xhat = mul2(add2(w.r.v[i], x0), x1), yhat = mul2(add2(w.y.v[i], y0), y1);
+                const float2 av = mul2(w1[v].v[i], w.dh.v[i]);
+                const float2 base = fma2(x1, av, w.dr.v[i]);
+                float2 c = w2[v].v[i];
+                if (GATE) c = mul2(c, a.gate_act == BF16OPT_GATE_SIGMOID ? sigmoid2(w.gate.v[i]) : w.gate.v[i]);
+                const float2 cy = mul2(c, yhat);
+                s2[0] = add2(s2[0], av);
+                s2[1] = fma2(av, xhat, s2[1]);
+                s2[2] = fma2(c, base, s2[2]);
+                s2[3] = add2(s2[3], c);
+                s2[4] = fma2(c, xhat, s2[4]);
+                s2[5] = fma2(cy, base, s2[5]);
+                s2[6] = add2(s2[6], cy);
+                s2[7] = fma2(cy, xhat, s2[7]);
+            }
         }
         float s[kSums];
 #pragma unroll
         for (int k = 0; k < kSums; ++k) s[k] = s2[k].x + s2[k].y;
-        const float sum = warp_sum8(s, lane);   // lane l < 8: value lane_value(l)
-        float *to = sums_of(turn) + (rank * warps + warp) * kSums + lane_value(lane & 7);
+        const float sum = warp_sum8(s, lane);   // value lane_value(lane & 7)
+        float *to = sm_sums + at + (rank * warps + warp) * kSums + lane_value(lane & 7);
         if (ranks > 1) {
-            if ((lane >> 3) < ranks) *cluster.map_shared_rank(to, lane >> 3) = sum;   // eight lanes to each rank
+            for (uint32_t r = lane >> 3; r < ranks; r += 4) *cluster.map_shared_rank(to, r) = sum;   // eight lanes to each rank
         } else if (lane < 8) {
             *to = sum;
         }
     };
+    // The sums of all entries, in their order: a lane adds up quarters (four values) of every sixteenth
+    // entry, then the lanes join, handing half of their values over while they have more than one.
+    auto totals = [&](uint32_t at, float (&s)[kSums]) {
+        const float4 *from = reinterpret_cast<const float4 *>(sm_sums + at);
+        float4 q4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (uint32_t i = lane; i < 2 * entries; i += 32) {
+            const float4 e = from[i];
+            q4.x += e.x, q4.y += e.y, q4.z += e.z, q4.w += e.w;
+        }
+        const bool hi = lane & 16, mid = lane & 8;
+        const float2 keep = hi ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y), give = hi ? make_float2(q4.x, q4.y) : make_float2(q4.z, q4.w);
+        const float2 h = make_float2(keep.x + __shfl_xor_sync(0xffffffffu, give.x, 16), keep.y + __shfl_xor_sync(0xffffffffu, give.y, 16));
+        float one = (mid ? h.y : h.x) + __shfl_xor_sync(0xffffffffu, mid ? h.x : h.y, 8);
+        one += __shfl_xor_sync(0xffffffffu, one, 4);
+        one += __shfl_xor_sync(0xffffffffu, one, 2);
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) s[k] = __shfl_sync(0xffffffffu, one, (k >> 2) | ((k >> 1) & 1) << 4 | (k & 1) << 3);
+    };
 
     float4 st = stats_of(row0), st1 = stats_of(row0 + 1);
-    uint32_t slot = 0, slot1 = depth == 1 ? 0 : 1;
-    if (row0 < row1) {
-        if (VEC) copy_wait_for(depth - 1);
-        publish(row0, 0, gate, st, 0);
-    }
+    uint32_t slot = 0, slot1 = 1;   // the ring is two rows deep at least
+    if (VEC) copy_wait_for(depth - 1);
+    publish(row0, 0, gate, st, 0);
     if (ranks > 1) cluster_arrive();
-    uint32_t turn = 0;
-    for (uint64_t row = row0; row < row1; ++row, ++turn) {
+    for (uint64_t row = row0; row < row1; ++row) {
         const float4 st2 = stats_of(row + 2);
+        const uint32_t at1 = sums_next(sums_at);
         if (ranks > 1) cluster_wait();
         else __syncthreads();
         // the next row's sums set out before this row's are used
+        GateRow gate1 = gate;
+        gate_next(gate1);
         if (row + 1 < row1) {
             if (VEC) copy_wait_for(depth - 2);
-            GateRow g = gate;
-            gate_next(g);
-            publish(row + 1, slot1, g, st1, turn + 1);
+            publish(row + 1, slot1, gate1, st1, at1);
         }
         if (ranks > 1) cluster_arrive();
 
-        float sum = 0.f;
-        for (uint32_t i = lane >> 3; i < ranks * warps; i += 4) sum += sums_of(turn)[i * kSums + (lane & 7)];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         float s[kSums];
-#pragma unroll
-        for (int k = 0; k < kSums; ++k) s[k] = __shfl_sync(0xffffffffu, sum, k);
+        totals(sums_at, s);
+        sums_at = at1;
         // g = base - (m1 + xhat m2);  e = c g;  dy = rs2 (e - n1 - yhat n2)
         const float m1 = pre_layer ? s[0] * inv_h * st.y : 0.f, m2 = s[1] * inv_h * st.y;
         const float n1 = post_layer ? (s[2] - m1 * s[3] - m2 * s[4]) * inv_h : 0.f;
         const float n2 = post ? (s[5] - m1 * s[6] - m2 * s[7]) * inv_h : 0.f;
-
-        const Row w = load_row(row, slot, gate);
         const float2 x1 = both(st.y), x0 = both(-st.x), y1 = both(st.w), y0 = both(-st.z);
         const float2 nm1 = both(-m1), nm2 = both(-m2), nn1 = both(-n1), nn2 = both(-n2);
-        Cols dx, dy, dgr;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 xhat = mul2(add2(w.r.v[i], x0), x1), yhat = mul2(add2(w.y.v[i], y0), y1);
-            const float2 base = fma2(x1, mul2(w1.v[i], w.dh.v[i]), w.dr.v[i]);
-            const float2 g = add2(fma2(xhat, nm2, base), nm1);
-            dx.v[i] = mul2(rs, g);
-            float2 dn = mul2(bs, g);
-            if (GATE) {
-                float2 act = w.gate.v[i];
-                const float2 du = mul2(dn, fma2(yhat, w2.v[i], b2.v[i]));
-                if (a.gate_act == BF16OPT_GATE_SIGMOID) {
-                    act = sigmoid2(act);
-                    dgr.v[i] = mul2(du, mul2(act, make_float2(1.f - act.x, 1.f - act.y)));
-                } else {
-                    dgr.v[i] = du;
-                }
-                dn = mul2(act, dn);
-            }
-            dw2.v[i] = fma2(dn, yhat, dw2.v[i]);
-            db2.v[i] = add2(db2.v[i], dn);
-            dw1.v[i] = fma2(w.dh.v[i], xhat, dw1.v[i]);
-            db1.v[i] = add2(db1.v[i], w.dh.v[i]);
-            dy.v[i] = mul2(y1, add2(fma2(w2.v[i], dn, mul2(yhat, nn2)), nn1));
-        }
+        // the gate's rows end, here or for this team; its sum is whole if they all are this team's,
+        // else a part: of the team's first gate, or of its last
+        const uint64_t gate_first = gate.row * a.rows_per_gate;
+        const bool gate_ends = GATE && q.shared_gate && (gate.left == 1 || row + 1 == row1), gate_whole = gate_first >= row0 && gate.left == 1;
         const uint64_t o = row * a.hidden + c0;
-        store_cols<VEC>(reinterpret_cast<TS *>(q.dx) + o, n, threads, t, dx);
-        store_cols<VEC>(reinterpret_cast<TB *>(q.dy) + o, n, threads, t, dy);
-        if (GATE && q.dgate) {
-            if (q.shared_gate) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) dg.v[i] = add2(dg.v[i], dgr.v[i]);
-                if (gate.left == 1 || row + 1 == row1) {   // its rows end, here or for this team
-                    const uint64_t first = gate.row * a.rows_per_gate;
-                    // the sum is whole if they all are this team's; else a part: the team's first gate's, or its last's
-                    if (first >= row0 && gate.left == 1) store_cols<VEC>(reinterpret_cast<TB *>(q.dgate) + gate.row * a.hidden + c0, n, threads, t, dg);
-                    else store_cols<VEC>(q.gate_part + (size_t)(2 * team + (first > row0)) * a.hidden + c0, n, threads, t, dg);
-                    dg = all8(0.f);
+        for (int v = 0; v < V; ++v) {
+            const Run w = load_run(row, slot, gate, v);
+            Cols dx, dy, dgr;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 xhat = mul2(add2(w.r.v[i], x0), x1), yhat = mul2(add2(w.y.v[i], y0), y1);
+                const float2 base = fma2(x1, mul2(w1[v].v[i], w.dh.v[i]), w.dr.v[i]);
+                float2 g = add2(fma2(xhat, nm2, base), nm1);
+                dx.v[i] = mul2(rs, g);
+                if (GATE) {
+                    float2 act = w.gate.v[i];
+                    const float2 du = mul2(g, fma2(yhat, w2[v].v[i], b2[v].v[i]));
+                    if (a.gate_act == BF16OPT_GATE_SIGMOID) {
+                        act = sigmoid2(act);
+                        dgr.v[i] = mul2(du, mul2(act, make_float2(1.f - act.x, 1.f - act.y)));
+                    } else {
+                        dgr.v[i] = du;
+                    }
+                    g = mul2(act, g);
                 }
-            } else {
-                store_cols<VEC>(reinterpret_cast<TB *>(q.dgate) + o, n, threads, t, dgr);
+                dw2[v].v[i] = fma2(g, yhat, dw2[v].v[i]);
+                db2[v].v[i] = add2(db2[v].v[i], g);
+                dw1[v].v[i] = fma2(w.dh.v[i], xhat, dw1[v].v[i]);
+                db1[v].v[i] = add2(db1[v].v[i], w.dh.v[i]);
+                dy.v[i] = mul2(y1, add2(fma2(w2[v].v[i], g, mul2(yhat, nn2)), nn1));
+            }
+            store_cols<VEC>(reinterpret_cast<TS *>(q.dx) + o, col(v), n, dx);
+            store_cols<VEC>(reinterpret_cast<TB *>(q.dy) + o, col(v), n, dy);
+            if (GATE && q.dgate) {
+                if (q.shared_gate) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dg[v].v[i] = add2(dg[v].v[i], dgr.v[i]);
+                    if (gate_ends) {
+                        if (gate_whole) store_cols<VEC>(reinterpret_cast<TB *>(q.dgate) + gate.row * a.hidden + c0, col(v), n, dg[v]);
+                        else store_cols<VEC>(q.gate_part + (size_t)(2 * team + (gate_first > row0 ? 1 : 0)) * a.hidden + c0, col(v), n, dg[v]);
+                        dg[v] = all8(0.f);
+                    }
+                } else {
+                    store_cols<VEC>(reinterpret_cast<TB *>(q.dgate) + o, col(v), n, dgr);
+                }
             }
         }
-        if (VEC) {
-            fill();
-            slot = slot1;
-            slot1 = slot1 + 1 == depth ? 0 : slot1 + 1;
-        }
+        if (VEC) fill();
+        slot = slot1;
+        slot1 = slot1 + 1 == depth ? 0 : slot1 + 1;
         st = st1, st1 = st2;
-        gate_next(gate);
+        gate = gate1;
     }
     if (ranks > 1) cluster_wait();   // for the last arrival: nobody leaves while others may write here
-    float *p = q.part + (size_t)team * 4 * a.hidden + c0;
-    if (q.want & 1) store_cols<VEC>(p, n, threads, t, dw1);
-    if (q.want & 2) store_cols<VEC>(p + a.hidden, n, threads, t, db1);
-    if (q.want & 4) store_cols<VEC>(p + 2 * (size_t)a.hidden, n, threads, t, dw2);
-    if (q.want & 8) store_cols<VEC>(p + 3 * (size_t)a.hidden, n, threads, t, db2);
+    const float2 bs = both(a.branch_scale);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float *p = q.part + (size_t)team * 4 * a.hidden + c0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dw2[v].v[i] = mul2(bs, dw2[v].v[i]), db2[v].v[i] = mul2(bs, db2[v].v[i]);
+        if (q.want & 1) store_cols<VEC>(p, col(v), n, dw1[v]);
+        if (q.want & 2) store_cols<VEC>(p + a.hidden, col(v), n, db1[v]);
+        if (q.want & 4) store_cols<VEC>(p + 2 * (size_t)a.hidden, col(v), n, dw2[v]);
+        if (q.want & 8) store_cols<VEC>(p + 3 * (size_t)a.hidden, col(v), n, db2[v]);
+    }
     pdl_leave();
 }
 
@@ -747,19 +813,26 @@ int by_types(const bf16opt_norm_gate_t *d, F &&f) {
 
 constexpr size_t kSmemBytes = 226 * 1024;   // of a multiprocessor; each CTA takes 1 KB besides its own
 
+// Runs of eight columns a thread has: two where whole vectors pass through the ring, and
+// there is no gate (its sums would not fit the registers).
+template <bool VEC, bool GATE>
+constexpr int runs_of() { return VEC && !GATE ? 2 : 1; }
+
 template <class TB, class TS, bool VEC, bool GATE>
 int shape_v(const bf16opt_norm_gate_t *d, int sms, Shape &s) {
-    s.cluster = (d->hidden + kColumns - 1) / kColumns;
-    if (s.cluster == 3) s.cluster = 4;
+    constexpr int V = runs_of<VEC, GATE>();
+    s.cluster = 1;
+    while (s.cluster * kColumns < d->hidden) s.cluster *= 2;
     const uint32_t cols = (d->hidden + s.cluster - 1) / s.cluster;
-    s.threads = ((cols + 7) / 8 + 31) / 32 * 32;
+    s.threads = ((cols + 8 * V - 1) / (8 * V) + 31) / 32 * 32;
     const unsigned per_sm = std::max(1u, std::min(512u / s.threads, 16u));   // 128 registers a thread
-    const size_t row = (size_t)s.threads * ring_units<TB, TS, GATE>() * 16, sums = 3 * s.cluster * s.threads / 32 * kSums * sizeof(float);
+    const size_t row = (size_t)s.threads * V * ring_units<TB, TS, GATE>() * 16, sums = 3 * s.cluster * s.threads / 32 * kSums * sizeof(float);
     s.depth = VEC ? (uint32_t)std::max<size_t>(2, std::min<size_t>(8, (kSmemBytes / per_sm - sums - 1024) / row)) : 2;
     s.smem = (VEC ? s.depth * row : 0) + sums;
-    uint64_t teams = (uint64_t)sms * per_sm;
+    const unsigned resident = std::min(per_sm, (unsigned)(kSmemBytes / (s.smem + 1024)));
+    uint64_t teams = (uint64_t)sms * resident;
     if (s.cluster > 1) {
-        auto k = k_norm_backward<TB, TS, VEC, GATE>;
+        auto k = k_norm_backward<TB, TS, VEC, GATE, runs_of<VEC, GATE>()>;
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
         int fit = 0;
         if (e == cudaSuccess) e = clusters_that_fit(Launch{s.cluster, s.threads, s.smem, nullptr, s.cluster, true}, k, fit);
@@ -779,7 +852,7 @@ int shape_t(const bf16opt_norm_gate_t *d, bool vec, int sms, Shape &s) {
 
 template <class TB, class TS, bool VEC, bool GATE>
 int backward_v(const Args &a, const BackArgs &q, const Shape &s, cudaStream_t st) {
-    auto k = k_norm_backward<TB, TS, VEC, GATE>;
+    auto k = k_norm_backward<TB, TS, VEC, GATE, runs_of<VEC, GATE>()>;
     if (s.smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
         if (e != cudaSuccess) return fail_cuda(e, "norm_gate kernel attribute");

@@ -27,8 +27,9 @@ namespace bf16ops {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 // Largest of the warp's values (NaN passed over), in every lane.
@@ -46,42 +47,31 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Two FP32 numbers in one register pair: one instruction for both.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t &>(r)) : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-    return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t &>(r)) : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-    return r;
-}
+#define BF16OPS_PAIR_OP(name, op)                                                                                             \
+    __device__ __forceinline__ float2 name(float2 a, float2 b) {                                                             \
+        float2 r;                                                                                                            \
+        asm("{\n .reg .b64 a, b, r;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n " op " r, a, b;\n mov.b64 {%0, %1}, r;\n}" \
+            : "=f"(r.x), "=f"(r.y)                                                                                           \
+            : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));                                                                       \
+        return r;                                                                                                            \
+    }
+BF16OPS_PAIR_OP(add2, "add.rn.f32x2")
+BF16OPS_PAIR_OP(mul2, "mul.rn.f32x2")
+#undef BF16OPS_PAIR_OP
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<uint64_t &>(r))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+    asm("{\n .reg .b64 a, b, c, r;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+        " fma.rn.f32x2 r, a, b, c;\n mov.b64 {%0, %1}, r;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return r;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // 16 bytes from global to shared memory without registers in between; the
 // thread's copies up to a commit are one group.
-__device__ __forceinline__ void copy_async16(void *smem, const void *src, uint64_t policy) {
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(src),
-                 "l"(policy)
-                 : "memory");
-}
-// L2 policies for data that is read once, and for data that is read again soon.
-__device__ __forceinline__ uint64_t l2_policy_first() {
-    uint64_t p;
-    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-__device__ __forceinline__ uint64_t l2_policy_normal() {
-    uint64_t p;
-    asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
-    return p;
+__device__ __forceinline__ void copy_async16(void *smem, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Until at most N of this thread's newest groups are in flight.
@@ -92,16 +82,14 @@ __device__ __forceinline__ void copy_wait() {
 
 // The same for a number that is the same in all threads; above 7 it waits for more than it need.
 __device__ __forceinline__ void copy_wait_for(uint32_t n) {
-    switch (n) {
-    case 0: copy_wait<0>(); break;
-    case 1: copy_wait<1>(); break;
-    case 2: copy_wait<2>(); break;
-    case 3: copy_wait<3>(); break;
-    case 4: copy_wait<4>(); break;
-    case 5: copy_wait<5>(); break;
-    case 6: copy_wait<6>(); break;
-    default: copy_wait<7>(); break;
-    }
+    if (n == 0) copy_wait<0>();
+    else if (n == 1) copy_wait<1>();
+    else if (n == 2) copy_wait<2>();
+    else if (n == 3) copy_wait<3>();
+    else if (n == 4) copy_wait<4>();
+    else if (n == 5) copy_wait<5>();
+    else if (n == 6) copy_wait<6>();
+    else copy_wait<7>();
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;
