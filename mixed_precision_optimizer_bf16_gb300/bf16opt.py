@@ -180,16 +180,16 @@ def load(path=None):
     L.bf16opt_set_lr_schedule.argtypes = [hp, ctypes.POINTER(bf16opt_lr_schedule_t)]
     L.bf16opt_grad_norm_static.restype = ctypes.c_int
     L.bf16opt_grad_norm_static.argtypes = [c_vp, c_u64, c_f32, c_f32, c_vp, c_vp]
-    dd, dn, db = (ctypes.POINTER(t) for t in (bf16opt_distill_t, bf16opt_norm_gate_t, bf16opt_balance_t))
-    L.bf16opt_distill_forward.argtypes = [dd, c_vp, c_vp, c_vp]
-    L.bf16opt_distill_backward.argtypes = [dd, c_vp, c_vp, c_vp, c_u64, c_vp]
-    L.bf16opt_distill_loss_grad.argtypes = [dd, c_vp, c_vp, c_vp, c_vp, c_u64, c_vp]
-    L.bf16opt_norm_gate_forward.argtypes = [dn, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]
-    L.bf16opt_norm_gate_workspace.argtypes = [dn, ctypes.POINTER(c_u64)]
-    L.bf16opt_norm_gate_backward.argtypes = [dn] + [c_vp] * 13 + [c_u64, c_vp]
-    L.bf16opt_balance_workspace.argtypes = [db, ctypes.POINTER(c_u64)]
-    L.bf16opt_balance_forward.argtypes = [db] + [c_vp] * 6 + [c_u64, c_vp]
-    L.bf16opt_balance_backward.argtypes = [db] + [c_vp] * 6 + [c_u64, c_vp]
+    # training operators: a descriptor is the struct or its packed bytes, an address an int (None, 0: NULL)
+    L.bf16opt_distill_forward.argtypes = [c_vp] * 4
+    L.bf16opt_distill_backward.argtypes = [c_vp] * 4 + [c_u64, c_vp]
+    L.bf16opt_distill_loss_grad.argtypes = [c_vp] * 5 + [c_u64, c_vp]
+    L.bf16opt_norm_gate_forward.argtypes = [c_vp] * 7
+    L.bf16opt_norm_gate_workspace.argtypes = [c_vp, ctypes.POINTER(c_u64)]
+    L.bf16opt_norm_gate_backward.argtypes = [c_vp] * 14 + [c_u64, c_vp]
+    L.bf16opt_balance_workspace.argtypes = [c_vp, ctypes.POINTER(c_u64)]
+    L.bf16opt_balance_forward.argtypes = [c_vp] * 7 + [c_u64, c_vp]
+    L.bf16opt_balance_backward.argtypes = [c_vp] * 7 + [c_u64, c_vp]
     for name in EXPORTS[-9:]:
         getattr(L, name).restype = ctypes.c_int
     if path == lib_path():
@@ -326,50 +326,54 @@ def bf16opt_step_path(h):
     return rc, path.value
 
 
-# Training operators: descriptors as structs, device addresses as ints (None: NULL).
+# Training operators: descriptors as structs or their packed bytes, device addresses as ints (None, 0: NULL).
+
+def _desc(d):
+    return ctypes.byref(d) if isinstance(d, ctypes.Structure) else d
+
 
 def bf16opt_distill_forward(d, loss, lse=None, stream=0):
-    return load().bf16opt_distill_forward(d, loss, lse, stream)
+    return load().bf16opt_distill_forward(_desc(d), loss, lse, stream)
 
 
 def bf16opt_distill_backward(d, lse, dloss, dlogits, dlogits_stride, stream=0):
-    return load().bf16opt_distill_backward(d, lse, dloss, dlogits, dlogits_stride, stream)
+    return load().bf16opt_distill_backward(_desc(d), lse, dloss, dlogits, dlogits_stride, stream)
 
 
 def bf16opt_distill_loss_grad(d, dloss, loss, lse, dlogits, dlogits_stride, stream=0):
-    return load().bf16opt_distill_loss_grad(d, dloss, loss, lse, dlogits, dlogits_stride, stream)
+    return load().bf16opt_distill_loss_grad(_desc(d), dloss, loss, lse, dlogits, dlogits_stride, stream)
 
 
 def bf16opt_norm_gate_forward(d, x, y, r, h=None, stats=None, stream=0):
-    return load().bf16opt_norm_gate_forward(d, x, y, r, h, stats, stream)
+    return load().bf16opt_norm_gate_forward(_desc(d), x, y, r, h, stats, stream)
 
 
 def bf16opt_norm_gate_workspace(d):
     """(status, bytes)."""
     n = c_u64(0)
-    rc = load().bf16opt_norm_gate_workspace(d, n)
+    rc = load().bf16opt_norm_gate_workspace(_desc(d), n)
     return rc, n.value
 
 
 def bf16opt_norm_gate_backward(d, dr, dh, r, y, stats, dx, dy, dgate, dpre_weight, dpre_bias, dpost_weight, dpost_bias,
                                workspace, workspace_bytes, stream=0):
-    return load().bf16opt_norm_gate_backward(d, dr, dh, r, y, stats, dx, dy, dgate, dpre_weight, dpre_bias, dpost_weight,
+    return load().bf16opt_norm_gate_backward(_desc(d), dr, dh, r, y, stats, dx, dy, dgate, dpre_weight, dpre_bias, dpost_weight,
                                              dpost_bias, workspace, workspace_bytes, stream)
 
 
 def bf16opt_balance_workspace(d):
     """(status, bytes)."""
     n = c_u64(0)
-    rc = load().bf16opt_balance_workspace(d, n)
+    rc = load().bf16opt_balance_workspace(_desc(d), n)
     return rc, n.value
 
 
 def bf16opt_balance_forward(d, ids, weights, counts, loss, saved, workspace=None, workspace_bytes=0, stream=0):
-    return load().bf16opt_balance_forward(d, ids, weights, counts, loss, saved, workspace, workspace_bytes, stream)
+    return load().bf16opt_balance_forward(_desc(d), ids, weights, counts, loss, saved, workspace, workspace_bytes, stream)
 
 
 def bf16opt_balance_backward(d, ids, counts, saved, dweights, dloss, dlogits, dlogits_stride, stream=0):
-    return load().bf16opt_balance_backward(d, ids, counts, saved, dweights, dloss, dlogits, dlogits_stride, stream)
+    return load().bf16opt_balance_backward(_desc(d), ids, counts, saved, dweights, dloss, dlogits, dlogits_stride, stream)
 
 
 def bf16opt_last_error(h=None):

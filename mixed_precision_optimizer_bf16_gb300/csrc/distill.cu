@@ -713,17 +713,13 @@ template <int kThreads, class T, bool FORWARD, bool GRAD, int POWER>
 int launch_k(const Args &a, unsigned cluster, cudaStream_t stream) {
     auto k = k_distill<kThreads, T, FORWARD, GRAD, POWER>;
     const size_t smem = (size_t)ring_depth(kThreads) * kThreads * kU * 16 + (size_t)(a.k + 1) * 12 + (GRAD ? table_size(a.k) * 4 : 0);
-    if (smem > 32 * 1024) {   // with the static arrays, more than a kernel may have unasked
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return fail_cuda(e, "distill kernel attribute");
-    }
     // As many clusters as fit at once (a cluster of eight cannot use every SM: those of a
     // processing cluster are not a multiple of it), each walking its rows; more would run as a
     // second wave: 57 clusters where 51 fit took 639 us on 2048 rows of 250880 bf16.
     Launch l{cluster, (unsigned)kThreads, smem, stream, cluster, true};
     int fit = 0;
     const cudaError_t eo = clusters_that_fit(l, k, fit);
-    if (eo != cudaSuccess || fit < 1) return fail_cuda(eo != cudaSuccess ? eo : cudaErrorLaunchOutOfResources, "distill occupancy");
+    if (eo != cudaSuccess) return fail_cuda(eo, "distill occupancy");
     // in equal shares: with 512 rows, 47 clusters of at most 11 rows instead of 51
     const uint64_t turns = (a.rows + fit - 1) / fit;
     l.grid = (unsigned)((a.rows + turns - 1) / turns) * cluster;

@@ -829,16 +829,11 @@ int shape_v(const bf16opt_norm_gate_t *d, int sms, Shape &s) {
     const size_t row = (size_t)s.threads * V * ring_units<TB, TS, GATE>() * 16, sums = 3 * s.cluster * s.threads / 32 * kSums * sizeof(float);
     s.depth = VEC ? (uint32_t)std::max<size_t>(2, std::min<size_t>(8, (kSmemBytes / per_sm - sums - 1024) / row)) : 2;
     s.smem = (VEC ? s.depth * row : 0) + sums;
-    const unsigned resident = std::min(per_sm, (unsigned)(kSmemBytes / (s.smem + 1024)));
-    uint64_t teams = (uint64_t)sms * resident;
-    if (s.cluster > 1) {
-        auto k = k_norm_backward<TB, TS, VEC, GATE, runs_of<VEC, GATE>()>;
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
-        int fit = 0;
-        if (e == cudaSuccess) e = clusters_that_fit(Launch{s.cluster, s.threads, s.smem, nullptr, s.cluster, true}, k, fit);
-        if (e != cudaSuccess || fit < 1) return fail_cuda(e != cudaSuccess ? e : cudaErrorLaunchOutOfResources, "norm_gate occupancy");
-        teams = fit;
-    }
+    int fit = 0;
+    const cudaError_t e = clusters_that_fit(Launch{s.cluster, s.threads, s.smem, nullptr, s.cluster, true},
+                                            k_norm_backward<TB, TS, VEC, GATE, V>, fit);
+    if (e != cudaSuccess) return fail_cuda(e, "norm_gate occupancy");
+    const uint64_t teams = fit;
     s.teams = (uint32_t)std::min<uint64_t>(teams, std::max<uint64_t>(1, d->rows));
     s.part_floats = (uint64_t)s.teams * 4 * d->hidden;
     s.gate_floats = d->gate_rows && d->gate_rows != d->rows ? (uint64_t)s.teams * 2 * d->hidden : 0;
@@ -853,10 +848,6 @@ int shape_t(const bf16opt_norm_gate_t *d, bool vec, int sms, Shape &s) {
 template <class TB, class TS, bool VEC, bool GATE>
 int backward_v(const Args &a, const BackArgs &q, const Shape &s, cudaStream_t st) {
     auto k = k_norm_backward<TB, TS, VEC, GATE, runs_of<VEC, GATE>()>;
-    if (s.smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
-        if (e != cudaSuccess) return fail_cuda(e, "norm_gate kernel attribute");
-    }
     Launch l{s.teams * s.cluster, s.threads, s.smem, st, s.cluster, true};
     const cudaError_t e = launch(l, k, a, q, s.depth);
     return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "norm_gate kernel launch");

@@ -215,10 +215,11 @@ struct Launch {
     bool dependent = false;  // programmatic dependent launch (the kernel calls pdl_enter)
 };
 
-// Clusters of this launch that the device holds at once.  The question costs
-// tens of microseconds, so the answers are kept, by kernel, device and shape.
+// Clusters (or CTAs) of this launch that the device holds at once, with the kernel
+// allowed its shared memory.  Both questions cost microseconds, so the answers
+// are kept, by kernel, device and shape.
 template <class... KArgs>
-cudaError_t clusters_that_fit(const Launch &l, void (*kernel)(KArgs...), int &n) {
+cudaError_t clusters_that_fit(const Launch &l, void (*kernel)(KArgs...), int &n, bool ask = false) {
     struct Known {
         const void *kernel;
         int device;
@@ -234,12 +235,18 @@ cudaError_t clusters_that_fit(const Launch &l, void (*kernel)(KArgs...), int &n)
     if (e != cudaSuccess) return e;
     const void *key = reinterpret_cast<const void *>(kernel);
     std::lock_guard<std::mutex> lock(mu);
-    for (unsigned i = 0; i < std::min(used, 64u); ++i) {
-        const Known &k = known[i];
-        if (k.kernel == key && k.device == dev && k.cluster == l.cluster && k.block == l.block && k.smem == l.smem) {
-            n = k.n;
-            return cudaSuccess;
+    if (!ask)
+        for (unsigned i = 0; i < std::min(used, 64u); ++i) {
+            const Known &k = known[i];
+            if (k.kernel == key && k.device == dev && k.cluster == l.cluster && k.block == l.block && k.smem == l.smem) {
+                n = k.n;
+                return cudaSuccess;
+            }
         }
+    if (l.smem > 32 * 1024) {   // with the static arrays, more than a kernel may have unasked
+        // as much as any shape of it takes, so that a smaller one's answer does not take it back
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(220 * 1024));
+        if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(l.cluster);
@@ -252,12 +259,13 @@ cudaError_t clusters_that_fit(const Launch &l, void (*kernel)(KArgs...), int &n)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e == cudaSuccess && n < 1) e = cudaErrorLaunchOutOfResources;
     if (e == cudaSuccess) known[used++ % 64] = Known{key, dev, l.cluster, l.block, l.smem, n};
     return e;
 }
 
 template <class... KArgs, class... Args>
-cudaError_t launch(const Launch &l, void (*kernel)(KArgs...), Args &&...args) {
+cudaError_t launch(const Launch &l, void (*kernel)(KArgs...), const Args &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(l.grid);
     cfg.blockDim = dim3(l.block);
@@ -278,7 +286,14 @@ cudaError_t launch(const Launch &l, void (*kernel)(KArgs...), Args &&...args) {
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e == cudaErrorInvalidValue && l.smem > 32 * 1024) {   // a context that replaced a reset one has the kernel without its shared memory
+        cudaGetLastError();
+        int fit = 0;
+        e = clusters_that_fit(l, kernel, fit, true);
+        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    }
+    return e;
 }
 
 }  // namespace bf16ops

@@ -12,6 +12,8 @@ can be captured in a CUDA graph.
   balance_forward / balance_backward, balance (autograd)
 """
 import contextlib
+import functools
+import struct
 
 import torch
 
@@ -23,22 +25,41 @@ _F32 = (torch.float32,)
 _NORM = {None: C.BF16OPT_NORM_NONE, "none": C.BF16OPT_NORM_NONE, "rms": C.BF16OPT_NORM_RMS, "layer": C.BF16OPT_NORM_LAYER}
 _ACT = {None: C.BF16OPT_GATE_IDENTITY, "none": C.BF16OPT_GATE_IDENTITY, "sigmoid": C.BF16OPT_GATE_SIGMOID}
 
+# The descriptors of include/bf16opt.h as packed bytes, in the structs' own layout:
+# a small call's cost is this file's, and packing takes a fraction of what a
+# ctypes structure takes.  (The tests compare both.)
+_DISTILL_T = struct.Struct("@QII4iPQPQPQPPPfff4x")
+_NORM_GATE_T = struct.Struct("@QI6iIQPPPPPfff4x")
+_BALANCE_T = struct.Struct("@QIIQiiPQPff")
 
-def _need(t, what, dtypes, shape, device, rows_apart=False):
-    """A tensor that the library may reach through a raw pointer: on `device`,
-    of one of `dtypes`, of `shape`, contiguous -- or, with rows_apart, with
-    contiguous rows that do not overlap."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+_empty, _empty_like = torch.empty, torch.empty_like
+_Tensor = torch.Tensor
+
+
+def _need(t, what, dtypes, shape, index, rows_apart=False):
+    """A tensor that the library may reach through a raw pointer: on CUDA device
+    `index`, of one of `dtypes`, of `shape`, contiguous -- or, with rows_apart,
+    with contiguous rows that do not overlap."""
+    if isinstance(t, _Tensor) and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{what}: must be a CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{what}: on {t.device}, expected cuda:{index}")
     if t.dtype not in dtypes:
         raise ValueError(f"{what}: dtype {t.dtype}, expected one of {[str(d) for d in dtypes]}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        if not rows_apart or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-            raise ValueError(f"{what}: must be contiguous" + (" within rows that do not overlap" if rows_apart else ""))
+    if not rows_apart or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{what}: must be contiguous" + (" within rows that do not overlap" if rows_apart else ""))
+
+
+def _matrix(t, what):
+    """(rows, columns, device index) of a CUDA matrix."""
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{what}: must be a CUDA tensor of two dimensions")
+    rows, columns = t.shape
+    return rows, columns, t.get_device()
 
 
 def _stride(t):
@@ -46,115 +67,106 @@ def _stride(t):
 
 
 def _p(t):
-    return t.data_ptr() if t is not None else None
+    return t.data_ptr() if t is not None else 0
 
 
-class _On:
-    """The device of `like` and `stream` (None: its current one) for a call:
-    `.handle` is the stream's.  Inputs are marked as used on a stream that is
-    not the current one, so that their memory outlives the kernels."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
-    __slots__ = ("like", "stream", "inputs", "handle", "_stack")
 
-    def __init__(self, like, stream, *inputs):
-        self.like, self.stream, self.inputs = like, stream, inputs
-
-    def __enter__(self):
-        self._stack = None
-        dev = self.like.device
-        if self.stream is None and dev.index == torch.cuda.current_device():
-            self.handle = torch.cuda.current_stream().cuda_stream
-            return self
-        self._stack = contextlib.ExitStack()
-        self._stack.enter_context(torch.cuda.device(dev))
-        stream = self.stream if self.stream is not None else torch.cuda.current_stream(dev)
-        if stream != torch.cuda.current_stream(dev):
-            for t in (self.like,) + self.inputs:
-                if t is not None:
-                    t.record_stream(stream)
-        self._stack.enter_context(torch.cuda.stream(stream))
-        self.handle = stream.cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        if self._stack is not None:
-            self._stack.close()
-        return False
+def _on_stream(call):
+    """Gives a function `stream=None`: it runs on the device of its first tensor,
+    on `stream` or on that device's current one.  Its inputs are marked as used
+    on a stream that is not the current one, so that their memory outlives the
+    kernels."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **more):
+        for first in args:
+            if first is not None:
+                break
+        if not isinstance(first, _Tensor) or not first.is_cuda or (stream is None and first.get_device() == _current_device()):
+            return call(*args, **more)
+        index = first.get_device()
+        with contextlib.ExitStack() as stack:
+            stack.enter_context(torch.cuda.device(index))
+            if stream is not None and stream != torch.cuda.current_stream(index):
+                for t in (*args, *more.values()):
+                    if isinstance(t, _Tensor) and t.is_cuda:
+                        t.record_stream(stream)
+                stack.enter_context(torch.cuda.stream(stream))
+            return call(*args, **more)
+    return run
 
 
 # ------------------------------------------------------------------ distillation
 
 def _distill(logits, teacher_ids, teacher_logits, temperature, kl_weight, ce_weight, labels, row_weight, teacher_lse):
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
-        raise ValueError("logits: must be a [rows, vocab] CUDA tensor")
-    rows, vocab = logits.shape
-    dev = logits.device
-    _need(logits, "logits", _TYPE, (rows, vocab), dev, rows_apart=True)
-    if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() != 2:
-        raise ValueError("teacher_ids: must be a [rows, k] CUDA tensor")
-    k = teacher_ids.shape[1]
-    _need(teacher_ids, "teacher_ids", _INDEX, (rows, k), dev, rows_apart=True)
-    _need(teacher_logits, "teacher_logits", _TYPE, (rows, k), dev, rows_apart=True)
+    """(descriptor, rows, device index)."""
+    rows, vocab, index = _matrix(logits, "logits")
+    k = _matrix(teacher_ids, "teacher_ids")[1]
+    _need(logits, "logits", _TYPE, (rows, vocab), index, True)
+    _need(teacher_ids, "teacher_ids", _INDEX, (rows, k), index, True)
+    _need(teacher_logits, "teacher_logits", _TYPE, (rows, k), index, True)
     if labels is not None:
-        _need(labels, "labels", _INDEX, (rows,), dev)
+        _need(labels, "labels", _INDEX, (rows,), index)
     if row_weight is not None:
-        _need(row_weight, "row_weight", _F32, (rows,), dev)
+        _need(row_weight, "row_weight", _F32, (rows,), index)
     if teacher_lse is not None:
-        _need(teacher_lse, "teacher_lse", _F32, (rows,), dev)
-    return C.bf16opt_distill_t(
+        _need(teacher_lse, "teacher_lse", _F32, (rows,), index)
+    return _DISTILL_T.pack(
         rows, vocab, k, _TYPE[logits.dtype], _TYPE[teacher_logits.dtype], _INDEX[teacher_ids.dtype],
         _INDEX[labels.dtype] if labels is not None else 0, logits.data_ptr(), _stride(logits), teacher_ids.data_ptr(),
         _stride(teacher_ids), teacher_logits.data_ptr(), _stride(teacher_logits), _p(teacher_lse), _p(labels),
-        _p(row_weight), temperature, kl_weight, ce_weight)
+        _p(row_weight), temperature, kl_weight, ce_weight), rows, index
 
 
+@_on_stream
 def distill_forward(logits, teacher_ids, teacher_logits, *, temperature=1.0, kl_weight=1.0, ce_weight=0.0, labels=None,
-                    row_weight=None, teacher_lse=None, stream=None):
+                    row_weight=None, teacher_lse=None):
     """Per-row loss [rows] and log-sum-exps [rows, 2] (FP32) of student logits
     [rows, vocab] (bf16 or FP32) against a teacher's kept entries [rows, k]
     (ids int32 or int64, logits bf16 or FP32; an id outside the vocabulary is
     no entry) and, with ce_weight, labels [rows] (outside: no label)."""
-    d = _distill(logits, teacher_ids, teacher_logits, temperature, kl_weight, ce_weight, labels, row_weight, teacher_lse)
-    with _On(logits, stream, teacher_ids, teacher_logits, labels, row_weight, teacher_lse) as on:
-        loss = torch.empty(d.rows, dtype=torch.float32, device=logits.device)
-        lse = torch.empty((d.rows, 2), dtype=torch.float32, device=logits.device)
-        C.check(C.bf16opt_distill_forward(d, loss.data_ptr(), lse.data_ptr(), on.handle))
+    d, rows, index = _distill(logits, teacher_ids, teacher_logits, temperature, kl_weight, ce_weight, labels, row_weight, teacher_lse)
+    loss = _empty(rows, dtype=torch.float32, device=logits.device)
+    lse = _empty((rows, 2), dtype=torch.float32, device=logits.device)
+    C.check(C.bf16opt_distill_forward(d, loss.data_ptr(), lse.data_ptr(), _raw_stream(index)))
     return loss, lse
 
 
-def _dlogits(logits, out):
+def _dlogits(logits, out, index):
     if out is None:
-        return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    _need(out, "out", (logits.dtype,), logits.shape, logits.device, rows_apart=True)
+        return _empty_like(logits, memory_format=torch.contiguous_format)
+    _need(out, "out", (logits.dtype,), logits.shape, index, True)
     return out
 
 
+@_on_stream
 def distill_backward(logits, teacher_ids, teacher_logits, lse, dloss=None, *, temperature=1.0, kl_weight=1.0, ce_weight=0.0,
-                     labels=None, row_weight=None, teacher_lse=None, out=None, stream=None):
+                     labels=None, row_weight=None, teacher_lse=None, out=None):
     """Gradient of the logits from that of the rows' losses (dloss [rows]
     FP32; None: 1), with distill_forward's arguments and lse.  out may be
     logits itself."""
-    d = _distill(logits, teacher_ids, teacher_logits, temperature, kl_weight, ce_weight, labels, row_weight, teacher_lse)
-    _need(lse, "lse", _F32, (d.rows, 2), logits.device)
+    d, rows, index = _distill(logits, teacher_ids, teacher_logits, temperature, kl_weight, ce_weight, labels, row_weight, teacher_lse)
+    _need(lse, "lse", _F32, (rows, 2), index)
     if dloss is not None:
-        _need(dloss, "dloss", _F32, (d.rows,), logits.device)
-    with _On(logits, stream, teacher_ids, teacher_logits, labels, row_weight, teacher_lse, lse, dloss, out) as on:
-        out = _dlogits(logits, out)
-        C.check(C.bf16opt_distill_backward(d, lse.data_ptr(), _p(dloss), out.data_ptr(), _stride(out), on.handle))
+        _need(dloss, "dloss", _F32, (rows,), index)
+    out = _dlogits(logits, out, index)
+    C.check(C.bf16opt_distill_backward(d, lse.data_ptr(), _p(dloss), out.data_ptr(), _stride(out), _raw_stream(index)))
     return out
 
 
+@_on_stream
 def distill_loss_grad(logits, teacher_ids, teacher_logits, dloss=None, *, temperature=1.0, kl_weight=1.0, ce_weight=0.0,
-                      labels=None, row_weight=None, teacher_lse=None, out=None, stream=None):
+                      labels=None, row_weight=None, teacher_lse=None, out=None):
     """Per-row loss and the gradient of the logits in one pass over them (for a
     gradient dloss, or 1, of each row's loss).  out may be logits itself."""
-    d = _distill(logits, teacher_ids, teacher_logits, temperature, kl_weight, ce_weight, labels, row_weight, teacher_lse)
+    d, rows, index = _distill(logits, teacher_ids, teacher_logits, temperature, kl_weight, ce_weight, labels, row_weight, teacher_lse)
     if dloss is not None:
-        _need(dloss, "dloss", _F32, (d.rows,), logits.device)
-    with _On(logits, stream, teacher_ids, teacher_logits, labels, row_weight, teacher_lse, dloss, out) as on:
-        loss = torch.empty(d.rows, dtype=torch.float32, device=logits.device)
-        out = _dlogits(logits, out)
-        C.check(C.bf16opt_distill_loss_grad(d, _p(dloss), loss.data_ptr(), None, out.data_ptr(), _stride(out), on.handle))
+        _need(dloss, "dloss", _F32, (rows,), index)
+    loss = _empty(rows, dtype=torch.float32, device=logits.device)
+    out = _dlogits(logits, out, index)
+    C.check(C.bf16opt_distill_loss_grad(d, _p(dloss), loss.data_ptr(), 0, out.data_ptr(), _stride(out), _raw_stream(index)))
     return loss, out
 
 
@@ -186,86 +198,84 @@ def distill_loss(logits, teacher_ids, teacher_logits, *, temperature=1.0, kl_wei
 
 # ------------------------------------------------------------------- gated norms
 
-def _norm_gate(stream_t, y, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate, gate_act, residual_scale,
-               branch_scale, eps, what):
-    if not isinstance(y, torch.Tensor) or y.dim() != 2:
-        raise ValueError("y: must be a [rows, hidden] CUDA tensor")
-    rows, hidden = y.shape
-    dev = y.device
-    _need(y, "y", _TYPE, (rows, hidden), dev)
-    if stream_t is not None:
-        _need(stream_t, what, _TYPE, (rows, hidden), dev)
+def _norm_gate(stream_t, what, y, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate, gate_act, residual_scale,
+               branch_scale, eps):
+    """(descriptor, rows, device index)."""
+    rows, hidden, index = _matrix(y, "y")
+    _need(y, "y", _TYPE, (rows, hidden), index)
+    _need(stream_t, what, _TYPE, (rows, hidden), index)
     if pre not in _NORM or post not in _NORM or gate_act not in _ACT:
         raise ValueError("pre, post: None, 'none', 'rms' or 'layer'; gate_act: None, 'none' or 'sigmoid'")
-    wtype = None
+    wtypes = _TYPE
     for n, w in (("pre_weight", pre_weight), ("pre_bias", pre_bias), ("post_weight", post_weight), ("post_bias", post_bias)):
         if w is not None:
-            _need(w, n, _TYPE if wtype is None else (wtype,), (hidden,), dev)
-            wtype = w.dtype
+            _need(w, n, wtypes, (hidden,), index)
+            wtypes = (w.dtype,)
     gate_rows = 0
     if gate is not None:
-        gate_rows = gate.shape[0] if isinstance(gate, torch.Tensor) and gate.dim() == 2 else -1
-        _need(gate, "gate", (y.dtype,), (gate_rows, hidden), dev)
-    return C.bf16opt_norm_gate_t(
-        rows, hidden, _TYPE[y.dtype], _TYPE[stream_t.dtype] if stream_t is not None else _TYPE[y.dtype],
-        _TYPE[wtype] if wtype is not None else 0, _NORM[pre], _NORM[post], _ACT[gate_act], 0, gate_rows, _p(gate),
-        _p(pre_weight), _p(pre_bias), _p(post_weight), _p(post_bias), residual_scale, branch_scale, eps)
+        gate_rows = _matrix(gate, "gate")[0]
+        _need(gate, "gate", (y.dtype,), (gate_rows, hidden), index)
+    return _NORM_GATE_T.pack(
+        rows, hidden, _TYPE[y.dtype], _TYPE[stream_t.dtype], _TYPE[wtypes[0]] if wtypes is not _TYPE else 0, _NORM[pre],
+        _NORM[post], _ACT[gate_act], 0, gate_rows, _p(gate), _p(pre_weight), _p(pre_bias), _p(post_weight), _p(post_bias),
+        residual_scale, branch_scale, eps), rows, index
 
 
+@_on_stream
 def norm_gate_forward(x, y, *, pre="rms", post="rms", pre_weight=None, pre_bias=None, post_weight=None, post_bias=None,
-                      gate=None, gate_act="none", residual_scale=1.0, branch_scale=1.0, eps=1e-5, out_r=None, out_h=None,
-                      stream=None):
+                      gate=None, gate_act="none", residual_scale=1.0, branch_scale=1.0, eps=1e-5, out_r=None, out_h=None):
     """r = residual_scale x + branch_scale act(gate) N_post(y) and h = N_pre(r)
     for the residual stream x and the block's output y [rows, hidden].  gate
     [gate_rows, hidden]: rows / gate_rows consecutive rows share one.  Returns
     (r, h, stats): h None if pre is None; stats [rows, 4] FP32 for the backward
     call.  out_r may be x, out_h may be y."""
-    d = _norm_gate(x, y, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate, gate_act, residual_scale,
-                   branch_scale, eps, "x")
-    if x is None:
-        raise ValueError("x: must be a [rows, hidden] CUDA tensor")
-    with _On(y, stream, x, pre_weight, pre_bias, post_weight, post_bias, gate, out_r, out_h) as on:
-        if out_r is not None:
-            _need(out_r, "out_r", (x.dtype,), x.shape, y.device)
-        if out_h is not None:
-            _need(out_h, "out_h", (y.dtype,), y.shape, y.device)
-        r = out_r if out_r is not None else torch.empty_like(x)
-        h = out_h
-        if d.pre != C.BF16OPT_NORM_NONE and h is None:
-            h = torch.empty_like(y)
-        stats = torch.empty((d.rows, 4), dtype=torch.float32, device=y.device)
-        C.check(C.bf16opt_norm_gate_forward(d, x.data_ptr(), y.data_ptr(), r.data_ptr(), _p(h), stats.data_ptr(), on.handle))
+    d, rows, index = _norm_gate(x, "x", y, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate, gate_act,
+                                residual_scale, branch_scale, eps)
+    if out_r is not None:
+        _need(out_r, "out_r", (x.dtype,), x.shape, index)
+    if out_h is not None:
+        _need(out_h, "out_h", (y.dtype,), y.shape, index)
+    r = out_r if out_r is not None else _empty_like(x)
+    h = out_h if out_h is not None or not _NORM[pre] else _empty_like(y)
+    stats = _empty((rows, 4), dtype=torch.float32, device=y.device)
+    C.check(C.bf16opt_norm_gate_forward(d, x.data_ptr(), y.data_ptr(), r.data_ptr(), _p(h), stats.data_ptr(), _raw_stream(index)))
     return r, h, stats
 
 
+@functools.lru_cache(maxsize=4096)
+def _norm_gate_workspace(rows, hidden, types, gate_rows, index):
+    """Bytes, by what they depend on: the sizes, the element types and the device."""
+    with torch.cuda.device(index):
+        rc, nbytes = C.bf16opt_norm_gate_workspace(
+            C.bf16opt_norm_gate_t(rows, hidden, *types, 0, 0, 0, 0, 0, gate_rows, 256 if gate_rows else None, None, None, None, None,
+                                  1.0, 1.0, 1.0))
+        C.check(rc)
+    return nbytes
+
+
+@_on_stream
 def norm_gate_backward(dr, dh, r, y, stats, *, pre="rms", post="rms", pre_weight=None, pre_bias=None, post_weight=None,
-                       post_bias=None, gate=None, gate_act="none", residual_scale=1.0, branch_scale=1.0, eps=1e-5,
-                       stream=None):
+                       post_bias=None, gate=None, gate_act="none", residual_scale=1.0, branch_scale=1.0, eps=1e-5):
     """Gradients of norm_gate_forward from those of r (dr, None: 0) and h (dh,
     None: 0): a dict of dx, dy, dgate, dpre_weight, dpre_bias, dpost_weight and
     dpost_bias, None for what is not there."""
     stream_t = r if r is not None else dr
-    if stream_t is None:
-        raise ValueError("r: must be a [rows, hidden] CUDA tensor")
-    d = _norm_gate(stream_t, y, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate, gate_act, residual_scale,
-                   branch_scale, eps, "r")
-    dev = y.device
+    d, rows, index = _norm_gate(stream_t, "r", y, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate, gate_act,
+                                residual_scale, branch_scale, eps)
+    hidden = y.shape[1]
     if dr is not None:
-        _need(dr, "dr", (stream_t.dtype,), y.shape, dev)
+        _need(dr, "dr", (stream_t.dtype,), (rows, hidden), index)
     if dh is not None:
-        _need(dh, "dh", (y.dtype,), y.shape, dev)
-    _need(stats, "stats", _F32, (d.rows, 4), dev)
-    with _On(y, stream, dr, dh, r, stats, pre_weight, pre_bias, post_weight, post_bias, gate) as on:
-        def like(t):
-            return torch.empty_like(t) if t is not None else None
-        dx, dy, dgate = torch.empty_like(stream_t), torch.empty_like(y), like(gate)
-        dw1, db1, dw2, db2 = like(pre_weight), like(pre_bias), like(post_weight), like(post_bias)
-        rc, nbytes = C.bf16opt_norm_gate_workspace(d)
-        C.check(rc)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        C.check(C.bf16opt_norm_gate_backward(d, _p(dr), _p(dh), _p(r), y.data_ptr(), stats.data_ptr(), dx.data_ptr(),
-                                             dy.data_ptr(), _p(dgate), _p(dw1), _p(db1), _p(dw2), _p(db2), ws.data_ptr(),
-                                             nbytes, on.handle))
+        _need(dh, "dh", (y.dtype,), (rows, hidden), index)
+    _need(stats, "stats", _F32, (rows, 4), index)
+    dx, dy = _empty_like(stream_t), _empty_like(y)
+    dgate, dw1, db1, dw2, db2 = (_empty_like(t) if t is not None else None
+                                 for t in (gate, pre_weight, pre_bias, post_weight, post_bias))
+    nbytes = _norm_gate_workspace(rows, hidden, (_TYPE[y.dtype], _TYPE[stream_t.dtype]), gate.shape[0] if gate is not None else 0, index)
+    ws = _empty(nbytes, dtype=torch.uint8, device=y.device)
+    C.check(C.bf16opt_norm_gate_backward(d, _p(dr), _p(dh), _p(r), y.data_ptr(), stats.data_ptr(), dx.data_ptr(),
+                                         dy.data_ptr(), _p(dgate), _p(dw1), _p(db1), _p(dw2), _p(db2), ws.data_ptr(),
+                                         nbytes, _raw_stream(index)))
     return dict(dx=dx, dy=dy, dgate=dgate, dpre_weight=dw1, dpre_bias=db1, dpost_weight=dw2, dpost_bias=db2)
 
 
@@ -301,57 +311,62 @@ def norm_gate(x, y, *, pre="rms", post="rms", pre_weight=None, pre_bias=None, po
 # ----------------------------------------------------------------- expert balance
 
 def _balance(logits, k, mask, groups, balance_weight, z_weight, renormalise):
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
-        raise ValueError("logits: must be a [tokens, experts] CUDA tensor")
-    tokens, experts = logits.shape
-    _need(logits, "logits", _TYPE, (tokens, experts), logits.device, rows_apart=True)
+    """(descriptor, tokens, experts, device index)."""
+    tokens, experts, index = _matrix(logits, "logits")
+    _need(logits, "logits", _TYPE, (tokens, experts), index, True)
     if mask is not None:
-        _need(mask, "mask", (torch.bool, torch.uint8), (tokens,), logits.device)
-    return C.bf16opt_balance_t(tokens, experts, k, groups, _TYPE[logits.dtype], 1 if renormalise else 0, logits.data_ptr(),
-                               _stride(logits), _p(mask), balance_weight, z_weight)
+        _need(mask, "mask", (torch.bool, torch.uint8), (tokens,), index)
+    return _BALANCE_T.pack(tokens, experts, k, groups, _TYPE[logits.dtype], 1 if renormalise else 0, logits.data_ptr(),
+                           _stride(logits), _p(mask), balance_weight, z_weight), tokens, experts, index
 
 
-def balance_forward(logits, k, *, mask=None, groups=1, balance_weight=1e-2, z_weight=0.0, renormalise=True, stream=None):
+@functools.lru_cache(maxsize=4096)
+def _balance_workspace(tokens, experts, k, groups, index):
+    with torch.cuda.device(index):
+        rc, nbytes = C.bf16opt_balance_workspace(
+            C.bf16opt_balance_t(tokens, experts, k, groups, 0, 0, None, experts, None, 0.0, 0.0))
+        C.check(rc)
+    return nbytes
+
+
+@_on_stream
+def balance_forward(logits, k, *, mask=None, groups=1, balance_weight=1e-2, z_weight=0.0, renormalise=True):
     """A router's choice: (ids [tokens, k] int32, weights [tokens, k] FP32,
     counts [groups, experts] int32, loss FP32, saved) for logits [tokens,
     experts] (bf16 or FP32); mask [tokens] bool or uint8, 0: the token counts
     for nothing; groups: runs of tokens balanced each for itself."""
-    d = _balance(logits, k, mask, groups, balance_weight, z_weight, renormalise)
-    with _On(logits, stream, mask) as on:
-        dev = logits.device
-        rc, nbytes = C.bf16opt_balance_workspace(d)
-        C.check(rc)
-        ids = torch.empty((d.tokens, k), dtype=torch.int32, device=dev)
-        weights = torch.empty((d.tokens, k), dtype=torch.float32, device=dev)
-        counts = torch.empty((groups, d.experts), dtype=torch.int32, device=dev)
-        loss = torch.empty((), dtype=torch.float32, device=dev)
-        saved = torch.empty(d.tokens + groups, dtype=torch.float32, device=dev)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        C.check(C.bf16opt_balance_forward(d, ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), loss.data_ptr(),
-                                          saved.data_ptr(), _p(ws), nbytes, on.handle))
+    d, tokens, experts, index = _balance(logits, k, mask, groups, balance_weight, z_weight, renormalise)
+    nbytes = _balance_workspace(tokens, experts, k, groups, index)
+    dev = logits.device
+    ids = _empty((tokens, k), dtype=torch.int32, device=dev)
+    weights = _empty((tokens, k), dtype=torch.float32, device=dev)
+    counts = _empty((groups, experts), dtype=torch.int32, device=dev)
+    loss = _empty((), dtype=torch.float32, device=dev)
+    saved = _empty(tokens + groups, dtype=torch.float32, device=dev)
+    ws = _empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    C.check(C.bf16opt_balance_forward(d, ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), loss.data_ptr(),
+                                      saved.data_ptr(), _p(ws), nbytes, _raw_stream(index)))
     return ids, weights, counts, loss, saved
 
 
+@_on_stream
 def balance_backward(logits, ids, counts, saved, dweights=None, dloss=None, *, mask=None, groups=1, balance_weight=1e-2,
-                     z_weight=0.0, renormalise=True, out=None, stream=None):
+                     z_weight=0.0, renormalise=True, out=None):
     """Gradient of the logits from those of the weights (None: 0) and of the
     loss (a tensor of one FP32; None: 1), with balance_forward's arguments and
     results.  out may be logits itself."""
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
-        raise ValueError("ids: must be a [tokens, k] CUDA tensor")
-    d = _balance(logits, ids.shape[1], mask, groups, balance_weight, z_weight, renormalise)
-    dev = logits.device
-    _need(ids, "ids", (torch.int32,), (d.tokens, d.k), dev)
-    _need(counts, "counts", (torch.int32,), (groups, d.experts), dev)
-    _need(saved, "saved", _F32, (d.tokens + groups,), dev)
+    k = _matrix(ids, "ids")[1]
+    d, tokens, experts, index = _balance(logits, k, mask, groups, balance_weight, z_weight, renormalise)
+    _need(ids, "ids", (torch.int32,), (tokens, k), index)
+    _need(counts, "counts", (torch.int32,), (groups, experts), index)
+    _need(saved, "saved", _F32, (tokens + groups,), index)
     if dweights is not None:
-        _need(dweights, "dweights", _F32, (d.tokens, d.k), dev)
+        _need(dweights, "dweights", _F32, (tokens, k), index)
     if dloss is not None:
-        _need(dloss, "dloss", _F32, dloss.shape if isinstance(dloss, torch.Tensor) and dloss.numel() == 1 else (1,), dev)
-    with _On(logits, stream, ids, counts, saved, dweights, dloss, out) as on:
-        out = _dlogits(logits, out)
-        C.check(C.bf16opt_balance_backward(d, ids.data_ptr(), counts.data_ptr(), saved.data_ptr(), _p(dweights), _p(dloss),
-                                           out.data_ptr(), _stride(out), on.handle))
+        _need(dloss, "dloss", _F32, dloss.shape if isinstance(dloss, _Tensor) and dloss.numel() == 1 else (1,), index)
+    out = _dlogits(logits, out, index)
+    C.check(C.bf16opt_balance_backward(d, ids.data_ptr(), counts.data_ptr(), saved.data_ptr(), _p(dweights), _p(dloss),
+                                       out.data_ptr(), _stride(out), _raw_stream(index)))
     return out
 
 

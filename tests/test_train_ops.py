@@ -22,6 +22,19 @@ def lib():
     return C.load()
 
 
+def test_packed_descriptors_have_the_structs_layout():
+    pytest.importorskip("torch")
+    from mixed_precision_optimizer_bf16_gb300 import train_ops as ops
+    for name, packed in (("distill", ops._DISTILL_T), ("norm_gate", ops._NORM_GATE_T), ("balance", ops._BALANCE_T)):
+        cls = getattr(C, f"bf16opt_{name}_t")
+        assert packed.size == ctypes.sizeof(cls)
+        values = [i + 0.5 if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(cls._fields_)]
+        d = cls(*values)
+        assert cls.from_buffer_copy(packed.pack(*values)).__class__ is cls
+        for f, v in zip(cls._fields_, values):
+            assert getattr(cls.from_buffer_copy(packed.pack(*values)), f[0]) == getattr(d, f[0]) == v, (name, f)
+
+
 def has_gpu():
     torch = pytest.importorskip("torch")
     return torch.cuda.is_available()
