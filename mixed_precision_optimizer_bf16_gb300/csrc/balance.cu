@@ -64,6 +64,34 @@ __device__ __forceinline__ float value_of(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+// A token's choice, one largest logit after another, is by far the most of the
+// forward pass's work.  For bf16 logits a key holds the logit's 16 bits in their order
+// and, below them, the expert counted backwards, so that keys are distinct and the
+// lowest expert wins a tie: a lane sorts its keys once (a network of exchanges), and a
+// choice is one reduction over the lanes' largest and one step of the winner's list.
+// FP32 logits leave no room for the expert: there a choice is a reduction and a
+// ballot, and the winner searches its run again.  Under this key come experts that are off.
+constexpr uint32_t kOff16 = 0x00800000u;
+
+// Eight keys in descending order: an odd-even merge network of 19 exchanges.
+__device__ __forceinline__ void order(uint32_t &a, uint32_t &b) {
+    const uint32_t hi = max(a, b), lo = min(a, b);
+    a = hi, b = lo;
+}
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
+    // odd-even merge sort (Batcher): p runs over the merged lengths, q over the exchange distances
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) order(k[i + j], k[i + j + q]);
+}
+
 // A lane's run of the row: experts [lane * PER, lane * PER + PER), -inf beyond.
 template <class T, int PER>
 __device__ __forceinline__ void load_run(const T *row, uint32_t experts, uint32_t lane, bool vec, float (&z)[PER]) {
@@ -140,6 +168,7 @@ __device__ __forceinline__ float cta_sum(float v, float *buf) {
 
 template <class T, int PER>
 __global__ void __launch_bounds__(kThreads) k_balance_forward(const Args a) {
+    constexpr bool kPacked = sizeof(T) == 2 && PER >= 2 && PER <= 8;   // keys of 16 bits and the expert
     extern __shared__ float sm[];
     float *sm_p = sm;                                             // [warps][experts]
     int *sm_count = reinterpret_cast<int *>(sm + kWarps * a.experts);   // [experts]
@@ -148,6 +177,7 @@ __global__ void __launch_bounds__(kThreads) k_balance_forward(const Args a) {
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = blockIdx.x;
     pdl_enter();
     const uint64_t t0 = team_row(a.tokens, a.teams, team), t1 = team_row(a.tokens, a.teams, team + 1);
+    const T *logits = reinterpret_cast<const T *>(a.logits);
     float whole = 0.f;   // one CTA: the loss of all groups
     for (uint64_t g = t0 / a.per_group; g * a.per_group < t1; ++g) {
         const uint64_t first = g * a.per_group, last = first + a.per_group;
@@ -157,65 +187,101 @@ __global__ void __launch_bounds__(kThreads) k_balance_forward(const Args a) {
         float sum[PER] = {};
         float squares = 0.f;
         int live = 0;
+        // a token's logits are asked for while the one before is worked on
+        float ahead[PER];
+        uint8_t on_ahead = 0;
+        auto fetch = [&](uint64_t t) {
+            if (t >= e) return;
+            on_ahead = a.mask ? a.mask[t] : 1;
+            load_run<T, PER>(logits + t * a.stride, a.experts, lane, a.vec, ahead);
+        };
+        fetch(b + warp);
         for (uint64_t t = b + warp; t < e; t += kWarps) {
             float z[PER];
-            const bool off = a.mask && a.mask[t] == 0;
-            float lse = -INFINITY, inv = 0.f, mx = 0.f;
-            uint32_t key[PER], best = 0, at = 0;
-            if (!off) {
-                load_run<T, PER>(reinterpret_cast<const T *>(a.logits) + t * a.stride, a.experts, lane, a.vec, z);
+            const bool on = on_ahead != 0;
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    key[i] = key_of(z[i]);
-                    if (key[i] > best) best = key[i], at = i;
-                }
-                const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-                mx = value_of(top);
-                if (top != 0u) {
-                    float s = 0.f;
+            for (int i = 0; i < PER; ++i) z[i] = ahead[i];
+            fetch(t + kWarps);
+            float lse = -INFINITY;
+            int32_t my_id = -1;     // lane c keeps choice c
+            float my_z = 0.f, total = 0.f, inv = 0.f, mx;
+            if (on) {
+                mx = z[0];
 #pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        z[i] = key[i] == 0u ? 0.f : ex2((z[i] - mx) * kLog2e);
-                        s += z[i];
-                    }
-                    s = warp_sum(s);
+                for (int i = 1; i < PER; ++i) mx = fmaxf(mx, z[i]);
+                mx = warp_max(mx);      // NaN passed over
+                const float m = mx == -INFINITY ? 0.f : mx;
+                float p[PER], s = 0.f;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) p[i] = ex2((z[i] - m) * kLog2e), s += p[i];
+                s = warp_sum(s);
+                if (s != 0.f) {         // some expert is there
                     inv = 1.f / s;
-                    lse = mx + logf(s);
+                    lse = m + logf(s);
 #pragma unroll
-                    for (int i = 0; i < PER; ++i) sum[i] = fmaf(z[i], inv, sum[i]);
+                    for (int i = 0; i < PER; ++i) sum[i] = fmaf(p[i], inv, sum[i]);
                     squares = fmaf(lse, lse, squares);
                     ++live;
+                    if constexpr (kPacked) {
+                        uint32_t key[PER];
+                        const bool odd = s != s;   // a NaN is among them: it comes after every number
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            const uint32_t bits = __float_as_uint(z[i] + 0.f);   // both zeros are one
+                            const uint32_t up = (int32_t)bits < 0 ? ~bits : bits | 0x80000000u;
+                            key[i] = (up & 0xffff0000u) | (0xffffu - (lane * PER + i));
+                            if (odd && z[i] != z[i]) key[i] = (kOff16 - 0x10000u) | (0xffffu - (lane * PER + i));
+                            if (odd && z[i] == -INFINITY) key[i] = 0u;
+                        }
+                        const uint32_t least = odd ? 0x10000u : kOff16;
+                        uint32_t mine = 0;
+                        sort_keys<PER>(key);
+                        for (uint32_t c = 0; c < a.k; ++c) {
+                            const uint32_t top = __reduce_max_sync(0xffffffffu, key[0]);
+                            if (top < least) break;
+                            if (lane == c) my_id = (int32_t)(0xffffu - (top & 0xffffu)), mine = top & 0xffff0000u;
+                            if (key[0] == top) {
+#pragma unroll
+                                for (int i = 0; i + 1 < PER; ++i) key[i] = key[i + 1];
+                                key[PER - 1] = 0u;
+                            }
+                        }
+                        // the logit back from its key
+                        my_z = mine < kOff16 ? NAN : __uint_as_float(mine & 0x80000000u ? mine ^ 0x80000000u : ~mine & 0xffff0000u);
+                    } else {
+                        uint32_t key[PER], best = 0, at = 0;
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            key[i] = key_of(z[i]);
+                            if (key[i] > best) best = key[i], at = i;
+                        }
+                        for (uint32_t c = 0; c < a.k; ++c) {
+                            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+                            if (top == 0u) break;
+                            const uint32_t from = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+                            const int32_t id = (int32_t)__shfl_sync(0xffffffffu, lane * PER + at, from);
+                            if (lane == c) my_id = id, my_z = value_of(top);
+                            if (lane == from) {
+                                best = 0;
+                                uint32_t next = 0;
+#pragma unroll
+                                for (int i = 0; i < PER; ++i) {
+                                    if (i == (int)at) key[i] = 0u;
+                                    if (key[i] > best) best = key[i], next = i;
+                                }
+                                at = next;
+                            }
+                        }
+                    }
+                    if (my_id >= 0) atomicAdd(&sm_count[my_id], 1);   // whole numbers: the order does not matter
+                    my_z = my_id >= 0 ? ex2((my_z - m) * kLog2e) * inv : 0.f;
+                    if (a.renormalise) total = warp_sum(my_z);
                 }
             }
             if (lane == 0) a.lse[t] = lse;
-            // the k largest, one by one; lane c keeps choice c
-            int32_t my_id = -1;
-            float my_p = 0.f, total = 0.f;
-            if (lse != -INFINITY) {
-                for (uint32_t c = 0; c < a.k; ++c) {
-                    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-                    if (top == 0u) break;
-                    const uint32_t from = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-                    const int32_t id = (int32_t)__shfl_sync(0xffffffffu, lane * PER + at, from);
-                    const float p = ex2((value_of(top) - mx) * kLog2e) * inv;
-                    total += p;
-                    if (lane == c) my_id = id, my_p = p;
-                    if (lane == from) {
-                        best = 0;
-                        uint32_t next = 0;
-#pragma unroll
-                        for (int i = 0; i < PER; ++i) {
-                            if (i == (int)at) key[i] = 0u;
-                            if (key[i] > best) best = key[i], next = i;
-                        }
-                        at = next;
-                    }
-                }
-                if (my_id >= 0) atomicAdd(&sm_count[my_id], 1);   // whole numbers: the order does not matter
-            }
             if (lane < a.k) {
                 a.ids[t * a.k + lane] = my_id;
-                a.weights[t * a.k + lane] = my_id < 0 ? 0.f : a.renormalise ? my_p / total : my_p;
+                a.weights[t * a.k + lane] = my_id < 0 ? 0.f : a.renormalise ? my_z / total : my_z;
             }
         }
         // the warps' sums, joined in their order
@@ -355,53 +421,68 @@ struct BackArgs {
     bool vec;
 };
 
+// What the choices add to their experts' elements goes through a row of shared
+// memory of the warp's own, all zeros between two tokens.
 template <class T, int PER>
 __global__ void __launch_bounds__(kThreads) k_balance_backward(const Args a, const BackArgs q) {
-    const uint32_t lane = threadIdx.x & 31;
+    extern __shared__ __align__(16) float sm_extra[];   // [warps][32 PER]
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float *extras = sm_extra + warp * 32 * PER;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) extras[lane + 32 * i] = 0.f;
+    __syncwarp();
     pdl_enter();
-    const uint64_t warps = (uint64_t)gridDim.x * kWarps, me = (uint64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const uint64_t warps = (uint64_t)gridDim.x * kWarps, me = (uint64_t)blockIdx.x * kWarps + warp;
+    // each warp a run of tokens, so that its group seldom changes
+    const uint64_t t0 = a.tokens / warps * me + a.tokens % warps * me / warps;
+    const uint64_t t1 = a.tokens / warps * (me + 1) + a.tokens % warps * (me + 1) / warps;
     const float dloss = q.dloss ? *q.dloss : 1.f;
-    uint64_t group = ~0ull;
-    float f[PER], scale = 0.f, share = 0.f;
-    for (uint64_t t = me; t < a.tokens; t += warps) {
-        const T *row = reinterpret_cast<const T *>(a.logits) + t * a.stride;
-        T *out = reinterpret_cast<T *>(q.dlogits) + t * q.stride;
-        const float lse = q.lse[t];
+    const T *logits = reinterpret_cast<const T *>(a.logits);
+    const bool chooses = lane < a.k && q.dweights;
+    uint64_t group = t0 < t1 ? t0 / a.per_group : 0, left = 0;   // left: tokens before the next group
+    if (t0 < t1) left = (group + 1) * a.per_group - t0;
+    bool fresh = true;
+    float f[PER], ab = 0.f, two_z = 0.f;
+    // A token's numbers are asked for one token ahead, its ids two, its chosen logits one.
+    float lse_next = 0.f, up_next = 0.f, zid_next = 0.f, ahead[PER];
+    int32_t id_next = -1, id_after = -1;
+    auto id_of = [&](uint64_t t) { return t < t1 && chooses ? q.ids[t * a.k + lane] : -1; };
+    auto fetch = [&](uint64_t t) {
+        id_next = id_after, id_after = id_of(t + 1);
+        if (t >= t1) return;
+        lse_next = q.lse[t];
+        load_run<T, PER>(logits + t * a.stride, a.experts, lane, a.vec, ahead);
+        const bool there = id_next >= 0 && id_next < (int32_t)a.experts;
+        if (!there) id_next = -1;
+        zid_next = there ? to_f32(logits[t * a.stride + id_next]) : 0.f;
+        up_next = there ? q.dweights[t * a.k + lane] : 0.f;
+    };
+    id_after = id_of(t0);
+    fetch(t0);
+    for (uint64_t t = t0; t < t1; ++t) {
+        const float lse = lse_next, up = up_next, zid = zid_next;
+        const int32_t id = id_next;
         float z[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) z[i] = ahead[i];
+        fetch(t + 1);
+        if (fresh) {
+            fresh = false;
+            const float n = q.live[group], scale = dloss / ((float)a.groups * n), share = (float)a.experts / ((float)a.k * n);
+            ab = a.balance_weight * scale, two_z = 2.f * a.z_weight * scale;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const uint32_t e = lane * PER + i;
+                f[i] = e < a.experts ? ab * share * (float)q.counts[group * a.experts + e] : 0.f;
+            }
+        }
+        if (--left == 0) ++group, left = a.per_group, fresh = true;
+        T *out = reinterpret_cast<T *>(q.dlogits) + t * q.stride;
         if (lse == -INFINITY) {   // masked
 #pragma unroll
             for (int i = 0; i < PER; ++i) z[i] = 0.f;
             store_run<T, PER>(out, a.experts, lane, q.vec, z);
             continue;
-        }
-        const uint64_t g = t / a.per_group;
-        if (g != group) {
-            group = g;
-            const float n = q.live[g];
-            scale = dloss / ((float)a.groups * n);
-            share = (float)a.experts / ((float)a.k * n);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const uint32_t e = lane * PER + i;
-                f[i] = e < a.experts ? share * (float)q.counts[g * a.experts + e] : 0.f;
-            }
-        }
-        load_run<T, PER>(row, a.experts, lane, a.vec, z);
-        // the choices: lane c has choice c
-        const bool mine = lane < a.k;
-        const int32_t id = mine ? q.ids[t * a.k + lane] : -1;
-        const bool there = id >= 0 && id < (int32_t)a.experts;
-        const float up = there && q.dweights ? q.dweights[t * a.k + lane] : 0.f;
-        const float p = there ? ex2((to_f32(row[id]) - lse) * kLog2e) : 0.f;
-        float extra, dot;
-        if (a.renormalise) {
-            const float w = p / warp_sum(p);
-            dot = warp_sum(there ? w * up : 0.f);
-            extra = w * (up - dot);
-            dot = 0.f;
-        } else {
-            extra = p * up;
-            dot = warp_sum(extra);
         }
         float s = 0.f;
 #pragma unroll
@@ -409,19 +490,29 @@ __global__ void __launch_bounds__(kThreads) k_balance_backward(const Args a, con
             z[i] = ex2((z[i] - lse) * kLog2e);
             s = fmaf(f[i], z[i], s);
         }
-        s = warp_sum(s);
-        const float ab = a.balance_weight * scale;
-        const float rest = 2.f * a.z_weight * scale * lse - ab * s - dot;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) z[i] *= fmaf(ab, f[i], rest);
-        __syncwarp();
-        store_run<T, PER>(out, a.experts, lane, q.vec, z);
-        __syncwarp();   // the row is stored: the choices' elements go over it
-        if (there && q.dweights) {
-            const float fe = share * (float)q.counts[g * a.experts + id];
-            from_f32(out[id], fmaf(p, fmaf(ab, fe, rest), extra));
+        float extra = 0.f, dot = 0.f;
+        if (q.dweights) {
+            float p = id >= 0 ? ex2((zid - lse) * kLog2e) : 0.f;
+            if (a.renormalise) p = p / warp_sum(p);
+            extra = p * up;
+            dot = warp_sum(extra);
+            if (a.renormalise) extra = fmaf(-p, dot, extra), dot = 0.f;
+            if (id >= 0) extras[id] = extra;
         }
+        const float rest = two_z * lse - warp_sum(s) - dot;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) z[i] *= f[i] + rest;
+        if (q.dweights) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < PER; ++i) z[i] += extras[lane * PER + i];
+            __syncwarp();
+            if (id >= 0) extras[id] = 0.f;
+            __syncwarp();
+        }
+        store_run<T, PER>(out, a.experts, lane, q.vec, z);
     }
+    pdl_leave();
 }
 
 // ---------------------------------------------------------------------- host
@@ -445,9 +536,9 @@ int check(const bf16opt_balance_t *d) {
     return BF16OPT_OK;
 }
 
-// CTAs of the forward pass: two per SM, each with at least 64 tokens.
+// CTAs of the forward pass: four per SM, each with at least 64 tokens.
 uint32_t teams_of(const bf16opt_balance_t *d, int sms) {
-    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>((uint64_t)sms * 2, d->tokens / 64));
+    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>((uint64_t)sms * 4, d->tokens / 64));
 }
 uint64_t workspace_floats(const bf16opt_balance_t *d, uint32_t teams) {
     return teams == 1 ? 0 : (d->groups + 3) / 4 * 4 + 2 * (uint64_t)teams * slot_floats(d->experts);
@@ -594,7 +685,7 @@ int backward(const bf16opt_balance_t *d, const int32_t *ids, const int32_t *coun
     const unsigned grid = (unsigned)std::min<uint64_t>((d->tokens + kWarps - 1) / kWarps, (uint64_t)sms * 8);
     return by_per(per, [&](auto p) {
         constexpr int PER = decltype(p)::value;
-        Launch l{grid, (unsigned)kThreads, 0, (cudaStream_t)stream, 0, true};
+        Launch l{grid, (unsigned)kThreads, (size_t)kThreads * PER * 4, (cudaStream_t)stream, 0, true};
         return done(d->logits_type == BF16OPT_TYPE_BF16 ? launch(l, k_balance_backward<__nv_bfloat16, PER>, a, q)
                                                         : launch(l, k_balance_backward<float, PER>, a, q));
     });
