@@ -92,44 +92,58 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
                     if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) order(k[i + j], k[i + j + q]);
 }
 
-// A lane's run of the row: experts [lane * PER, lane * PER + PER), -inf beyond.
+// A lane's run of a row as it lies in memory: experts [lane * PER, lane * PER + PER), -inf beyond.
 template <class T, int PER>
-__device__ __forceinline__ void load_run(const T *row, uint32_t experts, uint32_t lane, bool vec, float (&z)[PER]) {
+struct RunOf {
+    static constexpr int W = PER * (int)sizeof(T) < 4 ? 1 : PER * (int)sizeof(T) / 4;
+    uint32_t w[W];
+};
+template <class T, int PER>
+__device__ __forceinline__ RunOf<T, PER> load_run(const T *row, uint32_t experts, uint32_t lane, bool vec) {
+    RunOf<T, PER> r;
+    constexpr int W = RunOf<T, PER>::W;
     const uint32_t e0 = lane * PER;
-    constexpr int BYTES = PER * (int)sizeof(T);
-    if (vec && BYTES >= 4) {
+    if (vec && PER * sizeof(T) >= 4) {
         if (e0 < experts) {
-            if constexpr (BYTES >= 16) {
-                constexpr int N = Vec<T>::N;
+            if constexpr (W >= 4) {
 #pragma unroll
-                for (int v = 0; v < PER / N; ++v) {
-                    float f[N];
-                    Vec<T>::unpack(__ldcs(reinterpret_cast<const uint4 *>(row + e0) + v), f);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) z[v * N + i] = f[i];
+                for (int i = 0; i < W / 4; ++i) {
+                    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(row + e0) + i);
+                    r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
                 }
-            } else if constexpr (BYTES >= 4) {
-                uint32_t w[BYTES / 4];
-                if constexpr (BYTES == 8) {
-                    const uint2 q = __ldcs(reinterpret_cast<const uint2 *>(row + e0));
-                    w[0] = q.x, w[1] = q.y;
-                } else {
-                    w[0] = __ldcs(reinterpret_cast<const uint32_t *>(row + e0));
-                }
-#pragma unroll
-                for (int i = 0; i < BYTES / 4; ++i) {
-                    if constexpr (sizeof(T) == 2) z[2 * i] = bf16_lo(w[i]), z[2 * i + 1] = bf16_hi(w[i]);
-                    else z[i] = __uint_as_float(w[i]);
-                }
+            } else if constexpr (W == 2) {
+                const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(row + e0));
+                r.w[0] = v.x, r.w[1] = v.y;
+            } else if constexpr (PER * sizeof(T) == 4) {
+                r.w[0] = __ldcs(reinterpret_cast<const uint32_t *>(row + e0));
             }
-            return;
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) r.w[i] = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
         }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) z[i] = -INFINITY;
-        return;
+        return r;
     }
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) z[i] = e0 + i < experts ? to_f32(row[e0 + i]) : -INFINITY;
+        for (int i = 0; i < PER; ++i) r.w[i] = e0 + i < experts ? __float_as_uint(to_f32(row[e0 + i])) : 0xff800000u;
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            uint32_t lo = 0xff80u, hi = 0xff80u;
+            if (e0 + 2 * i < experts) lo = __bfloat16_as_ushort(row[e0 + 2 * i]);
+            if (PER > 1 && e0 + 2 * i + 1 < experts) hi = __bfloat16_as_ushort(row[e0 + 2 * i + 1]);
+            r.w[i] = lo | hi << 16;
+        }
+    }
+    return r;
+}
+template <class T, int PER>
+__device__ __forceinline__ void unpack_run(const RunOf<T, PER> &r, float (&z)[PER]) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if constexpr (sizeof(T) == 4) z[i] = __uint_as_float(r.w[i]);
+        else z[i] = i & 1 ? bf16_hi(r.w[i / 2]) : bf16_lo(r.w[i / 2]);
+    }
 }
 template <class T, int PER>
 __device__ __forceinline__ void store_run(T *row, uint32_t experts, uint32_t lane, bool vec, const float (&g)[PER]) {
@@ -155,6 +169,11 @@ __device__ __forceinline__ void store_run(T *row, uint32_t experts, uint32_t lan
         if (e0 + i < experts) from_f32(row[e0 + i], g[i]);
 }
 
+__device__ __forceinline__ float reciprocal(float x) {   // to one unit in the last place
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // sum over the CTA, the same bits in every thread
 __device__ __forceinline__ float cta_sum(float v, float *buf) {
     v = warp_sum(v);
@@ -187,67 +206,96 @@ __global__ void __launch_bounds__(kThreads) k_balance_forward(const Args a) {
         float sum[PER] = {};
         float squares = 0.f;
         int live = 0;
-        // a token's logits are asked for while the one before is worked on
-        float ahead[PER];
-        uint8_t on_ahead = 0;
+        // a token's logits are asked for while the two before are worked on
+        RunOf<T, PER> ahead, after;
+        uint8_t on_ahead = 0, on_after = 0;
         auto fetch = [&](uint64_t t) {
+            ahead = after, on_ahead = on_after;
             if (t >= e) return;
-            on_ahead = a.mask ? a.mask[t] : 1;
-            load_run<T, PER>(logits + t * a.stride, a.experts, lane, a.vec, ahead);
+            on_after = a.mask ? a.mask[t] : 1;
+            after = load_run<T, PER>(logits + t * a.stride, a.experts, lane, a.vec);
         };
         fetch(b + warp);
+        fetch(b + warp + kWarps);
         for (uint64_t t = b + warp; t < e; t += kWarps) {
-            float z[PER];
+            const RunOf<T, PER> run = ahead;
             const bool on = on_ahead != 0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) z[i] = ahead[i];
-            fetch(t + kWarps);
+            fetch(t + 2 * kWarps);
             float lse = -INFINITY;
             int32_t my_id = -1;     // lane c keeps choice c
-            float my_z = 0.f, total = 0.f, inv = 0.f, mx;
+            float my_p = 0.f;
             if (on) {
-                mx = z[0];
+                float z[PER];
+                unpack_run<T, PER>(run, z);
+                float mx = z[0];
 #pragma unroll
                 for (int i = 1; i < PER; ++i) mx = fmaxf(mx, z[i]);
                 mx = warp_max(mx);      // NaN passed over
                 const float m = mx == -INFINITY ? 0.f : mx;
-                float p[PER], s = 0.f;
+                float p[PER], s;
+                if constexpr (PER == 1) {
+                    s = p[0] = ex2((z[0] - m) * kLog2e);
+                } else {
+                    float2 s2 = both(0.f);
 #pragma unroll
-                for (int i = 0; i < PER; ++i) p[i] = ex2((z[i] - m) * kLog2e), s += p[i];
+                    for (int i = 0; i < PER; i += 2) {
+                        const float2 d = mul2(add2(make_float2(z[i], z[i + 1]), both(-m)), both(kLog2e));
+                        p[i] = ex2(d.x), p[i + 1] = ex2(d.y);
+                        s2 = add2(s2, make_float2(p[i], p[i + 1]));
+                    }
+                    s = s2.x + s2.y;
+                }
                 s = warp_sum(s);
                 if (s != 0.f) {         // some expert is there
-                    inv = 1.f / s;
+                    const float inv = reciprocal(s);
                     lse = m + logf(s);
 #pragma unroll
                     for (int i = 0; i < PER; ++i) sum[i] = fmaf(p[i], inv, sum[i]);
                     squares = fmaf(lse, lse, squares);
                     ++live;
+                    const bool odd = s != s;   // a NaN is among them: it comes after every number
                     if constexpr (kPacked) {
-                        uint32_t key[PER];
-                        const bool odd = s != s;   // a NaN is among them: it comes after every number
+                        uint32_t key[PER], mine = 0, least = kOff16;
+                        const uint32_t back = 0xffffu - lane * PER;
 #pragma unroll
-                        for (int i = 0; i < PER; ++i) {
-                            const uint32_t bits = __float_as_uint(z[i] + 0.f);   // both zeros are one
-                            const uint32_t up = (int32_t)bits < 0 ? ~bits : bits | 0x80000000u;
-                            key[i] = (up & 0xffff0000u) | (0xffffu - (lane * PER + i));
-                            if (odd && z[i] != z[i]) key[i] = (kOff16 - 0x10000u) | (0xffffu - (lane * PER + i));
-                            if (odd && z[i] == -INFINITY) key[i] = 0u;
+                        for (int i = 0; i < PER / 2; ++i) {   // two logits of a word at once
+                            uint32_t w;
+                            asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(w) : "r"(run.w[i]), "r"(0u));   // both zeros are one
+                            w ^= 0x80008000u | (w >> 15 & 0x00010001u) * 0x7fffu;   // ascending as unsigned numbers
+                            key[2 * i] = w << 16 | (back - 2 * i), key[2 * i + 1] = (w & 0xffff0000u) | (back - 2 * i - 1);
                         }
-                        const uint32_t least = odd ? 0x10000u : kOff16;
-                        uint32_t mine = 0;
-                        sort_keys<PER>(key);
-                        for (uint32_t c = 0; c < a.k; ++c) {
-                            const uint32_t top = __reduce_max_sync(0xffffffffu, key[0]);
-                            if (top < least) break;
-                            if (lane == c) my_id = (int32_t)(0xffffu - (top & 0xffffu)), mine = top & 0xffff0000u;
-                            if (key[0] == top) {
+                        if (odd) {
+                            least = 0x10000u;
 #pragma unroll
-                                for (int i = 0; i + 1 < PER; ++i) key[i] = key[i + 1];
-                                key[PER - 1] = 0u;
+                            for (int i = 0; i < PER; ++i) {
+                                if (z[i] != z[i]) key[i] = (kOff16 - 0x10000u) | (back - i);
+                                if (z[i] == -INFINITY) key[i] = 0u;
                             }
                         }
-                        // the logit back from its key
-                        my_z = mine < kOff16 ? NAN : __uint_as_float(mine & 0x80000000u ? mine ^ 0x80000000u : ~mine & 0xffff0000u);
+                        sort_keys<PER>(key);
+                        auto choose = [&](uint32_t c, int depth) {   // only `depth` keys of a lane can still come
+                            const uint32_t top = __reduce_max_sync(0xffffffffu, key[0]);
+                            if (lane == c) mine = top;
+                            if (key[0] == top) {
+#pragma unroll
+                                for (int i = 0; i + 1 < PER; ++i)
+                                    if (i < depth) key[i] = key[i + 1];
+                                if (depth >= PER) key[PER - 1] = 0u;
+                            }
+                        };
+                        if (a.k <= 8) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                if (c < (int)a.k) choose(c, 8 - c);
+                        } else {
+                            for (uint32_t c = 0; c < a.k; ++c) choose(c, PER);
+                        }
+                        if (mine >= least) {
+                            my_id = (int32_t)(0xffffu - (mine & 0xffffu));
+                            const uint32_t up = mine & 0xffff0000u;   // the logit back from its key
+                            const float my_z = up < kOff16 ? NAN : __uint_as_float(up & 0x80000000u ? up ^ 0x80000000u : ~up & 0xffff0000u);
+                            my_p = ex2((my_z - m) * kLog2e) * inv;
+                        }
                     } else {
                         uint32_t key[PER], best = 0, at = 0;
 #pragma unroll
@@ -260,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) k_balance_forward(const Args a) {
                             if (top == 0u) break;
                             const uint32_t from = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
                             const int32_t id = (int32_t)__shfl_sync(0xffffffffu, lane * PER + at, from);
-                            if (lane == c) my_id = id, my_z = value_of(top);
+                            if (lane == c) my_id = id, my_p = ex2((value_of(top) - m) * kLog2e) * inv;
                             if (lane == from) {
                                 best = 0;
                                 uint32_t next = 0;
@@ -274,14 +322,13 @@ __global__ void __launch_bounds__(kThreads) k_balance_forward(const Args a) {
                         }
                     }
                     if (my_id >= 0) atomicAdd(&sm_count[my_id], 1);   // whole numbers: the order does not matter
-                    my_z = my_id >= 0 ? ex2((my_z - m) * kLog2e) * inv : 0.f;
-                    if (a.renormalise) total = warp_sum(my_z);
+                    if (a.renormalise) my_p *= reciprocal(warp_sum(my_p));
                 }
             }
             if (lane == 0) a.lse[t] = lse;
             if (lane < a.k) {
                 a.ids[t * a.k + lane] = my_id;
-                a.weights[t * a.k + lane] = my_id < 0 ? 0.f : a.renormalise ? my_z / total : my_z;
+                a.weights[t * a.k + lane] = my_id < 0 ? 0.f : my_p;
             }
         }
         // the warps' sums, joined in their order
@@ -325,48 +372,64 @@ __global__ void __launch_bounds__(kThreads) k_balance_forward(const Args a) {
     if (a.teams == 1 && threadIdx.x == 0) *a.loss = whole / (float)a.groups;
 }
 
-// One cluster per group: joins the partial sums of a group that several CTAs
-// worked on.  A CTA takes a share of the experts; the loss's terms meet in rank 0.
-__global__ void __launch_bounds__(kThreads) k_balance_join(const Args a) {
-    __shared__ float sm_p[kWarps][32];
-    __shared__ int sm_c[kWarps][32];
-    __shared__ float sm_buf[kWarps], sm_rank[8];
+// Joins the partial sums of the groups that several CTAs worked on.  WHOLE: one
+// cluster for everything, the loss too: a CTA takes a share of the experts
+// of one group, or whole groups; the terms meet in rank 0.  Else a CTA per group, and
+// k_balance_sum after it.
+constexpr int kJoinWarps = 32;
+template <bool WHOLE>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_balance_join(const Args a) {
+    __shared__ float sm_p[kJoinWarps][32];
+    __shared__ int sm_c[kJoinWarps][32];
+    __shared__ float sm_buf[kJoinWarps], sm_rank[8];
+    __shared__ int sm_n[kJoinWarps];
     cg::cluster_group cluster = cg::this_cluster();
-    const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    const uint32_t ranks = WHOLE ? cluster.num_blocks() : 1, rank = WHOLE ? cluster.block_rank() : 0;
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto cta_total = [&](float v) {
+        v = warp_sum(v);
+        __syncthreads();
+        if (lane == 0) sm_buf[warp] = v;
+        __syncthreads();
+        return warp_sum(sm_buf[lane]);   // kJoinWarps is the warp's size
+    };
     pdl_enter();
-    if (ranks > 1) cluster.sync();
+    if (WHOLE && ranks > 1) cluster.sync();
     const size_t sf = slot_floats(a.experts);
-    for (uint64_t g = blockIdx.x / ranks; g < a.groups; g += gridDim.x / ranks) {
+    const bool split = WHOLE && a.groups == 1;   // the one group's experts over the CTAs
+    float whole = 0.f;
+    const uint64_t g0 = split ? 0 : WHOLE ? rank : blockIdx.x, gs = split ? 1 : WHOLE ? ranks : gridDim.x;
+    for (uint64_t g = g0; g < a.groups; g += gs) {
         const uint64_t first = g * a.per_group, last = first + a.per_group - 1;
         const uint32_t p0 = team_of(a.tokens, a.teams, first), p1 = team_of(a.tokens, a.teams, last);
-        if (p0 == p1) continue;
+        if (p0 == p1) {
+            if (WHOLE) whole += a.group_loss[g];
+            continue;
+        }
         const uint32_t parts = p1 - p0 + 1;
         const uint32_t second = first > team_row(a.tokens, a.teams, p0) ? 1 : 0;
         auto slot = [&](uint32_t i) { return a.slots + (2 * (size_t)(p0 + i) + (i == 0 ? second : 0)) * sf; };
         float sq = 0.f;
         int n = 0;
-        for (uint32_t i = threadIdx.x; i < parts; i += kThreads) {
+        for (uint32_t i = threadIdx.x; i < parts; i += 32 * kJoinWarps) {
             const float *s = slot(i);
             sq += s[2 * a.experts];
             n += __float_as_int(s[2 * a.experts + 1]);
         }
-        sq = cta_sum(sq, sm_buf);
-        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-        __shared__ int sm_n[kWarps];
+        sq = cta_total(sq);
+        n = __reduce_add_sync(0xffffffffu, n);
         if (lane == 0) sm_n[warp] = n;
         __syncthreads();
-        n = 0;
-        for (int i = 0; i < kWarps; ++i) n += sm_n[i];
+        n = __reduce_add_sync(0xffffffffu, sm_n[lane]);
         // experts by 32, the parts by runs over the warps
         float fp = 0.f;
-        for (uint32_t c = rank * 32; c < a.experts; c += ranks * 32) {
+        for (uint32_t c = split ? rank * 32 : 0; c < a.experts; c += (split ? ranks : 1) * 32) {
             const uint32_t e = c + lane;
             float p = 0.f;
             int cnt = 0;
-            const uint32_t i0 = parts * warp / kWarps, i1 = parts * (warp + 1) / kWarps;
+            const uint32_t i0 = parts * warp / kJoinWarps, i1 = parts * (warp + 1) / kJoinWarps;
             if (e < a.experts)
-#pragma unroll 4
+#pragma unroll 8
                 for (uint32_t i = i0; i < i1; ++i) {
                     const float *s = slot(i);
                     p += s[e];
@@ -375,31 +438,33 @@ __global__ void __launch_bounds__(kThreads) k_balance_join(const Args a) {
             sm_p[warp][lane] = p, sm_c[warp][lane] = cnt;
             __syncthreads();
             if (warp == 0 && e < a.experts) {
-                for (int w = 1; w < kWarps; ++w) p += sm_p[w][lane], cnt += sm_c[w][lane];
+                for (int w = 1; w < kJoinWarps; ++w) p += sm_p[w][lane], cnt += sm_c[w][lane];
                 a.counts[g * a.experts + e] = cnt;
                 fp = fmaf((float)cnt, p, fp);
             }
             __syncthreads();
         }
-        fp = cta_sum(fp, sm_buf);
-        if (ranks > 1) {
-            if (threadIdx.x == 0) *cluster.map_shared_rank(&sm_rank[rank], 0) = fp;
-            cluster.sync();
-            fp = 0.f;
-            if (rank == 0)
-                for (uint32_t i = 0; i < ranks; ++i) fp += sm_rank[i];
-            cluster.sync();
-        }
-        if (rank == 0 && threadIdx.x == 0) {
-            const float nf = (float)n;
-            const float l = n == 0 ? 0.f
-                                   : a.balance_weight * (fp / nf) * ((float)a.experts / ((float)a.k * nf)) + a.z_weight * (sq / nf);
+        fp = cta_total(fp);
+        const float nf = (float)n, share = (float)a.experts / ((float)a.k * nf);
+        float l = n == 0 ? 0.f : a.balance_weight * (fp / nf) * share;
+        if (!split || rank == 0) l += n == 0 ? 0.f : a.z_weight * (sq / nf);
+        if ((!split || rank == 0) && threadIdx.x == 0) {
             a.live[g] = nf;
-            if (a.groups == 1) *a.loss = l;
-            else a.group_loss[g] = l;
+            if (!WHOLE) a.group_loss[g] = l;
         }
-        __syncthreads();
+        whole += l;
     }
+    if (WHOLE) {
+        if (ranks > 1) {
+            if (threadIdx.x == 0) *cluster.map_shared_rank(&sm_rank[rank], 0) = whole;
+            cluster.sync();
+            whole = 0.f;
+            if (rank == 0)
+                for (uint32_t i = 0; i < ranks; ++i) whole += sm_rank[i];
+        }
+        if (rank == 0 && threadIdx.x == 0) *a.loss = whole / (float)a.groups;
+    }
+    pdl_leave();
 }
 
 // The groups' losses, summed in order by one CTA.
@@ -424,7 +489,7 @@ struct BackArgs {
 // What the choices add to their experts' elements goes through a row of shared
 // memory of the warp's own, all zeros between two tokens.
 template <class T, int PER>
-__global__ void __launch_bounds__(kThreads) k_balance_backward(const Args a, const BackArgs q) {
+__global__ void __launch_bounds__(kThreads, PER <= 8 ? 4 : 1) k_balance_backward(const Args a, const BackArgs q) {
     extern __shared__ __align__(16) float sm_extra[];   // [warps][32 PER]
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float *extras = sm_extra + warp * 32 * PER;
@@ -443,29 +508,31 @@ __global__ void __launch_bounds__(kThreads) k_balance_backward(const Args a, con
     if (t0 < t1) left = (group + 1) * a.per_group - t0;
     bool fresh = true;
     float f[PER], ab = 0.f, two_z = 0.f;
-    // A token's numbers are asked for one token ahead, its ids two, its chosen logits one.
-    float lse_next = 0.f, up_next = 0.f, zid_next = 0.f, ahead[PER];
-    int32_t id_next = -1, id_after = -1;
+    // A token's numbers are asked for two tokens ahead, its ids three, its chosen logits two.
+    float lse_next = 0.f, up_next = 0.f, zid_next = 0.f, lse_2 = 0.f, up_2 = 0.f, zid_2 = 0.f;
+    RunOf<T, PER> ahead, run_2;
+    int32_t id_next = -1, id_2 = -1, id_3 = -1;
     auto id_of = [&](uint64_t t) { return t < t1 && chooses ? q.ids[t * a.k + lane] : -1; };
     auto fetch = [&](uint64_t t) {
-        id_next = id_after, id_after = id_of(t + 1);
+        lse_next = lse_2, up_next = up_2, zid_next = zid_2, ahead = run_2, id_next = id_2;
+        id_2 = id_3, id_3 = id_of(t + 1);
         if (t >= t1) return;
-        lse_next = q.lse[t];
-        load_run<T, PER>(logits + t * a.stride, a.experts, lane, a.vec, ahead);
-        const bool there = id_next >= 0 && id_next < (int32_t)a.experts;
-        if (!there) id_next = -1;
-        zid_next = there ? to_f32(logits[t * a.stride + id_next]) : 0.f;
-        up_next = there ? q.dweights[t * a.k + lane] : 0.f;
+        lse_2 = q.lse[t];
+        run_2 = load_run<T, PER>(logits + t * a.stride, a.experts, lane, a.vec);
+        const bool there = id_2 >= 0 && id_2 < (int32_t)a.experts;
+        if (!there) id_2 = -1;
+        zid_2 = there ? to_f32(logits[t * a.stride + id_2]) : 0.f;
+        up_2 = there ? q.dweights[t * a.k + lane] : 0.f;
     };
-    id_after = id_of(t0);
+    id_3 = id_of(t0);
     fetch(t0);
+    fetch(t0 + 1);
     for (uint64_t t = t0; t < t1; ++t) {
         const float lse = lse_next, up = up_next, zid = zid_next;
         const int32_t id = id_next;
         float z[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) z[i] = ahead[i];
-        fetch(t + 1);
+        unpack_run<T, PER>(ahead, z);
+        fetch(t + 2);
         if (fresh) {
             fresh = false;
             const float n = q.live[group], scale = dloss / ((float)a.groups * n), share = (float)a.experts / ((float)a.k * n);
@@ -493,7 +560,7 @@ __global__ void __launch_bounds__(kThreads) k_balance_backward(const Args a, con
         float extra = 0.f, dot = 0.f;
         if (q.dweights) {
             float p = id >= 0 ? ex2((zid - lse) * kLog2e) : 0.f;
-            if (a.renormalise) p = p / warp_sum(p);
+            if (a.renormalise) p *= reciprocal(warp_sum(p));
             extra = p * up;
             dot = warp_sum(extra);
             if (a.renormalise) extra = fmaf(-p, dot, extra), dot = 0.f;
@@ -645,10 +712,14 @@ int forward(const bf16opt_balance_t *d, int32_t *ids, float *weights, int32_t *c
                                                         : launch(l, k_balance_forward<float, PER>, a));
     });
     if (r != BF16OPT_OK || teams == 1) return r;
-    const unsigned cluster = d->groups == 1 && (uint64_t)teams * d->experts >= 8192 ? 8 : 1;
-    Launch l{(unsigned)std::min<uint64_t>(d->groups, 1024) * cluster, (unsigned)kThreads, 0, st, cluster, true};
-    r = done(launch(l, k_balance_join, a));
-    if (r != BF16OPT_OK || d->groups == 1) return r;
+    if (d->groups <= 64) {   // few groups: one cluster joins them and adds up their losses
+        const unsigned cluster = (uint64_t)teams * d->experts >= 8192 || d->groups > 1 ? 8 : 1;
+        Launch l{cluster, 32 * kJoinWarps, 0, st, cluster, true};
+        return done(launch(l, k_balance_join<true>, a));
+    }
+    Launch l{(unsigned)std::min<uint64_t>(d->groups, 1024), 32 * kJoinWarps, 0, st, 0, true};
+    r = done(launch(l, k_balance_join<false>, a));
+    if (r != BF16OPT_OK) return r;
     Launch l2{1, (unsigned)kThreads, 0, st, 0, true};
     return done(launch(l2, k_balance_sum, (const float *)a.group_loss, a.groups, loss));
 }
