@@ -19,6 +19,9 @@ namespace cg = cooperative_groups;
 namespace bf16ops {
 namespace {
 
+// CTAs of an SM in the backward pass, up to 256 experts: 85 registers a thread (at 64 it spills:
+// 262144 x 256 took 266 us both ways, 220 us so).
+constexpr int kBackResident = 3;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
@@ -186,7 +189,7 @@ __device__ __forceinline__ float cta_sum(float v, float *buf) {
 }
 
 template <class T, int PER>
-__global__ void __launch_bounds__(kThreads) k_balance_forward(const Args a) {
+__global__ void __launch_bounds__(kThreads, PER <= 8 ? 4 : 1) k_balance_forward(const Args a) {
     constexpr bool kPacked = sizeof(T) == 2 && PER >= 2 && PER <= 8;   // keys of 16 bits and the expert
     extern __shared__ float sm[];
     float *sm_p = sm;                                             // [warps][experts]
@@ -209,18 +212,27 @@ __global__ void __launch_bounds__(kThreads) k_balance_forward(const Args a) {
         // a token's logits are asked for while the two before are worked on
         RunOf<T, PER> ahead, after;
         uint8_t on_ahead = 0, on_after = 0;
-        auto fetch = [&](uint64_t t) {
+        uint64_t t = b + warp;
+        uint32_t todo = t < e ? (uint32_t)((e - t + kWarps - 1) / kWarps) : 0u, to_fetch = todo;   // tokens of this warp
+        const T *row = logits + t * a.stride;
+        const uint8_t *mask = a.mask ? a.mask + t : nullptr;
+        auto fetch = [&]() {
             ahead = after, on_ahead = on_after;
-            if (t >= e) return;
-            on_after = a.mask ? a.mask[t] : 1;
-            after = load_run<T, PER>(logits + t * a.stride, a.experts, lane, a.vec);
+            if (to_fetch == 0) return;
+            --to_fetch;
+            on_after = mask ? *mask : 1;
+            after = load_run<T, PER>(row, a.experts, lane, a.vec);
+            row += kWarps * a.stride;
+            if (mask) mask += kWarps;
         };
-        fetch(b + warp);
-        fetch(b + warp + kWarps);
-        for (uint64_t t = b + warp; t < e; t += kWarps) {
+        fetch();
+        fetch();
+        float *lse_to = a.lse + t, *weight_to = a.weights + t * a.k + lane;
+        int32_t *id_to = a.ids + t * a.k + lane;
+        for (; todo != 0; --todo, lse_to += kWarps, weight_to += kWarps * a.k, id_to += kWarps * a.k) {
             const RunOf<T, PER> run = ahead;
             const bool on = on_ahead != 0;
-            fetch(t + 2 * kWarps);
+            fetch();
             float lse = -INFINITY;
             int32_t my_id = -1;     // lane c keeps choice c
             float my_p = 0.f;
@@ -325,11 +337,8 @@ __global__ void __launch_bounds__(kThreads) k_balance_forward(const Args a) {
                     if (a.renormalise) my_p *= reciprocal(warp_sum(my_p));
                 }
             }
-            if (lane == 0) a.lse[t] = lse;
-            if (lane < a.k) {
-                a.ids[t * a.k + lane] = my_id;
-                a.weights[t * a.k + lane] = my_id < 0 ? 0.f : my_p;
-            }
+            if (lane == 0) *lse_to = lse;
+            if (lane < a.k) *id_to = my_id, *weight_to = my_id < 0 ? 0.f : my_p;
         }
         // the warps' sums, joined in their order
 #pragma unroll
@@ -489,7 +498,7 @@ struct BackArgs {
 // What the choices add to their experts' elements goes through a row of shared
 // memory of the warp's own, all zeros between two tokens.
 template <class T, int PER>
-__global__ void __launch_bounds__(kThreads, PER <= 8 ? 4 : 1) k_balance_backward(const Args a, const BackArgs q) {
+__global__ void __launch_bounds__(kThreads, PER <= 8 ? kBackResident : 1) k_balance_backward(const Args a, const BackArgs q) {
     extern __shared__ __align__(16) float sm_extra[];   // [warps][32 PER]
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float *extras = sm_extra + warp * 32 * PER;
@@ -512,27 +521,41 @@ __global__ void __launch_bounds__(kThreads, PER <= 8 ? 4 : 1) k_balance_backward
     float lse_next = 0.f, up_next = 0.f, zid_next = 0.f, lse_2 = 0.f, up_2 = 0.f, zid_2 = 0.f;
     RunOf<T, PER> ahead, run_2;
     int32_t id_next = -1, id_2 = -1, id_3 = -1;
-    auto id_of = [&](uint64_t t) { return t < t1 && chooses ? q.ids[t * a.k + lane] : -1; };
-    auto fetch = [&](uint64_t t) {
-        lse_next = lse_2, up_next = up_2, zid_next = zid_2, ahead = run_2, id_next = id_2;
-        id_2 = id_3, id_3 = id_of(t + 1);
-        if (t >= t1) return;
-        lse_2 = q.lse[t];
-        run_2 = load_run<T, PER>(logits + t * a.stride, a.experts, lane, a.vec);
-        const bool there = id_2 >= 0 && id_2 < (int32_t)a.experts;
-        if (!there) id_2 = -1;
-        zid_2 = there ? to_f32(logits[t * a.stride + id_2]) : 0.f;
-        up_2 = there ? q.dweights[t * a.k + lane] : 0.f;
+    const T *row = logits + t0 * a.stride;
+    const float *lse_from = q.lse + t0, *up_from = chooses ? q.dweights + t0 * a.k + lane : nullptr;
+    const int32_t *id_from = chooses ? q.ids + t0 * a.k + lane : nullptr;
+    T *out = reinterpret_cast<T *>(q.dlogits) + t0 * q.stride;
+    const uint32_t tokens = (uint32_t)(t1 - t0);
+    uint32_t ids_left = tokens, to_fetch = tokens;
+    auto next_id = [&]() {
+        if (ids_left == 0 || !chooses) return -1;
+        --ids_left;
+        const int32_t id = *id_from;   // looked at when it has had time to come
+        id_from += a.k;
+        return id;
     };
-    id_3 = id_of(t0);
-    fetch(t0);
-    fetch(t0 + 1);
-    for (uint64_t t = t0; t < t1; ++t) {
+    auto fetch = [&]() {
+        lse_next = lse_2, up_next = up_2, zid_next = zid_2, ahead = run_2, id_next = id_2;
+        id_2 = id_3, id_3 = next_id();
+        if (to_fetch == 0) return;
+        --to_fetch;
+        lse_2 = *lse_from++;
+        run_2 = load_run<T, PER>(row, a.experts, lane, a.vec);
+        zid_2 = up_2 = 0.f;
+        if ((uint32_t)id_2 >= a.experts) id_2 = -1;
+        if (id_2 >= 0) zid_2 = to_f32(row[id_2]), up_2 = *up_from;
+        row += a.stride;
+        if (chooses) up_from += a.k;
+    };
+    id_3 = next_id();
+    fetch();
+    fetch();
+    for (uint32_t todo = tokens; todo != 0; --todo, out += q.stride) {
         const float lse = lse_next, up = up_next, zid = zid_next;
         const int32_t id = id_next;
         float z[PER];
         unpack_run<T, PER>(ahead, z);
-        fetch(t + 2);
+        fetch();
         if (fresh) {
             fresh = false;
             const float n = q.live[group], scale = dloss / ((float)a.groups * n), share = (float)a.experts / ((float)a.k * n);
@@ -544,18 +567,25 @@ __global__ void __launch_bounds__(kThreads, PER <= 8 ? 4 : 1) k_balance_backward
             }
         }
         if (--left == 0) ++group, left = a.per_group, fresh = true;
-        T *out = reinterpret_cast<T *>(q.dlogits) + t * q.stride;
         if (lse == -INFINITY) {   // masked
 #pragma unroll
             for (int i = 0; i < PER; ++i) z[i] = 0.f;
             store_run<T, PER>(out, a.experts, lane, q.vec, z);
             continue;
         }
-        float s = 0.f;
+        float s;
+        if constexpr (PER == 1) {
+            z[0] = ex2((z[0] - lse) * kLog2e);
+            s = f[0] * z[0];
+        } else {
+            float2 s2 = both(0.f);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            z[i] = ex2((z[i] - lse) * kLog2e);
-            s = fmaf(f[i], z[i], s);
+            for (int i = 0; i < PER; i += 2) {
+                const float2 d = mul2(add2(make_float2(z[i], z[i + 1]), both(-lse)), both(kLog2e));
+                z[i] = ex2(d.x), z[i + 1] = ex2(d.y);
+                s2 = fma2(make_float2(f[i], f[i + 1]), make_float2(z[i], z[i + 1]), s2);
+            }
+            s = s2.x + s2.y;
         }
         float extra = 0.f, dot = 0.f;
         if (q.dweights) {
@@ -567,12 +597,20 @@ __global__ void __launch_bounds__(kThreads, PER <= 8 ? 4 : 1) k_balance_backward
             if (id >= 0) extras[id] = extra;
         }
         const float rest = two_z * lse - warp_sum(s) - dot;
+        // p (f + rest), and what the choices add
+        if (q.dweights) __syncwarp();
+        if constexpr (PER == 1) {
+            z[0] = fmaf(z[0], f[0] + rest, q.dweights ? extras[lane] : 0.f);
+        } else {
+            const float2 *more = reinterpret_cast<const float2 *>(extras + lane * PER);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) z[i] *= f[i] + rest;
+            for (int i = 0; i < PER; i += 2) {
+                const float2 r = fma2(make_float2(z[i], z[i + 1]), add2(make_float2(f[i], f[i + 1]), both(rest)),
+                                      q.dweights ? more[i / 2] : both(0.f));
+                z[i] = r.x, z[i + 1] = r.y;
+            }
+        }
         if (q.dweights) {
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < PER; ++i) z[i] += extras[lane * PER + i];
             __syncwarp();
             if (id >= 0) extras[id] = 0.f;
             __syncwarp();
@@ -753,7 +791,7 @@ int backward(const bf16opt_balance_t *d, const int32_t *ids, const int32_t *coun
     const int per = per_of(d->experts);
     a.vec = runs(d->logits, d->logits_stride, d->experts, per, elem);
     q.vec = runs(dlogits, dlogits_stride, d->experts, per, elem);
-    const unsigned grid = (unsigned)std::min<uint64_t>((d->tokens + kWarps - 1) / kWarps, (uint64_t)sms * 8);
+    const unsigned grid = (unsigned)std::min<uint64_t>((d->tokens + kWarps - 1) / kWarps, (uint64_t)sms * (per <= 8 ? kBackResident : 1));
     return by_per(per, [&](auto p) {
         constexpr int PER = decltype(p)::value;
         Launch l{grid, (unsigned)kThreads, (size_t)kThreads * PER * 4, (cudaStream_t)stream, 0, true};

@@ -134,6 +134,77 @@ __device__ __forceinline__ float sigmoid(float x) {
     return y;
 }
 
+// Rows [first(p), first(p + 1)) are team p's.
+__host__ __device__ inline uint64_t team_row(uint64_t rows, uint32_t teams, uint32_t p) {
+    return rows / teams * p + rows % teams * p / teams;
+}
+
+// Eight columns of a row as four pairs.
+struct Cols {
+    float2 v[4];
+};
+template <class T>
+__device__ __forceinline__ Cols unpack8(const uint4 *p, uint32_t stride) {
+    Cols c;
+    const uint4 a = p[0];
+    if constexpr (sizeof(T) == 2) {
+        c.v[0] = make_float2(bf16_lo(a.x), bf16_hi(a.x)), c.v[1] = make_float2(bf16_lo(a.y), bf16_hi(a.y));
+        c.v[2] = make_float2(bf16_lo(a.z), bf16_hi(a.z)), c.v[3] = make_float2(bf16_lo(a.w), bf16_hi(a.w));
+    } else {
+        const uint4 b = p[stride];
+        c.v[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y)), c.v[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+        c.v[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y)), c.v[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+    }
+    return c;
+}
+__device__ __forceinline__ Cols all8(float x) {
+    Cols c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.v[i] = both(x);
+    return c;
+}
+__device__ __forceinline__ Cols cols_of(const float (&f)[8]) {
+    Cols c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+    return c;
+}
+// Eight columns from `c` on of a row of n: VEC: whole vectors, all of them there or none;
+// else one by one, 0 beyond the row.
+template <class T>
+__device__ __forceinline__ Cols load_cols(const T *row, uint32_t c, uint32_t n) {
+    float f[8];
+    if (c + 8 <= n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = to_f32(row[c + i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = c + i < n ? to_f32(row[c + i]) : 0.f;
+    }
+    return cols_of(f);
+}
+template <bool VEC, class T>
+__device__ __forceinline__ void store_cols(T *row, uint32_t c, uint32_t n, const Cols &x) {
+    const float f[8] = {x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y, x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y};
+    if (VEC) {
+        if (c >= n) return;
+        if constexpr (sizeof(T) == 2) {
+            __stcs(reinterpret_cast<uint4 *>(row + c), Vec<T>::pack(f));
+        } else {
+            __stcs(reinterpret_cast<float4 *>(row + c), make_float4(f[0], f[1], f[2], f[3]));
+            __stcs(reinterpret_cast<float4 *>(row + c) + 1, make_float4(f[4], f[5], f[6], f[7]));
+        }
+    } else if (c + 8 <= n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) from_f32(row[c + i], f[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < n) from_f32(row[c + i], f[i]);
+    }
+}
+__device__ __forceinline__ float2 sigmoid2(float2 x) { return make_float2(sigmoid(x.x), sigmoid(x.y)); }
+
 // ------------------------------------------------------------------------ forward
 
 // Sum over the CTA's threads of one row (a warp, or the whole CTA); the two
@@ -236,6 +307,141 @@ k_norm_forward(const Args a, const TS *x, const TB *y, TS *r, TB *h, float *stat
     if (stats && t == 0) stats[4 * row] = mean, stats[4 * row + 1] = rstd;
 }
 
+// Rows of whole vectors: a CTA walks down its rows, which come through a ring in
+// shared memory whose slots belong to one thread each, filled by asynchronous
+// copies `depth` rows ahead: with a row's loads, its two to four reductions one after the other
+// and its stores all in one CTA after the other, an SM that holds one wide row
+// moved 4.1 TB/s.  A thread has V runs of eight columns, `threads` runs apart.
+template <class TB, class TS, bool GATE, int V>
+__global__ void __launch_bounds__(V == 4 ? 512 : 384, V == 4 ? 1 : 2) k_norm_forward_ring(const Args a, const TS *x, const TB *y, TS *r, TB *h, float *stats, uint32_t depth) {
+    constexpr int UB = sizeof(TB) / 2, US = sizeof(TS) / 2, UNITS = (GATE ? 2 : 1) * UB + US;   // y, x, [gate]
+    extern __shared__ __align__(16) unsigned char ring_raw[];
+    __shared__ float buf[64];
+    const uint32_t threads = blockDim.x, t = threadIdx.x, n = a.hidden;
+    auto col = [&](int v) { return (v * threads + t) * 8; };
+    uint4 *ring = reinterpret_cast<uint4 *>(ring_raw) + t;   // [slot][run][unit][thread]
+    const uint32_t slot_units = threads * UNITS * V;
+    uint32_t turn = 0;
+    pdl_enter();
+    const uint64_t row0 = team_row(a.rows, gridDim.x, blockIdx.x), row1 = team_row(a.rows, gridDim.x, blockIdx.x + 1);
+    uint64_t copy_row = row0, gate_row = GATE ? row0 / a.rows_per_gate : 0, gate_left = GATE ? (gate_row + 1) * a.rows_per_gate - row0 : 0;
+    uint32_t copy_slot = 0;
+    auto fill = [&]() {
+        if (copy_row < row1) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (col(v) < n) {
+                    uint4 *to = ring + copy_slot * slot_units + v * UNITS * threads;
+                    const uint64_t o = copy_row * n + col(v);
+#pragma unroll
+                    for (int i = 0; i < UB; ++i) copy_async16(to + i * threads, reinterpret_cast<const uint4 *>(y + o) + i);
+#pragma unroll
+                    for (int i = 0; i < US; ++i) copy_async16(to + (UB + i) * threads, reinterpret_cast<const uint4 *>(x + o) + i);
+                    if (GATE) {
+                        const TB *g = reinterpret_cast<const TB *>(a.gate) + gate_row * n + col(v);
+#pragma unroll
+                        for (int i = 0; i < UB; ++i) copy_async16(to + (UB + US + i) * threads, reinterpret_cast<const uint4 *>(g) + i);
+                    }
+                }
+            }
+        }
+        copy_commit();
+        ++copy_row;
+        if (GATE && --gate_left == 0) ++gate_row, gate_left = a.rows_per_gate;
+        copy_slot = copy_slot + 1 == depth ? 0 : copy_slot + 1;
+    };
+    for (uint32_t s = 0; s < depth; ++s) fill();
+    // A weight's or bias's run, from L1 (read again for every row); bf16 or FP32.
+    auto weight = [&](const void *w, int v) {
+        if (a.weight_type == BF16OPT_TYPE_BF16) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(w) + col(v)));
+            return unpack8<__nv_bfloat16>(&q, 0);
+        }
+        const uint4 q[2] = {__ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(w) + col(v))),
+                            __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(w) + col(v)) + 1)};
+        return unpack8<float>(q, 1);
+    };
+    const float inv_n = 1.f / (float)n;
+    // Mean and 1/deviation of the row in u, as moments() but by pairs; runs beyond the row stay out.
+    auto moments2 = [&](const Cols(&u)[V], int kind, float &mean, float &rstd) {
+        mean = 0.f;
+        if (kind == BF16OPT_NORM_LAYER) {
+            float2 s = both(0.f);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s = add2(s, u[v].v[i]);
+            mean = row_sum<false>(s.x + s.y, buf, turn) * inv_n;
+        }
+        float2 q = both(0.f);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (col(v) < n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 d = add2(u[v].v[i], both(-mean));
+                    q = fma2(d, d, q);
+                }
+        rstd = 1.f / sqrtf(row_sum<false>(q.x + q.y, buf, turn) * inv_n + a.eps);
+    };
+    // (u - mean) rstd weight + bias
+    auto normed = [&](Cols u, const Norm &norm, float mean, float rstd, int v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u.v[i] = mul2(add2(u.v[i], both(-mean)), both(rstd));
+        if (norm.weight) {
+            const Cols w = weight(norm.weight, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u.v[i] = mul2(u.v[i], w.v[i]);
+        }
+        if (norm.bias) {
+            const Cols b = weight(norm.bias, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u.v[i] = add2(u.v[i], b.v[i]);
+        }
+        return u;
+    };
+    uint32_t slot = 0;
+    const float2 rs = both(a.residual_scale), bs = both(a.branch_scale);
+    for (uint64_t row = row0; row < row1; ++row) {
+        copy_wait_for(depth - 1);
+        const uint4 *from = ring + slot * slot_units;
+        Cols u[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) u[v] = col(v) < n ? unpack8<TB>(from + v * UNITS * threads, threads) : all8(0.f);
+        float mean = 0.f, rstd = 0.f;
+        const bool post = a.post.kind != BF16OPT_NORM_NONE;
+        if (post) moments2(u, a.post.kind, mean, rstd);
+        if (stats && t == 0) stats[4 * row + 2] = mean, stats[4 * row + 3] = rstd;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (col(v) < n) {   // else it stays 0
+                if (post) u[v] = normed(u[v], a.post, mean, rstd, v);
+                if (GATE) {
+                    const Cols g = unpack8<TB>(from + (v * UNITS + UB + US) * threads, threads);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        u[v].v[i] = mul2(u[v].v[i], a.gate_act == BF16OPT_GATE_SIGMOID ? sigmoid2(g.v[i]) : g.v[i]);
+                }
+                const Cols in = unpack8<TS>(from + (v * UNITS + UB) * threads, threads);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[v].v[i] = fma2(rs, in.v[i], mul2(bs, u[v].v[i]));
+                store_cols<true>(r + row * n, col(v), n, u[v]);
+            }
+        }
+        fill();   // the row's inputs are read
+        slot = slot + 1 == depth ? 0 : slot + 1;
+        mean = rstd = 0.f;
+        if (a.pre.kind != BF16OPT_NORM_NONE) {
+            moments2(u, a.pre.kind, mean, rstd);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (col(v) < n) store_cols<true>(h + row * n, col(v), n, normed(u[v], a.pre, mean, rstd, v));
+        }
+        if (stats && t == 0) stats[4 * row] = mean, stats[4 * row + 1] = rstd;
+    }
+    pdl_leave();
+}
+
 // ----------------------------------------------------------------------- backward
 
 // Columns of one CTA at most, so that two of 224 threads with 16 columns fit an
@@ -256,11 +462,6 @@ struct BackArgs {
     uint32_t want;         // bits: the weights' gradients asked for, in the order of part
     bool shared_gate;      // rows share gate rows and dgate is wanted
 };
-
-// Rows [first(p), first(p + 1)) are team p's.
-__host__ __device__ inline uint64_t team_row(uint64_t rows, uint32_t teams, uint32_t p) {
-    return rows / teams * p + rows % teams * p / teams;
-}
 
 // The team of a row.
 __device__ __forceinline__ uint32_t team_of(uint64_t rows, uint32_t teams, uint64_t row) {
@@ -296,72 +497,6 @@ __device__ __forceinline__ float warp_sum8(const float (&s)[8], uint32_t lane) {
     return c;
 }
 __device__ __forceinline__ uint32_t lane_value(uint32_t lane) { return (lane & 1) * 4 + (lane & 2) + ((lane & 4) >> 2); }
-
-// Eight columns of a row as four pairs.
-struct Cols {
-    float2 v[4];
-};
-template <class T>
-__device__ __forceinline__ Cols unpack8(const uint4 *p, uint32_t stride) {
-    Cols c;
-    const uint4 a = p[0];
-    if constexpr (sizeof(T) == 2) {
-        c.v[0] = make_float2(bf16_lo(a.x), bf16_hi(a.x)), c.v[1] = make_float2(bf16_lo(a.y), bf16_hi(a.y));
-        c.v[2] = make_float2(bf16_lo(a.z), bf16_hi(a.z)), c.v[3] = make_float2(bf16_lo(a.w), bf16_hi(a.w));
-    } else {
-        const uint4 b = p[stride];
-        c.v[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y)), c.v[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
-        c.v[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y)), c.v[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
-    }
-    return c;
-}
-__device__ __forceinline__ Cols all8(float x) {
-    Cols c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c.v[i] = both(x);
-    return c;
-}
-__device__ __forceinline__ Cols cols_of(const float (&f)[8]) {
-    Cols c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c.v[i] = make_float2(f[2 * i], f[2 * i + 1]);
-    return c;
-}
-// Eight columns from `c` on of a row of n: VEC: whole vectors, all of them there or none;
-// else one by one, 0 beyond the row.
-template <class T>
-__device__ __forceinline__ Cols load_cols(const T *row, uint32_t c, uint32_t n) {
-    float f[8];
-    if (c + 8 <= n) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = to_f32(row[c + i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = c + i < n ? to_f32(row[c + i]) : 0.f;
-    }
-    return cols_of(f);
-}
-template <bool VEC, class T>
-__device__ __forceinline__ void store_cols(T *row, uint32_t c, uint32_t n, const Cols &x) {
-    const float f[8] = {x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y, x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y};
-    if (VEC) {
-        if (c >= n) return;
-        if constexpr (sizeof(T) == 2) {
-            __stcs(reinterpret_cast<uint4 *>(row + c), Vec<T>::pack(f));
-        } else {
-            __stcs(reinterpret_cast<float4 *>(row + c), make_float4(f[0], f[1], f[2], f[3]));
-            __stcs(reinterpret_cast<float4 *>(row + c) + 1, make_float4(f[4], f[5], f[6], f[7]));
-        }
-    } else if (c + 8 <= n) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) from_f32(row[c + i], f[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < n) from_f32(row[c + i], f[i]);
-    }
-}
-__device__ __forceinline__ float2 sigmoid2(float2 x) { return make_float2(sigmoid(x.x), sigmoid(x.y)); }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -514,7 +649,7 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
 
     // the eight sums of a row, published to every CTA of the team
     auto publish = [&](uint64_t row, uint32_t slot, const GateRow &gr, const float4 &st, uint32_t at) {
-        const float2 x1 = both(st.y), x0 = both(-st.x), y1 = both(st.w), y0 = both(-st.z);
+        const float2 x1 = both(st.y), x0 = both(-st.x), y0 = both(-st.z);
         float2 s2[kSums];
 #pragma unroll
         for (int k = 0; k < kSums; ++k) s2[k] = both(0.f);
@@ -523,20 +658,21 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
             const Run w = load_run(row, slot, gr, v);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 xhat = mul2(add2(w.r.v[i], x0), x1), yhat = mul2(add2(w.y.v[i], y0), y1);
+                // xhat = x1 xc, yhat = y1 yc: the scales of a row come to its sums at the end
+                const float2 xc = add2(w.r.v[i], x0), yc = add2(w.y.v[i], y0);
                 const float2 av = mul2(w1[v].v[i], w.dh.v[i]);
                 const float2 base = fma2(x1, av, w.dr.v[i]);
                 float2 c = w2[v].v[i];
                 if (GATE) c = mul2(c, a.gate_act == BF16OPT_GATE_SIGMOID ? sigmoid2(w.gate.v[i]) : w.gate.v[i]);
-                const float2 cy = mul2(c, yhat);
+                const float2 cy = mul2(c, yc);
                 s2[0] = add2(s2[0], av);
-                s2[1] = fma2(av, xhat, s2[1]);
+                s2[1] = fma2(av, xc, s2[1]);
                 s2[2] = fma2(c, base, s2[2]);
                 s2[3] = add2(s2[3], c);
-                s2[4] = fma2(c, xhat, s2[4]);
+                s2[4] = fma2(c, xc, s2[4]);
                 s2[5] = fma2(cy, base, s2[5]);
                 s2[6] = add2(s2[6], cy);
-                s2[7] = fma2(cy, xhat, s2[7]);
+                s2[7] = fma2(cy, xc, s2[7]);
             }
         }
         float s[kSums];
@@ -591,12 +727,12 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
         float s[kSums];
         totals(sums_at, s);
         sums_at = at1;
-        // g = base - (m1 + xhat m2);  e = c g;  dy = rs2 (e - n1 - yhat n2)
-        const float m1 = pre_layer ? s[0] * inv_h * st.y : 0.f, m2 = s[1] * inv_h * st.y;
-        const float n1 = post_layer ? (s[2] - m1 * s[3] - m2 * s[4]) * inv_h : 0.f;
-        const float n2 = post ? (s[5] - m1 * s[6] - m2 * s[7]) * inv_h : 0.f;
+        // g = base - (m1 + xhat m2);  e = c g;  dy = rs2 (e - n1 - yhat n2); the sums are those of xc and yc
+        const float m1 = pre_layer ? s[0] * inv_h * st.y : 0.f, m2 = s[1] * st.y * inv_h * st.y;
+        const float n1 = post_layer ? (s[2] - m1 * s[3] - m2 * (s[4] * st.y)) * inv_h : 0.f;
+        const float n2 = post ? (s[5] - m1 * s[6] - m2 * (s[7] * st.y)) * st.w * inv_h : 0.f;
         const float2 x1 = both(st.y), x0 = both(-st.x), y1 = both(st.w), y0 = both(-st.z);
-        const float2 nm1 = both(-m1), nm2 = both(-m2), nn1 = both(-n1), nn2 = both(-n2);
+        const float2 nm1 = both(-m1), nm2 = both(-m2 * st.y), nn1 = both(-n1 * st.w), nn2 = both(-n2 * st.w * st.w);
         // the gate's rows end, here or for this team; its sum is whole if they all are this team's,
         // else a part: of the team's first gate, or of its last
         const uint64_t gate_first = gate.row * a.rows_per_gate;
@@ -608,13 +744,13 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
             Cols dx, dy, dgr;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 xhat = mul2(add2(w.r.v[i], x0), x1), yhat = mul2(add2(w.y.v[i], y0), y1);
-                const float2 base = fma2(x1, mul2(w1[v].v[i], w.dh.v[i]), w.dr.v[i]);
-                float2 g = add2(fma2(xhat, nm2, base), nm1);
+                const float2 xc = add2(w.r.v[i], x0), yc = add2(w.y.v[i], y0), xdh = mul2(x1, w.dh.v[i]);
+                const float2 base = fma2(w1[v].v[i], xdh, w.dr.v[i]);
+                float2 g = add2(fma2(xc, nm2, base), nm1);
                 dx.v[i] = mul2(rs, g);
                 if (GATE) {
                     float2 act = w.gate.v[i];
-                    const float2 du = mul2(g, fma2(yhat, w2[v].v[i], b2[v].v[i]));
+                    const float2 du = mul2(g, fma2(mul2(yc, y1), w2[v].v[i], b2[v].v[i]));
                     if (a.gate_act == BF16OPT_GATE_SIGMOID) {
                         act = sigmoid2(act);
                         dgr.v[i] = mul2(du, mul2(act, make_float2(1.f - act.x, 1.f - act.y)));
@@ -623,11 +759,12 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
                     }
                     g = mul2(act, g);
                 }
-                dw2[v].v[i] = fma2(g, yhat, dw2[v].v[i]);
+                const float2 gy = mul2(y1, g);
+                dw2[v].v[i] = fma2(gy, yc, dw2[v].v[i]);
                 db2[v].v[i] = add2(db2[v].v[i], g);
-                dw1[v].v[i] = fma2(w.dh.v[i], xhat, dw1[v].v[i]);
+                dw1[v].v[i] = fma2(xdh, xc, dw1[v].v[i]);
                 db1[v].v[i] = add2(db1[v].v[i], w.dh.v[i]);
-                dy.v[i] = mul2(y1, add2(fma2(w2[v].v[i], g, mul2(yhat, nn2)), nn1));
+                dy.v[i] = fma2(w2[v].v[i], gy, fma2(yc, nn2, nn1));
             }
             store_cols<VEC>(reinterpret_cast<TS *>(q.dx) + o, col(v), n, dx);
             store_cols<VEC>(reinterpret_cast<TB *>(q.dy) + o, col(v), n, dy);
@@ -778,6 +915,29 @@ bool vectors(const bf16opt_norm_gate_t *d, std::initializer_list<const void *> m
     return true;
 }
 
+constexpr size_t kSmemBytes = 226 * 1024;   // of a multiprocessor; each CTA takes 1 KB besides its own
+// What each of per_sm CTAs can have for its ring besides `other` bytes (at most what a kernel is allowed).
+size_t ring_bytes(unsigned per_sm, size_t other) {
+    return std::min<size_t>(kSmemBytes / per_sm - 1024, kMaxDynamic) - other;
+}
+
+template <class TB, class TS, bool GATE, int V>
+int forward_ring(const Args &a, const void *x, const void *y, void *r, void *h, float *stats, cudaStream_t st) {
+    auto k = k_norm_forward_ring<TB, TS, GATE, V>;
+    const uint32_t threads = ((a.hidden + 8 * V - 1) / (8 * V) + 31) / 32 * 32;
+    const size_t row = (size_t)threads * V * 16 * ((GATE ? 2 : 1) * sizeof(TB) / 2 + sizeof(TS) / 2);
+    const unsigned per_sm = std::max(1u, std::min((V == 4 ? 512u : 768u) / threads, 16u));   // by the registers
+    const uint32_t depth = (uint32_t)std::max<size_t>(1, std::min<size_t>(4, ring_bytes(per_sm, 256) / row));
+    Launch l{1, threads, depth * row, st, 1, true};
+    int fit = 0;
+    cudaError_t e = clusters_that_fit(l, k, fit);
+    if (e != cudaSuccess) return fail_cuda(e, "norm_gate occupancy");
+    l.grid = (unsigned)std::min<uint64_t>(a.rows, fit);
+    l.cluster = 0;
+    e = launch(l, k, a, (const TS *)x, (const TB *)y, (TS *)r, (TB *)h, stats, depth);
+    return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "norm_gate kernel launch");
+}
+
 template <class TB, class TS, bool VEC>
 int forward_v(const Args &a, const void *x, const void *y, void *r, void *h, float *stats, cudaStream_t st) {
     const uint32_t vecs = (a.hidden + 7) / 8;
@@ -788,10 +948,18 @@ int forward_v(const Args &a, const void *x, const void *y, void *r, void *h, flo
     };
     if (vecs <= 32) return go(k_norm_forward<TB, TS, VEC, true, 1>, 128, true);
     if (vecs <= 64) return go(k_norm_forward<TB, TS, VEC, true, 2>, 128, true);
-    auto block = [&](uint32_t nv) { return (unsigned)(((vecs + nv - 1) / nv + 31) / 32 * 32); };
-    if (vecs <= 512) return go(k_norm_forward<TB, TS, VEC, false, 1>, block(1), false);
-    if (vecs <= 1024) return go(k_norm_forward<TB, TS, VEC, false, 2>, block(2), false);
-    return go(k_norm_forward<TB, TS, VEC, false, 4>, block(4), false);
+    if constexpr (VEC) {
+        auto ring = [&](auto v) {
+            constexpr int V = decltype(v)::value;
+            return a.gate ? forward_ring<TB, TS, true, V>(a, x, y, r, h, stats, st) : forward_ring<TB, TS, false, V>(a, x, y, r, h, stats, st);
+        };
+        return vecs <= 768 ? ring(std::integral_constant<int, 2>()) : ring(std::integral_constant<int, 4>());
+    } else {
+        auto block = [&](uint32_t nv) { return (unsigned)(((vecs + nv - 1) / nv + 31) / 32 * 32); };
+        if (vecs <= 512) return go(k_norm_forward<TB, TS, VEC, false, 1>, block(1), false);
+        if (vecs <= 1024) return go(k_norm_forward<TB, TS, VEC, false, 2>, block(2), false);
+        return go(k_norm_forward<TB, TS, VEC, false, 4>, block(4), false);
+    }
 }
 
 // The backward pass's shape, from the sizes and the device alone.
@@ -811,8 +979,6 @@ int by_types(const bf16opt_norm_gate_t *d, F &&f) {
     return f((B *)nullptr, (B *)nullptr);
 }
 
-constexpr size_t kSmemBytes = 226 * 1024;   // of a multiprocessor; each CTA takes 1 KB besides its own
-
 // Runs of eight columns a thread has: two where whole vectors pass through the ring, and
 // there is no gate (its sums would not fit the registers).
 template <bool VEC, bool GATE>
@@ -827,7 +993,7 @@ int shape_v(const bf16opt_norm_gate_t *d, int sms, Shape &s) {
     s.threads = ((cols + 8 * V - 1) / (8 * V) + 31) / 32 * 32;
     const unsigned per_sm = std::max(1u, std::min(512u / s.threads, 16u));   // 128 registers a thread
     const size_t row = (size_t)s.threads * V * ring_units<TB, TS, GATE>() * 16, sums = 3 * s.cluster * s.threads / 32 * kSums * sizeof(float);
-    s.depth = VEC ? (uint32_t)std::max<size_t>(2, std::min<size_t>(8, (kSmemBytes / per_sm - sums - 1024) / row)) : 2;
+    s.depth = VEC ? (uint32_t)std::max<size_t>(2, std::min<size_t>(8, ring_bytes(per_sm, sums) / row)) : 2;
     s.smem = (VEC ? s.depth * row : 0) + sums;
     int fit = 0;
     const cudaError_t e = clusters_that_fit(Launch{s.cluster, s.threads, s.smem, nullptr, s.cluster, true},

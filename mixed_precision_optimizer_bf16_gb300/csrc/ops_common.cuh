@@ -215,6 +215,8 @@ struct Launch {
     bool dependent = false;  // programmatic dependent launch (the kernel calls pdl_enter)
 };
 
+constexpr size_t kMaxDynamic = 220 * 1024;   // shared memory that a kernel may ask for at a launch
+
 // Clusters (or CTAs) of this launch that the device holds at once, with the kernel
 // allowed its shared memory.  Both questions cost microseconds, so the answers
 // are kept, by kernel, device and shape.
@@ -245,7 +247,7 @@ cudaError_t clusters_that_fit(const Launch &l, void (*kernel)(KArgs...), int &n,
         }
     if (l.smem > 32 * 1024) {   // with the static arrays, more than a kernel may have unasked
         // as much as any shape of it takes, so that a smaller one's answer does not take it back
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(220 * 1024));
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDynamic);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
