@@ -45,15 +45,6 @@ struct Args {
 
 __host__ __device__ inline size_t slot_floats(uint32_t experts) { return 2 * (size_t)experts + 2; }
 
-__host__ __device__ inline uint64_t team_row(uint64_t rows, uint32_t teams, uint32_t p) {
-    return rows / teams * p + rows % teams * p / teams;
-}
-__device__ __forceinline__ uint32_t team_of(uint64_t rows, uint32_t teams, uint64_t row) {
-    uint32_t p = (uint32_t)(row / (rows / teams + 1));
-    while (team_row(rows, teams, p + 1) <= row) ++p;
-    return p;
-}
-
 // Logits as unsigned keys in their order: -inf (an expert that is off) 0, NaN 1,
 // then the numbers; both zeros are one key.
 __device__ __forceinline__ uint32_t key_of(float z) {

@@ -134,11 +134,6 @@ __device__ __forceinline__ float sigmoid(float x) {
     return y;
 }
 
-// Rows [first(p), first(p + 1)) are team p's.
-__host__ __device__ inline uint64_t team_row(uint64_t rows, uint32_t teams, uint32_t p) {
-    return rows / teams * p + rows % teams * p / teams;
-}
-
 // Eight columns of a row as four pairs.
 struct Cols {
     float2 v[4];
@@ -351,15 +346,24 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 384, V == 4 ? 1 : 2) k_norm_for
         copy_slot = copy_slot + 1 == depth ? 0 : copy_slot + 1;
     };
     for (uint32_t s = 0; s < depth; ++s) fill();
-    // A weight's or bias's run, from L1 (read again for every row); bf16 or FP32.
-    auto weight = [&](const void *w, int v) {
-        if (a.weight_type == BF16OPT_TYPE_BF16) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(w) + col(v)));
-            return unpack8<__nv_bfloat16>(&q, 0);
-        }
-        const uint4 q[2] = {__ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(w) + col(v))),
-                            __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(w) + col(v)) + 1)};
+    // The first 16 bytes of a weight's or bias's run: all of a bf16 one, half of an FP32 one. The weights'
+    // are asked for before the reduction that comes before their use: they come from L2 where
+    // the ring leaves L1 no room for them.
+    auto first16 = [&](const void *w, int v) {
+        return __ldg(reinterpret_cast<const uint4 *>((const char *)w + (size_t)col(v) * (a.weight_type == BF16OPT_TYPE_BF16 ? 2 : 4)));
+    };
+    auto weight = [&](const void *w, int v, const uint4 &first) {
+        uint4 q[2] = {first, first};
+        if (a.weight_type == BF16OPT_TYPE_BF16) return unpack8<__nv_bfloat16>(q, 0);
+        q[1] = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(w) + col(v)) + 1);
         return unpack8<float>(q, 1);
+    };
+    uint4 ahead[V];
+    auto ask = [&](const Norm &norm) {
+        if (norm.weight)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (col(v) < n) ahead[v] = first16(norm.weight, v);
     };
     const float inv_n = 1.f / (float)n;
     // Mean and 1/deviation of the row in u, as moments() but by pairs; runs beyond the row stay out.
@@ -389,12 +393,12 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 384, V == 4 ? 1 : 2) k_norm_for
 #pragma unroll
         for (int i = 0; i < 4; ++i) u.v[i] = mul2(add2(u.v[i], both(-mean)), both(rstd));
         if (norm.weight) {
-            const Cols w = weight(norm.weight, v);
+            const Cols w = weight(norm.weight, v, ahead[v]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) u.v[i] = mul2(u.v[i], w.v[i]);
         }
         if (norm.bias) {
-            const Cols b = weight(norm.bias, v);
+            const Cols b = weight(norm.bias, v, first16(norm.bias, v));
 #pragma unroll
             for (int i = 0; i < 4; ++i) u.v[i] = add2(u.v[i], b.v[i]);
         }
@@ -410,7 +414,10 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 384, V == 4 ? 1 : 2) k_norm_for
         for (int v = 0; v < V; ++v) u[v] = col(v) < n ? unpack8<TB>(from + v * UNITS * threads, threads) : all8(0.f);
         float mean = 0.f, rstd = 0.f;
         const bool post = a.post.kind != BF16OPT_NORM_NONE;
-        if (post) moments2(u, a.post.kind, mean, rstd);
+        if (post) {
+            ask(a.post);
+            moments2(u, a.post.kind, mean, rstd);
+        }
         if (stats && t == 0) stats[4 * row + 2] = mean, stats[4 * row + 3] = rstd;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -432,6 +439,7 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 384, V == 4 ? 1 : 2) k_norm_for
         slot = slot + 1 == depth ? 0 : slot + 1;
         mean = rstd = 0.f;
         if (a.pre.kind != BF16OPT_NORM_NONE) {
+            ask(a.pre);
             moments2(u, a.pre.kind, mean, rstd);
 #pragma unroll
             for (int v = 0; v < V; ++v)
@@ -462,13 +470,6 @@ struct BackArgs {
     uint32_t want;         // bits: the weights' gradients asked for, in the order of part
     bool shared_gate;      // rows share gate rows and dgate is wanted
 };
-
-// The team of a row.
-__device__ __forceinline__ uint32_t team_of(uint64_t rows, uint32_t teams, uint64_t row) {
-    uint32_t p = (uint32_t)(row / (rows / teams + 1));   // not beyond it
-    while (team_row(rows, teams, p + 1) <= row) ++p;
-    return p;
-}
 
 // Sum of eight values over a warp: each step a lane keeps half of the values
 // and hands the other half over, so it costs 9 shuffles, not 40.  Lane l ends up
@@ -503,9 +504,9 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // 16-byte units of eight columns of a row that a thread keeps in the ring: y, dh, [gate] of the
 // branch's type, r, dr of the stream's.
-template <class TB, class TS, bool GATE>
+template <class TB, class TS, int GATE>
 __host__ __device__ constexpr int ring_units() {
-    return (GATE ? 3 : 2) * (int)sizeof(TB) / 2 + 2 * (int)sizeof(TS) / 2;
+    return (GATE == 1 ? 3 : 2) * (int)sizeof(TB) / 2 + 2 * (int)sizeof(TS) / 2;
 }
 
 // A team (a CTA, or a cluster that shares the columns) walks down its rows in two
@@ -515,7 +516,13 @@ __host__ __device__ constexpr int ring_units() {
 // by asynchronous copies `depth` rows ahead.  A thread has V runs of eight columns,
 // `threads` runs apart.  VEC: rows of whole 16-byte vectors; else elements are
 // loaded one by one, twice, and there is no ring.
-template <class TB, class TS, bool VEC, bool GATE, int V>
+// GATE: 0 none; 1 a row of it comes with each row; 2 many rows share one (kGateRows at
+// least): its values are in w2, and since they are the same for all those rows, P = sum g yhat
+// and Q = sum g down the rows give all that depends on it when the rows end:
+//     dgate = act' (weight P + bias Q),  dweight += act P,  dbias += act Q.
+// There the row after the last is published only when the gate has changed.
+constexpr uint64_t kGateRows = 8;
+template <class TB, class TS, bool VEC, int GATE, int V>
 __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Args a, const BackArgs q, uint32_t depth) {
     constexpr int UNITS = ring_units<TB, TS, GATE>(), UB = sizeof(TB) / 2, US = sizeof(TS) / 2;
     extern __shared__ __align__(16) unsigned char ring_raw[];
@@ -576,7 +583,7 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
                     put(2 * UB, reinterpret_cast<const TS *>(q.r), o);
                 }
                 if (q.dr) put(2 * UB + US, reinterpret_cast<const TS *>(q.dr), o);
-                if (GATE) put(2 * UB + 2 * US, reinterpret_cast<const TB *>(a.gate), copy_gate.row * a.hidden + c0);
+                if (GATE == 1) put(2 * UB + 2 * US, reinterpret_cast<const TB *>(a.gate), copy_gate.row * a.hidden + c0);
             }
         }
         copy_commit();
@@ -602,7 +609,7 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
             const uint4 *p = ring + slot * slot_units + v * UNITS * threads;
             w.y = unpack8<TB>(p, threads), w.dh = unpack8<TB>(p + UB * threads, threads);
             w.r = unpack8<TS>(p + 2 * UB * threads, threads), w.dr = unpack8<TS>(p + (2 * UB + US) * threads, threads);
-            if constexpr (GATE) w.gate = unpack8<TB>(p + (2 * UB + 2 * US) * threads, threads);
+            if constexpr (GATE == 1) w.gate = unpack8<TB>(p + (2 * UB + 2 * US) * threads, threads);
         } else {
             const uint64_t o = row * a.hidden + c0;
             const Cols zero = all8(0.f);
@@ -610,7 +617,7 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
             w.dh = pre ? load_cols(reinterpret_cast<const TB *>(q.dh) + o, col(v), n) : zero;
             w.r = pre ? load_cols(reinterpret_cast<const TS *>(q.r) + o, col(v), n) : zero;
             w.dr = q.dr ? load_cols(reinterpret_cast<const TS *>(q.dr) + o, col(v), n) : zero;
-            if constexpr (GATE) w.gate = load_cols(reinterpret_cast<const TB *>(a.gate) + g.row * a.hidden + c0, col(v), n);
+            if constexpr (GATE == 1) w.gate = load_cols(reinterpret_cast<const TB *>(a.gate) + g.row * a.hidden + c0, col(v), n);
         }
         return w;
     };
@@ -627,18 +634,33 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
     // weights: 0 beyond the row, so that what is there counts for nothing; the post-norm's
     // with the branch's scale in it
     auto weights = [&](const void *w, float none, float scale, int v) {
-        float f[8];
+        Cols c = all8(0.f);
+        if (col(v) >= n) return c;
+        if (!w) c = all8(none);
+        else if (VEC && a.weight_type == BF16OPT_TYPE_BF16)
+            c = unpack8<__nv_bfloat16>(reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(w) + c0 + col(v)), 1);
+        else if (VEC)
+            c = unpack8<float>(reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(w) + c0 + col(v)), 1);
+        else if (a.weight_type == BF16OPT_TYPE_BF16)
+            c = load_cols(reinterpret_cast<const __nv_bfloat16 *>(w) + c0, col(v), n);
+        else
+            c = load_cols(reinterpret_cast<const float *>(w) + c0, col(v), n);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] = col(v) + i < n ? scale * (w ? load_typed(w, a.weight_type, c0 + col(v) + i) : none) : 0.f;
-        return cols_of(f);
+        for (int i = 0; i < 4; ++i) {
+            c.v[i] = mul2(c.v[i], both(scale));
+            if (!VEC && !w) {   // the last run may be part of the row only
+                if (col(v) + 2 * i >= n) c.v[i].x = 0.f;
+                if (col(v) + 2 * i + 1 >= n) c.v[i].y = 0.f;
+            }
+        }
+        return c;
     };
     Cols w1[V], w2[V], b2[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         w1[v] = weights(a.pre.weight, 1.f, 1.f, v);
         w2[v] = weights(a.post.weight, 1.f, a.branch_scale, v);
-        if (GATE) b2[v] = weights(a.post.bias, 0.f, a.branch_scale, v);
+        if (GATE == 1) b2[v] = weights(a.post.bias, 0.f, a.branch_scale, v);
     }
 
     // sums down the rows; of the post-norm's gradients without the branch's scale, which comes at the end
@@ -646,6 +668,62 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
 #pragma unroll
     for (int v = 0; v < V; ++v) dw1[v] = db1[v] = dw2[v] = db2[v] = dg[v] = all8(0.f);
     const float2 rs = both(a.residual_scale);
+
+    // GATE 2: the gate row's values into w2, and what its rows came to
+    auto gate_cols = [&](int v) {
+        const TB *g = reinterpret_cast<const TB *>(a.gate) + gate.row * a.hidden + c0;
+        if (!VEC) return load_cols(g, col(v), n);
+        return col(v) < n ? unpack8<TB>(reinterpret_cast<const uint4 *>(g + col(v)), 1) : all8(0.f);
+    };
+    auto take_gate = [&]() {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            w2[v] = weights(a.post.weight, 1.f, a.branch_scale, v);
+            const Cols g = gate_cols(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w2[v].v[i] = mul2(w2[v].v[i], a.gate_act == BF16OPT_GATE_SIGMOID ? sigmoid2(g.v[i]) : g.v[i]);
+        }
+    };
+    bool gates_before = false;
+    auto end_gate = [&](bool whole, bool last_of_team) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Cols g = gate_cols(v), w = weights(a.post.weight, 1.f, a.branch_scale, v), b = weights(a.post.bias, 0.f, a.branch_scale, v);
+            Cols d;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float2 act = g.v[i], slope = both(1.f);
+                if (a.gate_act == BF16OPT_GATE_SIGMOID) {
+                    act = sigmoid2(act);
+                    slope = mul2(act, make_float2(1.f - act.x, 1.f - act.y));
+                }
+                d.v[i] = mul2(slope, fma2(w.v[i], dw2[v].v[i], mul2(b.v[i], db2[v].v[i])));
+                dw2[v].v[i] = mul2(act, dw2[v].v[i]), db2[v].v[i] = mul2(act, db2[v].v[i]);
+            }
+            if (q.dgate) {
+                if (whole) store_cols<VEC>(reinterpret_cast<TB *>(q.dgate) + gate.row * a.hidden + c0, col(v), n, d);
+                else store_cols<VEC>(q.gate_part + (size_t)(2 * team + (gate.row * a.rows_per_gate > row0 ? 1 : 0)) * a.hidden + c0, col(v), n, d);
+            }
+            // the weights' sums over the gates so far are kept where the partial sums go
+            float *p = q.part + (size_t)team * 4 * a.hidden + c0;
+            if (gates_before) {
+                auto kept = [&](const float *f) {
+                    if (!VEC) return load_cols(f, col(v), n);
+                    return col(v) < n ? unpack8<float>(reinterpret_cast<const uint4 *>(f + col(v)), 1) : all8(0.f);
+                };
+                const Cols w0 = kept(p + 2 * (size_t)a.hidden), b0 = kept(p + 3 * (size_t)a.hidden);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dw2[v].v[i] = add2(w0.v[i], dw2[v].v[i]), db2[v].v[i] = add2(b0.v[i], db2[v].v[i]);
+            }
+            if (!last_of_team) {
+                store_cols<VEC>(p + 2 * (size_t)a.hidden, col(v), n, dw2[v]);
+                store_cols<VEC>(p + 3 * (size_t)a.hidden, col(v), n, db2[v]);
+                dw2[v] = db2[v] = all8(0.f);
+            }
+        }
+        gates_before = true;
+    };
+    if (GATE == 2) take_gate();
 
     // the eight sums of a row, published to every CTA of the team
     auto publish = [&](uint64_t row, uint32_t slot, const GateRow &gr, const float4 &st, uint32_t at) {
@@ -663,7 +741,7 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
                 const float2 av = mul2(w1[v].v[i], w.dh.v[i]);
                 const float2 base = fma2(x1, av, w.dr.v[i]);
                 float2 c = w2[v].v[i];
-                if (GATE) c = mul2(c, a.gate_act == BF16OPT_GATE_SIGMOID ? sigmoid2(w.gate.v[i]) : w.gate.v[i]);
+                if (GATE == 1) c = mul2(c, a.gate_act == BF16OPT_GATE_SIGMOID ? sigmoid2(w.gate.v[i]) : w.gate.v[i]);
                 const float2 cy = mul2(c, yc);
                 s2[0] = add2(s2[0], av);
                 s2[1] = fma2(av, xc, s2[1]);
@@ -718,11 +796,15 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
         // the next row's sums set out before this row's are used
         GateRow gate1 = gate;
         gate_next(gate1);
-        if (row + 1 < row1) {
-            if (VEC) copy_wait_for(depth - 2);
-            publish(row + 1, slot1, gate1, st1, at1);
-        }
-        if (ranks > 1) cluster_arrive();
+        const bool gate_over = GATE == 2 && (gate.left == 1 || row + 1 == row1);
+        auto publish_next = [&]() {
+            if (row + 1 < row1) {
+                if (VEC) copy_wait_for(depth - 2);
+                publish(row + 1, slot1, gate1, st1, at1);
+            }
+            if (ranks > 1) cluster_arrive();
+        };
+        if (!gate_over) publish_next();
 
         float s[kSums];
         totals(sums_at, s);
@@ -736,7 +818,7 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
         // the gate's rows end, here or for this team; its sum is whole if they all are this team's,
         // else a part: of the team's first gate, or of its last
         const uint64_t gate_first = gate.row * a.rows_per_gate;
-        const bool gate_ends = GATE && q.shared_gate && (gate.left == 1 || row + 1 == row1), gate_whole = gate_first >= row0 && gate.left == 1;
+        const bool gate_ends = GATE == 1 && q.shared_gate && (gate.left == 1 || row + 1 == row1), gate_whole = gate_first >= row0 && gate.left == 1;
         const uint64_t o = row * a.hidden + c0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -748,7 +830,7 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
                 const float2 base = fma2(w1[v].v[i], xdh, w.dr.v[i]);
                 float2 g = add2(fma2(xc, nm2, base), nm1);
                 dx.v[i] = mul2(rs, g);
-                if (GATE) {
+                if (GATE == 1) {
                     float2 act = w.gate.v[i];
                     const float2 du = mul2(g, fma2(mul2(yc, y1), w2[v].v[i], b2[v].v[i]));
                     if (a.gate_act == BF16OPT_GATE_SIGMOID) {
@@ -768,7 +850,7 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
             }
             store_cols<VEC>(reinterpret_cast<TS *>(q.dx) + o, col(v), n, dx);
             store_cols<VEC>(reinterpret_cast<TB *>(q.dy) + o, col(v), n, dy);
-            if (GATE && q.dgate) {
+            if (GATE == 1 && q.dgate) {
                 if (q.shared_gate) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) dg[v].v[i] = add2(dg[v].v[i], dgr.v[i]);
@@ -781,6 +863,12 @@ __global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Arg
                     store_cols<VEC>(reinterpret_cast<TB *>(q.dgate) + o, col(v), n, dgr);
                 }
             }
+        }
+        if (gate_over) {
+            end_gate(gate.row * a.rows_per_gate >= row0 && gate.left == 1, row + 1 == row1);
+            gate = gate1;
+            if (row + 1 < row1) take_gate();
+            publish_next();
         }
         if (VEC) fill();
         slot = slot1;
@@ -815,42 +903,57 @@ struct JoinArgs {
     uint32_t teams, hidden;
 };
 constexpr int kRuns = 16;
+template <int W>   // columns of a lane: 4 where the partial sums' rows are whole 16-byte vectors, else 1
 __global__ void __launch_bounds__(32 * kRuns) k_norm_join(const JoinArgs j) {
-    __shared__ float sm[kRuns][32];
+    __shared__ float sm[kRuns][32 * W];
     pdl_enter();
     const uint32_t lane = threadIdx.x & 31, run = threadIdx.x >> 5;
-    const uint32_t c = blockIdx.x * 32 + lane;
+    const uint32_t c = (blockIdx.x * 32 + lane) * W;
     for (uint64_t b = blockIdx.y; b < 4 + (j.dgate ? j.gate_rows : 0); b += gridDim.y) {
         const float *p;          // part i is p + i * stride (+ skip for i = 0)
         size_t stride, skip = 0;
         uint32_t count;
-        uint64_t at = c;
+        uint64_t at;
         void *out;
         if (b < 4) {
-            out = j.out[b];
+            out = b == 0 ? j.out[0] : b == 1 ? j.out[1] : b == 2 ? j.out[2] : j.out[3];
             p = j.part + b * j.hidden, stride = 4 * (size_t)j.hidden, count = j.teams;
+            at = 0;
         } else {
             const uint64_t g = b - 4, first = g * j.rows_per_gate, last = first + j.rows_per_gate - 1;
-            uint32_t p0 = team_of(j.rows, j.teams, first), p1 = team_of(j.rows, j.teams, last);
+            const uint32_t p0 = team_of(j.rows, j.teams, first), p1 = team_of(j.rows, j.teams, last);
             out = p0 == p1 ? nullptr : j.dgate;   // within one team: already written
-            at = g * j.hidden + c;
+            at = g * j.hidden;
             p = j.gate_part + (size_t)(2 * p0) * j.hidden, stride = 2 * (size_t)j.hidden, count = p1 - p0 + 1;
             skip = first > team_row(j.rows, j.teams, p0) ? j.hidden : 0;   // the first team's last gate, not its first
         }
         if (!out) continue;
-        float s = 0.f;
+        float s[W] = {};
         const uint32_t i0 = count * run / kRuns, i1 = count * (run + 1) / kRuns;
         if (c < j.hidden)
 #pragma unroll 8
-            for (uint32_t i = i0; i < i1; ++i) s += p[i * stride + (i ? 0 : skip) + c];
-        sm[run][lane] = s;
+            for (uint32_t i = i0; i < i1; ++i) {
+                const float *from = p + i * stride + (i ? 0 : skip) + c;
+                if constexpr (W == 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(from);
+                    s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
+                } else {
+                    s[0] += *from;
+                }
+            }
+#pragma unroll
+        for (int k = 0; k < W; ++k) sm[run][lane * W + k] = s[k];
         __syncthreads();
-        if (run == 0 && c < j.hidden) {
-            for (int i = 1; i < kRuns; ++i) s += sm[i][lane];
-            store_typed(out, b < 4 ? j.weight_type : j.gate_type, at, s);
+        if (threadIdx.x < 32 * W) {   // one thread a column
+            const uint32_t column = blockIdx.x * 32 * W + threadIdx.x;
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i) sum += sm[i][threadIdx.x];
+            if (column < j.hidden) store_typed(out, b < 4 ? j.weight_type : j.gate_type, at + column, sum);
         }
         __syncthreads();
     }
+    pdl_leave();
 }
 
 // ---------------------------------------------------------------------- host
@@ -980,11 +1083,11 @@ int by_types(const bf16opt_norm_gate_t *d, F &&f) {
 }
 
 // Runs of eight columns a thread has: two where whole vectors pass through the ring, and
-// there is no gate (its sums would not fit the registers).
-template <bool VEC, bool GATE>
-constexpr int runs_of() { return VEC && !GATE ? 2 : 1; }
+// no gate comes with every row (its sums would not fit the registers).
+template <bool VEC, int GATE>
+constexpr int runs_of() { return VEC && GATE != 1 ? 2 : 1; }
 
-template <class TB, class TS, bool VEC, bool GATE>
+template <class TB, class TS, bool VEC, int GATE>
 int shape_v(const bf16opt_norm_gate_t *d, int sms, Shape &s) {
     constexpr int V = runs_of<VEC, GATE>();
     s.cluster = 1;
@@ -1005,13 +1108,20 @@ int shape_v(const bf16opt_norm_gate_t *d, int sms, Shape &s) {
     s.gate_floats = d->gate_rows && d->gate_rows != d->rows ? (uint64_t)s.teams * 2 * d->hidden : 0;
     return BF16OPT_OK;
 }
+// How the backward pass has the gate (k_norm_backward's GATE).
+int gate_kind(const bf16opt_norm_gate_t *d) {
+    return !d->gate ? 0 : d->rows / d->gate_rows < kGateRows ? 1 : 2;
+}
 template <class TB, class TS>
 int shape_t(const bf16opt_norm_gate_t *d, bool vec, int sms, Shape &s) {
-    if (vec) return d->gate ? shape_v<TB, TS, true, true>(d, sms, s) : shape_v<TB, TS, true, false>(d, sms, s);
-    return d->gate ? shape_v<TB, TS, false, true>(d, sms, s) : shape_v<TB, TS, false, false>(d, sms, s);
+    switch (gate_kind(d)) {
+    case 0: return vec ? shape_v<TB, TS, true, 0>(d, sms, s) : shape_v<TB, TS, false, 0>(d, sms, s);
+    case 1: return vec ? shape_v<TB, TS, true, 1>(d, sms, s) : shape_v<TB, TS, false, 1>(d, sms, s);
+    default: return vec ? shape_v<TB, TS, true, 2>(d, sms, s) : shape_v<TB, TS, false, 2>(d, sms, s);
+    }
 }
 
-template <class TB, class TS, bool VEC, bool GATE>
+template <class TB, class TS, bool VEC, int GATE>
 int backward_v(const Args &a, const BackArgs &q, const Shape &s, cudaStream_t st) {
     auto k = k_norm_backward<TB, TS, VEC, GATE, runs_of<VEC, GATE>()>;
     Launch l{s.teams * s.cluster, s.threads, s.smem, st, s.cluster, true};
@@ -1122,8 +1232,11 @@ int backward(const bf16opt_norm_gate_t *d, const void *dr, const void *dh, const
     rc = by_types(d, [&](auto bp, auto tp) {
         using TB = std::remove_pointer_t<decltype(bp)>;
         using TS = std::remove_pointer_t<decltype(tp)>;
-        if (vec) return d->gate ? backward_v<TB, TS, true, true>(a, q, s, st) : backward_v<TB, TS, true, false>(a, q, s, st);
-        return d->gate ? backward_v<TB, TS, false, true>(a, q, s, st) : backward_v<TB, TS, false, false>(a, q, s, st);
+        switch (gate_kind(d)) {
+        case 0: return vec ? backward_v<TB, TS, true, 0>(a, q, s, st) : backward_v<TB, TS, false, 0>(a, q, s, st);
+        case 1: return vec ? backward_v<TB, TS, true, 1>(a, q, s, st) : backward_v<TB, TS, false, 1>(a, q, s, st);
+        default: return vec ? backward_v<TB, TS, true, 2>(a, q, s, st) : backward_v<TB, TS, false, 2>(a, q, s, st);
+        }
     });
     if (rc != BF16OPT_OK || (!want && !q.shared_gate)) return rc;
     JoinArgs j;
@@ -1133,14 +1246,16 @@ int backward(const bf16opt_norm_gate_t *d, const void *dr, const void *dh, const
     j.dgate = q.shared_gate ? dgate : nullptr;
     j.rows = a.rows, j.gate_rows = a.gate_rows, j.rows_per_gate = a.rows_per_gate;
     j.teams = s.teams, j.hidden = a.hidden;
-    dim3 grid((a.hidden + 31) / 32, (unsigned)std::min<uint64_t>(4 + (j.dgate ? a.gate_rows : 0), 4096));
+    // four columns a lane where that leaves a block for every SM (14336 columns: 18 us against 6 us; 2048: 6 against 10)
+    const uint32_t width = a.hidden % 4 == 0 && a.hidden >= 32u * (unsigned)sms ? 4 : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid, cfg.blockDim = dim3(32 * kRuns), cfg.stream = st;
+    cfg.gridDim = dim3((a.hidden + 32 * width - 1) / (32 * width), (unsigned)std::min<uint64_t>(4 + (j.dgate ? a.gate_rows : 0), 4096));
+    cfg.blockDim = dim3(32 * kRuns), cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at, cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_norm_join, j);
+    const cudaError_t e = width == 4 ? cudaLaunchKernelEx(&cfg, k_norm_join<4>, j) : cudaLaunchKernelEx(&cfg, k_norm_join<1>, j);
     return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "norm_gate kernel launch");
 }
 

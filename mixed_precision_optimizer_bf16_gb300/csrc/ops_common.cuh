@@ -144,6 +144,15 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// Rows [team_row(p), team_row(p + 1)) of `rows` are team p's: floor(p rows / teams).
+__host__ __device__ inline uint64_t team_row(uint64_t rows, uint32_t teams, uint32_t p) {
+    return rows / teams * p + rows % teams * p / teams;
+}
+// The team of a row: the last p with p rows / teams < row + 1.  (rows < 2^40)
+__device__ __forceinline__ uint32_t team_of(uint64_t rows, uint32_t teams, uint64_t row) {
+    return (uint32_t)(((row + 1) * teams - 1) / rows);
+}
+
 // Programmatic dependent launch: pdl_enter waits for the prerequisite grids
 // before the first memory access; pdl_leave, at a CTA's end, lets the successor's CTAs be
 // scheduled once every CTA has come that far.  (Allowed at the start,
