@@ -430,7 +430,8 @@ int bf16opt_pipeline_timeouts(uint32_t *count);
  * in a CUDA graph.  Every pointer is device memory unless stated otherwise, aligned to its
  * element; rows may start anywhere (a row stride counts elements and is at
  * least the row's length).  16-byte aligned rows run fastest.  An output may
- * not overlap an input or another output except where stated.  Descriptors are
+ * not overlap an input or another output except where stated (what counts is the
+ * span from the first row's start to the last row's end).  Descriptors are
  * read during the call.  Results are deterministic: the same inputs give the
  * same bits, whatever runs beside them.  Errors are reported as by the calls
  * without a handle: INVALID_ARG, ALIGNMENT, UNSUPPORTED (no CUDA device) or

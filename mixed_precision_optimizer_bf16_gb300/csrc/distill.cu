@@ -2,18 +2,27 @@
 // (bf16opt_distill_* of include/bf16opt.h).
 //
 // A row's loss needs the log-sum-exp of its logits and its gradient needs the
-// logits again.  A cluster of CTAs takes a row: each CTA streams its slice of
-// the row once, keeping a running maximum and sum per thread, and leaves the
-// slice in its shared memory; the CTAs' sums meet through distributed shared
-// memory; then each CTA writes its slice's gradient from the copy it kept.  So
-// every logit is read from HBM once and every gradient written once, the least
-// the operator can do (4 bytes per bf16 logit).
+// logits again.  A cluster of CTAs (often of one) takes a row: each CTA streams its
+// slice of the row once, keeping a running maximum and sums per thread; the CTAs' sums meet
+// through distributed shared memory; then each CTA writes its slice's gradient,
+// from what it kept of the slice in shared memory and, for the rest, from L2.  Every logit is
+// so read from HBM about once and every gradient written once: 4 bytes per bf16
+// logit, which is what bounds the operator (with two temperatures, the
+// special-function unit comes next).
 //
 // The teacher's k entries of a row (and the label, as one more entry) are held
 // in shared memory by every CTA of the cluster.  Their softmax is computed by
 // each CTA by itself, and their part of the gradient is put on top of the
 // slice's: an entry's element is recomputed and stored again with everything
 // that its id collects, rounded once.
+//
+// Measured on one GB300 (algorithmic bytes over the time; a copy of the same
+// buffers runs at 6.75 TB/s): 2048 rows of 250880 bf16 logits with 64 entries and
+// labels, T = 2, loss and gradient 410 us, 4.9 TB/s; 1024 such rows forward 91 us,
+// 5.6 TB/s, backward 171 us, 6.0 TB/s; 8192 rows of 32000 forward 103 us, 5.1 TB/s,
+// backward 173 us, 6.0 TB/s, loss and gradient 221 us, 4.7 TB/s. The two-pass kernel is
+// bound by issue (68 % of the slots) and by re-reads that miss L2 (17 % more DRAM bytes
+// than the operator needs at 250880); small rows by the latency of a row's reductions.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -25,29 +34,17 @@ namespace cg = cooperative_groups;
 namespace bf16ops {
 namespace {
 
-#ifndef BF16K_DISTILL_U
-#define BF16K_DISTILL_U 4
-#endif
-#ifndef BF16K_DISTILL_SMALL
-#define BF16K_DISTILL_SMALL 192
-#endif
-#ifndef BF16K_DISTILL_LARGE
-#define BF16K_DISTILL_LARGE 256
-#endif
-constexpr int kU = BF16K_DISTILL_U;   // vectors of a thread in a group
+// Vectors of a thread in a group of the ring.  8 gave 220 against 231 us at T = 1.5 on 1024 x
+// 250880, but 317 against 226 us on 8192 x 32000 (a row is then less than two groups).
+constexpr int kU = 4;
 constexpr int kMaxCluster = 8;
-constexpr int kSmall = BF16K_DISTILL_SMALL, kLarge = BF16K_DISTILL_LARGE;   // threads of a CTA
-#ifndef BF16K_DISTILL_LIMIT
-#define BF16K_DISTILL_LIMIT 5000
-#endif
-#ifndef BF16K_DISTILL_RES_SMALL
-#define BF16K_DISTILL_RES_SMALL 4
-#endif
-#ifndef BF16K_DISTILL_RES_LARGE
-#define BF16K_DISTILL_RES_LARGE 2
-#endif
-// CTAs of an SM, and groups in the ring of each, by their threads.
-__host__ __device__ constexpr int resident(int threads) { return threads == kLarge ? BF16K_DISTILL_RES_LARGE : BF16K_DISTILL_RES_SMALL; }
+// Threads of a CTA: of the kernels with one pass, and with both where rows are short (up to
+// kShortRow vectors); and with both where they are long, which wants more than 80 registers:
+// 1024 x 250880 took 256 us with 384 threads at 80 registers, 214 us so.
+constexpr int kSmall = 192, kLarge = 256;
+constexpr uint64_t kShortRow = 5000;
+// CTAs of an SM, and groups in the ring of each, by their threads: 200 KB of an SM are rings.
+__host__ __device__ constexpr int resident(int threads) { return threads == kLarge ? 2 : 4; }
 __host__ __device__ constexpr int ring_depth(int threads) { return 200 * 1024 / resident(threads) / (threads * kU * 16); }
 // Entries of one thread, the label's included.
 __host__ __device__ constexpr int entries(int threads) { return (BF16OPT_DISTILL_MAX_K + threads) / threads; }
@@ -357,9 +354,13 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
         copy_wait_for(issued - 1 - seen);
         const uint4 *from = ring + slot * kGroup + tid;
         const bool full = (i + 1) * kGroup <= nv;
+        if (full) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
-            q[u] = full || i * kGroup + u * kThreads + tid < nv ? from[u * kThreads] : nothing<T>();
+            for (int u = 0; u < kU; ++u) q[u] = from[u * kThreads];
+        } else {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) q[u] = i * kGroup + u * kThreads + tid < nv ? from[u * kThreads] : nothing<T>();
+        }
         ++seen;
         slot = slot + 1 == depth ? 0 : slot + 1;
     };
@@ -715,12 +716,12 @@ int launch_k(const Args &a, unsigned cluster, cudaStream_t stream) {
     const size_t smem = (size_t)ring_depth(kThreads) * kThreads * kU * 16 + (size_t)(a.k + 1) * 12 + (GRAD ? table_size(a.k) * 4 : 0);
     // As many clusters as fit at once (a cluster of eight cannot use every SM: those of a
     // processing cluster are not a multiple of it), each walking its rows; more would run as a
-    // second wave: 57 clusters where 51 fit took 639 us on 2048 rows of 250880 bf16.
+    // second wave: 57 clusters of eight where 51 fit took 639 us on 2048 rows of 250880 bf16, 51 took 469.
     Launch l{cluster, (unsigned)kThreads, smem, stream, cluster, true};
     int fit = 0;
     const cudaError_t eo = clusters_that_fit(l, k, fit);
     if (eo != cudaSuccess) return fail_cuda(eo, "distill occupancy");
-    // in equal shares: with 512 rows, 47 clusters of at most 11 rows instead of 51
+    // in equal shares: 512 rows on 51 clusters would be 11 rows for some, so 47 do
     const uint64_t turns = (a.rows + fit - 1) / fit;
     l.grid = (unsigned)((a.rows + turns - 1) / turns) * cluster;
     const cudaError_t e = launch(l, k, a);
@@ -731,14 +732,18 @@ template <class T, bool FORWARD, bool GRAD>
 int launch_t(const Args &a, int power, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "distill: no CUDA device");
-    // CTAs per row: so many that the rows in flight, but for what the rings hold of
-    // them, take less than half of L2; and, with few rows, so many that the SMs are used.
+    // CTAs per row.  With both passes: a slice of at most three rings, so that what is read again is
+    // still in L2 (two rings 444 us, three 411 us, six 470 us on 2048 x 250880). The backward pass:
+    // slices of at most 8192 vectors, since fewer rows at a time read and write closer together
+    // (1024 x 250880: 189 us with a CTA per row, 171 us with four; the forward pass does not care).
+    // With few rows: so many that the SMs are used.
     constexpr bool kBoth = FORWARD && GRAD;
     const uint64_t vecs = a.vocab / Vec<T>::N + 1;
-    const bool large = kBoth && vecs > BF16K_DISTILL_LIMIT;
+    const bool large = kBoth && vecs > kShortRow;
     const uint64_t ring = large ? (uint64_t)ring_depth(kLarge) * kU * kLarge : (uint64_t)ring_depth(kSmall) * kU * kSmall;
     unsigned cluster = 1;
     while (cluster < kMaxCluster && ((kBoth && vecs / cluster > ring * 3) ||
+                                     (!FORWARD && vecs / cluster > 8192) ||
                                      (a.rows * cluster <= (uint64_t)sms && vecs / cluster > 4 * kSmall)))
         cluster *= 2;
     auto go = [&](auto p) {
