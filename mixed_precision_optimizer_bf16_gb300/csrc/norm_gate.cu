@@ -452,11 +452,11 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 384, V == 4 ? 1 : 2) k_norm_for
 
 // ----------------------------------------------------------------------- backward
 
-// Columns of one CTA at most, so that two of 224 threads with 16 columns fit an
-// SM's registers (146 a thread).  With 8 columns a thread, what a row costs a warp
+// Threads of a CTA at most, and with them the columns: 448 threads of 128 registers, each
+// with one or two runs of eight columns.  With 8 columns a thread, what a row costs a warp
 // apart from its columns (the two reductions, addresses, copies) was as much as the
-// columns: 608 instructions a row of 8, 282 us on 4096 x 14336.
-constexpr int kColumns = 3584;
+// columns: 608 instructions a row of 8, 282 us on 4096 x 14336, against 217 us with 16.
+constexpr int kBackThreads = 448;
 constexpr int kSums = 8;         // per row
 
 struct BackArgs {
@@ -523,7 +523,7 @@ __host__ __device__ constexpr int ring_units() {
 // There the row after the last is published only when the gate has changed.
 constexpr uint64_t kGateRows = 8;
 template <class TB, class TS, bool VEC, int GATE, int V>
-__global__ void __launch_bounds__(kColumns / 8 / V, V) k_norm_backward(const Args a, const BackArgs q, uint32_t depth) {
+__global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a, const BackArgs q, uint32_t depth) {
     constexpr int UNITS = ring_units<TB, TS, GATE>(), UB = sizeof(TB) / 2, US = sizeof(TS) / 2;
     extern __shared__ __align__(16) unsigned char ring_raw[];
     cg::cluster_group cluster = cg::this_cluster();
@@ -1090,12 +1090,16 @@ constexpr int runs_of() { return VEC && GATE != 1 ? 2 : 1; }
 template <class TB, class TS, bool VEC, int GATE>
 int shape_v(const bf16opt_norm_gate_t *d, int sms, Shape &s) {
     constexpr int V = runs_of<VEC, GATE>();
-    s.cluster = 1;
-    while (s.cluster * kColumns < d->hidden) s.cluster *= 2;
-    const uint32_t cols = (d->hidden + s.cluster - 1) / s.cluster;
-    s.threads = ((cols + 8 * V - 1) / (8 * V) + 31) / 32 * 32;
+    // CTAs that share the columns: so many that a CTA's fit its threads, and two rows of them its ring
+    size_t row = 0, sums = 0;
+    for (s.cluster = 1;; s.cluster *= 2) {
+        const uint32_t cols = (d->hidden + s.cluster - 1) / s.cluster;
+        s.threads = ((cols + 8 * V - 1) / (8 * V) + 31) / 32 * 32;
+        row = (size_t)s.threads * V * ring_units<TB, TS, GATE>() * 16;
+        sums = 3 * s.cluster * s.threads / 32 * kSums * sizeof(float);
+        if (s.threads <= (uint32_t)kBackThreads && (!VEC || 2 * row + sums <= kMaxDynamic)) break;
+    }
     const unsigned per_sm = std::max(1u, std::min(512u / s.threads, 16u));   // 128 registers a thread
-    const size_t row = (size_t)s.threads * V * ring_units<TB, TS, GATE>() * 16, sums = 3 * s.cluster * s.threads / 32 * kSums * sizeof(float);
     s.depth = VEC ? (uint32_t)std::max<size_t>(2, std::min<size_t>(8, ring_bytes(per_sm, sums) / row)) : 2;
     s.smem = (VEC ? s.depth * row : 0) + sums;
     int fit = 0;
