@@ -789,7 +789,6 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a,
     publish(row0, 0, gate, st, 0);
     if (ranks > 1) cluster_arrive();
     for (uint64_t row = row0; row < row1; ++row) {
-        const float4 st2 = stats_of(row + 2);
         const uint32_t at1 = sums_next(sums_at);
         if (ranks > 1) cluster_wait();
         else __syncthreads();
@@ -805,6 +804,9 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a,
             if (ranks > 1) cluster_arrive();
         };
         if (!gate_over) publish_next();
+        // after the arrival: the release before it waits for loads on their way (205 against 181 us on
+        // 4096 x 14336 with these loads at the row's start)
+        const float4 st2 = stats_of(row + 2);
 
         float s[kSums];
         totals(sums_at, s);
