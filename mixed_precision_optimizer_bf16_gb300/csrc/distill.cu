@@ -18,9 +18,9 @@
 //
 // Measured on one GB300 (algorithmic bytes over the time; a copy of the same
 // buffers runs at 6.75 TB/s): 2048 rows of 250880 bf16 logits with 64 entries and
-// labels, T = 2, loss and gradient 410 us, 4.9 TB/s; 1024 such rows forward 91 us,
-// 5.6 TB/s, backward 171 us, 6.0 TB/s; 8192 rows of 32000 forward 103 us, 5.1 TB/s,
-// backward 173 us, 6.0 TB/s, loss and gradient 221 us, 4.7 TB/s. The two-pass kernel is
+// labels, T = 2, loss and gradient 415 us, 5.0 TB/s; 1024 such rows forward 88 us,
+// 5.8 TB/s, backward 172 us, 6.0 TB/s; 8192 rows of 32000 forward 109 us, 4.8 TB/s,
+// backward 174 us, 6.0 TB/s, loss and gradient 208 us, 5.0 TB/s. The two-pass kernel is
 // bound by issue (68 % of the slots) and by re-reads that miss L2 (17 % more DRAM bytes
 // than the operator needs at 250880); small rows by the latency of a row's reductions.
 #include <cooperative_groups.h>
@@ -77,9 +77,10 @@ struct Args {
 struct Stat {
     float m, st, s1;
 };
-// The teacher's: maximum of x = t / T, sum e of exp(x - max), sum of e (x - z / T).
+// The teacher's: maximum m of x = t / T, sum s of e = exp(x - m), sum d of e ((x - m) - (z - b) / T),
+// b the largest finite z: both taken from their largest, so that logits far from 0 cost no digits.
 struct Teach {
-    float m, s, d;
+    float m, b, s, d;
 };
 
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.f : m; }
@@ -97,16 +98,6 @@ __device__ __forceinline__ Stat join(const Stat &a, const Stat &b, float c_t) {
     r.s1 = POWER ? weighted(a.s1, ex2((a.m - m) * kLog2e), b.s1, ex2((b.m - m) * kLog2e)) : 0.f;
     return r;
 }
-__device__ __forceinline__ Teach join(const Teach &a, const Teach &b) {
-    Teach r;
-    r.m = fmaxf(a.m, b.m);
-    const float m = safe_max(r.m);
-    const float ea = ex2((a.m - m) * kLog2e), eb = ex2((b.m - m) * kLog2e);
-    r.s = weighted(a.s, ea, b.s, eb);
-    // a d of +inf (masked z) may meet a weight of 0
-    r.d = weighted(ea > 0.f ? a.d : 0.f, ea, eb > 0.f ? b.d : 0.f, eb);
-    return r;
-}
 // Joined over the warp: first the maximum, then the sums scaled to it, so that
 // a step is a shuffle and one operation; every lane gets the same bits.
 template <int POWER>
@@ -118,12 +109,14 @@ __device__ __forceinline__ Stat warp_join(const Stat &a, float c_t) {
     r.s1 = POWER ? warp_sum(a.s1 * ex2(d * kLog2e)) : 0.f;
     return r;
 }
-__device__ __forceinline__ Teach warp_join(const Teach &a) {
+__device__ __forceinline__ Teach warp_join(const Teach &a, float inv_t) {
     Teach r;
     r.m = warp_max(a.m);
-    const float e = ex2((a.m - safe_max(r.m)) * kLog2e);
+    r.b = warp_max(a.b);
+    const float x = a.m - safe_max(r.m), e = ex2(x * kLog2e);
     r.s = warp_sum(a.s * e);
-    r.d = warp_sum(e > 0.f ? a.d * e : 0.f);
+    // a d of +inf (masked z) may meet a weight of 0
+    r.d = warp_sum(e > 0.f ? e * (a.d + a.s * (x - (safe_max(a.b) - safe_max(r.b)) * inv_t)) : 0.f);
     return r;
 }
 
@@ -133,6 +126,11 @@ __device__ __forceinline__ float2 powered(float2 e) {
     const float2 q = mul2(e, e);
     return POWER == 4 ? mul2(q, q) : q;
 }
+
+// The exponents (z - m) c of a softmax in base 2.  The difference is formed first: exact near the top,
+// wherever the row lies.  (As z c - m c in one instruction the rounded product is off in every term,
+// 2e-6 of a loss at m = 20, overflows where the logits are the type's lowest, and no call was faster.)
+__device__ __forceinline__ float2 exponent(float2 z, float m, float c) { return mul2(add2(z, both(-m)), both(c)); }
 
 // A vector's elements as pairs.
 template <class T>
@@ -230,9 +228,10 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
     constexpr int N = Vec<T>::N, P = N / 2;
     constexpr uint32_t kGroup = kThreads * kU, depth = ring_depth(kThreads);
     constexpr int kWarps = kThreads / 32, kEntries = entries(kThreads);
-    constexpr bool kExact = sizeof(T) == 4;   // FP32 logits: z - base is formed before it is scaled
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    // slice | ids, x (then what the entry takes off the gradient), z of the entries
+    // 128 bytes: a ring that begins elsewhere splits every wavefront (1024 x 250880 forward, 80 bytes
+    // off: 108 against 88 us)
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    // ring | ids, x (then what the entry takes off the gradient), z of the entries
     uint4 *ring = reinterpret_cast<uint4 *>(smem_raw);
     int32_t *sm_id = reinterpret_cast<int32_t *>(smem_raw + (size_t)depth * kGroup * 16);
     float *sm_x = reinterpret_cast<float *>(sm_id + (a.k + 1));
@@ -408,26 +407,23 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
                 uint4 q[kU];
                 take(q, i, nv);
                 const float mx = largest<T, kU>(q);
-                if (mx > st.m) {
-                    const float m = safe_max(st.m);
-                    sum_t = mul2(sum_t, both(ex2((m - mx) * c_t)));
-                    if (POWER) sum_1 = mul2(sum_1, both(ex2((m - mx) * kLog2e)));
+                if (mx > st.m) {   // the sums move to the new maximum (the first time from -inf: by 0)
+                    sum_t = mul2(sum_t, both(ex2((st.m - mx) * c_t)));
+                    if (POWER) sum_1 = mul2(sum_1, both(ex2((st.m - mx) * kLog2e)));
                     st.m = mx;
                 }
                 const float m = safe_max(st.m);
-                const float2 neg = both(kExact ? -m : -(m * c_t)), neg1 = both(kExact ? -m : -(m * kLog2e));
-                const float2 ct2 = both(c_t), c12 = both(kLog2e);
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
                     float2 f[P];
                     pairs<T>(q[u], f);
 #pragma unroll
                     for (int i = 0; i < P; ++i) {
-                        const float2 d = kExact ? mul2(add2(f[i], neg), ct2) : fma2(f[i], ct2, neg);
+                        const float2 d = exponent(f[i], m, c_t);
                         const float2 e = make_float2(ex2(d.x), ex2(d.y));
                         sum_t = add2(sum_t, e);
                         if (POWER == 1) {
-                            const float2 d1 = kExact ? mul2(add2(f[i], neg1), c12) : fma2(f[i], c12, neg1);
+                            const float2 d1 = exponent(f[i], m, kLog2e);
                             sum_1 = add2(sum_1, make_float2(ex2(d1.x), ex2(d1.y)));
                         } else if (POWER > 1) {
                             sum_1 = add2(sum_1, powered<POWER>(e));
@@ -449,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
         }
 
         // ---- the entries' softmax
-        Teach te = {-INFINITY, 0.f, 0.f};
+        Teach te = {-INFINITY, -INFINITY, 0.f, 0.f};
         uint32_t slots[kEntries];   // where this thread's entries stand in the table
 #pragma unroll
         for (int i = 0; i < kEntries; ++i) slots[i] = 0xffffffffu;
@@ -477,8 +473,8 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
             const float zi = i == 0 ? entry_z : there ? to_f32(z[id]) : 0.f;
             sm_id[e] = id, sm_x[e] = x, sm_z[e] = zi;
             if (there) {
-                const Teach one = {x, 1.f, x - zi * a.inv_t};
-                te = i == 0 ? one : join(te, one);
+                te.m = fmaxf(te.m, x);
+                if (fabsf(zi) < INFINITY) te.b = fmaxf(te.b, zi);
             }
             slots[i] = enter(id);
         }
@@ -503,7 +499,13 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
         // ---- joined over the warp, and the warps of the cluster (CTA) in one step
         const uint32_t teach_warps = min((uint32_t)kWarps, (a.k + 31) / 32);
         if (warp < teach_warps) {   // (both, so that their shuffles run side by side)
-            te = warp_join(te);
+            te.m = warp_max(te.m), te.b = warp_max(te.b);
+            for (uint32_t i = tid; i < a.k; i += kThreads) {   // its own entries
+                const float x = sm_x[i] - safe_max(te.m), e = sm_id[i] < 0 ? 0.f : ex2(x * kLog2e);
+                te.s += e;
+                if (!(e <= 0.f)) te.d += e * (x - (sm_z[i] - safe_max(te.b)) * a.inv_t);
+            }
+            te.s = warp_sum(te.s), te.d = warp_sum(te.d);
             if (FORWARD) st = warp_join<POWER>(st, c_t);
             if (lane == 0) sm_teach[turn & 1][warp] = te;
         } else if (FORWARD) {
@@ -525,11 +527,11 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
 #pragma unroll
         for (int i = 0; i < kEntries; ++i)
             if (slots[i] != 0xffffffffu) sm_table[slots[i]] = -1;   // everybody's are in: for the next row
-        te = lane < teach_warps ? sm_teach[turn & 1][lane] : Teach{-INFINITY, 0.f, 0.f};
-        te = warp_join(te);
-        float lse_t, lse_1;
+        te = lane < teach_warps ? sm_teach[turn & 1][lane] : Teach{-INFINITY, -INFINITY, 0.f, 0.f};
+        te = warp_join(te, a.inv_t);
+        float lse_t, lse_1, log_t, log_1;   // lse_t = m / T + log_t, lse_1 = m + log_1
         bool empty;   // no logit but -inf in the row
-        // q = exp2((z - base_t) c_t + rest_t): the base near the row's top, so that z - base is exact there
+        // q = exp2((z - base_t) c_t) exp2(rest_t): the base near the row's top, so that z - base is exact there
         float base_t, rest_t, base_1, rest_1;
         if (FORWARD) {
             st = lane < ranks * kWarps ? sm_stat[turn & 1][lane] : Stat{-INFINITY, 0.f, 0.f};
@@ -537,8 +539,10 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
             st = warp_join<POWER>(st, c_t);
             const float m = safe_max(st.m);
             empty = st.m == -INFINITY && st.st == 0.f;
-            lse_t = empty ? -INFINITY : m * a.inv_t + logf(st.st);
-            lse_1 = empty ? -INFINITY : (POWER ? m + logf(st.s1) : lse_t);
+            log_t = logf(st.st);
+            log_1 = POWER ? logf(st.s1) : log_t;
+            lse_t = empty ? -INFINITY : m * a.inv_t + log_t;
+            lse_1 = empty ? -INFINITY : (POWER ? m + log_1 : lse_t);
             base_t = base_1 = m;
             rest_t = empty ? 0.f : -log2f(st.st);
             rest_1 = POWER && !empty ? -log2f(st.s1) : 0.f;
@@ -554,15 +558,17 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
 
         // ---- the row's loss
         const bool some = te.s != 0.f;   // the teacher has entries here (NaN counts)
-        const float lse_teacher = a.teacher_lse ? now.teacher_lse : te.m + logf(te.s);
-        const float mass = !some ? 0.f : a.teacher_lse ? te.s * ex2((te.m - lse_teacher) * kLog2e) : te.s == te.s ? 1.f : te.s;
+        const float log_teacher = a.teacher_lse ? now.teacher_lse - te.m : logf(te.s);   // the lse less te.m
+        const float mass = !some ? 0.f : a.teacher_lse ? te.s * ex2(-log_teacher * kLog2e) : te.s == te.s ? 1.f : te.s;
         const bool has_label = sm_label[turn & 1] >= 0;
         now = then;
         if (FORWARD && rank == 0 && tid == 0) {
             float kl = 0.f, ce = 0.f;
             if (some && a.kl_weight != 0.f && mass != 0.f)
-                kl = empty ? INFINITY : a.kl_weight * a.temperature * a.temperature * mass * (te.d / te.s + (lse_t - lse_teacher));
-            if (has_label) ce = empty ? INFINITY : a.ce_weight * (lse_1 - sm_label_z[turn & 1]);
+                kl = empty ? INFINITY
+                           : a.kl_weight * a.temperature * a.temperature * mass *
+                                 (te.d / te.s + ((base_t - safe_max(te.b)) * a.inv_t + log_t) - log_teacher);
+            if (has_label) ce = empty ? INFINITY : a.ce_weight * ((base_t - sm_label_z[turn & 1]) + log_1);
             a.loss[row] = wr * (kl + ce);
             if (a.lse_out) a.lse_out[2 * row] = lse_t, a.lse_out[2 * row + 1] = lse_1;
         }
@@ -574,22 +580,20 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
         // ---- the gradient of the slice
         const float hard = has_label ? up * a.ce_weight : 0.f;
         const float soft = up * a.kl_weight * a.temperature;
-        float a_t = soft * mass, a_1 = hard;
-        if (!POWER) a_t += hard, a_1 = 0.f;   // both terms have the same softmax
         // T = POWER: exp2((z - base_1) log2e + rest_1) = e^POWER exp2(shift), e the value at T; e <= 1 and the
-        // factor stays with a_1 (where a factor overflows, the top's own e is as small as the factor is large)
-        const float shift = POWER > 1 ? ((base_t - base_1) * kLog2e + (rest_1 - (float)POWER * rest_t)) : 0.f;
-        const float a_p = POWER > 1 ? a_1 * ex2(shift) : 0.f;
-        const float off_t = fmaf(-base_t, c_t, rest_t), off_1 = fmaf(-base_1, kLog2e, rest_1);
+        // factor stays with it (where a factor overflows, the top's own e is as small as the factor is large)
+        const float shift = POWER > 1 ? (base_t - base_1) * kLog2e + rest_1 : rest_1;
+        // both terms have the same softmax where POWER is 0
+        const float a_t = (soft * mass + (POWER ? 0.f : hard)) * ex2(rest_t), a_1 = POWER ? hard * ex2(shift) : 0.f;
         auto grad2 = [&](float2 f) {
-            const float2 d = kExact ? fma2(add2(f, both(-base_t)), both(c_t), both(rest_t)) : fma2(f, both(c_t), both(off_t));
+            const float2 d = exponent(f, base_t, c_t);
             const float2 e = make_float2(ex2(d.x), ex2(d.y));
             float2 g = mul2(both(a_t), e);
             if (POWER == 1) {
-                const float2 d1 = kExact ? fma2(add2(f, both(-base_1)), both(kLog2e), both(rest_1)) : fma2(f, both(kLog2e), both(off_1));
+                const float2 d1 = exponent(f, base_1, kLog2e);
                 g = fma2(both(a_1), make_float2(ex2(d1.x), ex2(d1.y)), g);
             } else if (POWER > 1) {
-                g = fma2(both(a_p), powered<POWER>(e), g);
+                g = fma2(both(a_1), powered<POWER>(e), g);
             }
             return g;
         };
@@ -636,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
         // ---- the entries of the slice
         const bool twice = sm_twice[turn & 1] == turn;
         ++turn;
-        for (uint32_t e = tid; e < a.k; e += kThreads) sm_x[e] = soft * ex2((sm_x[e] - lse_teacher) * kLog2e);
+        for (uint32_t e = tid; e < a.k; e += kThreads) sm_x[e] = soft * ex2(((sm_x[e] - te.m) - log_teacher) * kLog2e);
         if (tid == kThreads - 1) sm_x[a.k] = hard;
         __syncthreads();   // the slice's gradient is stored, the entries' parts are there
         auto put = [&](uint32_t e) {

@@ -310,7 +310,7 @@ k_norm_forward(const Args a, const TS *x, const TB *y, TS *r, TB *h, float *stat
 template <class TB, class TS, bool GATE, int V>
 __global__ void __launch_bounds__(V == 4 ? 512 : 384, V == 4 ? 1 : 2) k_norm_forward_ring(const Args a, const TS *x, const TB *y, TS *r, TB *h, float *stats, uint32_t depth) {
     constexpr int UB = sizeof(TB) / 2, US = sizeof(TS) / 2, UNITS = (GATE ? 2 : 1) * UB + US;   // y, x, [gate]
-    extern __shared__ __align__(16) unsigned char ring_raw[];
+    extern __shared__ __align__(128) unsigned char ring_raw[];
     __shared__ float buf[64];
     const uint32_t threads = blockDim.x, t = threadIdx.x, n = a.hidden;
     auto col = [&](int v) { return (v * threads + t) * 8; };
@@ -525,7 +525,7 @@ constexpr uint64_t kGateRows = 8;
 template <class TB, class TS, bool VEC, int GATE, int V>
 __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a, const BackArgs q, uint32_t depth) {
     constexpr int UNITS = ring_units<TB, TS, GATE>(), UB = sizeof(TB) / 2, US = sizeof(TS) / 2;
-    extern __shared__ __align__(16) unsigned char ring_raw[];
+    extern __shared__ __align__(128) unsigned char ring_raw[];
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const uint32_t threads = blockDim.x, t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = threads / 32;
