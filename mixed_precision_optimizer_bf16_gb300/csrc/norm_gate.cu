@@ -152,6 +152,35 @@ __device__ __forceinline__ Cols unpack8(const uint4 *p, uint32_t stride) {
     }
     return c;
 }
+// The same from a place between two 16-byte boundaries: p holds the vectors from the boundary before on, one
+// more than the columns fill, `mis` is how many bytes of the first come before the columns.
+template <class T>
+__device__ __forceinline__ Cols unpack8_shifted(const uint4 *p, uint32_t stride, uint32_t mis) {
+    constexpr int NW = sizeof(T) == 2 ? 8 : 12, N = sizeof(T) == 2 ? 5 : 8;   // words there, words needed
+    uint32_t w[NW];
+#pragma unroll
+    for (int i = 0; i < NW / 4; ++i) {
+        const uint4 q = p[i * stride];
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+    }
+#pragma unroll
+    for (int i = 0; i <= N; ++i) w[i] = mis & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = mis & 4 ? w[i + 1] : w[i];
+    Cols c;
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t pick = mis & 2 ? 0x5432u : 0x3210u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = __byte_perm(w[i], w[i + 1], pick);
+            c.v[i] = make_float2(bf16_lo(x), bf16_hi(x));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c.v[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+    return c;
+}
 __device__ __forceinline__ Cols all8(float x) {
     Cols c;
 #pragma unroll
@@ -196,6 +225,59 @@ __device__ __forceinline__ void store_cols(T *row, uint32_t c, uint32_t n, const
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (c + i < n) from_f32(row[c + i], f[i]);
+    }
+}
+// Eight columns of a row on a 16-byte boundary; VEC: all of them there or none.
+template <bool VEC, class T>
+__device__ __forceinline__ void store_cols_ended(T *row, uint32_t c, uint32_t n, const Cols &x) {
+    if (VEC || c + 8 <= n) store_cols<true>(row, c, n, x);
+    else store_cols<false>(row, c, n, x);
+}
+// Eight columns from c on, c a multiple of eight that grows by eight from lane to lane, of a row that begins
+// between two 16-byte boundaries: a lane stores the vectors that its columns begin in, together with the lane
+// before, whose last columns it gets by a shuffle; the columns at a warp's and the row's ends go one by one.
+// Every lane of the warp calls it.
+template <class T>
+__device__ __forceinline__ void store_cols_shifted(T *row, uint32_t c, uint32_t n, const Cols &x, uint32_t lane) {
+    constexpr int NW = sizeof(T) == 2 ? 4 : 8, BEFORE = sizeof(T) == 2 ? 4 : 3;
+    const float f[8] = {x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y, x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y};
+    uint32_t w[BEFORE + NW + 1];   // the last words of the lane before, this lane's
+    if constexpr (sizeof(T) == 2) {
+        const uint4 q = Vec<T>::pack(f);
+        w[4] = q.x, w[5] = q.y, w[6] = q.z, w[7] = q.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[3 + i] = __float_as_uint(f[i]);
+    }
+    w[BEFORE + NW] = 0u;
+#pragma unroll
+    for (int i = 0; i < BEFORE; ++i) w[i] = __shfl_up_sync(0xffffffffu, w[NW + i], 1);
+    const uint32_t mis = (uint32_t)(uintptr_t)row & 15u, ends = 8 - mis / (uint32_t)sizeof(T);   // columns [ends, 8) are the next lane's to store
+    const bool mine = lane != 0 && c + 8 <= n, next = lane != 31 && c + 16 <= n;
+    if (!mine || !next) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < n && !(i < (int)ends ? mine : next)) from_f32(row[c + i], f[i]);
+    }
+    const uint32_t back = BEFORE * 4 - mis;   // where in w the vectors begin, in bytes
+    if constexpr (sizeof(T) == 2) {           // 2 .. 14: mis is not 0
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = back & 8 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = back & 4 ? w[i + 1] : w[i];
+        const uint32_t pick = back & 2 ? 0x5432u : 0x3210u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __byte_perm(w[i], w[i + 1], pick);
+    } else {                                  // 0, 4, 8
+#pragma unroll
+        for (int i = 0; i < 9; ++i) w[i] = back & 8 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = back & 4 ? w[i + 1] : w[i];
+    }
+    if (mine) {
+        uint4 *to = reinterpret_cast<uint4 *>(reinterpret_cast<char *>(row + c) - mis);
+        __stcs(to, make_uint4(w[0], w[1], w[2], w[3]));
+        if constexpr (sizeof(T) == 4) __stcs(to + 1, make_uint4(w[4], w[5], w[6], w[7]));
     }
 }
 __device__ __forceinline__ float2 sigmoid2(float2 x) { return make_float2(sigmoid(x.x), sigmoid(x.y)); }
@@ -452,6 +534,51 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 384, V == 4 ? 1 : 2) k_norm_for
 
 // ----------------------------------------------------------------------- backward
 
+// 16-byte units of eight columns in the ring: one more where they lie between boundaries.
+template <class T, bool VEC>
+__host__ __device__ constexpr int units() {
+    return (int)sizeof(T) / 2 + (VEC ? 0 : 1);
+}
+// A thread's eight columns into its units, `stride` apart: columns c on of the row's n from element `off` on
+// of a tensor of `size`.  Not VEC: the vectors from the boundary before to the one after, the
+// columns' own elements alone at the tensor's ends.
+template <bool VEC, class E>
+__device__ __forceinline__ void copy_run(uint4 *to, uint32_t stride, const E *tensor, uint64_t off, uint32_t c, uint32_t n, uint64_t size) {
+    const uintptr_t from = VEC ? (uintptr_t)(tensor + off + c) : (uintptr_t)(tensor + off + c) & ~(uintptr_t)15;
+    if (VEC || (off >= 16 && off + n + 32 <= size)) {
+#pragma unroll
+        for (int i = 0; i < units<E, VEC>(); ++i) copy_async16(to + i * stride, reinterpret_cast<const uint4 *>(from) + i);
+    } else {
+        constexpr uint32_t PER = 16 / sizeof(E);
+        for (uint32_t e = 0; e < units<E, VEC>() * PER; ++e) {
+            const uintptr_t p = from + e * sizeof(E);
+            if (p >= (uintptr_t)tensor && p < (uintptr_t)(tensor + size))
+                reinterpret_cast<E *>(to + e / PER * stride)[e % PER] = *reinterpret_cast<const E *>(p);
+        }
+    }
+}
+// And out of them again; 0 beyond the row.
+__device__ __forceinline__ void end_row(Cols &x, uint32_t c, uint32_t n) {
+    if (c + 8 <= n) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (c + 2 * i >= n) x.v[i].x = 0.f;
+        if (c + 2 * i + 1 >= n) x.v[i].y = 0.f;
+    }
+}
+template <bool VEC, class E>
+__device__ __forceinline__ Cols read_run(const uint4 *from, uint32_t stride, const E *tensor, uint64_t off, uint32_t c, uint32_t n) {
+    if constexpr (VEC) return unpack8<E>(from, stride);
+    Cols x = unpack8_shifted<E>(from, stride, (uint32_t)(uintptr_t)(tensor + off) & 15u);
+    end_row(x, c, n);
+    return x;
+}
+template <bool VEC, class E>
+__device__ __forceinline__ void store_run(E *row, uint32_t c, uint32_t n, const Cols &x, uint32_t lane) {   // by the whole warp
+    if (VEC || ((uintptr_t)row & 15u) == 0) store_cols_ended<VEC>(row, c, n, x);
+    else store_cols_shifted(row, c, n, x, lane);
+}
+
 // Threads of a CTA at most, and with them the columns: 448 threads of 128 registers, each
 // with one or two runs of eight columns.  With 8 columns a thread, what a row costs a warp
 // apart from its columns (the two reductions, addresses, copies) was as much as the
@@ -473,7 +600,7 @@ struct BackArgs {
 
 // Sum of eight values over a warp: each step a lane keeps half of the values
 // and hands the other half over, so it costs 9 shuffles, not 40.  Lane l ends up
-// with the sum of value (l & 7) reversed in bits -- see lane_value.
+// with the sum of value lane_value(l & 7): its bits reversed.
 __device__ __forceinline__ float warp_sum8(const float (&s)[8], uint32_t lane) {
     float a[4], b[2], c;
 #pragma unroll
@@ -503,10 +630,10 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // 16-byte units of eight columns of a row that a thread keeps in the ring: y, dh, [gate] of the
-// branch's type, r, dr of the stream's.
-template <class TB, class TS, int GATE>
+// branch's type, r, dr of the stream's; not VEC: the eight columns lie between boundaries, in one more.
+template <class TB, class TS, bool VEC, int GATE>
 __host__ __device__ constexpr int ring_units() {
-    return (GATE == 1 ? 3 : 2) * (int)sizeof(TB) / 2 + 2 * (int)sizeof(TS) / 2;
+    return (GATE == 1 ? 3 : 2) * units<TB, VEC>() + 2 * units<TS, VEC>();
 }
 
 // A team (a CTA, or a cluster that shares the columns) walks down its rows in two
@@ -514,8 +641,9 @@ __host__ __device__ constexpr int ring_units() {
 // row k are still on their way, then row k's outputs are written.  The rows
 // come through a ring in shared memory whose slots belong to one thread each, filled
 // by asynchronous copies `depth` rows ahead.  A thread has V runs of eight columns,
-// `threads` runs apart.  VEC: rows of whole 16-byte vectors; else elements are
-// loaded one by one, twice, and there is no ring.
+// `threads` runs apart.  VEC: rows of whole 16-byte vectors; else a run lies between
+// boundaries: it is copied with one more vector, and shifted into place when it is read
+// (element by element, twice from L1: 8192 x 4097 bf16 585 us, so 282 us).
 // GATE: 0 none; 1 a row of it comes with each row; 2 many rows share one (kGateRows at
 // least): its values are in w2, and since they are the same for all those rows, P = sum g yhat
 // and Q = sum g down the rows give all that depends on it when the rows end:
@@ -524,7 +652,7 @@ __host__ __device__ constexpr int ring_units() {
 constexpr uint64_t kGateRows = 8;
 template <class TB, class TS, bool VEC, int GATE, int V>
 __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a, const BackArgs q, uint32_t depth) {
-    constexpr int UNITS = ring_units<TB, TS, GATE>(), UB = sizeof(TB) / 2, US = sizeof(TS) / 2;
+    constexpr int UNITS = ring_units<TB, TS, VEC, GATE>(), UB = units<TB, VEC>(), US = units<TS, VEC>();
     extern __shared__ __align__(128) unsigned char ring_raw[];
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -545,7 +673,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a,
     const uint32_t slot_units = threads * UNITS * V;
     // Sums of a row, [rank, warp][kSums], three rows deep: a CTA may still read one row's
     // after it has arrived for the next, when another sets out with the one after that.
-    float *sm_sums = reinterpret_cast<float *>(ring_raw + (VEC ? (size_t)depth * slot_units * 16 : 0));
+    float *sm_sums = reinterpret_cast<float *>(ring_raw + (size_t)depth * slot_units * 16);
     const uint32_t entries = ranks * warps;
     uint32_t sums_at = 0;   // of the row that is worked on
     auto sums_next = [&](uint32_t at) { return at == 2 * entries * kSums ? 0u : at + entries * kSums; };
@@ -566,24 +694,22 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a,
     uint32_t copy_slot = 0;
     // Copies the next row into its slot; missing inputs stay the zeros they are made below.
     auto fill = [&]() {
-        if (VEC && copy_row < row1) {
+        if (copy_row < row1) {
             const uint64_t o = copy_row * a.hidden + c0;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (col(v) >= n) break;
                 uint4 *to = ring + copy_slot * slot_units + v * UNITS * threads;
-                auto put = [&](int at, const auto *base, uint64_t off) {
-#pragma unroll
-                    for (int i = 0; i < (int)sizeof(*base) / 2; ++i)
-                        copy_async16(to + (at + i) * threads, reinterpret_cast<const uint4 *>(base + off + col(v)) + i);
+                auto put = [&](int at, const auto *base, uint64_t off, uint64_t rows) {
+                    copy_run<VEC>(to + at * threads, threads, base, off, col(v), n, rows * a.hidden);
                 };
-                put(0, reinterpret_cast<const TB *>(q.y), o);
+                put(0, reinterpret_cast<const TB *>(q.y), o, a.rows);
                 if (pre) {
-                    put(UB, reinterpret_cast<const TB *>(q.dh), o);
-                    put(2 * UB, reinterpret_cast<const TS *>(q.r), o);
+                    put(UB, reinterpret_cast<const TB *>(q.dh), o, a.rows);
+                    put(2 * UB, reinterpret_cast<const TS *>(q.r), o, a.rows);
                 }
-                if (q.dr) put(2 * UB + US, reinterpret_cast<const TS *>(q.dr), o);
-                if (GATE == 1) put(2 * UB + 2 * US, reinterpret_cast<const TB *>(a.gate), copy_gate.row * a.hidden + c0);
+                if (q.dr) put(2 * UB + US, reinterpret_cast<const TS *>(q.dr), o, a.rows);
+                if (GATE == 1) put(2 * UB + 2 * US, reinterpret_cast<const TB *>(a.gate), copy_gate.row * a.hidden + c0, a.gate_rows);
             }
         }
         copy_commit();
@@ -591,34 +717,26 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a,
         gate_next(copy_gate);
         copy_slot = copy_slot + 1 == depth ? 0 : copy_slot + 1;
     };
-    if (VEC) {
-        for (uint32_t s = 0; s < depth; ++s)   // what no copy fills
+    for (uint32_t s = 0; s < depth; ++s)   // what no copy fills
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                for (int i = 0; i < UNITS; ++i)
-                    if (col(v) >= n || (!pre && i >= UB && i < 2 * UB + US) || (!q.dr && i >= 2 * UB + US && i < 2 * UB + 2 * US))
-                        ring[s * slot_units + (v * UNITS + i) * threads] = make_uint4(0, 0, 0, 0);
-        for (uint32_t s = 0; s < depth; ++s) fill();
-    }
+        for (int v = 0; v < V; ++v)
+            for (int i = 0; i < UNITS; ++i)
+                if (col(v) >= n || (!pre && i >= UB && i < 2 * UB + US) || (!q.dr && i >= 2 * UB + US && i < 2 * UB + 2 * US))
+                    ring[s * slot_units + (v * UNITS + i) * threads] = make_uint4(0, 0, 0, 0);
+    for (uint32_t s = 0; s < depth; ++s) fill();
     struct Run {
         Cols y, dh, r, dr, gate;
     };
     auto load_run = [&](uint64_t row, uint32_t slot, const GateRow &g, int v) {
         Run w;
-        if constexpr (VEC) {
-            const uint4 *p = ring + slot * slot_units + v * UNITS * threads;
-            w.y = unpack8<TB>(p, threads), w.dh = unpack8<TB>(p + UB * threads, threads);
-            w.r = unpack8<TS>(p + 2 * UB * threads, threads), w.dr = unpack8<TS>(p + (2 * UB + US) * threads, threads);
-            if constexpr (GATE == 1) w.gate = unpack8<TB>(p + (2 * UB + 2 * US) * threads, threads);
-        } else {
-            const uint64_t o = row * a.hidden + c0;
-            const Cols zero = all8(0.f);
-            w.y = load_cols(reinterpret_cast<const TB *>(q.y) + o, col(v), n);
-            w.dh = pre ? load_cols(reinterpret_cast<const TB *>(q.dh) + o, col(v), n) : zero;
-            w.r = pre ? load_cols(reinterpret_cast<const TS *>(q.r) + o, col(v), n) : zero;
-            w.dr = q.dr ? load_cols(reinterpret_cast<const TS *>(q.dr) + o, col(v), n) : zero;
-            if constexpr (GATE == 1) w.gate = load_cols(reinterpret_cast<const TB *>(a.gate) + g.row * a.hidden + c0, col(v), n);
-        }
+        const uint4 *p = ring + slot * slot_units + v * UNITS * threads;
+        auto get = [&](int at, const auto *base, uint64_t off) { return read_run<VEC>(p + at * threads, threads, base, off, col(v), n); };
+        const uint64_t o = row * a.hidden + c0;
+        w.y = get(0, reinterpret_cast<const TB *>(q.y), o);
+        w.dh = get(UB, reinterpret_cast<const TB *>(q.dh), o);
+        w.r = get(2 * UB, reinterpret_cast<const TS *>(q.r), o);
+        w.dr = get(2 * UB + US, reinterpret_cast<const TS *>(q.dr), o);
+        if constexpr (GATE == 1) w.gate = get(2 * UB + 2 * US, reinterpret_cast<const TB *>(a.gate), g.row * a.hidden + c0);
         return w;
     };
     // Statistics of a row: mean and 1/deviation of r and of y; of a norm that is not there 0 and 1.
@@ -785,7 +903,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a,
 
     float4 st = stats_of(row0), st1 = stats_of(row0 + 1);
     uint32_t slot = 0, slot1 = 1;   // the ring is two rows deep at least
-    if (VEC) copy_wait_for(depth - 1);
+    copy_wait_for(depth - 1);
     publish(row0, 0, gate, st, 0);
     if (ranks > 1) cluster_arrive();
     for (uint64_t row = row0; row < row1; ++row) {
@@ -798,7 +916,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a,
         const bool gate_over = GATE == 2 && (gate.left == 1 || row + 1 == row1);
         auto publish_next = [&]() {
             if (row + 1 < row1) {
-                if (VEC) copy_wait_for(depth - 2);
+                copy_wait_for(depth - 2);
                 publish(row + 1, slot1, gate1, st1, at1);
             }
             if (ranks > 1) cluster_arrive();
@@ -850,8 +968,8 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a,
                 db1[v].v[i] = add2(db1[v].v[i], w.dh.v[i]);
                 dy.v[i] = fma2(w2[v].v[i], gy, fma2(yc, nn2, nn1));
             }
-            store_cols<VEC>(reinterpret_cast<TS *>(q.dx) + o, col(v), n, dx);
-            store_cols<VEC>(reinterpret_cast<TB *>(q.dy) + o, col(v), n, dy);
+            store_run<VEC>(reinterpret_cast<TS *>(q.dx) + o, col(v), n, dx, lane);
+            store_run<VEC>(reinterpret_cast<TB *>(q.dy) + o, col(v), n, dy, lane);
             if (GATE == 1 && q.dgate) {
                 if (q.shared_gate) {
 #pragma unroll
@@ -862,7 +980,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a,
                         dg[v] = all8(0.f);
                     }
                 } else {
-                    store_cols<VEC>(reinterpret_cast<TB *>(q.dgate) + o, col(v), n, dgr);
+                    store_run<VEC>(reinterpret_cast<TB *>(q.dgate) + o, col(v), n, dgr, lane);
                 }
             }
         }
@@ -872,7 +990,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) k_norm_backward(const Args a,
             if (row + 1 < row1) take_gate();
             publish_next();
         }
-        if (VEC) fill();
+        fill();
         slot = slot1;
         slot1 = slot1 + 1 == depth ? 0 : slot1 + 1;
         st = st1, st1 = st2;
@@ -1092,18 +1210,27 @@ constexpr int runs_of() { return VEC && GATE != 1 ? 2 : 1; }
 template <class TB, class TS, bool VEC, int GATE>
 int shape_v(const bf16opt_norm_gate_t *d, int sms, Shape &s) {
     constexpr int V = runs_of<VEC, GATE>();
-    // CTAs that share the columns: so many that a CTA's fit its threads, and two rows of them its ring
+    // CTAs that share the columns: so many that a CTA's fit its threads, and two rows of them its ring; and
+    // more where the SM then holds half as many threads again (8192 x 4097: two CTAs of 288 threads, one
+    // per SM, 340 us; four of 160, three per SM, 281 us).
     size_t row = 0, sums = 0;
+    auto per_sm_of = [](uint32_t threads) { return std::max(1u, std::min(512u / threads, 16u)); };   // 128 registers a thread
+    auto threads_of = [&](uint32_t cluster) {
+        const uint32_t cols = (d->hidden + cluster - 1) / cluster;
+        return ((cols + 8 * V - 1) / (8 * V) + 31) / 32 * 32;
+    };
     for (s.cluster = 1;; s.cluster *= 2) {
-        const uint32_t cols = (d->hidden + s.cluster - 1) / s.cluster;
-        s.threads = ((cols + 8 * V - 1) / (8 * V) + 31) / 32 * 32;
-        row = (size_t)s.threads * V * ring_units<TB, TS, GATE>() * 16;
+        s.threads = threads_of(s.cluster);
+        row = (size_t)s.threads * V * ring_units<TB, TS, VEC, GATE>() * 16;
         sums = 3 * s.cluster * s.threads / 32 * kSums * sizeof(float);
-        if (s.threads <= (uint32_t)kBackThreads && (!VEC || 2 * row + sums <= kMaxDynamic)) break;
+        if (s.threads > (uint32_t)kBackThreads || 2 * row + sums > kMaxDynamic) continue;
+        const uint32_t half = threads_of(2 * s.cluster);
+        if (s.cluster < 8 && 2 * half * per_sm_of(half) >= 3 * s.threads * per_sm_of(s.threads)) continue;
+        break;
     }
-    const unsigned per_sm = std::max(1u, std::min(512u / s.threads, 16u));   // 128 registers a thread
-    s.depth = VEC ? (uint32_t)std::max<size_t>(2, std::min<size_t>(8, ring_bytes(per_sm, sums) / row)) : 2;
-    s.smem = (VEC ? s.depth * row : 0) + sums;
+    const unsigned per_sm = per_sm_of(s.threads);
+    s.depth = (uint32_t)std::max<size_t>(2, std::min<size_t>(8, ring_bytes(per_sm, sums) / row));
+    s.smem = s.depth * row + sums;
     int fit = 0;
     const cudaError_t e = clusters_that_fit(Launch{s.cluster, s.threads, s.smem, nullptr, s.cluster, true},
                                             k_norm_backward<TB, TS, VEC, GATE, V>, fit);

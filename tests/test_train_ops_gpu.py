@@ -358,6 +358,35 @@ def test_norm_nan_stays_in_its_row():
     assert torch.isnan(got[0][3]).all() and torch.isnan(got[1][3]).all()
 
 
+@pytest.mark.parametrize("branch,stream", [(BF16, BF16), (BF16, F32), (F32, F32)])
+@pytest.mark.parametrize("rows,hidden,gates", [(90, 2, 0), (61, 9, 61), (33, 13, 0), (700, 31, 7), (40, 250, 40), (24, 1031, 2), (16, 4097, 0),
+                                               (5, 9001, 5), (3, 14333, 1)])
+def test_norm_rows_between_boundaries(rows, hidden, gates, branch, stream):
+    """Rows that begin anywhere between two 16-byte boundaries, each tensor at a place of its own: no row sees its
+    neighbours' elements, which are NaN in one row of all inputs."""
+    x, y, how = norm_case(rows, hidden, branch, stream, F32, "layer", "rms", gates, 7)
+    if gates:
+        how["gate_act"] = "sigmoid"
+    check_norm(x, y, how)
+
+    def placed(t, offset):
+        return torch.empty(t.numel() + offset, dtype=t.dtype, device="cuda")[offset:].view(t.shape).copy_(t)
+    g = gen(8)
+    r, h, stats = ops.norm_gate_forward(x, y, **how)
+    dr, dh = randn(g, rows, hidden).to(stream), randn(g, rows, hidden).to(branch)
+    clean = ops.norm_gate_backward(dr, dh, r, y, stats, **how)
+    spoilt = [t.clone() for t in (dr, dh, r, y)]
+    for t in spoilt:
+        t[rows // 2] = float("nan")
+    got = ops.norm_gate_backward(*[placed(t, i) for i, t in zip((1, 3, 2, 5), spoilt)], stats,
+                                 **{**how, **({"gate": placed(how["gate"], 7)} if gates else {})})
+    keep = torch.arange(rows, device="cuda") != rows // 2
+    for n in ("dx", "dy") + (("dgate",) if gates == rows else ()):
+        size = clean[n].double().abs().max()
+        close(got[n][keep], clean[n][keep], 40 * size, n)
+        assert bool(torch.isnan(got[n][rows // 2]).all())
+
+
 @pytest.mark.parametrize("offset", [0, 1])
 def test_norm_in_place_and_unaligned(offset):
     rows, hidden = 50, 1048
