@@ -9,13 +9,15 @@
 // order.  (f_e, the share of tokens of an expert, is known only after the last
 // token, so the gradient is a second pass.)
 //
-// Measured on one GB300: 262144 tokens, 256 experts, 8 of them, bf16: forward 121 us, 1.1 TB/s, join 10 us, backward 90 us,
-// 3.1 TB/s; both ways 218 us in a row. The forward pass is bound by integer instructions (69 % of that pipe's cycles, 76 % of
-// the issue slots): 430 a token, most of them the choice's. The backward pass waits for its loads (36 % of the
-// warps active, issue slots 54 %).  16384 tokens of 64 FP32 experts in 8 groups: 14 + 6 + 7 us, which the host's calls take longer than.
+// Measured on one GB300: 262144 tokens, 256 experts, 8 of them, bf16: forward 121 us, 1.1 TB/s, join 10 us,
+// backward 71 us, 4.0 TB/s; both ways 197 us in a row.  The forward pass is bound by integer instructions (69 %
+// of that pipe's cycles, 76 % of the issue slots): 430 a token, most of them the choice's.  The backward pass is
+// bound by issue (70 % of the slots) and a token's sums and lookups in shared memory.  16384 tokens of 64 FP32
+// experts in 8 groups: 14 + 6 + 7 us, which the host's calls take longer than.
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ops_common.cuh"
 
@@ -24,9 +26,10 @@ namespace cg = cooperative_groups;
 namespace bf16ops {
 namespace {
 
-// CTAs of an SM in the backward pass, up to 256 experts: 85 registers a thread (at 64 it spills:
-// 262144 x 256 took 266 us both ways, 220 us so).
-constexpr int kBackResident = 3;
+// CTAs of an SM in the backward pass, by the experts of a lane: three have 85 registers a thread (at 64 that of 256
+// experts spills: 262144 x 256 took 266 us both ways, 220 us so; 131072 x 256 FP32 backward 145 against 52 us); up to
+// 64 experts 64 registers are enough (262144 x 64 backward: FP32 52 against 64 us, bf16 62 against 80 us).
+__host__ __device__ constexpr int back_resident(int per) { return per <= 2 ? 4 : per <= 8 ? 3 : 1; }
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
@@ -491,11 +494,30 @@ struct BackArgs {
     bool vec;
 };
 
+// Tokens of a warp's ring in the backward pass (three to six take the same time), and the bytes of one: the row, its
+// ids, the gradients of its weights, its log-sum-exp.
+constexpr int kRing = 4;
+template <class T, int PER>
+__host__ __device__ constexpr uint32_t ring_slot() {
+    return 32 * PER * (uint32_t)sizeof(T) + 128 + 128 + 16;
+}
+// bf16 and a vector a lane: 262144 x 256 98 us through registers, 76 us through the ring. FP32 with a vector a lane: 68
+// against 72 us; two vectors: the ring is more than a launch gives without asking.
+template <class T, int PER>
+__host__ __device__ constexpr bool has_ring() {
+    return PER == 8 && sizeof(T) == 2;
+}
+__device__ __forceinline__ void copy_async4(void *smem, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(src) : "memory");
+}
+
 // What the choices add to their experts' elements goes through a row of shared
 // memory of the warp's own, all zeros between two tokens.
-template <class T, int PER>
-__global__ void __launch_bounds__(kThreads, PER <= 8 ? kBackResident : 1) k_balance_backward(const Args a, const BackArgs q) {
-    extern __shared__ __align__(16) float sm_extra[];   // [warps][32 PER]
+// RING: a lane's run is one 16-byte vector; tokens come through a ring of the warp's own, copied kRing
+// tokens ahead, and a choice's logit is looked up there. Else they come through registers, two ahead.
+template <class T, int PER, bool RING>
+__global__ void __launch_bounds__(kThreads, back_resident(PER)) k_balance_backward(const Args a, const BackArgs q) {
+    extern __shared__ __align__(128) float sm_extra[];   // [warps][32 PER], then RING: [warps][kRing] slots
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float *extras = sm_extra + warp * 32 * PER;
 #pragma unroll
@@ -543,15 +565,63 @@ __global__ void __launch_bounds__(kThreads, PER <= 8 ? kBackResident : 1) k_bala
         row += a.stride;
         if (chooses) up_from += a.k;
     };
-    id_3 = next_id();
-    fetch();
-    fetch();
-    for (uint32_t todo = tokens; todo != 0; --todo, out += q.stride) {
-        const float lse = lse_next, up = up_next, zid = zid_next;
-        const int32_t id = id_next;
-        float z[PER];
-        unpack_run<T, PER>(ahead, z);
+    char *ring = reinterpret_cast<char *>(sm_extra + kThreads * PER) + warp * kRing * ring_slot<T, PER>();
+    uint32_t slot = 0, copy_slot = 0;
+    constexpr uint32_t kRow = 32 * PER * sizeof(T), kRun = PER * sizeof(T);
+    auto fill = [&]() {
+        if (to_fetch != 0) {
+            --to_fetch;
+            char *to = ring + copy_slot * ring_slot<T, PER>();
+            if (lane * PER < a.experts) {
+#pragma unroll
+                for (uint32_t i = 0; i < kRun; i += 16) copy_async16(to + lane * kRun + i, reinterpret_cast<const char *>(row + lane * PER) + i);
+            }
+            if (chooses) copy_async4(to + kRow + lane * 4, id_from), copy_async4(to + kRow + 128 + lane * 4, up_from);
+            if (lane == 0) copy_async4(to + kRow + 256, lse_from);
+            row += a.stride, ++lse_from;
+            if (chooses) id_from += a.k, up_from += a.k;
+        }
+        copy_commit();
+        copy_slot = copy_slot + 1 == kRing ? 0 : copy_slot + 1;
+    };
+    if constexpr (RING) {
+        for (int i = 0; i < kRing; ++i) fill();
+    } else {
+        id_3 = next_id();
         fetch();
+        fetch();
+    }
+    for (uint32_t todo = tokens; todo != 0; --todo, out += q.stride) {
+        float z[PER], lse, up = 0.f, zid = 0.f;
+        int32_t id = -1;
+        if constexpr (RING) {
+            copy_wait<kRing - 1>();
+            __syncwarp();
+            const char *from = ring + slot * ring_slot<T, PER>();
+            lse = *reinterpret_cast<const float *>(from + kRow + 256);
+            if (chooses) {
+                id = *reinterpret_cast<const int32_t *>(from + kRow + lane * 4);
+                up = *reinterpret_cast<const float *>(from + kRow + 128 + lane * 4);
+                if ((uint32_t)id >= a.experts) id = -1;
+                if (id >= 0) zid = to_f32(reinterpret_cast<const T *>(from)[id]);
+            }
+            RunOf<T, PER> run;
+#pragma unroll
+            for (uint32_t i = 0; i < kRun / 4; i += 4) {
+                constexpr uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;   // -inf
+                const uint4 v = lane * PER < a.experts ? *reinterpret_cast<const uint4 *>(from + lane * kRun + i * 4)
+                                                       : make_uint4(none, none, none, none);
+                run.w[i] = v.x, run.w[i + 1] = v.y, run.w[i + 2] = v.z, run.w[i + 3] = v.w;
+            }
+            unpack_run<T, PER>(run, z);
+            __syncwarp();
+            fill();
+            slot = slot + 1 == kRing ? 0 : slot + 1;
+        } else {
+            lse = lse_next, up = up_next, zid = zid_next, id = id_next;
+            unpack_run<T, PER>(ahead, z);
+            fetch();
+        }
         if (fresh) {
             fresh = false;
             const float n = q.live[group], scale = dloss / ((float)a.groups * n), share = (float)a.experts / ((float)a.k * n);
@@ -787,12 +857,20 @@ int backward(const bf16opt_balance_t *d, const int32_t *ids, const int32_t *coun
     const int per = per_of(d->experts);
     a.vec = runs(d->logits, d->logits_stride, d->experts, per, elem);
     q.vec = runs(dlogits, dlogits_stride, d->experts, per, elem);
-    const unsigned grid = (unsigned)std::min<uint64_t>((d->tokens + kWarps - 1) / kWarps, (uint64_t)sms * (per <= 8 ? kBackResident : 1));
+    const unsigned grid = (unsigned)std::min<uint64_t>((d->tokens + kWarps - 1) / kWarps, (uint64_t)sms * back_resident(per));
     return by_per(per, [&](auto p) {
         constexpr int PER = decltype(p)::value;
-        Launch l{grid, (unsigned)kThreads, (size_t)kThreads * PER * 4, (cudaStream_t)stream, 0, true};
-        return done(d->logits_type == BF16OPT_TYPE_BF16 ? launch(l, k_balance_backward<__nv_bfloat16, PER>, a, q)
-                                                        : launch(l, k_balance_backward<float, PER>, a, q));
+        auto go = [&](auto *type) {
+            using T = std::remove_pointer_t<decltype(type)>;
+            Launch l{grid, (unsigned)kThreads, (size_t)kThreads * PER * 4, (cudaStream_t)stream, 0, true};
+            if constexpr (has_ring<T, PER>())
+                if (a.vec) {
+                    l.smem += (size_t)kWarps * kRing * ring_slot<T, PER>();
+                    return done(launch(l, k_balance_backward<T, PER, true>, a, q));
+                }
+            return done(launch(l, k_balance_backward<T, PER, false>, a, q));
+        };
+        return d->logits_type == BF16OPT_TYPE_BF16 ? go((__nv_bfloat16 *)nullptr) : go((float *)nullptr);
     });
 }
 
