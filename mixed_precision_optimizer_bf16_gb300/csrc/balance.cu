@@ -72,7 +72,9 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 // lowest expert wins a tie: a lane sorts its keys once (a network of exchanges), and a
 // choice is one reduction over the lanes' largest and one step of the winner's list.
 // FP32 logits leave no room for the expert: there a choice is a reduction and a
-// ballot, and the winner searches its run again.  Under this key come experts that are off.
+// ballot; a lane of up to 8 experts keeps its keys sorted beside their experts (262144
+// tokens forward, 64 experts 120 us, 128 experts 175 us), a longer one searches its run again when
+// it has won (so throughout: 133 and 207 us).  Under kOff16 come experts that are off.
 constexpr uint32_t kOff16 = 0x00800000u;
 
 // Eight keys in descending order: an odd-even merge network of 19 exchanges.
@@ -306,6 +308,31 @@ __global__ void __launch_bounds__(kThreads, PER <= 8 ? 4 : 1) k_balance_forward(
                             const uint32_t up = mine & 0xffff0000u;   // the logit back from its key
                             const float my_z = up < kOff16 ? NAN : __uint_as_float(up & 0x80000000u ? up ^ 0x80000000u : ~up & 0xffff0000u);
                             my_p = ex2((my_z - m) * kLog2e) * inv;
+                        }
+                    } else if constexpr (PER <= 8) {
+                        // the lane's keys in descending order, equal ones by their expert: neighbours change places
+                        uint32_t key[PER], at[PER];
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) key[i] = key_of(z[i]), at[i] = lane * PER + i;
+#pragma unroll
+                        for (int n = PER - 1; n > 0; --n)
+#pragma unroll
+                            for (int i = 0; i < n; ++i) {
+                                const bool swap = key[i + 1] > key[i];
+                                const uint32_t k0 = key[i], a0 = at[i];
+                                key[i] = swap ? key[i + 1] : k0, key[i + 1] = swap ? k0 : key[i + 1];
+                                at[i] = swap ? at[i + 1] : a0, at[i + 1] = swap ? a0 : at[i + 1];
+                            }
+                        for (uint32_t c = 0; c < a.k; ++c) {
+                            const uint32_t top = __reduce_max_sync(0xffffffffu, key[0]);
+                            if (top == 0u) break;
+                            const uint32_t from = __ffs(__ballot_sync(0xffffffffu, key[0] == top)) - 1;
+                            const int32_t id = (int32_t)__shfl_sync(0xffffffffu, at[0], from);
+                            if (lane == c) my_id = id, my_p = ex2((value_of(top) - m) * kLog2e) * inv;
+                            const bool won = lane == from;
+#pragma unroll
+                            for (int i = 0; i + 1 < PER; ++i) key[i] = won ? key[i + 1] : key[i], at[i] = won ? at[i + 1] : at[i];
+                            key[PER - 1] = won ? 0u : key[PER - 1];
                         }
                     } else {
                         uint32_t key[PER], best = 0, at = 0;
