@@ -104,13 +104,14 @@ __device__ __forceinline__ void store8(T *row, uint32_t n, uint32_t slot, uint32
     }
 }
 
-// Weights: read again and again, so kept in L1.
+// Weights: read again and again, so kept in L1.  Beyond the row 0, also where there are none: a norm that
+// subtracts a mean leaves nothing there then, and the next norm's mean is the row's alone.
 template <bool VEC>
 __device__ __forceinline__ void load8_weight(const void *w, int type, uint32_t n, uint32_t slot, uint32_t threads, uint32_t t,
                                              float none, float (&f)[8]) {
     if (!w) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = none;
+        for (int i = 0; i < 8; ++i) f[i] = column<VEC>(slot, threads, t, i) < n ? none : 0.f;
         return;
     }
     if constexpr (VEC) {

@@ -1,0 +1,44 @@
+"""The training operators on the GPU where they are easily wrong: rows far from zero, norms without weights,
+tokens that are off, and what autograd and streams ask of them.
+
+Tolerances as in test_train_ops_gpu.py: an output's own rounding, and 2e-5 of the magnitudes summed in FP32.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import train_ops_reference as R  # noqa: E402
+from mixed_precision_optimizer_bf16_gb300 import train_ops as ops  # noqa: E402
+from test_train_ops_gpu import BF16, F32, check_norm, close, norm_case, rowmax  # noqa: E402
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
+
+
+# ------------------------------------------------------------------- gated norms
+
+BARE = pytest.mark.parametrize("hidden", [1, 7, 40, 257, 264, 500, 1031, 2049, 4104, 9001])
+
+
+def bare(hidden, branch, stream, gate, bias):
+    x, y, how = norm_case(6, hidden, branch, stream, F32, "layer", "layer", 3 if gate else 0)
+    how = {n: v for n, v in how.items() if not n.endswith("_weight") and (bias or not n.endswith("_bias"))}
+    return x, y, dict(how, gate_act=gate or "none")
+
+
+@pytest.mark.parametrize("branch,stream", [(BF16, BF16), (BF16, F32), (F32, F32)])
+@BARE
+@pytest.mark.parametrize("gate", [None, "none", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_norm_layer_norms_without_weights(hidden, branch, stream, gate, bias):
+    """Both norms subtract a mean and have no weight: what lies beyond a row's end in its threads counts for nothing."""
+    x, y, how = bare(hidden, branch, stream, gate, bias)
+    r, h, stats = ops.norm_gate_forward(x, y + 3, **how)
+    for got, want, n in zip((r, h, stats), R.norm_gate(x, y + 3, **how), ("r", "h", "stats")):
+        close(got, want, rowmax(want) if n != "stats" else 1 + want.abs(), n)
+
+
+@pytest.mark.parametrize("branch,stream", [(BF16, BF16), (BF16, F32), (F32, F32)])
+@BARE
+@pytest.mark.parametrize("gate", [None, "sigmoid"])
+def test_norm_layer_norms_without_weights_backward(hidden, branch, stream, gate):
+    check_norm(*bare(hidden, branch, stream, gate, False))
