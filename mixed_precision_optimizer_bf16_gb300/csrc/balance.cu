@@ -178,6 +178,8 @@ __device__ __forceinline__ float reciprocal(float x) {   // to one unit in the l
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The z-loss of a group; 0 where its weight is, though a square of far logits does not fit FP32.
+__device__ __forceinline__ float z_loss(float weight, float squares, float n) { return weight != 0.f ? weight * (squares / n) : 0.f; }
 // sum over the CTA, the same bits in every thread
 __device__ __forceinline__ float cta_sum(float v, float *buf) {
     v = warp_sum(v);
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, PER <= 8 ? 4 : 1) k_balance_forward(
             fp = cta_sum(fp, sm_buf);
             const float nf = (float)n;
             const float l = n == 0 ? 0.f
-                                   : a.balance_weight * (fp / nf) * ((float)a.experts / ((float)a.k * nf)) + a.z_weight * (sq / nf);
+                                   : a.balance_weight * (fp / nf) * ((float)a.experts / ((float)a.k * nf)) + z_loss(a.z_weight, sq, nf);
             whole += l;
             if (threadIdx.x == 0) {
                 a.live[g] = nf;
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_balance_join(const Args a) 
         fp = cta_total(fp);
         const float nf = (float)n, share = (float)a.experts / ((float)a.k * nf);
         float l = n == 0 ? 0.f : a.balance_weight * (fp / nf) * share;
-        if (!split || rank == 0) l += n == 0 ? 0.f : a.z_weight * (sq / nf);
+        if (!split || rank == 0) l += n == 0 ? 0.f : z_loss(a.z_weight, sq, nf);
         if ((!split || rank == 0) && threadIdx.x == 0) {
             a.live[g] = nf;
             if (!WHOLE) a.group_loss[g] = l;

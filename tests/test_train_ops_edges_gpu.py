@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 
 import train_ops_reference as R  # noqa: E402
 from mixed_precision_optimizer_bf16_gb300 import train_ops as ops  # noqa: E402
-from test_train_ops_gpu import BF16, F32, check_norm, close, norm_case, rowmax  # noqa: E402
+from test_train_ops_gpu import BF16, F32, check_norm, close, gen, norm_case, randn, rowmax  # noqa: E402
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
 
@@ -42,3 +42,25 @@ def test_norm_layer_norms_without_weights(hidden, branch, stream, gate, bias):
 @pytest.mark.parametrize("gate", [None, "sigmoid"])
 def test_norm_layer_norms_without_weights_backward(hidden, branch, stream, gate):
     check_norm(*bare(hidden, branch, stream, gate, False))
+
+
+# ----------------------------------------------------------------- expert balance
+
+def from_top(z):
+    """Logits less their token's largest, in 64 bits: the same softmax, where the type's lowest would leave the
+    logarithm of a sum no room in 64 bits either.  (Not with a z-loss.)"""
+    top = z.double().amax(1, keepdim=True)
+    return z.double() - torch.where(torch.isfinite(top), top, torch.zeros_like(top))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tokens,groups", [(70, 2), (4000, 1), (4000, 4), (4000, 100)])
+def test_balance_loss_of_the_lowest_logits(tokens, groups, dtype):
+    """Without the z-loss the square of a far log-sum-exp, which FP32 cannot hold, is no part of the loss."""
+    z = randn(gen(6), tokens, 16).to(dtype)
+    z[::9] = torch.finfo(dtype).min
+    got = ops.balance_forward(z, 2, groups=groups, balance_weight=0.5)
+    want = R.balance(from_top(z), 2, groups=groups, balance_weight=0.5)
+    assert torch.equal(got[0].cpu(), want[0]) and torch.equal(got[2].cpu(), want[2])
+    close(got[1], want[1], 1.0 * (want[1] != 0), "weights")
+    close(got[3], want[3], want[3].abs(), "loss")
