@@ -77,13 +77,20 @@ struct Args {
 struct Stat {
     float m, st, s1;
 };
-// The teacher's: maximum m of x = t / T, sum s of e = exp(x - m), sum d of e ((x - m) - (z - b) / T),
-// b the largest finite z: both taken from their largest, so that logits far from 0 cost no digits.
+// The teacher's: maximum m of t, sum s of e = exp((t - m) / T), sum d of e ((t - m) / T - (z - b) / T),
+// b the largest finite z: both taken from their largest before anything is rounded, so that logits far
+// from 0 cost no digits.
 struct Teach {
     float m, b, s, d;
 };
 
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.f : m; }
+
+// y - m / T, where both are large and near one another: with the quotient's rounding error.
+__device__ __forceinline__ float less_quotient(float y, float m, float inv_t, float t) {
+    const float q = m * inv_t;
+    return fabsf(q) < INFINITY ? (y - q) - fmaf(-q, t, m) * inv_t : y - q;
+}
 
 // Each product and sum rounded by itself, so that join(a, b) and join(b, a) are the same bits.
 __device__ __forceinline__ float weighted(float a, float ea, float b, float eb) {
@@ -113,7 +120,7 @@ __device__ __forceinline__ Teach warp_join(const Teach &a, float inv_t) {
     Teach r;
     r.m = warp_max(a.m);
     r.b = warp_max(a.b);
-    const float x = a.m - safe_max(r.m), e = ex2(x * kLog2e);
+    const float x = (a.m - safe_max(r.m)) * inv_t, e = ex2(x * kLog2e);
     r.s = warp_sum(a.s * e);
     // a d of +inf (masked z) may meet a weight of 0
     r.d = warp_sum(e > 0.f ? e * (a.d + a.s * (x - (safe_max(a.b) - safe_max(r.b)) * inv_t)) : 0.f);
@@ -231,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
     // 128 bytes: a ring that begins elsewhere splits every wavefront (1024 x 250880 forward, 80 bytes
     // off: 108 against 88 us)
     extern __shared__ __align__(128) unsigned char smem_raw[];
-    // ring | ids, x (then what the entry takes off the gradient), z of the entries
+    // ring | ids, t (then what the entry takes off the gradient), z of the entries
     uint4 *ring = reinterpret_cast<uint4 *>(smem_raw);
     int32_t *sm_id = reinterpret_cast<int32_t *>(smem_raw + (size_t)depth * kGroup * 16);
     float *sm_x = reinterpret_cast<float *>(sm_id + (a.k + 1));
@@ -467,13 +474,13 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
             const uint32_t e = tid + i * kThreads;
             if (e >= a.k) break;
             const int64_t id64 = i == 0 ? entry.id : load_index(a.ids, a.ids_type, row * a.ids_stride + e);
-            const float x = (i == 0 ? entry.t : load_typed(a.teacher, a.teacher_type, row * a.teacher_stride + e)) * a.inv_t;
-            const bool there = id64 >= 0 && id64 < (int64_t)a.vocab && x != -INFINITY;
+            const float t = i == 0 ? entry.t : load_typed(a.teacher, a.teacher_type, row * a.teacher_stride + e);
+            const bool there = id64 >= 0 && id64 < (int64_t)a.vocab && t != -INFINITY;
             const int32_t id = there ? (int32_t)id64 : -1;
             const float zi = i == 0 ? entry_z : there ? to_f32(z[id]) : 0.f;
-            sm_id[e] = id, sm_x[e] = x, sm_z[e] = zi;
+            sm_id[e] = id, sm_x[e] = t, sm_z[e] = zi;
             if (there) {
-                te.m = fmaxf(te.m, x);
+                te.m = fmaxf(te.m, t);
                 if (fabsf(zi) < INFINITY) te.b = fmaxf(te.b, zi);
             }
             slots[i] = enter(id);
@@ -501,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
         if (warp < teach_warps) {   // (both, so that their shuffles run side by side)
             te.m = warp_max(te.m), te.b = warp_max(te.b);
             for (uint32_t i = tid; i < a.k; i += kThreads) {   // its own entries
-                const float x = sm_x[i] - safe_max(te.m), e = sm_id[i] < 0 ? 0.f : ex2(x * kLog2e);
+                const float x = (sm_x[i] - safe_max(te.m)) * a.inv_t, e = sm_id[i] < 0 ? 0.f : ex2(x * kLog2e);
                 te.s += e;
                 if (!(e <= 0.f)) te.d += e * (x - (sm_z[i] - safe_max(te.b)) * a.inv_t);
             }
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
 
         // ---- the row's loss
         const bool some = te.s != 0.f;   // the teacher has entries here (NaN counts)
-        const float log_teacher = a.teacher_lse ? now.teacher_lse - te.m : logf(te.s);   // the lse less te.m
+        const float log_teacher = a.teacher_lse ? less_quotient(now.teacher_lse, te.m, a.inv_t, a.temperature) : logf(te.s);   // the lse less te.m / T
         const float mass = !some ? 0.f : a.teacher_lse ? te.s * ex2(-log_teacher * kLog2e) : te.s == te.s ? 1.f : te.s;
         const bool has_label = sm_label[turn & 1] >= 0;
         now = then;
@@ -640,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
         // ---- the entries of the slice
         const bool twice = sm_twice[turn & 1] == turn;
         ++turn;
-        for (uint32_t e = tid; e < a.k; e += kThreads) sm_x[e] = soft * ex2(((sm_x[e] - te.m) - log_teacher) * kLog2e);
+        for (uint32_t e = tid; e < a.k; e += kThreads) sm_x[e] = soft * ex2(((sm_x[e] - te.m) * a.inv_t - log_teacher) * kLog2e);
         if (tid == kThreads - 1) sm_x[a.k] = hard;
         __syncthreads();   // the slice's gradient is stored, the entries' parts are there
         auto put = [&](uint32_t e) {

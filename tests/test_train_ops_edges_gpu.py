@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 
 import train_ops_reference as R  # noqa: E402
 from mixed_precision_optimizer_bf16_gb300 import train_ops as ops  # noqa: E402
-from test_train_ops_gpu import BF16, F32, check_norm, close, gen, norm_case, randn, rowmax  # noqa: E402
+from test_train_ops_gpu import BF16, F32, check_norm, close, distill_case, gen, loss_scale, norm_case, randn, rowmax  # noqa: E402
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
 
@@ -42,6 +42,36 @@ def test_norm_layer_norms_without_weights(hidden, branch, stream, gate, bias):
 @pytest.mark.parametrize("gate", [None, "sigmoid"])
 def test_norm_layer_norms_without_weights_backward(hidden, branch, stream, gate):
     check_norm(*bare(hidden, branch, stream, gate, False))
+
+
+# ------------------------------------------------------------------ distillation
+
+@pytest.mark.parametrize("temperature", [1.5, 0.7, 2.0])
+@pytest.mark.parametrize("full", [False, True])
+@pytest.mark.parametrize("away", [1e4, -1e4, 1e6])
+def test_distill_teacher_far_from_zero(away, full, temperature):
+    """Distinct teacher's logits far from zero: their softmax comes from differences."""
+    z, ids, top, how = distill_case(5, 3001, 21, F32, 12, labels=True, temperature=temperature)
+    top = top + away
+    if full:    # the normaliser as an FP32 number, whatever it comes to: the formula takes it as it is
+        how["teacher_lse"] = torch.logsumexp(top.double() / temperature, 1).float()
+    exact = dict(how, temperature=torch.tensor(temperature).item())      # the number that the call takes: FP32
+    loss_r, dz_r, scale, _ = R.distill(z, ids, top, **exact)
+    loss, dz = ops.distill_loss_grad(z, ids, top, **how)
+    close(loss, loss_r, loss_scale(z, top - away, how), "loss")
+    close(dz, dz_r, scale, "dlogits")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_distill_teacher_at_the_types_ends(sign, dtype):
+    """t / T does not fit FP32 at T = 0.5: the largest entry alone has a probability."""
+    z, ids, top, how = distill_case(4, 515, 6, F32, 13, labels=True, temperature=0.5)
+    top = (sign * torch.finfo(dtype).max * (1 - torch.arange(6, device="cuda") / 16.0)).to(dtype).expand(4, 6).contiguous()
+    loss_r, dz_r, scale, _ = R.distill(z, ids, top, **how)
+    loss, dz = ops.distill_loss_grad(z, ids, top, **how)
+    close(loss, loss_r, loss_scale(z, torch.zeros_like(top), how), "loss")
+    close(dz, dz_r, scale, "dlogits")
 
 
 # ----------------------------------------------------------------- expert balance
