@@ -489,8 +489,10 @@ int bf16opt_distill_forward(const bf16opt_distill_t *d, float *loss, float *lse,
 
 /* dlogits [rows, vocab], rounded once from FP32; it may be d->logits itself
  * with the same stride (the logits are then overwritten).  lse: as the forward
- * call with the same descriptor left it.  dloss: NULL (1), or [rows] FP32: the
- * gradient of the row's loss. */
+ * call with the same descriptor left it (a row for which one of them is 128 or
+ * more in magnitude is read twice: one FP32 number does not hold the sum of a row
+ * that lies far from 0).  dloss: NULL (1), or [rows] FP32: the gradient of the
+ * row's loss. */
 int bf16opt_distill_backward(const bf16opt_distill_t *d, const float *lse, const float *dloss, void *dlogits,
                              uint64_t dlogits_stride, void *stream);
 

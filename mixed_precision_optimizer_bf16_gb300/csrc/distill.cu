@@ -46,6 +46,9 @@ constexpr uint64_t kShortRow = 5000;
 // CTAs of an SM, and groups in the ring of each, by their threads: 200 KB of an SM are rings.
 __host__ __device__ constexpr int resident(int threads) { return threads == kLarge ? 2 : 4; }
 __host__ __device__ constexpr int ring_depth(int threads) { return 200 * 1024 / resident(threads) / (threads * kU * 16); }
+// Saved log-sum-exps below this are taken as they are: their rounding is at most 2^-18, which is how far it
+// moves a softmax, as much as the exponents' own.
+constexpr float kFar = 128.f;
 // Entries of one thread, the label's included.
 __host__ __device__ constexpr int entries(int threads) { return (BF16OPT_DISTILL_MAX_K + threads) / threads; }
 
@@ -218,6 +221,12 @@ __host__ __device__ constexpr uint32_t table_size(uint32_t k) {
     return n;
 }
 
+// A row whose saved log-sum-exps do not say enough for its gradient: one FP32 number has no room for the sum's
+// logarithm beside a far maximum, or is infinite (where every logit is masked, too).
+__device__ __forceinline__ bool is_far(const Args &a, float lse_t, float lse_1) {
+    return !(fabsf(lse_t) < kFar && fabsf(lse_1) < kFar && fabsf(lse_t * a.temperature) < INFINITY);
+}
+
 // FORWARD: the row's sums are computed here (else read from lse_in).  GRAD: the
 // gradient is written.  POWER: 0, only the softmax at T is needed; 1, the one at
 // temperature 1 too; 2 or 4, the same with T = POWER, where exp(d) is a power
@@ -230,7 +239,12 @@ __host__ __device__ constexpr uint32_t table_size(uint32_t k) {
 // or of the cluster's next ones.  With both passes (FORWARD and GRAD) the slice's last
 // `depth` groups stay in the ring for the gradient, which starts with them; the ones
 // before are read a second time, from L2, where the row still is.
-template <int kThreads, class T, bool FORWARD, bool GRAD, int POWER>
+//
+// Without FORWARD far rows are passed over. FAR: those rows alone, their sums computed once more, and no loss
+// written: the second launch of the backward call, over at once where there are none.  (With the sums of far rows
+// in one kernel, in any place of it, registers spilled: 1024 x 250880 bf16 241 to 249 us, 1021 x 32003 FP32 62 to
+// 69 us, so 181 and 58 us, 178 and 55 us without the second launch.)
+template <int kThreads, class T, bool FORWARD, bool GRAD, int POWER, bool FAR = false>
 __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const Args a) {
     constexpr int N = Vec<T>::N, P = N / 2;
     constexpr uint32_t kGroup = kThreads * kU, depth = ring_depth(kThreads);
@@ -264,10 +278,18 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
         __syncthreads();
     }
     pdl_enter();
+    if constexpr (FAR) {
+        bool any = false;
+        for (uint64_t r = blockIdx.x / ranks + tid * step; r < a.rows; r += kThreads * step) any |= is_far(a, a.lse_in[2 * r], a.lse_in[2 * r + 1]);
+        if (!__syncthreads_or(any)) return;   // the same in every CTA of the cluster
+    }
     if (FORWARD && ranks > 1) cluster.sync();   // every CTA's shared memory exists
 
     auto row_of = [&](uint64_t row) { return reinterpret_cast<const T *>(a.logits) + row * a.logits_stride; };
-    auto weight_of = [&](uint64_t row) { return row >= a.rows ? 0.f : a.row_weight ? a.row_weight[row] : 1.f; };
+    auto weight_of = [&](uint64_t row) {
+        if (row >= a.rows || (FAR && !is_far(a, a.lse_in[2 * row], a.lse_in[2 * row + 1]))) return 0.f;
+        return a.row_weight ? a.row_weight[row] : 1.f;
+    };
     // Entry `tid` of a row (of thread kThreads - 1 the label, where it has no entry; further
     // entries when they are needed): its id and logit are asked for two rows ahead, the student's
     // logit at the id one row ahead.
@@ -385,14 +407,14 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
         const float w_after = weight_of(next + step);
         const Scalars then = scalars_of(next);
 
-        if (w == 0.f) {   // not read: zeros
-            if (GRAD) {
+        if (w == 0.f) {   // not read: zeros (which the first launch has written where FAR)
+            if (GRAD && !FAR) {
                 float zero[N] = {};
                 for (uint32_t j = tid; j < nv; j += kThreads) store_vec<T>(ov + (size_t)j * N, zero, whole);
                 if (rank == 0 && tid < s.head) from_f32(out[tid], 0.f);
                 if (rank + 1 == ranks && tid < a.vocab - s.tail0) from_f32(out[s.tail0 + tid], 0.f);
             }
-            if (FORWARD && rank == 0 && tid == 0) {
+            if (FORWARD && !FAR && rank == 0 && tid == 0) {
                 a.loss[row] = 0.f;
                 if (a.lse_out) a.lse_out[2 * row] = a.lse_out[2 * row + 1] = 0.f;
             }
@@ -556,10 +578,10 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
         } else {
             lse_t = now.lse_t;
             lse_1 = now.lse_1;
-            empty = lse_t == -INFINITY;
-            base_t = empty ? 0.f : lse_t * a.temperature;
-            rest_t = empty ? 0.f : fmaf(lse_t, a.temperature, -base_t) * -c_t;
-            base_1 = empty ? 0.f : lse_1;
+            empty = false;
+            base_t = lse_t * a.temperature;
+            rest_t = fmaf(lse_t, a.temperature, -base_t) * -c_t;
+            base_1 = lse_1;
             rest_1 = 0.f;
         }
 
@@ -568,8 +590,9 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
         const float log_teacher = a.teacher_lse ? less_quotient(now.teacher_lse, te.m, a.inv_t, a.temperature) : logf(te.s);   // the lse less te.m / T
         const float mass = !some ? 0.f : a.teacher_lse ? te.s * ex2(-log_teacher * kLog2e) : te.s == te.s ? 1.f : te.s;
         const bool has_label = sm_label[turn & 1] >= 0;
+        const bool skip = !FORWARD && is_far(a, now.lse_t, now.lse_1);   // its gradient is the second launch's
         now = then;
-        if (FORWARD && rank == 0 && tid == 0) {
+        if (FORWARD && !FAR && rank == 0 && tid == 0) {
             float kl = 0.f, ce = 0.f;
             if (some && a.kl_weight != 0.f && mass != 0.f)
                 kl = empty ? INFINITY
@@ -637,11 +660,11 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
         for (uint32_t i = 0; i < (FORWARD ? stay : n); ++i) {
             uint4 q[kU];
             take(q, i, nv);
-            grad_group(q, i);
+            if (!skip) grad_group(q, i);
             issue();
         }
-        if (rank == 0 && tid < s.head) from_f32(out[tid], grad(to_f32(z[tid])));
-        if (rank + 1 == ranks && tid < a.vocab - s.tail0)
+        if (rank == 0 && tid < s.head && !skip) from_f32(out[tid], grad(to_f32(z[tid])));
+        if (rank + 1 == ranks && tid < a.vocab - s.tail0 && !skip)
             from_f32(out[s.tail0 + tid], grad(to_f32(z[s.tail0 + tid])));
 
         // ---- the entries of the slice
@@ -664,8 +687,10 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) k_distill(const 
             }
             from_f32(out[id], grad(sm_z[e]) - take);
         };
-        for (uint32_t e = tid; e < a.k; e += kThreads) put(e);
-        if (tid == kThreads - 1) put(a.k);
+        if (!skip) {
+            for (uint32_t e = tid; e < a.k; e += kThreads) put(e);
+            if (tid == kThreads - 1) put(a.k);
+        }
         if (twice) __syncthreads();   // the next row overwrites entries that others read
     }
     pdl_leave();
@@ -721,9 +746,9 @@ int check(const bf16opt_distill_t *d, const void *loss, bool need_loss, const vo
     return BF16OPT_OK;
 }
 
-template <int kThreads, class T, bool FORWARD, bool GRAD, int POWER>
+template <int kThreads, class T, bool FORWARD, bool GRAD, int POWER, bool FAR = false>
 int launch_k(const Args &a, unsigned cluster, cudaStream_t stream) {
-    auto k = k_distill<kThreads, T, FORWARD, GRAD, POWER>;
+    auto k = k_distill<kThreads, T, FORWARD, GRAD, POWER, FAR>;
     const size_t smem = (size_t)ring_depth(kThreads) * kThreads * kU * 16 + (size_t)(a.k + 1) * 12 + (GRAD ? table_size(a.k) * 4 : 0);
     // As many clusters as fit at once (a cluster of eight cannot use every SM: those of a
     // processing cluster are not a multiple of it), each walking its rows; more would run as a
@@ -761,7 +786,10 @@ int launch_t(const Args &a, int power, cudaStream_t stream) {
         constexpr int POWER = decltype(p)::value;
         if constexpr (kBoth)
             if (large) return launch_k<kLarge, T, FORWARD, GRAD, POWER>(a, cluster, stream);
-        return launch_k<kSmall, T, FORWARD, GRAD, POWER>(a, cluster, stream);
+        const int rc = launch_k<kSmall, T, FORWARD, GRAD, POWER>(a, cluster, stream);
+        if constexpr (!FORWARD)
+            if (rc == BF16OPT_OK) return launch_k<kSmall, T, true, true, POWER, true>(a, cluster, stream);
+        return rc;
     };
     switch (power) {
     case 0: return go(std::integral_constant<int, 0>());

@@ -9,7 +9,8 @@ torch = pytest.importorskip("torch")
 
 import train_ops_reference as R  # noqa: E402
 from mixed_precision_optimizer_bf16_gb300 import train_ops as ops  # noqa: E402
-from test_train_ops_gpu import BF16, F32, check_norm, close, distill_case, gen, loss_scale, norm_case, randn, rowmax  # noqa: E402
+from test_train_ops_gpu import (BF16, F32, INF, check_norm, close, distill_case, gen, loss_scale, norm_case, randn,  # noqa: E402
+                                rowmax)
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
 
@@ -72,6 +73,49 @@ def test_distill_teacher_at_the_types_ends(sign, dtype):
     loss, dz = ops.distill_loss_grad(z, ids, top, **how)
     close(loss, loss_r, loss_scale(z, torch.zeros_like(top), how), "loss")
     close(dz, dz_r, scale, "dlogits")
+
+
+def far_case(rows, vocab, k, dtype, away, temperature, weights=False):
+    z, ids, top, how = distill_case(rows, vocab, k, dtype, 11, labels=True, weights=weights, temperature=temperature)
+    if isinstance(away, str):
+        away = (-1 if away == "lowest" else 1) * torch.finfo(dtype).max
+    z = (z.float() + away).to(dtype)
+    return z, z.double() - away, ids, top, how
+
+
+@pytest.mark.parametrize("temperature", [1.0, 2.0, 1.5, 0.5])
+@pytest.mark.parametrize("away", [300.0, -300.0, 1e4, -1e6, "lowest", "largest"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_distill_backward_far_from_zero(dtype, away, temperature):
+    """The gradient from saved log-sum-exps, whose FP32 number has no room for the sum's logarithm beside a far maximum."""
+    z, near, ids, top, how = far_case(5, 6007, 37, dtype, away, temperature)
+    _, dz_r, scale, _ = R.distill(near, ids, top, **how)
+    dloss = torch.ones(5, device="cuda")
+    lse = ops.distill_forward(z, ids, top, **how)[1]
+    back = ops.distill_backward(z, ids, top, lse, dloss, **how)
+    close(back, dz_r, scale, "dlogits of the backward call")
+    leaf = z.clone().requires_grad_(True)
+    ops.distill_loss(leaf, ids, top, **how).sum().backward()
+    assert torch.equal(leaf.grad, back)
+    assert torch.equal(ops.distill_backward(z, ids, top, lse, dloss, out=z, **how), back)    # in place
+
+
+@pytest.mark.parametrize("dtype,rows,vocab", [(F32, 330, 40001), (BF16, 3, 250880), (BF16, 310, 70001), (F32, 700, 2051)])
+@pytest.mark.parametrize("temperature", [1.0, 4.0])
+def test_distill_backward_far_and_near_rows(dtype, rows, vocab, temperature):
+    """Rows far from zero among others and rows of weight 0, several to each cluster of CTAs; an all-masked row."""
+    z, near, ids, top, how = far_case(rows, vocab, 9, dtype, 0.0, temperature, weights=True)
+    z[1::3] = (z[1::3].float() - 5000).to(dtype)
+    near[1::3] = z[1::3].double() + 5000
+    how["row_weight"][0] = 1.0
+    z[0], near[0], ids[0], how["labels"][0] = -INF, -INF, -1, -1
+    _, dz_r, scale, _ = R.distill(near, ids, top, **how)
+    lse = ops.distill_forward(z, ids, top, **how)[1]
+    back = ops.distill_backward(z, ids, top, lse, **how)
+    close(back, dz_r, scale, "dlogits of the backward call")
+    assert not back[0].any()
+    for _ in range(2):
+        assert torch.equal(ops.distill_backward(z, ids, top, lse, **how), back)
 
 
 # ----------------------------------------------------------------- expert balance
