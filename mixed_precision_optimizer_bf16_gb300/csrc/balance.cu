@@ -540,6 +540,11 @@ __device__ __forceinline__ void copy_async4(void *smem, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(src) : "memory");
 }
 
+// Saved log-sum-exps below this are taken as they are: their rounding is at most 2^-21, the exponents' own. Beside a
+// maximum far from 0 an FP32 number has no room for the sum's logarithm; there the probabilities are divided by
+// their sum (262144 x 256 bf16 75 us either way, 85 us where all tokens are far).
+constexpr float kFar = 16.f;
+
 // What the choices add to their experts' elements goes through a row of shared
 // memory of the warp's own, all zeros between two tokens.
 // RING: a lane's run is one 16-byte vector; tokens come through a ring of the warp's own, copied kRing
@@ -682,9 +687,19 @@ __global__ void __launch_bounds__(kThreads, back_resident(PER)) k_balance_backwa
             }
             s = s2.x + s2.y;
         }
+        float scale = 1.f;
+        if (!(fabsf(lse) < kFar)) {   // the same in all lanes
+            float total = 0.f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) total += z[i];
+            scale = reciprocal(warp_sum(total));
+#pragma unroll
+            for (int i = 0; i < PER; ++i) z[i] *= scale;
+            s *= scale;
+        }
         float extra = 0.f, dot = 0.f;
         if (q.dweights) {
-            float p = id >= 0 ? ex2((zid - lse) * kLog2e) : 0.f;
+            float p = id >= 0 ? ex2((zid - lse) * kLog2e) * scale : 0.f;
             if (a.renormalise) p *= reciprocal(warp_sum(p));
             extra = p * up;
             dot = warp_sum(extra);

@@ -9,8 +9,8 @@ torch = pytest.importorskip("torch")
 
 import train_ops_reference as R  # noqa: E402
 from mixed_precision_optimizer_bf16_gb300 import train_ops as ops  # noqa: E402
-from test_train_ops_gpu import (BF16, F32, INF, check_norm, close, distill_case, gen, loss_scale, norm_case, randn,  # noqa: E402
-                                rowmax)
+from test_train_ops_gpu import (BF16, F32, INF, check_balance, check_norm, close, distill_case, gen, loss_scale,  # noqa: E402
+                                norm_case, randn, rowmax)
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
 
@@ -127,6 +127,18 @@ def from_top(z):
     return z.double() - torch.where(torch.isfinite(top), top, torch.zeros_like(top))
 
 
+def check_balance_far(z, k, **how):
+    """check_balance without a z-loss, for logits anywhere."""
+    dw = torch.randn(z.shape[0], k, device="cuda", generator=gen(11))
+    ids, weights, counts, loss, saved = ops.balance_forward(z, k, **how)
+    dz = ops.balance_backward(z, ids, counts, saved, dw, **how)
+    r = R.balance(from_top(z), k, dweights=dw, **how)
+    assert torch.equal(ids.cpu(), r[0]) and torch.equal(counts.cpu(), r[2])
+    close(weights, r[1], 1.0 * (r[1] != 0), "weights")
+    close(loss, r[3], r[3].abs(), "loss")
+    close(dz, r[4], 0.2 * rowmax(r[4]) + rowmax(dw.double()).cpu(), "dlogits")
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("tokens,groups", [(70, 2), (4000, 1), (4000, 4), (4000, 100)])
 def test_balance_loss_of_the_lowest_logits(tokens, groups, dtype):
@@ -138,3 +150,14 @@ def test_balance_loss_of_the_lowest_logits(tokens, groups, dtype):
     assert torch.equal(got[0].cpu(), want[0]) and torch.equal(got[2].cpu(), want[2])
     close(got[1], want[1], 1.0 * (want[1] != 0), "weights")
     close(got[3], want[3], want[3].abs(), "loss")
+
+
+@pytest.mark.parametrize("renormalise", [True, False])
+@pytest.mark.parametrize("dtype,experts", [(F32, 8), (BF16, 24), (BF16, 64), (BF16, 200), (F32, 256), (F32, 600)])
+@pytest.mark.parametrize("away", [20.0, -300.0, 1e4, -1e6, "lowest", "largest"])
+def test_balance_far_from_zero(dtype, experts, away, renormalise):
+    """Adding a number to a token's logits changes neither its weights nor, without the z-loss, loss and gradient."""
+    if isinstance(away, str):
+        away = (-1 if away == "lowest" else 1) * torch.finfo(dtype).max
+    z = (2 * randn(gen(3), 70, experts) + away).to(dtype)
+    check_balance_far(z, 3, balance_weight=0.5, renormalise=renormalise, groups=2)
