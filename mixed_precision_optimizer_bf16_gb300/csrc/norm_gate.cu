@@ -111,7 +111,7 @@ __device__ __forceinline__ void load8_weight(const void *w, int type, uint32_t n
                                              float none, float (&f)[8]) {
     if (!w) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = column<VEC>(slot, threads, t, i) < n ? none : 0.f;
+        for (int i = 0; i < 8; ++i) f[i] = column<VEC>(slot, threads, t, VEC ? 0 : i) < n ? none : 0.f;
         return;
     }
     if constexpr (VEC) {
