@@ -161,3 +161,23 @@ def test_balance_far_from_zero(dtype, experts, away, renormalise):
         away = (-1 if away == "lowest" else 1) * torch.finfo(dtype).max
     z = (2 * randn(gen(3), 70, experts) + away).to(dtype)
     check_balance_far(z, 3, balance_weight=0.5, renormalise=renormalise, groups=2)
+
+
+# ----------------------------------------------------------------------- many rows
+
+def test_norm_more_rows_than_a_grid_has_blocks_for():
+    """2^33 and a few rows of one column, the stream in place: 34 GB."""
+    rows = 2 ** 33 + 7
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("34 GB of device memory wanted")
+    x = torch.empty(rows, 1, dtype=BF16, device="cuda")
+    y = torch.empty(rows, 1, dtype=BF16, device="cuda")
+    for a in range(0, rows, 1 << 30):
+        b = min(rows, a + (1 << 30))
+        y[a:b] = torch.randint(-100, 100, (b - a, 1), device="cuda", dtype=torch.int8)
+        x[a:b] = 8.0
+    d = ops.C.bf16opt_norm_gate_t(rows, 1, 0, 0, 0, 0, 0, 0, 0, 0, None, None, None, None, None, 1.0, 1.0, 1e-5)
+    ops.C.check(ops.C.bf16opt_norm_gate_forward(d, x.data_ptr(), y.data_ptr(), x.data_ptr(), None, None, torch.cuda.current_stream().cuda_stream))
+    for a in range(0, rows, 1 << 30):
+        b = min(rows, a + (1 << 30))
+        assert torch.equal(x[a:b], y[a:b] + 8.0)       # whole numbers below 2^8: exact
