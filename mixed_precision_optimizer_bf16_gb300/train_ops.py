@@ -75,16 +75,16 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 
 
 def _on_stream(call):
-    """Gives a function `stream=None`: it runs on the device of its first tensor,
-    on `stream` or on that device's current one.  Its inputs are marked as used
+    """Gives a function `stream=None`: it runs on the device of its first tensor
+    (by place or by name), on `stream` or on that device's current one.  Its inputs are marked as used
     on a stream that is not the current one, so that their memory outlives the
     kernels."""
     @functools.wraps(call)
     def run(*args, stream=None, **more):
-        for first in args:
-            if first is not None:
-                break
-        if not isinstance(first, _Tensor) or not first.is_cuda or (stream is None and first.get_device() == _current_device()):
+        first = args[0] if args else None
+        if not isinstance(first, _Tensor):
+            first = next((t for t in (*args, *more.values()) if isinstance(t, _Tensor)), None)
+        if first is None or not first.is_cuda or (stream is None and first.get_device() == _current_device()):
             return call(*args, **more)
         index = first.get_device()
         with contextlib.ExitStack() as stack:

@@ -163,6 +163,44 @@ def test_balance_far_from_zero(dtype, experts, away, renormalise):
     check_balance_far(z, 3, balance_weight=0.5, renormalise=renormalise, groups=2)
 
 
+# -------------------------------------------------------- autograd, outputs, streams
+
+def test_tensors_by_name():
+    z, ids, top, how = distill_case(6, 300, 5, F32, 1, labels=True)
+    named = dict(logits=z, teacher_ids=ids, teacher_logits=top, **how)
+    loss, lse = ops.distill_forward(**named)
+    for a, b in zip((loss, lse), ops.distill_forward(z, ids, top, **how)):
+        assert torch.equal(a, b)
+    assert torch.equal(ops.distill_backward(lse=lse, **named), ops.distill_backward(z, ids, top, lse, **how))
+    assert torch.equal(ops.distill_loss_grad(**named)[1], ops.distill_loss_grad(z, ids, top, **how)[1])
+    x, y, nh = norm_case(6, 72, F32, F32, F32, "rms", "rms", 0)
+    r, h, stats = ops.norm_gate_forward(x=x, y=y, **nh)
+    got, want = ops.norm_gate_backward(dr=r, dh=h, r=r, y=y, stats=stats, **nh), ops.norm_gate_backward(r, h, r, y, stats, **nh)
+    assert torch.equal(got["dy"], want["dy"]) and torch.equal(got["dpre_weight"], want["dpre_weight"])
+    zb = randn(gen(2), 24, 8)
+    b = ops.balance_forward(logits=zb, k=2)
+    assert torch.equal(ops.balance_backward(logits=zb, ids=b[0], counts=b[2], saved=b[4]), ops.balance_backward(zb, b[0], b[2], b[4]))
+
+
+@pytest.mark.parametrize("named", [False, True])
+def test_a_stream_is_taken_where_the_first_tensors_are_not_there(named, monkeypatch):
+    """norm_gate_backward without dr, or with every tensor by name, launches on the stream that it was given."""
+    x, y, nh = norm_case(24, 264, F32, F32, F32, "rms", "layer", 0)
+    r, h, stats = ops.norm_gate_forward(x, y, **nh)
+    want = ops.norm_gate_backward(None, h, r, y, stats, **nh)
+    streams = []
+    backward = ops.C.bf16opt_norm_gate_backward
+    monkeypatch.setattr(ops.C, "bf16opt_norm_gate_backward", lambda *a: streams.append(a[-1]) or backward(*a))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    how = dict(dh=h, r=r, y=y, stats=stats, stream=side, **nh)
+    got = ops.norm_gate_backward(dr=None, **how) if named else ops.norm_gate_backward(None, **how)
+    torch.cuda.synchronize()
+    assert streams == [side.cuda_stream]
+    for n in ("dx", "dy", "dpre_weight"):
+        assert torch.equal(got[n], want[n])
+
+
 # ----------------------------------------------------------------------- many rows
 
 def test_norm_more_rows_than_a_grid_has_blocks_for():
