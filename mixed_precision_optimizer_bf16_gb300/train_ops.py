@@ -10,6 +10,9 @@ can be captured in a CUDA graph.
   distill_forward / distill_backward / distill_loss_grad, distill_loss (autograd)
   norm_gate_forward / norm_gate_backward, norm_gate (autograd)
   balance_forward / balance_backward, balance (autograd)
+
+The autograd forms have first derivatives only: going through a gradient of theirs once more
+is an error.
 """
 import contextlib
 import functools
@@ -98,6 +101,31 @@ def _on_stream(call):
     return run
 
 
+class _First(torch.autograd.Function):
+    """A gradient as it is; to go through it once more is an error."""
+    @staticmethod
+    def forward(ctx, gradient):
+        return gradient.detach()
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("train_ops: these operators have no second derivative")
+
+
+def _first_only(backward):
+    """For the backward of an autograd form: under create_graph its gradients, which come from raw
+    pointers, would else pass for constants.  (once_differentiable sees only the incoming gradients, and lets
+    those of a plain sum through.)"""
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        return tuple(_First.apply(g.detach().requires_grad_()) if g is not None else None for g in out)
+    return run
+
+
 # ------------------------------------------------------------------ distillation
 
 def _distill(logits, teacher_ids, teacher_logits, temperature, kl_weight, ce_weight, labels, row_weight, teacher_lse):
@@ -179,6 +207,7 @@ class _Distill(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @_first_only
     def backward(ctx, dloss):
         logits, ids, top, lse, *tensors = ctx.saved_tensors
         return (distill_backward(logits, ids, top, lse, dloss.float().contiguous(), **ctx.how,
@@ -290,6 +319,7 @@ class _NormGate(torch.autograd.Function):
         return r, h
 
     @staticmethod
+    @_first_only
     def backward(ctx, dr, dh):
         if dr is None and dh is None:
             return (None,) * 8
@@ -381,6 +411,7 @@ class _Balance(torch.autograd.Function):
         return ids, weights, counts, loss
 
     @staticmethod
+    @_first_only
     def backward(ctx, _ids, dweights, _counts, dloss):
         if dweights is None and dloss is None:
             return None, None, None, None

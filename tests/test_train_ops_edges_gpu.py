@@ -165,6 +165,30 @@ def test_balance_far_from_zero(dtype, experts, away, renormalise):
 
 # -------------------------------------------------------- autograd, outputs, streams
 
+def graphs():
+    """Each operator on leaves of its own: (leaf, outputs)."""
+    z, ids, top, how = distill_case(6, 300, 5, F32, 1, labels=True, temperature=2.0)
+    z.requires_grad_(True)
+    yield "distill", z, ops.distill_loss(z, ids, top, **how).sum()
+    x, y, nh = norm_case(6, 72, F32, F32, F32, "rms", "layer", 1)
+    y.requires_grad_(True)
+    r, h = ops.norm_gate(x, y, **nh)
+    yield "norm", y, (r * r).sum() + (h * h * h).sum()
+    z = randn(gen(2), 24, 8).requires_grad_(True)
+    ids, w, counts, loss = ops.balance(z, 2, z_weight=0.1)
+    yield "balance", z, (w * w).sum() + loss
+
+
+def test_gradients_of_gradients_are_refused():
+    """create_graph keeps the gradients themselves; going through them once more is an error, not a constant."""
+    for name, leaf, value in graphs():
+        plain, = torch.autograd.grad(value, leaf, retain_graph=True)
+        first, = torch.autograd.grad(value, leaf, create_graph=True)
+        assert torch.equal(first, plain), name
+        with pytest.raises(RuntimeError, match="train_ops"):
+            (value + first.square().sum()).backward()
+
+
 def test_tensors_by_name():
     z, ids, top, how = distill_case(6, 300, 5, F32, 1, labels=True)
     named = dict(logits=z, teacher_ids=ids, teacher_logits=top, **how)
