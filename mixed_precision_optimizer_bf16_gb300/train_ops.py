@@ -65,6 +65,19 @@ def _matrix(t, what):
     return rows, columns, t.get_device()
 
 
+def _writable(t, what):
+    """An output of the caller's: autograd has to be able to do without its old values, and to see that they are gone."""
+    if t.requires_grad and torch.is_grad_enabled() and (t.is_leaf or (t._is_view() and t._base.is_leaf)):
+        raise ValueError(f"{what}: a leaf (or a view of one) that requires a gradient is not written in place")
+
+
+def _written(*outs):
+    """The caller's outputs of a call that has gone through: their versions move on, as under torch's own writes."""
+    for t in outs:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _stride(t):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
@@ -166,6 +179,7 @@ def _dlogits(logits, out, index):
     if out is None:
         return _empty_like(logits, memory_format=torch.contiguous_format)
     _need(out, "out", (logits.dtype,), logits.shape, index, True)
+    _writable(out, "out")
     return out
 
 
@@ -179,8 +193,9 @@ def distill_backward(logits, teacher_ids, teacher_logits, lse, dloss=None, *, te
     _need(lse, "lse", _F32, (rows, 2), index)
     if dloss is not None:
         _need(dloss, "dloss", _F32, (rows,), index)
-    out = _dlogits(logits, out, index)
+    given, out = out, _dlogits(logits, out, index)
     C.check(C.bf16opt_distill_backward(d, lse.data_ptr(), _p(dloss), out.data_ptr(), _stride(out), _raw_stream(index)))
+    _written(given)
     return out
 
 
@@ -193,8 +208,9 @@ def distill_loss_grad(logits, teacher_ids, teacher_logits, dloss=None, *, temper
     if dloss is not None:
         _need(dloss, "dloss", _F32, (rows,), index)
     loss = _empty(rows, dtype=torch.float32, device=logits.device)
-    out = _dlogits(logits, out, index)
+    given, out = out, _dlogits(logits, out, index)
     C.check(C.bf16opt_distill_loss_grad(d, _p(dloss), loss.data_ptr(), 0, out.data_ptr(), _stride(out), _raw_stream(index)))
+    _written(given)
     return loss, out
 
 
@@ -262,12 +278,15 @@ def norm_gate_forward(x, y, *, pre="rms", post="rms", pre_weight=None, pre_bias=
                                 residual_scale, branch_scale, eps)
     if out_r is not None:
         _need(out_r, "out_r", (x.dtype,), x.shape, index)
+        _writable(out_r, "out_r")
     if out_h is not None:
         _need(out_h, "out_h", (y.dtype,), y.shape, index)
+        _writable(out_h, "out_h")
     r = out_r if out_r is not None else _empty_like(x)
     h = out_h if out_h is not None or not _NORM[pre] else _empty_like(y)
     stats = _empty((rows, 4), dtype=torch.float32, device=y.device)
     C.check(C.bf16opt_norm_gate_forward(d, x.data_ptr(), y.data_ptr(), r.data_ptr(), _p(h), stats.data_ptr(), _raw_stream(index)))
+    _written(out_r, out_h)
     return r, h, stats
 
 
@@ -394,9 +413,10 @@ def balance_backward(logits, ids, counts, saved, dweights=None, dloss=None, *, m
         _need(dweights, "dweights", _F32, (tokens, k), index)
     if dloss is not None:
         _need(dloss, "dloss", _F32, dloss.shape if isinstance(dloss, _Tensor) and dloss.numel() == 1 else (1,), index)
-    out = _dlogits(logits, out, index)
+    given, out = out, _dlogits(logits, out, index)
     C.check(C.bf16opt_balance_backward(d, ids.data_ptr(), counts.data_ptr(), saved.data_ptr(), _p(dweights), _p(dloss),
                                        out.data_ptr(), _stride(out), _raw_stream(index)))
+    _written(given)
     return out
 
 

@@ -189,6 +189,63 @@ def test_gradients_of_gradients_are_refused():
             (value + first.square().sum()).backward()
 
 
+def test_written_tensors_are_marked_as_written():
+    z, ids, top, how = distill_case(6, 300, 5, BF16, 1, labels=True)
+    lse = ops.distill_forward(z, ids, top, **how)[1]
+    for call in (lambda o: ops.distill_backward(z, ids, top, lse, out=o, **how),
+                 lambda o: ops.distill_loss_grad(z, ids, top, out=o, **how)):
+        o = torch.empty_like(z)
+        before = o._version
+        call(o)
+        assert o._version > before
+    zb = randn(gen(2), 24, 8)
+    b = ops.balance_forward(zb, 2)
+    o = torch.empty_like(zb)
+    before = o._version
+    ops.balance_backward(zb, b[0], b[2], b[4], out=o)
+    assert o._version > before
+    x, y, nh = norm_case(6, 72, BF16, BF16, BF16, "rms", "rms", 0)
+    xv, yv = x._version, y._version
+    ops.norm_gate_forward(x, y, out_r=x, out_h=y, **nh)
+    assert x._version > xv and y._version > yv
+    with torch.inference_mode():                       # such tensors have no version
+        ops.distill_loss_grad(z.clone(), ids, top, out=torch.empty_like(z), **how)
+
+
+def test_a_saved_tensor_that_was_overwritten_is_an_error():
+    """A loss by autograd, then both at once over the same logits in place, then the first one's backward."""
+    z, ids, top, how = distill_case(6, 300, 5, F32, 1, labels=True)
+    leaf = z.clone().requires_grad_(True)
+    logits = leaf * 1.0
+    loss = ops.distill_loss(logits, ids, top, **how)
+    _, dlogits = ops.distill_loss_grad(logits, ids, top, out=logits, **how)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.sum().backward()
+    logits = leaf + 1.0                                # nothing saved: the gradient goes on from where the logits were
+    _, dlogits = ops.distill_loss_grad(logits, ids, top, out=logits, **how)
+    logits.backward(dlogits.detach().clone())
+    assert torch.equal(leaf.grad, ops.distill_loss_grad(z + 1.0, ids, top, **how)[1])
+
+
+def test_a_leaf_that_requires_a_gradient_is_not_written():
+    z, ids, top, how = distill_case(6, 300, 5, F32, 1, labels=True)
+    lse = ops.distill_forward(z, ids, top, **how)[1]
+    zb = randn(gen(2), 24, 8)
+    b = ops.balance_forward(zb, 2)
+    x, y, nh = norm_case(6, 72, F32, F32, F32, "rms", "rms", 0)
+    calls = [(z, lambda o: ops.distill_loss_grad(z, ids, top, out=o, **how)), (z, lambda o: ops.distill_backward(z, ids, top, lse, out=o, **how)),
+             (zb, lambda o: ops.balance_backward(zb, b[0], b[2], b[4], out=o)), (x, lambda o: ops.norm_gate_forward(x, y, out_r=o, **nh)),
+             (y, lambda o: ops.norm_gate_forward(x, y, out_h=o, **nh))]
+    for like, call in calls:
+        for leaf in (torch.zeros_like(like).requires_grad_(True), torch.zeros_like(like).requires_grad_(True)[:]):
+            with pytest.raises(ValueError, match="requires a gradient"):
+                call(leaf)
+            assert not leaf.any()
+        with torch.no_grad():
+            call(leaf)
+        assert bool(leaf.any())
+
+
 def test_tensors_by_name():
     z, ids, top, how = distill_case(6, 300, 5, F32, 1, labels=True)
     named = dict(logits=z, teacher_ids=ids, teacher_logits=top, **how)
