@@ -301,12 +301,19 @@ def _norm_gate_workspace(rows, hidden, types, gate_rows, index):
     return nbytes
 
 
-@_on_stream
 def norm_gate_backward(dr, dh, r, y, stats, *, pre="rms", post="rms", pre_weight=None, pre_bias=None, post_weight=None,
-                       post_bias=None, gate=None, gate_act="none", residual_scale=1.0, branch_scale=1.0, eps=1e-5):
+                       post_bias=None, gate=None, gate_act="none", residual_scale=1.0, branch_scale=1.0, eps=1e-5, stream=None):
     """Gradients of norm_gate_forward from those of r (dr, None: 0) and h (dh,
     None: 0): a dict of dx, dy, dgate, dpre_weight, dpre_bias, dpost_weight and
     dpost_bias, None for what is not there."""
+    return _norm_gate_backward((True,) * 5, dr, dh, r, y, stats, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate,
+                               gate_act, residual_scale, branch_scale, eps, stream=stream)
+
+
+@_on_stream
+def _norm_gate_backward(want, dr, dh, r, y, stats, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate, gate_act,
+                        residual_scale, branch_scale, eps):
+    """want: whether the gradients of gate, pre_weight, pre_bias, post_weight and post_bias are asked for."""
     stream_t = r if r is not None else dr
     d, rows, index = _norm_gate(stream_t, "r", y, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate, gate_act,
                                 residual_scale, branch_scale, eps)
@@ -317,8 +324,8 @@ def norm_gate_backward(dr, dh, r, y, stats, *, pre="rms", post="rms", pre_weight
         _need(dh, "dh", (y.dtype,), (rows, hidden), index)
     _need(stats, "stats", _F32, (rows, 4), index)
     dx, dy = _empty_like(stream_t), _empty_like(y)
-    dgate, dw1, db1, dw2, db2 = (_empty_like(t) if t is not None else None
-                                 for t in (gate, pre_weight, pre_bias, post_weight, post_bias))
+    dgate, dw1, db1, dw2, db2 = (_empty_like(t) if t is not None and w else None
+                                 for t, w in zip((gate, pre_weight, pre_bias, post_weight, post_bias), want))
     nbytes = _norm_gate_workspace(rows, hidden, (_TYPE[y.dtype], _TYPE[stream_t.dtype]), gate.shape[0] if gate is not None else 0, index)
     ws = _empty(nbytes, dtype=torch.uint8, device=y.device)
     C.check(C.bf16opt_norm_gate_backward(d, _p(dr), _p(dh), _p(r), y.data_ptr(), stats.data_ptr(), dx.data_ptr(),
@@ -343,9 +350,10 @@ class _NormGate(torch.autograd.Function):
         if dr is None and dh is None:
             return (None,) * 8
         r, y, stats, pre_weight, pre_bias, post_weight, post_bias, gate = ctx.saved_tensors
-        g = norm_gate_backward(dr.contiguous() if dr is not None else None, dh.contiguous() if dh is not None else None,
-                               r, y, stats, pre_weight=pre_weight, pre_bias=pre_bias, post_weight=post_weight,
-                               post_bias=post_bias, gate=gate, **ctx.how)
+        _, _, *weights, wants_gate, _ = ctx.needs_input_grad
+        g = _norm_gate_backward((wants_gate, *weights), dr.contiguous() if dr is not None else None,
+                                dh.contiguous() if dh is not None else None, r, y, stats, pre_weight=pre_weight, pre_bias=pre_bias,
+                                post_weight=post_weight, post_bias=post_bias, gate=gate, **ctx.how)
         return (g["dx"], g["dy"], g["dpre_weight"], g["dpre_bias"], g["dpost_weight"], g["dpost_bias"], g["dgate"], None)
 
 

@@ -246,6 +246,34 @@ def test_a_leaf_that_requires_a_gradient_is_not_written():
         assert bool(leaf.any())
 
 
+def test_frozen_weights_cost_nothing(monkeypatch):
+    """Gradients that nobody asked for are not computed."""
+    x, y, nh = norm_case(24, 264, F32, F32, F32, "layer", "layer", 3)
+    names = ["gate", "pre_weight", "pre_bias", "post_weight", "post_bias"]
+    asked = []
+    backward = ops.C.bf16opt_norm_gate_backward
+
+    def recorded(d, dr, dh, r, yy, stats, dx, dy, *weights):
+        asked.append([bool(w) for w in weights[:5]])
+        return backward(d, dr, dh, r, yy, stats, dx, dy, *weights)
+    monkeypatch.setattr(ops.C, "bf16opt_norm_gate_backward", recorded)
+
+    def grads(wanted):
+        leaves = {n: nh[n].clone().requires_grad_(n in wanted) for n in names}
+        yy = y.clone().requires_grad_(True)
+        r, h = ops.norm_gate(x, yy, **{**nh, **leaves})
+        ((r * r).sum() + h.square().sum()).backward()
+        return {"y": yy.grad, **{n: leaves[n].grad for n in names}}
+    everything = grads(names)
+    for wanted in ([], ["gate"], ["pre_bias"], ["post_weight"], ["gate", "pre_weight", "post_bias"]):
+        got = grads(wanted)
+        assert asked[-1] == [n in wanted for n in names]
+        for n, v in got.items():
+            assert (v is None) == (n != "y" and n not in wanted)
+            if v is not None:
+                assert torch.equal(v, everything[n]), n
+
+
 def test_tensors_by_name():
     z, ids, top, how = distill_case(6, 300, 5, F32, 1, labels=True)
     named = dict(logits=z, teacher_ids=ids, teacher_logits=top, **how)
