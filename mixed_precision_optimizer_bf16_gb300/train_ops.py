@@ -235,7 +235,12 @@ _DISTILL_TENSORS = ("labels", "row_weight", "teacher_lse")
 
 def distill_loss(logits, teacher_ids, teacher_logits, *, temperature=1.0, kl_weight=1.0, ce_weight=0.0, labels=None,
                  row_weight=None, teacher_lse=None):
-    """The rows' losses [rows] as distill_forward, differentiable in logits."""
+    """The rows' losses [rows] as distill_forward, differentiable in logits.
+    The teacher is a constant: no gradient goes to teacher_logits or
+    teacher_lse.  A row_weight that requires a gradient is refused (multiply the
+    losses by it instead)."""
+    if isinstance(row_weight, _Tensor) and row_weight.requires_grad and torch.is_grad_enabled():
+        raise ValueError("row_weight: requires a gradient, which the loss does not give; multiply the losses by it, or detach it")
     return _Distill.apply(logits, teacher_ids, teacher_logits,
                           dict(temperature=temperature, kl_weight=kl_weight, ce_weight=ce_weight, labels=labels,
                                row_weight=row_weight, teacher_lse=teacher_lse))

@@ -274,6 +274,15 @@ def test_frozen_weights_cost_nothing(monkeypatch):
                 assert torch.equal(v, everything[n]), n
 
 
+def test_a_row_weight_that_requires_a_gradient_is_refused():
+    z, ids, top, how = distill_case(6, 300, 5, F32, 1, labels=True, weights=True)
+    how["row_weight"].requires_grad_(True)
+    with pytest.raises(ValueError, match="row_weight"):
+        ops.distill_loss(z.requires_grad_(True), ids, top, **how)
+    with torch.no_grad():
+        assert ops.distill_loss(z, ids, top, **how).shape == (6,)
+
+
 def test_tensors_by_name():
     z, ids, top, how = distill_case(6, 300, 5, F32, 1, labels=True)
     named = dict(logits=z, teacher_ids=ids, teacher_logits=top, **how)
