@@ -577,7 +577,8 @@ int bf16opt_norm_gate_backward(const bf16opt_norm_gate_t *d, const void *dr, con
  * A masked token has ids -1, weights and gradient 0.  An expert whose logit
  * is -inf is never chosen (missing choices: id -1, weight 0, not counted); a token whose logits
  * all are is as if masked.  A NaN is chosen after every number but before -inf;
- * it makes the token's weights, the loss and the group's gradient NaN. */
+ * it makes the token's weights and gradient and the loss NaN (the other tokens'
+ * gradients depend on it through the counts alone). */
 #define BF16OPT_BALANCE_MAX_EXPERTS 1024
 #define BF16OPT_BALANCE_MAX_K 32
 

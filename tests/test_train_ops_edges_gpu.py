@@ -163,6 +163,24 @@ def test_balance_far_from_zero(dtype, experts, away, renormalise):
     check_balance_far(z, 3, balance_weight=0.5, renormalise=renormalise, groups=2)
 
 
+def test_balance_nan_backward_stays_in_its_token():
+    """A NaN makes its token's gradient NaN; the counts, which the others' depend on, stay whole numbers."""
+    for dtype, experts in ((F32, 40), (BF16, 64), (BF16, 256)):
+        z = randn(gen(4), 130, experts).to(dtype)
+        z[10, 7] = z[77, 0] = float("nan")
+        up = torch.randn(130, 5, device="cuda", generator=gen(5))
+        how = dict(balance_weight=0.3, z_weight=0.1, groups=2)
+        ids, w, counts, loss, saved = ops.balance_forward(z, 5, **how)
+        dz = ops.balance_backward(z, ids, counts, saved, up, **how)
+        want = R.balance(z, 5, dweights=up, **how)
+        assert torch.equal(ids.cpu(), want[0]) and torch.equal(counts.cpu(), want[2]) and bool(torch.isnan(loss))
+        keep = torch.ones(130, dtype=torch.bool)
+        keep[[10, 77]] = False
+        assert bool(torch.isnan(dz[[10, 77]]).all()) and bool(torch.isnan(w[[10, 77]]).all())
+        close(dz.cpu()[keep], want[4][keep], 0.2 * want[4][keep].abs().amax(1, keepdim=True) + up.double().cpu()[keep].abs().amax(1, keepdim=True),
+              "dlogits")
+
+
 # -------------------------------------------------------- autograd, outputs, streams
 
 def graphs():
