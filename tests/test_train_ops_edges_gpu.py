@@ -9,8 +9,8 @@ torch = pytest.importorskip("torch")
 
 import train_ops_reference as R  # noqa: E402
 from mixed_precision_optimizer_bf16_gb300 import train_ops as ops  # noqa: E402
-from test_train_ops_gpu import (BF16, F32, INF, check_balance, check_norm, close, distill_case, gen, loss_scale,  # noqa: E402
-                                norm_case, randn, rowmax)
+from test_train_ops_gpu import (BF16, F32, INF, check_balance, check_distill, check_norm, close, distill_case, gen,  # noqa: E402
+                                loss_scale, norm_case, randn, rowmax)
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
 
@@ -118,6 +118,13 @@ def test_distill_backward_far_and_near_rows(dtype, rows, vocab, temperature):
         assert torch.equal(ops.distill_backward(z, ids, top, lse, **how), back)
 
 
+@pytest.mark.parametrize("dtype,rows,vocab", [(BF16, 400, 130001), (F32, 330, 40001)])
+def test_distill_rows_of_weight_zero_in_clusters(dtype, rows, vocab):
+    """Several CTAs to a row and several rows to a cluster, some of weight 0."""
+    z, ids, top, how = distill_case(rows, vocab, 9, dtype, 14, labels=True, weights=True, temperature=2.0)
+    check_distill(z, ids, top, how)
+
+
 # ----------------------------------------------------------------- expert balance
 
 def from_top(z):
@@ -179,6 +186,109 @@ def test_balance_nan_backward_stays_in_its_token():
         assert bool(torch.isnan(dz[[10, 77]]).all()) and bool(torch.isnan(w[[10, 77]]).all())
         close(dz.cpu()[keep], want[4][keep], 0.2 * want[4][keep].abs().amax(1, keepdim=True) + up.double().cpu()[keep].abs().amax(1, keepdim=True),
               "dlogits")
+
+
+@pytest.mark.parametrize("experts", [33, 40, 64, 100, 128, 200, 256])
+@pytest.mark.parametrize("k", [1, 5, 8, 9, 32])
+def test_balance_bf16_ties_off_experts_and_nan(experts, k):
+    """The choice from sorted keys of 16 bits: many ties, both zeros, experts that are off, NaN, more than eight choices."""
+    tokens = 60
+    z = torch.randint(-2, 3, (tokens, experts), device="cuda", generator=gen(experts)).bfloat16()
+    zero = (z == 0) & (torch.rand(tokens, experts, device="cuda", generator=gen(1)) < 0.5)
+    z[zero] = -0.0
+    z[3, min(2, k):] = -INF                           # two experts on, or as many as are chosen
+    z[4] = -INF
+    z[5, ::2] = -INF
+    z[6] = torch.finfo(BF16).min                      # a number like any other
+    z[7, 1:] = torch.finfo(BF16).min
+    z[8, 1:] = -INF
+    check_balance_far(z, k, balance_weight=0.1)
+    bad = z.clone()
+    bad[10, 7] = float("nan")
+    bad[11, : experts - 1] = float("nan")             # one number, the rest NaN
+    bad[12, 1::2] = -INF
+    bad[12, 0] = -float("nan")
+    bad[13] = float("nan")
+    got = ops.balance_forward(bad, k)
+    want = R.balance(from_top(bad), k)
+    assert torch.equal(got[0].cpu(), want[0]) and torch.equal(got[2].cpu(), want[2])
+    odd = [10, 11, 12, 13]
+    there = got[0][odd] >= 0
+    assert bool(torch.isnan(got[1][odd][there]).all()) and not got[1][odd][~there].any() and bool(torch.isnan(got[3]))
+    keep = [t for t in range(tokens) if t not in odd]
+    close(got[1].cpu()[keep], want[1][keep], 1.0 * (want[1][keep] != 0), "weights")
+
+
+def balance_plain(z, k, mask, groups, balance_weight, z_weight, renormalise, dweights, dloss):
+    """R.balance for many tokens: by whole tensors, on their device, without NaN."""
+    z = z.double()
+    tokens, experts = z.shape
+    live = (mask.bool() & ~(z == -INF).all(1))[:, None]
+    p, lse = R._soft(z)
+    order = torch.argsort(z, dim=1, descending=True, stable=True)[:, :k]
+    there = live & (z.gather(1, order) != -INF)
+    w = torch.where(there, p.gather(1, order), 0.0)
+    weights = w / torch.where(live, w.sum(1, keepdim=True), 1.0) if renormalise else w
+    sent = torch.zeros_like(z).scatter_add_(1, order, there.double())
+    counts = sent.reshape(groups, -1, experts).sum(1)
+    n = live.double().reshape(groups, -1).sum(1, keepdim=True)
+    f = (counts * experts / (k * n.clamp(min=1))).repeat_interleave(tokens // groups, 0)
+    per = (dloss / (groups * n.clamp(min=1))).repeat_interleave(tokens // groups, 0)
+    lse = torch.where(live, lse[:, None], 0.0)
+    dz = per * (balance_weight * p * (f - (p * f).sum(1, keepdim=True)) + 2 * z_weight * lse * p)
+    if dweights is not None:
+        u = torch.where(there, dweights.double(), 0.0)
+        dot = (weights * u).sum(1, keepdim=True)
+        dz = dz.scatter_add(1, order, weights * (u - dot) if renormalise else weights * u) - (0.0 if renormalise else p * dot)
+    return torch.where(there, order, -1).int(), weights, counts.int(), torch.where(live, dz, 0.0)
+
+
+@pytest.mark.parametrize("experts", [136, 200, 256])
+@pytest.mark.parametrize("groups", [1, 6, 900])
+@pytest.mark.parametrize("renormalise", [True, False])
+def test_balance_backward_ring(experts, groups, renormalise):
+    """bf16 and 129 to 256 experts, several tokens to a warp: groups, masked tokens, experts that are off, rows apart, in place."""
+    tokens, k = 19800, 7
+    g = gen(groups)
+    z = randn(g, tokens, experts).bfloat16()
+    z[torch.rand(tokens, experts, device="cuda", generator=g) < 0.05] = -INF
+    z[3, 4:] = -INF                                   # fewer than k
+    z[5::50] = -INF
+    mask = torch.rand(tokens, device="cuda", generator=g) < 0.7
+    mask[tokens // groups: 2 * (tokens // groups)] = False
+    mask[:4] = True
+    how = dict(groups=groups, mask=mask, renormalise=renormalise, balance_weight=0.3, z_weight=0.01)
+    up = torch.randn(tokens, k, device="cuda", generator=gen(11))
+    dloss = torch.tensor(0.6, device="cuda")
+    ids, w, counts, loss, saved = ops.balance_forward(z, k, **how)
+    dz = ops.balance_backward(z, ids, counts, saved, up, dloss, **how)
+    want = balance_plain(z, k, dweights=up, dloss=0.6, **how)
+    assert torch.equal(ids, want[0]) and torch.equal(counts, want[2])
+    close(w, want[1], 1.0 * (want[1] != 0), "weights")
+    close(dz, want[3], 0.2 * rowmax(want[3]) + rowmax(up.double()), "dlogits")
+    wide = torch.full((tokens, experts + 16), 5.0, dtype=BF16, device="cuda")
+    apart = wide[:, 8:8 + experts]
+    apart.copy_(z)
+    got = ops.balance_backward(apart, ids, counts, saved, up, dloss, out=apart, **how)
+    assert torch.equal(got, dz) and bool((wide[:, :8] == 5).all() and (wide[:, 8 + experts:] == 5).all())
+    alone = ops.balance_backward(z, ids, counts, saved, None, **how)
+    want = balance_plain(z, k, dweights=None, dloss=1.0, **how)
+    close(alone, want[3], 0.2 * rowmax(want[3]), "dlogits without the weights' gradients")
+
+
+def test_balance_plain_against_the_reference():
+    """The form for many tokens is the one token by token."""
+    z = randn(gen(7), 120, 24).bfloat16()
+    z[torch.rand(120, 24, device="cuda", generator=gen(8)) < 0.2] = -INF
+    z[5] = z[40, 2:] = -INF
+    mask = torch.rand(120, device="cuda", generator=gen(9)) < 0.7
+    mask[24:48] = False
+    up = torch.randn(120, 3, device="cuda", generator=gen(11))
+    for renormalise in (True, False):
+        how = dict(mask=mask, groups=5, balance_weight=0.3, z_weight=0.01, renormalise=renormalise, dweights=up, dloss=0.6)
+        got, want = balance_plain(z, 3, **how), R.balance(z, 3, **how)
+        assert torch.equal(got[0].cpu(), want[0]) and torch.equal(got[2].cpu(), want[2])
+        assert float((got[1].cpu() - want[1]).abs().max()) < 1e-13 and float((got[3].cpu() - want[4]).abs().max()) < 1e-13
 
 
 # -------------------------------------------------------- autograd, outputs, streams
