@@ -311,13 +311,13 @@ def norm_gate_backward(dr, dh, r, y, stats, *, pre="rms", post="rms", pre_weight
     """Gradients of norm_gate_forward from those of r (dr, None: 0) and h (dh,
     None: 0): a dict of dx, dy, dgate, dpre_weight, dpre_bias, dpost_weight and
     dpost_bias, None for what is not there."""
-    return _norm_gate_backward((True,) * 5, dr, dh, r, y, stats, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate,
-                               gate_act, residual_scale, branch_scale, eps, stream=stream)
+    return _norm_gate_backward(dr, dh, r, y, stats, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate, gate_act,
+                               residual_scale, branch_scale, eps, stream=stream)
 
 
 @_on_stream
-def _norm_gate_backward(want, dr, dh, r, y, stats, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate, gate_act,
-                        residual_scale, branch_scale, eps):
+def _norm_gate_backward(dr, dh, r, y, stats, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate, gate_act,
+                        residual_scale, branch_scale, eps, want=(True,) * 5):
     """want: whether the gradients of gate, pre_weight, pre_bias, post_weight and post_bias are asked for."""
     stream_t = r if r is not None else dr
     d, rows, index = _norm_gate(stream_t, "r", y, pre, post, pre_weight, pre_bias, post_weight, post_bias, gate, gate_act,
@@ -356,9 +356,9 @@ class _NormGate(torch.autograd.Function):
             return (None,) * 8
         r, y, stats, pre_weight, pre_bias, post_weight, post_bias, gate = ctx.saved_tensors
         _, _, *weights, wants_gate, _ = ctx.needs_input_grad
-        g = _norm_gate_backward((wants_gate, *weights), dr.contiguous() if dr is not None else None,
-                                dh.contiguous() if dh is not None else None, r, y, stats, pre_weight=pre_weight, pre_bias=pre_bias,
-                                post_weight=post_weight, post_bias=post_bias, gate=gate, **ctx.how)
+        g = _norm_gate_backward(dr.contiguous() if dr is not None else None, dh.contiguous() if dh is not None else None,
+                                r, y, stats, pre_weight=pre_weight, pre_bias=pre_bias, post_weight=post_weight,
+                                post_bias=post_bias, gate=gate, want=(wants_gate, *weights), **ctx.how)
         return (g["dx"], g["dy"], g["dpre_weight"], g["dpre_bias"], g["dpost_weight"], g["dpost_bias"], g["dgate"], None)
 
 
