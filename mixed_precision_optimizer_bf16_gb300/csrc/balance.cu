@@ -179,7 +179,7 @@ __device__ __forceinline__ float reciprocal(float x) {   // to one unit in the l
     return y;
 }
 // The z-loss of a group; 0 where its weight is, though a square of far logits does not fit FP32.
-__device__ __forceinline__ float z_loss(float weight, float squares, float n) { return weight != 0.f ? weight * (squares / n) : 0.f; }
+__device__ __forceinline__ float z_loss(float weight, float squares, float n) { return weight * ((weight != 0.f ? squares : 0.f) / n); }
 // sum over the CTA, the same bits in every thread
 __device__ __forceinline__ float cta_sum(float v, float *buf) {
     v = warp_sum(v);
