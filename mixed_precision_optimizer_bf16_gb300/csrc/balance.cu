@@ -10,7 +10,7 @@
 // token, so the gradient is a second pass.)
 //
 // Measured on one GB300: 262144 tokens, 256 experts, 8 of them, bf16: forward 121 us, 1.1 TB/s, join 10 us,
-// backward 71 us, 4.0 TB/s; both ways 197 us in a row.  The forward pass is bound by integer instructions (69 %
+// backward 71 us, 4.0 TB/s; both ways 198 us in a row.  The forward pass is bound by integer instructions (69 %
 // of that pipe's cycles, 76 % of the issue slots): 430 a token, most of them the choice's.  The backward pass is
 // bound by issue (70 % of the slots) and a token's sums and lookups in shared memory.  16384 tokens of 64 FP32
 // experts in 8 groups: 14 + 6 + 7 us, which the host's calls take longer than.
@@ -699,11 +699,16 @@ __global__ void __launch_bounds__(kThreads, back_resident(PER)) k_balance_backwa
         }
         float extra = 0.f, dot = 0.f;
         if (q.dweights) {
-            float p = id >= 0 ? ex2((zid - lse) * kLog2e) * scale : 0.f;
-            if (a.renormalise) p *= reciprocal(warp_sum(p));
-            extra = p * up;
-            dot = warp_sum(extra);
-            if (a.renormalise) extra = fmaf(-p, dot, extra), dot = 0.f;
+            const float p = id >= 0 ? ex2((zid - lse) * kLog2e) * scale : 0.f, pu = p * up;
+            dot = warp_sum(pu);
+            if (a.renormalise) {
+                // w (u - sum w u), w = p / sum: as p / sum^2 (u sum - sum p u), whose difference is 0 to the bit where one
+                // choice has all the weight (two roundings of one product: no fused multiply-add)
+                const float sum = warp_sum(p), inv = reciprocal(sum);
+                extra = p * inv * (inv * __fsub_rn(__fmul_rn(up, sum), dot)), dot = 0.f;
+            } else {
+                extra = pu;
+            }
             if (id >= 0) extras[id] = extra;
         }
         const float rest = two_z * lse - warp_sum(s) - dot;

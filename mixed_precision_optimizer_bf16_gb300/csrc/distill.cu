@@ -17,12 +17,13 @@
 // that its id collects, rounded once.
 //
 // Measured on one GB300 (algorithmic bytes over the time; a copy of the same
-// buffers runs at 6.75 TB/s): 2048 rows of 250880 bf16 logits with 64 entries and
-// labels, T = 2, loss and gradient 415 us, 5.0 TB/s; 1024 such rows forward 88 us,
-// 5.8 TB/s, backward 172 us, 6.0 TB/s; 8192 rows of 32000 forward 109 us, 4.8 TB/s,
-// backward 174 us, 6.0 TB/s, loss and gradient 208 us, 5.0 TB/s. The two-pass kernel is
-// bound by issue (68 % of the slots) and by re-reads that miss L2 (17 % more DRAM bytes
-// than the operator needs at 250880); small rows by the latency of a row's reductions.
+// buffers runs at 6.75 TB/s), bf16 logits with 64 entries: 2048 rows of 250880 with
+// labels, T = 2, loss and gradient 422 us, 4.9 TB/s; at T = 1 without labels 1024 rows of 250880
+// forward 90 us, 5.7 TB/s, backward 175 us, 5.9 TB/s; 8192 rows of 32000 forward 108 us, 4.8 TB/s,
+// backward 177 us, 5.9 TB/s, loss and gradient 209 us, 5.0 TB/s (241 us with labels at T = 2).
+// At 250880 the two-pass kernel reads 51 % more from DRAM than the operator needs, what did not stay
+// in its ring and misses L2 (22 % more bytes in all), which is most of its time; it issues in
+// 59 % of the slots.  Small rows are bound by the latency of a row's reductions.
 #include <cooperative_groups.h>
 
 #include <algorithm>

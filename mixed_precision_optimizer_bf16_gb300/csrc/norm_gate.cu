@@ -19,8 +19,9 @@
 // 2048 102 us, 5.3 TB/s; 4096 of 14336 125 us, 3.8 TB/s; those with an FP32 stream and a gate 167 us,
 // 4.2 TB/s.  Backward: 32768 of 2048 181 us, 4.4 TB/s; 4096 of 14336 182 us, 3.9 TB/s; 8192 of 2048 with biases and a
 // gate for each sequence 68 us, 3.0 TB/s.  What bounds a wide row is its own chain -- loads, reductions one after the other,
-// stores -- with one or two CTAs in an SM (warps active 22 %, issue slots 33 % forward, 51 % backward); registers leave
-// no room for more.
+// stores -- with one or two CTAs in an SM (warps active 22 %, issue slots 33 % forward, 51 % backward).  The backward
+// kernels with two runs a thread spill 76 to 116 bytes under their 128 registers; they would not at 144, which
+// 448 threads could have where one CTA is all that an SM holds (not measured).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -202,8 +203,7 @@ __device__ __forceinline__ Cols cols_of(const float (&f)[8]) {
     for (int i = 0; i < 4; ++i) c.v[i] = make_float2(f[2 * i], f[2 * i + 1]);
     return c;
 }
-// Eight columns from `c` on of a row of n: VEC: whole vectors, all of them there or none;
-// else one by one, 0 beyond the row.
+// Eight columns from `c` on of a row of n, one by one, 0 beyond the row.
 template <class T>
 __device__ __forceinline__ Cols load_cols(const T *row, uint32_t c, uint32_t n) {
     float f[8];
@@ -216,6 +216,7 @@ __device__ __forceinline__ Cols load_cols(const T *row, uint32_t c, uint32_t n) 
     }
     return cols_of(f);
 }
+// And stored.  VEC: whole vectors, all of them there or none; else one by one.
 template <bool VEC, class T>
 __device__ __forceinline__ void store_cols(T *row, uint32_t c, uint32_t n, const Cols &x) {
     const float f[8] = {x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y, x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y};

@@ -39,7 +39,8 @@ __device__ __forceinline__ float warp_max(float x) {
     return y;
 }
 
-// 2^x by the special-function unit, subnormal results flushed to 0.
+// 2^x by the special-function unit, to two units in the last place (less than what the exponent's own product is
+// rounded by, from |x| of a few on), subnormal results flushed to 0.
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

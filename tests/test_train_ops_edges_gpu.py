@@ -219,6 +219,22 @@ def test_balance_bf16_ties_off_experts_and_nan(experts, k):
     close(got[1].cpu()[keep], want[1][keep], 1.0 * (want[1][keep] != 0), "weights")
 
 
+@pytest.mark.parametrize("dtype,experts", [(F32, 1), (F32, 9), (BF16, 48), (F32, 119), (BF16, 256), (F32, 600)])
+def test_balance_one_choice_has_all_the_weight(dtype, experts):
+    """Renormalised, a single choice's weight is 1 whatever the logits are: nothing comes back through it, not even a
+    rounding, which would be large beside the balance loss's own gradient over many tokens."""
+    z = randn(gen(10), 500, experts).to(dtype)
+    up = torch.randn(500, 1, device="cuda", generator=gen(11))
+    ids, w, counts, loss, saved = ops.balance_forward(z, 1)
+    close(w, torch.ones_like(w), 0.0, "weights")
+    assert torch.equal(ops.balance_backward(z, ids, counts, saved, up), ops.balance_backward(z, ids, counts, saved))
+    z[:, 1:] = -INF                                   # or the only expert that is on
+    if experts > 1:
+        ids, w, counts, loss, saved = ops.balance_forward(z, 2)
+        up = torch.randn(500, 2, device="cuda", generator=gen(11))
+        assert torch.equal(ops.balance_backward(z, ids, counts, saved, up), ops.balance_backward(z, ids, counts, saved))
+
+
 def balance_plain(z, k, mask, groups, balance_weight, z_weight, renormalise, dweights, dloss):
     """R.balance for many tokens: by whole tensors, on their device, without NaN."""
     z = z.double()
