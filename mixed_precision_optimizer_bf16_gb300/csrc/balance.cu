@@ -10,10 +10,10 @@
 // token, so the gradient is a second pass.)
 //
 // Measured on one GB300: 262144 tokens, 256 experts, 8 of them, bf16: forward 121 us, 1.1 TB/s, join 10 us,
-// backward 71 us, 4.0 TB/s; both ways 198 us in a row.  The forward pass is bound by integer instructions (69 %
+// backward 68 us, 4.2 TB/s; both ways 198 us in a row.  The forward pass is bound by integer instructions (69 %
 // of that pipe's cycles, 76 % of the issue slots): 430 a token, most of them the choice's.  The backward pass is
 // bound by issue (70 % of the slots) and a token's sums and lookups in shared memory.  16384 tokens of 64 FP32
-// experts in 8 groups: 14 + 6 + 7 us, which the host's calls take longer than.
+// experts in 8 groups: 13 + 6 + 7 us, which the host's calls take longer than.
 #include <cooperative_groups.h>
 
 #include <algorithm>
