@@ -83,7 +83,7 @@ extern "C" {
  * changes.  bf16opt_abi_version() returns the value the library was built
  * with; code compiled against a header with another value must not use it.
  * No CUDA call; never fails. */
-#define BF16OPT_ABI_VERSION 3
+#define BF16OPT_ABI_VERSION 4
 int bf16opt_abi_version(void);
 
 /* ---- modes and flags --------------------------------------------------- */
@@ -422,8 +422,9 @@ int bf16opt_pipeline_timeouts(uint32_t *count);
 /* ---- training operators ------------------------------------------------------
  * The memory-bound operators of a training step whose bf16 gradients the
  * accumulate passes take: a distillation loss at the head, the norms, gate and
- * residual scale around a block, and a router's balance loss, each with its
- * gradient.  No counterpart in the paper.
+ * residual scale around a block, a router's balance loss, policy and preference losses of
+ * given tokens, a feed-forward block's activation with its inputs kept in 8 bits, and rotary
+ * positions, each with its gradient.  No counterpart in the paper.
  *
  * They need no handle.  A call enqueues its kernels on `stream`, on the
  * current device, and neither allocates nor synchronises, so it can be captured
@@ -609,6 +610,180 @@ int bf16opt_balance_forward(const bf16opt_balance_t *d, int32_t *ids, float *wei
 int bf16opt_balance_backward(const bf16opt_balance_t *d, const int32_t *ids, const int32_t *counts, const float *saved,
                              const float *dweights, const float *dloss, void *dlogits, uint64_t dlogits_stride,
                              void *stream);
+
+/* Log-probabilities of given tokens, and two losses of them.  z: a row's logits, l its
+ * label, T the temperature, s = softmax(z / T):
+ *   logp = log s_l.
+ * A row whose row_weight is 0, or whose label is outside [0, vocab), does not count: it is not
+ * read, and its loss, log-probability, saved numbers and gradient are 0.  Logits of
+ * -inf are masked vocabulary (s = 0; a label on one, or a row with no other logit, has
+ * logp -inf; in the latter s = 0 everywhere).  NaN and +inf in a row give NaN in that row
+ * (and in what is summed over it) alone.
+ *
+ * saved [rows, 4] FP32 (16-byte aligned), which the forward calls leave for
+ * bf16opt_token_logp_backward: the row's largest logit m, the sum of exp((z_j - m) / T), the
+ * derivative c of the loss by logp, and the index (int32 bits) of the loss that it belongs
+ * to, -1 for none. */
+#define BF16OPT_TOKENS_MAX_ROWS 0x7fffffff
+
+typedef struct {
+    uint64_t rows;               /* tokens, at most BF16OPT_TOKENS_MAX_ROWS */
+    uint32_t vocab;              /* 1 .. 2^30 */
+    int32_t logits_type;         /* BF16OPT_TYPE_* of logits and dlogits */
+    int32_t labels_type;         /* BF16OPT_INDEX_* of labels */
+    float temperature;           /* finite, > 0, with a finite reciprocal */
+    const void *logits;          /* [rows, vocab] */
+    uint64_t logits_stride;
+    const void *labels;          /* [rows] */
+    const float *row_weight;     /* NULL (1), or [rows] */
+} bf16opt_tokens_t;
+
+/* logp [rows] FP32 (a weight other than 0 changes nothing here); saved may be NULL; c = 1. */
+int bf16opt_token_logp_forward(const bf16opt_tokens_t *d, float *logp, float *saved, void *stream);
+
+/* The backward call of all three: dz_j = c dloss[index] / T ([j = l] - s_j), rounded once.
+ * saved: as a forward call with the same logits, labels and temperature left it (the
+ * weights are in it).  dloss: NULL (1), or [losses] FP32 (an index outside counts as
+ * none).  Rows whose c dloss is 0 are not read.  dlogits may be d->logits itself with the same stride. */
+int bf16opt_token_logp_backward(const bf16opt_tokens_t *d, const float *saved, const float *dloss, uint64_t losses,
+                                void *dlogits, uint64_t dlogits_stride, void *stream);
+
+/* Clipped policy loss with a KL term.  A: advantage, w: row_weight,
+ *   r = exp(logp - old_logp)  (old_logp NULL: it is logp itself, a constant: r = 1),
+ *   k = exp(ref_logp - logp) - 1 - (ref_logp - logp)  (ref_logp NULL: 0),
+ *   loss = w [ -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A) + kl_weight k ],
+ *   c = w [ -(r A where the minimum is r A, else 0) + kl_weight (1 - exp(ref_logp - logp)) ]. */
+typedef struct {
+    const float *advantage;      /* [rows] */
+    const float *old_logp;       /* NULL, or [rows] */
+    const float *ref_logp;       /* NULL, or [rows] */
+    float clip_low, clip_high;   /* >= 0, clip_low <= 1; clip_high may be +inf */
+    float kl_weight;             /* finite, >= 0 */
+    uint32_t reserved;           /* must be 0 */
+} bf16opt_policy_t;
+
+/* loss, logp: [rows] FP32.  saved may be NULL. */
+int bf16opt_policy_forward(const bf16opt_tokens_t *d, const bf16opt_policy_t *p, float *loss, float *logp, float *saved,
+                           void *stream);
+
+/* Loss and gradient (for a gradient of dloss [rows], or 1, of each row's loss) in one
+ * pass over the logits.  dlogits as above; logp may be NULL. */
+int bf16opt_policy_loss_grad(const bf16opt_tokens_t *d, const bf16opt_policy_t *p, const float *dloss, float *loss,
+                             float *logp, void *dlogits, uint64_t dlogits_stride, void *stream);
+
+/* Preference loss of pairs of sequences.  offsets [2 pairs + 1]: sequence i is rows
+ * [offsets[i], offsets[i + 1]); sequence i < pairs is preferred to sequence pairs + i.
+ * L_i: the sum of logp over the sequence's rows that count (row_weight is NULL here), divided by their
+ * number if length_normalise (a sequence without any: 0).  ref_logp NULL: 0.
+ *   h = (L_i - ref_i) - (L_j - ref_j), j = pairs + i;
+ *   BF16OPT_PREFER_SIGMOID  m = beta h - margin;  loss = -(1 - e) log sigmoid(m) - e log sigmoid(-m),  e = label_smoothing,
+ *   BF16OPT_PREFER_HINGE    m = beta h - margin;  loss = max(0, 1 - m),
+ *   BF16OPT_PREFER_IPO      loss = (h - margin - 1 / (2 beta))^2.
+ * Sums over a sequence are FP64.  Rows outside the sequences do not count.  Offsets that descend or lie
+ * outside [0, rows] are taken to the nearest that do not (the sequence is then
+ * shorter or empty); nothing outside the tensors is touched. */
+#define BF16OPT_PREFER_SIGMOID 0
+#define BF16OPT_PREFER_HINGE 1
+#define BF16OPT_PREFER_IPO 2
+#define BF16OPT_PREFER_MAX_PAIRS 65536
+
+typedef struct {
+    uint64_t pairs;              /* 0 .. BF16OPT_PREFER_MAX_PAIRS */
+    int32_t offsets_type;        /* BF16OPT_INDEX_* */
+    int32_t kind;                /* BF16OPT_PREFER_* */
+    const void *offsets;         /* [2 pairs + 1] */
+    const float *ref_logp;       /* NULL, or [2 pairs] */
+    float beta;                  /* finite, > 0 */
+    float label_smoothing;       /* 0 .. 0.5; SIGMOID alone uses it */
+    float margin;                /* finite */
+    int32_t length_normalise;    /* 0 or 1 */
+} bf16opt_preference_t;
+
+/* loss [pairs], logp [2 pairs] (L): FP32.  saved must be given. */
+int bf16opt_preference_forward(const bf16opt_tokens_t *d, const bf16opt_preference_t *p, float *loss, float *logp,
+                               float *saved, void *stream);
+
+/* Activations kept in 8 bits, and the activation of a feed-forward block that keeps its inputs so.
+ * A row's columns form runs of 32 (the last one may be shorter).  A run's scale is
+ * 2^(b - 127), b the smallest byte for which its largest finite magnitude is at most 448
+ * scales; each element is divided by it and rounded to the nearest e4m3 number, ties to even
+ * (bias 7, largest 448, no infinities; one that would be 2^128 is kept as 1.875 2^127).  Inf and NaN are kept as NaN.
+ * codes [rows, 32 runs], scales [rows, runs], runs = ceil(columns / 32); codes behind a
+ * row's end are 0.  A row's elements are contiguous; its stride counts elements. */
+#define BF16OPT_PACK_RUN 32
+
+typedef struct {
+    uint64_t rows;
+    uint32_t columns;            /* 1 .. 2^30 */
+    int32_t type;                /* BF16OPT_TYPE_* of everything that is not kept */
+} bf16opt_pack_t;
+
+/* codes: 16-byte aligned. */
+int bf16opt_pack(const bf16opt_pack_t *d, const void *x, uint64_t x_stride, uint8_t *codes, uint8_t *scales, void *stream);
+int bf16opt_unpack(const bf16opt_pack_t *d, const uint8_t *codes, const uint8_t *scales, void *x, uint64_t x_stride, void *stream);
+
+/* h = act(gate) up  (up NULL: h = act(gate)), act one of
+ *   BF16OPT_GLU_SILU  g sigmoid(g),
+ *   BF16OPT_GLU_GELU  g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2.
+ * The forward call keeps gate and up in 8 bits (codes [parts, rows, 32 runs], scales
+ * [parts, rows, runs]: gate's, then up's); the backward call works on what was kept, g' and u':
+ *   dgate = dh u' act'(g'),  dup = dh act(g'),  and, if wanted, h' = act(g') u'
+ * (which the gradient of the weights behind h needs, where h itself is not kept). */
+#define BF16OPT_GLU_SILU 0
+#define BF16OPT_GLU_GELU 1
+
+typedef struct {
+    uint64_t rows;
+    uint32_t columns;            /* 1 .. 2^30 */
+    int32_t type;                /* BF16OPT_TYPE_* of everything that is not kept */
+    int32_t act;                 /* BF16OPT_GLU_* */
+    int32_t gated;               /* 1: gate and up; 0: gate alone (up, dup: NULL) */
+} bf16opt_glu_t;
+
+/* codes and scales both NULL: nothing is kept.  h may be gate or up with the same stride. */
+int bf16opt_glu_forward(const bf16opt_glu_t *d, const void *gate, uint64_t gate_stride, const void *up, uint64_t up_stride,
+                        void *h, uint64_t h_stride, uint8_t *codes, uint8_t *scales, void *stream);
+
+/* h may be NULL.  One of dgate, dup and h may be dh with the same stride.  Outputs may
+ * be column ranges of one matrix (the same stride, no element twice). */
+int bf16opt_glu_backward(const bf16opt_glu_t *d, const void *dh, uint64_t dh_stride, const uint8_t *codes, const uint8_t *scales,
+                         void *dgate, uint64_t dgate_stride, void *dup, uint64_t dup_stride, void *h, uint64_t h_stride,
+                         void *stream);
+
+/* Rotary positions.  A head's first rotary_dim elements are pairs (x_i, x_{i + rotary_dim / 2})
+ * (BF16OPT_ROTARY_HALF) or (x_{2i}, x_{2i + 1}) (BF16OPT_ROTARY_INTERLEAVED), i < rotary_dim / 2;
+ * at position p each is turned by the angle p frequencies[i]:
+ *   (a, b) -> scale (a cos - b sin, b cos + a sin)   (inverse: -sin),
+ * the other elements are copied.  inverse gives the gradient of the inputs from that of the outputs.
+ * The angle's whole turns are taken off in 64-bit whole numbers (p times the frequency in
+ * 2^-64 turns), so far positions are as exact as near ones.  Results are rounded once. */
+#define BF16OPT_ROTARY_HALF 0
+#define BF16OPT_ROTARY_INTERLEAVED 1
+#define BF16OPT_ROTARY_MAX_DIM 256
+
+typedef struct {
+    uint64_t batch, seq;
+    uint32_t heads, kv_heads;    /* of q and of k (0: no k) */
+    uint32_t dim;                /* elements of a head, 1 .. 65536 */
+    uint32_t rotary_dim;         /* even, 2 .. min(dim, BF16OPT_ROTARY_MAX_DIM) */
+    int32_t type;                /* BF16OPT_TYPE_* of all four */
+    int32_t layout;              /* BF16OPT_ROTARY_* */
+    int32_t positions_type;      /* BF16OPT_INDEX_* */
+    int32_t inverse;             /* 0 or 1 */
+    const void *positions;       /* NULL (0, 1, ..), or [seq], or [batch, seq] */
+    uint64_t positions_stride;   /* between batches: 0 or seq */
+    int64_t offset;              /* added to every position */
+    const double *frequencies;   /* host memory, [rotary_dim / 2]: radians per position, finite; read during the call */
+    float scale;                 /* finite */
+    uint32_t reserved;           /* must be 0 */
+    uint64_t q_stride[3], k_stride[3], out_q_stride[3], out_k_stride[3];   /* elements between batches, tokens, heads */
+} bf16opt_rotary_t;
+
+/* A head's elements are contiguous; inputs may have any strides, outputs no element twice.  out_q
+ * may be q and out_k k (with the same strides): then what is not turned is not touched.
+ * Outputs may lie in one matrix with one another or with the inputs where every token's
+ * (or every batch's) elements are apart. */
+int bf16opt_rotary(const bf16opt_rotary_t *d, const void *q, const void *k, void *out_q, void *out_k, void *stream);
 
 /* ---- checked build -------------------------------------------------------
  * No counterpart in the paper: a debugging aid standing in for a memory

@@ -44,6 +44,17 @@ BF16OPT_GATE_SIGMOID = 1
 BF16OPT_NORM_MAX_HIDDEN = 16384
 BF16OPT_BALANCE_MAX_EXPERTS = 1024
 BF16OPT_BALANCE_MAX_K = 32
+BF16OPT_TOKENS_MAX_ROWS = 0x7fffffff
+BF16OPT_PREFER_SIGMOID = 0
+BF16OPT_PREFER_HINGE = 1
+BF16OPT_PREFER_IPO = 2
+BF16OPT_PREFER_MAX_PAIRS = 65536
+BF16OPT_PACK_RUN = 32
+BF16OPT_GLU_SILU = 0
+BF16OPT_GLU_GELU = 1
+BF16OPT_ROTARY_HALF = 0
+BF16OPT_ROTARY_INTERLEAVED = 1
+BF16OPT_ROTARY_MAX_DIM = 256
 
 c_u64, c_u32, c_i32, c_f32, c_vp = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
 
@@ -99,6 +110,36 @@ class bf16opt_balance_t(ctypes.Structure):
                 ("balance_weight", c_f32), ("z_weight", c_f32)]
 
 
+class bf16opt_tokens_t(ctypes.Structure):
+    _fields_ = [("rows", c_u64), ("vocab", c_u32), ("logits_type", c_i32), ("labels_type", c_i32), ("temperature", c_f32),
+                ("logits", c_vp), ("logits_stride", c_u64), ("labels", c_vp), ("row_weight", c_vp)]
+
+
+class bf16opt_policy_t(ctypes.Structure):
+    _fields_ = [("advantage", c_vp), ("old_logp", c_vp), ("ref_logp", c_vp), ("clip_low", c_f32), ("clip_high", c_f32),
+                ("kl_weight", c_f32), ("reserved", c_u32)]
+
+
+class bf16opt_preference_t(ctypes.Structure):
+    _fields_ = [("pairs", c_u64), ("offsets_type", c_i32), ("kind", c_i32), ("offsets", c_vp), ("ref_logp", c_vp),
+                ("beta", c_f32), ("label_smoothing", c_f32), ("margin", c_f32), ("length_normalise", c_i32)]
+
+
+class bf16opt_pack_t(ctypes.Structure):
+    _fields_ = [("rows", c_u64), ("columns", c_u32), ("type", c_i32)]
+
+
+class bf16opt_glu_t(ctypes.Structure):
+    _fields_ = [("rows", c_u64), ("columns", c_u32), ("type", c_i32), ("act", c_i32), ("gated", c_i32)]
+
+
+class bf16opt_rotary_t(ctypes.Structure):
+    _fields_ = [("batch", c_u64), ("seq", c_u64), ("heads", c_u32), ("kv_heads", c_u32), ("dim", c_u32), ("rotary_dim", c_u32),
+                ("type", c_i32), ("layout", c_i32), ("positions_type", c_i32), ("inverse", c_i32), ("positions", c_vp),
+                ("positions_stride", c_u64), ("offset", ctypes.c_int64), ("frequencies", c_vp), ("scale", c_f32), ("reserved", c_u32),
+                ("q_stride", c_u64 * 3), ("k_stride", c_u64 * 3), ("out_q_stride", c_u64 * 3), ("out_k_stride", c_u64 * 3)]
+
+
 # Functions the header declares (the tests check the library exports them all).
 EXPORTS = ("bf16opt_create", "bf16opt_create_offload", "bf16opt_accumulate", "bf16opt_grad_norm", "bf16opt_step", "bf16opt_destroy",
            "bf16opt_get_step", "bf16opt_set_step", "bf16opt_error_string", "bf16opt_last_error",
@@ -108,9 +149,12 @@ EXPORTS = ("bf16opt_create", "bf16opt_create_offload", "bf16opt_accumulate", "bf
            "bf16opt_pipeline_timeouts", "bf16opt_step_path", "bf16opt_abi_version",
            "bf16opt_distill_forward", "bf16opt_distill_backward", "bf16opt_distill_loss_grad",
            "bf16opt_norm_gate_forward", "bf16opt_norm_gate_workspace", "bf16opt_norm_gate_backward",
-           "bf16opt_balance_workspace", "bf16opt_balance_forward", "bf16opt_balance_backward")
+           "bf16opt_balance_workspace", "bf16opt_balance_forward", "bf16opt_balance_backward",
+           "bf16opt_token_logp_forward", "bf16opt_token_logp_backward", "bf16opt_policy_forward", "bf16opt_policy_loss_grad",
+           "bf16opt_preference_forward", "bf16opt_pack", "bf16opt_unpack", "bf16opt_glu_forward", "bf16opt_glu_backward",
+           "bf16opt_rotary")
 
-ABI_VERSION = 3   # BF16OPT_ABI_VERSION of the header these declarations mirror
+ABI_VERSION = 4   # BF16OPT_ABI_VERSION of the header these declarations mirror
 
 _lib = None
 
@@ -190,7 +234,17 @@ def load(path=None):
     L.bf16opt_balance_workspace.argtypes = [c_vp, ctypes.POINTER(c_u64)]
     L.bf16opt_balance_forward.argtypes = [c_vp] * 7 + [c_u64, c_vp]
     L.bf16opt_balance_backward.argtypes = [c_vp] * 7 + [c_u64, c_vp]
-    for name in EXPORTS[-9:]:
+    L.bf16opt_token_logp_forward.argtypes = [c_vp] * 4
+    L.bf16opt_token_logp_backward.argtypes = [c_vp] * 3 + [c_u64, c_vp, c_u64, c_vp]
+    L.bf16opt_policy_forward.argtypes = [c_vp] * 6
+    L.bf16opt_policy_loss_grad.argtypes = [c_vp] * 6 + [c_u64, c_vp]
+    L.bf16opt_preference_forward.argtypes = [c_vp] * 6
+    L.bf16opt_pack.argtypes = [c_vp, c_vp, c_u64, c_vp, c_vp, c_vp]
+    L.bf16opt_unpack.argtypes = [c_vp] * 4 + [c_u64, c_vp]
+    L.bf16opt_glu_forward.argtypes = [c_vp] + [c_vp, c_u64] * 3 + [c_vp] * 3
+    L.bf16opt_glu_backward.argtypes = [c_vp, c_vp, c_u64, c_vp, c_vp] + [c_vp, c_u64] * 3 + [c_vp]
+    L.bf16opt_rotary.argtypes = [c_vp] * 6
+    for name in EXPORTS[EXPORTS.index("bf16opt_distill_forward"):]:
         getattr(L, name).restype = ctypes.c_int
     if path == lib_path():
         _lib = L
@@ -374,6 +428,46 @@ def bf16opt_balance_forward(d, ids, weights, counts, loss, saved, workspace=None
 
 def bf16opt_balance_backward(d, ids, counts, saved, dweights, dloss, dlogits, dlogits_stride, stream=0):
     return load().bf16opt_balance_backward(_desc(d), ids, counts, saved, dweights, dloss, dlogits, dlogits_stride, stream)
+
+
+def bf16opt_token_logp_forward(d, logp, saved=None, stream=0):
+    return load().bf16opt_token_logp_forward(_desc(d), logp, saved, stream)
+
+
+def bf16opt_token_logp_backward(d, saved, dloss, losses, dlogits, dlogits_stride, stream=0):
+    return load().bf16opt_token_logp_backward(_desc(d), saved, dloss, losses, dlogits, dlogits_stride, stream)
+
+
+def bf16opt_policy_forward(d, p, loss, logp, saved=None, stream=0):
+    return load().bf16opt_policy_forward(_desc(d), _desc(p), loss, logp, saved, stream)
+
+
+def bf16opt_policy_loss_grad(d, p, dloss, loss, logp, dlogits, dlogits_stride, stream=0):
+    return load().bf16opt_policy_loss_grad(_desc(d), _desc(p), dloss, loss, logp, dlogits, dlogits_stride, stream)
+
+
+def bf16opt_preference_forward(d, p, loss, logp, saved, stream=0):
+    return load().bf16opt_preference_forward(_desc(d), _desc(p), loss, logp, saved, stream)
+
+
+def bf16opt_pack(d, x, x_stride, codes, scales, stream=0):
+    return load().bf16opt_pack(_desc(d), x, x_stride, codes, scales, stream)
+
+
+def bf16opt_unpack(d, codes, scales, x, x_stride, stream=0):
+    return load().bf16opt_unpack(_desc(d), codes, scales, x, x_stride, stream)
+
+
+def bf16opt_glu_forward(d, gate, gate_stride, up, up_stride, h, h_stride, codes=None, scales=None, stream=0):
+    return load().bf16opt_glu_forward(_desc(d), gate, gate_stride, up, up_stride, h, h_stride, codes, scales, stream)
+
+
+def bf16opt_glu_backward(d, dh, dh_stride, codes, scales, dgate, dgate_stride, dup, dup_stride, h=None, h_stride=0, stream=0):
+    return load().bf16opt_glu_backward(_desc(d), dh, dh_stride, codes, scales, dgate, dgate_stride, dup, dup_stride, h, h_stride, stream)
+
+
+def bf16opt_rotary(d, q, k, out_q, out_k, stream=0):
+    return load().bf16opt_rotary(_desc(d), q, k, out_q, out_k, stream)
 
 
 def bf16opt_last_error(h=None):

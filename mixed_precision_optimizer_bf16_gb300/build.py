@@ -5,9 +5,9 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB_PATH = os.path.join(HERE, "libbf16opt.so")
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("bf16opt.cu", "distill.cu", "norm_gate.cu", "balance.cu")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("bf16opt.cu", "distill.cu", "norm_gate.cu", "balance.cu", "logp.cu", "glu.cu", "rotary.cu")]
 DEPS = SOURCES + [os.path.join(HERE, "csrc", "kernels.cuh"), os.path.join(HERE, "csrc", "host_adam.h"),
-                  os.path.join(HERE, "csrc", "ops_common.cuh"), os.path.join(ROOT, "include", "bf16opt.h")]
+                  os.path.join(HERE, "csrc", "ops_common.cuh"), os.path.join(HERE, "csrc", "logits.cuh"), os.path.join(ROOT, "include", "bf16opt.h")]
 
 # -ffp-contract=off: host code rounds every product on its own (the offloaded
 # step's host update repeats the device kernel's operations exactly)

@@ -1,0 +1,637 @@
+// logp.cu -- log-probabilities of given tokens, and the policy and preference losses of them, forward
+// and backward (bf16opt_token_logp_*, bf16opt_policy_*, bf16opt_preference_* of include/bf16opt.h).
+//
+// A row leaves two numbers, its largest logit m and the sum of exp((z - m) / T); a loss gives one number
+// back, its derivative c by the row's log-probability; the gradient is c / T ([j = l] - softmax_j).  So
+// the forward pass reads the logits once, the backward pass reads and writes them once, and where a row's loss
+// depends on that row alone (the policy loss) both go in one kernel, which reads a row a second
+// time while it is in L2.
+#include <cooperative_groups.h>
+
+#include "logits.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace bf16ops {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kU = 4;              // vectors of a thread at a time
+constexpr int kMaxCluster = 8;
+constexpr int kPairThreads = 512;
+constexpr uint64_t kSliceVectors = 4 * kThreads * kU;   // of the backward kernel's CTAs
+// A row whose largest logit m is below this (|m| / T, in powers of two) has its exponents z c - m c in one
+// instruction for two logits: the product is exact, and m c is off by its rounding (2^-4 at most), the same for the
+// whole row, which goes into the row's factor.  Beyond, they are formed from the differences z - m, with m known.
+constexpr float kFar = 0x1p20f;
+
+enum Kind { LOGP, POLICY, PREFER };
+
+struct Args {
+    uint64_t rows;
+    uint32_t vocab, slices;
+    const void *logits;
+    uint64_t logits_stride;
+    const void *labels;
+    int labels_type;
+    const float *row_weight;
+    float c;                       // log2(e) / T
+    float inv_t;
+    double inv_t64;
+    // policy
+    const float *advantage, *old_logp, *ref_logp;
+    float lowest, highest, kl_weight;   // of the ratio
+    // preference
+    const void *offsets;
+    int offsets_type;
+    uint64_t pairs;
+
+    const float4 *saved_in;
+    const float *dloss;
+    uint64_t losses;
+    float *loss, *logp;
+    float4 *saved;
+    void *dlogits;
+    uint64_t dlogits_stride;
+};
+
+// A stream's largest number and the sum of exp2((z - m) c).
+struct Stat {
+    float m, s;
+};
+__device__ __forceinline__ Stat warp_join(const Stat &a, float c) {
+    Stat r;
+    r.m = warp_max(a.m);
+    r.s = warp_sum(a.s * ex2((a.m - safe_max(r.m)) * c));
+    return r;
+}
+// (A sum that is not finite belongs to a row that is NaN, or far and summed once more.)
+
+template <bool FAR>
+__device__ __forceinline__ float2 exponent(float2 z, float m, float mc, float c) {
+    if (FAR) return mul2(add2(z, both(-m)), both(c));
+    return fma2(z, both(c), both(-mc));
+}
+
+// This thread's part of a slice.  FAR: around the row's largest logit, which is known.
+template <class T, bool FAR>
+__device__ __forceinline__ Stat thread_stat(const T *z, const Slice &s, uint32_t vocab, uint32_t rank, uint32_t ranks, float c, float top) {
+    constexpr int P = Vec<T>::N / 2;
+    const uint32_t tid = threadIdx.x, nv = s.v1 - s.v0;
+    const uint4 *zv = reinterpret_cast<const uint4 *>(z + s.head) + s.v0;
+    Stat st = {FAR ? top : -INFINITY, 0.f};
+    float mc = 0.f;
+    float2 sum = both(0.f);
+    for (uint32_t i = tid; i < nv; i += kThreads * kU) {
+        uint4 q[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) q[u] = i + u * kThreads < nv ? zv[i + u * kThreads] : nothing<T>();
+        if (!FAR) {
+            const float mx = largest<T, kU>(q);
+            if (mx > st.m) {
+                const float to = fmaxf(fminf(mx * c, kFar), -kFar);
+                sum = mul2(sum, both(st.m == -INFINITY ? 0.f : ex2(mc - to)));
+                st.m = mx, mc = to;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            float2 f[P];
+            pairs<T>(q[u], f);
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                const float2 d = exponent<FAR>(f[k], safe_max(st.m), mc, c);
+                sum = add2(sum, make_float2(ex2(d.x), ex2(d.y)));
+            }
+        }
+    }
+    st.s = sum.x + sum.y;
+    // mc is m c rounded, or -kFar: what is lost there is 2^-126 of a row that is not far
+    if (!FAR && st.s != 0.f) st.s *= ex2(fmaf(-st.m, c, mc));
+    uint32_t at = 0xffffffffu;
+    if (rank == 0 && tid < s.head) at = tid;
+    else if (rank + 1 == ranks && tid >= 32 && tid - 32 < vocab - s.tail0) at = s.tail0 + tid - 32;
+    if (at != 0xffffffffu) {
+        const float f = to_f32(z[at]);
+        const float m = FAR ? top : fmaxf(st.m, f);   // (a NaN passed over)
+        const float b = safe_max(m);
+        st.s = st.s * ex2((st.m - b) * c) + ex2((f - b) * c);
+        st.m = m;
+    }
+    return st;
+}
+
+// log(x) of a positive sum, in 64 bits from a logarithm of its fraction in 32 (in [-0.35, 0.35]: off by 2^-25 or so).
+__device__ __forceinline__ double log_of(float x) {
+    if (!(x > 0.f && x < INFINITY)) return logf(x);
+    int k;
+    float f = frexpf(x, &k);   // in [0.5, 1)
+    if (f < 0.70710678f) f *= 2.f, --k;
+    return fma((double)k, 0.69314718055994530942, (double)logf(f));
+}
+
+// A counted row's log-probability, loss and slope.
+struct Terms {
+    float loss, logp, slope;
+};
+template <int KIND>
+__device__ __forceinline__ Terms terms_of(const Args &a, uint64_t row, float w, float m, float s, float z) {
+    Terms t;
+    const double logp = m == -INFINITY && s == 0.f ? -INFINITY : ((double)z - m) * a.inv_t64 - log_of(s);
+    t.logp = (float)logp;
+    t.loss = 0.f, t.slope = 1.f;
+    if (KIND == POLICY) {
+        const float adv = a.advantage[row];
+        const float ratio = expf(a.old_logp ? (float)(logp - a.old_logp[row]) : t.logp - t.logp);
+        const float kept = adv >= 0.f ? (ratio > a.highest ? a.highest : ratio) : (ratio < a.lowest ? a.lowest : ratio);   // NaN stays
+        t.loss = -kept * adv;
+        t.slope = kept == ratio || ratio != ratio ? -ratio * adv : 0.f;
+        if (a.ref_logp) {
+            const float d = (float)(a.ref_logp[row] - logp), e = expm1f(d);
+            t.loss += a.kl_weight * (d == INFINITY ? d : e - d);
+            t.slope -= a.kl_weight * e;
+        }
+        t.loss *= w, t.slope *= w;
+    }
+    return t;
+}
+
+// The gradient of a slice: scale_q softmax's exponentials, and scale at the label.
+template <class T, bool FAR>
+__device__ __forceinline__ void grad_slice(const T *z, T *out, uint32_t head, uint32_t v0, uint32_t nv, bool first, bool last, uint32_t tail0,
+                                           uint32_t vocab, float m, float c, float scale_q, float scale, uint32_t label) {
+    constexpr int N = Vec<T>::N, P = N / 2;
+    const uint32_t tid = threadIdx.x;
+    const uint4 *zv = reinterpret_cast<const uint4 *>(z + head) + v0;
+    T *ov = out + head + (size_t)v0 * N;
+    const bool whole = (((uintptr_t)out ^ (uintptr_t)z) & 15u) == 0;
+    const float base = safe_max(m), mc = base * c;
+    const float corrected = FAR ? scale_q : scale_q * ex2(fmaf(-base, c, mc));
+    auto one = [&](uint32_t at) {
+        const float f = to_f32(z[at]);
+        const float2 d = exponent<FAR>(make_float2(f, f), base, mc, c);
+        from_f32(out[at], fmaf(corrected, ex2(d.x), at == label ? scale : 0.f));
+    };
+    const uint32_t mine = label - head - v0 * N;   // the label's place in the slice, if it is there
+    for (uint32_t i = tid; i < nv; i += kThreads * kU) {
+        uint4 q[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            if (i + u * kThreads < nv) q[u] = zv[i + u * kThreads];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const uint32_t j = i + u * kThreads;
+            if (j >= nv) break;
+            float2 f[P];
+            pairs<T>(q[u], f);
+            float g[N];
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                const float2 d = exponent<FAR>(f[k], base, mc, c);
+                const float2 r = mul2(both(corrected), make_float2(ex2(d.x), ex2(d.y)));
+                g[2 * k] = r.x, g[2 * k + 1] = r.y;
+            }
+            if (mine / N == j && label >= head) {
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    if (mine % N == k) g[k] += scale;
+            }
+            store_vec<T>(ov + (size_t)j * N, g, whole);
+        }
+    }
+    if (first && tid < head) one(tid);
+    if (last && tid < vocab - tail0) one(tail0 + tid);
+}
+
+template <class T>
+__device__ __forceinline__ void zero_slice(const T *z, T *out, uint32_t head, uint32_t v0, uint32_t nv, bool first, bool last, uint32_t tail0,
+                                           uint32_t vocab) {
+    constexpr int N = Vec<T>::N;
+    T *ov = out + head + (size_t)v0 * N;
+    const bool whole = (((uintptr_t)out ^ (uintptr_t)z) & 15u) == 0;
+    const float zero[N] = {};
+    for (uint32_t i = threadIdx.x; i < nv; i += kThreads) store_vec<T>(ov + (size_t)i * N, zero, whole);
+    if (first && threadIdx.x < head) from_f32(out[threadIdx.x], 0.f);
+    if (last && threadIdx.x < vocab - tail0) from_f32(out[tail0 + threadIdx.x], 0.f);
+}
+
+__device__ __forceinline__ bool far_row(float m, float c) { return !(fabsf(m * c) < kFar) && m != -INFINITY; }
+
+// A cluster of CTAs (or one) takes a row.
+template <class T, int KIND, bool GRAD>
+__global__ void __launch_bounds__(kThreads) k_rows(const Args a) {
+    __shared__ Stat sm[2][kMaxCluster * kWarps];
+    cg::cluster_group cluster = cg::this_cluster();
+    const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint64_t row = blockIdx.x / ranks;
+    pdl_enter();
+    const int64_t label = load_index(a.labels, a.labels_type, row);
+    float w = a.row_weight ? a.row_weight[row] : 1.f;
+    if (KIND == PREFER && a.pairs == 0) {
+        w = 0.f;
+    } else if (KIND == PREFER) {
+        const int64_t lo = load_index(a.offsets, a.offsets_type, 0), hi = load_index(a.offsets, a.offsets_type, 2 * a.pairs);
+        if ((int64_t)row < lo || (int64_t)row >= hi) w = 0.f;
+    }
+    const bool counts = w != 0.f && label >= 0 && label < (int64_t)a.vocab;
+    const T *z = reinterpret_cast<const T *>(a.logits) + row * a.logits_stride;
+    T *out = GRAD ? reinterpret_cast<T *>(a.dlogits) + row * a.dlogits_stride : nullptr;
+    const Slice s = slice_of(z, a.vocab, rank, ranks, 31 - __clz(ranks));
+    if (!counts) {   // the same in the whole cluster
+        if (GRAD) zero_slice<T>(z, out, s.head, s.v0, s.v1 - s.v0, rank == 0, rank + 1 == ranks, s.tail0, a.vocab);
+        if (rank == 0 && tid == 0) {
+            if (KIND == POLICY) a.loss[row] = 0.f;
+            if (KIND != PREFER && a.logp) a.logp[row] = 0.f;
+            if (!GRAD && a.saved) a.saved[row] = make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
+        }
+        pdl_leave();
+        return;
+    }
+    if (ranks > 1) cluster.sync();   // every CTA's shared memory exists
+    const float z_label = to_f32(z[label]);
+
+    auto joined = [&](Stat st, int turn) {
+        st = warp_join(st, a.c);
+        if (lane < ranks) {
+            Stat *to = &sm[turn][rank * kWarps + warp];
+            *(ranks > 1 ? cluster.map_shared_rank(to, lane) : to) = st;
+        }
+        if (ranks > 1) cluster.sync();
+        else __syncthreads();
+        Stat all = lane < ranks * kWarps ? sm[turn][lane] : Stat{-INFINITY, 0.f};
+        for (uint32_t i = lane + 32; i < ranks * kWarps; i += 32) {
+            const Stat b = sm[turn][i];
+            const float m = fmaxf(all.m, b.m), t = safe_max(m);
+            all.s = all.s * ex2((all.m - t) * a.c) + b.s * ex2((b.m - t) * a.c);
+            all.m = m;
+        }
+        return warp_join(all, a.c);
+    };
+    Stat st = joined(thread_stat<T, false>(z, s, a.vocab, rank, ranks, a.c, 0.f), 0);
+    const bool far = far_row(st.m, a.c);
+    if (far) st = joined(thread_stat<T, true>(z, s, a.vocab, rank, ranks, a.c, st.m), 1);
+
+    if (!GRAD && (rank != 0 || tid != 0)) return;
+    float4 keep = make_float4(st.m, st.s, 0.f, __int_as_float((int)row));
+    float scale = 0.f;
+    if (KIND != PREFER) {
+        const Terms t = terms_of<KIND>(a, row, w, st.m, st.s, z_label);
+        if (rank == 0 && tid == 0) {
+            if (KIND == POLICY) a.loss[row] = t.loss;
+            if (a.logp) a.logp[row] = t.logp;
+        }
+        keep.z = t.slope;
+        scale = t.slope * (a.dloss ? a.dloss[row] : 1.f) * a.inv_t;
+    }
+    if (!GRAD) {
+        if (a.saved) a.saved[row] = keep;
+        return;
+    }
+    const uint32_t nv = s.v1 - s.v0;
+    const bool first = rank == 0, last = rank + 1 == ranks;
+    if (scale == 0.f) zero_slice<T>(z, out, s.head, s.v0, nv, first, last, s.tail0, a.vocab);
+    else {
+        const float scale_q = st.s == 0.f ? 0.f : -scale / st.s;
+        if (far) grad_slice<T, true>(z, out, s.head, s.v0, nv, first, last, s.tail0, a.vocab, st.m, a.c, scale_q, scale, (uint32_t)label);
+        else grad_slice<T, false>(z, out, s.head, s.v0, nv, first, last, s.tail0, a.vocab, st.m, a.c, scale_q, scale, (uint32_t)label);
+    }
+    pdl_leave();
+}
+
+// The backward pass: a CTA takes a slice of a row.
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_backward(const Args a) {
+    pdl_enter();
+    const uint64_t row = blockIdx.x / a.slices;
+    const uint32_t slice = (uint32_t)(blockIdx.x - row * a.slices);
+    const float4 keep = a.saved_in[row];
+    const int index = __float_as_int(keep.w);
+    float scale = 0.f;
+    if (index >= 0 && (!a.dloss || (uint64_t)index < a.losses)) scale = keep.z * (a.dloss ? a.dloss[index] : 1.f) * a.inv_t;
+    const T *z = reinterpret_cast<const T *>(a.logits) + row * a.logits_stride;
+    T *out = reinterpret_cast<T *>(a.dlogits) + row * a.dlogits_stride;
+    const Slice s = slice_of(z, a.vocab, 0, 1, 0);
+    const uint32_t v0 = (uint32_t)((uint64_t)s.nv * slice / a.slices), nv = (uint32_t)((uint64_t)s.nv * (slice + 1) / a.slices) - v0;
+    const bool first = slice == 0, last = slice + 1 == a.slices;
+    if (scale == 0.f) {
+        zero_slice<T>(z, out, s.head, v0, nv, first, last, s.tail0, a.vocab);
+    } else {
+        const int64_t label = load_index(a.labels, a.labels_type, row);
+        const uint32_t at = label >= 0 && label < (int64_t)a.vocab ? (uint32_t)label : 0xffffffffu;
+        const float scale_q = keep.y == 0.f ? 0.f : -scale / keep.y;
+        if (far_row(keep.x, a.c)) grad_slice<T, true>(z, out, s.head, v0, nv, first, last, s.tail0, a.vocab, keep.x, a.c, scale_q, scale, at);
+        else grad_slice<T, false>(z, out, s.head, v0, nv, first, last, s.tail0, a.vocab, keep.x, a.c, scale_q, scale, at);
+    }
+    pdl_leave();
+}
+
+// ------------------------------------------------------------------ pairs of sequences
+
+struct PairArgs {
+    Args a;
+    int kind, mean;
+    float beta, smoothing, margin;
+    const float *ref;
+};
+
+template <class V, class F>
+__device__ __forceinline__ V block_reduce(V v, V *sm, F &&f) {   // the same in every thread
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = sm[threadIdx.x & 31 & (kPairThreads / 32 - 1)];
+#pragma unroll
+    for (int o = kPairThreads / 64; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+    __syncthreads();
+    return v;
+}
+
+// A CTA takes a pair: its sums, its loss, and its rows' slopes.
+template <class T>
+__global__ void __launch_bounds__(kPairThreads) k_pairs(const PairArgs p) {
+    __shared__ double sm_d[kPairThreads / 32];
+    __shared__ long long sm_i[kPairThreads / 32];
+    const Args &a = p.a;
+    pdl_enter();
+    const uint64_t n = 2 * a.pairs;
+    const long long rows = (long long)a.rows;
+    auto offset = [&](uint64_t i) {
+        const long long o = load_index(a.offsets, a.offsets_type, i);
+        return o < 0 ? 0ll : o > rows ? rows : o;
+    };
+    const long long end = offset(n);
+    // the offset that counts: the largest so far, at most the last one
+    auto largest_to = [&](uint64_t i) {
+        long long m = 0;
+        for (uint64_t j = threadIdx.x; j <= i; j += kPairThreads) m = max(m, offset(j));
+        m = block_reduce(m, sm_i, [](long long x, long long y) { return max(x, y); });
+        return min(m, end);
+    };
+    long long lo[2], hi[2];
+    double sum[2];
+    long long count[2];
+    for (int k = 0; k < 2; ++k) {
+        const uint64_t i = blockIdx.x + k * a.pairs;
+        lo[k] = largest_to(i);
+        hi[k] = max(lo[k], min(end, offset(i + 1)));
+        double s = 0;
+        long long c = 0;
+        for (long long r = lo[k] + threadIdx.x; r < hi[k]; r += kPairThreads) {
+            const float4 keep = a.saved[r];
+            if (__float_as_int(keep.w) < 0) continue;
+            ++c;
+            const float z = to_f32(reinterpret_cast<const T *>(a.logits)[(uint64_t)r * a.logits_stride + load_index(a.labels, a.labels_type, r)]);
+            s += keep.x == -INFINITY && keep.y == 0.f ? -INFINITY : ((double)z - keep.x) * a.inv_t64 - log_of(keep.y);
+        }
+        sum[k] = block_reduce(s, sm_d, [](double x, double y) { return x + y; });
+        count[k] = block_reduce(c, sm_i, [](long long x, long long y) { return x + y; });
+        if (p.mean && count[k] > 0) sum[k] /= (double)count[k];
+    }
+    double h = sum[0] - sum[1];
+    if (p.ref) h = (sum[0] - p.ref[blockIdx.x]) - (sum[1] - p.ref[blockIdx.x + a.pairs]);
+    float loss, slope;   // slope: by h
+    if (p.kind == BF16OPT_PREFER_IPO) {
+        const double d = h - p.margin - 0.5 / (double)p.beta;
+        loss = (float)(d * d), slope = 2.f * (float)d;
+    } else {
+        const float m = (float)(h * p.beta - p.margin);
+        if (p.kind == BF16OPT_PREFER_HINGE) {
+            loss = m < 1.f ? 1.f - m : m == m ? 0.f : m;
+            slope = m < 1.f ? -p.beta : m == m ? 0.f : m;
+        } else {
+            const float e = expf(-fabsf(m)), soft = log1pf(e);
+            const float up = m >= 0.f ? 1.f / (1.f + e) : e / (1.f + e), down = m >= 0.f ? e / (1.f + e) : 1.f / (1.f + e);   // sigmoid(m), sigmoid(-m)
+            const float q = p.smoothing;
+            loss = (1.f - q) * (soft + (m < 0.f ? -m : 0.f)) + (q != 0.f ? q * (soft + (m > 0.f ? m : 0.f)) : 0.f);
+            slope = p.beta * (q * up - (1.f - q) * down);
+        }
+    }
+    if (threadIdx.x == 0) {
+        a.loss[blockIdx.x] = loss;
+        a.logp[blockIdx.x] = (float)sum[0];
+        a.logp[blockIdx.x + a.pairs] = (float)sum[1];
+    }
+    for (int k = 0; k < 2; ++k) {
+        const float own = (k ? -slope : slope) * (p.mean && count[k] > 0 ? 1.f / (float)count[k] : 1.f);
+        for (long long r = lo[k] + threadIdx.x; r < hi[k]; r += kPairThreads) {
+            float4 &keep = a.saved[r];
+            if (__float_as_int(keep.w) >= 0) keep.z = own, keep.w = __int_as_float((int)blockIdx.x);
+        }
+    }
+    pdl_leave();
+}
+
+// ---------------------------------------------------------------------- host
+
+struct Part {
+    const void *p;
+    uint64_t n;
+};
+
+int bad(const char *m) { return fail(BF16OPT_ERR_INVALID_ARG, std::string("logp: ") + m); }
+
+// What the calls share: the descriptor, then the outputs against the inputs and one another.  `in` and `outs`: 4-byte
+// aligned arrays; `grad`: dlogits is written.
+int check(const bf16opt_tokens_t *d, std::initializer_list<Part> in, std::initializer_list<Part> outs, const void *dlogits,
+          uint64_t dlogits_stride, bool grad) {
+    const uint64_t eb = type_bytes(d->logits_type);
+    uint64_t zb = 0, gb = 0;
+    if (d->logits_stride < d->vocab || (grad && dlogits_stride < d->vocab)) return bad("a row stride is below vocab");
+    if (!span_bytes(d->rows, d->logits_stride, d->vocab, eb, zb) || (grad && !span_bytes(d->rows, dlogits_stride, d->vocab, eb, gb)))
+        return bad("the sizes overflow");
+    if (d->rows == 0) return BF16OPT_OK;
+    if (!d->logits || !d->labels) return bad("an input pointer is NULL");
+    if (grad && !dlogits) return bad("dlogits is NULL");
+    if (misaligned(d->logits, eb) || misaligned(dlogits, eb) || misaligned(d->labels, index_bytes(d->labels_type)) || misaligned(d->row_weight, 4))
+        return fail(BF16OPT_ERR_ALIGNMENT, "logp: a pointer is not aligned to its element");
+    for (auto *parts : {&in, &outs})
+        for (const Part &x : *parts)
+            if (misaligned(x.p, 4)) return fail(BF16OPT_ERR_ALIGNMENT, "logp: a pointer is not aligned to its element");
+    const Part own[] = {{d->logits, zb}, {d->labels, d->rows * index_bytes(d->labels_type)}, {d->row_weight, d->rows * 4}};
+    const Part dz = {grad ? dlogits : nullptr, gb};
+    auto meets = [&](const Part &o, bool gradient) {
+        for (const Part &x : own) {
+            if (gradient && x.p == d->logits && dlogits == d->logits && dlogits_stride == d->logits_stride) continue;   // in place
+            if (overlap(o.p, o.n, x.p, x.n)) return true;
+        }
+        for (const Part &x : in)
+            if (overlap(o.p, o.n, x.p, x.n)) return true;
+        return false;
+    };
+    if (meets(dz, true)) return bad("an output overlaps an input");
+    for (const Part *o = outs.begin(); o != outs.end(); ++o) {
+        if (meets(*o, false)) return bad("an output overlaps an input");
+        if (overlap(o->p, o->n, dz.p, dz.n)) return bad("two outputs overlap");
+        for (const Part *q = outs.begin(); q != o; ++q)
+            if (overlap(o->p, o->n, q->p, q->n)) return bad("two outputs overlap");
+    }
+    return BF16OPT_OK;
+}
+
+int check_tokens(const bf16opt_tokens_t *d) {
+    if (!d) return bad("the descriptor is NULL");
+    if (!type_ok(d->logits_type)) return bad("unknown element type");
+    if (!index_ok(d->labels_type)) return bad("unknown index type");
+    if (d->vocab < 1 || d->vocab > (1u << 30)) return bad("vocab must lie in [1, 2^30]");
+    if (d->rows > BF16OPT_TOKENS_MAX_ROWS) return bad("rows exceeds BF16OPT_TOKENS_MAX_ROWS");
+    if (!(std::isfinite(d->temperature) && d->temperature > 0.f) || !std::isfinite(1.f / d->temperature) ||
+        !((float)(1.4426950408889634074 / (double)d->temperature) < 1e36f))
+        return bad("temperature must be finite and > 0, with a finite reciprocal");
+    return BF16OPT_OK;
+}
+
+Args args_of(const bf16opt_tokens_t *d) {
+    Args a = {};
+    a.rows = d->rows, a.vocab = d->vocab;
+    a.logits = d->logits, a.logits_stride = d->logits_stride;
+    a.labels = d->labels, a.labels_type = d->labels_type, a.row_weight = d->row_weight;
+    a.inv_t64 = 1.0 / (double)d->temperature, a.inv_t = (float)a.inv_t64;
+    a.c = (float)(1.4426950408889634074 / (double)d->temperature);
+    return a;
+}
+
+template <class T, int KIND, bool GRAD>
+int launch_rows(const Args &a, cudaStream_t stream) {
+    const int sms = sm_count();
+    if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "logp: no CUDA device");
+    // CTAs per row: as many as keep the SMs busy with few rows
+    const uint64_t vecs = a.vocab / Vec<T>::N + 1;
+    unsigned cluster = 1;
+    while (cluster < kMaxCluster && a.rows * cluster <= (uint64_t)sms * 4 && vecs / cluster > 2 * kThreads * kU) cluster *= 2;
+    const Launch l{(unsigned)(a.rows * cluster), kThreads, 0, stream, cluster, true};
+    const cudaError_t e = launch(l, k_rows<T, KIND, GRAD>, a);
+    return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "logp kernel launch");
+}
+
+template <int KIND, bool GRAD>
+int rows_kernel(const Args &a, int type, void *stream) {
+    return type == BF16OPT_TYPE_BF16 ? launch_rows<__nv_bfloat16, KIND, GRAD>(a, (cudaStream_t)stream)
+                                     : launch_rows<float, KIND, GRAD>(a, (cudaStream_t)stream);
+}
+
+int logp_forward(const bf16opt_tokens_t *d, float *logp, float *saved, void *stream) {
+    bf16opt_fail_unbound(BF16OPT_OK, "");
+    int rc = check_tokens(d);
+    if (rc != BF16OPT_OK) return rc;
+    rc = check(d, {}, {{logp, d->rows * 4}, {saved, d->rows * 16}}, nullptr, 0, false);
+    if (rc != BF16OPT_OK || d->rows == 0) return rc;
+    if (!logp) return bad("an output pointer is NULL");
+    if (misaligned(saved, 16)) return fail(BF16OPT_ERR_ALIGNMENT, "logp: saved must be 16-byte aligned");
+    Args a = args_of(d);
+    a.logp = logp, a.saved = reinterpret_cast<float4 *>(saved);
+    return rows_kernel<LOGP, false>(a, d->logits_type, stream);
+}
+
+int logp_backward(const bf16opt_tokens_t *d, const float *saved, const float *dloss, uint64_t losses, void *dlogits, uint64_t dlogits_stride, void *stream) {
+    bf16opt_fail_unbound(BF16OPT_OK, "");
+    int rc = check_tokens(d);
+    if (rc != BF16OPT_OK) return rc;
+    if (losses > BF16OPT_TOKENS_MAX_ROWS) return bad("losses exceeds BF16OPT_TOKENS_MAX_ROWS");
+    rc = check(d, {{saved, d->rows * 16}, {dloss, losses * 4}}, {}, dlogits, dlogits_stride, true);
+    if (rc != BF16OPT_OK || d->rows == 0) return rc;
+    if (!saved) return bad("saved is NULL");
+    if (misaligned(saved, 16)) return fail(BF16OPT_ERR_ALIGNMENT, "logp: saved must be 16-byte aligned");
+    if (sm_count() < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "logp: no CUDA device");
+    Args a = args_of(d);
+    a.saved_in = reinterpret_cast<const float4 *>(saved);
+    a.dloss = dloss, a.losses = losses, a.dlogits = dlogits, a.dlogits_stride = dlogits_stride;
+    const uint64_t vecs = d->vocab / (16 / type_bytes(d->logits_type));
+    a.slices = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(1, vecs / kSliceVectors), 0x7fffffffu / d->rows);
+    const Launch l{(unsigned)(a.rows * a.slices), kThreads, 0, (cudaStream_t)stream, 0, true};
+    const cudaError_t e = d->logits_type == BF16OPT_TYPE_BF16 ? launch(l, k_backward<__nv_bfloat16>, a) : launch(l, k_backward<float>, a);
+    return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "logp kernel launch");
+}
+
+int check_policy(const bf16opt_tokens_t *d, const bf16opt_policy_t *p) {
+    const int rc = check_tokens(d);
+    if (rc != BF16OPT_OK) return rc;
+    if (!p) return bad("the policy's descriptor is NULL");
+    if (!(p->clip_low >= 0.f && p->clip_low <= 1.f) || !(p->clip_high >= 0.f)) return bad("clip_low must lie in [0, 1], clip_high be >= 0");
+    if (!(std::isfinite(p->kl_weight) && p->kl_weight >= 0.f)) return bad("kl_weight must be finite and >= 0");
+    if (p->reserved) return bad("reserved must be 0");
+    return BF16OPT_OK;
+}
+
+template <bool GRAD>
+int policy(const bf16opt_tokens_t *d, const bf16opt_policy_t *p, const float *dloss, float *loss, float *logp, float *saved, void *dlogits,
+           uint64_t dlogits_stride, void *stream) {
+    bf16opt_fail_unbound(BF16OPT_OK, "");
+    int rc = check_policy(d, p);
+    if (rc != BF16OPT_OK) return rc;
+    const uint64_t r4 = d->rows * 4;
+    rc = check(d, {{p->advantage, r4}, {p->old_logp, r4}, {p->ref_logp, r4}, {dloss, r4}}, {{loss, r4}, {logp, r4}, {saved, 4 * r4}}, dlogits,
+               dlogits_stride, GRAD);
+    if (rc != BF16OPT_OK || d->rows == 0) return rc;
+    if (!loss || !p->advantage || (!GRAD && !logp)) return bad("a pointer is NULL");
+    if (misaligned(saved, 16)) return fail(BF16OPT_ERR_ALIGNMENT, "logp: saved must be 16-byte aligned");
+    Args a = args_of(d);
+    a.advantage = p->advantage, a.old_logp = p->old_logp, a.ref_logp = p->kl_weight != 0.f ? p->ref_logp : nullptr;
+    a.lowest = 1.f - p->clip_low, a.highest = 1.f + p->clip_high, a.kl_weight = p->kl_weight;
+    a.dloss = dloss, a.loss = loss, a.logp = logp, a.saved = reinterpret_cast<float4 *>(saved);
+    a.dlogits = dlogits, a.dlogits_stride = dlogits_stride;
+    return rows_kernel<POLICY, GRAD>(a, d->logits_type, stream);
+}
+
+int preference(const bf16opt_tokens_t *d, const bf16opt_preference_t *p, float *loss, float *logp, float *saved, void *stream) {
+    bf16opt_fail_unbound(BF16OPT_OK, "");
+    int rc = check_tokens(d);
+    if (rc != BF16OPT_OK) return rc;
+    if (!p) return bad("the preference's descriptor is NULL");
+    if (!index_ok(p->offsets_type)) return bad("unknown index type");
+    if (p->kind != BF16OPT_PREFER_SIGMOID && p->kind != BF16OPT_PREFER_HINGE && p->kind != BF16OPT_PREFER_IPO) return bad("unknown kind of loss");
+    if (p->pairs > BF16OPT_PREFER_MAX_PAIRS) return bad("pairs exceeds BF16OPT_PREFER_MAX_PAIRS");
+    if (!(std::isfinite(p->beta) && p->beta > 0.f) || !std::isfinite(0.5f / p->beta)) return bad("beta must be finite and > 0");
+    if (!(p->label_smoothing >= 0.f && p->label_smoothing <= 0.5f)) return bad("label_smoothing must lie in [0, 0.5]");
+    if (!std::isfinite(p->margin)) return bad("margin must be finite");
+    if (p->length_normalise != 0 && p->length_normalise != 1) return bad("length_normalise must be 0 or 1");
+    if (d->row_weight) return bad("row_weight must be NULL: labels say which rows count");
+    const uint64_t pairs = p->pairs, ib = index_bytes(p->offsets_type);
+    if (pairs && (!p->offsets || !loss || !logp)) return bad("a pointer is NULL");
+    if (pairs && misaligned(p->offsets, ib)) return fail(BF16OPT_ERR_ALIGNMENT, "logp: a pointer is not aligned to its element");
+    rc = check(d, {{p->offsets, (2 * pairs + 1) * ib}, {p->ref_logp, pairs * 8}}, {{loss, pairs * 4}, {logp, pairs * 8}, {saved, d->rows * 16}}, nullptr, 0, false);
+    if (rc != BF16OPT_OK) return rc;
+    if (d->rows && !saved) return bad("saved is NULL");
+    if (misaligned(saved, 16) || misaligned(loss, 4) || misaligned(logp, 4) || misaligned(p->ref_logp, 4))
+        return fail(BF16OPT_ERR_ALIGNMENT, "logp: saved must be 16-byte aligned, FP32 arrays to their element");
+    Args a = args_of(d);
+    a.offsets = p->offsets, a.offsets_type = p->offsets_type, a.pairs = pairs;
+    a.loss = loss, a.logp = logp, a.saved = reinterpret_cast<float4 *>(saved);
+    if (d->rows) {
+        rc = rows_kernel<PREFER, false>(a, d->logits_type, stream);
+        if (rc != BF16OPT_OK) return rc;
+    }
+    if (!pairs) return BF16OPT_OK;
+    if (sm_count() < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "logp: no CUDA device");
+    PairArgs q = {a, p->kind, p->length_normalise, p->beta, p->label_smoothing, p->margin, p->ref_logp};
+    const Launch l{(unsigned)pairs, kPairThreads, 0, (cudaStream_t)stream, 0, true};
+    const cudaError_t e = d->logits_type == BF16OPT_TYPE_BF16 ? launch(l, k_pairs<__nv_bfloat16>, q) : launch(l, k_pairs<float>, q);
+    return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "logp kernel launch");
+}
+
+}  // namespace
+}  // namespace bf16ops
+
+extern "C" int bf16opt_token_logp_forward(const bf16opt_tokens_t *d, float *logp, float *saved, void *stream) {
+    return bf16ops::guarded([&] { return bf16ops::logp_forward(d, logp, saved, stream); });
+}
+
+extern "C" int bf16opt_token_logp_backward(const bf16opt_tokens_t *d, const float *saved, const float *dloss, uint64_t losses,
+                                           void *dlogits, uint64_t dlogits_stride, void *stream) {
+    return bf16ops::guarded([&] { return bf16ops::logp_backward(d, saved, dloss, losses, dlogits, dlogits_stride, stream); });
+}
+
+extern "C" int bf16opt_policy_forward(const bf16opt_tokens_t *d, const bf16opt_policy_t *p, float *loss, float *logp, float *saved, void *stream) {
+    return bf16ops::guarded([&] { return bf16ops::policy<false>(d, p, nullptr, loss, logp, saved, nullptr, 0, stream); });
+}
+
+extern "C" int bf16opt_policy_loss_grad(const bf16opt_tokens_t *d, const bf16opt_policy_t *p, const float *dloss, float *loss, float *logp,
+                                        void *dlogits, uint64_t dlogits_stride, void *stream) {
+    return bf16ops::guarded([&] { return bf16ops::policy<true>(d, p, dloss, loss, logp, nullptr, dlogits, dlogits_stride, stream); });
+}
+
+extern "C" int bf16opt_preference_forward(const bf16opt_tokens_t *d, const bf16opt_preference_t *p, float *loss, float *logp, float *saved, void *stream) {
+    return bf16ops::guarded([&] { return bf16ops::preference(d, p, loss, logp, saved, stream); });
+}

@@ -188,6 +188,16 @@ inline bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
     return a && b && na && nb && x < y + nb && y < x + na;
 }
 
+// Whether two sets of rows share a byte: `rows` rows of `na` (`nb`) bytes, `sa` (`sb`) bytes apart.  Rows that
+// are columns of one matrix (the same distance apart) do not where their places in that distance are apart.
+inline bool rows_overlap(const void *a, uint64_t sa, uint64_t na, const void *b, uint64_t sb, uint64_t nb, uint64_t rows) {
+    if (rows == 0 || !overlap(a, (rows - 1) * sa + na, b, (rows - 1) * sb + nb)) return false;
+    if (rows == 1 || sa != sb) return true;
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    const uint64_t from = y >= x ? (y - x) % sa : (sa - (x - y) % sa) % sa;   // where b's rows begin behind a's
+    return !(from >= na && from + nb <= sa);
+}
+
 // Multiprocessors of the current device; 0 without one.  Asked once per device.
 inline int sm_count() {
     static std::atomic<int> known[64];

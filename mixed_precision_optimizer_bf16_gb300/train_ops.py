@@ -1,4 +1,5 @@
-"""Training operators from torch tensors: distillation loss, gated norms, expert balance.
+"""Training operators from torch tensors: distillation loss, gated norms, expert balance, policy and
+preference losses, activations kept in 8 bits, rotary positions.
 
 Marshalling only (shapes, types, data_ptr()s, stream handles, status ->
 exception); all arithmetic is in libbf16opt.so (the "training operators" of
@@ -10,12 +11,17 @@ can be captured in a CUDA graph.
   distill_forward / distill_backward / distill_loss_grad, distill_loss (autograd)
   norm_gate_forward / norm_gate_backward, norm_gate (autograd)
   balance_forward / balance_backward, balance (autograd)
+  token_logp_forward / policy_forward / preference_forward, token_logp_backward (of all three),
+  policy_loss_grad; token_logp, policy_loss, preference_loss (autograd)
+  pack8 / unpack8; glu8_forward / glu8_backward, glu8 (autograd)
+  rotary_forward / rotary_backward, rotary (autograd)
 
 The autograd forms have first derivatives only: going through a gradient of theirs once more
 is an error.
 """
 import contextlib
 import functools
+import math
 import struct
 
 import torch
@@ -34,6 +40,12 @@ _ACT = {None: C.BF16OPT_GATE_IDENTITY, "none": C.BF16OPT_GATE_IDENTITY, "sigmoid
 _DISTILL_T = struct.Struct("@QII4iPQPQPQPPPfff4x")
 _NORM_GATE_T = struct.Struct("@QI6iIQPPPPPfff4x")
 _BALANCE_T = struct.Struct("@QIIQiiPQPff")
+_TOKENS_T = struct.Struct("@QIiifPQPP")
+_POLICY_T = struct.Struct("@PPPfffI")
+_PREFERENCE_T = struct.Struct("@QiiPPfffi")
+_PACK_T = struct.Struct("@QIi")
+_GLU_T = struct.Struct("@QIiii")
+_ROTARY_T = struct.Struct("@QQIIIIiiiiPQqPfI12Q")
 
 _empty, _empty_like = torch.empty, torch.empty_like
 _Tensor = torch.Tensor
@@ -460,3 +472,432 @@ def balance(logits, k, *, mask=None, groups=1, balance_weight=1e-2, z_weight=0.0
     through weights and loss."""
     return _Balance.apply(logits, k, mask, dict(groups=groups, balance_weight=balance_weight, z_weight=z_weight,
                                                 renormalise=renormalise))
+
+
+# ------------------------------------- log-probabilities, policy and preference losses
+
+_PREFER = {"sigmoid": C.BF16OPT_PREFER_SIGMOID, "hinge": C.BF16OPT_PREFER_HINGE, "ipo": C.BF16OPT_PREFER_IPO}
+
+
+def _tokens(logits, labels, temperature, row_weight):
+    """(descriptor, rows, device index)."""
+    rows, vocab, index = _matrix(logits, "logits")
+    _need(logits, "logits", _TYPE, (rows, vocab), index, True)
+    _need(labels, "labels", _INDEX, (rows,), index)
+    if row_weight is not None:
+        _need(row_weight, "row_weight", _F32, (rows,), index)
+    return _TOKENS_T.pack(rows, vocab, _TYPE[logits.dtype], _INDEX[labels.dtype], temperature, logits.data_ptr(), _stride(logits),
+                          labels.data_ptr(), _p(row_weight)), rows, index
+
+
+def _policy(rows, index, advantage, old_logp, ref_logp, clip_low, clip_high, kl_weight):
+    _need(advantage, "advantage", _F32, (rows,), index)
+    if old_logp is not None:
+        _need(old_logp, "old_logp", _F32, (rows,), index)
+    if ref_logp is not None:
+        _need(ref_logp, "ref_logp", _F32, (rows,), index)
+    return _POLICY_T.pack(advantage.data_ptr(), _p(old_logp), _p(ref_logp), clip_low, clip_high, kl_weight, 0)
+
+
+def _rows_of(logits, columns):
+    shape = (logits.shape[0], columns) if columns else logits.shape[:1]
+    return _empty(shape, dtype=torch.float32, device=logits.device)
+
+
+@_on_stream
+def token_logp_forward(logits, labels, *, temperature=1.0, row_weight=None):
+    """Log-probabilities [rows] (FP32) that softmax(logits / temperature) gives
+    to labels [rows] (int32 or int64), and saved [rows, 4] for
+    token_logp_backward.  logits: [rows, vocab] bf16 or FP32.  A row with row_weight 0 or
+    with a label outside the vocabulary does not count: it is not read and has 0."""
+    d, rows, index = _tokens(logits, labels, temperature, row_weight)
+    logp, saved = _rows_of(logits, 0), _rows_of(logits, 4)
+    C.check(C.bf16opt_token_logp_forward(d, logp.data_ptr(), saved.data_ptr(), _raw_stream(index)))
+    return logp, saved
+
+
+@_on_stream
+def policy_forward(logits, labels, advantage, *, old_logp=None, ref_logp=None, clip_low=0.2, clip_high=0.2, kl_weight=0.0,
+                   temperature=1.0, row_weight=None):
+    """Clipped policy loss of each token, with kl_weight times an estimate of the
+    KL distance to a reference: (loss [rows], logp [rows], saved [rows, 4]), FP32.
+    advantage, old_logp (None: the tokens are this model's own, ratio 1) and ref_logp (None: no
+    KL term): [rows] FP32, constants."""
+    d, rows, index = _tokens(logits, labels, temperature, row_weight)
+    p = _policy(rows, index, advantage, old_logp, ref_logp, clip_low, clip_high, kl_weight)
+    loss, logp, saved = _rows_of(logits, 0), _rows_of(logits, 0), _rows_of(logits, 4)
+    C.check(C.bf16opt_policy_forward(d, p, loss.data_ptr(), logp.data_ptr(), saved.data_ptr(), _raw_stream(index)))
+    return loss, logp, saved
+
+
+@_on_stream
+def policy_loss_grad(logits, labels, advantage, dloss=None, *, old_logp=None, ref_logp=None, clip_low=0.2, clip_high=0.2,
+                     kl_weight=0.0, temperature=1.0, row_weight=None, out=None):
+    """(loss [rows], logp [rows], gradient of the logits), for a gradient dloss
+    [rows], or 1, of each row's loss, in one pass over the logits.  out may be logits itself."""
+    d, rows, index = _tokens(logits, labels, temperature, row_weight)
+    p = _policy(rows, index, advantage, old_logp, ref_logp, clip_low, clip_high, kl_weight)
+    if dloss is not None:
+        _need(dloss, "dloss", _F32, (rows,), index)
+    loss, logp = _rows_of(logits, 0), _rows_of(logits, 0)
+    given, out = out, _dlogits(logits, out, index)
+    C.check(C.bf16opt_policy_loss_grad(d, p, _p(dloss), loss.data_ptr(), logp.data_ptr(), out.data_ptr(), _stride(out), _raw_stream(index)))
+    _written(given)
+    return loss, logp, out
+
+
+@_on_stream
+def preference_forward(logits, labels, offsets, *, ref_logp=None, kind="sigmoid", beta=0.1, label_smoothing=0.0, margin=0.0,
+                       length_normalise=False, temperature=1.0):
+    """Loss of pairs of sequences, one preferred to the other: (loss [pairs], logp
+    [2 pairs] (the sequences' log-probabilities), saved [rows, 4]), FP32.  offsets [2 pairs + 1] (int32 or
+    int64): sequence i is rows offsets[i] to offsets[i + 1]; sequence i is preferred to sequence
+    pairs + i.  Rows whose label is outside the vocabulary (prompts, padding) and rows outside the
+    sequences do not count.  ref_logp [2 pairs] FP32: a reference's (None: 0).
+    kind: 'sigmoid', 'hinge' or 'ipo'."""
+    d, rows, index = _tokens(logits, labels, temperature, None)
+    if kind not in _PREFER:
+        raise ValueError("kind: 'sigmoid', 'hinge' or 'ipo'")
+    entries = offsets.shape[0] if isinstance(offsets, _Tensor) and offsets.dim() == 1 else 0
+    if entries % 2 == 0:
+        raise ValueError("offsets: must be [2 pairs + 1]")
+    _need(offsets, "offsets", _INDEX, (entries,), index)
+    if ref_logp is not None:
+        _need(ref_logp, "ref_logp", _F32, (entries - 1,), index)
+    pairs = entries // 2
+    p = _PREFERENCE_T.pack(pairs, _INDEX[offsets.dtype], _PREFER[kind], offsets.data_ptr(), _p(ref_logp), beta, label_smoothing, margin,
+                           1 if length_normalise else 0)
+    loss = _empty(pairs, dtype=torch.float32, device=logits.device)
+    logp = _empty(2 * pairs, dtype=torch.float32, device=logits.device)
+    saved = _rows_of(logits, 4)
+    C.check(C.bf16opt_preference_forward(d, p, loss.data_ptr(), logp.data_ptr(), saved.data_ptr(), _raw_stream(index)))
+    return loss, logp, saved
+
+
+@_on_stream
+def token_logp_backward(logits, labels, saved, dloss=None, *, temperature=1.0, out=None):
+    """Gradient of the logits from that of the losses (or log-probabilities) of
+    token_logp_forward, policy_forward or preference_forward, with its saved and the same
+    logits, labels and temperature.  dloss: FP32, one for each loss; None: 1.  out may be
+    logits itself."""
+    d, rows, index = _tokens(logits, labels, temperature, None)
+    _need(saved, "saved", _F32, (rows, 4), index)
+    losses = 0
+    if dloss is not None:
+        losses = dloss.shape[0] if isinstance(dloss, _Tensor) and dloss.dim() == 1 else 0
+        _need(dloss, "dloss", _F32, (losses,), index)
+    given, out = out, _dlogits(logits, out, index)
+    C.check(C.bf16opt_token_logp_backward(d, saved.data_ptr(), _p(dloss), losses, out.data_ptr(), _stride(out), _raw_stream(index)))
+    _written(given)
+    return out
+
+
+def _constants(**tensors):
+    """The losses are differentiable in the logits alone."""
+    for n, t in tensors.items():
+        if isinstance(t, _Tensor) and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{n}: requires a gradient, which the loss does not give; detach it")
+
+
+class _TokenLoss(torch.autograd.Function):
+    """The three forward calls: (losses, further results that are constants)."""
+    @staticmethod
+    def forward(ctx, logits, labels, temperature, call):
+        loss, *more, saved = call()
+        ctx.save_for_backward(logits, labels, saved)
+        ctx.temperature = temperature
+        ctx.mark_non_differentiable(*more)
+        return (loss, *more)
+
+    @staticmethod
+    @_first_only
+    def backward(ctx, dloss, *_):
+        logits, labels, saved = ctx.saved_tensors
+        return token_logp_backward(logits, labels, saved, dloss.float().contiguous(), temperature=ctx.temperature), None, None, None
+
+
+def token_logp(logits, labels, *, temperature=1.0, row_weight=None):
+    """Log-probabilities [rows] as token_logp_forward, differentiable in logits."""
+    _constants(row_weight=row_weight)
+    return _TokenLoss.apply(logits, labels, temperature,
+                            lambda: token_logp_forward(logits, labels, temperature=temperature, row_weight=row_weight))[0]
+
+
+def policy_loss(logits, labels, advantage, *, old_logp=None, ref_logp=None, clip_low=0.2, clip_high=0.2, kl_weight=0.0,
+                temperature=1.0, row_weight=None):
+    """(loss [rows], logp [rows]) as policy_forward, the loss differentiable in logits; logp is a constant."""
+    _constants(advantage=advantage, old_logp=old_logp, ref_logp=ref_logp, row_weight=row_weight)
+    return _TokenLoss.apply(logits, labels, temperature, lambda: policy_forward(
+        logits, labels, advantage, old_logp=old_logp, ref_logp=ref_logp, clip_low=clip_low, clip_high=clip_high,
+        kl_weight=kl_weight, temperature=temperature, row_weight=row_weight))
+
+
+def preference_loss(logits, labels, offsets, *, ref_logp=None, kind="sigmoid", beta=0.1, label_smoothing=0.0, margin=0.0,
+                    length_normalise=False, temperature=1.0):
+    """(loss [pairs], logp [2 pairs]) as preference_forward, the loss differentiable in logits; logp is a constant."""
+    _constants(ref_logp=ref_logp)
+    return _TokenLoss.apply(logits, labels, temperature, lambda: preference_forward(
+        logits, labels, offsets, ref_logp=ref_logp, kind=kind, beta=beta, label_smoothing=label_smoothing, margin=margin,
+        length_normalise=length_normalise, temperature=temperature))
+
+
+# -------------------------------------------------------- activations kept in 8 bits
+
+_GLU = {"silu": C.BF16OPT_GLU_SILU, "gelu": C.BF16OPT_GLU_GELU}
+_U8 = (torch.uint8,)
+
+
+def _output(out, like, what, shape, index):
+    if out is None:
+        return _empty(shape, dtype=like.dtype, device=like.device)
+    _need(out, what, (like.dtype,), shape, index, True)
+    _writable(out, what)
+    return out
+
+
+@_on_stream
+def pack8(x):
+    """(codes [rows, 32 runs], scales [rows, runs]), uint8, of an activation x [rows,
+    columns] (bf16 or FP32): each run of 32 columns as e4m3 numbers times the power of two
+    2^(scale - 127)."""
+    rows, columns, index = _matrix(x, "x")
+    _need(x, "x", _TYPE, (rows, columns), index, True)
+    runs = (columns + 31) // 32
+    codes = _empty((rows, 32 * runs), dtype=torch.uint8, device=x.device)
+    scales = _empty((rows, runs), dtype=torch.uint8, device=x.device)
+    C.check(C.bf16opt_pack(_PACK_T.pack(rows, columns, _TYPE[x.dtype]), x.data_ptr(), _stride(x), codes.data_ptr(), scales.data_ptr(),
+                           _raw_stream(index)))
+    return codes, scales
+
+
+@_on_stream
+def unpack8(codes, scales, columns, *, dtype=torch.bfloat16, out=None):
+    """[rows, columns] of what pack8 kept, rounded to dtype (bf16 holds it exactly but below its smallest normal
+    number)."""
+    rows, wide, index = _matrix(codes, "codes")
+    runs = (columns + 31) // 32
+    _need(codes, "codes", _U8, (rows, 32 * runs), index)
+    _need(scales, "scales", _U8, (rows, runs), index)
+    if dtype not in _TYPE:
+        raise ValueError("dtype: bf16 or FP32")
+    if out is None:
+        x = _empty((rows, columns), dtype=dtype, device=codes.device)
+    else:
+        _need(out, "out", (dtype,), (rows, columns), index, True)
+        _writable(out, "out")
+        x = out
+    C.check(C.bf16opt_unpack(_PACK_T.pack(rows, columns, _TYPE[dtype]), codes.data_ptr(), scales.data_ptr(), x.data_ptr(), _stride(x),
+                             _raw_stream(index)))
+    _written(out)
+    return x
+
+
+@_on_stream
+def glu8_forward(gate, up=None, *, act="silu", keep=True, out=None):
+    """(h, codes, scales): h = act(gate) up, or act(gate) without up, [rows, columns] bf16
+    or FP32 (rows may be apart: halves of one projection); codes [parts, rows, 32 runs] and scales [parts, rows, runs],
+    uint8: gate and up as pack8 keeps them, for glu8_backward (keep=False: None).
+    act: 'silu' or 'gelu' (by tanh).  out may be gate or up."""
+    rows, columns, index = _matrix(gate, "gate")
+    _need(gate, "gate", _TYPE, (rows, columns), index, True)
+    if up is not None:
+        _need(up, "up", (gate.dtype,), (rows, columns), index, True)
+    if act not in _GLU:
+        raise ValueError("act: 'silu' or 'gelu'")
+    parts, runs = 1 if up is None else 2, (columns + 31) // 32
+    h = _output(out, gate, "out", (rows, columns), index)
+    codes = _empty((parts, rows, 32 * runs), dtype=torch.uint8, device=gate.device) if keep else None
+    scales = _empty((parts, rows, runs), dtype=torch.uint8, device=gate.device) if keep else None
+    d = _GLU_T.pack(rows, columns, _TYPE[gate.dtype], _GLU[act], parts - 1)
+    C.check(C.bf16opt_glu_forward(d, gate.data_ptr(), _stride(gate), _p(up), _stride(up) if up is not None else 0, h.data_ptr(), _stride(h),
+                                  _p(codes), _p(scales), _raw_stream(index)))
+    _written(out)
+    return h, codes, scales
+
+
+@_on_stream
+def glu8_backward(dh, codes, scales, *, act="silu", out_gate=None, out_up=None, out_h=None):
+    """(dgate, dup) of glu8_forward from the gradient of h and what was kept; dup None without up.  out_gate and
+    out_up may be halves of one matrix; out_h: where act(gate) up of what was kept is wanted too.  One of
+    them may be dh."""
+    rows, columns, index = _matrix(dh, "dh")
+    _need(dh, "dh", _TYPE, (rows, columns), index, True)
+    runs = (columns + 31) // 32
+    parts = codes.shape[0] if isinstance(codes, _Tensor) and codes.dim() == 3 and codes.shape[0] in (1, 2) else 2
+    _need(codes, "codes", _U8, (parts, rows, 32 * runs), index)
+    _need(scales, "scales", _U8, (parts, rows, runs), index)
+    if act not in _GLU:
+        raise ValueError("act: 'silu' or 'gelu'")
+    if parts == 1 and out_up is not None:
+        raise ValueError("out_up: there is no up")
+    dgate = _output(out_gate, dh, "out_gate", (rows, columns), index)
+    dup = _output(out_up, dh, "out_up", (rows, columns), index) if parts == 2 else None
+    if out_h is not None:
+        _output(out_h, dh, "out_h", (rows, columns), index)
+    d = _GLU_T.pack(rows, columns, _TYPE[dh.dtype], _GLU[act], parts - 1)
+    C.check(C.bf16opt_glu_backward(d, dh.data_ptr(), _stride(dh), codes.data_ptr(), scales.data_ptr(), dgate.data_ptr(), _stride(dgate),
+                                   _p(dup), _stride(dup) if dup is not None else 0, _p(out_h), _stride(out_h) if out_h is not None else 0,
+                                   _raw_stream(index)))
+    _written(out_gate, out_up, out_h)
+    return dgate, dup
+
+
+class _Glu8(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate, up, act):
+        h, codes, scales = glu8_forward(gate, up, act=act, keep=any(ctx.needs_input_grad))
+        ctx.save_for_backward(codes, scales)
+        ctx.act = act
+        return h
+
+    @staticmethod
+    @_first_only
+    def backward(ctx, dh):
+        codes, scales = ctx.saved_tensors
+        return (*glu8_backward(dh if dh.stride(1) == 1 and dh.stride(0) >= dh.shape[1] else dh.contiguous(), codes, scales, act=ctx.act), None)
+
+
+def glu8(gate, up=None, *, act="silu"):
+    """h as glu8_forward, differentiable in gate and up.  Autograd keeps 33 / 32 bytes for each of their elements, and
+    their gradients are those at the values that were kept."""
+    return _Glu8.apply(gate, up, act)
+
+
+# ------------------------------------------------------------------ rotary positions
+
+_LAYOUT = {"half": C.BF16OPT_ROTARY_HALF, "interleaved": C.BF16OPT_ROTARY_INTERLEAVED}
+
+
+@functools.lru_cache(maxsize=256)
+def _frequencies(rotary_dim, base, scaling, factor, original_length, slow, fast):
+    """(radians per position as packed doubles, their address, factor on the turned pairs' length)."""
+    import ctypes
+    if not (isinstance(rotary_dim, int) and rotary_dim >= 2 and rotary_dim % 2 == 0):
+        raise ValueError("rotary_dim: must be even and at least 2")
+    if not (math.isfinite(base) and base > 0 and math.isfinite(factor) and factor > 0):
+        raise ValueError("base, factor: must be finite and > 0")
+    scale = 1.0
+    if scaling == "ntk":
+        if rotary_dim < 4:
+            raise ValueError("scaling 'ntk': rotary_dim must be at least 4")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = [base ** (-2 * i / rotary_dim) for i in range(rotary_dim // 2)]
+    if scaling == "linear":
+        f = [v / factor for v in f]
+    elif scaling == "yarn":
+        if not (original_length > 0 and 0 <= slow < fast):
+            raise ValueError("scaling 'yarn': original_length > 0 and 0 <= slow < fast")
+        keep = [min(1.0, max(0.0, (original_length * v / (2 * math.pi) - slow) / (fast - slow))) for v in f]
+        f = [v * (k + (1 - k) / factor) for v, k in zip(f, keep)]
+        scale = 0.1 * math.log(factor) + 1 if factor > 1 else 1.0
+    elif scaling not in (None, "none", "ntk"):
+        raise ValueError("scaling: None, 'linear', 'ntk' or 'yarn'")
+    table = (ctypes.c_double * len(f))(*f)
+    return table, ctypes.addressof(table), scale
+
+
+def _heads(t, what, dtypes, like=None):
+    """(strides between batches, tokens and heads) of [tokens, heads, dim] or [batch, tokens, heads, dim]."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise ValueError(f"{what}: must be a CUDA tensor")
+    n = t.dim()
+    if n not in (3, 4) or t.dtype not in dtypes or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what}: must be [tokens, heads, dim] or [batch, tokens, heads, dim], of {[str(d) for d in dtypes]}, contiguous within heads")
+    if like is not None and (t.get_device() != like.get_device() or t.shape[:-2] != like.shape[:-2] or t.shape[-1] != like.shape[-1]):
+        raise ValueError(f"{what}: shape {tuple(t.shape)} on {t.device} does not go with {tuple(like.shape)} on {like.device}")
+    s = t.stride()
+    return (0, s[0], s[1]) if n == 3 else s[:3]
+
+
+@_on_stream
+def _rotary(q, k, positions, rotary_dim, layout, base, scaling, factor, original_length, slow, fast, offset, out_q, out_k, inverse):
+    sq = _heads(q, "q", _TYPE)
+    index, dim, heads = q.get_device(), q.shape[-1], q.shape[-2]
+    dtypes = (q.dtype,)
+    sk, kv = (0, 0, 0), 0
+    if k is not None:
+        sk, kv = _heads(k, "k", dtypes, q), k.shape[-2]
+    batch, seq = (1, q.shape[0]) if q.dim() == 3 else q.shape[:2]
+    if layout not in _LAYOUT:
+        raise ValueError("layout: 'half' or 'interleaved'")
+    each = 0
+    if positions is not None:
+        shared = isinstance(positions, _Tensor) and positions.dim() == 1
+        _need(positions, "positions", _INDEX, (seq,) if shared else (batch, seq), index)
+        each = 0 if shared else seq
+    if out_k is not None and k is None:
+        raise ValueError("out_k: there is no k")
+    outs = []
+    for x, out, what in ((q, out_q, "out_q"), (k, out_k, "out_k")):
+        if out is not None:
+            _heads(out, what, dtypes, q)
+            if out.shape != x.shape:
+                raise ValueError(f"{what}: shape {tuple(out.shape)}, expected {tuple(x.shape)}")
+            _writable(out, what)
+        outs.append(out if out is not None or x is None else _empty(x.shape, dtype=x.dtype, device=x.device))
+    rq, rk = outs
+    rotary_dim = dim if rotary_dim is None else rotary_dim
+    if kv == 0 or heads == 0:   # nothing of k (or of q)
+        if heads == 0:
+            if kv == 0:
+                return rq, rk
+            sq, heads, kv, sk = sk, kv, 0, (0, 0, 0)
+            first, second, ofirst, osecond = k, None, rk, None
+        else:
+            first, second, ofirst, osecond = q, None, rq, None
+    else:
+        first, second, ofirst, osecond = q, k, rq, rk
+    table, address, scale = _frequencies(rotary_dim, base, scaling, factor, original_length, slow, fast)
+    so = _heads(ofirst, "out_q", dtypes)
+    d = _ROTARY_T.pack(batch, seq, heads, kv, dim, rotary_dim, _TYPE[q.dtype], _LAYOUT[layout],
+                       _INDEX[positions.dtype] if positions is not None else 0, inverse, _p(positions), each, offset, address, scale, 0,
+                       *sq, *sk, *so, *(_heads(osecond, "out_k", dtypes) if osecond is not None else (0, 0, 0)))
+    C.check(C.bf16opt_rotary(d, first.data_ptr(), _p(second), ofirst.data_ptr(), _p(osecond), _raw_stream(index)))
+    _written(out_q, out_k)
+    return rq, rk
+
+
+def rotary_forward(q, k=None, positions=None, *, rotary_dim=None, layout="half", base=10000.0, scaling=None, factor=1.0,
+                   original_length=2048, slow=1.0, fast=32.0, offset=0, out_q=None, out_k=None, stream=None):
+    """(q, k) with positions turned into the first rotary_dim elements of each head
+    (None: all).  q: [tokens, heads, dim] or [batch, tokens, heads, dim], k (or None) the same with its own number of
+    heads; bf16 or FP32; any strides with contiguous heads.  positions: None (0, 1, ..), [tokens] or [batch, tokens],
+    int32 or int64; offset is added.  layout: pairs are (i, i + rotary_dim / 2) ('half') or neighbours
+    ('interleaved').  Pair i turns by base^(-2 i / rotary_dim) a position;
+    scaling for longer contexts: 'linear' (frequencies / factor), 'ntk' (base factor^(d / (d - 2))), 'yarn'
+    (pairs that turn less than `slow` times in original_length are slowed by factor, those above `fast` are
+    not, between them a ramp; the turned pairs are 0.1 ln(factor) + 1 times as long).  out_q may be q, out_k may be k."""
+    return _rotary(q, k, positions, rotary_dim, layout, base, scaling, factor, original_length, slow, fast, offset, out_q, out_k, 0,
+                   stream=stream)
+
+
+def rotary_backward(dq, dk=None, positions=None, *, rotary_dim=None, layout="half", base=10000.0, scaling=None, factor=1.0,
+                    original_length=2048, slow=1.0, fast=32.0, offset=0, out_q=None, out_k=None, stream=None):
+    """Gradients of rotary_forward's inputs from those of its results: the same, turned back."""
+    return _rotary(dq, dk, positions, rotary_dim, layout, base, scaling, factor, original_length, slow, fast, offset, out_q, out_k, 1,
+                   stream=stream)
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, how):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(positions)
+        ctx.how = how
+        return rotary_forward(q, k, positions, **how)
+
+    @staticmethod
+    @_first_only
+    def backward(ctx, dq, dk):
+        positions, = ctx.saved_tensors
+        grads = [g if g is None or g.shape[-1] < 2 or g.stride(-1) == 1 else g.contiguous() for g in (dq, dk)]
+        if grads[0] is None:
+            return None, rotary_backward(grads[1], None, positions, **ctx.how)[0] if grads[1] is not None else None, None, None
+        return (*rotary_backward(grads[0], grads[1], positions, **ctx.how), None, None)
+
+
+def rotary(q, k=None, positions=None, *, rotary_dim=None, layout="half", base=10000.0, scaling=None, factor=1.0,
+           original_length=2048, slow=1.0, fast=32.0, offset=0):
+    """(q, k) as rotary_forward, differentiable in both."""
+    return _Rotary.apply(q, k, positions, dict(rotary_dim=rotary_dim, layout=layout, base=base, scaling=scaling, factor=factor,
+                                               original_length=original_length, slow=slow, fast=fast, offset=offset))
