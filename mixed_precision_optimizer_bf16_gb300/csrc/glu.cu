@@ -21,39 +21,60 @@ struct Rows {
     uint64_t stride;   // elements
 };
 
+// n / d for every 32-bit n: the high word of n times m, m the first number that 2^(32 + shift) / d, less 2^32, does not
+// exceed (Granlund and Montgomery, PLDI 1994).
+struct Divisor {
+    uint32_t d, m, shift;
+    Divisor() = default;
+    explicit Divisor(uint32_t x) : d(x) {
+        uint32_t l = 0;
+        while ((1ull << l) < x) ++l;
+        m = (uint32_t)(((1ull << 32) * ((1ull << l) - x)) / x + 1);
+        shift = l;
+    }
+    __host__ __device__ __forceinline__ uint32_t of(uint32_t n) const {
+        const uint32_t t = (uint32_t)((uint64_t)n * m >> 32);
+        return shift ? (t + ((n - t) >> 1)) >> (shift - 1) : n;
+    }
+};
+
 struct Args {
     Rows x[2];         // forward: gate, up; backward: dh
     void *out[3];      // forward: h; backward: dgate, dup, h
     uint64_t out_stride[3];
     uint8_t *codes, *scales;
     uint64_t rows;
-    uint32_t columns, runs;
+    uint32_t columns;
+    Divisor runs;      // of a row
+    uint32_t all_runs; // rows times them, below 2^31
 };
 
 // ------------------------------------------------------------------ a run's scale
 
 // The scale's byte for a run whose largest finite magnitude has the bits `m`: its exponent less 8, one
-// more where the fraction is above 1.75 (448 = 1.75 * 2^8), and no less than 0.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t m) {
-    const uint32_t e = (m + 0x1fffffu) >> 23;
+// more where the fraction is above 1.75 (448 = 1.75 * 2^8), and no less than 0.  It grows with m, so a run's is the
+// largest of its parts'.
+__device__ __forceinline__ uint32_t scale_byte(float m) {
+    const uint32_t e = (__float_as_uint(m) + 0x1fffffu) >> 23;
     return e > 8 ? e - 8 : 0u;
 }
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 1u << 22); }   // 2^(byte - 127)
 __device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// What would be rounded to 2^128 is kept as the number below it, 1.875 2^127; an infinity as NaN.
-constexpr float kTooLarge = 0x1.fp127f;
+// What would be rounded to 2^128 is kept as the number below it, 1.875 2^127; an infinity as NaN.  Only a run
+// with the largest byte there is, which an infinity gives too, may have either.
+constexpr uint32_t kLargestByte = 247;
 __device__ __forceinline__ float holdable(float x) {
-    return fabsf(x) < kTooLarge ? x : fabsf(x) < INFINITY ? copysignf(0x1.ep127f, x) : NAN;
+    return fabsf(x) < 0x1.fp127f ? x : fabsf(x) < INFINITY ? copysignf(0x1.ep127f, x) : NAN;
 }
 
-// Two floats to e4m3, the first in the low byte.  (NaN stays NaN; an infinity is made one before.)
+// Two floats to e4m3, the first in the low byte (NaN stays NaN), and back, exact in fp16.
 __device__ __forceinline__ uint32_t to_codes(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ float2 from_codes(uint32_t two) {   // exact in fp16
+__device__ __forceinline__ float2 from_codes(uint32_t two) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
     float2 f;
@@ -63,210 +84,305 @@ __device__ __forceinline__ float2 from_codes(uint32_t two) {   // exact in fp16
 
 // ------------------------------------------------------------------ the activation
 
-// sigmoid(y) and 1 - sigmoid(y): e = exp(-y), 1 / (1 + e) and e / (1 + e), each exact where the other cancels.  The
-// exponent stops at 2^127: 1 / (1 + 2^127) is flushed to 0, and 0 e is 0.
-__device__ __forceinline__ void sigmoids(float y, float &s, float &rest) {
-    const float x = y * -kLog2e;
-    const float e = ex2(x > 127.f ? 127.f : x);   // (a NaN stays one)
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
-    rest = e * s;
+__device__ __forceinline__ float clamped(float x, float most) {   // NaN stays
+    float r;
+    asm("{\n .reg .f32 t;\n min.NaN.f32 t, %1, %2;\n max.NaN.f32 %0, t, %3;\n}" : "=f"(r) : "f"(x), "f"(most), "f"(-most));
+    return r;
+}
+__device__ __forceinline__ float reciprocal(float x) {   // 0 above 2^126
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-// act(g) = g sigmoid(y), y = g (silu) or 2 sqrt(2 / pi) (g + 0.044715 g^3) (gelu: (1 + tanh(y / 2)) / 2 = sigmoid(y)), and
-// act'(g) = sigmoid(y) + g sigmoid(y) (1 - sigmoid(y)) y'.  Beyond +-64 the sigmoid is 0 or 1, and g^3 is not formed.
+// act(g) = g s, s = sigmoid(y), y = g (silu) or 2 sqrt(2 / pi) (g + 0.044715 g^3) (gelu: (1 + tanh(y / 2)) / 2 = sigmoid(y));
+// act'(g) = s + g y' s (1 - s).  1 - s as a difference is off by 2^-24, which times g y' is about |y| 2^-24 of act'.  Beyond
+// +-64 gelu's sigmoid is 0 or 1, and g^3 is not formed.
 template <int ACT>
-__device__ __forceinline__ float activate(float g, float &slope) {
+__device__ __forceinline__ float2 activate(float2 g, float2 &slope) {
     constexpr float kRoot = 1.59576912160573071f;   // 2 sqrt(2 / pi)
-    float y = g, c = g, dy = 1.f;
+    float2 y = g, p = g;
     if (ACT == BF16OPT_GLU_GELU) {
-        c = g > 64.f ? 64.f : g < -64.f ? -64.f : g;
-        const float q = c * c;
-        y = kRoot * c * fmaf(0.044715f, q, 1.f);
-        dy = kRoot * fmaf(3.f * 0.044715f, q, 1.f);
+        const float2 c = make_float2(clamped(g.x, 64.f), clamped(g.y, 64.f)), q = mul2(c, c), r = mul2(c, both(kRoot));
+        y = mul2(r, fma2(q, both(0.044715f), both(1.f)));
+        p = mul2(r, fma2(q, both(3.f * 0.044715f), both(1.f)));
     }
-    float s, rest;
-    sigmoids(y, s, rest);
-    slope = fmaf(c * dy, s * rest, s);
-    return g * s;
+    const float2 x = mul2(y, both(-kLog2e)), t = add2(make_float2(ex2(x.x), ex2(x.y)), both(1.f));
+    const float2 s = make_float2(reciprocal(t.x), reciprocal(t.y));
+    slope = fma2(p, mul2(s, fma2(s, both(-1.f), both(1.f))), s);
+    return mul2(g, s);
 }
 
 // ------------------------------------------------------------------ eight columns of a thread
 
-// VECTOR: eight neighbours, four lanes to a run; rows and their starts are multiples of 16 bytes.
-// Otherwise columns lane, lane + 32, ..: a run is a warp's, whatever the alignment.
+// VECTOR: eight neighbours from `first`, four lanes to a run; rows and their starts are multiples of 16 bytes.
+// Otherwise columns first, first + 32, ..: a run is a warp's, whatever the alignment.
 template <class T, bool VECTOR>
 struct Eight {
-    // column of element i
+    static constexpr int W = sizeof(T) / 2;
+    union {
+        uint4 v[W];
+        T e[8];
+    };
+    __device__ __forceinline__ Eight() {}
     __device__ __forceinline__ static uint32_t column(uint32_t first, int i) { return VECTOR ? first + i : first + 32 * i; }
-    __device__ __forceinline__ static void load(const T *row, uint32_t first, uint32_t columns, float (&f)[8]) {
+    __device__ __forceinline__ void load(const T *row, uint32_t first, uint32_t columns) {
         if (VECTOR && first + 8 <= columns) {
-            const uint4 *v = reinterpret_cast<const uint4 *>(row + first);
-            if constexpr (sizeof(T) == 2) {
-                Vec<T>::unpack(__ldcs(v), f);
-            } else {
-                float a[4], b[4];
-                const uint4 x = __ldcs(v), y = __ldcs(v + 1);
-                Vec<T>::unpack(x, a), Vec<T>::unpack(y, b);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
-            }
+            for (int w = 0; w < W; ++w) v[w] = __ldcs(reinterpret_cast<const uint4 *>(row + first) + w);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = column(first, i) < columns ? to_f32(row[column(first, i)]) : 0.f;
+            for (int i = 0; i < 8; ++i) {
+                if (column(first, i) < columns) e[i] = row[column(first, i)];
+                else from_f32(e[i], 0.f);
+            }
         }
     }
-    __device__ __forceinline__ static void store(T *row, uint32_t first, uint32_t columns, const float (&f)[8]) {
+    __device__ __forceinline__ void store(T *row, uint32_t first, uint32_t columns) const {
         if (VECTOR && first + 8 <= columns) {
-            uint4 *v = reinterpret_cast<uint4 *>(row + first);
-            if constexpr (sizeof(T) == 2) {
-                __stcs(v, Vec<T>::pack(f));
-            } else {
-                __stcs(v, Vec<T>::pack({f[0], f[1], f[2], f[3]}));
-                __stcs(v + 1, Vec<T>::pack({f[4], f[5], f[6], f[7]}));
-            }
+#pragma unroll
+            for (int w = 0; w < W; ++w) __stcs(reinterpret_cast<uint4 *>(row + first) + w, v[w]);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (column(first, i) < columns) from_f32(row[column(first, i)], f[i]);
+                if (column(first, i) < columns) row[column(first, i)] = e[i];
+        }
+    }
+    __device__ __forceinline__ void unpack(float2 (&f)[4]) const {
+        if constexpr (sizeof(T) == 2) {
+            f[0] = make_float2(bf16_lo(v[0].x), bf16_hi(v[0].x)), f[1] = make_float2(bf16_lo(v[0].y), bf16_hi(v[0].y));
+            f[2] = make_float2(bf16_lo(v[0].z), bf16_hi(v[0].z)), f[3] = make_float2(bf16_lo(v[0].w), bf16_hi(v[0].w));
+        } else {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                f[2 * w] = make_float2(__uint_as_float(v[w].x), __uint_as_float(v[w].y));
+                f[2 * w + 1] = make_float2(__uint_as_float(v[w].z), __uint_as_float(v[w].w));
+            }
+        }
+    }
+    __device__ __forceinline__ void pack(const float2 (&f)[4]) {
+        if constexpr (sizeof(T) == 2) {
+            v[0] = make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y), pack_bf16(f[2].x, f[2].y), pack_bf16(f[3].x, f[3].y));
+        } else {
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+                v[w] = make_uint4(__float_as_uint(f[2 * w].x), __float_as_uint(f[2 * w].y), __float_as_uint(f[2 * w + 1].x), __float_as_uint(f[2 * w + 1].y));
         }
     }
 };
 
-// Keeps the warp's (or its quads') values.  Every lane of the warp takes part; `there`: the lane's columns lie
-// within the row's runs.
+// Where a thread's columns lie.  VECTOR: the warp has eight runs in a row of all the rows' runs, so narrow rows
+// fill it too; otherwise eight runs of one row (`spans` of them to a row).
+struct Place {
+    uint64_t row;
+    uint32_t first, run;   // first column; its run in the row
+    bool there;            // the thread has columns within the row's runs
+};
 template <bool VECTOR>
-__device__ __forceinline__ void keep(const float (&f)[8], uint8_t *codes, uint8_t *scales, uint32_t first, uint32_t runs, bool there) {
+__device__ __forceinline__ Place place_of(const Args &a, uint64_t w, const Divisor &spans) {
+    const uint32_t lane = threadIdx.x & 31;
+    Place p;
     if (VECTOR) {
-        float m = 0.f;
+        const uint32_t r = (uint32_t)w * 8 + lane / 4;
+        p.there = r < a.all_runs;
+        const uint32_t row = a.runs.of(p.there ? r : a.all_runs - 1);   // (idle lanes look at the last run, and do nothing)
+        p.row = row;
+        p.run = (p.there ? r : a.all_runs - 1) - row * a.runs.d;
+        p.first = p.run * kRun + (lane & 3) * 8;
+    } else {
+        const uint32_t row = spans.of((uint32_t)w);
+        p.row = row;
+        p.run = ((uint32_t)w - row * spans.d) * 8;
+        p.first = p.run * kRun + lane;
+        p.there = p.first < a.runs.d * kRun;
+    }
+    return p;
+}
+
+// Keeps what the warp has.  Every lane takes part.
+template <bool VECTOR, int PARTS>
+__device__ __forceinline__ void keep(const Args &a, const float2 (&f)[PARTS][4], const Place &p) {
+    if (VECTOR) {
+        uint32_t bytes = 0;   // of gate and of up, 16 bits each
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));   // NaN passed over
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        float x[8];
+        for (int k = 0; k < PARTS; ++k) {
+            float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = f[i];
-        if (__any_sync(0xffffffffu, m >= kTooLarge)) {   // the largest finite one, NaN for the infinite
-            m = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (fabsf(f[i]) < INFINITY) m = fmaxf(m, fabsf(f[i]));
-                x[i] = holdable(f[i]);
-            }
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(f[k][i].x), fabsf(f[k][i].y)));   // NaN passed over
+            bytes |= scale_byte(m) << (16 * k);
         }
-        if (!there) return;
-        const uint32_t byte = scale_byte(__float_as_uint(m));
-        const float inv = inverse_scale(byte);
-        uint2 c;
-        c.x = to_codes(x[0] * inv, x[1] * inv) | to_codes(x[2] * inv, x[3] * inv) << 16;
-        c.y = to_codes(x[4] * inv, x[5] * inv) | to_codes(x[6] * inv, x[7] * inv) << 16;
-        *reinterpret_cast<uint2 *>(codes + first) = c;
-        if ((first & (kRun - 1)) == 0) scales[first / kRun] = (uint8_t)byte;
+        bytes = __vmaxu2(bytes, __shfl_xor_sync(0xffffffffu, bytes, 1));
+        bytes = __vmaxu2(bytes, __shfl_xor_sync(0xffffffffu, bytes, 2));
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+            uint32_t byte = bytes >> (16 * k) & 0xffffu;
+            float2 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = f[k][i];
+            if (__any_sync(0xffffffffu, byte >= kLargestByte)) {   // the largest finite one again
+                float m = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    m = fmaxf(m, fmaxf(fabsf(x[i].x) < INFINITY ? fabsf(x[i].x) : 0.f, fabsf(x[i].y) < INFINITY ? fabsf(x[i].y) : 0.f));
+                    x[i] = make_float2(holdable(x[i].x), holdable(x[i].y));
+                }
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                byte = scale_byte(fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2)));
+            }
+            const float2 inv = both(inverse_scale(byte));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], inv);
+            uint2 c;
+            c.x = to_codes(x[0].x, x[0].y) | to_codes(x[1].x, x[1].y) << 16;
+            c.y = to_codes(x[2].x, x[2].y) | to_codes(x[3].x, x[3].y) << 16;
+            if (p.there) {
+                const uint64_t at = (k * a.rows + p.row) * a.runs.d;
+                __stcs(reinterpret_cast<uint2 *>(a.codes + at * kRun + p.first), c);
+                if ((threadIdx.x & 3) == 0) a.scales[at + p.run] = (uint8_t)byte;
+            }
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool fine = fabsf(f[i]) < INFINITY;
-            const float m = warp_max(fine ? fabsf(f[i]) : 0.f);
-            const uint32_t byte = scale_byte(__float_as_uint(m));
-            const uint32_t run = first / kRun + i;
-            if (run < runs) {
-                codes[first + 32 * i] = (uint8_t)to_codes(holdable(f[i]) * inverse_scale(byte), 0.f);
-                if ((first & (kRun - 1)) == 0) scales[run] = (uint8_t)byte;
+        for (int k = 0; k < PARTS; ++k) {
+            const uint64_t at = (k * a.rows + p.row) * a.runs.d;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float x = i & 1 ? f[k][i / 2].y : f[k][i / 2].x;
+                const uint32_t byte = scale_byte(warp_max(fabsf(x) < INFINITY ? fabsf(x) : 0.f));
+                if (p.run + i < a.runs.d) {
+                    a.codes[at * kRun + p.first + 32 * i] = (uint8_t)to_codes(holdable(x) * inverse_scale(byte), 0.f);
+                    if ((threadIdx.x & 31) == 0) a.scales[at + p.run + i] = (uint8_t)byte;
+                }
             }
         }
     }
 }
 
+// What was kept, on its way: VECTOR: eight codes and their scale.
 template <bool VECTOR>
-__device__ __forceinline__ void read(const uint8_t *codes, const uint8_t *scales, uint32_t first, uint32_t runs, float (&f)[8]) {
-    if (VECTOR) {
-        const uint2 c = __ldcs(reinterpret_cast<const uint2 *>(codes + first));
-        const float s = scale_of(scales[first / kRun]);
-        const uint32_t two[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
+struct Kept {
+    uint2 c;
+    uint32_t byte;
+    uint8_t codes[VECTOR ? 1 : 8], bytes[VECTOR ? 1 : 8];
+    __device__ __forceinline__ void load(const Args &a, int k, const Place &p) {
+        const uint64_t at = (k * a.rows + p.row) * a.runs.d;
+        if (VECTOR) {
+            c = __ldcs(reinterpret_cast<const uint2 *>(a.codes + at * kRun + p.first));
+            byte = a.scales[at + p.run];
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = mul2(from_codes(two[i]), both(s));
-            f[2 * i] = v.x, f[2 * i + 1] = v.y;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t run = first / kRun + i;
-            f[i] = run < runs ? from_codes(codes[first + 32 * i]).x * scale_of(scales[run]) : 0.f;
+            for (int i = 0; i < 8; ++i) {
+                const bool there = p.run + i < a.runs.d;
+                codes[VECTOR ? 0 : i] = there ? a.codes[at * kRun + p.first + 32 * i] : (uint8_t)0;
+                bytes[VECTOR ? 0 : i] = there ? a.scales[at + p.run + i] : (uint8_t)0;
+            }
         }
     }
-}
+    __device__ __forceinline__ void unpack(float2 (&f)[4]) const {
+        if (VECTOR) {
+            const float2 s = both(scale_of(byte));
+            f[0] = mul2(from_codes(c.x & 0xffffu), s), f[1] = mul2(from_codes(c.x >> 16), s);
+            f[2] = mul2(from_codes(c.y & 0xffffu), s), f[3] = mul2(from_codes(c.y >> 16), s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int x = VECTOR ? 0 : 2 * i, y = VECTOR ? 0 : 2 * i + 1;
+                f[i] = mul2(from_codes(codes[x] | (uint32_t)codes[y] << 8), make_float2(scale_of(bytes[x]), scale_of(bytes[y])));
+            }
+        }
+    }
+};
 
 // ------------------------------------------------------------------ the kernels
 
-// A warp takes 256 columns of a row at a time.  PARTS: 1 or 2 of what is kept; ACT < 0: nothing but keeping or reading.
+// A warp walks over its 256 columns at a time, the next ones on their way while it works on these.
+template <bool VECTOR>
+__device__ __forceinline__ uint32_t steps_of(const Args &a, const Divisor &spans) {
+    return VECTOR ? (a.all_runs + 7) / 8 : (uint32_t)a.rows * spans.d;
+}
+
+// PARTS: 1 or 2 of what is kept; ACT < 0: nothing but keeping or reading.
 template <class T, bool VECTOR, int PARTS, int ACT, bool KEEP>
-__global__ void __launch_bounds__(kThreads) k_forward(const Args a) {
+__global__ void __launch_bounds__(kThreads) k_forward(const Args a, const Divisor spans) {
     using E = Eight<T, VECTOR>;
     pdl_enter();
-    const uint32_t lane = threadIdx.x & 31;
-    const uint32_t spans = (a.columns + 255) / 256;
-    const uint64_t n = a.rows * spans, step = (uint64_t)gridDim.x * (kThreads / 32);
-    for (uint64_t w = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; w < n; w += step) {
-        const uint64_t row = w / spans;
-        const uint32_t first = (uint32_t)(w - row * spans) * 256 + (VECTOR ? lane * 8 : lane);
-        float f[PARTS][8];
+    const uint32_t n = steps_of<VECTOR>(a, spans), step = gridDim.x * (kThreads / 32);
+    E next[PARTS];
+    Place p, q = {};
+    auto ask = [&](uint64_t w) {
+        q = place_of<VECTOR>(a, w, spans);
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) E::load(reinterpret_cast<const T *>(a.x[p].p) + row * a.x[p].stride, first, a.columns, f[p]);
-        if (ACT >= 0) {
-            float h[8], slope;
+        for (int k = 0; k < PARTS; ++k) next[k].load(reinterpret_cast<const T *>(a.x[k].p) + q.row * a.x[k].stride, q.there ? q.first : a.columns, a.columns);
+    };
+    uint64_t w = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    if (w < n) ask(w);
+    for (; w < n; w += step) {
+        float2 f[PARTS][4];
+        p = q;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+        for (int k = 0; k < PARTS; ++k) next[k].unpack(f[k]);
+        if (w + step < n) ask(w + step);
+        if (ACT >= 0 && p.there) {
+            float2 h[4], slope;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
                 h[i] = activate<ACT>(f[0][i], slope);
-                if (PARTS > 1) h[i] *= f[PARTS - 1][i];
+                if (PARTS > 1) h[i] = mul2(h[i], f[PARTS - 1][i]);
             }
-            E::store(reinterpret_cast<T *>(a.out[0]) + row * a.out_stride[0], first, a.columns, h);
+            E e;
+            e.pack(h);
+            e.store(reinterpret_cast<T *>(a.out[0]) + p.row * a.out_stride[0], p.first, a.columns);
         }
-        if (KEEP) {
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p) {
-                const uint64_t at = (p * a.rows + row) * a.runs;
-                keep<VECTOR>(f[p], a.codes + at * kRun, a.scales + at, first, a.runs, first < a.runs * kRun);
-            }
-        }
+        if (KEEP) keep<VECTOR, PARTS>(a, f, p);
     }
     pdl_leave();
 }
 
 template <class T, bool VECTOR, int PARTS, int ACT>
-__global__ void __launch_bounds__(kThreads) k_backward(const Args a) {
+__global__ void __launch_bounds__(kThreads, VECTOR ? 4 : 2) k_backward(const Args a, const Divisor spans) {
     using E = Eight<T, VECTOR>;
     pdl_enter();
-    const uint32_t lane = threadIdx.x & 31;
-    const uint32_t spans = (a.columns + 255) / 256;
-    const uint64_t n = a.rows * spans, step = (uint64_t)gridDim.x * (kThreads / 32);
-    for (uint64_t w = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; w < n; w += step) {
-        const uint64_t row = w / spans;
-        const uint32_t first = (uint32_t)(w - row * spans) * 256 + (VECTOR ? lane * 8 : lane);
-        if (first >= a.runs * kRun) continue;
-        float f[PARTS][8], dh[8];
-        if (ACT >= 0) E::load(reinterpret_cast<const T *>(a.x[0].p) + row * a.x[0].stride, first, a.columns, dh);
+    const uint32_t n = steps_of<VECTOR>(a, spans), step = gridDim.x * (kThreads / 32);
+    E next;
+    Kept<VECTOR> kept[PARTS];
+    Place p, q = {};
+    auto ask = [&](uint64_t w) {
+        q = place_of<VECTOR>(a, w, spans);
+        if (!q.there) return;
+        if (ACT >= 0) next.load(reinterpret_cast<const T *>(a.x[0].p) + q.row * a.x[0].stride, q.first, a.columns);
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) {
-            const uint64_t at = (p * a.rows + row) * a.runs;
-            read<VECTOR>(a.codes + at * kRun, a.scales + at, first, a.runs, f[p]);
+        for (int k = 0; k < PARTS; ++k) kept[k].load(a, k, q);
+    };
+    uint64_t w = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    if (w < n) ask(w);
+    for (; w < n; w += step) {
+        float2 f[PARTS][4], dh[4];
+        p = q;
+        if (p.there) {
+            if (ACT >= 0) next.unpack(dh);
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) kept[k].unpack(f[k]);
         }
-        auto put = [&](int i, const float (&v)[8]) { E::store(reinterpret_cast<T *>(a.out[i]) + row * a.out_stride[i], first, a.columns, v); };
+        if (w + step < n) ask(w + step);
+        if (!p.there) continue;
+        auto put = [&](int i, const float2 (&v)[4]) {
+            E e;
+            e.pack(v);
+            e.store(reinterpret_cast<T *>(a.out[i]) + p.row * a.out_stride[i], p.first, a.columns);
+        };
         if constexpr (ACT < 0) {
             put(0, f[0]);
         } else {
-            float dg[8], du[8], h[8];
+            float2 dg[4], du[4], h[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float slope;
-                const float act = activate<ACT>(f[0][i], slope);
-                dg[i] = dh[i] * slope;
-                h[i] = act;
+            for (int i = 0; i < 4; ++i) {
+                float2 slope;
+                h[i] = activate<ACT>(f[0][i], slope);
+                dg[i] = mul2(dh[i], slope);
                 if (PARTS > 1) {
-                    dg[i] *= f[PARTS - 1][i];
-                    du[i] = dh[i] * act;
-                    h[i] *= f[PARTS - 1][i];
+                    dg[i] = mul2(dg[i], f[PARTS - 1][i]);
+                    du[i] = mul2(dh[i], h[i]);
+                    h[i] = mul2(h[i], f[PARTS - 1][i]);
                 }
             }
             put(0, dg);
@@ -300,7 +416,7 @@ int check(uint64_t rows, uint32_t columns, int type, uint32_t parts, std::initia
         if (!span_bytes(rows, t.stride, columns, e, bytes)) return bad("the sizes overflow");
     }
     const uint64_t runs = (columns + kRun - 1) / kRun;
-    if (!span_bytes(rows, runs * kRun * parts, runs * kRun * parts, 1, bytes) || rows >= (1ull << 40)) return bad("the sizes overflow");
+    if (rows >= (1ull << 31) || rows * runs >= (1ull << 31)) return bad("the sizes overflow: rows times runs must be below 2^31");
     if (rows == 0) {
         skip = true;
         return BF16OPT_OK;
@@ -328,12 +444,18 @@ int check(uint64_t rows, uint32_t columns, int type, uint32_t parts, std::initia
     return BF16OPT_OK;
 }
 
-template <class K>
+template <bool VECTOR, class K>
 int start(K kernel, const Args &a, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "glu: no CUDA device");
-    const uint64_t warps = a.rows * ((a.columns + 255) / 256), ctas = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    const cudaError_t e = launch(Launch{(unsigned)std::min<uint64_t>(ctas, (uint64_t)sms * 8), kThreads, 0, stream, 0, true}, kernel, a);
+    const Divisor spans((a.columns + 255) / 256);
+    const uint64_t warps = VECTOR ? (a.all_runs + 7ull) / 8 : a.rows * spans.d, ctas = (warps + kThreads / 32 - 1) / (kThreads / 32);
+    Launch l{0, kThreads, 0, stream, 1, true};
+    int fit = 0;   // as many as the device holds at once: each walks on
+    cudaError_t e = clusters_that_fit(l, kernel, fit);
+    if (e != cudaSuccess) return fail_cuda(e, "glu occupancy");
+    l.grid = (unsigned)std::min<uint64_t>(ctas, fit);
+    e = launch(l, kernel, a, spans);
     return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "glu kernel launch");
 }
 
@@ -368,14 +490,14 @@ int pack(const bf16opt_pack_t *d, const void *x, uint64_t x_stride, uint8_t *cod
     if (rc != BF16OPT_OK || skip) return rc;
     if (!codes || !scales) return bad("a pointer is NULL");
     Args a = {};
-    a.rows = d->rows, a.columns = d->columns, a.runs = (d->columns + kRun - 1) / kRun;
+    a.rows = d->rows, a.columns = d->columns, a.runs = Divisor((d->columns + kRun - 1) / kRun), a.all_runs = (uint32_t)d->rows * a.runs.d;
     a.codes = codes, a.scales = scales;
     if (back) a.out[0] = const_cast<void *>(x), a.out_stride[0] = x_stride;
     else a.x[0] = {x, x_stride};
     return by_type(d->type, vectors(d->type, {t}), [&](auto zero, auto v) {
         using T = decltype(zero);
         constexpr bool V = decltype(v)::value;
-        return back ? start(k_backward<T, V, 1, -1>, a, (cudaStream_t)stream) : start(k_forward<T, V, 1, -1, true>, a, (cudaStream_t)stream);
+        return back ? start<V>(k_backward<T, V, 1, -1>, a, (cudaStream_t)stream) : start<V>(k_forward<T, V, 1, -1, true>, a, (cudaStream_t)stream);
     });
 }
 
@@ -397,7 +519,7 @@ int forward(const bf16opt_glu_t *d, Tensor gate, Tensor up, Tensor h, uint8_t *c
                   : check(d->rows, d->columns, d->type, 1, {gate, h}, codes, scales, codes != nullptr, skip);
     if (rc != BF16OPT_OK || skip) return rc;
     Args a = {};
-    a.rows = d->rows, a.columns = d->columns, a.runs = (d->columns + kRun - 1) / kRun;
+    a.rows = d->rows, a.columns = d->columns, a.runs = Divisor((d->columns + kRun - 1) / kRun), a.all_runs = (uint32_t)d->rows * a.runs.d;
     a.codes = codes, a.scales = scales;
     a.x[0] = {gate.p, gate.stride}, a.x[1] = {up.p, up.stride};
     a.out[0] = const_cast<void *>(h.p), a.out_stride[0] = h.stride;
@@ -407,7 +529,7 @@ int forward(const bf16opt_glu_t *d, Tensor gate, Tensor up, Tensor h, uint8_t *c
         constexpr bool V = decltype(v)::value;
         return by_act(d->act, d->gated, [&](auto act, auto parts) {
             constexpr int A = decltype(act)::value, P = decltype(parts)::value;
-            return codes ? start(k_forward<T, V, P, A, true>, a, (cudaStream_t)stream) : start(k_forward<T, V, P, A, false>, a, (cudaStream_t)stream);
+            return codes ? start<V>(k_forward<T, V, P, A, true>, a, (cudaStream_t)stream) : start<V>(k_forward<T, V, P, A, false>, a, (cudaStream_t)stream);
         });
     });
 }
@@ -424,7 +546,7 @@ int backward(const bf16opt_glu_t *d, Tensor dh, const uint8_t *codes, const uint
     if (rc != BF16OPT_OK || skip) return rc;
     if (!codes || !scales) return bad("a pointer is NULL");
     Args a = {};
-    a.rows = d->rows, a.columns = d->columns, a.runs = (d->columns + kRun - 1) / kRun;
+    a.rows = d->rows, a.columns = d->columns, a.runs = Divisor((d->columns + kRun - 1) / kRun), a.all_runs = (uint32_t)d->rows * a.runs.d;
     a.codes = const_cast<uint8_t *>(codes), a.scales = const_cast<uint8_t *>(scales);
     a.x[0] = {dh.p, dh.stride};
     const Tensor *outs[3] = {&dgate, &dup, &h};
@@ -437,7 +559,7 @@ int backward(const bf16opt_glu_t *d, Tensor dh, const uint8_t *codes, const uint
         using T = decltype(zero);
         constexpr bool V = decltype(v)::value;
         return by_act(d->act, d->gated, [&](auto act, auto parts) {
-            return start(k_backward<T, V, decltype(parts)::value, decltype(act)::value>, a, (cudaStream_t)stream);
+            return start<V>(k_backward<T, V, decltype(parts)::value, decltype(act)::value>, a, (cudaStream_t)stream);
         });
     });
 }

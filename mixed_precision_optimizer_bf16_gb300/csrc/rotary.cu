@@ -7,6 +7,8 @@
 //
 // The angle: position times frequency, both whole numbers (2^-64 turns), wraps around
 // at whole turns by itself; what is left, in (-1/2, 1/2] turns, goes to FP32.
+#include <type_traits>
+
 #include "ops_common.cuh"
 
 namespace bf16ops {
@@ -38,53 +40,52 @@ struct Args {
     uint64_t turns[BF16OPT_ROTARY_MAX_DIM / 2];   // 2^-64 turns per position
 };
 
-// N elements at p as floats, and back.  WIDE: as one access.
+// N elements as one access (WIDE) or as N.
 template <class T, int N, bool WIDE>
-__device__ __forceinline__ void load_n(const T *p, float (&f)[N]) {
-    if constexpr (WIDE && N * sizeof(T) == 16) {
-        Vec<T>::unpack(__ldcs(reinterpret_cast<const uint4 *>(p)), f);
-    } else if constexpr (WIDE && N * sizeof(T) == 8) {
-        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
-        if constexpr (sizeof(T) == 2) f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
-        else f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
-    } else if constexpr (WIDE && N * sizeof(T) == 4 && sizeof(T) == 2) {
-        const uint32_t v = __ldcs(reinterpret_cast<const unsigned int *>(p));
-        f[0] = bf16_lo(v), f[1] = bf16_hi(v);
-    } else {
+struct Piece {
+    T e[N];
+    __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = to_f32(p[i]);
+        for (int i = 0; i < N; ++i) e[i] = p[i];
     }
-}
-template <class T, int N, bool WIDE>
-__device__ __forceinline__ void store_n(T *p, const float (&f)[N]) {
-    if constexpr (WIDE && N * sizeof(T) == 16) {
-        __stcs(reinterpret_cast<uint4 *>(p), Vec<T>::pack(f));
-    } else if constexpr (WIDE && N * sizeof(T) == 8) {
-        uint2 v;
-        if constexpr (sizeof(T) == 2) v = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
-        else v = make_uint2(__float_as_uint(f[0]), __float_as_uint(f[1]));
-        __stcs(reinterpret_cast<uint2 *>(p), v);
-    } else if constexpr (WIDE && N * sizeof(T) == 4 && sizeof(T) == 2) {
-        __stcs(reinterpret_cast<unsigned int *>(p), pack_bf16(f[0], f[1]));
-    } else {
+    __device__ __forceinline__ void store(T *p) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i) from_f32(p[i], f[i]);
+        for (int i = 0; i < N; ++i) p[i] = e[i];
     }
-}
-
-template <class T, int N, bool WIDE>
-__device__ __forceinline__ void copy_n(T *to, const T *from) {
-    if constexpr (WIDE && N * sizeof(T) == 16) {
-        __stcs(reinterpret_cast<uint4 *>(to), __ldcs(reinterpret_cast<const uint4 *>(from)));
-    } else if constexpr (WIDE && N * sizeof(T) == 8) {
-        __stcs(reinterpret_cast<uint2 *>(to), __ldcs(reinterpret_cast<const uint2 *>(from)));
-    } else if constexpr (WIDE && N * sizeof(T) == 4 && sizeof(T) == 2) {
-        __stcs(reinterpret_cast<unsigned int *>(to), __ldcs(reinterpret_cast<const unsigned int *>(from)));
-    } else {
+    __device__ __forceinline__ void unpack(float (&f)[N]) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i) to[i] = from[i];
+        for (int i = 0; i < N; ++i) f[i] = to_f32(e[i]);
     }
-}
+    __device__ __forceinline__ void pack(const float (&f)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) from_f32(e[i], f[i]);
+    }
+};
+template <class T, int N>
+struct Piece<T, N, true> {
+    static constexpr int W = N * sizeof(T) / 4;
+    using Word = std::conditional_t<W == 4, uint4, std::conditional_t<W == 2, uint2, unsigned int>>;
+    union {
+        Word v;
+        uint32_t w[W];
+    };
+    __device__ __forceinline__ void load(const T *p) { v = __ldcs(reinterpret_cast<const Word *>(p)); }
+    __device__ __forceinline__ void store(T *p) const { __stcs(reinterpret_cast<Word *>(p), v); }
+    __device__ __forceinline__ void unpack(float (&f)[N]) const {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if constexpr (sizeof(T) == 2) f[2 * i] = bf16_lo(w[i]), f[2 * i + 1] = bf16_hi(w[i]);
+            else f[i] = __uint_as_float(w[i]);
+        }
+    }
+    __device__ __forceinline__ void pack(const float (&f)[N]) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if constexpr (sizeof(T) == 2) w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+            else w[i] = __float_as_uint(f[i]);
+        }
+    }
+};
 
 // (Spelt out, so that a result does not depend on the variant that computes it.)
 __device__ __forceinline__ void turned_pair(float a, float b, float c, float s, float &u, float &v) {
@@ -92,63 +93,89 @@ __device__ __forceinline__ void turned_pair(float a, float b, float c, float s, 
     v = fmaf(a, s, __fmul_rn(b, c));
 }
 
-// HALF: a thread turns N pairs (i, i + turned / 2); else N / 2 pairs of neighbours.
+// HALF: a thread turns N pairs (i, i + turned / 2); else N / 2 pairs of neighbours.  What is not turned is copied by threads
+// of its own, in the same walk.  A thread asks for kBatch heads' pieces before it uses the first.
 template <class T, int N, bool WIDE, bool HALF>
-__global__ void __launch_bounds__(kThreads) k_rotary(const Args a) {
+__global__ void __launch_bounds__(kThreads, N == 8 ? 3 : 4) k_rotary(const Args a) {
     constexpr int P = HALF ? N : N / 2;   // pairs of a thread
+    constexpr int V = HALF ? 2 : 1;       // pieces of a head
+    constexpr int kBatch = 4 / V;
+    __shared__ uint64_t turns[BF16OPT_ROTARY_MAX_DIM / 2];
+    for (uint32_t i = threadIdx.x; i < a.turned / 2; i += kThreads) turns[i] = a.turns[i];
+    __syncthreads();
     pdl_enter();
     const uint32_t per_token = a.units * a.lanes;
     const uint32_t slot = threadIdx.x / per_token, left = threadIdx.x - slot * per_token;
     const uint32_t lane = left / a.units, unit = left - lane * a.units;
     if (slot >= a.group) return;
     const bool turn = unit < a.turning;
-    const uint32_t at = turn ? unit * N : a.turned + (unit - a.turning) * N;   // the thread's first element
-    uint64_t turns[P];
+    const uint32_t copying = a.units - a.turning;
+    const uint32_t at = turn ? unit * N : a.turned + (unit - a.turning) * N;   // the thread's first piece
+    const uint32_t apart = turn ? a.turned / 2 : copying * N;                  // and from it to the second
+    uint32_t whole = 0;   // pieces that are there whole
 #pragma unroll
-    for (int i = 0; i < P; ++i) turns[i] = turn ? a.turns[unit * P + i] : 0;
+    for (int v = 0; v < V; ++v) whole += turn || at + v * apart + N <= a.dim;
+    const bool more = at + whole * apart < a.dim && !turn;
     for (uint64_t token = (uint64_t)blockIdx.x * a.group + slot; token < a.tokens; token += (uint64_t)gridDim.x * a.group) {
         const uint64_t b = a.tokens == a.seq ? 0 : token / a.seq, t = token - b * a.seq;
+        const T *q_in = reinterpret_cast<const T *>(a.q.in) + b * a.q.in_b + t * a.q.in_t + at;
+        const T *k_in = reinterpret_cast<const T *>(a.k.in) + b * a.k.in_b + t * a.k.in_t + at;
+        T *q_out = reinterpret_cast<T *>(a.q.out) + b * a.q.out_b + t * a.q.out_t + at;
+        T *k_out = reinterpret_cast<T *>(a.k.out) + b * a.k.out_b + t * a.k.out_t + at;
+        auto in_of = [&](uint32_t h) { return h < a.heads ? q_in + h * a.q.in_h : k_in + (h - a.heads) * a.k.in_h; };
+        auto out_of = [&](uint32_t h) { return h < a.heads ? q_out + h * a.q.out_h : k_out + (h - a.heads) * a.k.out_h; };
+        auto copied = [&](uint32_t h) { return !turn && (h < a.heads ? q_in == q_out : k_in == k_out); };   // in place: nothing to do
         float cs[P], sn[P];
-        if (turn) {
-            const int64_t pos = (a.positions ? load_index(a.positions, a.positions_type, b * a.positions_stride + t) : (int64_t)t);
+        bool first = true;
+        for (uint32_t head = lane; head < a.all_heads; head += a.lanes * kBatch) {
+            Piece<T, N, WIDE> x[kBatch][V];
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int32_t part = (int32_t)(((uint64_t)pos + (uint64_t)a.offset) * turns[i] >> 32);   // of a turn, in 2^-32
-                sincospif((float)part * 0x1p-31f, &sn[i], &cs[i]);
-                cs[i] *= a.scale;
-                sn[i] *= a.inverse ? -a.scale : a.scale;
-            }
-        }
-        for (uint32_t head = lane; head < a.all_heads; head += a.lanes) {
-            const bool is_q = head < a.heads;
-            const Place &pl = is_q ? a.q : a.k;
-            const uint32_t h = is_q ? head : head - a.heads;
-            const T *in = reinterpret_cast<const T *>(pl.in) + b * pl.in_b + t * pl.in_t + h * pl.in_h + at;
-            T *out = reinterpret_cast<T *>(pl.out) + b * pl.out_b + t * pl.out_t + h * pl.out_h + at;
-            if (turn) {
-                if constexpr (HALF) {
-                    const uint32_t half = a.turned / 2;
-                    float x[N], y[N], u[N], v[N];
-                    load_n<T, N, WIDE>(in, x);
-                    load_n<T, N, WIDE>(in + half, y);
+            for (int i = 0; i < kBatch; ++i) {
+                const uint32_t h = head + i * a.lanes;
+                if (h < a.all_heads && !copied(h)) {
 #pragma unroll
-                    for (int i = 0; i < N; ++i) turned_pair(x[i], y[i], cs[i], sn[i], u[i], v[i]);
-                    store_n<T, N, WIDE>(out, u);
-                    store_n<T, N, WIDE>(out + half, v);
-                } else {
-                    float x[N], u[N];
-                    load_n<T, N, WIDE>(in, x);
-#pragma unroll
-                    for (int i = 0; i < P; ++i) turned_pair(x[2 * i], x[2 * i + 1], cs[i], sn[i], u[2 * i], u[2 * i + 1]);
-                    store_n<T, N, WIDE>(out, u);
+                    for (int v = 0; v < V; ++v)
+                        if (v < whole) x[i][v].load(in_of(h) + v * apart);
                 }
-            } else if (in != out) {
-                for (uint32_t i = 0; at + i < a.dim; i += (a.units - a.turning) * N) {
-                    if (WIDE || at + i + N <= a.dim) {
-                        copy_n<T, N, WIDE>(out + i, in + i);
+            }
+            if (first && turn) {
+                const int64_t pos = a.positions ? load_index(a.positions, a.positions_type, b * a.positions_stride + t) : (int64_t)t;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const int32_t part = (int32_t)(((uint64_t)pos + (uint64_t)a.offset) * turns[unit * P + i] >> 32);   // of a turn, in 2^-32
+                    sincospif((float)part * 0x1p-31f, &sn[i], &cs[i]);
+                    cs[i] *= a.scale;
+                    sn[i] *= a.inverse ? -a.scale : a.scale;
+                }
+            }
+            first = false;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const uint32_t h = head + i * a.lanes;
+                if (h >= a.all_heads || copied(h)) continue;
+                if (turn) {
+                    if constexpr (HALF) {
+                        float f[N], g[N], u[N], w[N];
+                        x[i][0].unpack(f), x[i][1].unpack(g);
+#pragma unroll
+                        for (int k = 0; k < N; ++k) turned_pair(f[k], g[k], cs[k], sn[k], u[k], w[k]);
+                        x[i][0].pack(u), x[i][1].pack(w);
                     } else {
-                        for (uint32_t j = i; at + j < a.dim; ++j) out[j] = in[j];
+                        float f[N], u[N];
+                        x[i][0].unpack(f);
+#pragma unroll
+                        for (int k = 0; k < P; ++k) turned_pair(f[2 * k], f[2 * k + 1], cs[k], sn[k], u[2 * k], u[2 * k + 1]);
+                        x[i][0].pack(u);
                     }
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (v < whole) x[i][v].store(out_of(h) + v * apart);
+                if (more) {   // a last piece that is not whole, the rest of a long head
+                    const T *in = in_of(h);
+                    T *out = out_of(h);
+                    for (uint32_t k = whole * apart; at + k < a.dim; k += apart)
+                        for (uint32_t e = k; e < k + N && at + e < a.dim; ++e) out[e] = in[e];
                 }
             }
         }
@@ -223,7 +250,9 @@ int start(Args &a, cudaStream_t stream) {
     if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "rotary: no CUDA device");
     const uint32_t width = HALF ? 2 * N : N;   // elements that a thread turns
     a.turning = a.turned / width;
-    a.units = a.turning + std::min((a.dim - a.turned + N - 1) / N, (uint32_t)kThreads / 2);   // (at most half the threads turn)
+    // copying threads have two pieces too where the turning ones do (at most half the threads turn)
+    const uint32_t pieces = (a.dim - a.turned + N - 1) / N;
+    a.units = a.turning + std::min(HALF ? (pieces + 1) / 2 : pieces, (uint32_t)kThreads / 2);
     // heads side by side: a thread takes up to eight heads of a token (its sines serve them all), fewer while the SMs are not full
     uint32_t most = 8;
     while (most > 1 && a.tokens * ((a.all_heads + most - 1) / most) * a.units < (uint64_t)sms * 1024) most /= 2;
