@@ -21,32 +21,15 @@ struct Rows {
     uint64_t stride;   // elements
 };
 
-// n / d for every 32-bit n: the high word of n times m, m the first number that 2^(32 + shift) / d, less 2^32, does not
-// exceed (Granlund and Montgomery, PLDI 1994).
-struct Divisor {
-    uint32_t d, m, shift;
-    Divisor() = default;
-    explicit Divisor(uint32_t x) : d(x) {
-        uint32_t l = 0;
-        while ((1ull << l) < x) ++l;
-        m = (uint32_t)(((1ull << 32) * ((1ull << l) - x)) / x + 1);
-        shift = l;
-    }
-    __host__ __device__ __forceinline__ uint32_t of(uint32_t n) const {
-        const uint32_t t = (uint32_t)((uint64_t)n * m >> 32);
-        return shift ? (t + ((n - t) >> 1)) >> (shift - 1) : n;
-    }
-};
-
 struct Args {
     Rows x[2];         // forward: gate, up; backward: dh
     void *out[3];      // forward: h; backward: dgate, dup, h
     uint64_t out_stride[3];
     uint8_t *codes, *scales;
     uint64_t rows;
-    uint32_t columns;
-    Divisor runs;      // of a row
-    uint32_t all_runs; // rows times them, below 2^31
+    uint32_t columns, runs;   // of a row
+    // A CTA has `width` threads side by side along a row (of which there are `blocks` such pieces), `deep` rows at a time.
+    uint32_t width, blocks, deep;
 };
 
 // ------------------------------------------------------------------ a run's scale
@@ -84,32 +67,30 @@ __device__ __forceinline__ float2 from_codes(uint32_t two) {
 
 // ------------------------------------------------------------------ the activation
 
-__device__ __forceinline__ float clamped(float x, float most) {   // NaN stays
-    float r;
-    asm("{\n .reg .f32 t;\n min.NaN.f32 t, %1, %2;\n max.NaN.f32 %0, t, %3;\n}" : "=f"(r) : "f"(x), "f"(most), "f"(-most));
-    return r;
-}
 __device__ __forceinline__ float reciprocal(float x) {   // 0 above 2^126
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
-// act(g) = g s, s = sigmoid(y), y = g (silu) or 2 sqrt(2 / pi) (g + 0.044715 g^3) (gelu: (1 + tanh(y / 2)) / 2 = sigmoid(y));
-// act'(g) = s + g y' s (1 - s).  1 - s as a difference is off by 2^-24, which times g y' is about |y| 2^-24 of act'.  Beyond
-// +-64 gelu's sigmoid is 0 or 1, and g^3 is not formed.
+// act(g) = g s, s = sigmoid(y), y = g (silu) or g (a + b g^2), a = 2 sqrt(2 / pi), b = 0.044715 a (gelu: (1 + tanh(y / 2)) / 2 =
+// sigmoid(y)); act'(g) = s + g y' s (1 - s).  1 - s as a difference is off by 2^-24, which times g y' is about |y| 2^-24 of
+// act'.  From |g| = 64 on gelu's sigmoid is 0 or 1, and g^2 stops growing.  (NaN goes through g.)
 template <int ACT>
 __device__ __forceinline__ float2 activate(float2 g, float2 &slope) {
-    constexpr float kRoot = 1.59576912160573071f;   // 2 sqrt(2 / pi)
-    float2 y = g, p = g;
+    constexpr float kA = 1.59576912160573071f, kB = 0.044715f * kA;
+    float2 y = g, dy = both(1.f);
     if (ACT == BF16OPT_GLU_GELU) {
-        const float2 c = make_float2(clamped(g.x, 64.f), clamped(g.y, 64.f)), q = mul2(c, c), r = mul2(c, both(kRoot));
-        y = mul2(r, fma2(q, both(0.044715f), both(1.f)));
-        p = mul2(r, fma2(q, both(3.f * 0.044715f), both(1.f)));
+        float2 q = mul2(g, g);
+        q = make_float2(fminf(q.x, 4096.f), fminf(q.y, 4096.f));
+        y = mul2(g, fma2(q, both(kB), both(kA)));
+        dy = fma2(q, both(3.f * kB), both(kA));
     }
     const float2 x = mul2(y, both(-kLog2e)), t = add2(make_float2(ex2(x.x), ex2(x.y)), both(1.f));
     const float2 s = make_float2(reciprocal(t.x), reciprocal(t.y));
-    slope = fma2(p, mul2(s, fma2(s, both(-1.f), both(1.f))), s);
+    float2 w = mul2(s, fma2(s, both(-1.f), both(1.f)));
+    if (ACT == BF16OPT_GLU_GELU) w = mul2(w, dy);
+    slope = fma2(g, w, s);
     return mul2(g, s);
 }
 
@@ -171,37 +152,28 @@ struct Eight {
     }
 };
 
-// Where a thread's columns lie.  VECTOR: the warp has eight runs in a row of all the rows' runs, so narrow rows
-// fill it too; otherwise eight runs of one row (`spans` of them to a row).
+// A thread's columns, and the rows that it walks down: the CTA's first one, then every `step`-th.
 struct Place {
-    uint64_t row;
     uint32_t first, run;   // first column; its run in the row
     bool there;            // the thread has columns within the row's runs
+    uint32_t row, step;
 };
 template <bool VECTOR>
-__device__ __forceinline__ Place place_of(const Args &a, uint64_t w, const Divisor &spans) {
-    const uint32_t lane = threadIdx.x & 31;
+__device__ __forceinline__ Place place_of(const Args &a) {
+    const uint32_t group = blockIdx.x / a.blocks, block = blockIdx.x - group * a.blocks;
+    const uint32_t slot = threadIdx.x / a.width, i = block * a.width + (threadIdx.x - slot * a.width);
     Place p;
-    if (VECTOR) {
-        const uint32_t r = (uint32_t)w * 8 + lane / 4;
-        p.there = r < a.all_runs;
-        const uint32_t row = a.runs.of(p.there ? r : a.all_runs - 1);   // (idle lanes look at the last run, and do nothing)
-        p.row = row;
-        p.run = (p.there ? r : a.all_runs - 1) - row * a.runs.d;
-        p.first = p.run * kRun + (lane & 3) * 8;
-    } else {
-        const uint32_t row = spans.of((uint32_t)w);
-        p.row = row;
-        p.run = ((uint32_t)w - row * spans.d) * 8;
-        p.first = p.run * kRun + lane;
-        p.there = p.first < a.runs.d * kRun;
-    }
+    p.first = VECTOR ? i * 8 : i / 32 * 256 + i % 32;
+    p.run = p.first / kRun;
+    p.there = p.first < a.runs * kRun && slot < a.deep;
+    p.row = group * a.deep + slot;
+    p.step = gridDim.x / a.blocks * a.deep;
     return p;
 }
 
-// Keeps what the warp has.  Every lane takes part.
+// Keeps the thread's columns of one row.  Every lane of the warp takes part; `there`: it has any.
 template <bool VECTOR, int PARTS>
-__device__ __forceinline__ void keep(const Args &a, const float2 (&f)[PARTS][4], const Place &p) {
+__device__ __forceinline__ void keep(const Args &a, const float2 (&f)[PARTS][4], uint8_t *codes, uint8_t *scales, const Place &p, bool there) {
     if (VECTOR) {
         uint32_t bytes = 0;   // of gate and of up, 16 bits each
 #pragma unroll
@@ -235,23 +207,21 @@ __device__ __forceinline__ void keep(const Args &a, const float2 (&f)[PARTS][4],
             uint2 c;
             c.x = to_codes(x[0].x, x[0].y) | to_codes(x[1].x, x[1].y) << 16;
             c.y = to_codes(x[2].x, x[2].y) | to_codes(x[3].x, x[3].y) << 16;
-            if (p.there) {
-                const uint64_t at = (k * a.rows + p.row) * a.runs.d;
-                __stcs(reinterpret_cast<uint2 *>(a.codes + at * kRun + p.first), c);
-                if ((threadIdx.x & 3) == 0) a.scales[at + p.run] = (uint8_t)byte;
+            if (there) {
+                __stcs(reinterpret_cast<uint2 *>(codes + k * a.rows * a.runs * kRun), c);
+                if ((p.first & (kRun - 1)) == 0) scales[k * a.rows * a.runs] = (uint8_t)byte;
             }
         }
     } else {
 #pragma unroll
         for (int k = 0; k < PARTS; ++k) {
-            const uint64_t at = (k * a.rows + p.row) * a.runs.d;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float x = i & 1 ? f[k][i / 2].y : f[k][i / 2].x;
                 const uint32_t byte = scale_byte(warp_max(fabsf(x) < INFINITY ? fabsf(x) : 0.f));
-                if (p.run + i < a.runs.d) {
-                    a.codes[at * kRun + p.first + 32 * i] = (uint8_t)to_codes(holdable(x) * inverse_scale(byte), 0.f);
-                    if ((threadIdx.x & 31) == 0) a.scales[at + p.run + i] = (uint8_t)byte;
+                if (there && p.run + i < a.runs) {
+                    codes[k * a.rows * a.runs * kRun + 32 * i] = (uint8_t)to_codes(holdable(x) * inverse_scale(byte), 0.f);
+                    if ((threadIdx.x & 31) == 0) scales[k * a.rows * a.runs + i] = (uint8_t)byte;
                 }
             }
         }
@@ -264,17 +234,15 @@ struct Kept {
     uint2 c;
     uint32_t byte;
     uint8_t codes[VECTOR ? 1 : 8], bytes[VECTOR ? 1 : 8];
-    __device__ __forceinline__ void load(const Args &a, int k, const Place &p) {
-        const uint64_t at = (k * a.rows + p.row) * a.runs.d;
+    __device__ __forceinline__ void load(const uint8_t *from, const uint8_t *scale, uint32_t run, uint32_t runs) {
         if (VECTOR) {
-            c = __ldcs(reinterpret_cast<const uint2 *>(a.codes + at * kRun + p.first));
-            byte = a.scales[at + p.run];
+            c = __ldcs(reinterpret_cast<const uint2 *>(from));
+            byte = *scale;
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const bool there = p.run + i < a.runs.d;
-                codes[VECTOR ? 0 : i] = there ? a.codes[at * kRun + p.first + 32 * i] : (uint8_t)0;
-                bytes[VECTOR ? 0 : i] = there ? a.scales[at + p.run + i] : (uint8_t)0;
+                codes[VECTOR ? 0 : i] = run + i < runs ? from[32 * i] : (uint8_t)0;
+                bytes[VECTOR ? 0 : i] = run + i < runs ? scale[i] : (uint8_t)0;
             }
         }
     }
@@ -295,99 +263,131 @@ struct Kept {
 
 // ------------------------------------------------------------------ the kernels
 
-// A warp walks over its 256 columns at a time, the next ones on their way while it works on these.
-template <bool VECTOR>
-__device__ __forceinline__ uint32_t steps_of(const Args &a, const Divisor &spans) {
-    return VECTOR ? (a.all_runs + 7) / 8 : (uint32_t)a.rows * spans.d;
-}
+// A thread has its columns and walks down the rows with them, `U` rows at a time, the next ones on their way while it
+// works on these: addresses only go on by a stride.  U: so many that 32 bytes or so of each thread are on their way.
 
 // PARTS: 1 or 2 of what is kept; ACT < 0: nothing but keeping or reading.
 template <class T, bool VECTOR, int PARTS, int ACT, bool KEEP>
-__global__ void __launch_bounds__(kThreads) k_forward(const Args a, const Divisor spans) {
+__global__ void __launch_bounds__(kThreads) k_forward(const Args a) {
+    constexpr int U = sizeof(T) == 2 && PARTS == 1 && VECTOR ? 2 : 1;
     using E = Eight<T, VECTOR>;
     pdl_enter();
-    const uint32_t n = steps_of<VECTOR>(a, spans), step = gridDim.x * (kThreads / 32);
-    E next[PARTS];
-    Place p, q = {};
-    auto ask = [&](uint64_t w) {
-        q = place_of<VECTOR>(a, w, spans);
+    const Place p = place_of<VECTOR>(a);
+    const T *x[PARTS];
 #pragma unroll
-        for (int k = 0; k < PARTS; ++k) next[k].load(reinterpret_cast<const T *>(a.x[k].p) + q.row * a.x[k].stride, q.there ? q.first : a.columns, a.columns);
-    };
-    uint64_t w = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-    if (w < n) ask(w);
-    for (; w < n; w += step) {
-        float2 f[PARTS][4];
-        p = q;
+    for (int k = 0; k < PARTS; ++k) x[k] = reinterpret_cast<const T *>(a.x[k].p) + p.row * a.x[k].stride;
+    T *h = reinterpret_cast<T *>(a.out[0]) + p.row * a.out_stride[0];
+    uint8_t *codes = a.codes + (uint64_t)p.row * a.runs * kRun + p.first, *scales = a.scales + (uint64_t)p.row * a.runs + p.run;
+    E next[U][PARTS];
+    auto ask = [&](uint32_t row) {
 #pragma unroll
-        for (int k = 0; k < PARTS; ++k) next[k].unpack(f[k]);
-        if (w + step < n) ask(w + step);
-        if (ACT >= 0 && p.there) {
-            float2 h[4], slope;
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                h[i] = activate<ACT>(f[0][i], slope);
-                if (PARTS > 1) h[i] = mul2(h[i], f[PARTS - 1][i]);
+            for (int k = 0; k < PARTS; ++k) {
+                next[u][k].load(x[k], p.there && row + u * p.step < a.rows ? p.first : a.columns, a.columns);
+                x[k] += p.step * a.x[k].stride;
             }
-            E e;
-            e.pack(h);
-            e.store(reinterpret_cast<T *>(a.out[0]) + p.row * a.out_stride[0], p.first, a.columns);
         }
-        if (KEEP) keep<VECTOR, PARTS>(a, f, p);
+    };
+    ask(p.row);
+    // (the same number of turns for the whole CTA: its lanes look at one another's columns)
+    for (uint32_t row = p.row, top = p.row - threadIdx.x / a.width; top < a.rows; row += U * p.step, top += U * p.step) {
+        float2 f[U][PARTS][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) next[u][k].unpack(f[u][k]);
+        ask(row + U * p.step);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool there = p.there && row + u * p.step < a.rows;
+            if (ACT >= 0) {
+                float2 v[4], slope;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = activate<ACT>(f[u][0][i], slope);
+                    if (PARTS > 1) v[i] = mul2(v[i], f[u][PARTS - 1][i]);
+                }
+                E e;
+                e.pack(v);
+                if (there) e.store(h, p.first, a.columns);
+                h += p.step * a.out_stride[0];
+            }
+            if (KEEP) {
+                keep<VECTOR, PARTS>(a, f[u], codes, scales, p, there);
+                codes += (uint64_t)p.step * a.runs * kRun, scales += (uint64_t)p.step * a.runs;
+            }
+        }
     }
     pdl_leave();
 }
 
 template <class T, bool VECTOR, int PARTS, int ACT>
-__global__ void __launch_bounds__(kThreads, VECTOR ? 4 : 2) k_backward(const Args a, const Divisor spans) {
+__global__ void __launch_bounds__(kThreads, VECTOR ? 4 : 2) k_backward(const Args a) {
+    constexpr int U = ACT < 0 && VECTOR ? 4 : 1;
     using E = Eight<T, VECTOR>;
     pdl_enter();
-    const uint32_t n = steps_of<VECTOR>(a, spans), step = gridDim.x * (kThreads / 32);
+    const Place p = place_of<VECTOR>(a);
+    if (!p.there) return;
+    const T *x = reinterpret_cast<const T *>(a.x[0].p) + p.row * a.x[0].stride;
+    const uint8_t *codes = a.codes + (uint64_t)p.row * a.runs * kRun + p.first, *scales = a.scales + (uint64_t)p.row * a.runs + p.run;
+    constexpr int kOuts = ACT < 0 ? 1 : 3;
+    T *out[kOuts];
+#pragma unroll
+    for (int i = 0; i < kOuts; ++i) out[i] = reinterpret_cast<T *>(a.out[i]) + p.row * a.out_stride[i];
     E next;
-    Kept<VECTOR> kept[PARTS];
-    Place p, q = {};
-    auto ask = [&](uint64_t w) {
-        q = place_of<VECTOR>(a, w, spans);
-        if (!q.there) return;
-        if (ACT >= 0) next.load(reinterpret_cast<const T *>(a.x[0].p) + q.row * a.x[0].stride, q.first, a.columns);
+    Kept<VECTOR> kept[U][PARTS];
+    auto ask = [&](uint32_t row) {
 #pragma unroll
-        for (int k = 0; k < PARTS; ++k) kept[k].load(a, k, q);
-    };
-    uint64_t w = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-    if (w < n) ask(w);
-    for (; w < n; w += step) {
-        float2 f[PARTS][4], dh[4];
-        p = q;
-        if (p.there) {
-            if (ACT >= 0) next.unpack(dh);
+        for (int u = 0; u < U; ++u) {
+            if (row + u * p.step < a.rows) {
+                if (ACT >= 0) next.load(x, p.first, a.columns);
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k) kept[k].unpack(f[k]);
+                for (int k = 0; k < PARTS; ++k)
+                    kept[u][k].load(codes + k * a.rows * a.runs * kRun, scales + k * a.rows * a.runs, p.run, a.runs);
+            }
+            if (ACT >= 0) x += p.step * a.x[0].stride;
+            codes += (uint64_t)p.step * a.runs * kRun, scales += (uint64_t)p.step * a.runs;
         }
-        if (w + step < n) ask(w + step);
-        if (!p.there) continue;
+    };
+    ask(p.row);
+    for (uint32_t row = p.row; row < a.rows; row += U * p.step) {
+        float2 f[U][PARTS][4], dh[4];
+        if (ACT >= 0) next.unpack(dh);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) kept[u][k].unpack(f[u][k]);
+        ask(row + U * p.step);
         auto put = [&](int i, const float2 (&v)[4]) {
             E e;
             e.pack(v);
-            e.store(reinterpret_cast<T *>(a.out[i]) + p.row * a.out_stride[i], p.first, a.columns);
+            e.store(out[i], p.first, a.columns);
         };
         if constexpr (ACT < 0) {
-            put(0, f[0]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (row + u * p.step < a.rows) put(0, f[u][0]);
+                out[0] += p.step * a.out_stride[0];
+            }
         } else {
             float2 dg[4], du[4], h[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float2 slope;
-                h[i] = activate<ACT>(f[0][i], slope);
+                h[i] = activate<ACT>(f[0][0][i], slope);
                 dg[i] = mul2(dh[i], slope);
                 if (PARTS > 1) {
-                    dg[i] = mul2(dg[i], f[PARTS - 1][i]);
+                    dg[i] = mul2(dg[i], f[0][PARTS - 1][i]);
                     du[i] = mul2(dh[i], h[i]);
-                    h[i] = mul2(h[i], f[PARTS - 1][i]);
+                    h[i] = mul2(h[i], f[0][PARTS - 1][i]);
                 }
             }
             put(0, dg);
             if (PARTS > 1) put(1, du);
             if (a.out[2]) put(2, h);
+#pragma unroll
+            for (int i = 0; i < kOuts; ++i) out[i] += p.step * a.out_stride[i];
         }
     }
     pdl_leave();
@@ -416,7 +416,7 @@ int check(uint64_t rows, uint32_t columns, int type, uint32_t parts, std::initia
         if (!span_bytes(rows, t.stride, columns, e, bytes)) return bad("the sizes overflow");
     }
     const uint64_t runs = (columns + kRun - 1) / kRun;
-    if (rows >= (1ull << 31) || rows * runs >= (1ull << 31)) return bad("the sizes overflow: rows times runs must be below 2^31");
+    if (rows >= (1ull << 31) || !span_bytes(rows, runs * kRun * parts, runs * kRun * parts, 1, bytes)) return bad("the sizes overflow");
     if (rows == 0) {
         skip = true;
         return BF16OPT_OK;
@@ -445,17 +445,21 @@ int check(uint64_t rows, uint32_t columns, int type, uint32_t parts, std::initia
 }
 
 template <bool VECTOR, class K>
-int start(K kernel, const Args &a, cudaStream_t stream) {
-    const int sms = sm_count();
-    if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "glu: no CUDA device");
-    const Divisor spans((a.columns + 255) / 256);
-    const uint64_t warps = VECTOR ? (a.all_runs + 7ull) / 8 : a.rows * spans.d, ctas = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    Launch l{0, kThreads, 0, stream, 1, true};
+int start(K kernel, Args a, cudaStream_t stream) {
+    if (sm_count() < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "glu: no CUDA device");
+    // threads along a row (whole runs, whole warps where a run is a warp's), in pieces of up to a CTA's
+    const uint32_t quantum = VECTOR ? 4 : 32;
+    const uint32_t along = VECTOR ? a.runs * 4 : (a.columns + 255) / 256 * 32;
+    a.blocks = (along + kThreads - 1) / kThreads;
+    a.width = (along / quantum + a.blocks - 1) / a.blocks * quantum;
+    a.deep = (uint32_t)std::min<uint64_t>(kThreads / a.width, a.rows);
+    Launch l{0, (a.width * a.deep + 31) / 32 * 32, 0, stream, 1, true};
     int fit = 0;   // as many as the device holds at once: each walks on
     cudaError_t e = clusters_that_fit(l, kernel, fit);
     if (e != cudaSuccess) return fail_cuda(e, "glu occupancy");
-    l.grid = (unsigned)std::min<uint64_t>(ctas, fit);
-    e = launch(l, kernel, a, spans);
+    const uint64_t groups = (a.rows + a.deep - 1) / a.deep;
+    l.grid = (unsigned)std::min<uint64_t>(groups, std::max(1u, fit / a.blocks)) * a.blocks;
+    e = launch(l, kernel, a);
     return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "glu kernel launch");
 }
 
@@ -490,7 +494,7 @@ int pack(const bf16opt_pack_t *d, const void *x, uint64_t x_stride, uint8_t *cod
     if (rc != BF16OPT_OK || skip) return rc;
     if (!codes || !scales) return bad("a pointer is NULL");
     Args a = {};
-    a.rows = d->rows, a.columns = d->columns, a.runs = Divisor((d->columns + kRun - 1) / kRun), a.all_runs = (uint32_t)d->rows * a.runs.d;
+    a.rows = d->rows, a.columns = d->columns, a.runs = (d->columns + kRun - 1) / kRun;
     a.codes = codes, a.scales = scales;
     if (back) a.out[0] = const_cast<void *>(x), a.out_stride[0] = x_stride;
     else a.x[0] = {x, x_stride};
@@ -519,7 +523,7 @@ int forward(const bf16opt_glu_t *d, Tensor gate, Tensor up, Tensor h, uint8_t *c
                   : check(d->rows, d->columns, d->type, 1, {gate, h}, codes, scales, codes != nullptr, skip);
     if (rc != BF16OPT_OK || skip) return rc;
     Args a = {};
-    a.rows = d->rows, a.columns = d->columns, a.runs = Divisor((d->columns + kRun - 1) / kRun), a.all_runs = (uint32_t)d->rows * a.runs.d;
+    a.rows = d->rows, a.columns = d->columns, a.runs = (d->columns + kRun - 1) / kRun;
     a.codes = codes, a.scales = scales;
     a.x[0] = {gate.p, gate.stride}, a.x[1] = {up.p, up.stride};
     a.out[0] = const_cast<void *>(h.p), a.out_stride[0] = h.stride;
@@ -546,7 +550,7 @@ int backward(const bf16opt_glu_t *d, Tensor dh, const uint8_t *codes, const uint
     if (rc != BF16OPT_OK || skip) return rc;
     if (!codes || !scales) return bad("a pointer is NULL");
     Args a = {};
-    a.rows = d->rows, a.columns = d->columns, a.runs = Divisor((d->columns + kRun - 1) / kRun), a.all_runs = (uint32_t)d->rows * a.runs.d;
+    a.rows = d->rows, a.columns = d->columns, a.runs = (d->columns + kRun - 1) / kRun;
     a.codes = const_cast<uint8_t *>(codes), a.scales = const_cast<uint8_t *>(scales);
     a.x[0] = {dh.p, dh.stride};
     const Tensor *outs[3] = {&dgate, &dup, &h};
