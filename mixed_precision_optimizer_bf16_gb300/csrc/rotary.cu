@@ -15,26 +15,31 @@ namespace bf16ops {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kResident = 4;   // CTAs of an SM: 64 registers
+// Heads whose pieces a thread asks for at a time: 64 bytes, at most eight pieces.
+template <class T, int N, bool HALF>
+constexpr int kBatchOf = std::max(1, std::min(8, 64 / (int)(N * sizeof(T))) / (HALF ? 2 : 1));
 
-struct Place {
+// One of q and k, and how a CTA takes it.
+struct Part {
     const void *in;
     void *out;
     uint64_t in_b, in_t, in_h, out_b, out_t, out_h;   // elements between batches, tokens, heads
+    uint32_t heads;
+    uint32_t lanes;             // heads side by side in a CTA
+    uint32_t group;             // tokens side by side in a CTA
 };
 
 struct Args {
-    Place q, k;
+    Part part[2];
     uint64_t tokens, seq;       // tokens: batch * seq
     const void *positions;
     uint64_t positions_stride;
     int64_t offset;
     int positions_type;
-    uint32_t heads, all_heads;  // of q; of q and k
     uint32_t dim, turned;
     uint32_t units;             // threads of a head: the ones that turn, then the ones that copy
     uint32_t turning;           // of them turning
-    uint32_t lanes;             // heads side by side in a CTA
-    uint32_t group;             // tokens side by side in a CTA
     float scale;
     uint32_t inverse;
     uint64_t turns[BF16OPT_ROTARY_MAX_DIM / 2];   // 2^-64 turns per position
@@ -87,98 +92,130 @@ struct Piece<T, N, true> {
     }
 };
 
-// (Spelt out, so that a result does not depend on the variant that computes it.)
+// Each product and sum spelt out, so that a result does not depend on the variant that computes it.
 __device__ __forceinline__ void turned_pair(float a, float b, float c, float s, float &u, float &v) {
     u = fmaf(-b, s, __fmul_rn(a, c));
     v = fmaf(a, s, __fmul_rn(b, c));
 }
 
+__device__ __forceinline__ uint64_t position_of(const Args &a, uint64_t token) {
+    const uint64_t b = a.tokens == a.seq ? 0 : token / a.seq, t = token - b * a.seq;
+    return (a.positions ? (uint64_t)load_index(a.positions, a.positions_type, b * a.positions_stride + t) : t) + (uint64_t)a.offset;
+}
+
 // HALF: a thread turns N pairs (i, i + turned / 2); else N / 2 pairs of neighbours.  What is not turned is copied by threads
-// of its own, in the same walk.  A thread asks for kBatch heads' pieces before it uses the first.
+// of its own, in the same walk.  A CTA has `group` tokens at a time, of q and then of k: its threads ask for their pieces of
+// kBatch heads, then take the tokens' sines and cosines, together, into shared memory (the positions were asked for a
+// group before), and then use both.
 template <class T, int N, bool WIDE, bool HALF>
-__global__ void __launch_bounds__(kThreads, N == 8 ? 3 : 4) k_rotary(const Args a) {
-    constexpr int P = HALF ? N : N / 2;   // pairs of a thread
-    constexpr int V = HALF ? 2 : 1;       // pieces of a head
-    constexpr int kBatch = 4 / V;
-    __shared__ uint64_t turns[BF16OPT_ROTARY_MAX_DIM / 2];
-    for (uint32_t i = threadIdx.x; i < a.turned / 2; i += kThreads) turns[i] = a.turns[i];
-    __syncthreads();
+__global__ void __launch_bounds__(kThreads, kResident) k_rotary(const Args a) {
+    constexpr int P = HALF ? N : N / 2;       // pairs of a thread
+    constexpr int V = HALF ? 2 : 1;           // pieces of a head
+    constexpr int kBatch = kBatchOf<T, N, HALF>;
+    constexpr uint32_t kTable = kThreads * P; // pairs of a CTA's tokens, at most
+    __shared__ __align__(16) float cosines[kTable], sines[kTable];
+    __shared__ uint64_t positions[kThreads];
+    const uint32_t pairs = a.turned / 2, side = kThreads / pairs;   // tokens whose sines are taken side by side
+    const uint32_t pair = threadIdx.x % pairs, by = threadIdx.x / pairs;
+    const uint64_t turns = a.turns[pair];
     pdl_enter();
-    const uint32_t per_token = a.units * a.lanes;
-    const uint32_t slot = threadIdx.x / per_token, left = threadIdx.x - slot * per_token;
-    const uint32_t lane = left / a.units, unit = left - lane * a.units;
-    if (slot >= a.group) return;
-    const bool turn = unit < a.turning;
-    const uint32_t copying = a.units - a.turning;
-    const uint32_t at = turn ? unit * N : a.turned + (unit - a.turning) * N;   // the thread's first piece
-    const uint32_t apart = turn ? a.turned / 2 : copying * N;                  // and from it to the second
-    uint32_t whole = 0;   // pieces that are there whole
+    uint64_t begun = 0;   // groups of the parts before
+    for (int k = 0; k < 2; ++k) {
+        const Part &pt = a.part[k];
+        if (pt.heads == 0) continue;
+        const uint32_t lanes = pt.lanes, group = pt.group;
+        const uint64_t groups = (a.tokens + group - 1) / group;
+        // the turning threads of a token first, then the copying ones: most warps do one or the other
+        const uint32_t per_token = a.units * lanes, copying = a.units - a.turning;
+        const uint32_t slot = threadIdx.x / per_token, left = threadIdx.x - slot * per_token;
+        const bool turn = left < a.turning * lanes;
+        const uint32_t rest = turn ? left : left - a.turning * lanes, each = turn ? a.turning : copying;
+        const uint32_t lane = rest / each, unit = rest - lane * each;
+        const uint32_t at = turn ? unit * N : a.turned + unit * N;      // the thread's first piece
+        const uint32_t apart = turn ? a.turned / 2 : copying * N;       // and from it to the second
+        uint32_t whole = 0;   // pieces that are there whole
 #pragma unroll
-    for (int v = 0; v < V; ++v) whole += turn || at + v * apart + N <= a.dim;
-    const bool more = at + whole * apart < a.dim && !turn;
-    for (uint64_t token = (uint64_t)blockIdx.x * a.group + slot; token < a.tokens; token += (uint64_t)gridDim.x * a.group) {
-        const uint64_t b = a.tokens == a.seq ? 0 : token / a.seq, t = token - b * a.seq;
-        const T *q_in = reinterpret_cast<const T *>(a.q.in) + b * a.q.in_b + t * a.q.in_t + at;
-        const T *k_in = reinterpret_cast<const T *>(a.k.in) + b * a.k.in_b + t * a.k.in_t + at;
-        T *q_out = reinterpret_cast<T *>(a.q.out) + b * a.q.out_b + t * a.q.out_t + at;
-        T *k_out = reinterpret_cast<T *>(a.k.out) + b * a.k.out_b + t * a.k.out_t + at;
-        auto in_of = [&](uint32_t h) { return h < a.heads ? q_in + h * a.q.in_h : k_in + (h - a.heads) * a.k.in_h; };
-        auto out_of = [&](uint32_t h) { return h < a.heads ? q_out + h * a.q.out_h : k_out + (h - a.heads) * a.k.out_h; };
-        auto copied = [&](uint32_t h) { return !turn && (h < a.heads ? q_in == q_out : k_in == k_out); };   // in place: nothing to do
-        float cs[P], sn[P];
-        bool first = true;
-        for (uint32_t head = lane; head < a.all_heads; head += a.lanes * kBatch) {
+        for (int v = 0; v < V; ++v) whole += turn || at + v * apart + N <= a.dim;
+        const bool more = at + whole * apart < a.dim && !turn;
+        const uint64_t in_step = lanes * pt.in_h, out_step = lanes * pt.out_h;
+        // the groups go round the CTAs, on from where those of the part before ended
+        uint64_t g = (blockIdx.x + gridDim.x - begun % gridDim.x) % gridDim.x;
+        begun += groups;
+        auto ask_position = [&](uint64_t g) {
+            const uint64_t token = g * group + threadIdx.x;
+            return threadIdx.x < group && token < a.tokens ? position_of(a, token) : 0;
+        };
+        uint64_t position = ask_position(g);
+        for (; g < groups; g += gridDim.x) {
+            const uint64_t token = g * group + slot, b = a.tokens == a.seq ? 0 : token / a.seq, t = token - b * a.seq;
+            const T *in = reinterpret_cast<const T *>(pt.in) + (b * pt.in_b + t * pt.in_t + lane * pt.in_h + at);
+            T *out = reinterpret_cast<T *>(pt.out) + (b * pt.out_b + t * pt.out_t + lane * pt.out_h + at);
+            // this thread's heads; none where there is nothing to copy (in place)
+            const uint32_t heads = slot < group && token < a.tokens && (turn || in != out) ? pt.heads : 0;
             Piece<T, N, WIDE> x[kBatch][V];
+            auto ask = [&](uint32_t head) {
+                const T *from = in;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const uint32_t h = head + i * a.lanes;
-                if (h < a.all_heads && !copied(h)) {
+                for (int i = 0; i < kBatch; ++i) {
+                    if (head + i * lanes < heads) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        if (v < whole) x[i][v].load(in_of(h) + v * apart);
-                }
-            }
-            if (first && turn) {
-                const int64_t pos = a.positions ? load_index(a.positions, a.positions_type, b * a.positions_stride + t) : (int64_t)t;
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const int32_t part = (int32_t)(((uint64_t)pos + (uint64_t)a.offset) * turns[unit * P + i] >> 32);   // of a turn, in 2^-32
-                    sincospif((float)part * 0x1p-31f, &sn[i], &cs[i]);
-                    cs[i] *= a.scale;
-                    sn[i] *= a.inverse ? -a.scale : a.scale;
-                }
-            }
-            first = false;
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const uint32_t h = head + i * a.lanes;
-                if (h >= a.all_heads || copied(h)) continue;
-                if (turn) {
-                    if constexpr (HALF) {
-                        float f[N], g[N], u[N], w[N];
-                        x[i][0].unpack(f), x[i][1].unpack(g);
-#pragma unroll
-                        for (int k = 0; k < N; ++k) turned_pair(f[k], g[k], cs[k], sn[k], u[k], w[k]);
-                        x[i][0].pack(u), x[i][1].pack(w);
-                    } else {
-                        float f[N], u[N];
-                        x[i][0].unpack(f);
-#pragma unroll
-                        for (int k = 0; k < P; ++k) turned_pair(f[2 * k], f[2 * k + 1], cs[k], sn[k], u[2 * k], u[2 * k + 1]);
-                        x[i][0].pack(u);
+                        for (int v = 0; v < V; ++v)
+                            if (v < whole) x[i][v].load(from + v * apart);
                     }
+                    from += in_step;
+                }
+            };
+            ask(lane);
+            if (threadIdx.x < group) positions[threadIdx.x] = position;
+            __syncthreads();   // (the last group's sines are used, too)
+            position = ask_position(g + gridDim.x);
+            if (by < side)
+                for (uint32_t i = by; i < group; i += side) {
+                    const int32_t part = (int32_t)(positions[i] * turns >> 32);   // of a turn, in 2^-32
+                    float sine, cosine;
+                    sincospif((float)part * 0x1p-31f, &sine, &cosine);
+                    cosines[i * pairs + pair] = cosine * a.scale;
+                    sines[i * pairs + pair] = sine * (a.inverse ? -a.scale : a.scale);
+                }
+            __syncthreads();
+            for (uint32_t head = lane; head < heads; head += lanes * kBatch) {
+                float c[P], s[P];
+                if (turn) {
+                    const uint32_t from = slot * pairs + unit * P;
+#pragma unroll
+                    for (int k = 0; k < P; ++k) c[k] = cosines[from + k], s[k] = sines[from + k];
                 }
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (v < whole) x[i][v].store(out_of(h) + v * apart);
-                if (more) {   // a last piece that is not whole, the rest of a long head
-                    const T *in = in_of(h);
-                    T *out = out_of(h);
-                    for (uint32_t k = whole * apart; at + k < a.dim; k += apart)
-                        for (uint32_t e = k; e < k + N && at + e < a.dim; ++e) out[e] = in[e];
+                for (int i = 0; i < kBatch; ++i) {
+                    if (head + i * lanes < heads) {
+                        if (turn) {
+                            if constexpr (HALF) {
+                                float f[N], g[N], u[N], w[N];
+                                x[i][0].unpack(f), x[i][1].unpack(g);
+#pragma unroll
+                                for (int k = 0; k < N; ++k) turned_pair(f[k], g[k], c[k], s[k], u[k], w[k]);
+                                x[i][0].pack(u), x[i][1].pack(w);
+                            } else {
+                                float f[N], u[N];
+                                x[i][0].unpack(f);
+#pragma unroll
+                                for (int k = 0; k < P; ++k) turned_pair(f[2 * k], f[2 * k + 1], c[k], s[k], u[2 * k], u[2 * k + 1]);
+                                x[i][0].pack(u);
+                            }
+                        }
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+                            if (v < whole) x[i][v].store(out + v * apart);
+                        if (more)   // a last piece that is not whole, the rest of a long head
+                            for (uint32_t k = whole * apart; at + k < a.dim; k += apart)
+                                for (uint32_t e = k; e < k + N && at + e < a.dim; ++e) out[e] = in[e];
+                    }
+                    in += in_step, out += out_step;
                 }
+                if (head + lanes * kBatch < heads) ask(head + lanes * kBatch);
             }
         }
+        __syncthreads();   // the next part's tables go where this one's were
     }
     pdl_leave();
 }
@@ -253,14 +290,23 @@ int start(Args &a, cudaStream_t stream) {
     // copying threads have two pieces too where the turning ones do (at most half the threads turn)
     const uint32_t pieces = (a.dim - a.turned + N - 1) / N;
     a.units = a.turning + std::min(HALF ? (pieces + 1) / 2 : pieces, (uint32_t)kThreads / 2);
-    // heads side by side: a thread takes up to eight heads of a token (its sines serve them all), fewer while the SMs are not full
-    uint32_t most = 8;
-    while (most > 1 && a.tokens * ((a.all_heads + most - 1) / most) * a.units < (uint64_t)sms * 1024) most /= 2;
-    a.lanes = std::min(kThreads / a.units, (a.all_heads + most - 1) / most);
-    a.group = kThreads / (a.units * a.lanes);
-    const uint64_t ctas = (a.tokens + a.group - 1) / a.group;
-    Launch l{(unsigned)std::min<uint64_t>(ctas, (uint64_t)sms * 8 * 4), kThreads, 0, stream, 0, true};
-    const cudaError_t e = launch(l, k_rotary<T, N, WIDE, HALF>, a);
+    // heads side by side: a thread takes one batch of a token's heads, fewer while the SMs are not full
+    constexpr uint32_t kBatch = kBatchOf<T, N, HALF>;
+    uint64_t groups = 0;
+    for (Part &p : a.part) {
+        if (p.heads == 0) continue;
+        uint32_t most = kBatch;
+        while (most > 1 && a.tokens * ((p.heads + most - 1) / most) * a.units < (uint64_t)sms * 1024) most /= 2;
+        p.lanes = std::min(kThreads / a.units, (p.heads + most - 1) / most);
+        p.group = kThreads / (a.units * p.lanes);
+        groups += (a.tokens + p.group - 1) / p.group;
+    }
+    Launch l{0, kThreads, 0, stream, 1, true};
+    int fit = 0;   // as many as the device holds at once: each walks on
+    cudaError_t e = clusters_that_fit(l, k_rotary<T, N, WIDE, HALF>, fit);
+    if (e != cudaSuccess) return fail_cuda(e, "rotary occupancy");
+    l.grid = (unsigned)std::min<uint64_t>(groups, fit);
+    e = launch(l, k_rotary<T, N, WIDE, HALF>, a);
     return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "rotary kernel launch");
 }
 
@@ -310,10 +356,10 @@ int run(const bf16opt_rotary_t *d, const void *q, const void *k, void *out_q, vo
     if (n > 1 && may_overlap(out[0], out[1])) return bad("two outputs overlap");
 
     Args a = {};
-    Place *place[2] = {&a.q, &a.k};
     uint64_t bits = 0;   // everything that has to be a multiple of a vector's bytes
     for (int i = 0; i < n; ++i) {
-        *place[i] = Place{in[i].p, const_cast<void *>(out[i].p), in[i].s[0] / e, in[i].s[1] / e, in[i].s[2] / e, out[i].s[0] / e, out[i].s[1] / e, out[i].s[2] / e};
+        a.part[i] = Part{in[i].p, const_cast<void *>(out[i].p), in[i].s[0] / e, in[i].s[1] / e, in[i].s[2] / e,
+                         out[i].s[0] / e, out[i].s[1] / e, out[i].s[2] / e, i ? d->kv_heads : d->heads, 0, 0};
         bits |= (uintptr_t)in[i].p | (uintptr_t)out[i].p;
         for (int s = 0; s < 3; ++s) bits |= in[i].s[s] | out[i].s[s];
     }
@@ -322,7 +368,6 @@ int run(const bf16opt_rotary_t *d, const void *q, const void *k, void *out_q, vo
     a.tokens = d->batch * d->seq, a.seq = d->seq;
     a.positions = d->positions, a.positions_stride = d->positions_stride, a.positions_type = d->positions_type;
     a.offset = d->offset;
-    a.heads = d->heads, a.all_heads = d->heads + d->kv_heads;
     a.dim = d->dim, a.turned = d->rotary_dim;
     a.scale = d->scale, a.inverse = (uint32_t)d->inverse;
     for (uint32_t i = 0; i < d->rotary_dim / 2; ++i) {
