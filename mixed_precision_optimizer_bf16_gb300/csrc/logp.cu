@@ -8,6 +8,8 @@
 // time while it is in L2.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "logits.cuh"
 
 namespace cg = cooperative_groups;
@@ -15,8 +17,7 @@ namespace cg = cooperative_groups;
 namespace bf16ops {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 256, kFew = 64;   // of a CTA; for short rows
 constexpr int kU = 4;              // vectors of a thread at a time
 constexpr int kMaxCluster = 8;
 constexpr int kPairThreads = 512;
@@ -25,6 +26,9 @@ constexpr uint64_t kSliceVectors = 4 * kThreads * kU;   // of the backward kerne
 // instruction for two logits: the product is exact, and m c is off by its rounding (2^-4 at most), the same for the
 // whole row, which goes into the row's factor.  Beyond, they are formed from the differences z - m, with m known.
 constexpr float kFar = 0x1p20f;
+
+constexpr uint64_t kInFlight = 60 << 20;
+constexpr int kHeld = 8;
 
 enum Kind { LOGP, POLICY, PREFER };
 
@@ -56,6 +60,9 @@ struct Args {
     uint64_t dlogits_stride;
 };
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 // A stream's largest number and the sum of exp2((z - m) c).
 struct Stat {
     float m, s;
@@ -74,53 +81,64 @@ __device__ __forceinline__ float2 exponent(float2 z, float m, float mc, float c)
     return fma2(z, both(c), both(-mc));
 }
 
-// This thread's part of a slice.  FAR: around the row's largest logit, which is known.
-template <class T, bool FAR>
-__device__ __forceinline__ Stat thread_stat(const T *z, const Slice &s, uint32_t vocab, uint32_t rank, uint32_t ranks, float c, float top) {
-    constexpr int P = Vec<T>::N / 2;
-    const uint32_t tid = threadIdx.x, nv = s.v1 - s.v0;
-    const uint4 *zv = reinterpret_cast<const uint4 *>(z + s.head) + s.v0;
-    Stat st = {FAR ? top : -INFINITY, 0.f};
-    float mc = 0.f;
-    float2 sum = both(0.f);
-    for (uint32_t i = tid; i < nv; i += kThreads * kU) {
-        uint4 q[kU];
+// One thread's vectors of a slice, kThreads apart: groups of U of them, the first of which it asks for before anything else.  HELD: the
+// slice is no longer than that and stays in registers.
+template <class T, int kThreads, int U>
+struct Group {
+    uint4 q[U];
+    __device__ __forceinline__ void load(const uint4 *zv, uint32_t i, uint32_t nv) {
+        if (i + (U - 1) * kThreads < nv) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) q[u] = i + u * kThreads < nv ? zv[i + u * kThreads] : nothing<T>();
+            for (int u = 0; u < U; ++u) q[u] = zv[i + u * kThreads];
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = i + u * kThreads < nv ? zv[i + u * kThreads] : nothing<T>();
+        }
+    }
+};
+
+// A thread's maximum and sum so far.  FAR: around the row's largest logit, which is known.
+template <class T, bool FAR>
+struct Running {
+    float m, mc;
+    float2 sum;
+    __device__ __forceinline__ explicit Running(float top) : m(FAR ? top : -INFINITY), mc(0.f), sum(both(0.f)) {}
+    template <int U>
+    __device__ __forceinline__ void add(const uint4 (&q)[U], float c) {
+        constexpr int P = Vec<T>::N / 2;
         if (!FAR) {
-            const float mx = largest<T, kU>(q);
-            if (mx > st.m) {
+            const float mx = largest<T, U>(q);
+            if (mx > m) {
                 const float to = fmaxf(fminf(mx * c, kFar), -kFar);
-                sum = mul2(sum, both(st.m == -INFINITY ? 0.f : ex2(mc - to)));
-                st.m = mx, mc = to;
+                sum = mul2(sum, both(m == -INFINITY ? 0.f : ex2(mc - to)));
+                m = mx, mc = to;
             }
         }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
+        for (int u = 0; u < U; ++u) {
             float2 f[P];
             pairs<T>(q[u], f);
 #pragma unroll
             for (int k = 0; k < P; ++k) {
-                const float2 d = exponent<FAR>(f[k], safe_max(st.m), mc, c);
+                const float2 d = exponent<FAR>(f[k], safe_max(m), mc, c);
                 sum = add2(sum, make_float2(ex2(d.x), ex2(d.y)));
             }
         }
     }
-    st.s = sum.x + sum.y;
-    // mc is m c rounded, or -kFar: what is lost there is 2^-126 of a row that is not far
-    if (!FAR && st.s != 0.f) st.s *= ex2(fmaf(-st.m, c, mc));
-    uint32_t at = 0xffffffffu;
-    if (rank == 0 && tid < s.head) at = tid;
-    else if (rank + 1 == ranks && tid >= 32 && tid - 32 < vocab - s.tail0) at = s.tail0 + tid - 32;
-    if (at != 0xffffffffu) {
-        const float f = to_f32(z[at]);
-        const float m = FAR ? top : fmaxf(st.m, f);   // (a NaN passed over)
-        const float b = safe_max(m);
-        st.s = st.s * ex2((st.m - b) * c) + ex2((f - b) * c);
-        st.m = m;
+    // with the element at a row's end that is this thread's, if any
+    __device__ __forceinline__ Stat result(float c, bool one, float f) {
+        Stat st = {m, sum.x + sum.y};
+        // mc is m c rounded, or -kFar: what is lost there is 2^-126 of a row that is not far
+        if (!FAR && st.s != 0.f) st.s *= ex2(fmaf(-m, c, mc));
+        if (one) {
+            const float top = FAR ? m : fmaxf(m, f);   // (a NaN passed over)
+            const float b = safe_max(top);
+            st.s = st.s * ex2((m - b) * c) + ex2((f - b) * c);
+            st.m = top;
+        }
+        return st;
     }
-    return st;
-}
+};
 
 // log(x) of a positive sum, in 64 bits from a logarithm of its fraction in 32 (in [-0.35, 0.35]: off by 2^-25 or so).
 __device__ __forceinline__ double log_of(float x) {
@@ -157,76 +175,111 @@ __device__ __forceinline__ Terms terms_of(const Args &a, uint64_t row, float w, 
     return t;
 }
 
-// The gradient of a slice: scale_q softmax's exponentials, and scale at the label.
-template <class T, bool FAR>
-__device__ __forceinline__ void grad_slice(const T *z, T *out, uint32_t head, uint32_t v0, uint32_t nv, bool first, bool last, uint32_t tail0,
-                                           uint32_t vocab, float m, float c, float scale_q, float scale, uint32_t label) {
-    constexpr int N = Vec<T>::N, P = N / 2;
-    const uint32_t tid = threadIdx.x;
-    const uint4 *zv = reinterpret_cast<const uint4 *>(z + head) + v0;
-    T *ov = out + head + (size_t)v0 * N;
-    const bool whole = (((uintptr_t)out ^ (uintptr_t)z) & 15u) == 0;
-    const float base = safe_max(m), mc = base * c;
-    const float corrected = FAR ? scale_q : scale_q * ex2(fmaf(-base, c, mc));
-    auto one = [&](uint32_t at) {
-        const float f = to_f32(z[at]);
-        const float2 d = exponent<FAR>(make_float2(f, f), base, mc, c);
-        from_f32(out[at], fmaf(corrected, ex2(d.x), at == label ? scale : 0.f));
-    };
-    const uint32_t mine = label - head - v0 * N;   // the label's place in the slice, if it is there
-    for (uint32_t i = tid; i < nv; i += kThreads * kU) {
+// A slice of a row's gradient: vectors [v0, v0 + nv), with the elements before the first or behind the last vector of the row.
+template <class T>
+struct Target {
+    const T *z;
+    T *out;
+    uint32_t head, v0, nv, tail0, vocab;
+    bool first, last;   // the slice has the row's ends
+    __device__ __forceinline__ bool whole() const { return (((uintptr_t)out ^ (uintptr_t)z) & 15u) == 0; }
+    __device__ __forceinline__ T *vectors() const { return out + head + (size_t)v0 * Vec<T>::N; }
+};
+
+// scale_q exp2((z - m) c), and scale at the label.
+template <class T, bool FAR, int kThreads>
+struct Gradient {
+    static constexpr int N = Vec<T>::N, P = N / 2;
+    float base, mc, c, factor, scale;
+    uint32_t label, own, lane;   // own: the vector of the slice that has the label, if it is this thread's; the label's place in it
+    T *ov;
+    bool whole;
+    __device__ __forceinline__ Gradient(const Target<T> &t, float m, float c_, float scale_q, float scale_, uint32_t label_)
+        : base(safe_max(m)), mc(base * c_), c(c_), factor(FAR ? scale_q : scale_q * ex2(fmaf(-base, c_, mc))), scale(scale_), label(label_), ov(t.vectors()),
+          whole(t.whole()) {
+        const uint32_t at = label - t.head - t.v0 * N;
+        own = label >= t.head && at / N < t.nv && at / N % kThreads == threadIdx.x ? at / N : 0xffffffffu;
+        lane = at % N;
+    }
+    __device__ __forceinline__ void put(const uint4 &q, uint32_t j) const {
+        float2 f[P];
+        pairs<T>(q, f);
+        float g[N];
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            const float2 d = exponent<FAR>(f[k], base, mc, c);
+            const float2 r = mul2(both(factor), make_float2(ex2(d.x), ex2(d.y)));
+            g[2 * k] = r.x, g[2 * k + 1] = r.y;
+        }
+        if (j == own) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (lane == k) g[k] += scale;
+        }
+        store_vec<T>(ov + (size_t)j * N, g, whole);
+    }
+    __device__ __forceinline__ void ends(const Target<T> &t) const {
+        auto one = [&](uint32_t at) {
+            const float f = to_f32(t.z[at]);
+            const float2 d = exponent<FAR>(make_float2(f, f), base, mc, c);
+            from_f32(t.out[at], fmaf(factor, ex2(d.x), at == label ? scale : 0.f));
+        };
+        if (t.first && threadIdx.x < t.head) one(threadIdx.x);
+        if (t.last && threadIdx.x < t.vocab - t.tail0) one(t.tail0 + threadIdx.x);
+    }
+};
+
+template <class T, bool FAR, int kThreads>
+__device__ __forceinline__ void grad_slice(const Target<T> &t, float m, float c, float scale_q, float scale, uint32_t label) {
+    const Gradient<T, FAR, kThreads> g(t, m, c, scale_q, scale, label);
+    const uint4 *zv = reinterpret_cast<const uint4 *>(t.z + t.head) + t.v0;
+    for (uint32_t i = threadIdx.x; i < t.nv; i += kThreads * kU) {
         uint4 q[kU];
+        if (i + (kU - 1) * kThreads < t.nv) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
-            if (i + u * kThreads < nv) q[u] = zv[i + u * kThreads];
+            for (int u = 0; u < kU; ++u) q[u] = zv[i + u * kThreads];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const uint32_t j = i + u * kThreads;
-            if (j >= nv) break;
-            float2 f[P];
-            pairs<T>(q[u], f);
-            float g[N];
-#pragma unroll
-            for (int k = 0; k < P; ++k) {
-                const float2 d = exponent<FAR>(f[k], base, mc, c);
-                const float2 r = mul2(both(corrected), make_float2(ex2(d.x), ex2(d.y)));
-                g[2 * k] = r.x, g[2 * k + 1] = r.y;
-            }
-            if (mine / N == j && label >= head) {
-#pragma unroll
-                for (int k = 0; k < N; ++k)
-                    if (mine % N == k) g[k] += scale;
-            }
-            store_vec<T>(ov + (size_t)j * N, g, whole);
+            for (int u = 0; u < kU; ++u) g.put(q[u], i + u * kThreads);
+        } else {
+            for (uint32_t j = i; j < t.nv; j += kThreads) g.put(zv[j], j);
         }
     }
-    if (first && tid < head) one(tid);
-    if (last && tid < vocab - tail0) one(tail0 + tid);
+    g.ends(t);
 }
 
-template <class T>
-__device__ __forceinline__ void zero_slice(const T *z, T *out, uint32_t head, uint32_t v0, uint32_t nv, bool first, bool last, uint32_t tail0,
-                                           uint32_t vocab) {
+template <class T, int kThreads>
+__device__ __forceinline__ void zero_slice(const Target<T> &t) {
     constexpr int N = Vec<T>::N;
-    T *ov = out + head + (size_t)v0 * N;
-    const bool whole = (((uintptr_t)out ^ (uintptr_t)z) & 15u) == 0;
+    T *ov = t.vectors();
+    const bool whole = t.whole();
     const float zero[N] = {};
-    for (uint32_t i = threadIdx.x; i < nv; i += kThreads) store_vec<T>(ov + (size_t)i * N, zero, whole);
-    if (first && threadIdx.x < head) from_f32(out[threadIdx.x], 0.f);
-    if (last && threadIdx.x < vocab - tail0) from_f32(out[tail0 + threadIdx.x], 0.f);
+    for (uint32_t i = threadIdx.x; i < t.nv; i += kThreads) store_vec<T>(ov + (size_t)i * N, zero, whole);
+    if (t.first && threadIdx.x < t.head) from_f32(t.out[threadIdx.x], 0.f);
+    if (t.last && threadIdx.x < t.vocab - t.tail0) from_f32(t.out[t.tail0 + threadIdx.x], 0.f);
 }
 
 __device__ __forceinline__ bool far_row(float m, float c) { return !(fabsf(m * c) < kFar) && m != -INFINITY; }
 
-// A cluster of CTAs (or one) takes a row.
-template <class T, int KIND, bool GRAD>
-__global__ void __launch_bounds__(kThreads) k_rows(const Args a) {
+// A cluster of CTAs (or one) takes a row.  HELD vectors of a thread (0: none) stay in registers between the two passes: the slice is
+// no longer than that.
+template <class T, int KIND, bool GRAD, int kThreads, int HELD>
+__global__ void __launch_bounds__(kThreads, HELD == 8 ? 3 : kThreads == kFew ? 16 : 5) k_rows(const Args a) {
+    constexpr int U = HELD ? HELD : kU, kWarps = kThreads / 32;
     __shared__ Stat sm[2][kMaxCluster * kWarps];
+    __shared__ float sm_scale;
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint64_t row = blockIdx.x / ranks;
+    if (ranks > 1) cluster_arrive();   // (every CTA's shared memory has to exist before another one writes there)
     pdl_enter();
+    const T *z = reinterpret_cast<const T *>(a.logits) + row * a.logits_stride;
+    const Slice s = slice_of(z, a.vocab, rank, ranks, 31 - __clz(ranks));
+    const uint4 *zv = reinterpret_cast<const uint4 *>(z + s.head) + s.v0;
+    const uint32_t nv = s.v1 - s.v0;
+    // asked for before it is known whether the row counts
+    Group<T, kThreads, U> group;
+    group.load(zv, tid, nv);
     const int64_t label = load_index(a.labels, a.labels_type, row);
     float w = a.row_weight ? a.row_weight[row] : 1.f;
     if (KIND == PREFER && a.pairs == 0) {
@@ -236,11 +289,11 @@ __global__ void __launch_bounds__(kThreads) k_rows(const Args a) {
         if ((int64_t)row < lo || (int64_t)row >= hi) w = 0.f;
     }
     const bool counts = w != 0.f && label >= 0 && label < (int64_t)a.vocab;
-    const T *z = reinterpret_cast<const T *>(a.logits) + row * a.logits_stride;
-    T *out = GRAD ? reinterpret_cast<T *>(a.dlogits) + row * a.dlogits_stride : nullptr;
-    const Slice s = slice_of(z, a.vocab, rank, ranks, 31 - __clz(ranks));
+    const Target<T> target = {z, GRAD ? reinterpret_cast<T *>(a.dlogits) + row * a.dlogits_stride : nullptr, s.head, s.v0, nv, s.tail0, a.vocab,
+                              rank == 0, rank + 1 == ranks};
+    if (ranks > 1) cluster_wait();
     if (!counts) {   // the same in the whole cluster
-        if (GRAD) zero_slice<T>(z, out, s.head, s.v0, s.v1 - s.v0, rank == 0, rank + 1 == ranks, s.tail0, a.vocab);
+        if (GRAD) zero_slice<T, kThreads>(target);
         if (rank == 0 && tid == 0) {
             if (KIND == POLICY) a.loss[row] = 0.f;
             if (KIND != PREFER && a.logp) a.logp[row] = 0.f;
@@ -249,8 +302,11 @@ __global__ void __launch_bounds__(kThreads) k_rows(const Args a) {
         pdl_leave();
         return;
     }
-    if (ranks > 1) cluster.sync();   // every CTA's shared memory exists
     const float z_label = to_f32(z[label]);
+    uint32_t at = 0xffffffffu;
+    if (target.first && tid < s.head) at = tid;
+    else if (target.last && tid >= 32 && tid - 32 < a.vocab - s.tail0) at = s.tail0 + tid - 32;
+    const float z_end = at != 0xffffffffu ? to_f32(z[at]) : 0.f;
 
     auto joined = [&](Stat st, int turn) {
         st = warp_join(st, a.c);
@@ -269,34 +325,57 @@ __global__ void __launch_bounds__(kThreads) k_rows(const Args a) {
         }
         return warp_join(all, a.c);
     };
-    Stat st = joined(thread_stat<T, false>(z, s, a.vocab, rank, ranks, a.c, 0.f), 0);
+    auto pass = [&](auto far, float top) {
+        Running<T, decltype(far)::value> run(top);
+        if (HELD) {
+            run.add(group.q, a.c);
+        } else {
+            if (decltype(far)::value) group.load(zv, tid, nv);
+            for (uint32_t i = tid; i < nv; i += kThreads * U) {
+                run.add(group.q, a.c);
+                group.load(zv, i + kThreads * U, nv);
+            }
+        }
+        return run.result(a.c, at != 0xffffffffu, z_end);
+    };
+    Stat st = joined(pass(std::false_type(), 0.f), 0);
     const bool far = far_row(st.m, a.c);
-    if (far) st = joined(thread_stat<T, true>(z, s, a.vocab, rank, ranks, a.c, st.m), 1);
+    if (far) st = joined(pass(std::true_type(), st.m), 1);
 
     if (!GRAD && (rank != 0 || tid != 0)) return;
     float4 keep = make_float4(st.m, st.s, 0.f, __int_as_float((int)row));
     float scale = 0.f;
-    if (KIND != PREFER) {
+    if (KIND != PREFER && warp == 0) {   // (a few operations in 64 bits: one warp's)
         const Terms t = terms_of<KIND>(a, row, w, st.m, st.s, z_label);
         if (rank == 0 && tid == 0) {
             if (KIND == POLICY) a.loss[row] = t.loss;
             if (a.logp) a.logp[row] = t.logp;
         }
         keep.z = t.slope;
-        scale = t.slope * (a.dloss ? a.dloss[row] : 1.f) * a.inv_t;
+        if (GRAD && tid == 0) sm_scale = t.slope * (a.dloss ? a.dloss[row] : 1.f) * a.inv_t;
     }
     if (!GRAD) {
         if (a.saved) a.saved[row] = keep;
         return;
     }
-    const uint32_t nv = s.v1 - s.v0;
-    const bool first = rank == 0, last = rank + 1 == ranks;
-    if (scale == 0.f) zero_slice<T>(z, out, s.head, s.v0, nv, first, last, s.tail0, a.vocab);
-    else {
+    __syncthreads();
+    scale = sm_scale;
+    auto gradient = [&](auto far) {
+        constexpr bool FAR = decltype(far)::value;
         const float scale_q = st.s == 0.f ? 0.f : -scale / st.s;
-        if (far) grad_slice<T, true>(z, out, s.head, s.v0, nv, first, last, s.tail0, a.vocab, st.m, a.c, scale_q, scale, (uint32_t)label);
-        else grad_slice<T, false>(z, out, s.head, s.v0, nv, first, last, s.tail0, a.vocab, st.m, a.c, scale_q, scale, (uint32_t)label);
-    }
+        if (HELD) {
+            const Gradient<T, FAR, kThreads> g(target, st.m, a.c, scale_q, scale, (uint32_t)label);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (tid + u * kThreads < nv) g.put(group.q[u], tid + u * kThreads);
+            g.ends(target);
+        } else {
+            grad_slice<T, FAR, kThreads>(target, st.m, a.c, scale_q, scale, (uint32_t)label);
+        }
+    };
+    if (scale == 0.f) zero_slice<T, kThreads>(target);
+    else if (far) gradient(std::true_type());
+    else gradient(std::false_type());
     pdl_leave();
 }
 
@@ -311,18 +390,18 @@ __global__ void __launch_bounds__(kThreads) k_backward(const Args a) {
     float scale = 0.f;
     if (index >= 0 && (!a.dloss || (uint64_t)index < a.losses)) scale = keep.z * (a.dloss ? a.dloss[index] : 1.f) * a.inv_t;
     const T *z = reinterpret_cast<const T *>(a.logits) + row * a.logits_stride;
-    T *out = reinterpret_cast<T *>(a.dlogits) + row * a.dlogits_stride;
     const Slice s = slice_of(z, a.vocab, 0, 1, 0);
     const uint32_t v0 = (uint32_t)((uint64_t)s.nv * slice / a.slices), nv = (uint32_t)((uint64_t)s.nv * (slice + 1) / a.slices) - v0;
-    const bool first = slice == 0, last = slice + 1 == a.slices;
+    const Target<T> target = {z, reinterpret_cast<T *>(a.dlogits) + row * a.dlogits_stride, s.head, v0, nv, s.tail0, a.vocab,
+                              slice == 0, slice + 1 == a.slices};
     if (scale == 0.f) {
-        zero_slice<T>(z, out, s.head, v0, nv, first, last, s.tail0, a.vocab);
+        zero_slice<T, kThreads>(target);
     } else {
         const int64_t label = load_index(a.labels, a.labels_type, row);
         const uint32_t at = label >= 0 && label < (int64_t)a.vocab ? (uint32_t)label : 0xffffffffu;
         const float scale_q = keep.y == 0.f ? 0.f : -scale / keep.y;
-        if (far_row(keep.x, a.c)) grad_slice<T, true>(z, out, s.head, v0, nv, first, last, s.tail0, a.vocab, keep.x, a.c, scale_q, scale, at);
-        else grad_slice<T, false>(z, out, s.head, v0, nv, first, last, s.tail0, a.vocab, keep.x, a.c, scale_q, scale, at);
+        if (far_row(keep.x, a.c)) grad_slice<T, true, kThreads>(target, keep.x, a.c, scale_q, scale, at);
+        else grad_slice<T, false, kThreads>(target, keep.x, a.c, scale_q, scale, at);
     }
     pdl_leave();
 }
@@ -493,23 +572,35 @@ Args args_of(const bf16opt_tokens_t *d) {
     return a;
 }
 
+template <class T, int KIND, bool GRAD, int kThreads, int HELD>
+int launch_rows(const Args &a, unsigned cluster, cudaStream_t stream) {
+    const Launch l{(unsigned)(a.rows * cluster), (unsigned)kThreads, 0, stream, cluster, true};
+    const cudaError_t e = launch(l, k_rows<T, KIND, GRAD, kThreads, HELD>, a);
+    return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "logp kernel launch");
+}
+
 template <class T, int KIND, bool GRAD>
-int launch_rows(const Args &a, cudaStream_t stream) {
+int choose_rows(const Args &a, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "logp: no CUDA device");
-    // CTAs per row: as many as keep the SMs busy with few rows
     const uint64_t vecs = a.vocab / Vec<T>::N + 1;
+    // CTAs per row: as many as keep the SMs busy with few rows
     unsigned cluster = 1;
     while (cluster < kMaxCluster && a.rows * cluster <= (uint64_t)sms * 4 && vecs / cluster > 2 * kThreads * kU) cluster *= 2;
-    const Launch l{(unsigned)(a.rows * cluster), kThreads, 0, stream, cluster, true};
-    const cudaError_t e = launch(l, k_rows<T, KIND, GRAD>, a);
-    return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "logp kernel launch");
+    if (vecs <= kFew * kU) return launch_rows<T, KIND, GRAD, kFew, GRAD ? kU : 0>(a, 1, stream);
+    if (GRAD) {
+        if (vecs <= (uint64_t)cluster * kThreads * kHeld) return launch_rows<T, KIND, GRAD, kThreads, GRAD ? kHeld : 0>(a, cluster, stream);
+        // what the SMs have of rows at a time has to stay in L2 for the second pass
+        while (cluster < kMaxCluster && (uint64_t)sms * 5 / cluster * vecs * 16 > kInFlight && a.rows * vecs * 16 > kInFlight) cluster *= 2;
+        if (vecs <= (uint64_t)cluster * kThreads * kHeld) return launch_rows<T, KIND, GRAD, kThreads, GRAD ? kHeld : 0>(a, cluster, stream);
+    }
+    return launch_rows<T, KIND, GRAD, kThreads, 0>(a, cluster, stream);
 }
 
 template <int KIND, bool GRAD>
 int rows_kernel(const Args &a, int type, void *stream) {
-    return type == BF16OPT_TYPE_BF16 ? launch_rows<__nv_bfloat16, KIND, GRAD>(a, (cudaStream_t)stream)
-                                     : launch_rows<float, KIND, GRAD>(a, (cudaStream_t)stream);
+    return type == BF16OPT_TYPE_BF16 ? choose_rows<__nv_bfloat16, KIND, GRAD>(a, (cudaStream_t)stream)
+                                     : choose_rows<float, KIND, GRAD>(a, (cudaStream_t)stream);
 }
 
 int logp_forward(const bf16opt_tokens_t *d, float *logp, float *saved, void *stream) {
