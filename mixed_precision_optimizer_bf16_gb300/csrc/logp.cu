@@ -28,7 +28,6 @@ constexpr uint64_t kSliceVectors = 4 * kThreads * kU;   // of the backward kerne
 constexpr float kFar = 0x1p20f;
 
 constexpr uint64_t kInFlight = 60 << 20;
-constexpr int kHeld = 8;
 
 enum Kind { LOGP, POLICY, PREFER };
 
@@ -41,7 +40,7 @@ struct Args {
     int labels_type;
     const float *row_weight;
     float c;                       // log2(e) / T
-    float inv_t;
+    float inv_t, inv_t_rest;       // 1 / T
     double inv_t64;
     // policy
     const float *advantage, *old_logp, *ref_logp;
@@ -149,28 +148,73 @@ __device__ __forceinline__ double log_of(float x) {
     return fma((double)k, 0.69314718055994530942, (double)logf(f));
 }
 
-// A counted row's log-probability, loss and slope.
+// a + b, and what rounding took off it (Knuth).
+__device__ __forceinline__ float two_sum(float a, float b, float &off) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    off = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+    return s;
+}
+
+// What a row's loss needs beside its logits, asked for with the first of them.
+struct Given {
+    float w, advantage, old_logp, ref_logp, dloss;
+};
+template <int KIND, bool GRAD>
+__device__ __forceinline__ Given given_of(const Args &a, uint64_t row) {
+    Given g = {1.f, 0.f, 0.f, 0.f, 1.f};
+    if (a.row_weight) g.w = a.row_weight[row];
+    if (KIND == POLICY) {
+        g.advantage = a.advantage[row];
+        if (a.old_logp) g.old_logp = a.old_logp[row];
+        if (a.ref_logp) g.ref_logp = a.ref_logp[row];
+    }
+    if (GRAD && a.dloss) g.dloss = a.dloss[row];
+    return g;
+}
+
+// A counted row's log-probability, loss and slope.  logp = (z - m) / T - log s is kept as a sum of two numbers until it is compared with
+// the others', so that a ratio is as exact as its exponential.  log s = k ln 2 + log f, f in [0.7, 1.4]; k times the leading bits
+// of ln 2 is exact.
 struct Terms {
     float loss, logp, slope;
 };
 template <int KIND>
-__device__ __forceinline__ Terms terms_of(const Args &a, uint64_t row, float w, float m, float s, float z) {
+__device__ __forceinline__ Terms terms_of(const Args &a, const Given &g, float m, float s, float z) {
     Terms t;
-    const double logp = m == -INFINITY && s == 0.f ? -INFINITY : ((double)z - m) * a.inv_t64 - log_of(s);
-    t.logp = (float)logp;
+    float hi, lo = 0.f, off;
+    float d = two_sum(z, -m, off);
+    const float p = d * a.inv_t;
+    if (fabsf(p) < INFINITY && s > 0.f && s < INFINITY) {
+        int k;
+        float f = frexpf(s, &k);
+        if (f < 0.70710678f) f *= 2.f, --k;
+        lo = fmaf(d, a.inv_t, -p) + fmaf(d, a.inv_t_rest, off * a.inv_t) - fmaf((float)k, 1.42860677e-6f, logf(f));
+        hi = two_sum(p, -0.693145751953125f * (float)k, off);
+        lo += off;
+    } else {
+        hi = m == -INFINITY && s == 0.f ? -INFINITY : (z - m) * a.inv_t - logf(s);
+    }
+    t.logp = hi + lo;
     t.loss = 0.f, t.slope = 1.f;
     if (KIND == POLICY) {
-        const float adv = a.advantage[row];
-        const float ratio = expf(a.old_logp ? (float)(logp - a.old_logp[row]) : t.logp - t.logp);
+        const bool fine = fabsf(hi) < INFINITY;
+        float x = t.logp - t.logp;
+        if (a.old_logp) {
+            x = two_sum(hi, -g.old_logp, off);
+            if (fine) x += lo + off;
+        }
+        const float adv = g.advantage, ratio = expf(x);
         const float kept = adv >= 0.f ? (ratio > a.highest ? a.highest : ratio) : (ratio < a.lowest ? a.lowest : ratio);   // NaN stays
         t.loss = -kept * adv;
         t.slope = kept == ratio || ratio != ratio ? -ratio * adv : 0.f;
         if (a.ref_logp) {
-            const float d = (float)(a.ref_logp[row] - logp), e = expm1f(d);
+            d = two_sum(g.ref_logp, -hi, off);
+            if (fine) d += off - lo;
+            const float e = expm1f(d);
             t.loss += a.kl_weight * (d == INFINITY ? d : e - d);
             t.slope -= a.kl_weight * e;
         }
-        t.loss *= w, t.slope *= w;
+        t.loss *= g.w, t.slope *= g.w;
     }
     return t;
 }
@@ -281,7 +325,8 @@ __global__ void __launch_bounds__(kThreads, HELD == 8 ? 3 : kThreads == kFew ? 1
     Group<T, kThreads, U> group;
     group.load(zv, tid, nv);
     const int64_t label = load_index(a.labels, a.labels_type, row);
-    float w = a.row_weight ? a.row_weight[row] : 1.f;
+    const Given given = given_of<KIND, GRAD>(a, row);
+    float w = given.w;
     if (KIND == PREFER && a.pairs == 0) {
         w = 0.f;
     } else if (KIND == PREFER) {
@@ -345,14 +390,14 @@ __global__ void __launch_bounds__(kThreads, HELD == 8 ? 3 : kThreads == kFew ? 1
     if (!GRAD && (rank != 0 || tid != 0)) return;
     float4 keep = make_float4(st.m, st.s, 0.f, __int_as_float((int)row));
     float scale = 0.f;
-    if (KIND != PREFER && warp == 0) {   // (a few operations in 64 bits: one warp's)
-        const Terms t = terms_of<KIND>(a, row, w, st.m, st.s, z_label);
+    if (KIND != PREFER && warp == 0) {
+        const Terms t = terms_of<KIND>(a, given, st.m, st.s, z_label);
         if (rank == 0 && tid == 0) {
             if (KIND == POLICY) a.loss[row] = t.loss;
             if (a.logp) a.logp[row] = t.logp;
         }
         keep.z = t.slope;
-        if (GRAD && tid == 0) sm_scale = t.slope * (a.dloss ? a.dloss[row] : 1.f) * a.inv_t;
+        if (GRAD && tid == 0) sm_scale = t.slope * given.dloss * a.inv_t;
     }
     if (!GRAD) {
         if (a.saved) a.saved[row] = keep;
@@ -567,7 +612,7 @@ Args args_of(const bf16opt_tokens_t *d) {
     a.rows = d->rows, a.vocab = d->vocab;
     a.logits = d->logits, a.logits_stride = d->logits_stride;
     a.labels = d->labels, a.labels_type = d->labels_type, a.row_weight = d->row_weight;
-    a.inv_t64 = 1.0 / (double)d->temperature, a.inv_t = (float)a.inv_t64;
+    a.inv_t64 = 1.0 / (double)d->temperature, a.inv_t = (float)a.inv_t64, a.inv_t_rest = (float)(a.inv_t64 - (double)a.inv_t);
     a.c = (float)(1.4426950408889634074 / (double)d->temperature);
     return a;
 }
@@ -583,16 +628,16 @@ template <class T, int KIND, bool GRAD>
 int choose_rows(const Args &a, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "logp: no CUDA device");
-    const uint64_t vecs = a.vocab / Vec<T>::N + 1;
+    const uint64_t vecs = a.vocab / Vec<T>::N;   // of a row, at most
     // CTAs per row: as many as keep the SMs busy with few rows
     unsigned cluster = 1;
     while (cluster < kMaxCluster && a.rows * cluster <= (uint64_t)sms * 4 && vecs / cluster > 2 * kThreads * kU) cluster *= 2;
     if (vecs <= kFew * kU) return launch_rows<T, KIND, GRAD, kFew, GRAD ? kU : 0>(a, 1, stream);
     if (GRAD) {
-        if (vecs <= (uint64_t)cluster * kThreads * kHeld) return launch_rows<T, KIND, GRAD, kThreads, GRAD ? kHeld : 0>(a, cluster, stream);
+        if (vecs <= (uint64_t)cluster * kThreads * 4) return launch_rows<T, KIND, GRAD, kThreads, GRAD ? 4 : 0>(a, cluster, stream);
+        if (vecs <= (uint64_t)cluster * kThreads * 8) return launch_rows<T, KIND, GRAD, kThreads, GRAD ? 8 : 0>(a, cluster, stream);
         // what the SMs have of rows at a time has to stay in L2 for the second pass
         while (cluster < kMaxCluster && (uint64_t)sms * 5 / cluster * vecs * 16 > kInFlight && a.rows * vecs * 16 > kInFlight) cluster *= 2;
-        if (vecs <= (uint64_t)cluster * kThreads * kHeld) return launch_rows<T, KIND, GRAD, kThreads, GRAD ? kHeld : 0>(a, cluster, stream);
     }
     return launch_rows<T, KIND, GRAD, kThreads, 0>(a, cluster, stream);
 }
