@@ -17,7 +17,7 @@ namespace cg = cooperative_groups;
 namespace bf16ops {
 namespace {
 
-constexpr int kThreads = 256, kFew = 64;   // of a CTA; for short rows
+constexpr int kThreads = 256, kFew = 64, kMany = 384;   // of a CTA; for short rows; where a slice stays in shared memory
 constexpr int kU = 4;              // vectors of a thread at a time
 constexpr int kMaxCluster = 8;
 constexpr int kPairThreads = 512;
@@ -27,7 +27,11 @@ constexpr uint64_t kSliceVectors = 4 * kThreads * kU;   // of the backward kerne
 // whole row, which goes into the row's factor.  Beyond, they are formed from the differences z - m, with m known.
 constexpr float kFar = 0x1p20f;
 
+// Of rows that are read a second time, at a time: what L2 keeps of them (two dies, each of which holds what its SMs ask
+// for: at 95 MB 2048 x 250880 took 419 us instead of 341).
 constexpr uint64_t kInFlight = 60 << 20;
+constexpr unsigned kResident = 6;   // CTAs of an SM there (five: 350 us)
+constexpr uint64_t kStage = 72 * 1024 / 16;   // vectors of a slice in shared memory
 
 enum Kind { LOGP, POLICY, PREFER };
 
@@ -304,11 +308,16 @@ __device__ __forceinline__ void zero_slice(const Target<T> &t) {
 
 __device__ __forceinline__ bool far_row(float m, float c) { return !(fabsf(m * c) < kFar) && m != -INFINITY; }
 
-// A cluster of CTAs (or one) takes a row.  HELD vectors of a thread (0: none) stay in registers between the two passes: the slice is
-// no longer than that.
+constexpr int kStaged = -1;
+
+// A cluster of CTAs (or one) takes a row.  HELD vectors of a thread stay in registers between the two passes: the slice is
+// no longer than that.  kStaged: it comes through, and stays in, shared memory, where each thread has places of its own.  0: it is
+// read again.
 template <class T, int KIND, bool GRAD, int kThreads, int HELD>
-__global__ void __launch_bounds__(kThreads, HELD == 8 ? 3 : kThreads == kFew ? 16 : 5) k_rows(const Args a) {
-    constexpr int U = HELD ? HELD : kU, kWarps = kThreads / 32;
+__global__ void __launch_bounds__(kThreads, HELD == 8 || HELD == kStaged ? 3 : kThreads == kFew ? 16 : GRAD && HELD == 0 ? kResident : 5) k_rows(const Args a) {
+    constexpr bool STAGED = HELD == kStaged;
+    constexpr int U = HELD > 0 ? HELD : kU, kWarps = kThreads / 32;
+    extern __shared__ __align__(128) uint4 stage[];
     __shared__ Stat sm[2][kMaxCluster * kWarps];
     __shared__ float sm_scale;
     cg::cluster_group cluster = cg::this_cluster();
@@ -323,7 +332,17 @@ __global__ void __launch_bounds__(kThreads, HELD == 8 ? 3 : kThreads == kFew ? 1
     const uint32_t nv = s.v1 - s.v0;
     // asked for before it is known whether the row counts
     Group<T, kThreads, U> group;
-    group.load(zv, tid, nv);
+    uint32_t groups = 0;   // of copies on their way
+    if constexpr (STAGED) {
+        for (uint32_t i = tid; i < nv + tid; i += kThreads * U, ++groups) {   // (the same number of turns for all)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i + u * kThreads < nv) copy_async16(stage + i + u * kThreads, zv + i + u * kThreads);
+            copy_commit();
+        }
+    } else {
+        group.load(zv, tid, nv);
+    }
     const int64_t label = load_index(a.labels, a.labels_type, row);
     const Given given = given_of<KIND, GRAD>(a, row);
     float w = given.w;
@@ -338,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, HELD == 8 ? 3 : kThreads == kFew ? 1
                               rank == 0, rank + 1 == ranks};
     if (ranks > 1) cluster_wait();
     if (!counts) {   // the same in the whole cluster
+        if constexpr (STAGED) copy_wait<0>();
         if (GRAD) zero_slice<T, kThreads>(target);
         if (rank == 0 && tid == 0) {
             if (KIND == POLICY) a.loss[row] = 0.f;
@@ -372,7 +392,13 @@ __global__ void __launch_bounds__(kThreads, HELD == 8 ? 3 : kThreads == kFew ? 1
     };
     auto pass = [&](auto far, float top) {
         Running<T, decltype(far)::value> run(top);
-        if (HELD) {
+        if constexpr (STAGED) {
+            for (uint32_t i = tid, left = groups; i < nv + tid; i += kThreads * U) {
+                copy_wait_for(--left);
+                group.load(stage, i, nv);
+                run.add(group.q, a.c);
+            }
+        } else if constexpr (HELD > 0) {
             run.add(group.q, a.c);
         } else {
             if (decltype(far)::value) group.load(zv, tid, nv);
@@ -408,7 +434,12 @@ __global__ void __launch_bounds__(kThreads, HELD == 8 ? 3 : kThreads == kFew ? 1
     auto gradient = [&](auto far) {
         constexpr bool FAR = decltype(far)::value;
         const float scale_q = st.s == 0.f ? 0.f : -scale / st.s;
-        if (HELD) {
+        if constexpr (STAGED) {
+            const Gradient<T, FAR, kThreads> g(target, st.m, a.c, scale_q, scale, (uint32_t)label);
+#pragma unroll 4
+            for (uint32_t j = tid; j < nv; j += kThreads) g.put(stage[j], j);
+            g.ends(target);
+        } else if constexpr (HELD > 0) {
             const Gradient<T, FAR, kThreads> g(target, st.m, a.c, scale_q, scale, (uint32_t)label);
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -618,9 +649,15 @@ Args args_of(const bf16opt_tokens_t *d) {
 }
 
 template <class T, int KIND, bool GRAD, int kThreads, int HELD>
-int launch_rows(const Args &a, unsigned cluster, cudaStream_t stream) {
-    const Launch l{(unsigned)(a.rows * cluster), (unsigned)kThreads, 0, stream, cluster, true};
-    const cudaError_t e = launch(l, k_rows<T, KIND, GRAD, kThreads, HELD>, a);
+int launch_rows(const Args &a, unsigned cluster, cudaStream_t stream, size_t smem = 0) {
+    auto k = k_rows<T, KIND, GRAD, kThreads, HELD>;
+    const Launch l{(unsigned)(a.rows * cluster), (unsigned)kThreads, smem, stream, cluster, true};
+    if (smem) {
+        int fit = 0;   // (allows the kernel its shared memory)
+        const cudaError_t e = clusters_that_fit(l, k, fit);
+        if (e != cudaSuccess) return fail_cuda(e, "logp occupancy");
+    }
+    const cudaError_t e = launch(l, k, a);
     return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "logp kernel launch");
 }
 
@@ -633,11 +670,18 @@ int choose_rows(const Args &a, cudaStream_t stream) {
     unsigned cluster = 1;
     while (cluster < kMaxCluster && a.rows * cluster <= (uint64_t)sms * 4 && vecs / cluster > 2 * kThreads * kU) cluster *= 2;
     if (vecs <= kFew * kU) return launch_rows<T, KIND, GRAD, kFew, GRAD ? kU : 0>(a, 1, stream);
-    if (GRAD) {
-        if (vecs <= (uint64_t)cluster * kThreads * 4) return launch_rows<T, KIND, GRAD, kThreads, GRAD ? 4 : 0>(a, cluster, stream);
-        if (vecs <= (uint64_t)cluster * kThreads * 8) return launch_rows<T, KIND, GRAD, kThreads, GRAD ? 8 : 0>(a, cluster, stream);
-        // what the SMs have of rows at a time has to stay in L2 for the second pass
-        while (cluster < kMaxCluster && (uint64_t)sms * 5 / cluster * vecs * 16 > kInFlight && a.rows * vecs * 16 > kInFlight) cluster *= 2;
+    if constexpr (GRAD) {
+        // in registers; or in shared memory, where a CTA's part of it is enough (several CTAs per row wait for one another: 2048 x 128256
+        // took 184 us either way, 4096 x 50257 170 us, 145 us from L2)
+        if (vecs <= (uint64_t)cluster * kThreads * 4) return launch_rows<T, KIND, GRAD, kThreads, 4>(a, cluster, stream);
+        if (vecs <= (uint64_t)cluster * kThreads * 8) return launch_rows<T, KIND, GRAD, kThreads, 8>(a, cluster, stream);
+        if (cluster == 1 && vecs <= kStage) return launch_rows<T, KIND, GRAD, kMany, kStaged>(a, 1, stream, vecs * 16);
+        // the second pass from L2: so many CTAs per row, and so few of an SM, that what the SMs have of rows at a time stays there
+        const uint64_t row = vecs * 16, all = a.rows * row;
+        while (cluster < kMaxCluster && sms * kResident / cluster * row > kInFlight && all > kInFlight) cluster *= 2;
+        const uint64_t resident = std::max<uint64_t>(2, kInFlight * cluster / (sms * row));
+        const bool fewer = resident < kResident && all > kInFlight;
+        return launch_rows<T, KIND, GRAD, kThreads, 0>(a, cluster, stream, fewer ? 224 * 1024 / (resident + 1) : 0);
     }
     return launch_rows<T, KIND, GRAD, kThreads, 0>(a, cluster, stream);
 }

@@ -252,6 +252,46 @@ def test_policy_in_place(rows, vocab, dtype):
     assert got[2] is z and all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+@pytest.mark.parametrize("vocab,dtype,pad,shift", [(40009, BF16, 0, 0), (36872, BF16, 8, 0), (100003, BF16, 3, 5), (131072, BF16, 0, 0), (24577, F32, 0, 1), (66001, F32, 0, 0)])
+def test_policy_many_long_rows(vocab, dtype, pad, shift):
+    """More rows than the SMs, longer than shared memory's part of them: masked ones side by side, clipped ones, far ones, masks, NaN, in place."""
+    rows = 640
+    z, labels, adv, how = policy_case(rows, vocab, dtype, vocab % 97, weights=True, pad=pad, shift=shift)
+    how["row_weight"][150:310] = 0                     # whole CTAs' turns
+    labels[400:402] = -100
+    how["old_logp"][410:415] -= 3                     # clipped where the advantage is positive
+    how["ref_logp"][410:415] = R.logp(z[410:415], labels[410:415])[0].float()
+    how["kl_weight"] = 0.0
+    z[500] *= 1e6
+    z[501] = torch.finfo(dtype).min
+    z[502, vocab // 2:] = -INF
+    for r in (500, 501, 502):
+        labels[r] = 3
+        how["row_weight"][r] = 0.5
+        how["old_logp"][r] = (R.logp(z[r:r + 1], labels[r:r + 1])[0] - 0.05).float()
+    loss_r, logp_r, slope_r, dz_r, scale = (x[480:] for x in R.policy(z, labels, adv, **how))
+    off = sum_error(vocab) + 2.0 ** -21
+    got = ops.policy_loss_grad(z, labels, adv, **how)
+    loss, logp, saved = ops.policy_forward(z, labels, adv, **how)
+    back = ops.token_logp_backward(z, labels, saved, temperature=how["temperature"])
+    close(got[0][480:], loss_r, off * 2 * (loss_r.abs() + slope_r.abs()), "loss")
+    close(got[1][480:], logp_r, sum_error(vocab) + 2.0 ** -23 * logp_r.abs(), "logp")
+    close(got[2][480:], dz_r, gradient_slack(scale, vocab) + 2 * off * scale, "dlogits")
+    # the other rows against the two calls: the same sums in another order, so a step of the type apart at most, and what the sums are off by
+    assert torch.equal(got[2] == 0, back == 0)
+    u = 2.0 ** -7 if dtype == BF16 else 2.0 ** -22
+    assert bool(((got[2].double() - back.double()).abs() <= u * back.double().abs() + 4 * off * back.double().abs().amax(1, keepdim=True) + 2.0 ** -126).all())
+    assert not got[2][150:310].any() and not got[2][400:402].any()
+    z[320, 7], z[321, 0] = NAN, INF
+    how["row_weight"][319:323] = 1.0
+    how["old_logp"][319:323] = logp[319:323] if bool(logp[319:323].all()) else how["old_logp"][319:323]
+    again = ops.policy_loss_grad(z, labels, adv, out=z, **how)
+    assert bool(torch.isnan(again[2][320:322]).all()) and bool(torch.isnan(again[0][320:322]).all())
+    same = torch.ones(rows, dtype=torch.bool, device="cuda")
+    same[319:323] = False
+    assert all(torch.equal(a[same], b[same]) for a, b in zip(got, again))
+
+
 def test_policy_a_masked_label_and_rows_of_nothing():
     z, labels, adv, how = policy_case(4, 600, F32, 23)
     z[0, 300:], labels[0] = -INF, 400
