@@ -21,15 +21,15 @@ constexpr int kThreads = 256, kFew = 64, kMany = 384;   // of a CTA; for short r
 constexpr int kU = 4;              // vectors of a thread at a time
 constexpr int kMaxCluster = 8;
 constexpr int kPairThreads = 512;
-constexpr uint64_t kSliceVectors = 4 * kThreads * kU;   // of the backward kernel's CTAs
+constexpr uint64_t kSliceVectors = 2 * kThreads * kU;   // of the backward kernel's CTAs (twice as many: 1021 x 32003 FP32 55 us, 48 so; half: 2048 x 250880 341 us, 298)
 // A row whose largest logit m is below this (|m| / T, in powers of two) has its exponents z c - m c in one
 // instruction for two logits: the product is exact, and m c is off by its rounding (2^-4 at most), the same for the
 // whole row, which goes into the row's factor.  Beyond, they are formed from the differences z - m, with m known.
 constexpr float kFar = 0x1p20f;
 
 // Of rows that are read a second time, at a time: what L2 keeps of them (two dies, each of which holds what its SMs ask
-// for: at 95 MB 2048 x 250880 took 419 us instead of 341).
-constexpr uint64_t kInFlight = 60 << 20;
+// for: at 95 MB 2048 x 250880 took 419 us instead of 341, at 76 MB 1024 x 250880 FP32 405 us, 426 us at 57).
+constexpr uint64_t kInFlight = 76 << 20;
 constexpr unsigned kResident = 6;   // CTAs of an SM there (five: 350 us)
 constexpr uint64_t kStage = 72 * 1024 / 16;   // vectors of a slice in shared memory
 
@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, HELD == 8 || HELD == kStaged ? 3 : k
         }
         return warp_join(all, a.c);
     };
+    uint32_t last = tid;   // where the group that is in registers begins
     auto pass = [&](auto far, float top) {
         Running<T, decltype(far)::value> run(top);
         if constexpr (STAGED) {
@@ -402,9 +403,10 @@ __global__ void __launch_bounds__(kThreads, HELD == 8 || HELD == kStaged ? 3 : k
             run.add(group.q, a.c);
         } else {
             if (decltype(far)::value) group.load(zv, tid, nv);
-            for (uint32_t i = tid; i < nv; i += kThreads * U) {
+            for (last = tid;; last += kThreads * U) {
                 run.add(group.q, a.c);
-                group.load(zv, i + kThreads * U, nv);
+                if (last + kThreads * U >= nv) break;
+                group.load(zv, last + kThreads * U, nv);
             }
         }
         return run.result(a.c, at != 0xffffffffu, z_end);
@@ -446,7 +448,16 @@ __global__ void __launch_bounds__(kThreads, HELD == 8 || HELD == kStaged ? 3 : k
                 if (tid + u * kThreads < nv) g.put(group.q[u], tid + u * kThreads);
             g.ends(target);
         } else {
-            grad_slice<T, FAR, kThreads>(target, st.m, a.c, scale_q, scale, (uint32_t)label);
+            // backwards, what was read last first: the last group is in registers, the ones before it are the likeliest to be in L2
+            const Gradient<T, FAR, kThreads> g(target, st.m, a.c, scale_q, scale, (uint32_t)label);
+            for (uint32_t i = last;; i -= kThreads * U) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i + u * kThreads < nv) g.put(group.q[u], i + u * kThreads);
+                if (i < kThreads * U) break;
+                group.load(zv, i - kThreads * U, nv);
+            }
+            g.ends(target);
         }
     };
     if (scale == 0.f) zero_slice<T, kThreads>(target);
