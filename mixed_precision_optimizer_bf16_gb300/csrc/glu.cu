@@ -96,59 +96,140 @@ __device__ __forceinline__ float2 activate(float2 g, float2 &slope) {
 
 // ------------------------------------------------------------------ eight columns of a thread
 
-// VECTOR: eight neighbours from `first`, four lanes to a run; rows and their starts are multiples of 16 bytes.
-// Otherwise columns first, first + 32, ..: a run is a warp's, whatever the alignment.
-template <class T, bool VECTOR>
+// Eight neighbours from `first`, four lanes to a run.  ALIGNED: rows begin on 16 bytes.  Otherwise the warp has 256 neighbours of
+// one row: each lane reads the aligned vectors that hold its columns, and writes the aligned 16 bytes (32 of FP32) that
+// hold its first column, with what the lane before it has of them; nothing but a warp's two ends is written element by element.
+template <class T, bool ALIGNED>
 struct Eight {
-    static constexpr int W = sizeof(T) / 2;
+    static constexpr int W = sizeof(T) / 2, N = 8 / W, K = 4 * W;   // vectors; elements of a vector; words
     union {
         uint4 v[W];
+        uint32_t w[K];
         T e[8];
     };
     __device__ __forceinline__ Eight() {}
-    __device__ __forceinline__ static uint32_t column(uint32_t first, int i) { return VECTOR ? first + i : first + 32 * i; }
-    __device__ __forceinline__ void load(const T *row, uint32_t first, uint32_t columns) {
-        if (VECTOR && first + 8 <= columns) {
+
+    // Eight elements of x (2 K words) from element t on, 0 <= t < 8.
+    __device__ __forceinline__ static void window(uint32_t (&x)[2 * K], uint32_t t, Eight &to) {
+        if constexpr (sizeof(T) == 4) {
+            if (t & 4)
 #pragma unroll
-            for (int w = 0; w < W; ++w) v[w] = __ldcs(reinterpret_cast<const uint4 *>(row + first) + w);
+                for (int i = 0; i < 11; ++i) x[i] = x[i + 4];
+            if (t & 2)
+#pragma unroll
+                for (int i = 0; i < 9; ++i) x[i] = x[i + 2];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) to.w[i] = t & 1 ? x[i + 1] : x[i];
         } else {
+            if (t & 4)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (column(first, i) < columns) e[i] = row[column(first, i)];
-                else from_f32(e[i], 0.f);
-            }
+                for (int i = 0; i < 6; ++i) x[i] = x[i + 2];
+            if (t & 2)
+#pragma unroll
+                for (int i = 0; i < 5; ++i) x[i] = x[i + 1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to.w[i] = t & 1 ? __funnelshift_r(x[i], x[i + 1], 16) : x[i];
         }
     }
+    // Elements between the 16-byte boundary before it and p.
+    __device__ __forceinline__ static uint32_t beyond(const T *p) { return (uint32_t)((uintptr_t)p & 15u) / (uint32_t)sizeof(T); }
+
     __device__ __forceinline__ void store(T *row, uint32_t first, uint32_t columns) const {
-        if (VECTOR && first + 8 <= columns) {
+        const uint32_t s = ALIGNED ? 0 : beyond(row);
+        if (ALIGNED || s == 0) {
+            if (first + 8 <= columns) {
 #pragma unroll
-            for (int w = 0; w < W; ++w) __stcs(reinterpret_cast<uint4 *>(row + first) + w, v[w]);
-        } else {
+                for (int i = 0; i < W; ++i) __stcs(reinterpret_cast<uint4 *>(row + first) + i, v[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (first + i < columns) row[first + i] = e[i];
+            }
+            return;
+        }
+        const uint32_t lane = threadIdx.x & 31;
+        uint32_t x[2 * K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            x[i] = i < K - 4 ? 0 : __shfl_up_sync(0xffffffffu, w[i], 1);   // (less than a vector of them)
+            x[K + i] = w[i];
+        }
+        Eight block;   // columns [first - s, first - s + 8): its own first 8 - s, behind the last s of the lane before
+        window(x, 8 - s, block);
+        const bool mine = lane > 0 && first - s + 8 <= columns, next = lane < 31 && first - s + 16 <= columns;
+        if (mine) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) __stcs(reinterpret_cast<uint4 *>(row + (first - s)) + i, block.v[i]);
+        }
+        // its own elements that neither its vectors nor the next lane's have
+        const uint32_t split = (1u << (8 - s)) - 1, valid = first + 8 <= columns ? 0xffu : first < columns ? (1u << (columns - first)) - 1 : 0u;
+        const uint32_t left = ((mine ? 0 : split) | (next ? 0 : 0xffu & ~split)) & valid;
+        if (left) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (column(first, i) < columns) row[column(first, i)] = e[i];
+                if (left >> i & 1) row[first + i] = e[i];
         }
     }
     __device__ __forceinline__ void unpack(float2 (&f)[4]) const {
         if constexpr (sizeof(T) == 2) {
-            f[0] = make_float2(bf16_lo(v[0].x), bf16_hi(v[0].x)), f[1] = make_float2(bf16_lo(v[0].y), bf16_hi(v[0].y));
-            f[2] = make_float2(bf16_lo(v[0].z), bf16_hi(v[0].z)), f[3] = make_float2(bf16_lo(v[0].w), bf16_hi(v[0].w));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
         } else {
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                f[2 * w] = make_float2(__uint_as_float(v[w].x), __uint_as_float(v[w].y));
-                f[2 * w + 1] = make_float2(__uint_as_float(v[w].z), __uint_as_float(v[w].w));
-            }
+            for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
         }
     }
     __device__ __forceinline__ void pack(const float2 (&f)[4]) {
         if constexpr (sizeof(T) == 2) {
-            v[0] = make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y), pack_bf16(f[2].x, f[2].y), pack_bf16(f[3].x, f[3].y));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = pack_bf16(f[i].x, f[i].y);
         } else {
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
-                v[w] = make_uint4(__float_as_uint(f[2 * w].x), __float_as_uint(f[2 * w].y), __float_as_uint(f[2 * w + 1].x), __float_as_uint(f[2 * w + 1].y));
+            for (int i = 0; i < 4; ++i) w[2 * i] = __float_as_uint(f[i].x), w[2 * i + 1] = __float_as_uint(f[i].y);
         }
+    }
+
+    // Up to n (8 or a vector's) elements of a row from column `at` on, an aligned address, as vectors where they all are the row's; 0 else.
+    __device__ __forceinline__ void piece(const T *row, int32_t at, int n, uint32_t columns) {
+        if (at >= 0 && at + n <= (int32_t)columns) {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                if (i * N < n) v[i] = __ldcs(reinterpret_cast<const uint4 *>(row + at) + i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i < n && at + i >= 0 && at + i < (int32_t)columns) e[i] = row[at + i];
+                else from_f32(e[i], 0.f);
+            }
+        }
+    }
+};
+
+// Columns [first, first + 8) of a row on their way, 0 behind its end.
+template <class T, bool ALIGNED>
+struct Coming {
+    using E = Eight<T, ALIGNED>;
+    E block;
+    uint32_t s;                   // elements beyond a boundary
+    Eight<T, ALIGNED> behind;     // the next vector (s of its elements are wanted, less than it has), which the next lane has too
+    __device__ __forceinline__ void ask(const T *row, uint32_t first, uint32_t columns) {
+        if (ALIGNED) {
+            block.piece(row, (int32_t)first, 8, columns);
+        } else {
+            s = E::beyond(row);
+            block.piece(row, (int32_t)(first - s), 8, columns);
+            if (s) behind.piece(row, (int32_t)(first - s + 8), E::N, columns);
+        }
+    }
+    __device__ __forceinline__ E take() const {
+        if (ALIGNED || s == 0) return block;
+        constexpr int K = E::K;
+        uint32_t x[2 * K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) x[i] = block.w[i], x[K + i] = i < 4 ? behind.w[i] : 0;
+        E e;
+        E::window(x, s, e);
+        return e;
     }
 };
 
@@ -158,12 +239,11 @@ struct Place {
     bool there;            // the thread has columns within the row's runs
     uint32_t row, step;
 };
-template <bool VECTOR>
 __device__ __forceinline__ Place place_of(const Args &a) {
     const uint32_t group = blockIdx.x / a.blocks, block = blockIdx.x - group * a.blocks;
     const uint32_t slot = threadIdx.x / a.width, i = block * a.width + (threadIdx.x - slot * a.width);
     Place p;
-    p.first = VECTOR ? i * 8 : i / 32 * 256 + i % 32;
+    p.first = i * 8;
     p.run = p.first / kRun;
     p.there = p.first < a.runs * kRun && slot < a.deep;
     p.row = group * a.deep + slot;
@@ -172,92 +252,59 @@ __device__ __forceinline__ Place place_of(const Args &a) {
 }
 
 // Keeps the thread's columns of one row.  Every lane of the warp takes part; `there`: it has any.
-template <bool VECTOR, int PARTS>
+template <int PARTS>
 __device__ __forceinline__ void keep(const Args &a, const float2 (&f)[PARTS][4], uint8_t *codes, uint8_t *scales, const Place &p, bool there) {
-    if (VECTOR) {
-        uint32_t bytes = 0;   // of gate and of up, 16 bits each
+    uint32_t bytes = 0;   // of gate and of up, 16 bits each
 #pragma unroll
-        for (int k = 0; k < PARTS; ++k) {
+    for (int k = 0; k < PARTS; ++k) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(f[k][i].x), fabsf(f[k][i].y)));   // NaN passed over
+        bytes |= scale_byte(m) << (16 * k);
+    }
+    bytes = __vmaxu2(bytes, __shfl_xor_sync(0xffffffffu, bytes, 1));
+    bytes = __vmaxu2(bytes, __shfl_xor_sync(0xffffffffu, bytes, 2));
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+        uint32_t byte = bytes >> (16 * k) & 0xffffu;
+        float2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = f[k][i];
+        if (__any_sync(0xffffffffu, byte >= kLargestByte)) {   // the largest finite one again
             float m = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(f[k][i].x), fabsf(f[k][i].y)));   // NaN passed over
-            bytes |= scale_byte(m) << (16 * k);
+            for (int i = 0; i < 4; ++i) {
+                m = fmaxf(m, fmaxf(fabsf(x[i].x) < INFINITY ? fabsf(x[i].x) : 0.f, fabsf(x[i].y) < INFINITY ? fabsf(x[i].y) : 0.f));
+                x[i] = make_float2(holdable(x[i].x), holdable(x[i].y));
+            }
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            byte = scale_byte(fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2)));
         }
-        bytes = __vmaxu2(bytes, __shfl_xor_sync(0xffffffffu, bytes, 1));
-        bytes = __vmaxu2(bytes, __shfl_xor_sync(0xffffffffu, bytes, 2));
+        const float2 inv = both(inverse_scale(byte));
 #pragma unroll
-        for (int k = 0; k < PARTS; ++k) {
-            uint32_t byte = bytes >> (16 * k) & 0xffffu;
-            float2 x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = f[k][i];
-            if (__any_sync(0xffffffffu, byte >= kLargestByte)) {   // the largest finite one again
-                float m = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    m = fmaxf(m, fmaxf(fabsf(x[i].x) < INFINITY ? fabsf(x[i].x) : 0.f, fabsf(x[i].y) < INFINITY ? fabsf(x[i].y) : 0.f));
-                    x[i] = make_float2(holdable(x[i].x), holdable(x[i].y));
-                }
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                byte = scale_byte(fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2)));
-            }
-            const float2 inv = both(inverse_scale(byte));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], inv);
-            uint2 c;
-            c.x = to_codes(x[0].x, x[0].y) | to_codes(x[1].x, x[1].y) << 16;
-            c.y = to_codes(x[2].x, x[2].y) | to_codes(x[3].x, x[3].y) << 16;
-            if (there) {
-                __stcs(reinterpret_cast<uint2 *>(codes + k * a.rows * a.runs * kRun), c);
-                if ((p.first & (kRun - 1)) == 0) scales[k * a.rows * a.runs] = (uint8_t)byte;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < PARTS; ++k) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x = i & 1 ? f[k][i / 2].y : f[k][i / 2].x;
-                const uint32_t byte = scale_byte(warp_max(fabsf(x) < INFINITY ? fabsf(x) : 0.f));
-                if (there && p.run + i < a.runs) {
-                    codes[k * a.rows * a.runs * kRun + 32 * i] = (uint8_t)to_codes(holdable(x) * inverse_scale(byte), 0.f);
-                    if ((threadIdx.x & 31) == 0) scales[k * a.rows * a.runs + i] = (uint8_t)byte;
-                }
-            }
+        for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], inv);
+        uint2 c;
+        c.x = to_codes(x[0].x, x[0].y) | to_codes(x[1].x, x[1].y) << 16;
+        c.y = to_codes(x[2].x, x[2].y) | to_codes(x[3].x, x[3].y) << 16;
+        if (there) {
+            __stcs(reinterpret_cast<uint2 *>(codes + k * a.rows * a.runs * kRun), c);
+            if ((p.first & (kRun - 1)) == 0) scales[k * a.rows * a.runs] = (uint8_t)byte;
         }
     }
 }
 
-// What was kept, on its way: VECTOR: eight codes and their scale.
-template <bool VECTOR>
+// Eight columns of what was kept, on their way.
 struct Kept {
     uint2 c;
     uint32_t byte;
-    uint8_t codes[VECTOR ? 1 : 8], bytes[VECTOR ? 1 : 8];
-    __device__ __forceinline__ void load(const uint8_t *from, const uint8_t *scale, uint32_t run, uint32_t runs) {
-        if (VECTOR) {
-            c = __ldcs(reinterpret_cast<const uint2 *>(from));
-            byte = *scale;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                codes[VECTOR ? 0 : i] = run + i < runs ? from[32 * i] : (uint8_t)0;
-                bytes[VECTOR ? 0 : i] = run + i < runs ? scale[i] : (uint8_t)0;
-            }
-        }
+    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scale) {
+        c = __ldcs(reinterpret_cast<const uint2 *>(codes));
+        byte = *scale;
     }
     __device__ __forceinline__ void unpack(float2 (&f)[4]) const {
-        if (VECTOR) {
-            const float2 s = both(scale_of(byte));
-            f[0] = mul2(from_codes(c.x & 0xffffu), s), f[1] = mul2(from_codes(c.x >> 16), s);
-            f[2] = mul2(from_codes(c.y & 0xffffu), s), f[3] = mul2(from_codes(c.y >> 16), s);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int x = VECTOR ? 0 : 2 * i, y = VECTOR ? 0 : 2 * i + 1;
-                f[i] = mul2(from_codes(codes[x] | (uint32_t)codes[y] << 8), make_float2(scale_of(bytes[x]), scale_of(bytes[y])));
-            }
-        }
+        const float2 s = both(scale_of(byte));
+        f[0] = mul2(from_codes(c.x & 0xffffu), s), f[1] = mul2(from_codes(c.x >> 16), s);
+        f[2] = mul2(from_codes(c.y & 0xffffu), s), f[3] = mul2(from_codes(c.y >> 16), s);
     }
 };
 
@@ -267,24 +314,25 @@ struct Kept {
 // works on these: addresses only go on by a stride.  U: so many that 32 bytes or so of each thread are on their way.
 
 // PARTS: 1 or 2 of what is kept; ACT < 0: nothing but keeping or reading.
-template <class T, bool VECTOR, int PARTS, int ACT, bool KEEP>
+template <class T, bool ALIGNED, int PARTS, int ACT, bool KEEP>
 __global__ void __launch_bounds__(kThreads) k_forward(const Args a) {
-    constexpr int U = sizeof(T) == 2 && PARTS == 1 && VECTOR ? 2 : 1;
-    using E = Eight<T, VECTOR>;
+    constexpr int U = sizeof(T) == 2 && PARTS == 1 && ALIGNED ? 2 : 1;
+    using E = Eight<T, ALIGNED>;
     pdl_enter();
-    const Place p = place_of<VECTOR>(a);
+    const Place p = place_of(a);
     const T *x[PARTS];
 #pragma unroll
     for (int k = 0; k < PARTS; ++k) x[k] = reinterpret_cast<const T *>(a.x[k].p) + p.row * a.x[k].stride;
     T *h = reinterpret_cast<T *>(a.out[0]) + p.row * a.out_stride[0];
     uint8_t *codes = a.codes + (uint64_t)p.row * a.runs * kRun + p.first, *scales = a.scales + (uint64_t)p.row * a.runs + p.run;
-    E next[U][PARTS];
+    Coming<T, ALIGNED> next[U][PARTS];
     auto ask = [&](uint32_t row) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) {
-                next[u][k].load(x[k], p.there && row + u * p.step < a.rows ? p.first : a.columns, a.columns);
+                if (ALIGNED) next[u][k].ask(x[k], p.there && row + u * p.step < a.rows ? p.first : a.columns, a.columns);
+                else if (row + u * p.step < a.rows) next[u][k].ask(x[k], p.first, a.columns);   // (the same in the warp)
                 x[k] += p.step * a.x[k].stride;
             }
         }
@@ -296,7 +344,7 @@ __global__ void __launch_bounds__(kThreads) k_forward(const Args a) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k) next[u][k].unpack(f[u][k]);
+            for (int k = 0; k < PARTS; ++k) next[u][k].take().unpack(f[u][k]);
         ask(row + U * p.step);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -310,11 +358,11 @@ __global__ void __launch_bounds__(kThreads) k_forward(const Args a) {
                 }
                 E e;
                 e.pack(v);
-                if (there) e.store(h, p.first, a.columns);
+                if (ALIGNED ? there : row + u * p.step < a.rows) e.store(h, p.first, a.columns);
                 h += p.step * a.out_stride[0];
             }
             if (KEEP) {
-                keep<VECTOR, PARTS>(a, f[u], codes, scales, p, there);
+                keep<PARTS>(a, f[u], codes, scales, p, there);
                 codes += (uint64_t)p.step * a.runs * kRun, scales += (uint64_t)p.step * a.runs;
             }
         }
@@ -322,29 +370,25 @@ __global__ void __launch_bounds__(kThreads) k_forward(const Args a) {
     pdl_leave();
 }
 
-template <class T, bool VECTOR, int PARTS, int ACT>
-__global__ void __launch_bounds__(kThreads, VECTOR ? 4 : 2) k_backward(const Args a) {
-    constexpr int U = ACT < 0 && VECTOR ? 4 : 1;
-    using E = Eight<T, VECTOR>;
+template <class T, bool ALIGNED, int PARTS, int ACT>
+__global__ void __launch_bounds__(kThreads, 4) k_backward(const Args a) {
+    constexpr int U = ACT < 0 && ALIGNED ? 4 : 1;
+    using E = Eight<T, ALIGNED>;
     pdl_enter();
-    const Place p = place_of<VECTOR>(a);
-    if (!p.there) return;
+    const Place p = place_of(a);
+    if (ALIGNED && !p.there) return;   // (otherwise a warp's lanes, of one row, stay together)
     const T *x = reinterpret_cast<const T *>(a.x[0].p) + p.row * a.x[0].stride;
     const uint8_t *codes = a.codes + (uint64_t)p.row * a.runs * kRun + p.first, *scales = a.scales + (uint64_t)p.row * a.runs + p.run;
-    constexpr int kOuts = ACT < 0 ? 1 : 3;
-    T *out[kOuts];
-#pragma unroll
-    for (int i = 0; i < kOuts; ++i) out[i] = reinterpret_cast<T *>(a.out[i]) + p.row * a.out_stride[i];
-    E next;
-    Kept<VECTOR> kept[U][PARTS];
+    Coming<T, ALIGNED> next;
+    Kept kept[U][PARTS] = {};
     auto ask = [&](uint32_t row) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (row + u * p.step < a.rows) {
-                if (ACT >= 0) next.load(x, p.first, a.columns);
+                if (ACT >= 0) next.ask(x, p.first, a.columns);
 #pragma unroll
                 for (int k = 0; k < PARTS; ++k)
-                    kept[u][k].load(codes + k * a.rows * a.runs * kRun, scales + k * a.rows * a.runs, p.run, a.runs);
+                    if (ALIGNED || p.there) kept[u][k].load(codes + k * a.rows * a.runs * kRun, scales + k * a.rows * a.runs);
             }
             if (ACT >= 0) x += p.step * a.x[0].stride;
             codes += (uint64_t)p.step * a.runs * kRun, scales += (uint64_t)p.step * a.runs;
@@ -353,23 +397,21 @@ __global__ void __launch_bounds__(kThreads, VECTOR ? 4 : 2) k_backward(const Arg
     ask(p.row);
     for (uint32_t row = p.row; row < a.rows; row += U * p.step) {
         float2 f[U][PARTS][4], dh[4];
-        if (ACT >= 0) next.unpack(dh);
+        if (ACT >= 0) next.take().unpack(dh);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) kept[u][k].unpack(f[u][k]);
         ask(row + U * p.step);
-        auto put = [&](int i, const float2 (&v)[4]) {
+        auto put = [&](int i, uint32_t r, const float2 (&v)[4]) {
             E e;
             e.pack(v);
-            e.store(out[i], p.first, a.columns);
+            e.store(reinterpret_cast<T *>(a.out[i]) + r * a.out_stride[i], p.first, a.columns);
         };
         if constexpr (ACT < 0) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (row + u * p.step < a.rows) put(0, f[u][0]);
-                out[0] += p.step * a.out_stride[0];
-            }
+            for (int u = 0; u < U; ++u)
+                if (row + u * p.step < a.rows) put(0, row + u * p.step, f[u][0]);
         } else {
             float2 dg[4], du[4], h[4];
 #pragma unroll
@@ -383,11 +425,9 @@ __global__ void __launch_bounds__(kThreads, VECTOR ? 4 : 2) k_backward(const Arg
                     h[i] = mul2(h[i], f[0][PARTS - 1][i]);
                 }
             }
-            put(0, dg);
-            if (PARTS > 1) put(1, du);
-            if (a.out[2]) put(2, h);
-#pragma unroll
-            for (int i = 0; i < kOuts; ++i) out[i] += p.step * a.out_stride[i];
+            put(0, row, dg);
+            if (PARTS > 1) put(1, row, du);
+            if (a.out[2]) put(2, row, h);
         }
     }
     pdl_leave();
@@ -444,12 +484,12 @@ int check(uint64_t rows, uint32_t columns, int type, uint32_t parts, std::initia
     return BF16OPT_OK;
 }
 
-template <bool VECTOR, class K>
+template <bool ALIGNED, class K>
 int start(K kernel, Args a, cudaStream_t stream) {
     if (sm_count() < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "glu: no CUDA device");
-    // threads along a row (whole runs, whole warps where a run is a warp's), in pieces of up to a CTA's
-    const uint32_t quantum = VECTOR ? 4 : 32;
-    const uint32_t along = VECTOR ? a.runs * 4 : (a.columns + 255) / 256 * 32;
+    // threads along a row (whole runs; whole warps where a warp has one row), in pieces of up to a CTA's
+    const uint32_t quantum = ALIGNED ? 4 : 32;
+    const uint32_t along = (a.runs * 4 + quantum - 1) / quantum * quantum;
     a.blocks = (along + kThreads - 1) / kThreads;
     a.width = (along / quantum + a.blocks - 1) / a.blocks * quantum;
     a.deep = (uint32_t)std::min<uint64_t>(kThreads / a.width, a.rows);
