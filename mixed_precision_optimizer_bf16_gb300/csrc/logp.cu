@@ -205,7 +205,7 @@ __device__ __forceinline__ Terms terms_of(const Args &a, const Given &g, float m
         float x = t.logp - t.logp;
         if (a.old_logp) {
             x = two_sum(hi, -g.old_logp, off);
-            if (fine) x += lo + off;
+            if (fine && fabsf(x) < INFINITY) x += lo + off;
         }
         const float adv = g.advantage, ratio = expf(x);
         const float kept = adv >= 0.f ? (ratio > a.highest ? a.highest : ratio) : (ratio < a.lowest ? a.lowest : ratio);   // NaN stays
@@ -213,7 +213,7 @@ __device__ __forceinline__ Terms terms_of(const Args &a, const Given &g, float m
         t.slope = kept == ratio || ratio != ratio ? -ratio * adv : 0.f;
         if (a.ref_logp) {
             d = two_sum(g.ref_logp, -hi, off);
-            if (fine) d += off - lo;
+            if (fine && fabsf(d) < INFINITY) d += off - lo;
             const float e = expm1f(d);
             t.loss += a.kl_weight * (d == INFINITY ? d : e - d);
             t.slope -= a.kl_weight * e;

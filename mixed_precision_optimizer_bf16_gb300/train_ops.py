@@ -499,11 +499,6 @@ def _policy(rows, index, advantage, old_logp, ref_logp, clip_low, clip_high, kl_
     return _POLICY_T.pack(advantage.data_ptr(), _p(old_logp), _p(ref_logp), clip_low, clip_high, kl_weight, 0)
 
 
-def _rows_of(logits, columns):
-    shape = (logits.shape[0], columns) if columns else logits.shape[:1]
-    return _empty(shape, dtype=torch.float32, device=logits.device)
-
-
 @_on_stream
 def token_logp_forward(logits, labels, *, temperature=1.0, row_weight=None):
     """Log-probabilities [rows] (FP32) that softmax(logits / temperature) gives
@@ -511,7 +506,9 @@ def token_logp_forward(logits, labels, *, temperature=1.0, row_weight=None):
     token_logp_backward.  logits: [rows, vocab] bf16 or FP32.  A row with row_weight 0 or
     with a label outside the vocabulary does not count: it is not read and has 0."""
     d, rows, index = _tokens(logits, labels, temperature, row_weight)
-    logp, saved = _rows_of(logits, 0), _rows_of(logits, 4)
+    dev = logits.device
+    logp = _empty(rows, dtype=torch.float32, device=dev)
+    saved = _empty((rows, 4), dtype=torch.float32, device=dev)
     C.check(C.bf16opt_token_logp_forward(d, logp.data_ptr(), saved.data_ptr(), _raw_stream(index)))
     return logp, saved
 
@@ -525,7 +522,10 @@ def policy_forward(logits, labels, advantage, *, old_logp=None, ref_logp=None, c
     KL term): [rows] FP32, constants."""
     d, rows, index = _tokens(logits, labels, temperature, row_weight)
     p = _policy(rows, index, advantage, old_logp, ref_logp, clip_low, clip_high, kl_weight)
-    loss, logp, saved = _rows_of(logits, 0), _rows_of(logits, 0), _rows_of(logits, 4)
+    dev = logits.device
+    loss = _empty(rows, dtype=torch.float32, device=dev)
+    logp = _empty(rows, dtype=torch.float32, device=dev)
+    saved = _empty((rows, 4), dtype=torch.float32, device=dev)
     C.check(C.bf16opt_policy_forward(d, p, loss.data_ptr(), logp.data_ptr(), saved.data_ptr(), _raw_stream(index)))
     return loss, logp, saved
 
@@ -539,7 +539,9 @@ def policy_loss_grad(logits, labels, advantage, dloss=None, *, old_logp=None, re
     p = _policy(rows, index, advantage, old_logp, ref_logp, clip_low, clip_high, kl_weight)
     if dloss is not None:
         _need(dloss, "dloss", _F32, (rows,), index)
-    loss, logp = _rows_of(logits, 0), _rows_of(logits, 0)
+    dev = logits.device
+    loss = _empty(rows, dtype=torch.float32, device=dev)
+    logp = _empty(rows, dtype=torch.float32, device=dev)
     given, out = out, _dlogits(logits, out, index)
     C.check(C.bf16opt_policy_loss_grad(d, p, _p(dloss), loss.data_ptr(), logp.data_ptr(), out.data_ptr(), _stride(out), _raw_stream(index)))
     _written(given)
@@ -567,9 +569,10 @@ def preference_forward(logits, labels, offsets, *, ref_logp=None, kind="sigmoid"
     pairs = entries // 2
     p = _PREFERENCE_T.pack(pairs, _INDEX[offsets.dtype], _PREFER[kind], offsets.data_ptr(), _p(ref_logp), beta, label_smoothing, margin,
                            1 if length_normalise else 0)
-    loss = _empty(pairs, dtype=torch.float32, device=logits.device)
-    logp = _empty(2 * pairs, dtype=torch.float32, device=logits.device)
-    saved = _rows_of(logits, 4)
+    dev = logits.device
+    loss = _empty(pairs, dtype=torch.float32, device=dev)
+    logp = _empty(2 * pairs, dtype=torch.float32, device=dev)
+    saved = _empty((rows, 4), dtype=torch.float32, device=dev)
     C.check(C.bf16opt_preference_forward(d, p, loss.data_ptr(), logp.data_ptr(), saved.data_ptr(), _raw_stream(index)))
     return loss, logp, saved
 

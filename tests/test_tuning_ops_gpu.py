@@ -74,7 +74,7 @@ def check_logp(z, labels, temperature=1.0, row_weight=None, dloss=None):
     return logp, saved, got
 
 
-SIZES = [(1, 1), (3, 2), (2, 7), (5, 8), (4, 9), (3, 31), (300, 257), (40, 2053), (9, 4096), (700, 1000), (3, 33000), (2, 70001), (2, 250880)]
+SIZES = [(1, 1), (3, 2), (2, 7), (5, 8), (4, 9), (3, 31), (300, 257), (40, 2053), (9, 4096), (700, 1000), (310, 12000), (3, 33000), (2, 70001), (2, 250880)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -252,7 +252,7 @@ def test_policy_in_place(rows, vocab, dtype):
     assert got[2] is z and all(torch.equal(a, b) for a, b in zip(want, got))
 
 
-@pytest.mark.parametrize("vocab,dtype,pad,shift", [(40009, BF16, 0, 0), (36872, BF16, 8, 0), (100003, BF16, 3, 5), (131072, BF16, 0, 0), (24577, F32, 0, 1), (66001, F32, 0, 0)])
+@pytest.mark.parametrize("vocab,dtype,pad,shift", [(20011, BF16, 1, 3), (36000, BF16, 0, 0), (12345, F32, 0, 0), (40009, BF16, 0, 0), (36872, BF16, 8, 0), (100003, BF16, 3, 5), (131072, BF16, 0, 0), (24577, F32, 0, 1), (66001, F32, 0, 0)])
 def test_policy_many_long_rows(vocab, dtype, pad, shift):
     """More rows than the SMs, longer than shared memory's part of them: masked ones side by side, clipped ones, far ones, masks, NaN, in place."""
     rows = 640
@@ -370,6 +370,17 @@ def test_preference_without_pairs_or_rows():
     assert torch.allclose(loss, torch.full_like(loss, math.log(2))) and not logp.any()
     assert ops.token_logp_forward(z[:0], labels[:0])[0].numel() == 0
     assert ops.policy_loss_grad(z[:0], labels[:0], z[:0, 0])[2].shape == (0, 130)
+
+
+def test_policy_log_probabilities_at_the_ends():
+    """A sampler's or a reference's -inf: the formula's value, in that row alone."""
+    z, labels, adv, how = policy_case(6, 300, F32, 27)
+    adv[:] = torch.tensor([1.0, -1.0, 1.0, 1.0, -1.0, 0.5], device="cuda")
+    how["old_logp"][0], how["old_logp"][1], how["ref_logp"][2], how["ref_logp"][3] = -INF, -INF, -INF, INF
+    loss, logp, saved = ops.policy_forward(z, labels, adv, **how)
+    want = R.policy(z, labels, adv, **how)
+    assert loss[1] == INF and loss[2] == INF and loss[3] == INF and bool(torch.isfinite(loss[[0, 4, 5]]).all())
+    assert abs(float(loss[0] - want[0][0])) < 1e-5 and torch.equal(torch.isfinite(saved[:, 2]), torch.isfinite(want[2]))
 
 
 def test_preference_extremes():
