@@ -44,8 +44,7 @@ struct Args {
     int labels_type;
     const float *row_weight;
     float c;                       // log2(e) / T
-    float inv_t, inv_t_rest;       // 1 / T
-    double inv_t64;
+    float inv_t, inv_t_rest;       // 1 / T, and what it lacks
     // policy
     const float *advantage, *old_logp, *ref_logp;
     float lowest, highest, kl_weight;   // of the ratio
@@ -147,15 +146,6 @@ struct Running {
     }
 };
 
-// log(x) of a positive sum, in 64 bits from a logarithm of its fraction in 32 (in [-0.35, 0.35]: off by 2^-25 or so).
-__device__ __forceinline__ double log_of(float x) {
-    if (!(x > 0.f && x < INFINITY)) return logf(x);
-    int k;
-    float f = frexpf(x, &k);   // in [0.5, 1)
-    if (f < 0.70710678f) f *= 2.f, --k;
-    return fma((double)k, 0.69314718055994530942, (double)logf(f));
-}
-
 // a + b, and what rounding took off it (Knuth).
 __device__ __forceinline__ float two_sum(float a, float b, float &off) {
     const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
@@ -180,45 +170,48 @@ __device__ __forceinline__ Given given_of(const Args &a, uint64_t row) {
     return g;
 }
 
-// A counted row's log-probability, loss and slope.  logp = (z - m) / T - log s is kept as a sum of two numbers until it is compared with
-// the others', so that a ratio is as exact as its exponential.  log s = k ln 2 + log f, f in [0.7, 1.4]; k times the leading bits
-// of ln 2 is exact.
+// A number as a sum of two, hi the nearest to it; lo 0 beside an infinite or NaN hi.
+struct Two {
+    float hi, lo;
+    __device__ __forceinline__ Two operator+(const Two &b) const {   // (a + b and b + a are the same bits)
+        float off;
+        const float s = two_sum(hi, b.hi, off);
+        return {s, fabsf(s) < INFINITY ? __fadd_rn(__fadd_rn(lo, b.lo), off) : 0.f};
+    }
+    __device__ __forceinline__ float value() const { return hi + lo; }
+};
+
+// A row's log-probability (z - m) / T - log s.  log s = k ln 2 + log f, f in [0.7, 1.4]; k times the leading bits of ln 2 is exact.
+__device__ __forceinline__ Two logp_of(const Args &a, float m, float s, float z) {
+    float off;
+    const float d = two_sum(z, -m, off), p = d * a.inv_t;
+    if (!(fabsf(p) < INFINITY && s > 0.f && s < INFINITY)) return {m == -INFINITY && s == 0.f ? -INFINITY : (z - m) * a.inv_t - logf(s), 0.f};
+    int k;
+    float f = frexpf(s, &k);
+    if (f < 0.70710678f) f *= 2.f, --k;
+    const float lo = fmaf(d, a.inv_t, -p) + fmaf(d, a.inv_t_rest, off * a.inv_t) - fmaf((float)k, 1.42860677e-6f, logf(f));
+    return Two{p, lo} + Two{-0.693145751953125f * (float)k, 0.f};
+}
+
+// A counted row's log-probability, loss and slope.  The log-probability stays a sum of two numbers until it is compared with the others', so
+// that a ratio is as exact as its exponential.
 struct Terms {
     float loss, logp, slope;
 };
 template <int KIND>
 __device__ __forceinline__ Terms terms_of(const Args &a, const Given &g, float m, float s, float z) {
     Terms t;
-    float hi, lo = 0.f, off;
-    float d = two_sum(z, -m, off);
-    const float p = d * a.inv_t;
-    if (fabsf(p) < INFINITY && s > 0.f && s < INFINITY) {
-        int k;
-        float f = frexpf(s, &k);
-        if (f < 0.70710678f) f *= 2.f, --k;
-        lo = fmaf(d, a.inv_t, -p) + fmaf(d, a.inv_t_rest, off * a.inv_t) - fmaf((float)k, 1.42860677e-6f, logf(f));
-        hi = two_sum(p, -0.693145751953125f * (float)k, off);
-        lo += off;
-    } else {
-        hi = m == -INFINITY && s == 0.f ? -INFINITY : (z - m) * a.inv_t - logf(s);
-    }
-    t.logp = hi + lo;
+    const Two logp = logp_of(a, m, s, z);
+    t.logp = logp.value();
     t.loss = 0.f, t.slope = 1.f;
     if (KIND == POLICY) {
-        const bool fine = fabsf(hi) < INFINITY;
-        float x = t.logp - t.logp;
-        if (a.old_logp) {
-            x = two_sum(hi, -g.old_logp, off);
-            if (fine && fabsf(x) < INFINITY) x += lo + off;
-        }
+        const float x = a.old_logp ? (logp + Two{-g.old_logp, 0.f}).value() : t.logp - t.logp;
         const float adv = g.advantage, ratio = expf(x);
         const float kept = adv >= 0.f ? (ratio > a.highest ? a.highest : ratio) : (ratio < a.lowest ? a.lowest : ratio);   // NaN stays
         t.loss = -kept * adv;
         t.slope = kept == ratio || ratio != ratio ? -ratio * adv : 0.f;
         if (a.ref_logp) {
-            d = two_sum(g.ref_logp, -hi, off);
-            if (fine && fabsf(d) < INFINITY) d += off - lo;
-            const float e = expm1f(d);
+            const float d = (Two{g.ref_logp, 0.f} + Two{-logp.hi, -logp.lo}).value(), e = expm1f(d);
             t.loss += a.kl_weight * (d == INFINITY ? d : e - d);
             t.slope -= a.kl_weight * e;
         }
@@ -503,93 +496,107 @@ struct PairArgs {
     Args a;
     int kind, mean;
     float beta, smoothing, margin;
+    double centre;   // 1 / (2 beta)
     const float *ref;
 };
 
-template <class V, class F>
-__device__ __forceinline__ V block_reduce(V v, V *sm, F &&f) {   // the same in every thread
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = sm[threadIdx.x & 31 & (kPairThreads / 32 - 1)];
-#pragma unroll
-    for (int o = kPairThreads / 64; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    return v;
-}
-
-// A CTA takes a pair: its sums, its loss, and its rows' slopes.
+// A CTA takes a pair: its sums, its loss, and its rows' slopes.  The two sequences are one range of rows, so that the loads that wait
+// for one another (offsets, saved numbers and labels, the labels' logits) are waited for once; sums are pairs of FP32 numbers,
+// and what is computed in 64 bits is one warp's (with sums in 64 bits, one sequence after the other: 14 us for 24 or 300 rows).
 template <class T>
 __global__ void __launch_bounds__(kPairThreads) k_pairs(const PairArgs p) {
-    __shared__ double sm_d[kPairThreads / 32];
-    __shared__ long long sm_i[kPairThreads / 32];
+    constexpr int kWarps = kPairThreads / 32;
+    __shared__ int sm_offset[2][kWarps], sm_count[2][kWarps];
+    __shared__ Two sm_sum[2][kWarps];
+    __shared__ float sm_slope[2];
     const Args &a = p.a;
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_enter();
-    const uint64_t n = 2 * a.pairs;
-    const long long rows = (long long)a.rows;
-    auto offset = [&](uint64_t i) {
-        const long long o = load_index(a.offsets, a.offsets_type, i);
-        return o < 0 ? 0ll : o > rows ? rows : o;
+    const uint32_t n = 2 * (uint32_t)a.pairs, first = blockIdx.x, second = blockIdx.x + (uint32_t)a.pairs;
+    auto offset = [&](uint32_t i) {   // within the rows
+        const int64_t o = load_index(a.offsets, a.offsets_type, i);
+        return (int)(o < 0 ? 0 : o > (int64_t)a.rows ? (int64_t)a.rows : o);
     };
-    const long long end = offset(n);
-    // the offset that counts: the largest so far, at most the last one
-    auto largest_to = [&](uint64_t i) {
-        long long m = 0;
-        for (uint64_t j = threadIdx.x; j <= i; j += kPairThreads) m = max(m, offset(j));
-        m = block_reduce(m, sm_i, [](long long x, long long y) { return max(x, y); });
-        return min(m, end);
-    };
-    long long lo[2], hi[2];
-    double sum[2];
-    long long count[2];
-    for (int k = 0; k < 2; ++k) {
-        const uint64_t i = blockIdx.x + k * a.pairs;
-        lo[k] = largest_to(i);
-        hi[k] = max(lo[k], min(end, offset(i + 1)));
-        double s = 0;
-        long long c = 0;
-        for (long long r = lo[k] + threadIdx.x; r < hi[k]; r += kPairThreads) {
-            const float4 keep = a.saved[r];
-            if (__float_as_int(keep.w) < 0) continue;
-            ++c;
-            const float z = to_f32(reinterpret_cast<const T *>(a.logits)[(uint64_t)r * a.logits_stride + load_index(a.labels, a.labels_type, r)]);
-            s += keep.x == -INFINITY && keep.y == 0.f ? -INFINITY : ((double)z - keep.x) * a.inv_t64 - log_of(keep.y);
-        }
-        sum[k] = block_reduce(s, sm_d, [](double x, double y) { return x + y; });
-        count[k] = block_reduce(c, sm_i, [](long long x, long long y) { return x + y; });
-        if (p.mean && count[k] > 0) sum[k] /= (double)count[k];
+    // the offsets that count: the largest so far, at most the last one
+    const int end = offset(n), behind[2] = {offset(first + 1), offset(second + 1)};
+    int most[2] = {0, 0};
+    for (uint32_t j = tid; j <= second; j += kPairThreads) {
+        const int o = offset(j);
+        most[1] = max(most[1], o);
+        if (j <= first) most[0] = max(most[0], o);
     }
-    double h = sum[0] - sum[1];
-    if (p.ref) h = (sum[0] - p.ref[blockIdx.x]) - (sum[1] - p.ref[blockIdx.x + a.pairs]);
-    float loss, slope;   // slope: by h
-    if (p.kind == BF16OPT_PREFER_IPO) {
-        const double d = h - p.margin - 0.5 / (double)p.beta;
-        loss = (float)(d * d), slope = 2.f * (float)d;
-    } else {
-        const float m = (float)(h * p.beta - p.margin);
-        if (p.kind == BF16OPT_PREFER_HINGE) {
-            loss = m < 1.f ? 1.f - m : m == m ? 0.f : m;
-            slope = m < 1.f ? -p.beta : m == m ? 0.f : m;
+    for (int k = 0; k < 2; ++k) {
+        most[k] = __reduce_max_sync(0xffffffffu, most[k]);
+        if (lane == 0) sm_offset[k][warp] = most[k];
+    }
+    __syncthreads();
+    int lo[2], len[2];
+    for (int k = 0; k < 2; ++k) {
+        lo[k] = min(end, __reduce_max_sync(0xffffffffu, sm_offset[k][lane % kWarps]));
+        len[k] = max(0, min(end, behind[k]) - lo[k]);
+    }
+    const uint32_t all = (uint32_t)len[0] + (uint32_t)len[1];   // below 2^32
+    auto row_of = [&](uint32_t t) { return t < (uint32_t)len[0] ? (uint64_t)lo[0] + t : (uint64_t)lo[1] + (t - (uint32_t)len[0]); };
+    Two sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+    int count[2] = {0, 0};
+    for (uint64_t t = tid; t < all; t += kPairThreads) {
+        const uint64_t r = row_of((uint32_t)t);
+        const float4 keep = a.saved[r];
+        const int64_t label = load_index(a.labels, a.labels_type, r);
+        if (__float_as_int(keep.w) < 0) continue;
+        const Two logp = logp_of(a, keep.x, keep.y, to_f32(reinterpret_cast<const T *>(a.logits)[r * a.logits_stride + label]));
+        const bool k = t >= (uint32_t)len[0];
+        if (k) sum[1] = sum[1] + logp, ++count[1];
+        else sum[0] = sum[0] + logp, ++count[0];
+    }
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            sum[k] = sum[k] + Two{__shfl_xor_sync(0xffffffffu, sum[k].hi, o), __shfl_xor_sync(0xffffffffu, sum[k].lo, o)};
+        count[k] = __reduce_add_sync(0xffffffffu, count[k]);
+        if (lane == 0) sm_sum[k][warp] = sum[k], sm_count[k][warp] = count[k];
+    }
+    __syncthreads();
+    if (warp == 0) {
+        double total[2];
+        for (int k = 0; k < 2; ++k) {
+            sum[k] = sm_sum[k][lane % kWarps];
+#pragma unroll
+            for (int o = kWarps / 2; o > 0; o >>= 1)
+                sum[k] = sum[k] + Two{__shfl_xor_sync(0xffffffffu, sum[k].hi, o), __shfl_xor_sync(0xffffffffu, sum[k].lo, o)};
+            count[k] = __reduce_add_sync(0xffffffffu, lane < kWarps ? sm_count[k][lane] : 0);
+            total[k] = (double)sum[k].hi + sum[k].lo;
+            if (p.mean && count[k] > 0) total[k] /= (double)count[k];
+        }
+        double h = total[0] - total[1];
+        if (p.ref) h = (total[0] - p.ref[first]) - (total[1] - p.ref[second]);
+        float loss, slope;   // slope: by h
+        if (p.kind == BF16OPT_PREFER_IPO) {
+            const double d = h - p.margin - p.centre;
+            loss = (float)(d * d), slope = 2.f * (float)d;
         } else {
-            const float e = expf(-fabsf(m)), soft = log1pf(e);
-            const float up = m >= 0.f ? 1.f / (1.f + e) : e / (1.f + e), down = m >= 0.f ? e / (1.f + e) : 1.f / (1.f + e);   // sigmoid(m), sigmoid(-m)
-            const float q = p.smoothing;
-            loss = (1.f - q) * (soft + (m < 0.f ? -m : 0.f)) + (q != 0.f ? q * (soft + (m > 0.f ? m : 0.f)) : 0.f);
-            slope = p.beta * (q * up - (1.f - q) * down);
+            const float m = (float)(h * p.beta - p.margin);
+            if (p.kind == BF16OPT_PREFER_HINGE) {
+                loss = m < 1.f ? 1.f - m : m == m ? 0.f : m;
+                slope = m < 1.f ? -p.beta : m == m ? 0.f : m;
+            } else {
+                const float e = expf(-fabsf(m)), soft = log1pf(e);
+                const float up = m >= 0.f ? 1.f / (1.f + e) : e / (1.f + e), down = m >= 0.f ? e / (1.f + e) : 1.f / (1.f + e);   // sigmoid(m), sigmoid(-m)
+                const float q = p.smoothing;
+                loss = (1.f - q) * (soft + (m < 0.f ? -m : 0.f)) + (q != 0.f ? q * (soft + (m > 0.f ? m : 0.f)) : 0.f);
+                slope = p.beta * (q * up - (1.f - q) * down);
+            }
+        }
+        if (lane == 0) {
+            a.loss[first] = loss;
+            a.logp[first] = (float)total[0], a.logp[second] = (float)total[1];
+            for (int k = 0; k < 2; ++k) sm_slope[k] = (k ? -slope : slope) * (p.mean && count[k] > 0 ? 1.f / (float)count[k] : 1.f);
         }
     }
-    if (threadIdx.x == 0) {
-        a.loss[blockIdx.x] = loss;
-        a.logp[blockIdx.x] = (float)sum[0];
-        a.logp[blockIdx.x + a.pairs] = (float)sum[1];
-    }
-    for (int k = 0; k < 2; ++k) {
-        const float own = (k ? -slope : slope) * (p.mean && count[k] > 0 ? 1.f / (float)count[k] : 1.f);
-        for (long long r = lo[k] + threadIdx.x; r < hi[k]; r += kPairThreads) {
-            float4 &keep = a.saved[r];
-            if (__float_as_int(keep.w) >= 0) keep.z = own, keep.w = __int_as_float((int)blockIdx.x);
-        }
+    __syncthreads();
+    for (uint64_t t = tid; t < all; t += kPairThreads) {
+        float4 &keep = a.saved[row_of((uint32_t)t)];
+        if (__float_as_int(keep.w) >= 0) keep.z = sm_slope[t >= (uint32_t)len[0]], keep.w = __int_as_float((int)blockIdx.x);
     }
     pdl_leave();
 }
@@ -658,7 +665,8 @@ Args args_of(const bf16opt_tokens_t *d) {
     a.rows = d->rows, a.vocab = d->vocab;
     a.logits = d->logits, a.logits_stride = d->logits_stride;
     a.labels = d->labels, a.labels_type = d->labels_type, a.row_weight = d->row_weight;
-    a.inv_t64 = 1.0 / (double)d->temperature, a.inv_t = (float)a.inv_t64, a.inv_t_rest = (float)(a.inv_t64 - (double)a.inv_t);
+    const double inv_t = 1.0 / (double)d->temperature;
+    a.inv_t = (float)inv_t, a.inv_t_rest = (float)(inv_t - (double)a.inv_t);
     a.c = (float)(1.4426950408889634074 / (double)d->temperature);
     return a;
 }
@@ -800,7 +808,7 @@ int preference(const bf16opt_tokens_t *d, const bf16opt_preference_t *p, float *
     }
     if (!pairs) return BF16OPT_OK;
     if (sm_count() < 1) return fail(BF16OPT_ERR_UNSUPPORTED, "logp: no CUDA device");
-    PairArgs q = {a, p->kind, p->length_normalise, p->beta, p->label_smoothing, p->margin, p->ref_logp};
+    PairArgs q = {a, p->kind, p->length_normalise, p->beta, p->label_smoothing, p->margin, 0.5 / (double)p->beta, p->ref_logp};
     const Launch l{(unsigned)pairs, kPairThreads, 0, (cudaStream_t)stream, 0, true};
     const cudaError_t e = d->logits_type == BF16OPT_TYPE_BF16 ? launch(l, k_pairs<__nv_bfloat16>, q) : launch(l, k_pairs<float>, q);
     return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "logp kernel launch");
