@@ -769,6 +769,7 @@ def glu8(gate, up=None, *, act="silu"):
 # ------------------------------------------------------------------ rotary positions
 
 _LAYOUT = {"half": C.BF16OPT_ROTARY_HALF, "interleaved": C.BF16OPT_ROTARY_INTERLEAVED}
+_NOWHERE = (0, 0, 0)
 
 
 @functools.lru_cache(maxsize=256)
@@ -800,62 +801,64 @@ def _frequencies(rotary_dim, base, scaling, factor, original_length, slow, fast)
 
 
 def _heads(t, what, dtypes, like=None):
-    """(strides between batches, tokens and heads) of [tokens, heads, dim] or [batch, tokens, heads, dim]."""
+    """(shape, strides between batches, tokens and heads) of [tokens, heads, dim] or [batch, tokens, heads, dim]."""
     if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{what}: must be a CUDA tensor")
-    n = t.dim()
-    if n not in (3, 4) or t.dtype not in dtypes or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    shape, s = t.shape, t.stride()
+    n = len(s)
+    if (n != 3 and n != 4) or t.dtype not in dtypes or (s[-1] != 1 and shape[-1] > 1):
         raise ValueError(f"{what}: must be [tokens, heads, dim] or [batch, tokens, heads, dim], of {[str(d) for d in dtypes]}, contiguous within heads")
-    if like is not None and (t.get_device() != like.get_device() or t.shape[:-2] != like.shape[:-2] or t.shape[-1] != like.shape[-1]):
-        raise ValueError(f"{what}: shape {tuple(t.shape)} on {t.device} does not go with {tuple(like.shape)} on {like.device}")
-    s = t.stride()
-    return (0, s[0], s[1]) if n == 3 else s[:3]
+    if like is not None and (t.get_device() != like.get_device() or shape[:-2] != like.shape[:-2] or shape[-1] != like.shape[-1]):
+        raise ValueError(f"{what}: shape {tuple(shape)} on {t.device} does not go with {tuple(like.shape)} on {like.device}")
+    return shape, ((0, s[0], s[1]) if n == 3 else s[:3])
+
+
+def _turned(x, out, what, dtypes, shape):
+    """(a result of x's shape, its strides): the caller's or a new one."""
+    if out is None:
+        heads, dim = shape[-2:]
+        return _empty(shape, dtype=x.dtype, device=x.device), (shape[-3] * heads * dim, heads * dim, dim)
+    got, strides = _heads(out, what, dtypes, x)
+    if got != shape:
+        raise ValueError(f"{what}: shape {tuple(got)}, expected {tuple(shape)}")
+    _writable(out, what)
+    return out, strides
 
 
 @_on_stream
 def _rotary(q, k, positions, rotary_dim, layout, base, scaling, factor, original_length, slow, fast, offset, out_q, out_k, inverse):
-    sq = _heads(q, "q", _TYPE)
-    index, dim, heads = q.get_device(), q.shape[-1], q.shape[-2]
-    dtypes = (q.dtype,)
-    sk, kv = (0, 0, 0), 0
-    if k is not None:
-        sk, kv = _heads(k, "k", dtypes, q), k.shape[-2]
-    batch, seq = (1, q.shape[0]) if q.dim() == 3 else q.shape[:2]
+    shape, sq = _heads(q, "q", _TYPE)
+    index, dtypes = q.get_device(), (q.dtype,)
+    *batch, seq, heads, dim = shape
+    batch = batch[0] if batch else 1
     if layout not in _LAYOUT:
         raise ValueError("layout: 'half' or 'interleaved'")
+    sk, kv = _NOWHERE, 0
+    if k is not None:
+        k_shape, sk = _heads(k, "k", dtypes, q)
+        kv = k_shape[-2]
+    elif out_k is not None:
+        raise ValueError("out_k: there is no k")
     each = 0
     if positions is not None:
         shared = isinstance(positions, _Tensor) and positions.dim() == 1
         _need(positions, "positions", _INDEX, (seq,) if shared else (batch, seq), index)
         each = 0 if shared else seq
-    if out_k is not None and k is None:
-        raise ValueError("out_k: there is no k")
-    outs = []
-    for x, out, what in ((q, out_q, "out_q"), (k, out_k, "out_k")):
-        if out is not None:
-            _heads(out, what, dtypes, q)
-            if out.shape != x.shape:
-                raise ValueError(f"{what}: shape {tuple(out.shape)}, expected {tuple(x.shape)}")
-            _writable(out, what)
-        outs.append(out if out is not None or x is None else _empty(x.shape, dtype=x.dtype, device=x.device))
-    rq, rk = outs
     rotary_dim = dim if rotary_dim is None else rotary_dim
-    if kv == 0 or heads == 0:   # nothing of k (or of q)
-        if heads == 0:
-            if kv == 0:
-                return rq, rk
-            sq, heads, kv, sk = sk, kv, 0, (0, 0, 0)
-            first, second, ofirst, osecond = k, None, rk, None
-        else:
-            first, second, ofirst, osecond = q, None, rq, None
-    else:
-        first, second, ofirst, osecond = q, k, rq, rk
     table, address, scale = _frequencies(rotary_dim, base, scaling, factor, original_length, slow, fast)
-    so = _heads(ofirst, "out_q", dtypes)
-    d = _ROTARY_T.pack(batch, seq, heads, kv, dim, rotary_dim, _TYPE[q.dtype], _LAYOUT[layout],
+    rq, so_q = _turned(q, out_q, "out_q", dtypes, shape)
+    rk, so_k = _turned(k, out_k, "out_k", dtypes, k_shape) if k is not None else (None, _NOWHERE)
+    one, two = (q, rq, sq, so_q, heads), (k, rk, sk, so_k, kv)
+    if heads == 0:   # nothing of q: k in its place
+        one, two = two, (None, None, _NOWHERE, _NOWHERE, 0)
+        if kv == 0:
+            return rq, rk
+    elif kv == 0:
+        two = (None, None, _NOWHERE, _NOWHERE, 0)
+    d = _ROTARY_T.pack(batch, seq, one[4], two[4], dim, rotary_dim, _TYPE[q.dtype], _LAYOUT[layout],
                        _INDEX[positions.dtype] if positions is not None else 0, inverse, _p(positions), each, offset, address, scale, 0,
-                       *sq, *sk, *so, *(_heads(osecond, "out_k", dtypes) if osecond is not None else (0, 0, 0)))
-    C.check(C.bf16opt_rotary(d, first.data_ptr(), _p(second), ofirst.data_ptr(), _p(osecond), _raw_stream(index)))
+                       *one[2], *two[2], *one[3], *two[3])
+    C.check(C.bf16opt_rotary(d, one[0].data_ptr(), _p(two[0]), one[1].data_ptr(), _p(two[1]), _raw_stream(index)))
     _written(out_q, out_k)
     return rq, rk
 
