@@ -6,8 +6,13 @@
 // backward 2 (dh) + the same kept ones, and 2 for each gradient.
 //
 // A scale is a power of two, so dividing by it is exact and a code depends on nothing but the
-// element and its run's largest: no rounding but the one to e4m3 (half a step of three bits: 2^-4
-// relative at most, down to 2^-14 of the run's largest or so).
+// element and its run's largest: no rounding but the one to e4m3 (half a step of three bits, 2^-4
+// relative at most; of what is below 2^-6 scales, 2^-10 scales).
+//
+// Measured on one GB300 (a copy runs at 6.69 TB/s): 2048 x 57344 bf16, silu, gated, forward 143 us and backward 160 us, 6.2
+// TB/s together; 8192 x 8192 gelu backward 95 us, 5.7 TB/s; 4096 x 8192 FP32 gelu both ways 152 us, 6.2 TB/s; 8192 x 14336 bf16
+// packed and unpacked 116 us, 6.1 TB/s.  Loads wait for memory (9 to 11 cycles an issue) at 52 to 60 % of the issue slots.  Rows
+// between 16-byte boundaries take twice the instructions: 2213 x 18799 both ways 225 us, 3 TB/s.
 #include "ops_common.cuh"
 
 namespace bf16ops {

@@ -2,11 +2,16 @@
 //
 // Every element is read once and written once, which is what bounds the operator; q and k go
 // in one launch.  A thread has one place in the head (a vector of elements and, in the half layout, its
-// partners') and walks over tokens and heads with it, so its frequencies stay in registers
-// and an angle's sine and cosine are computed once per token for all the heads that it turns.
+// partners') and walks over tokens and heads with it; an angle's sine and cosine are computed once per token (of
+// q and of k) for all the heads that it turns.
 //
 // The angle: position times frequency, both whole numbers (2^-64 turns), wraps around
 // at whole turns by itself; what is left, in (-1/2, 1/2] turns, goes to FP32.
+//
+// Measured on one GB300 (a copy runs at 6.69 TB/s): 8192 tokens of 112 and 16 heads of 128 bf16, parts of one projection, 64 elements turned,
+// 87 us, 6.2 TB/s; all turned (half) 91 us, 5.9 TB/s; 32 and 8 heads 35 us, 4.7 TB/s; one head of each, where every piece has sines of
+// its own, 32768 tokens 27 us, 1.3 TB/s.  Sines in each thread's registers, a token's heads one batch after the other, took 109 us
+// for the first, and a CTA for each group of tokens, instead of one that walks on, 49 us for the last.
 #include <type_traits>
 
 #include "ops_common.cuh"
