@@ -614,6 +614,43 @@ def test_glu_ends_of_the_type(act, dtype):
     assert bool(torch.isfinite(h[0, 3:]).all())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("columns", [5, 8, 9, 31, 250, 256, 263, 520])
+def test_glu_rows_anywhere(columns, dtype):
+    """Each tensor's rows begin somewhere else between boundaries; results are those of aligned rows, and nothing beside the rows is written."""
+    rows, places = 5, 8 if dtype == BF16 else 4
+
+    def placed(x, at, pad):
+        flat = torch.full((rows * (columns + pad) + 16,), 3.0, dtype=dtype, device="cuda")
+        view = flat[at:at + rows * (columns + pad)].view(rows, columns + pad)[:, :columns]
+        if x is not None:
+            view.copy_(x)
+        return flat, view
+
+    def untouched(flat, view):
+        return int((flat == 3.0).sum()) == flat.numel() - rows * columns + int((view == 3.0).sum())
+
+    gate, up, dh = (activations(rows, columns, dtype, i) for i in range(3))
+    wide = [torch.zeros(rows, 2 * columns + 16, dtype=dtype, device="cuda")[:, :columns] for _ in range(3)]   # aligned rows
+    for w, x in zip(wide, (gate, up, dh)):
+        w.copy_(x)
+    h, codes, scales = ops.glu8_forward(wide[0], wide[1], act="gelu")
+    dgate, dup = ops.glu8_backward(wide[2], codes, scales, act="gelu")
+    again = torch.empty_like(h)
+    ops.glu8_backward(wide[2], codes, scales, act="gelu", out_h=again)
+    for at in range(places):
+        for pad in (0, 1, 3):
+            a, b, d = (placed(x, (at * k + k) % places, pad + k) for k, x in ((0, gate), (1, up), (3, dh)))
+            outs = [placed(None, (at + 2 * k + 1) % places, pad + 2 * k) for k in range(4)]
+            got = ops.glu8_forward(a[1], b[1], act="gelu", out=outs[0][1])
+            assert torch.equal(outs[0][1], h) and torch.equal(got[1], codes) and torch.equal(got[2], scales)
+            ops.glu8_backward(d[1], codes, scales, act="gelu", out_gate=outs[1][1], out_up=outs[2][1], out_h=outs[3][1])
+            assert torch.equal(outs[1][1], dgate) and torch.equal(outs[2][1], dup) and torch.equal(outs[3][1], again)
+            assert all(untouched(*o) for o in outs), (at, pad)
+            assert torch.equal(ops.unpack8(codes[0], scales[0], columns, dtype=dtype, out=a[1]), ops.unpack8(codes[0], scales[0], columns, dtype=dtype))
+            assert untouched(*a)
+
+
 def test_glu_keeps_nothing_on_request_and_no_rows():
     gate, up = activations(5, 100, BF16, 6), activations(5, 100, BF16, 7)
     h, codes, scales = ops.glu8_forward(gate, up, keep=False)
