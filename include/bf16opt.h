@@ -614,8 +614,8 @@ int bf16opt_balance_backward(const bf16opt_balance_t *d, const int32_t *ids, con
 /* Log-probabilities of given tokens, and two losses of them.  z: a row's logits, l its
  * label, T the temperature, s = softmax(z / T):
  *   logp = log s_l.
- * A row whose row_weight is 0, or whose label is outside [0, vocab), does not count: it is not
- * read, and its loss, log-probability, saved numbers and gradient are 0.  Logits of
+ * A row whose row_weight is 0, or whose label is outside [0, vocab), does not count: what stands in
+ * it has no effect, and its loss, log-probability, saved numbers and gradient are 0.  Logits of
  * -inf are masked vocabulary (s = 0; a label on one, or a row with no other logit, has
  * logp -inf; in the latter s = 0 everywhere).  NaN and +inf in a row give NaN in that row
  * (and in what is summed over it) alone.

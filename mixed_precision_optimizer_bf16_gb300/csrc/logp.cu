@@ -10,7 +10,7 @@
 //
 // Measured on one GB300 (algorithmic bytes over the time; a copy of the same buffers runs at 6.69 TB/s), bf16: forward 2048 x
 // 250880 150 us, 6.8 TB/s; backward 299 us, 6.9 TB/s; loss and gradient at once 353 us, 5.8 TB/s, 8192 x 32000 159 us, 6.6 TB/s,
-// 8192 x 8192 53 us, 5.1 TB/s.  The one-pass kernel of long rows is bound by what happens between its passes: CTAs of a cluster
+// 8192 x 8192 48 us, 5.6 TB/s.  The one-pass kernel of long rows is bound by what happens between its passes: CTAs of a cluster
 // wait for one another (issue 55 %, 67 % of the warps active), and a row per CTA would not stay in L2.  What was tried for them
 // instead: rows in registers across a cluster (16 vectors a thread, two CTAs of an SM: 442 us), in shared memory across a
 // cluster (360 us), a CTA of 1024 threads per SM with a ring (436 us, issue 81 %).

@@ -311,6 +311,7 @@ int start(Args &a, cudaStream_t stream) {
     cudaError_t e = clusters_that_fit(l, k_rotary<T, N, WIDE, HALF>, fit);
     if (e != cudaSuccess) return fail_cuda(e, "rotary occupancy");
     l.grid = (unsigned)std::min<uint64_t>(groups, fit);
+    l.cluster = 0;   // (CTAs start faster without the attribute)
     e = launch(l, k_rotary<T, N, WIDE, HALF>, a);
     return e == cudaSuccess ? BF16OPT_OK : fail_cuda(e, "rotary kernel launch");
 }

@@ -504,7 +504,7 @@ def token_logp_forward(logits, labels, *, temperature=1.0, row_weight=None):
     """Log-probabilities [rows] (FP32) that softmax(logits / temperature) gives
     to labels [rows] (int32 or int64), and saved [rows, 4] for
     token_logp_backward.  logits: [rows, vocab] bf16 or FP32.  A row with row_weight 0 or
-    with a label outside the vocabulary does not count: it is not read and has 0."""
+    with a label outside the vocabulary does not count: what stands in it has no effect, and it has 0."""
     d, rows, index = _tokens(logits, labels, temperature, row_weight)
     dev = logits.device
     logp = _empty(rows, dtype=torch.float32, device=dev)
