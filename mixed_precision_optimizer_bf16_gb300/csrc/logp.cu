@@ -213,7 +213,8 @@ __device__ __forceinline__ Terms terms_of(const Args &a, const Given &g, float m
     t.logp = logp.value();
     t.loss = 0.f, t.slope = 1.f;
     if (KIND == POLICY) {
-        const float x = a.old_logp ? (logp + Two{-g.old_logp, 0.f}).value() : t.logp - t.logp;
+        // of its own tokens the ratio is the constant 1, an infinite log-probability's too; NaN stays
+        const float x = a.old_logp ? (logp + Two{-g.old_logp, 0.f}).value() : t.logp == t.logp ? 0.f : t.logp;
         const float adv = g.advantage, ratio = expf(x);
         const float kept = adv >= 0.f ? (ratio > a.highest ? a.highest : ratio) : (ratio < a.lowest ? a.lowest : ratio);   // NaN stays
         t.loss = -kept * adv;

@@ -1,0 +1,43 @@
+"""The fine-tuning operators on the GPU where they are easily wrong: tokens that the vocabulary masks.
+
+Tolerances as in test_tuning_ops_gpu.py."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import tuning_reference as R  # noqa: E402
+from mixed_precision_optimizer_bf16_gb300 import train_ops as ops  # noqa: E402
+from test_tuning_ops_gpu import BF16, F32, INF, NAN, close, gradient_slack, randn, rows_case  # noqa: E402
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
+
+
+# ------------------------------------------------------------------ token losses
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,vocab", [(6, 600), (6, 1500), (700, 3001), (6, 12000), (700, 20011), (6, 70001)])
+def test_policy_of_its_own_tokens_is_a_constant_ratio(rows, vocab, dtype):
+    """Without a sampler's log-probabilities the ratio is 1, whatever the log-probability: a masked label's and an empty row's loss
+    and gradient are finite; a NaN or +inf in the row is NaN."""
+    z, labels, g = rows_case(rows, vocab, dtype, vocab)
+    z[0, vocab // 2:], labels[0] = -INF, vocab - 1
+    z[1] = -INF
+    z[2, 1], z[3, vocab - 1] = NAN, INF
+    labels[4] = -100
+    adv = randn(g, rows)
+    w, up = torch.rand(rows, device="cuda", generator=g) + 0.2, torch.rand(rows, device="cuda", generator=g) + 0.1
+    v, p, one = R.logp(z, labels.clamp(min=0))
+    live = R.counts(labels, vocab, w)
+    ratio = torch.where(torch.isnan(v), v, torch.ones_like(v))
+    slope = torch.where(live, -ratio * adv.double() * w.double(), torch.zeros_like(v))
+    dz, scale = R.gradient(live, slope * up.double(), p, one, 1.0)
+    slack = gradient_slack(scale.nan_to_num(0, 0, 0), vocab)
+    loss, logp, saved = ops.policy_forward(z, labels, adv, row_weight=w)
+    assert logp[0] == -INF and logp[1] == -INF and logp[4] == 0
+    close(loss, slope, 0.0, "loss")                   # (w times A is rounded once)
+    close(saved[:, 2], slope, 0.0, "slope")
+    close(ops.token_logp_backward(z, labels, saved, up), dz, slack, "dlogits of the backward call")
+    both = ops.policy_loss_grad(z, labels, adv, up, row_weight=w)
+    close(both[0], slope, 0.0, "loss of the single pass")
+    close(both[2], dz, slack, "dlogits of the single pass")
+    assert bool(torch.isfinite(both[2][:2]).all())
