@@ -679,9 +679,10 @@ int bf16opt_policy_loss_grad(const bf16opt_tokens_t *d, const bf16opt_policy_t *
  *   BF16OPT_PREFER_SIGMOID  m = beta h - margin;  loss = -(1 - e) log sigmoid(m) - e log sigmoid(-m),  e = label_smoothing,
  *   BF16OPT_PREFER_HINGE    m = beta h - margin;  loss = max(0, 1 - m),
  *   BF16OPT_PREFER_IPO      loss = (h - margin - 1 / (2 beta))^2.
- * Sums over a sequence are pairs of FP32 numbers (48 bits).  Rows outside the sequences do not count.  Offsets that descend or lie
- * outside [0, rows] are taken to the nearest that do not (the sequence is then
- * shorter or empty); nothing outside the tensors is touched. */
+ * Sums over a sequence are pairs of FP32 numbers (an addition is off by 2^-47 of the sum at
+ * most).  Rows outside the sequences do not count.  Offsets that descend or lie outside
+ * [0, rows] are taken to the nearest that do not (the sequence is then shorter or empty);
+ * nothing outside the tensors is touched. */
 #define BF16OPT_PREFER_SIGMOID 0
 #define BF16OPT_PREFER_HINGE 1
 #define BF16OPT_PREFER_IPO 2

@@ -178,18 +178,21 @@ __device__ __forceinline__ Given given_of(const Args &a, uint64_t row) {
     return g;
 }
 
-// A number as a sum of two, hi the nearest to it; lo 0 beside an infinite or NaN hi.
+// A number as a sum of two, hi the nearest to it; lo 0 beside an infinite or NaN hi.  A sum is off by 2^-47 of it at most where both have the
+// same sign (what rounding takes off the two small additions), and hi and lo are made apart again each time: small terms would else
+// gather in lo, which alone is an FP32 sum.
 struct Two {
     float hi, lo;
     __device__ __forceinline__ Two operator+(const Two &b) const {   // (a + b and b + a are the same bits)
-        float off;
-        const float s = two_sum(hi, b.hi, off);
-        return {s, fabsf(s) < INFINITY ? __fadd_rn(__fadd_rn(lo, b.lo), off) : 0.f};
+        float off, rest;
+        const float s = two_sum(hi, b.hi, off), h = two_sum(s, __fadd_rn(__fadd_rn(lo, b.lo), off), rest);
+        return fabsf(h) < INFINITY ? Two{h, rest} : Two{s, 0.f};
     }
     __device__ __forceinline__ float value() const { return hi + lo; }
 };
 
-// A row's log-probability (z - m) / T - log s.  log s = k ln 2 + log f, f in [0.7, 1.4]; k times the leading bits of ln 2 is exact.
+// A row's log-probability (z - m) / T - log s.  log s = k ln 2 + log f, f in [0.7, 1.4], ln 2 as its leading bits, k times which is
+// exact, and the rest (Cody and Waite's reduction).
 __device__ __forceinline__ Two logp_of(const Args &a, float m, float s, float z) {
     float off;
     const float d = two_sum(z, -m, off), p = d * a.inv_t;
@@ -197,8 +200,9 @@ __device__ __forceinline__ Two logp_of(const Args &a, float m, float s, float z)
     int k;
     float f = frexpf(s, &k);
     if (f < 0.70710678f) f *= 2.f, --k;
-    const float lo = fmaf(d, a.inv_t, -p) + fmaf(d, a.inv_t_rest, off * a.inv_t) - fmaf((float)k, 1.42860677e-6f, logf(f));
-    return Two{p, lo} + Two{-0.693145751953125f * (float)k, 0.f};
+    constexpr float kLn2 = 0.693145751953125f, kLn2Rest = (float)(0.69314718055994530942 - (double)kLn2);
+    const float lo = fmaf(d, a.inv_t, -p) + fmaf(d, a.inv_t_rest, off * a.inv_t) - fmaf((float)k, kLn2Rest, logf(f));
+    return Two{p, lo} + Two{-kLn2 * (float)k, 0.f};
 }
 
 // A counted row's log-probability, loss and slope.  The log-probability stays a sum of two numbers until it is compared with the others', so

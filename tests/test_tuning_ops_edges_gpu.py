@@ -1,4 +1,5 @@
-"""The fine-tuning operators on the GPU where they are easily wrong: tokens that the vocabulary masks.
+"""The fine-tuning operators on the GPU where they are easily wrong: tokens that the vocabulary masks and sums of many
+small log-probabilities.
 
 Tolerances as in test_tuning_ops_gpu.py."""
 import pytest
@@ -7,7 +8,7 @@ torch = pytest.importorskip("torch")
 
 import tuning_reference as R  # noqa: E402
 from mixed_precision_optimizer_bf16_gb300 import train_ops as ops  # noqa: E402
-from test_tuning_ops_gpu import BF16, F32, INF, NAN, close, gradient_slack, randn, rows_case  # noqa: E402
+from test_tuning_ops_gpu import BF16, F32, INF, NAN, close, gen, gradient_slack, randn, rows_case  # noqa: E402
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
 
@@ -41,3 +42,26 @@ def test_policy_of_its_own_tokens_is_a_constant_ratio(rows, vocab, dtype):
     close(both[0], slope, 0.0, "loss of the single pass")
     close(both[2], dz, slack, "dlogits of the single pass")
     assert bool(torch.isfinite(both[2][:2]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lengths", [(2048, 1500), (65536, 60001), (3, 40000)])
+def test_preference_sums_of_small_log_probabilities(lengths, dtype):
+    """Tokens that the model is sure of: the label has the largest logit and the sum of exponentials lies in [1, 1.29], so a log-probability is
+    one FP32 number, -log of it, and the sequence's sum is the 64-bit sum of those numbers within 2^-40 of it.  (Of 65536 such, a plain FP32
+    sum is 8e-4 off.)  The loss h^2 beside 1 shows that: ref_logp is the sum rounded to FP32."""
+    rows = sum(lengths)
+    g = gen(rows)
+    z = (-3.2 - 1.8 * torch.rand(rows, 8, device="cuda", generator=g)).to(dtype)
+    labels = torch.randint(0, 8, (rows,), device="cuda", generator=g)
+    z.scatter_(1, labels[:, None], 0.0)
+    each, saved = ops.token_logp_forward(z, labels)
+    ends = torch.tensor([0, *lengths], device="cuda").cumsum(0)
+    total = torch.stack([x.double().sum() for x in each.split(list(lengths))])
+    ref = total.float()
+    loss, logp, kept = ops.preference_forward(z, labels, ends, ref_logp=ref, kind="ipo", beta=0.5)
+    assert torch.equal(kept[:, :2], saved[:, :2])
+    close(logp, total, 2.0 ** -40 * total.abs(), "logp")
+    off = total - ref.double()
+    d = off[0] - off[1] - 1.0
+    close(loss, (d * d)[None], 2 * d.abs() * 2.0 ** -40 * total.abs().sum(), "loss")
