@@ -725,7 +725,8 @@ int bf16opt_unpack(const bf16opt_pack_t *d, const uint8_t *codes, const uint8_t 
 
 /* h = act(gate) up  (up NULL: h = act(gate)), act one of
  *   BF16OPT_GLU_SILU  g sigmoid(g),
- *   BF16OPT_GLU_GELU  g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2.
+ *   BF16OPT_GLU_GELU  g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 = g sigmoid(2 sqrt(2 / pi) (g + 0.044715 g^3))
+ * (a sigmoid below 2^-128 counts as 0).
  * The forward call keeps gate and up in 8 bits (codes [parts, rows, 32 runs], scales
  * [parts, rows, runs]: gate's, then up's); the backward call works on what was kept, g' and u':
  *   dgate = dh u' act'(g'),  dup = dh act(g'),  and, if wanted, h' = act(g') u'

@@ -81,9 +81,11 @@ __device__ __forceinline__ float reciprocal(float x) {   // 0 above 2^126
 // act(g) = g s, s = sigmoid(y), y = g (silu) or g (a + b g^2), a = 2 sqrt(2 / pi), b = 0.044715 a (gelu: (1 + tanh(y / 2)) / 2 =
 // sigmoid(y)); act'(g) = s + g y' s (1 - s).  1 - s as a difference is off by 2^-24, which times g y' is about |y| 2^-24 of
 // act'.  From |g| = 64 on gelu's sigmoid is 0 or 1, and g^2 stops growing.  (NaN goes through g.)
+// 1 + exp(-y) is taken 2^-32 times, so that its reciprocal is a normal number as long as the exponential is finite: a sigmoid
+// down to 2^-128 counts, which times g is a normal number (silu(-88) = -5e-37).
 template <int ACT>
 __device__ __forceinline__ float2 activate(float2 g, float2 &slope) {
-    constexpr float kA = 1.59576912160573071f, kB = 0.044715f * kA;
+    constexpr float kA = 1.59576912160573071f, kB = 0.044715f * kA, kSmall = 0x1p-32f;
     float2 y = g, dy = both(1.f);
     if (ACT == BF16OPT_GLU_GELU) {
         float2 q = mul2(g, g);
@@ -91,8 +93,8 @@ __device__ __forceinline__ float2 activate(float2 g, float2 &slope) {
         y = mul2(g, fma2(q, both(kB), both(kA)));
         dy = fma2(q, both(3.f * kB), both(kA));
     }
-    const float2 x = mul2(y, both(-kLog2e)), t = add2(make_float2(ex2(x.x), ex2(x.y)), both(1.f));
-    const float2 s = make_float2(reciprocal(t.x), reciprocal(t.y));
+    const float2 x = mul2(y, both(-kLog2e)), t = fma2(make_float2(ex2(x.x), ex2(x.y)), both(kSmall), both(kSmall));
+    const float2 s = mul2(make_float2(reciprocal(t.x), reciprocal(t.y)), both(kSmall));
     float2 w = mul2(s, fma2(s, both(-1.f), both(1.f)));
     if (ACT == BF16OPT_GLU_GELU) w = mul2(w, dy);
     slope = fma2(g, w, s);

@@ -1,5 +1,5 @@
-"""The fine-tuning operators on the GPU where they are easily wrong: tokens that the vocabulary masks and sums of many
-small log-probabilities.
+"""The fine-tuning operators on the GPU where they are easily wrong: tokens that the vocabulary masks, sums of many
+small log-probabilities, and sigmoids at the end of FP32.
 
 Tolerances as in test_tuning_ops_gpu.py."""
 import pytest
@@ -65,3 +65,35 @@ def test_preference_sums_of_small_log_probabilities(lengths, dtype):
     off = total - ref.double()
     d = off[0] - off[1] - 1.0
     close(loss, (d * d)[None], 2 * d.abs() * 2.0 ** -40 * total.abs().sum(), "loss")
+
+
+# ------------------------------------------------------------------ 8 bits
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("act,low,high", [("silu", -88.7, -80.0), ("gelu", -10.05, -9.5)])
+def test_glu_sigmoids_below_the_smallest_normal_number(act, low, high, dtype):
+    """Down to 2^-128 a sigmoid counts: times its input it is a normal number."""
+    gate = torch.linspace(low, high, 40 * 33, device="cuda").view(40, 33).to(dtype)
+    gate = gate.clamp(min=low) if dtype == F32 else torch.where(gate.double() < low, torch.full_like(gate, high), gate)
+    gate[0, 0] = -88.0 if act == "silu" else -10.0
+    up = 1.0 + torch.rand(40, 33, device="cuda", generator=gen(1)).to(dtype)
+    dh = torch.ones_like(gate)
+
+    def slack(y, value, sigmoids):                    # the exponential's and its argument's errors, and a subnormal sigmoid's rounding
+        return value.abs() * (2.0 ** -20 + y.abs() * 2.0 ** -21) + sigmoids.abs() * 2.0 ** -148
+
+    a, _, y = R.act(gate.double(), act)
+    want = a * up.double()
+    h, codes, scales = ops.glu8_forward(gate, up, act=act)
+    assert bool((want.abs() > 2.0 ** -126).all())
+    got = h.double()
+    u = 2.0 ** -8 if dtype == BF16 else 2.0 ** -23
+    assert bool(((got - want).abs() <= u * want.abs() + slack(y, want, gate.double() * up.double())).all()), float(((got - want) / want).abs().max())
+    g, v = (R.unpack(codes[i], scales[i], 33) for i in range(2))
+    fine = torch.sigmoid(R.act(g, act)[2]) > 2.0 ** -127.9
+    a, slope, y = R.act(g, act)
+    dgate, dup = (x.double() for x in ops.glu8_backward(dh, codes, scales, act=act))
+    steep = (g * (1 if act == "silu" else 1.6 * (1 + 0.135 * g * g))).abs() + 1
+    for got, want, terms in ((dgate, v * slope, v * steep), (dup, a, g)):
+        assert bool(((got - want).abs() <= u * want.abs() + slack(2 * y, want, terms))[fine].all())
+    assert bool(fine.any()) and bool(((torch.sigmoid(y) < 2.0 ** -126) & fine).any() or act == "gelu")
