@@ -757,8 +757,9 @@ int bf16opt_glu_backward(const bf16opt_glu_t *d, const void *dh, uint64_t dh_str
  * at position p each is turned by the angle p frequencies[i]:
  *   (a, b) -> scale (a cos - b sin, b cos + a sin)   (inverse: -sin),
  * the other elements are copied.  inverse gives the gradient of the inputs from that of the outputs.
- * The angle's whole turns are taken off in 64-bit whole numbers (p times the frequency in
- * 2^-64 turns), so far positions are as exact as near ones.  Results are rounded once. */
+ * The angle's whole turns are taken off in 64-bit whole numbers: p times the frequency to the nearest
+ * 2^-64 turns, so up to |p| = 2^36 an angle is as exact as a near one (its FP32 number's 2^-24;
+ * 2^-22 at 2^40).  Results are rounded once. */
 #define BF16OPT_ROTARY_HALF 0
 #define BF16OPT_ROTARY_INTERLEAVED 1
 #define BF16OPT_ROTARY_MAX_DIM 256

@@ -6,7 +6,7 @@
 // q and of k) for all the heads that it turns.
 //
 // The angle: position times frequency, both whole numbers (2^-64 turns), wraps around
-// at whole turns by itself; what is left, in (-1/2, 1/2] turns, goes to FP32.
+// at whole turns by itself; what is left, in [-1/2, 1/2) turns, goes to FP32.
 //
 // Measured on one GB300 (a copy runs at 6.69 TB/s): 8192 tokens of 112 and 16 heads of 128 bf16, parts of one projection, 64 elements turned,
 // 87 us, 6.2 TB/s; all turned (half) 91 us, 5.9 TB/s; 32 and 8 heads 35 us, 4.7 TB/s; one head of each, where every piece has sines of
@@ -286,6 +286,22 @@ bool same(const Box &x, const Box &y) {
     return x.p == y.p && x.s[0] == y.s[0] && x.s[1] == y.s[1] && x.s[2] == y.s[2];
 }
 
+// f radians in 2^-64 turns, to the nearest; whole turns do not count, since a position is a whole number.  The product with 1 / (2 pi)
+// is a sum of two doubles: rounded to one, it is off by 2^-56 turns or so, which a position of 2^36 makes an angle's 2^-17.
+uint64_t turns_of(double f) {
+    constexpr double kTurn = 0.15915494309189533577, kRest = -9.839338337591243e-18;   // 1 / (2 pi), and what the double lacks of it
+    double rest = 0.;   // what is left of the parts so far, less than a unit
+    auto units = [&](double x) {
+        x -= std::rint(x);
+        const double high = x * 0x1p32, h = std::rint(high), low = (high - h) * 0x1p32 + rest, l = std::rint(low);
+        rest = low - l;
+        return ((uint64_t)(int64_t)h << 32) + (uint64_t)(int64_t)l;
+    };
+    const double p = f * kTurn;
+    const uint64_t n = units(p);
+    return n + units(std::fma(f, kRest, std::fma(f, kTurn, -p)));
+}
+
 template <class T, int N, bool WIDE, bool HALF>
 int start(Args &a, cudaStream_t stream) {
     const int sms = sm_count();
@@ -376,10 +392,7 @@ int run(const bf16opt_rotary_t *d, const void *q, const void *k, void *out_q, vo
     a.offset = d->offset;
     a.dim = d->dim, a.turned = d->rotary_dim;
     a.scale = d->scale, a.inverse = (uint32_t)d->inverse;
-    for (uint32_t i = 0; i < d->rotary_dim / 2; ++i) {
-        const double turns = d->frequencies[i] * 0.15915494309189533577;   // 1 / (2 pi)
-        a.turns[i] = (uint64_t)std::llrint((turns - std::rint(turns)) * 0x1p63) << 1;   // a position is a whole number: whole turns do not count
-    }
+    for (uint32_t i = 0; i < d->rotary_dim / 2; ++i) a.turns[i] = turns_of(d->frequencies[i]);
     const cudaStream_t st = (cudaStream_t)stream;
     const auto whole = [&](uint64_t n) { return bits % n == 0; };
     if (d->type == BF16OPT_TYPE_BF16) {

@@ -1,14 +1,17 @@
 """The fine-tuning operators on the GPU where they are easily wrong: tokens that the vocabulary masks, sums of many
-small log-probabilities, and sigmoids at the end of FP32.
+small log-probabilities, sigmoids at the end of FP32, and positions beyond 2^32.
 
 Tolerances as in test_tuning_ops_gpu.py."""
+import decimal
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import tuning_reference as R  # noqa: E402
 from mixed_precision_optimizer_bf16_gb300 import train_ops as ops  # noqa: E402
-from test_tuning_ops_gpu import BF16, F32, INF, NAN, close, gen, gradient_slack, randn, rows_case  # noqa: E402
+from test_tuning_ops_gpu import (BF16, F32, F64, INF, NAN, close, gen, gradient_slack, randn, rotary_slack, rows_case)
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
 
@@ -97,3 +100,32 @@ def test_glu_sigmoids_below_the_smallest_normal_number(act, low, high, dtype):
     for got, want, terms in ((dgate, v * slope, v * steep), (dup, a, g)):
         assert bool(((got - want).abs() <= u * want.abs() + slack(2 * y, want, terms))[fine].all())
     assert bool(fine.any()) and bool(((torch.sigmoid(y) < 2.0 ** -126) & fine).any() or act == "gelu")
+
+
+# ------------------------------------------------------------------ rotary positions
+
+TURN = decimal.Decimal("6.28318530717958647692528676655900576839433879875021164194988918461563281257")
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("far", [31, 36, 40])
+def test_rotary_positions_beyond_32_bits(far, layout):
+    """The angle is the position times the frequency (a number of 64 bits), whose whole turns are exact: against decimal arithmetic.  A frequency in
+    2^-64 turns is off by half a unit, which a position multiplies."""
+    g = gen(far)
+    tokens, heads, dim = 24, 3, 64
+    q = randn(g, tokens, heads, dim)
+    positions = torch.randint(-(1 << far), 1 << far, (tokens,), device="cuda", generator=g)
+    f = R.frequencies(dim)[0]
+    with decimal.localcontext() as ctx:
+        ctx.prec = 90
+        left = [[float((decimal.Decimal(p) * decimal.Decimal(v) / TURN) % 1) for v in f] for p in positions.tolist()]
+    angle = 2 * math.pi * torch.tensor(left, dtype=F64, device="cuda")
+    c, s = angle.cos()[:, None], angle.sin()[:, None]
+    first, second = (slice(0, 32), slice(32, 64)) if layout == "half" else (slice(0, 64, 2), slice(1, 64, 2))
+    a, b = q.double()[..., first], q.double()[..., second]
+    want = torch.empty(tokens, heads, dim, dtype=F64, device="cuda")
+    want[..., first], want[..., second] = a * c - b * s, b * c + a * s
+    slack = rotary_slack(q, {}) + 2.0 ** (far - 65) * 2 * math.pi * 1.5 * q.double().abs().amax(-1, keepdim=True)
+    close(ops.rotary_forward(q, None, positions, layout=layout)[0], want, slack, "q")
+    close(ops.rotary_forward(q, None, positions - (1 << 35), layout=layout, offset=1 << 35)[0], want, slack, "q by an offset")
