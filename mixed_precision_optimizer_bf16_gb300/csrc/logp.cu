@@ -633,14 +633,16 @@ int check(const bf16opt_tokens_t *d, std::initializer_list<Part> in, std::initia
     if (d->logits_stride < d->vocab || (grad && dlogits_stride < d->vocab)) return bad("a row stride is below vocab");
     if (!span_bytes(d->rows, d->logits_stride, d->vocab, eb, zb) || (grad && !span_bytes(d->rows, dlogits_stride, d->vocab, eb, gb)))
         return bad("the sizes overflow");
-    if (d->rows == 0) return BF16OPT_OK;
-    if (!d->logits || !d->labels) return bad("an input pointer is NULL");
-    if (grad && !dlogits) return bad("dlogits is NULL");
-    if (misaligned(d->logits, eb) || misaligned(dlogits, eb) || misaligned(d->labels, index_bytes(d->labels_type)) || misaligned(d->row_weight, 4))
-        return fail(BF16OPT_ERR_ALIGNMENT, "logp: a pointer is not aligned to its element");
-    for (auto *parts : {&in, &outs})
-        for (const Part &x : *parts)
-            if (misaligned(x.p, 4)) return fail(BF16OPT_ERR_ALIGNMENT, "logp: a pointer is not aligned to its element");
+    const auto unaligned = [] { return fail(BF16OPT_ERR_ALIGNMENT, "logp: a pointer is not aligned to its element"); };
+    if (d->rows) {   // (of no rows there are still a preference's losses, sums and offsets)
+        if (!d->logits || !d->labels) return bad("an input pointer is NULL");
+        if (grad && !dlogits) return bad("dlogits is NULL");
+        if (misaligned(d->logits, eb) || misaligned(dlogits, eb) || misaligned(d->labels, index_bytes(d->labels_type)) || misaligned(d->row_weight, 4))
+            return unaligned();
+        for (auto *parts : {&in, &outs})
+            for (const Part &x : *parts)
+                if (misaligned(x.p, 4)) return unaligned();
+    }
     const Part own[] = {{d->logits, zb}, {d->labels, d->rows * index_bytes(d->labels_type)}, {d->row_weight, d->rows * 4}};
     const Part dz = {grad ? dlogits : nullptr, gb};
     auto meets = [&](const Part &o, bool gradient) {
