@@ -1,5 +1,6 @@
 """The fine-tuning operators on the GPU where they are easily wrong: tokens that the vocabulary masks, sums of many
-small log-probabilities, sigmoids at the end of FP32, and positions beyond 2^32.
+small log-probabilities, sigmoids at the end of FP32, positions beyond 2^32, and calls so large that a kernel's threads
+walk on.
 
 Tolerances as in test_tuning_ops_gpu.py."""
 import decimal
@@ -11,7 +12,8 @@ torch = pytest.importorskip("torch")
 
 import tuning_reference as R  # noqa: E402
 from mixed_precision_optimizer_bf16_gb300 import train_ops as ops  # noqa: E402
-from test_tuning_ops_gpu import (BF16, F32, F64, INF, NAN, close, gen, gradient_slack, randn, rotary_slack, rows_case)
+from test_tuning_ops_gpu import (BF16, F32, F64, INF, NAN, activations, check_glu, close, gen, gradient_slack, randn,  # noqa: E402
+                                 rotary_slack, rows_case, sum_error, turned)
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
 
@@ -70,6 +72,32 @@ def test_preference_sums_of_small_log_probabilities(lengths, dtype):
     close(loss, (d * d)[None], 2 * d.abs() * 2.0 ** -40 * total.abs().sum(), "loss")
 
 
+@pytest.mark.parametrize("pairs", [257, 2100])
+@pytest.mark.parametrize("mean", [False, True])
+def test_preference_of_many_pairs(pairs, mean):
+    """More pairs than a CTA has threads, sequences of no or a few tokens, some offsets that descend."""
+    g = gen(pairs)
+    lengths = torch.randint(0, 7, (2 * pairs,), device="cuda", generator=g)
+    ends = torch.cat([torch.zeros(1, dtype=torch.long, device="cuda"), lengths.cumsum(0)])
+    rows, vocab = int(ends[-1]) + 5, 50
+    z, labels, g = rows_case(rows, vocab, F32, 3, spread=1.0)
+    labels[torch.rand(rows, device="cuda", generator=g) < 0.3] = -100
+    down = torch.randint(1, 2 * pairs, (pairs // 8,), device="cuda", generator=g)
+    ends[down] -= 4
+    how = dict(beta=0.3, label_smoothing=0.1, margin=0.2, length_normalise=mean)
+    dloss = torch.rand(pairs, device="cuda", generator=g) + 0.2
+    ref = randn(g, 2 * pairs) - 10.0
+    loss_r, logp_r, dz_r, scale = R.preference(z, labels, ends, ref, dloss=dloss, **how)
+    loss, logp, saved = ops.preference_forward(z, labels, ends.int(), ref_logp=ref, **how)
+    most = int(ends.cummax(0).values.clamp(max=int(ends[-1])).diff().max())
+    off = most * sum_error(vocab)                     # of a sequence's sum
+    size = (logp_r.abs() + ref.abs().double()).view(2, pairs).sum(0)
+    close(logp, logp_r, off, "logp")
+    close(loss, loss_r, 0.3 * 2 * off + 2.0 ** -21 * (1 + 0.3 * size), "loss")
+    slope_off = 0.3 * 0.3 * 2 * off + 0.3 * 2.0 ** -20 + 0.3 * 0.3 * float(size.max()) * 2.0 ** -23
+    close(ops.token_logp_backward(z, labels, saved, dloss), dz_r, gradient_slack(scale, vocab) + 1.2 * slope_off * 2 * (scale > 0), "dlogits")
+
+
 # ------------------------------------------------------------------ 8 bits
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -102,7 +130,69 @@ def test_glu_sigmoids_below_the_smallest_normal_number(act, low, high, dtype):
     assert bool(fine.any()) and bool(((torch.sigmoid(y) < 2.0 ** -126) & fine).any() or act == "gelu")
 
 
+LARGE = [(50003, 40, 0, 0), (3001, 2056, 8, 0), (1501, 8200, 0, 0), (9001, 45, 3, 1), (3001, 2053, 0, 0), (1501, 8200, 3, 1)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows,columns,pad,shift", LARGE)
+def test_glu_more_rows_than_are_resident(rows, columns, pad, shift, gated, dtype):
+    """Threads that walk down several rows, the next ones on their way, with a remainder; in place too; twice the same bits."""
+    act = "gelu" if pad else "silu"
+    gate = activations(rows, columns, dtype, 1, pad, shift)
+    up = activations(rows, columns, dtype, 2, pad, shift) if gated else None
+    dh = activations(rows, columns, dtype, 3, pad, shift)
+    h, codes, scales, dgate, dup, again = check_glu(gate, up, act, dh)
+    for _ in range(2):
+        got = ops.glu8_backward(dh, codes, scales, act=act)
+        assert torch.equal(got[0], dgate) and (not gated or torch.equal(got[1], dup))
+    for out in ("out_gate", "out_h", *(["out_up"] if gated else [])):
+        mine = activations(rows, columns, dtype, 3, pad, shift)
+        got = ops.glu8_backward(mine, codes, scales, act=act, **{out: mine})
+        assert torch.equal(mine, {"out_gate": dgate, "out_up": dup, "out_h": again}[out])
+        assert out == "out_gate" or torch.equal(got[0], dgate)
+    for k, x in enumerate([gate, up] if gated else [gate]):
+        mine = activations(rows, columns, dtype, 1 + k, pad, shift)
+        got = ops.glu8_forward(*([mine] if not gated else [mine, up] if k == 0 else [gate, mine]), act=act, out=mine)
+        assert torch.equal(mine, h) and torch.equal(got[1], codes) and torch.equal(got[2], scales)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,columns,pad,shift", LARGE)
+def test_pack_more_rows_than_are_resident(rows, columns, pad, shift, dtype):
+    x = activations(rows, columns, dtype, 5, pad, shift)
+    codes, scales = ops.pack8(x)
+    want = R.pack(x)
+    assert torch.equal(scales, want[1]) and torch.equal(codes, want[0])
+    for t in (BF16, F32):
+        out = torch.full((rows, columns + pad), 7.0, dtype=t, device="cuda")
+        ops.unpack8(codes, scales, columns, dtype=t, out=out[:, :columns])
+        assert torch.equal(out[:, :columns], R.unpack(*want, columns).to(t)) and bool((out[:, columns:] == 7).all())
+
+
 # ------------------------------------------------------------------ rotary positions
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("tokens,heads,kv,dim,part", [(40009, 1, 1, 128, 128), (20011, 8, 2, 128, 64), (1503, 112, 16, 128, 128), (9001, 3, 1, 50, 20), (30011, 2, 5, 31, 30)])
+def test_rotary_more_tokens_than_are_resident(tokens, heads, kv, dim, part, layout, dtype):
+    """CTAs that walk from one group of tokens to the next, from q's to k's, with tables and positions of their own each time; in place too."""
+    g = gen(tokens)
+    rows = randn(g, tokens, heads + 2 * kv, dim).to(dtype)
+    q, k = rows[:, :heads], rows[:, heads:heads + kv]
+    positions = torch.randint(0, 100000, (tokens,), device="cuda", generator=g)
+    how = dict(layout=layout, rotary_dim=part)
+    for call, inverse in ((ops.rotary_forward, False), (ops.rotary_backward, True)):
+        got = call(q, k, positions, **how)
+        for x, y in zip((q, k), got):
+            close(y, turned(x, positions, how, inverse), rotary_slack(x, how), (layout, inverse))
+            assert torch.equal(y[..., part:], x[..., part:])
+        same = rows.clone()
+        call(same[:, :heads], same[:, heads:heads + kv], positions, out_q=same[:, :heads], out_k=same[:, heads:heads + kv], **how)
+        assert torch.equal(same[:, :heads], got[0]) and torch.equal(same[:, heads:heads + kv], got[1]) and torch.equal(same[:, heads + kv:], rows[:, heads + kv:])
+        one = rows.clone()[:, heads:heads + kv]        # k by itself, in place of q
+        assert torch.equal(call(one, None, positions, **how)[0], got[1])
+
 
 TURN = decimal.Decimal("6.28318530717958647692528676655900576839433879875021164194988918461563281257")
 
