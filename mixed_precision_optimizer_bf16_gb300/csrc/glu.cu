@@ -12,7 +12,8 @@
 // Measured on one GB300 (a copy runs at 6.69 TB/s): 2048 x 57344 bf16, silu, gated, forward 143 us and backward 160 us, 6.2
 // TB/s together; 8192 x 8192 gelu backward 95 us, 5.7 TB/s; 4096 x 8192 FP32 gelu both ways 152 us, 6.2 TB/s; 8192 x 14336 bf16
 // packed and unpacked 116 us, 6.1 TB/s.  Loads wait for memory (9 to 11 cycles an issue) at 52 to 60 % of the issue slots.  Rows
-// between 16-byte boundaries take twice the instructions: 2213 x 18799 both ways 225 us, 3 TB/s.
+// between 16-byte boundaries take twice the instructions: 2213 x 18799 both ways 225 us, 3 TB/s.  With a gate, the backward kernels of bf16 and
+// the forward ones of rows between boundaries spill (32 to 104 bytes).
 #include "ops_common.cuh"
 
 namespace bf16ops {
@@ -79,8 +80,10 @@ __device__ __forceinline__ float reciprocal(float x) {   // 0 above 2^126
 }
 
 // act(g) = g s, s = sigmoid(y), y = g (silu) or g (a + b g^2), a = 2 sqrt(2 / pi), b = 0.044715 a (gelu: (1 + tanh(y / 2)) / 2 =
-// sigmoid(y)); act'(g) = s + g y' s (1 - s).  1 - s as a difference is off by 2^-24, which times g y' is about |y| 2^-24 of
-// act'.  From |g| = 64 on gelu's sigmoid is 0 or 1, and g^2 stops growing.  (NaN goes through g.)
+// sigmoid(y)); act'(g) = s + g y' s (1 - s).  The exponential is off by 2^-22 and by its argument's rounding, |y| 2^-23 or so, the
+// reciprocal by 2^-23, both the special-function unit's for FP32 too (whole outputs are 1.9e-7 off, 8e-8 by torch's functions in
+// FP32); 1 - s as a difference is off by 2^-24, which is |g y'| 2^-24 of act' (|y| 2^-24 for silu, up to three times that for
+// gelu).  From |g| = 64 on gelu's sigmoid is 0 or 1, and g^2 stops growing.  (NaN goes through g.)
 // 1 + exp(-y) is taken 2^-32 times, so that its reciprocal is a normal number as long as the exponential is finite: a sigmoid
 // down to 2^-128 counts, which times g is a normal number (silu(-88) = -5e-37).
 template <int ACT>
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_forward(co
 }
 
 // Two gradients and what is kept leave few registers: of bf16 five CTAs of an SM ask for a row when they have written the last one,
-// which beats four that ask before (2048 x 57344: 160 against 186 us); of FP32 three that ask before (4096 x 8192: 79 against
+// which beats four that ask before (2048 x 57344: 160 against 165 us); of FP32 three that ask before (4096 x 8192: 79 against
 // 91 us).  (A ring of asynchronous copies, two to four rows ahead, took 161 and 98 us.)
 template <class T, bool ALIGNED, int PARTS, int ACT>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : ALIGNED && ACT >= 0 ? 5 : 4) k_backward(const Args a) {

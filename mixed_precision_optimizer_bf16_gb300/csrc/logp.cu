@@ -36,7 +36,8 @@ constexpr uint64_t kSliceVectors = 2 * kThreads * kU;   // of the backward kerne
 constexpr float kFar = 0x1p20f;
 
 // Of rows that are read a second time, at a time: what L2 keeps of them (two dies, each of which holds what its SMs ask
-// for: at 95 MB 2048 x 250880 took 419 us instead of 341, at 76 MB 1024 x 250880 FP32 405 us, 426 us at 57).
+// for: at 95 MB 2048 x 250880 took 419 us instead of 341, at 76 MB 1024 x 250880 FP32 405 us, 426 us at 57; other lengths were not
+// timed with other limits).
 constexpr uint64_t kInFlight = 76 << 20;
 constexpr unsigned kResident = 6;   // CTAs of an SM there (five: 350 us)
 constexpr uint64_t kStage = 72 * 1024 / 16;   // vectors of a slice in shared memory
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, HELD == 8 || HELD == kStaged ? (kThr
     const Slice s = slice_of(z, a.vocab, rank, ranks, 31 - __clz(ranks));
     const uint4 *zv = reinterpret_cast<const uint4 *>(z + s.head) + s.v0;
     const uint32_t nv = s.v1 - s.v0;
-    // asked for before it is known whether the row counts
+    // asked for before it is known whether the row counts: of one that does not, all that is held (up to 72 KB), else the first group, is read
     Group<T, kThreads, U> group;
     uint32_t groups = 0;   // of copies on their way
     if constexpr (STAGED) {

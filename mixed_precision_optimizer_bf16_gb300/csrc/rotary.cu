@@ -20,7 +20,7 @@ namespace bf16ops {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kResident = 4;   // CTAs of an SM: 64 registers
+constexpr int kResident = 4;   // CTAs of an SM: 64 registers (pieces of four and eight bf16 spill 20 to 44 bytes)
 // Heads whose pieces a thread asks for at a time: 64 bytes, at most eight pieces.
 template <class T, int N, bool HALF>
 constexpr int kBatchOf = std::max(1, std::min(8, 64 / (int)(N * sizeof(T))) / (HALF ? 2 : 1));

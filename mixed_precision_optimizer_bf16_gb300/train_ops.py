@@ -556,7 +556,7 @@ def preference_forward(logits, labels, offsets, *, ref_logp=None, kind="sigmoid"
     int64): sequence i is rows offsets[i] to offsets[i + 1]; sequence i is preferred to sequence
     pairs + i.  Rows whose label is outside the vocabulary (prompts, padding) and rows outside the
     sequences do not count.  ref_logp [2 pairs] FP32: a reference's (None: 0).
-    kind: 'sigmoid', 'hinge' or 'ipo'."""
+    kind: 'sigmoid', 'hinge' or 'ipo'; label_smoothing is the sigmoid's, the others take no notice of it."""
     d, rows, index = _tokens(logits, labels, temperature, None)
     if kind not in _PREFER:
         raise ValueError("kind: 'sigmoid', 'hinge' or 'ipo'")
@@ -869,7 +869,7 @@ def rotary_forward(q, k=None, positions=None, *, rotary_dim=None, layout="half",
     (None: all).  q: [tokens, heads, dim] or [batch, tokens, heads, dim], k (or None) the same with its own number of
     heads; bf16 or FP32; any strides with contiguous heads.  positions: None (0, 1, ..), [tokens] or [batch, tokens],
     int32 or int64; offset is added.  layout: pairs are (i, i + rotary_dim / 2) ('half') or neighbours
-    ('interleaved').  Pair i turns by base^(-2 i / rotary_dim) a position;
+    ('interleaved').  Pair i turns by base^(-2 i / rotary_dim), a 64-bit number, a position;
     scaling for longer contexts: 'linear' (frequencies / factor), 'ntk' (base factor^(d / (d - 2))), 'yarn'
     (pairs that turn less than `slow` times in original_length are slowed by factor, those above `fast` are
     not, between them a ramp; the turned pairs are 0.1 ln(factor) + 1 times as long).  out_q may be q, out_k may be k."""
