@@ -197,7 +197,11 @@ struct Two {
 __device__ __forceinline__ Two logp_of(const Args &a, float m, float s, float z) {
     float off;
     const float d = two_sum(z, -m, off), p = d * a.inv_t;
-    if (!(fabsf(p) < INFINITY && s > 0.f && s < INFINITY)) return {m == -INFINITY && s == 0.f ? -INFINITY : (z - m) * a.inv_t - logf(s), 0.f};
+    if (!(fabsf(p) < INFINITY && s > 0.f && s < INFINITY)) {
+        if (m == -INFINITY && s == 0.f) return {-INFINITY, 0.f};
+        // (a difference that no FP32 number holds, of numbers of opposite signs, may be one when it is divided)
+        return {(fabsf(d) < INFINITY ? p : z * a.inv_t - m * a.inv_t) - logf(s), 0.f};
+    }
     int k;
     float f = frexpf(s, &k);
     if (f < 0.70710678f) f *= 2.f, --k;

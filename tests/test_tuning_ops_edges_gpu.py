@@ -1,6 +1,5 @@
 """The fine-tuning operators on the GPU where they are easily wrong: tokens that the vocabulary masks, sums of many
-small log-probabilities, sigmoids at the end of FP32, positions beyond 2^32, and calls so large that a kernel's threads
-walk on.
+small log-probabilities, sigmoids at the end of FP32, positions beyond 2^32, and calls so large that a kernel's threads walk on.
 
 Tolerances as in test_tuning_ops_gpu.py."""
 import decimal
@@ -12,8 +11,8 @@ torch = pytest.importorskip("torch")
 
 import tuning_reference as R  # noqa: E402
 from mixed_precision_optimizer_bf16_gb300 import train_ops as ops  # noqa: E402
-from test_tuning_ops_gpu import (BF16, F32, F64, INF, NAN, activations, check_glu, close, gen, gradient_slack, randn,  # noqa: E402
-                                 rotary_slack, rows_case, sum_error, turned)
+from test_tuning_ops_gpu import (BF16, F32, F64, INF, NAN, activations, check_glu, check_logp, close, gen, gradient_slack,  # noqa: E402
+                                 randn, rotary_slack, rows_case, sum_error, turned)
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
 
@@ -47,6 +46,21 @@ def test_policy_of_its_own_tokens_is_a_constant_ratio(rows, vocab, dtype):
     close(both[0], slope, 0.0, "loss of the single pass")
     close(both[2], dz, slack, "dlogits of the single pass")
     assert bool(torch.isfinite(both[2][:2]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("vocab", [7, 3000, 33000])
+@pytest.mark.parametrize("temperature", [4.0, 65536.0])
+def test_logp_of_differences_that_no_number_holds(temperature, vocab, dtype):
+    """The type's lowest value beside its largest: their difference is infinite in FP32, divided by the temperature it is not."""
+    z, labels, g = rows_case(4, vocab, dtype, vocab)
+    big = torch.finfo(dtype).max
+    z[0, 1], z[0, 0], labels[0] = big, -big, 0
+    z[1], z[1, vocab - 1], labels[1] = -big, big, 2
+    z[2, 1], z[2, 0], labels[2] = big, -INF, 0
+    check_logp(z, labels, temperature)
+    loss = ops.policy_loss_grad(z, labels, torch.ones(4, device="cuda"), temperature=temperature)
+    assert torch.equal(loss[1], ops.token_logp_forward(z, labels, temperature=temperature)[0])
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
